@@ -21,6 +21,7 @@ from .build import LIB_PATH
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_MISALIGNED, FA_ERR_CUDA, \
     FA_ERR_TIMEOUT = range(6)
 FA_DECODE_MAX_SQ = 16
+FA_TREE_MAX_NODES = 1024
 
 # name -> (restype, argtypes); must match include/fa.h
 _VP, _I, _F, _LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong
@@ -40,6 +41,26 @@ SIGNATURES = {
     "fa_fwd_decode": (_I, _FWD + [_VP]),
     "fa_fwd_decode_splits": (_I, _FWD + [_I, _VP]),
     "fa_fwd_decode_noalloc": (_I, _FWD + [_VP]),
+    "fa_fwd_prefill_first": (_I, _FWD + [_I, _I, _VP, _VP]),
+    "fa_fwd_prefill_varlen_first": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I,
+                                         _I, _I, _I, _F, _I, _I, _I, _VP, _VP]),
+    "fa_fwd_prefill_varlen_paged_first": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I,
+                                               _I, _I, _I, _I, _I, _I, _F, _I, _I, _I, _VP, _VP]),
+    "fa_fwd_decode_first": (_I, _FWD + [_I, _I, _VP, _VP]),
+    "fa_fwd_decode_paged_first": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _I, _I,
+                                       _I, _I, _F, _I, _I, _I, _VP, _VP]),
+    "fa_fwd_decode_tree": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _VP, _I, _VP, _I,
+                                _F, _VP, _VP]),
+    "fa_fwd_decode_tree_paged": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _I, _I,
+                                      _I, _VP, _I, _VP, _I, _F, _VP, _VP]),
+    "fa_tree_mask": (_I, [_VP, _VP, _I, _I, _VP]),
+    "fa_cache_fork": (_I, [_VP, _I, _VP, _I, _VP, _I, _VP, _VP, _I, _VP, _VP]),
+    "fa_cache_reserve": (_I, [_VP, _I, _VP, _I, _VP, _I, _VP, _I, _VP, _VP, _VP]),
+    "fa_cache_free": (_I, [_VP, _I, _VP, _I, _VP, _I, _VP, _I, _VP]),
+    "fa_cache_append": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _I,
+                             _VP, _VP, _VP]),
+    "fa_cache_copy": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I, _VP]),
+    "fa_cache_compact": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I, _VP, _I, _VP, _I, _VP, _VP]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_get_device_error": (_I, [_VP]),
     "fa_get_device_error_word": (_I, [_VP, ctypes.POINTER(ctypes.c_uint)]),
@@ -141,16 +162,20 @@ def _check_sinks(sinks, hq):
 
 
 def prefill(q, k, v, scale=None, causal=False, seqlens_k=None, out=None, lse=None,
-            stream=None, window=0, sinks=None):
+            stream=None, window=0, sinks=None, first=0):
     """Attention forward through ``fa_fwd_prefill`` (``fa_fwd_prefill_ex`` with
-    a sliding ``window`` > 0 or per-head ``sinks``); returns (o, lse)."""
+    a sliding ``window`` > 0 or per-head ``sinks``, ``fa_fwd_prefill_first`` with
+    a window whose ``first`` keys stay visible); returns (o, lse)."""
     B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
     out, lse = _outputs(q, out, lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
-    if (window and window > 0) or sinks is not None:
+    if first:
+        st = lib().fa_fwd_prefill_first(*args, int(window or 0), int(first), _ptr(sinks),
+                                        _stream_ptr(stream))
+    elif (window and window > 0) or sinks is not None:
         st = lib().fa_fwd_prefill_ex(*args, int(window or 0), _ptr(sinks), _stream_ptr(stream))
     else:
         st = lib().fa_fwd_prefill(*args, _stream_ptr(stream))
@@ -160,19 +185,24 @@ def prefill(q, k, v, scale=None, causal=False, seqlens_k=None, out=None, lse=Non
 
 
 def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=None,
-           lse=None, stream=None, window=0, sinks=None):
+           lse=None, stream=None, window=0, sinks=None, first=0):
     """Split-KV attention forward through ``fa_fwd_decode_splits``
     (num_splits <= 0 lets the library choose, as ``fa_fwd_decode`` does), or
-    ``fa_fwd_decode_ex`` with a sliding ``window`` > 0 or per-head ``sinks``."""
+    ``fa_fwd_decode_ex`` with a sliding ``window`` > 0 or per-head ``sinks``, or
+    ``fa_fwd_decode_first`` with a window whose ``first`` keys stay visible."""
     B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
     out, lse = _outputs(q, out, lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
-    if (window and window > 0) or sinks is not None:
+    if first or (window and window > 0) or sinks is not None:
         if num_splits and num_splits > 0:
             raise ValueError("num_splits cannot be combined with window or sinks")
+    if first:
+        st = lib().fa_fwd_decode_first(*args, int(window or 0), int(first), _ptr(sinks),
+                                       _stream_ptr(stream))
+    elif (window and window > 0) or sinks is not None:
         st = lib().fa_fwd_decode_ex(*args, int(window or 0), _ptr(sinks), _stream_ptr(stream))
     elif num_splits and num_splits > 0:
         st = lib().fa_fwd_decode_splits(*args, int(num_splits), _stream_ptr(stream))
@@ -183,7 +213,8 @@ def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=
     return out, lse
 
 
-def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out, lse, stream):
+def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out, lse, stream,
+           *more):
     if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda):
         raise ValueError("q and the caches must be CUDA tensors")
     if q.dtype != torch.bfloat16 or k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
@@ -204,7 +235,7 @@ def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     st = getattr(lib(), name)(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), B, Hq,
                               Hkv, Sq, _ptr(seqlens_k), _ptr(block_table), block_table.shape[1],
-                              page_size, num_pages, d, scale, int(bool(causal)),
+                              page_size, num_pages, d, scale, int(bool(causal)), *more,
                               _stream_ptr(stream))
     if st != FA_OK:
         raise FaError(st, name)
@@ -212,9 +243,10 @@ def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out
 
 
 def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale=None,
-                   causal=False, window=0, sinks=None, out=None, lse=None, stream=None):
-    """Prefill over packed sequences through ``fa_fwd_prefill_varlen``:
-    q [total_q, Hq, d], k and v [total_k, Hkv, d] bf16, int32 offsets
+                   causal=False, window=0, sinks=None, out=None, lse=None, stream=None, first=0):
+    """Prefill over packed sequences through ``fa_fwd_prefill_varlen``
+    (``fa_fwd_prefill_varlen_first`` with a window whose ``first`` keys stay
+    visible): q [total_q, Hq, d], k and v [total_k, Hkv, d] bf16, int32 offsets
     cu_seqlens_q / cu_seqlens_k [B + 1]; returns o [total_q, Hq, d] and
     lse [Hq, total_q]."""
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
@@ -242,11 +274,13 @@ def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, total_q]")
     sinks = _check_sinks(sinks, Hq)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    st = lib().fa_fwd_prefill_varlen(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                                     _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B, int(max_seqlen_q),
-                                     int(max_seqlen_k), total_q, total_k, Hq, Hkv, d, scale,
-                                     int(bool(causal)), int(window), _ptr(sinks),
-                                     _stream_ptr(stream))
+    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
+            _ptr(cu_seqlens_k), B, int(max_seqlen_q), int(max_seqlen_k), total_q, total_k, Hq, Hkv,
+            d, scale, int(bool(causal)), int(window))
+    if first:
+        st = lib().fa_fwd_prefill_varlen_first(*args, int(first), _ptr(sinks), _stream_ptr(stream))
+    else:
+        st = lib().fa_fwd_prefill_varlen(*args, _ptr(sinks), _stream_ptr(stream))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_prefill_varlen")
     return out, lse
@@ -254,11 +288,12 @@ def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
 
 def prefill_varlen_paged(q, k_cache, v_cache, cu_seqlens_q, max_seqlen_q, block_table, seqlens_k,
                          scale=None, causal=False, window=0, sinks=None, out=None, lse=None,
-                         stream=None):
+                         stream=None, first=0):
     """Packed queries q [total_q, Hq, d] (offsets cu_seqlens_q [B + 1]) over
     paged caches [num_pages, Hkv, page_size, d] (block_table [B, max_pages],
-    seqlens_k [B]) through ``fa_fwd_prefill_varlen_paged``; returns
-    o [total_q, Hq, d] and lse [Hq, total_q]."""
+    seqlens_k [B]) through ``fa_fwd_prefill_varlen_paged``
+    (``fa_fwd_prefill_varlen_paged_first`` with a window whose ``first`` keys
+    stay visible); returns o [total_q, Hq, d] and lse [Hq, total_q]."""
     if not q.is_cuda or q.dtype != torch.bfloat16 or q.dim() != 3:
         raise ValueError("q must be a CUDA bf16 tensor [tokens, heads, d]")
     if (k_cache.shape != v_cache.shape or k_cache.dim() != 4 or not k_cache.is_cuda
@@ -289,11 +324,14 @@ def prefill_varlen_paged(q, k_cache, v_cache, cu_seqlens_q, max_seqlen_q, block_
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, total_q]")
     sinks = _check_sinks(sinks, Hq)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    st = lib().fa_fwd_prefill_varlen_paged(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
-        _ptr(seqlens_k), _ptr(block_table), block_table.shape[1], page_size, num_pages, B,
-        int(max_seqlen_q), total_q, Hq, Hkv, d, scale, int(bool(causal)), int(window),
-        _ptr(sinks), _stream_ptr(stream))
+    args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
+            _ptr(seqlens_k), _ptr(block_table), block_table.shape[1], page_size, num_pages, B,
+            int(max_seqlen_q), total_q, Hq, Hkv, d, scale, int(bool(causal)), int(window))
+    if first:
+        st = lib().fa_fwd_prefill_varlen_paged_first(*args, int(first), _ptr(sinks),
+                                                     _stream_ptr(stream))
+    else:
+        st = lib().fa_fwd_prefill_varlen_paged(*args, _ptr(sinks), _stream_ptr(stream))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_prefill_varlen_paged")
     return out, lse
@@ -308,10 +346,276 @@ def prefill_paged(q, k_cache, v_cache, block_table, seqlens_k, scale=None, causa
 
 
 def decode_paged(q, k_cache, v_cache, block_table, seqlens_k, scale=None, causal=False,
-                 out=None, lse=None, stream=None):
-    """Decode over paged caches through ``fa_fwd_decode_paged``; returns (o, lse)."""
+                 out=None, lse=None, stream=None, window=0, sinks=None, first=0):
+    """Decode over paged caches through ``fa_fwd_decode_paged``
+    (``fa_fwd_decode_paged_first`` with a sliding ``window`` > 0, whose
+    ``first`` keys stay visible, or per-head ``sinks``); returns (o, lse)."""
+    if first or (window and window > 0) or sinks is not None:
+        sinks = _check_sinks(sinks, q.shape[1])
+        return _paged("fa_fwd_decode_paged_first", q, k_cache, v_cache, block_table, seqlens_k,
+                      scale, causal, out, lse, stream, int(window or 0), int(first), _ptr(sinks))
     return _paged("fa_fwd_decode_paged", q, k_cache, v_cache, block_table, seqlens_k, scale,
                   causal, out, lse, stream)
+
+
+# ------------------------------------------- trees of drafted tokens, cache pages ----
+
+def _on(stream, device):
+    """The stream to launch on (the device's current one) for tensors of
+    ``device``, which has to be the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
+    return _stream_ptr(stream)
+
+
+def _ints(name, t, dim, device):
+    """Checks an int32 tensor of ``dim`` dimensions that a kernel reads or writes in place."""
+    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s) on {device}")
+    return _ptr(t)
+
+
+def _tree_args(q, k, v, tree_mask, tree_lens, sinks, scale, out, lse):
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be bfloat16")
+        if t.device != dev or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 4-D tensor on {dev}")
+    B, Hq, T, d = q.shape
+    if v.shape != k.shape or k.shape[3] != d:
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
+    words = (T + 31) // 32
+    shared = tree_mask.dim() == 2
+    if tuple(tree_mask.shape) != ((T, words) if shared else (B, T, words)):
+        raise ValueError(f"tree_mask must be [{B}, {T}, {words}] or [{T}, {words}]")
+    mask = _ints("tree_mask", tree_mask, 2 if shared else 3, dev)
+    if tree_lens is not None and tree_lens.shape != (B,):
+        raise ValueError("tree_lens must be [B]")
+    if sinks is not None and sinks.device != dev:
+        raise ValueError(f"sinks must be on {dev}")
+    out, lse = _outputs(q, out, lse)
+    if out.device != dev or lse.device != dev:
+        raise ValueError(f"out and lse must be on {dev}")
+    return (mask, int(shared),
+            None if tree_lens is None else _ints("tree_lens", tree_lens, 1, dev), d,
+            1.0 / math.sqrt(d) if scale is None else float(scale)), _check_sinks(sinks, Hq), out, lse
+
+
+def tree_mask(parents, out=None, stream=None):
+    """Mask words int32 [B, T, ceil(T / 32)] of trees given by their parents
+    int32 [B, T] through ``fa_tree_mask``: node i sees itself and the nodes on
+    its way up (bit j % 32 of word j / 32)."""
+    if not parents.is_cuda:
+        raise ValueError("parents must be a CUDA tensor")
+    src = _ints("parents", parents, 2, parents.device)
+    B, T = parents.shape
+    words = (T + 31) // 32
+    if out is None:
+        out = torch.empty((B, T, words), dtype=torch.int32, device=parents.device)
+    dst = _ints("out", out, 3, parents.device)
+    if out.shape != (B, T, words):
+        raise ValueError(f"out must be [{B}, {T}, {words}]")
+    st = lib().fa_tree_mask(src, dst, B, T, _on(stream, parents.device))
+    if st != FA_OK:
+        raise FaError(st, "fa_tree_mask")
+    return out
+
+
+def decode_tree(q, k, v, tree_mask, scale=None, seqlens_k=None, tree_lens=None, sinks=None,
+                out=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens through ``fa_fwd_decode_tree``:
+    q [B, Hq, T, d] are the nodes, whose keys are each sequence's last
+    tree_lens[b] (default T) of k, v [B, Hkv, Sk, d]; a node sees every key
+    before the tree and the nodes of its mask bits, tree_mask int32
+    [B, T, ceil(T / 32)] or [T, ceil(T / 32)].  Returns (o, lse); rows past a
+    tree's nodes are not written."""
+    more, sinks, out, lse = _tree_args(q, k, v, tree_mask, tree_lens, sinks, scale, out, lse)
+    B, Hq, T, d = q.shape
+    if k.shape[0] != B:
+        raise ValueError("k and v must have q's batch")
+    if seqlens_k is not None and seqlens_k.shape != (B,):
+        raise ValueError("seqlens_k must be [B]")
+    lens = None if seqlens_k is None else _ints("seqlens_k", seqlens_k, 1, q.device)
+    st = lib().fa_fwd_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq,
+                                  k.shape[1], T, k.shape[2], lens, *more, _ptr(sinks),
+                                  _on(stream, q.device))
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_decode_tree")
+    return out, lse
+
+
+def decode_tree_paged(q, k_cache, v_cache, block_table, seqlens_k, tree_mask, scale=None,
+                      tree_lens=None, sinks=None, out=None, lse=None, stream=None):
+    """``decode_tree`` over paged caches [num_pages, Hkv, page_size, d] through
+    ``fa_fwd_decode_tree_paged``; returns (o, lse)."""
+    more, sinks, out, lse = _tree_args(q, k_cache, v_cache, tree_mask, tree_lens, sinks, scale, out,
+                                       lse)
+    B, Hq, T, d = q.shape
+    num_pages, Hkv, page_size, _ = k_cache.shape
+    table = _ints("block_table", block_table, 2, q.device)
+    if block_table.shape[0] != B or seqlens_k.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seqlens_k [B]")
+    st = lib().fa_fwd_decode_tree_paged(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), B, Hq, Hkv, T,
+        _ints("seqlens_k", seqlens_k, 1, q.device), table, block_table.shape[1], page_size,
+        num_pages, *more, _ptr(sinks), _on(stream, q.device))
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_decode_tree_paged")
+    return out, lse
+
+
+def _table(refs, block_table, seqlens):
+    if not block_table.is_cuda:
+        raise ValueError("block_table must be a CUDA tensor")
+    dev = block_table.device
+    B, max_pages = block_table.shape if block_table.dim() == 2 else (-1, -1)
+    if seqlens.dim() != 1 or seqlens.numel() != B:
+        raise ValueError("block_table must be [B, max_pages] and seqlens [B]")
+    return (_ints("refs", refs, 1, dev), refs.numel(), _ints("block_table", block_table, 2, dev),
+            max_pages, _ints("seqlens", seqlens, 1, dev), B)
+
+
+def _status(status, device):
+    if status is None:
+        return torch.empty(1, dtype=torch.int32, device=device)
+    _ints("status", status, 1, device)
+    if status.numel() != 1:
+        raise ValueError("status must be [1]")
+    return status
+
+
+def cache_fork(refs, block_table, seqlens, src, dst, status=None, stream=None):
+    """Rows dst[i] share the pages of rows src[i], through ``fa_cache_fork``;
+    refs [num_pages], block_table [B, max_pages] and seqlens [B] (int32) change
+    in place.  Returns status int32 [1]: 0, or 1 + the first pair refused
+    (nothing is changed then)."""
+    dev = block_table.device
+    args = _table(refs, block_table, seqlens)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    status = _status(status, dev)
+    st = lib().fa_cache_fork(*args, _ints("src", src, 1, dev), _ints("dst", dst, 1, dev),
+                             src.numel(), _ptr(status), _on(stream, dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_fork")
+    return status
+
+
+def cache_reserve(refs, block_table, seqlens, extra, page_size, copies=None, status=None,
+                  stream=None):
+    """Pages for extra[b] more keys of every row (negative: the row is left
+    alone) through ``fa_cache_reserve``: from the page that its next key goes to
+    on, missing ones are taken from the free pages and shared ones replaced
+    (copy on write), in place.  Returns (copies int32 [B, 3], status int32 [1]):
+    copies is for ``cache_append`` or ``cache_copy``; status is 0, the number of
+    pages lacking, or -1 - b for a row too long (nothing is reserved then)."""
+    dev = block_table.device
+    args = _table(refs, block_table, seqlens)
+    B = seqlens.numel()
+    if extra.shape != (B,):
+        raise ValueError("extra must be [B]")
+    if copies is None:
+        copies = torch.empty((B, 3), dtype=torch.int32, device=dev)
+    if copies.shape != (B, 3):
+        raise ValueError("copies must be [B, 3]")
+    status = _status(status, dev)
+    st = lib().fa_cache_reserve(*args, _ints("extra", extra, 1, dev), int(page_size),
+                                _ints("copies", copies, 2, dev), _ptr(status), _on(stream, dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_reserve")
+    return copies, status
+
+
+def cache_free(refs, block_table, seqlens, rows, stream=None):
+    """Gives up the pages of the listed rows through ``fa_cache_free``."""
+    dev = block_table.device
+    args = _table(refs, block_table, seqlens)
+    st = lib().fa_cache_free(*args, _ints("rows", rows, 1, dev), rows.numel(), _on(stream, dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_free")
+
+
+def _caches(k_cache, v_cache):
+    if not k_cache.is_cuda or k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+        raise ValueError("the caches must be CUDA bf16 tensors")
+    if (k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.device != k_cache.device
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError("the caches must share a shape [num_pages, Hkv, page_size, d], contiguous")
+    return (_ptr(k_cache), _ptr(v_cache), *k_cache.shape)
+
+
+def _new_rows(name, t, hkv, d, device):
+    """New rows [B, Hkv, n, d] of any strides that are multiples of 8 elements
+    over a contiguous last dimension (else a copy that has them)."""
+    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.shape[1] != hkv \
+            or t.shape[3] != d:
+        raise ValueError(f"{name} must be a bf16 tensor [B, {hkv}, n, {d}] on {device}")
+    s = t.stride()
+    if s[3] != 1 or s[0] % 8 or s[1] % 8 or s[2] % 8 or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+        s = t.stride()
+    return t, (ctypes.c_longlong * 3)(s[0], s[1], s[2])
+
+
+def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=None, copies=None,
+                 stream=None):
+    """Writes k_new, v_new [B, Hkv, n, d] (any strides) as keys seqlens[b] + i,
+    i < n_new[b] (default n), of the paged caches through ``fa_cache_append``,
+    after the page copies of ``cache_reserve`` when they are given.  seqlens is
+    not changed."""
+    kc = _caches(k_cache, v_cache)
+    dev = k_cache.device
+    B = seqlens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or k_new.shape != v_new.shape \
+            or k_new.shape[0] != B:
+        raise ValueError("block_table must be [B, max_pages], seqlens [B], k_new and v_new [B, Hkv, n, d]")
+    if n_new is not None and n_new.shape != (B,):
+        raise ValueError("n_new must be [B]")
+    if copies is not None and copies.shape != (B, 3):
+        raise ValueError("copies must be [B, 3]")
+    k_new, ks = _new_rows("k_new", k_new, kc[3], kc[5], dev)
+    v_new, vs = _new_rows("v_new", v_new, kc[3], kc[5], dev)
+    st = lib().fa_cache_append(
+        *kc, _ints("block_table", block_table, 2, dev), block_table.shape[1],
+        _ints("seqlens", seqlens, 1, dev), B, _ptr(k_new), ks, _ptr(v_new), vs, k_new.shape[2],
+        None if n_new is None else _ints("n_new", n_new, 1, dev),
+        None if copies is None else _ints("copies", copies, 2, dev), _on(stream, dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_append")
+
+
+def cache_copy(k_cache, v_cache, copies, stream=None):
+    """Copies rows of pages, copies int32 [n, 3] of (from, to, rows), in both
+    caches through ``fa_cache_copy``."""
+    kc = _caches(k_cache, v_cache)
+    dev = k_cache.device
+    if copies.dim() != 2 or copies.shape[1] != 3:
+        raise ValueError("copies must be [n, 3]")
+    st = lib().fa_cache_copy(*kc, _ints("copies", copies, 2, dev), copies.shape[0],
+                             _on(stream, dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_copy")
+
+
+def cache_compact(k_cache, v_cache, block_table, start, keep, n_keep, stream=None):
+    """Key start[b] + a takes key start[b] + keep[b, a], a < n_keep[b], of both
+    caches through ``fa_cache_compact`` (keep int32 [B, n], strictly ascending):
+    the accepted nodes of a tree move together."""
+    kc = _caches(k_cache, v_cache)
+    dev = k_cache.device
+    B = start.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B or keep.dim() != 2 \
+            or keep.shape[0] != B or n_keep.shape != (B,):
+        raise ValueError("block_table must be [B, max_pages], start and n_keep [B], keep [B, n]")
+    st = lib().fa_cache_compact(
+        *kc, _ints("block_table", block_table, 2, dev), block_table.shape[1],
+        _ints("start", start, 1, dev), B, _ints("keep", keep, 2, dev), keep.shape[1],
+        _ints("n_keep", n_keep, 1, dev), _on(stream, dev))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_compact")
 
 
 def get_device_error(stream=None) -> int:

@@ -207,7 +207,14 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
                        int hq, int hkv, int sq, int sk, const int* seqlens_k, int head_dim,
                        float scale, int causal, int window, const float* sinks,
                        const int* block_table, int max_pages, int page_size, int num_pages,
-                       fa_stream_t stream, const Varlen* vl);
+                       fa_stream_t stream, const Varlen* vl, int first = 0);
+
+// Mask of a tree of query nodes (see fa_fwd_decode_tree).
+struct Tree {
+    const uint32_t* mask;
+    const int* lens;
+    bool shared;
+};
 
 // Query rows per kv head (G * sq) from which a decode call at head_dim 128
 // runs the head-packed prefill kernel instead of the split-KV kernel.  Past
@@ -223,12 +230,17 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
                       int hq, int hkv, int sq, int sk, const int* seqlens_k, int head_dim,
                       float scale, int causal, int window, const float* sinks, int num_splits,
                       fa_stream_t stream, const int* block_table = nullptr, int max_pages = 0,
-                      int page_size = 0, int num_pages = 0) {
+                      int page_size = 0, int num_pages = 0, int first = 0,
+                      const Tree* tree = nullptr) {
     Common c;
     fa_status st = check_common(q, k, v, o, lse, batch, hq, hkv, sq, sk, scale, c);
     if (st != FA_OK || c.noop) return st;
     if ((reinterpret_cast<uintptr_t>(sinks) & 3u) != 0) return FA_ERR_MISALIGNED;
-    if (sq > FA_DECODE_MAX_SQ) return FA_ERR_INVALID_ARG;
+    if (first < 0 || sq > (tree ? FA_TREE_MAX_NODES : FA_DECODE_MAX_SQ)) return FA_ERR_INVALID_ARG;
+    if (tree && !tree->mask) return FA_ERR_INVALID_ARG;
+    if (tree && ((reinterpret_cast<uintptr_t>(tree->mask) & 3u) != 0 ||
+                 (reinterpret_cast<uintptr_t>(tree->lens) & 3u) != 0))
+        return FA_ERR_MISALIGNED;
     if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FA_ERR_UNSUPPORTED;
     const long long q_elems = (long long)batch * hq * sq * head_dim;
     if (q_elems >= (1ll << 31)) return FA_ERR_INVALID_ARG;
@@ -236,14 +248,14 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     if (!di) return FA_ERR_CUDA;
     if (!di->supported) return FA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (sk == 0)
+    if (sk == 0 && !tree)
         return from_cuda(launch_fill_empty(static_cast<uint16_t*>(o), lse,
                                            (long long)batch * hq * sq, head_dim, sinks, hq, sq,
                                            s));
     // several queries of a GQA group (contiguous caches, no window, the
     // library's own split count): the prefill kernel with the group's heads
     // packed into one tile
-    if (num_splits <= 0 && block_table == nullptr && window <= 0 && head_dim == 128 &&
+    if (!tree && num_splits <= 0 && block_table == nullptr && window <= 0 && head_dim == 128 &&
         (hq / hkv) * sq >= kDecodeToPrefillRows)
         return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                             causal, 0, sinks, nullptr, 0, 0, 0, stream, nullptr);
@@ -265,6 +277,13 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     a.n_mtiles = (a.rows + 15) / 16;
     a.causal = causal ? 1 : 0;
     a.window = window > 0 ? window : 0;
+    a.first = window > 0 ? std::min(first, sk) : 0;
+    if (tree) {
+        a.tree_mask = tree->mask;
+        a.tree_lens = tree->lens;
+        a.tree_words = (sq + 31) / 32;
+        a.tree_stride = tree->shared ? 0 : (long long)sq * a.tree_words;
+    }
     a.sinks = sinks;
     a.block_table = block_table;
     a.max_pages = max_pages;
@@ -275,9 +294,12 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     // split planning: equal chunks of a multiple of 64 keys over the keys a
     // sequence's rows can see: all sk, or with a sliding window the last
     // window + sq - 1 (the splits start at each sequence's first visible key,
-    // rounded down to a multiple of 64: up to 63 more)
-    const long long span = a.window > 0 ? std::min<long long>(sk, (long long)a.window + sq + 62)
-                                        : (long long)sk;
+    // rounded down to a multiple of 64: up to 63 more), plus the first keys
+    // rounded up to one where they stay visible; at least 1 (a tree over no
+    // keys: the split kernel does nothing, the combine writes the rows)
+    const long long window_keys = (long long)a.window + sq + 62 + (a.first + 63ll) / 64 * 64;
+    const long long span =
+        std::max<long long>(1, a.window > 0 ? std::min<long long>(sk, window_keys) : (long long)sk);
     int splits = num_splits;
     if (splits <= 0) {
         const long long pairs = (long long)batch * hkv * a.n_mtiles;
@@ -320,10 +342,11 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
                        int hq, int hkv, int sq, int sk, const int* seqlens_k, int head_dim,
                        float scale, int causal, int window, const float* sinks,
                        const int* block_table, int max_pages, int page_size, int num_pages,
-                       fa_stream_t stream, const Varlen* vl = nullptr) {
+                       fa_stream_t stream, const Varlen* vl, int first) {
     Common c;
     fa_status st = check_common(q, k, v, o, lse, batch, hq, hkv, sq, sk, scale, c);
     if (st != FA_OK || c.noop) return st;
+    if (first < 0) return FA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(sinks) & 3u) != 0) return FA_ERR_MISALIGNED;
     if (!prefill_head_dim_ok(head_dim)) return FA_ERR_UNSUPPORTED;
     const DeviceInfo* di = device_info();
@@ -417,6 +440,7 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
     // tile; no gain measured at the other head dimensions)
     a.q_prefetch = head_dim == 256 ? di->num_sms : 0;
     a.window = window > 0 ? window : 0;
+    a.first = window > 0 ? first : 0;
     a.sinks = sinks;
     a.block_table = block_table;
     a.max_pages = max_pages;
@@ -474,14 +498,22 @@ fa_status fa_fwd_prefill_ex(const void* q, const void* k, const void* v, void* o
                             int head_dim, float scale, int causal, int window,
                             const float* sinks, fa_stream_t stream) {
     return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
-                        causal, window, sinks, nullptr, 0, 0, 0, stream);
+                        causal, window, sinks, nullptr, 0, 0, 0, stream, nullptr);
+}
+
+fa_status fa_fwd_prefill_first(const void* q, const void* k, const void* v, void* o, float* lse,
+                               int batch, int hq, int hkv, int sq, int sk, const int* seqlens_k,
+                               int head_dim, float scale, int causal, int window, int first,
+                               const float* sinks, fa_stream_t stream) {
+    return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
+                        causal, window, sinks, nullptr, 0, 0, 0, stream, nullptr, first);
 }
 
 fa_status fa_fwd_prefill(const void* q, const void* k, const void* v, void* o, float* lse,
                          int batch, int hq, int hkv, int sq, int sk, const int* seqlens_k,
                          int head_dim, float scale, int causal, fa_stream_t stream) {
     return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
-                        causal, 0, nullptr, nullptr, 0, 0, 0, stream);
+                        causal, 0, nullptr, nullptr, 0, 0, 0, stream, nullptr);
 }
 
 fa_status fa_fwd_prefill_paged(const void* q, const void* k_cache, const void* v_cache, void* o,
@@ -495,14 +527,15 @@ fa_status fa_fwd_prefill_paged(const void* q, const void* k_cache, const void* v
     if (page_size % 128 != 0) return FA_ERR_UNSUPPORTED;   // a key tile must fit a page
     return prefill_impl(q, k_cache, v_cache, o, lse, batch, hq, hkv, sq, max_pages * page_size,
                         seqlens_k, head_dim, scale, causal, 0, nullptr, block_table, max_pages,
-                        page_size, num_pages, stream);
+                        page_size, num_pages, stream, nullptr);
 }
 
-fa_status fa_fwd_prefill_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
-                                const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
-                                int max_seqlen_q, int max_seqlen_k, int total_q, int total_k,
-                                int hq, int hkv, int head_dim, float scale, int causal,
-                                int window, const float* sinks, fa_stream_t stream) {
+fa_status fa_fwd_prefill_varlen_first(const void* q, const void* k, const void* v, void* o,
+                                      float* lse, const int* cu_seqlens_q,
+                                      const int* cu_seqlens_k, int batch, int max_seqlen_q,
+                                      int max_seqlen_k, int total_q, int total_k, int hq, int hkv,
+                                      int head_dim, float scale, int causal, int window,
+                                      int first, const float* sinks, fa_stream_t stream) {
     if (batch < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || total_q < 0 || total_k < 0)
         return FA_ERR_INVALID_ARG;
     if (batch == 0 || total_q == 0 || hq == 0) return FA_OK;   // nothing to compute
@@ -517,16 +550,27 @@ fa_status fa_fwd_prefill_varlen(const void* q, const void* k, const void* v, voi
     const Varlen vl{cu_seqlens_q, cu_seqlens_k, total_q, total_k};
     return prefill_impl(q, k, v, o, lse, batch, hq, hkv, max_seqlen_q,
                         total_k > 0 ? max_seqlen_k : 0, nullptr, head_dim, scale, causal, window,
-                        sinks, nullptr, 0, 0, 0, stream, &vl);
+                        sinks, nullptr, 0, 0, 0, stream, &vl, first);
 }
 
-fa_status fa_fwd_prefill_varlen_paged(const void* q, const void* k_cache, const void* v_cache,
-                                      void* o, float* lse, const int* cu_seqlens_q,
-                                      const int* seqlens_k, const int* block_table,
-                                      int max_pages, int page_size, int num_pages, int batch,
-                                      int max_seqlen_q, int total_q, int hq, int hkv,
-                                      int head_dim, float scale, int causal, int window,
-                                      const float* sinks, fa_stream_t stream) {
+fa_status fa_fwd_prefill_varlen(const void* q, const void* k, const void* v, void* o, float* lse,
+                                const int* cu_seqlens_q, const int* cu_seqlens_k, int batch,
+                                int max_seqlen_q, int max_seqlen_k, int total_q, int total_k,
+                                int hq, int hkv, int head_dim, float scale, int causal,
+                                int window, const float* sinks, fa_stream_t stream) {
+    return fa_fwd_prefill_varlen_first(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, batch,
+                                       max_seqlen_q, max_seqlen_k, total_q, total_k, hq, hkv,
+                                       head_dim, scale, causal, window, 0, sinks, stream);
+}
+
+fa_status fa_fwd_prefill_varlen_paged_first(const void* q, const void* k_cache,
+                                            const void* v_cache, void* o, float* lse,
+                                            const int* cu_seqlens_q, const int* seqlens_k,
+                                            const int* block_table, int max_pages, int page_size,
+                                            int num_pages, int batch, int max_seqlen_q,
+                                            int total_q, int hq, int hkv, int head_dim,
+                                            float scale, int causal, int window, int first,
+                                            const float* sinks, fa_stream_t stream) {
     if (batch < 0 || max_seqlen_q < 0 || total_q < 0) return FA_ERR_INVALID_ARG;
     if (batch == 0 || total_q == 0 || hq == 0) return FA_OK;   // nothing to compute
     if (max_seqlen_q == 0 || !cu_seqlens_q) return FA_ERR_INVALID_ARG;
@@ -539,7 +583,20 @@ fa_status fa_fwd_prefill_varlen_paged(const void* q, const void* k_cache, const 
     const Varlen vl{cu_seqlens_q, nullptr, total_q, 0};
     return prefill_impl(q, k_cache, v_cache, o, lse, batch, hq, hkv, max_seqlen_q,
                         max_pages * page_size, seqlens_k, head_dim, scale, causal, window, sinks,
-                        block_table, max_pages, page_size, num_pages, stream, &vl);
+                        block_table, max_pages, page_size, num_pages, stream, &vl, first);
+}
+
+fa_status fa_fwd_prefill_varlen_paged(const void* q, const void* k_cache, const void* v_cache,
+                                      void* o, float* lse, const int* cu_seqlens_q,
+                                      const int* seqlens_k, const int* block_table,
+                                      int max_pages, int page_size, int num_pages, int batch,
+                                      int max_seqlen_q, int total_q, int hq, int hkv,
+                                      int head_dim, float scale, int causal, int window,
+                                      const float* sinks, fa_stream_t stream) {
+    return fa_fwd_prefill_varlen_paged_first(q, k_cache, v_cache, o, lse, cu_seqlens_q, seqlens_k,
+                                             block_table, max_pages, page_size, num_pages, batch,
+                                             max_seqlen_q, total_q, hq, hkv, head_dim, scale,
+                                             causal, window, 0, sinks, stream);
 }
 
 fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void* o, float* lse,
@@ -568,6 +625,52 @@ fa_status fa_fwd_decode_paged(const void* q, const void* k_cache, const void* v_
     return decode_impl(q, k_cache, v_cache, o, lse, batch, hq, hkv, sq, max_pages * page_size,
                        seqlens_k, head_dim, scale, causal, 0, nullptr, 0, stream, block_table,
                        max_pages, page_size, num_pages);
+}
+
+fa_status fa_fwd_decode_first(const void* q, const void* k, const void* v, void* o, float* lse,
+                              int batch, int hq, int hkv, int sq, int sk, const int* seqlens_k,
+                              int head_dim, float scale, int causal, int window, int first,
+                              const float* sinks, fa_stream_t stream) {
+    return decode_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
+                       causal, window, sinks, 0, stream, nullptr, 0, 0, 0, first);
+}
+
+fa_status fa_fwd_decode_paged_first(const void* q, const void* k_cache, const void* v_cache,
+                                    void* o, float* lse, int batch, int hq, int hkv, int sq,
+                                    const int* seqlens_k, const int* block_table, int max_pages,
+                                    int page_size, int num_pages, int head_dim, float scale,
+                                    int causal, int window, int first, const float* sinks,
+                                    fa_stream_t stream) {
+    fa_status st = check_paged(seqlens_k, block_table, max_pages, page_size, num_pages, batch, hq,
+                               sq);
+    if (st != FA_OK) return st;
+    return decode_impl(q, k_cache, v_cache, o, lse, batch, hq, hkv, sq, max_pages * page_size,
+                       seqlens_k, head_dim, scale, causal, window, sinks, 0, stream, block_table,
+                       max_pages, page_size, num_pages, first);
+}
+
+fa_status fa_fwd_decode_tree(const void* q, const void* k, const void* v, void* o, float* lse,
+                             int batch, int hq, int hkv, int nodes, int sk, const int* seqlens_k,
+                             const unsigned int* tree_mask, int shared_mask, const int* tree_lens,
+                             int head_dim, float scale, const float* sinks, fa_stream_t stream) {
+    const Tree tree{tree_mask, tree_lens, shared_mask != 0};
+    return decode_impl(q, k, v, o, lse, batch, hq, hkv, nodes, sk, seqlens_k, head_dim, scale, 0,
+                       0, sinks, 0, stream, nullptr, 0, 0, 0, 0, &tree);
+}
+
+fa_status fa_fwd_decode_tree_paged(const void* q, const void* k_cache, const void* v_cache,
+                                   void* o, float* lse, int batch, int hq, int hkv, int nodes,
+                                   const int* seqlens_k, const int* block_table, int max_pages,
+                                   int page_size, int num_pages, const unsigned int* tree_mask,
+                                   int shared_mask, const int* tree_lens, int head_dim,
+                                   float scale, const float* sinks, fa_stream_t stream) {
+    fa_status st = check_paged(seqlens_k, block_table, max_pages, page_size, num_pages, batch, hq,
+                               nodes);
+    if (st != FA_OK) return st;
+    const Tree tree{tree_mask, tree_lens, shared_mask != 0};
+    return decode_impl(q, k_cache, v_cache, o, lse, batch, hq, hkv, nodes, max_pages * page_size,
+                       seqlens_k, head_dim, scale, 0, 0, sinks, 0, stream, block_table, max_pages,
+                       page_size, num_pages, 0, &tree);
 }
 
 fa_status fa_fwd_decode_splits(const void* q, const void* k, const void* v, void* o, float* lse,

@@ -1,0 +1,570 @@
+// Operators on the pages of a key/value cache.
+//
+// A cache is what the paged attention reads: k_cache, v_cache
+// [num_pages, hkv, page_size, d] bf16 and a block table int32[batch,
+// max_pages] whose entry j is the page of keys [j page_size, (j + 1)
+// page_size) of its sequence, or -1.  refs int32[num_pages] counts the table
+// entries that hold a page (0: the page is free).  Everything lives on the
+// device, so that a serving step that forks, grows and frees sequences needs
+// no synchronisation and can be captured.
+//
+// Two kinds of kernels.  Table kernels (fork, reserve, free) read and write
+// only the integers; fork and reserve check everything first and change all
+// or nothing, free takes each entry by an atomic exchange so that a row
+// listed twice is freed once.  Row kernels (append, copy, compact) move
+// 16-byte granules of key and value rows; they are bound by the bytes moved,
+// each read once and written once.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/fa.h"
+
+namespace fa {
+namespace {
+
+constexpr int kTableThreads = 1024;
+
+__device__ __forceinline__ bool is_page(int e, int num_pages) {
+    return (unsigned)e < (unsigned)num_pages;
+}
+
+// Exclusive prefix sum over the block's kTableThreads threads, and the
+// total.  scratch: 33 ints of shared memory; two barriers inside.
+__device__ __forceinline__ int block_scan(int v, int* scratch, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();   // the last call's readers are done
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = scratch[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        scratch[lane] = w;
+    }
+    __syncthreads();
+    total = scratch[31];
+    return x - v + (warp > 0 ? scratch[warp - 1] : 0);
+}
+
+struct TableArgs {
+    int* refs;
+    int num_pages;
+    int* table;        // [batch, max_pages]
+    int max_pages;
+    int* lens;         // [batch]
+    int batch;
+    int* status;
+};
+
+// --------------------------------------------------------------- fork ----
+
+// One CTA.  Pass 1 checks the pairs, a warp each; pass 2 (if all passed)
+// copies the rows and counts the pages.
+__global__ void __launch_bounds__(kTableThreads)
+    cache_fork_kernel(const TableArgs t, const int* src, const int* dst, int n) {
+    __shared__ int bad;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) bad = n;
+    __syncthreads();
+    for (int i = warp; i < n; i += kTableThreads / 32) {
+        const int s = src[i], d = dst[i];
+        bool ok = (unsigned)s < (unsigned)t.batch && (unsigned)d < (unsigned)t.batch;
+        if (ok) {
+            if (t.lens[d] > 0) ok = false;
+            for (int j = lane; j < t.max_pages; j += 32)   // dst holds nothing
+                if (is_page(t.table[(size_t)d * t.max_pages + j], t.num_pages)) ok = false;
+            for (int j = lane; j < n; j += 32)   // nor is any pair's src or an earlier dst
+                if (src[j] == d || (j < i && dst[j] == d)) ok = false;
+        }
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicMin(&bad, i);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) *t.status = bad < n ? bad + 1 : 0;
+    if (bad < n) return;
+    for (int i = warp; i < n; i += kTableThreads / 32) {
+        const int* from = t.table + (size_t)src[i] * t.max_pages;
+        int* to = t.table + (size_t)dst[i] * t.max_pages;
+        for (int j = lane; j < t.max_pages; j += 32) {
+            const int e = from[j];
+            const bool held = is_page(e, t.num_pages);
+            to[j] = held ? e : -1;
+            if (held) atomicAdd(t.refs + e, 1);
+        }
+        if (lane == 0) t.lens[dst[i]] = t.lens[src[i]];
+    }
+}
+
+// --------------------------------------------------------------- free ----
+
+__global__ void __launch_bounds__(256)
+    cache_free_kernel(const TableArgs t, const int* rows, int n) {
+    for (int i = blockIdx.x; i < n; i += gridDim.x) {
+        const int r = rows[i];
+        if ((unsigned)r >= (unsigned)t.batch) continue;
+        for (int j = threadIdx.x; j < t.max_pages; j += blockDim.x) {
+            const int e = atomicExch(t.table + (size_t)r * t.max_pages + j, -1);
+            if (is_page(e, t.num_pages)) atomicSub(t.refs + e, 1);
+        }
+        if (threadIdx.x == 0) t.lens[r] = 0;
+    }
+}
+
+// ------------------------------------------------------------ reserve ----
+
+// Entries [first, last) of a row: its open page (the one its last keys fill in
+// part) and those that its next `extra` keys will be written to.
+struct Span {
+    int first, last;
+    bool fits;
+};
+__device__ __forceinline__ Span reserve_span(const TableArgs& t, const int* extra, int page_size,
+                                             int r) {
+    Span s{0, 0, true};
+    const long long len = max(t.lens[r], 0), more = extra[r];
+    if (more < 0) return s;
+    const long long last = (len + more + page_size - 1) / page_size;
+    s.fits = last <= t.max_pages;
+    s.first = (int)min(len / page_size, (long long)t.max_pages);
+    s.last = s.fits ? (int)last : s.first;
+    return s;
+}
+
+// One CTA.  Needed entries of a row's span are those that hold no page and
+// those whose page another entry shares (it would be written under the
+// other's eyes); in (row, entry) order they take the free pages in ascending
+// order.
+//   1  count the needed entries, a thread per row; shared ones are marked in
+//      the table as -2 - page and entries that are no page as -1, so that
+//      pass 3 sees the same set whatever it does to refs
+//   2  list the free pages, as many as are needed (ascending; the scan stops
+//      early)
+//   3  give them out, or take the marks back where they do not suffice
+__global__ void __launch_bounds__(kTableThreads)
+    cache_reserve_kernel(const TableArgs t, const int* extra, int page_size, int* copies,
+                         int* free_list) {
+    __shared__ int scratch[33];
+    __shared__ int long_row;   // first row whose span does not fit the table
+    if (threadIdx.x == 0) long_row = t.batch;
+    __syncthreads();
+    int needed = 0;
+    for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
+        const int r = r0 + threadIdx.x;
+        int count = 0;
+        if (r < t.batch) {
+            const Span s = reserve_span(t, extra, page_size, r);
+            if (!s.fits) atomicMin(&long_row, r);
+            int* row = t.table + (size_t)r * t.max_pages;
+            for (int j = s.first; j < s.last; ++j) {
+                const int e = row[j];
+                if (!is_page(e, t.num_pages)) {
+                    row[j] = -1;
+                    ++count;
+                } else if (t.refs[e] > 1) {
+                    row[j] = -2 - e;
+                    ++count;
+                }
+            }
+        }
+        int total;
+        block_scan(count, scratch, total);
+        needed += total;
+    }
+    int found = 0;
+    for (int p0 = 0; p0 < t.num_pages && found < needed; p0 += kTableThreads) {
+        const int p = p0 + threadIdx.x;
+        const int is_free = p < t.num_pages && t.refs[p] == 0;
+        int total;
+        const int k = found + block_scan(is_free, scratch, total);
+        if (is_free && k < needed) free_list[k] = p;
+        found += total;
+    }
+    const bool fits = long_row == t.batch;   // (the scans' barriers order it)
+    const bool grant = fits && found >= needed;
+    if (threadIdx.x == 0) *t.status = !fits ? -1 - long_row : (grant ? 0 : needed - found);
+    __syncthreads();   // free_list
+    int base = 0;
+    for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
+        const int r = r0 + threadIdx.x;
+        Span s{0, 0, true};
+        int* row = t.table + (size_t)r * t.max_pages;
+        int count = 0;
+        if (r < t.batch) {
+            s = reserve_span(t, extra, page_size, r);
+            for (int j = s.first; j < s.last; ++j) count += row[j] < 0;
+        }
+        int total;
+        int k = base + block_scan(count, scratch, total);
+        base += total;
+        if (r >= t.batch) continue;
+        int from = -1, to = -1, rows = 0;
+        for (int j = s.first; j < s.last; ++j) {
+            const int e = row[j];
+            if (e >= 0) continue;
+            if (!grant) {
+                if (e <= -2) row[j] = -2 - e;
+                continue;
+            }
+            const int page = free_list[k++];
+            row[j] = page;
+            t.refs[page] = 1;
+            if (e <= -2) {
+                atomicSub(t.refs + (-2 - e), 1);
+                const int used = t.lens[r] % page_size;
+                if (j == s.first && used > 0) {   // (lens[r] > 0 here)
+                    from = -2 - e;
+                    to = page;
+                    rows = used;
+                }
+            }
+        }
+        copies[3 * r] = from;
+        copies[3 * r + 1] = to;
+        copies[3 * r + 2] = rows;
+    }
+}
+
+// ------------------------------------------------------- append, copy ----
+
+struct RowArgs {
+    uint4* k;                  // caches, in 16-byte granules
+    uint4* v;
+    int num_pages, hkv, page_size, granules;   // granules of a row: d / 8
+    const int* table;
+    int max_pages;
+    const int* lens;
+    // append: k_new, v_new [batch, hkv, n, d] with strides (granules)
+    const uint4* k_new;
+    const uint4* v_new;
+    long long ks[3], vs[3];    // batch, head, token
+    int n;
+    const int* n_new;          // [batch] or nullptr (n)
+    const int* copies;         // [*, 3] or nullptr: source page, page, rows
+};
+
+constexpr int kRowThreads = 128;
+constexpr int kRowChunk = 64;   // rows of a head that one CTA moves
+
+// CTA (chunk of rows, head, batch entry).  First the entry's copy (rows
+// [0, c) of a page, c the third number of copies[b]), then its new rows;
+// the two never touch the same row.
+__global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const RowArgs a) {
+    const int b = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * kRowChunk;
+    const int G = a.granules;
+    if (a.copies != nullptr) {
+        const int src = a.copies[3 * b], dst = a.copies[3 * b + 1];
+        const int rows = min(min(a.copies[3 * b + 2], a.page_size), r0 + kRowChunk);
+        if (is_page(src, a.num_pages) && is_page(dst, a.num_pages) && src != dst && r0 < rows) {
+            const size_t row = (size_t)a.page_size * G;
+            const size_t s0 = ((size_t)src * a.hkv + h) * row, d0 = ((size_t)dst * a.hkv + h) * row;
+            for (int e = r0 * G + threadIdx.x; e < rows * G; e += kRowThreads) {
+                a.k[d0 + e] = a.k[s0 + e];
+                a.v[d0 + e] = a.v[s0 + e];
+            }
+        }
+    }
+    if (a.k_new == nullptr) return;
+    const int n = min(min(a.n_new != nullptr ? a.n_new[b] : a.n, a.n), r0 + kRowChunk);
+    if (r0 >= n) return;
+    const long long len = max(a.lens[b], 0);
+    for (int e = r0 * G + threadIdx.x; e < n * G; e += kRowThreads) {
+        const int i = e / G, g = e % G;
+        const long long pos = len + i;
+        if (pos >= (long long)a.max_pages * a.page_size) break;
+        const int page = a.table[(size_t)b * a.max_pages + pos / a.page_size];
+        if (!is_page(page, a.num_pages)) continue;
+        const size_t to =
+            (((size_t)page * a.hkv + h) * a.page_size + pos % a.page_size) * G + g;
+        a.k[to] = a.k_new[b * a.ks[0] + h * a.ks[1] + i * a.ks[2] + g];
+        a.v[to] = a.v_new[b * a.vs[0] + h * a.vs[1] + i * a.vs[2] + g];
+    }
+}
+
+// ------------------------------------------------------------ compact ----
+
+// CTA (head, batch entry): row start + keep[a] moves to row start + a.  keep
+// ascends strictly, so keep[a] >= a: a row written is never the source of a
+// later a, and rows of one round are all read before any is written.
+__global__ void __launch_bounds__(kRowThreads)
+    cache_compact_kernel(const RowArgs a, const int* start, const int* keep, int stride,
+                         const int* n_keep) {
+    const int b = blockIdx.y, h = blockIdx.x;
+    const int G = a.granules;
+    const int n = min(n_keep[b], stride);
+    const long long s0 = max(start[b], 0);
+    const long long limit = (long long)a.max_pages * a.page_size;
+    const int* table = a.table + (size_t)b * a.max_pages;
+    const int* kp = keep + (size_t)b * stride;
+    auto row = [&](long long pos, size_t& at) -> bool {
+        if (pos < 0 || pos >= limit) return false;
+        const int page = table[pos / a.page_size];
+        if (!is_page(page, a.num_pages)) return false;
+        at = (((size_t)page * a.hkv + h) * a.page_size + pos % a.page_size) * G;
+        return true;
+    };
+    for (int e0 = 0; e0 < n * G; e0 += kRowThreads) {
+        const int e = e0 + threadIdx.x;
+        size_t from = 0, to = 0;
+        bool move = e < n * G;
+        uint4 kx, vx;
+        if (move) {
+            const int i = e / G, g = e % G, x = kp[i];
+            move = x > i && row(s0 + x, from) && row(s0 + i, to);
+            if (move) {
+                kx = a.k[from + g];
+                vx = a.v[from + g];
+                to += g;
+            }
+        }
+        __syncthreads();
+        if (move) {
+            a.k[to] = kx;
+            a.v[to] = vx;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------- tree mask ----
+
+// Words of a tree's ancestor mask: node i sees itself and every node on the
+// way up, parent after parent (parents[i] < i; anything else ends the walk,
+// so a cycle cannot be followed).  A thread per (tree, node, word).
+__global__ void __launch_bounds__(256)
+    tree_mask_kernel(const int* parents, unsigned int* mask, int batch, int nodes, int words) {
+    const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= (long long)batch * nodes * words) return;
+    const int w = (int)(e % words), i = (int)(e / words % nodes);
+    const int* p = parents + e / words / nodes * nodes;
+    unsigned int bits = 0;
+    for (int x = i; x >= 0;) {
+        if ((x >> 5) == w) bits |= 1u << (x & 31);
+        if ((x >> 5) < w) break;
+        const int up = p[x];
+        x = up < x ? up : -1;
+    }
+    mask[e] = bits;
+}
+
+// -------------------------------------------------------------- host ----
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// The kernels of this library are compiled for sm_103 only.
+fa_status device_ok() {
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return major == 10 && minor == 3 ? FA_OK : FA_ERR_UNSUPPORTED;
+}
+
+fa_status check_table(const TableArgs& t, bool need_status) {
+    if (t.num_pages < 0 || t.max_pages < 0 || t.batch < 0) return FA_ERR_INVALID_ARG;
+    if (t.batch > 0 && (!t.table || !t.lens || !t.refs)) return FA_ERR_INVALID_ARG;
+    if (need_status && !t.status) return FA_ERR_INVALID_ARG;
+    if (!aligned4(t.refs) || !aligned4(t.table) || !aligned4(t.lens) || !aligned4(t.status))
+        return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+// Checks of the caches and their table; noop where there is nothing to move.
+fa_status check_rows(const RowArgs& a, int batch, int head_dim, bool need_table) {
+    if (batch < 0 || a.num_pages < 0 || a.hkv < 0 || a.page_size < 0 || a.max_pages < 0 ||
+        a.n < 0)
+        return FA_ERR_INVALID_ARG;
+    if (batch > 65535 || a.hkv > 65535) return FA_ERR_INVALID_ARG;
+    if (head_dim <= 0 || head_dim % 8 != 0) return FA_ERR_UNSUPPORTED;
+    if (batch == 0 || a.num_pages == 0 || a.hkv == 0 || a.page_size == 0) return FA_OK;
+    if (!a.k || !a.v || (need_table && (!a.table || !a.lens))) return FA_ERR_INVALID_ARG;
+    // positions and the indexes of a head's granules stay below 2^31
+    if ((long long)a.max_pages * a.page_size >= (1ll << 31) ||
+        (long long)a.page_size * (head_dim / 8) >= (1ll << 31) ||
+        (long long)a.n * (head_dim / 8) >= (1ll << 31))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(a.k) || !aligned16(a.v) || !aligned4(a.table) || !aligned4(a.lens))
+        return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_cache_fork(int* refs, int num_pages, int* block_table, int max_pages, int* seqlens,
+                        int batch, const int* src, const int* dst, int n, int* status,
+                        fa_stream_t stream) {
+    const TableArgs t{refs, num_pages, block_table, max_pages, seqlens, batch, status};
+    fa_status st = check_table(t, true);
+    if (st != FA_OK) return st;
+    if (n < 0 || (n > 0 && (!src || !dst))) return FA_ERR_INVALID_ARG;
+    if (!aligned4(src) || !aligned4(dst)) return FA_ERR_MISALIGNED;
+    if ((st = device_ok()) != FA_OK) return st;
+    cache_fork_kernel<<<1, kTableThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(t, src, dst,
+                                                                                       n);
+    return launched();
+}
+
+fa_status fa_cache_free(int* refs, int num_pages, int* block_table, int max_pages, int* seqlens,
+                        int batch, const int* rows, int n, fa_stream_t stream) {
+    const TableArgs t{refs, num_pages, block_table, max_pages, seqlens, batch, nullptr};
+    fa_status st = check_table(t, false);
+    if (st != FA_OK) return st;
+    if (n < 0 || (n > 0 && !rows)) return FA_ERR_INVALID_ARG;
+    if (!aligned4(rows)) return FA_ERR_MISALIGNED;
+    if (n == 0 || batch == 0) return FA_OK;
+    if ((st = device_ok()) != FA_OK) return st;
+    cache_free_kernel<<<n < 4096 ? n : 4096, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        t, rows, n);
+    return launched();
+}
+
+fa_status fa_cache_reserve(int* refs, int num_pages, int* block_table, int max_pages,
+                           const int* seqlens, int batch, const int* extra, int page_size,
+                           int* copies, int* status, fa_stream_t stream) {
+    const TableArgs t{refs, num_pages, block_table, max_pages, const_cast<int*>(seqlens), batch,
+                      status};
+    fa_status st = check_table(t, true);
+    if (st != FA_OK) return st;
+    if (page_size <= 0 || (batch > 0 && (!extra || !copies))) return FA_ERR_INVALID_ARG;
+    if ((long long)max_pages * page_size >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    if (!aligned4(extra) || !aligned4(copies)) return FA_ERR_MISALIGNED;
+    if ((st = device_ok()) != FA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    long long entries = (long long)batch * max_pages;
+    if (entries > num_pages) entries = num_pages;
+    void* list = nullptr;
+    if (entries > 0 && cudaMallocAsync(&list, entries * sizeof(int), s) != cudaSuccess)
+        return FA_ERR_CUDA;
+    cache_reserve_kernel<<<1, kTableThreads, 0, s>>>(t, extra, page_size, copies,
+                                                     static_cast<int*>(list));
+    st = launched();
+    if (list != nullptr && cudaFreeAsync(list, s) != cudaSuccess) return FA_ERR_CUDA;
+    return st;
+}
+
+fa_status fa_cache_append(void* k_cache, void* v_cache, int num_pages, int hkv, int page_size,
+                          int head_dim, const int* block_table, int max_pages, const int* seqlens,
+                          int batch, const void* k_new, const long long* k_strides,
+                          const void* v_new, const long long* v_strides, int n, const int* n_new,
+                          const int* copies, fa_stream_t stream) {
+    RowArgs a{};
+    a.k = static_cast<uint4*>(k_cache);
+    a.v = static_cast<uint4*>(v_cache);
+    a.num_pages = num_pages;
+    a.hkv = hkv;
+    a.page_size = page_size;
+    a.granules = head_dim / 8;
+    a.table = block_table;
+    a.max_pages = max_pages;
+    a.lens = seqlens;
+    a.n = n;
+    a.n_new = n_new;
+    a.copies = copies;
+    fa_status st = check_rows(a, batch, head_dim, true);
+    if (st != FA_OK) return st;
+    if (!aligned4(n_new) || !aligned4(copies)) return FA_ERR_MISALIGNED;
+    if (batch == 0 || num_pages == 0 || hkv == 0 || page_size == 0) return FA_OK;
+    if (n > 0) {
+        if (!k_new || !v_new || !k_strides || !v_strides) return FA_ERR_INVALID_ARG;
+        if (!aligned16(k_new) || !aligned16(v_new)) return FA_ERR_MISALIGNED;
+        for (int i = 0; i < 3; ++i) {
+            if (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0) return FA_ERR_MISALIGNED;
+            a.ks[i] = k_strides[i] / 8;
+            a.vs[i] = v_strides[i] / 8;
+        }
+        a.k_new = static_cast<const uint4*>(k_new);
+        a.v_new = static_cast<const uint4*>(v_new);
+    } else if (!copies) {
+        return FA_OK;
+    }
+    if ((st = device_ok()) != FA_OK) return st;
+    int rows = n;
+    if (copies && page_size > rows) rows = page_size;
+    const dim3 grid((unsigned)((rows + kRowChunk - 1) / kRowChunk), (unsigned)hkv, (unsigned)batch);
+    cache_append_kernel<<<grid, kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return launched();
+}
+
+fa_status fa_cache_copy(void* k_cache, void* v_cache, int num_pages, int hkv, int page_size,
+                        int head_dim, const int* copies, int n, fa_stream_t stream) {
+    RowArgs a{};
+    a.k = static_cast<uint4*>(k_cache);
+    a.v = static_cast<uint4*>(v_cache);
+    a.num_pages = num_pages;
+    a.hkv = hkv;
+    a.page_size = page_size;
+    a.granules = head_dim / 8;
+    a.copies = copies;
+    fa_status st = check_rows(a, n, head_dim, false);
+    if (st != FA_OK) return st;
+    if (n == 0 || num_pages == 0 || hkv == 0 || page_size == 0) return FA_OK;
+    if (!copies) return FA_ERR_INVALID_ARG;
+    if (!aligned4(copies)) return FA_ERR_MISALIGNED;
+    if ((st = device_ok()) != FA_OK) return st;
+    const dim3 grid((unsigned)((page_size + kRowChunk - 1) / kRowChunk), (unsigned)hkv,
+                    (unsigned)n);
+    cache_append_kernel<<<grid, kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return launched();
+}
+
+fa_status fa_cache_compact(void* k_cache, void* v_cache, int num_pages, int hkv, int page_size,
+                           int head_dim, const int* block_table, int max_pages, const int* start,
+                           int batch, const int* keep, int keep_stride, const int* n_keep,
+                           fa_stream_t stream) {
+    RowArgs a{};
+    a.k = static_cast<uint4*>(k_cache);
+    a.v = static_cast<uint4*>(v_cache);
+    a.num_pages = num_pages;
+    a.hkv = hkv;
+    a.page_size = page_size;
+    a.granules = head_dim / 8;
+    a.table = block_table;
+    a.max_pages = max_pages;
+    a.lens = start;
+    a.n = keep_stride;
+    fa_status st = check_rows(a, batch, head_dim, true);
+    if (st != FA_OK) return st;
+    if (batch == 0 || num_pages == 0 || hkv == 0 || page_size == 0 || keep_stride == 0)
+        return FA_OK;
+    if (!keep || !n_keep) return FA_ERR_INVALID_ARG;
+    if (!aligned4(keep) || !aligned4(n_keep)) return FA_ERR_MISALIGNED;
+    if ((st = device_ok()) != FA_OK) return st;
+    cache_compact_kernel<<<dim3((unsigned)hkv, (unsigned)batch), kRowThreads, 0,
+                           reinterpret_cast<cudaStream_t>(stream)>>>(a, start, keep, keep_stride,
+                                                                     n_keep);
+    return launched();
+}
+
+fa_status fa_tree_mask(const int* parents, unsigned int* mask, int batch, int nodes,
+                       fa_stream_t stream) {
+    if (batch < 0 || nodes < 0 || nodes > FA_TREE_MAX_NODES) return FA_ERR_INVALID_ARG;
+    if (batch == 0 || nodes == 0) return FA_OK;
+    if (!parents || !mask) return FA_ERR_INVALID_ARG;
+    if (!aligned4(parents) || !aligned4(mask)) return FA_ERR_MISALIGNED;
+    const int words = (nodes + 31) / 32;
+    const long long blocks = ((long long)batch * nodes * words + 255) / 256;
+    if (blocks >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    fa_status st = device_ok();
+    if (st != FA_OK) return st;
+    tree_mask_kernel<<<(unsigned)blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        parents, mask, batch, nodes, words);
+    return launched();
+}
+
+}  // extern "C"

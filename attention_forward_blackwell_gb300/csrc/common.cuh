@@ -26,6 +26,7 @@ struct PrefillArgs {
     int B, Hq, Hkv, Sq, Sk;
     int group;                  // Hq / Hkv
     int window;                 // sliding window in keys (<= 0: none)
+    int first;                  // with a window: keys [0, first) stay visible (0: none)
     const float* sinks;         // [Hq] sink logits (scaled-score units) or nullptr
     // Paged K/V (nullptr: contiguous [B, Hkv, Sk, d]): the caches are
     // [num_pages, Hkv, page_size, d] and key j of sequence b is row
@@ -230,6 +231,16 @@ struct DecodeArgs {
     int chunk;                  // keys per split (multiple of 64)
     int causal;
     int window;                 // sliding window in keys (<= 0: none)
+    int first;                  // with a window: keys [0, first) stay visible (0: none)
+    // Tree of query nodes (tree_mask not null): the last t_b = tree_lens[b]
+    // (null: Sq) keys of a sequence are its query rows' own; row i sees every
+    // key before them and node j where bit j % 32 of
+    // tree_mask[b * tree_stride + i * tree_words + j / 32] is set.  Rows
+    // i >= t_b are not written.
+    const uint32_t* tree_mask;
+    const int* tree_lens;
+    int tree_words;
+    long long tree_stride;      // words per batch entry (0: one mask for all)
     const float* sinks;         // [Hq] sink logits (scaled-score units) or nullptr
     // Paged K/V (nullptr: contiguous): caches [num_pages, Hkv, page_size, d],
     // key j of sequence b at row j % page_size of page

@@ -55,7 +55,38 @@ __device__ __forceinline__ uint32_t swz(int key, int g) {
     return (uint32_t)(key * DecodeTraits<D>::ROW + ((g ^ (key & 7)) << 4));
 }
 
-template <int D, bool PAGED>
+// What a query row sees (an instance of each kernel per mode, so that the
+// plain one pays for none of the others).
+enum DecodeMode {
+    kModePlain = 0,   // every key, or a causal limit and / or a sliding window
+    kModeFirst = 1,   // a sliding window whose first `first` keys stay visible
+    kModeTree = 2     // a tree of query nodes (DecodeArgs::tree_mask)
+};
+
+// Keys of a sequence of L keys that the splits of kModeFirst walk: positions
+// [0, span) stand for the keys [0, head) and then [base, L).  head: the first
+// keys rounded up to a multiple of 64; base: the first key any query row's
+// window holds, rounded down to one (16-key slices then never straddle the
+// gap).  Where the two meet there is no gap: head = 0, base = 0.
+struct FirstSpan {
+    int head, base, span;
+    __device__ __forceinline__ int key(int x) const { return x < head ? x : x - head + base; }
+};
+__device__ __forceinline__ FirstSpan first_span(const DecodeArgs& a, int L) {
+    FirstSpan f;
+    f.base = max(0, L - a.Sq - a.window + 1) & ~63;
+    f.head = ((a.first - 1) | 63) + 1;
+    if (a.first > L || f.head >= f.base) f.head = f.base = 0;
+    f.span = f.head + L - f.base;
+    return f;
+}
+
+// Nodes of sequence b (kModeTree).
+__device__ __forceinline__ int tree_nodes(const DecodeArgs& a, int b) {
+    return a.tree_lens != nullptr ? max(0, min(a.tree_lens[b], a.Sq)) : a.Sq;
+}
+
+template <int D, bool PAGED, int MODE>
 __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     decode_split_kernel(const DecodeArgs a) {
     using T = DecodeTraits<D>;
@@ -70,10 +101,17 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     // splits start at the first key any query row of the sequence can see,
     // rounded down to a multiple of 64 (with a sliding window, the keys
     // before it are never read; the rounding keeps 16-key slices aligned)
-    const int k_base = (a.window > 0) ? (max(0, L - a.Sq - a.window + 1) & ~63) : 0;
+    // (kModeFirst: k_lo, k_hi and the slices' key0 below are positions of its
+    // FirstSpan)
+    FirstSpan fs{0, 0, L};
+    if constexpr (MODE == kModeFirst) fs = first_span(a, L);
+    const int k_base =
+        (MODE == kModePlain && a.window > 0) ? (max(0, L - a.Sq - a.window + 1) & ~63) : 0;
     const int k_lo = k_base + split * a.chunk;
-    if (k_lo >= L) return;                       // nothing of this sequence here
-    const int k_hi = min(k_lo + a.chunk, L);
+    if (k_lo >= fs.span) return;                 // nothing of this sequence here
+    const int k_hi = min(k_lo + a.chunk, fs.span);
+    const int nodes = MODE == kModeTree ? tree_nodes(a, b) : 0;
+    const int node0 = L - nodes;                 // key of node 0
     const int nblk = (k_hi - k_lo + T::KB - 1) / T::KB;
     const int my_blocks = nblk > warp ? (nblk - warp + T::WARPS - 1) / T::WARPS : 0;
 
@@ -86,6 +124,11 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
         const int pr = rbase + (lane >> 2) + 8 * hrow;
         if (pr < a.rows) {
             const int g = pr / a.Sq, i = pr % a.Sq;
+            if (MODE == kModeTree && i >= nodes) {   // a row past the tree: padding
+                qi[hrow] = -1;
+                qoff[hrow] = -1;
+                continue;
+            }
             qi[hrow] = i;
             qoff[hrow] = ((b * a.Hq + hkv * a.group + g) * a.Sq + i) * D;
         } else {
@@ -115,8 +158,9 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     int lo_min = 0x7fffffff;
 #pragma unroll
     for (int hrow = 0; hrow < 2; ++hrow) {
-        lim[hrow] = k_hi - 1;
-        if (a.causal && qi[hrow] >= 0) lim[hrow] = min(lim[hrow], qi[hrow] + L - a.Sq);
+        lim[hrow] = MODE == kModeFirst ? L - 1 : k_hi - 1;
+        if (MODE != kModeTree && a.causal && qi[hrow] >= 0)
+            lim[hrow] = min(lim[hrow], qi[hrow] + L - a.Sq);
         lo[hrow] = (a.window > 0 && qi[hrow] >= 0) ? qi[hrow] + L - a.Sq - a.window + 1 : 0;
         if (qi[hrow] >= 0) lo_min = min(lo_min, lo[hrow]);
     }
@@ -126,7 +170,10 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, 4));
     lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, 8));
     lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, 16));
-    if (k_hi <= lo_min) return;
+    if (MODE == kModePlain && k_hi <= lo_min) return;
+    // first key that some row's window holds: between the first keys and it
+    // no row sees anything, and nothing is read
+    const int lo_all = MODE == kModeFirst ? max(0, L - a.Sq - a.window + 1) : 0;
 
     const uint32_t wbase = smem_u32(smem) + warp * T::WARP_BYTES;
     const size_t head_off = ((size_t)b * a.Hkv + hkv) * (size_t)a.Sk * D;
@@ -148,14 +195,18 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
         const int key0 = k_lo + T::KB * (warp + T::WARPS * i);
         const uint32_t sk = wbase + stage * 2 * T::SLICE;
         const uint32_t sv = sk + T::SLICE;
-        const size_t slice_off = slice_pages ? row_off(key0) : 0;
+        const size_t slice_off = slice_pages ? row_off(fs.key(key0)) : 0;
 #pragma unroll
         for (int e = lane; e < T::KB * T::GRAN; e += 32) {
             const int kr = e / T::GRAN, g = e % T::GRAN;
             const int key = key0 + kr;
-            const bool valid = key < k_hi;
+            bool valid = key < k_hi;
+            if constexpr (MODE == kModeFirst) {
+                const int x = fs.key(key);
+                valid = valid && (x >= lo_all || x < a.first);
+            }
             const size_t src = (slice_pages ? slice_off + (size_t)(valid ? kr : 0) * D
-                                            : row_off(valid ? key : k_lo)) + g * 8;
+                                            : row_off(fs.key(valid ? key : k_lo))) + g * 8;
             cp_async_16(sk + swz<D>(kr, g), a.k + src, valid ? 16u : 0u);
             cp_async_16(sv + swz<D>(kr, g), a.v + src, valid ? 16u : 0u);
         }
@@ -206,7 +257,23 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
                 for (int e = 0; e < 2; ++e) {
                     const int key = key0 + n * 8 + 2 * (lane & 3) + e;
                     float& sv_ = sacc[n][2 * hrow + e];
-                    sv_ = (key <= lim[hrow] && key >= lo[hrow]) ? sv_ : -INFINITY;
+                    bool vis;
+                    if constexpr (MODE == kModeFirst) {
+                        const int x = fs.key(key);
+                        vis = key < k_hi && x <= lim[hrow] && (x >= lo[hrow] || x < a.first);
+                    } else if constexpr (MODE == kModeTree) {
+                        vis = key <= lim[hrow];
+                        if (vis && key >= node0 && qi[hrow] >= 0) {
+                            const int j = key - node0;
+                            const uint32_t word =
+                                a.tree_mask[b * a.tree_stride +
+                                            (long long)qi[hrow] * a.tree_words + (j >> 5)];
+                            vis = (word >> (j & 31)) & 1u;
+                        }
+                    } else {
+                        vis = key <= lim[hrow] && key >= lo[hrow];
+                    }
+                    sv_ = vis ? sv_ : -INFINITY;
                     mx = fmaxf(mx, sv_);
                 }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -294,6 +361,7 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
         for (int w = 0; w < T::WARPS; ++w) M = fmaxf(M, wm[w * 16 + r]);
         const int pr = rbase + r;
         const int g = pr / a.Sq, qi_ = pr % a.Sq;
+        if (MODE == kModeTree && qi_ >= nodes) continue;
         const size_t row_id = ((size_t)b * a.Hq + hkv * a.group + g) * a.Sq + qi_;
         const size_t part = (size_t)split * a.B * a.Hq * a.Sq + row_id;
         float o = 0.f, lse2 = -INFINITY;
@@ -316,7 +384,7 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
 // One warp per query row (b, hq, i): LSE-weighted merge of the splits that
 // reach the row's keys, plus the row's attention sink (one more term of the
 // normaliser without a value) if there is one.
-template <int D>
+template <int D, int MODE>
 __global__ void __launch_bounds__(256) decode_combine_kernel(const DecodeArgs a) {
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -327,15 +395,25 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const DecodeArgs a)
     const int i = (int)(row % a.Sq);
     int L = a.Sk;
     if (a.seqlens_k != nullptr) L = max(0, min(a.seqlens_k[b], a.Sk));
-    // the row's visible keys [k_first, k_last]
-    int k_last = L - 1;
-    if (a.causal) k_last = min(k_last, i + L - a.Sq);
-    const int k_first = (a.window > 0) ? max(0, i + L - a.Sq - a.window + 1) : 0;
-    // the splits start at the sequence's first visible key, rounded down to a
-    // multiple of 64 (see the split kernel)
-    const int k_base = (a.window > 0) ? (max(0, L - a.Sq - a.window + 1) & ~63) : 0;
-    const int s_lo = (k_first - k_base) / a.chunk;
-    const int ns = (k_last >= k_first) ? (L - k_base + a.chunk - 1) / a.chunk : 0;
+    int s_lo = 0, ns;
+    if constexpr (MODE == kModePlain) {
+        // the row's visible keys [k_first, k_last]
+        int k_last = L - 1;
+        if (a.causal) k_last = min(k_last, i + L - a.Sq);
+        const int k_first = (a.window > 0) ? max(0, i + L - a.Sq - a.window + 1) : 0;
+        // the splits start at the sequence's first visible key, rounded down
+        // to a multiple of 64 (see the split kernel)
+        const int k_base = (a.window > 0) ? (max(0, L - a.Sq - a.window + 1) & ~63) : 0;
+        s_lo = (k_first - k_base) / a.chunk;
+        ns = (k_last >= k_first) ? (L - k_base + a.chunk - 1) / a.chunk : 0;
+    } else if constexpr (MODE == kModeFirst) {
+        // every split of the sequence's span was written (-inf where the row
+        // sees none of its keys)
+        ns = (first_span(a, L).span + a.chunk - 1) / a.chunk;
+    } else {
+        if (i >= tree_nodes(a, b)) return;   // a row past the tree stays as it was
+        ns = (L + a.chunk - 1) / a.chunk;
+    }
     const size_t stride = (size_t)a.B * a.Hq * a.Sq;
     const float sg = (a.sinks != nullptr) ? a.sinks[h] * kLog2ef : -INFINITY;
     float M = sg;
@@ -365,11 +443,11 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const DecodeArgs a)
     if (lane == 0) a.lse[row] = (wsum > 0.f) ? (M + lg2_approx(wsum)) * kLn2f : -INFINITY;
 }
 
-template <int D>
-cudaError_t launch_decode_impl(const DecodeArgs& a, cudaStream_t s) {
+template <int D, int MODE>
+cudaError_t launch_decode_mode(const DecodeArgs& a, cudaStream_t s) {
     using T = DecodeTraits<D>;
-    void (*split)(DecodeArgs) =
-        a.block_table != nullptr ? decode_split_kernel<D, true> : decode_split_kernel<D, false>;
+    void (*split)(DecodeArgs) = a.block_table != nullptr ? decode_split_kernel<D, true, MODE>
+                                                         : decode_split_kernel<D, false, MODE>;
     cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          T::SMEM);
     if (e != cudaSuccess) return e;
@@ -378,8 +456,15 @@ cudaError_t launch_decode_impl(const DecodeArgs& a, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const long long rows = (long long)a.B * a.Hq * a.Sq;
-    decode_combine_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
+    decode_combine_kernel<D, MODE><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
     return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_decode_impl(const DecodeArgs& a, cudaStream_t s) {
+    if (a.tree_mask != nullptr) return launch_decode_mode<D, kModeTree>(a, s);
+    if (a.window > 0 && a.first > 0) return launch_decode_mode<D, kModeFirst>(a, s);
+    return launch_decode_mode<D, kModePlain>(a, s);
 }
 
 // ------------------------------------------------------ auxiliary kernels ----

@@ -267,6 +267,7 @@ struct PrefillWork {
     int n_kv[2];   // key blocks of this piece visited by Q tile 0 / 1
     int n_max;
     int kb;        // first key block of the piece (0 for a whole unit)
+    int nf;        // leading blocks [0, nf) visited before it (WINDOW == 2)
     int piece;     // -1 for a whole unit, else the piece's scratch slot
     int tail;      // tail unit of the piece (its merge counter)
     // packed sequences only: query rows of the sequence, and its first query
@@ -275,10 +276,26 @@ struct PrefillWork {
     int dv0;       // first output column of this CTA (0 unless DV_SPLIT > 1)
 };
 
-template <class T, bool CAUSAL, bool WINDOW, bool VARLEN>
+// WINDOW (of every kernel template below): 0 no window, 1 a sliding window,
+// 2 a sliding window whose first PrefillArgs::first keys stay visible.  With
+// 2 a unit visits the key blocks [0, nf) that hold those first keys and then,
+// skipping what lies between, its window's blocks from kb on; where the two
+// meet, nf is 0 and the blocks run from 0.  The causal limit never cuts the
+// leading blocks: kb > 0 only when the unit's first row stands in a block
+// >= kb >= nf.
+
+// Key block of a unit's (or piece's) j-th step.
+template <int WINDOW>
+__device__ __forceinline__ int key_block(const PrefillWork& w, int j) {
+    if constexpr (WINDOW == 2) return j < w.nf ? j : w.kb - w.nf + j;
+    return w.kb + j;
+}
+
+template <class T, bool CAUSAL, int WINDOW, bool VARLEN>
 __device__ __forceinline__ PrefillWork prefill_work(const PrefillArgs& a, int c) {
     PrefillWork w;
     w.dv0 = 0;
+    w.nf = 0;
     if constexpr (T::DV_SPLIT > 1) {
         w.dv0 = (c % T::DV_SPLIT) * T::D_COLS;
         c /= T::DV_SPLIT;
@@ -340,6 +357,10 @@ __device__ __forceinline__ PrefillWork prefill_work(const PrefillArgs& a, int c)
         // no row of the unit sees a key below its first row's window
         const int lo_min = w.row0 + w.off - a.window + 1;
         if (lo_min > 0) w.kb = max(w.kb, lo_min / T::BN);
+        if constexpr (WINDOW == 2) {
+            w.nf = (a.first - 1) / T::BN + 1;
+            if (w.nf >= w.kb) w.nf = w.kb = 0;
+        }
     }
     w.n_kv[0] = w.n_kv[1] = 0;
 #pragma unroll
@@ -348,7 +369,7 @@ __device__ __forceinline__ PrefillWork prefill_work(const PrefillArgs& a, int c)
         if (CAUSAL) last = min(last, w.row0 + (t + 1) * T::BM - 1 + w.off);
         const int n = last >= 0 ? last / T::BN + 1 : 0;
         const int cnt = min(n, ke) - w.kb;
-        w.n_kv[t] = cnt > 0 ? cnt : 0;
+        w.n_kv[t] = cnt > 0 ? cnt + w.nf : 0;
         // a tile past the end of its sequence has nothing to compute
         if (VARLEN && w.row0 + t * T::BM >= w.Lq) w.n_kv[t] = 0;
     }
@@ -356,7 +377,7 @@ __device__ __forceinline__ PrefillWork prefill_work(const PrefillArgs& a, int c)
     return w;
 }
 
-template <class T, bool CAUSAL, bool WINDOW, bool VARLEN>
+template <class T, bool CAUSAL, int WINDOW, bool VARLEN>
 __device__ __forceinline__ void prefetch_q_of(const CUtensorMap* tm_q, const PrefillArgs& a,
                                               int c2) {
     const PrefillWork w2 = prefill_work<T, CAUSAL, WINDOW, VARLEN>(a, c2);
@@ -404,7 +425,7 @@ __device__ __forceinline__ uint32_t ring_phase(int p) { return (uint32_t)((p / T
 
 // L2 prefetch of the Q tiles of the unit that CTA c2 (a later CTA of the
 // grid) will process; issued by the producer lane after its own first loads.
-template <class T, bool CAUSAL, bool WINDOW, bool VARLEN>
+template <class T, bool CAUSAL, int WINDOW, bool VARLEN>
 __device__ __forceinline__ void prefetch_q_of(const CUtensorMap* tm_q, const PrefillArgs& a,
                                               int c2);
 
@@ -462,7 +483,7 @@ __device__ __forceinline__ void zero_value_rows(uint32_t slot_addr, int r0) {
 
 // ------------------------------------------------------------ producer ----
 
-template <class T, bool CAUSAL, bool WINDOW, bool VARLEN>
+template <class T, bool CAUSAL, int WINDOW, bool VARLEN>
 __device__ void prefill_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                                   const CUtensorMap* tm_v, const PrefillArgs& a,
                                   const PrefillWork& w, PrefillAux<T>* aux, uint32_t sQ,
@@ -505,7 +526,7 @@ __device__ void prefill_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm
             break;
         trace_mark(tr, kTrLoad, p >> 3, p & 7);
         const uint32_t full = smem_u32(&aux->bar_full[slot]);
-        const int jk = w.kb + j;          // key block
+        const int jk = key_block<WINDOW>(w, j);
         const int rv = w.L - jk * T::BN;  // valid rows of this tile
         int ty, tz;
         coords(jk, ty, tz);
@@ -800,7 +821,7 @@ __device__ void prefill_mma_role(int tq, const PrefillArgs& a, const PrefillWork
 // V_j.  A partial last value tile is zeroed past the sequence end before it
 // is published; `ntail` counts those copies (the parity of bar_tail).
 // Executed by the producer warp (lane 0 issues).
-template <class T, bool VARLEN>
+template <class T, int WINDOW, bool VARLEN>
 __device__ __forceinline__ bool load_piece(const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                            const PrefillArgs& a, const PrefillWork& w,
                                            PrefillAux<T>* aux, uint32_t sRing, const WaitCtx& wc,
@@ -814,7 +835,7 @@ __device__ __forceinline__ bool load_piece(const CUtensorMap* tm_k, const CUtens
     trace_mark(tr, kTrLoad, p >> 4, p & 15);   // position p's copy issued
     const uint32_t full = smem_u32(&aux->bar_full[slot]);
     const uint32_t dst = sRing + slot * T::SLOT;
-    const int jk = w.kb + j;
+    const int jk = key_block<WINDOW>(w, j);
     const int rv = w.L - jk * T::BN;
     int ty = (VARLEN ? w.k0 : 0) + jk * T::BN, tz = VARLEN ? w.hk : w.b * a.Hkv + w.hk;
     if (a.block_table != nullptr) {
@@ -866,7 +887,7 @@ __device__ __forceinline__ bool load_piece(const CUtensorMap* tm_k, const CUtens
 }
 
 // Producer: Q once, then the pieces in consumption order.
-template <class T, bool CAUSAL, bool WINDOW, bool VARLEN>
+template <class T, bool CAUSAL, int WINDOW, bool VARLEN>
 __device__ void prefill_load_role_dv(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                                      const CUtensorMap* tm_v, const PrefillArgs& a,
                                      const PrefillWork& w, PrefillAux<T>* aux, uint32_t sQ,
@@ -886,7 +907,7 @@ __device__ void prefill_load_role_dv(const CUtensorMap* tm_q, const CUtensorMap*
     int p = 0;       // ring position of the next piece
     int ntail = 0;   // partial value pieces loaded so far
     auto load = [&](int j, bool is_v, int pc) -> bool {
-        return load_piece<T, VARLEN>(tm_k, tm_v, a, w, aux, sRing, wc, tr, j, is_v, pc, p, ntail);
+        return load_piece<T, WINDOW, VARLEN>(tm_k, tm_v, a, w, aux, sRing, wc, tr, j, is_v, pc, p, ntail);
     };
     bool ok = true;
     for (int pc = 0; pc < T::PIECES && ok; ++pc) ok = load(0, false, pc);
@@ -1241,7 +1262,7 @@ __device__ void softmax_epilogue_part(int t, const CUtensorMap* tm_o, const Pref
 // this CTA processes; J0 counts the key blocks of its earlier units, and the
 // barriers, mailboxes and score buffers are indexed by the CTA-wide block
 // index J0 + j.
-template <class T, bool CAUSAL, bool WINDOW, bool VARLEN, bool PERSIST = false>
+template <class T, bool CAUSAL, int WINDOW, bool VARLEN, bool PERSIST = false>
 __device__ void prefill_softmax_role(int t, const CUtensorMap* tm_o, const PrefillArgs& a,
                                      const PrefillWork& w, PrefillAux<T>* aux, uint32_t tmem,
                                      uint32_t sQ, const WaitCtx& wc, unsigned long long* tr,
@@ -1254,10 +1275,13 @@ __device__ void prefill_softmax_role(int t, const CUtensorMap* tm_o, const Prefi
     const int row = w.row0 + t * T::BM + r;
     int lim = w.L - 1;                                       // last visible key of this row
     if (CAUSAL) lim = min(lim, row + w.off);
-    lim -= w.kb * T::BN;   // keys counted from the piece's first key block
+    // keys counted from the piece's first key block (WINDOW == 2: from key 0,
+    // because the blocks visited are not consecutive)
+    const int key_org = WINDOW == 2 ? 0 : w.kb * T::BN;
+    lim -= key_org;
     // first visible key of this row (sliding window), same origin; the
     // kernels without a window compile none of this
-    const int lo = WINDOW ? row + w.off - a.window + 1 - w.kb * T::BN : 0;
+    const int lo = WINDOW ? row + w.off - a.window + 1 - key_org : 0;
     const float sl2 = a.scale_log2;
     const int nk = w.n_kv[t];
     float m_run = -INFINITY;   // running max of scaled scores, log2 units (the basis)
@@ -1289,15 +1313,20 @@ __device__ void prefill_softmax_role(int t, const CUtensorMap* tm_o, const Prefi
 #pragma unroll
         for (int c = 0; c < 128; ++c) s[c] = __uint_as_float(u[c >> 5][c & 31]);
         // mask: only tiles that reach past this row's last visible key
-        const int kv0 = j * T::BN;   // relative to the piece's first key (lim is too)
-        const bool masked = lim - kv0 < T::BN - 1 || (WINDOW && lo - kv0 > 0);
+        // first key of the block, in the origin of lim and lo
+        const int kv0 = (WINDOW == 2 ? key_block<WINDOW>(w, j) : j) * T::BN;
+        const bool masked =
+            lim - kv0 < T::BN - 1 ||
+            (WINDOW && lo - kv0 > 0 && (WINDOW != 2 || a.first - kv0 < T::BN));
         const bool warp_masked = __any_sync(0xffffffffu, masked);
         if (masked) {
             const int nvis = lim - kv0 + 1;                  // visible columns [c0, nvis)
             const int c0 = WINDOW ? lo - kv0 : 0;
+            const int cf = WINDOW == 2 ? a.first - kv0 : 0;   // columns below it: first keys
 #pragma unroll
             for (int c = 0; c < 128; ++c)
-                s[c] = (c < nvis && (!WINDOW || c >= c0)) ? s[c] : -INFINITY;
+                s[c] = (c < nvis && (!WINDOW || c >= c0 || (WINDOW == 2 && c < cf))) ? s[c]
+                                                                                     : -INFINITY;
         }
         // row max: four independent 3-input-max chains, then combine
         float mq[4];
@@ -1710,7 +1739,7 @@ __device__ void prefill_correction_role(const CUtensorMap* tm_o, const PrefillAr
 
 // --------------------------------------------------------------- kernel ----
 
-template <int D, bool CAUSAL, bool WINDOW, bool VARLEN>
+template <int D, bool CAUSAL, int WINDOW, bool VARLEN>
 __global__ void __launch_bounds__(PrefillTraits<D>::THREADS, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
@@ -1832,7 +1861,7 @@ __device__ __forceinline__ int persist_unit(int i, int x, int G) {
     return i * G + ((i & 1) ? G - 1 - x : x);
 }
 
-template <class T, bool CAUSAL, bool WINDOW>
+template <class T, bool CAUSAL, int WINDOW>
 __device__ void prefill_load_role_persist(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                                           const CUtensorMap* tm_v, const PrefillArgs& a,
                                           PrefillAux<T>* aux, uint32_t sQ, uint32_t sRing,
@@ -1854,8 +1883,8 @@ __device__ void prefill_load_role_persist(const CUtensorMap* tm_q, const CUtenso
         const PrefillWork w = prefill_work<T, CAUSAL, WINDOW, false>(a, u);
         if (w.n_max <= 0) continue;
         auto load = [&](int j, bool is_v, int pc) -> bool {
-            return load_piece<T, false>(tm_k, tm_v, a, w, aux, sRing, wc, tr, j, is_v, pc, p,
-                                        ntail);
+            return load_piece<T, WINDOW, false>(tm_k, tm_v, a, w, aux, sRing, wc, tr, j, is_v,
+                                                pc, p, ntail);
         };
         // K_0 first: its slots are free while the previous unit's last
         // score MMA still reads Q
@@ -1891,7 +1920,7 @@ __device__ void prefill_load_role_persist(const CUtensorMap* tm_q, const CUtenso
 // MMA issue over the CTA's units.  Block J of the CTA uses score buffer
 // J & 1; S(J) waits for PV(J - 2), the last reader of that buffer's P, also
 // across a unit boundary.
-template <class T, bool CAUSAL, bool WINDOW>
+template <class T, bool CAUSAL, int WINDOW>
 __device__ void prefill_mma_role_persist(const PrefillArgs& a, PrefillAux<T>* aux, uint32_t tmem,
                                          uint32_t sQ, uint32_t sRing, const WaitCtx& wc,
                                          unsigned long long* tr) {
@@ -2024,7 +2053,7 @@ __device__ void write_empty_unit(const PrefillArgs& a, const PrefillWork& w) {
             (lf > 0.f) ? (mf + lg2_approx(lf)) * kLn2 : -INFINITY;
 }
 
-template <int D, bool CAUSAL, bool WINDOW>
+template <int D, bool CAUSAL, int WINDOW>
 __global__ void __launch_bounds__(PrefillTraits<D>::THREADS, 1)
     prefill_kernel_persist(const __grid_constant__ CUtensorMap tm_q,
                            const __grid_constant__ CUtensorMap tm_k,
@@ -2144,24 +2173,28 @@ namespace fa {
 using PrefillKernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, PrefillArgs);
 
 template <int D, bool VARLEN>
-PrefillKernelFn pick_prefill_kernel(bool causal, bool window) {
-    return window ? (causal ? prefill_kernel<D, true, true, VARLEN> : prefill_kernel<D, false, true, VARLEN>)
-                  : (causal ? prefill_kernel<D, true, false, VARLEN>
-                            : prefill_kernel<D, false, false, VARLEN>);
+PrefillKernelFn pick_prefill_kernel(bool causal, int window) {
+    if (window == 2)
+        return causal ? prefill_kernel<D, true, 2, VARLEN> : prefill_kernel<D, false, 2, VARLEN>;
+    return window ? (causal ? prefill_kernel<D, true, 1, VARLEN> : prefill_kernel<D, false, 1, VARLEN>)
+                  : (causal ? prefill_kernel<D, true, 0, VARLEN>
+                            : prefill_kernel<D, false, 0, VARLEN>);
 }
 
 template <int D>
 cudaError_t launch_prefill_impl(const PrefillLaunch& p, cudaStream_t stream) {
     using T = PrefillTraits<D>;
-    const bool window = p.args.window > 0;
+    const int window = p.args.window > 0 ? (p.args.first > 0 ? 2 : 1) : 0;
     if constexpr (D == 256) {
         // dense launches of whole units: one persistent CTA per SM
         if (p.args.cu_seqlens_q == nullptr && p.n_tail == 0 && p.num_sms > 0 && p.args.n_full > 0) {
             const PrefillKernelFn kern =
-                window ? (p.causal ? prefill_kernel_persist<D, true, true>
-                                   : prefill_kernel_persist<D, false, true>)
-                       : (p.causal ? prefill_kernel_persist<D, true, false>
-                                   : prefill_kernel_persist<D, false, false>);
+                window == 2 ? (p.causal ? prefill_kernel_persist<D, true, 2>
+                                        : prefill_kernel_persist<D, false, 2>)
+                : window    ? (p.causal ? prefill_kernel_persist<D, true, 1>
+                                        : prefill_kernel_persist<D, false, 1>)
+                            : (p.causal ? prefill_kernel_persist<D, true, 0>
+                                        : prefill_kernel_persist<D, false, 0>);
             cudaError_t e = cudaFuncSetAttribute(
                 kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_TOTAL);
             if (e != cudaSuccess) return e;

@@ -222,6 +222,7 @@ __device__ __forceinline__ PrefillWork wide_work(const PrefillArgs& a, int u) {
         const int n = last >= 0 ? last / T::BN + 1 : 0;
         const int cnt = min(n, ke) - kb;
         w.kb = kb;
+        w.nf = 0;
         w.n_kv[0] = w.n_kv[1] = cnt > 0 ? cnt : 0;
         w.n_max = w.n_kv[0];
         w.Lq = w.q0 = w.k0 = 0;

@@ -249,6 +249,165 @@ fa_status fa_fwd_decode_ex(const void *q, const void *k, const void *v, void *o,
                            int window, const float *sinks, fa_stream_t stream);
 
 /*
+ * A sliding window whose first keys stay visible (for every window call: dense
+ * and packed prefill, packed prefill over paged caches, decode over contiguous
+ * and over paged caches).  With window > 0 and first > 0, key j is visible to
+ * query row i, which stands at key p = i + (L_b - sq), if
+ *     j < L_b,  j <= p (causal),  and  j > p - window  or  j < first.
+ * With window <= 0 or first = 0 the calls are the ones without `_first`
+ * (fa_fwd_decode_paged_first: paged decode with a window and sinks).  Only the
+ * key blocks that hold the first keys and those of the window are visited, so
+ * time and traffic do not grow with the sequence.  The prefill kernels read
+ * whole blocks of 128 keys: within the first block(s) and the blocks of the
+ * window, keys j < L_b must be finite even where they are masked (a masked
+ * key's probability, zero, multiplies its value row).  Decode reads only keys
+ * that some query row of the sequence sees.  first < 0: FA_ERR_INVALID_ARG.
+ */
+fa_status fa_fwd_prefill_first(const void *q, const void *k, const void *v, void *o,
+                               float *lse, int batch, int hq, int hkv, int sq, int sk,
+                               const int *seqlens_k, int head_dim, float scale, int causal,
+                               int window, int first, const float *sinks, fa_stream_t stream);
+fa_status fa_fwd_prefill_varlen_first(const void *q, const void *k, const void *v, void *o,
+                                      float *lse, const int *cu_seqlens_q,
+                                      const int *cu_seqlens_k, int batch, int max_seqlen_q,
+                                      int max_seqlen_k, int total_q, int total_k, int hq, int hkv,
+                                      int head_dim, float scale, int causal, int window,
+                                      int first, const float *sinks, fa_stream_t stream);
+fa_status fa_fwd_prefill_varlen_paged_first(const void *q, const void *k_cache,
+                                            const void *v_cache, void *o, float *lse,
+                                            const int *cu_seqlens_q, const int *seqlens_k,
+                                            const int *block_table, int max_pages, int page_size,
+                                            int num_pages, int batch, int max_seqlen_q,
+                                            int total_q, int hq, int hkv, int head_dim,
+                                            float scale, int causal, int window, int first,
+                                            const float *sinks, fa_stream_t stream);
+fa_status fa_fwd_decode_first(const void *q, const void *k, const void *v, void *o, float *lse,
+                              int batch, int hq, int hkv, int sq, int sk, const int *seqlens_k,
+                              int head_dim, float scale, int causal, int window, int first,
+                              const float *sinks, fa_stream_t stream);
+fa_status fa_fwd_decode_paged_first(const void *q, const void *k_cache, const void *v_cache,
+                                    void *o, float *lse, int batch, int hq, int hkv, int sq,
+                                    const int *seqlens_k, const int *block_table, int max_pages,
+                                    int page_size, int num_pages, int head_dim, float scale,
+                                    int causal, int window, int first, const float *sinks,
+                                    fa_stream_t stream);
+
+/* Most nodes of a tree (query rows of a sequence) of the tree calls. */
+#define FA_TREE_MAX_NODES 1024
+
+/*
+ * Attention of a tree of drafted tokens over a cache, all nodes in one pass.
+ * Sequence b has t_b = tree_lens[b] nodes (tree_lens NULL: `nodes`; clamped to
+ * [0, nodes]); their keys are the sequence's last t_b keys, in node order.
+ * Node i sees every key before the tree (j < L_b - t_b) and node n of the
+ * tree iff bit n % 32 of word n / 32 of its mask row is set:
+ *     q, o       : [batch, hq, nodes, head_dim] bf16; lse [batch, hq, nodes]
+ *     tree_mask  : device uint32[batch, nodes, ceil(nodes / 32)], or with
+ *                  shared_mask nonzero uint32[nodes, ceil(nodes / 32)], the
+ *                  same tree for every sequence; fa_tree_mask makes it from
+ *                  parents, and any other pattern is allowed
+ *     seqlens_k  : as everywhere (L_b counts the nodes' keys)
+ *     sinks      : NULL or per-head sink logits (see fa_fwd_prefill_ex)
+ * Rows i >= t_b of o and lse are not written.  A node that sees no key gets
+ * O = 0 and LSE = -inf (or the sink).  Keys j < L_b must be finite even where
+ * they are masked.  head_dim 64, 128 or 256; nodes <= FA_TREE_MAX_NODES;
+ * batch * hq * nodes * head_dim < 2^31.  Scratch is stream-ordered, as in
+ * fa_fwd_decode.  The paged call takes the caches, block table and page sizes
+ * of fa_fwd_decode_paged.
+ */
+fa_status fa_fwd_decode_tree(const void *q, const void *k, const void *v, void *o, float *lse,
+                             int batch, int hq, int hkv, int nodes, int sk, const int *seqlens_k,
+                             const unsigned int *tree_mask, int shared_mask, const int *tree_lens,
+                             int head_dim, float scale, const float *sinks, fa_stream_t stream);
+fa_status fa_fwd_decode_tree_paged(const void *q, const void *k_cache, const void *v_cache,
+                                   void *o, float *lse, int batch, int hq, int hkv, int nodes,
+                                   const int *seqlens_k, const int *block_table, int max_pages,
+                                   int page_size, int num_pages, const unsigned int *tree_mask,
+                                   int shared_mask, const int *tree_lens, int head_dim,
+                                   float scale, const float *sinks, fa_stream_t stream);
+
+/*
+ * Mask words of trees given by their parents: parents int32[batch, nodes],
+ * parents[i] < i the node that node i continues, or -1 (anything that is not
+ * a smaller node counts as -1); mask uint32[batch, nodes, ceil(nodes / 32)]:
+ * each node sees itself and the nodes on its way up.
+ */
+fa_status fa_tree_mask(const int *parents, unsigned int *mask, int batch, int nodes,
+                       fa_stream_t stream);
+
+/*
+ * Pages of a cache.  The state is what the paged attention calls read, plus a
+ * count per page:
+ *     block_table : int32[batch, max_pages], a page or -1 (any value outside
+ *                   [0, num_pages) is no page)
+ *     seqlens     : int32[batch], keys of each row
+ *     refs        : int32[num_pages], the number of table entries that hold
+ *                   the page; 0: free
+ * all on the device, changed in place; nothing synchronises, so the calls can
+ * be captured.  The table calls change only the integers; a model's layers
+ * share them, and each layer's caches follow with fa_cache_append /
+ * fa_cache_copy / fa_cache_compact.
+ *
+ * fa_cache_fork: row dst[i] becomes a copy of row src[i] that shares all its
+ *   pages (refs + 1 each) and has its length.  Every dst row must hold no page
+ *   and have length 0, be listed once and be no pair's src; a src may repeat.
+ *   Checked on the device before anything changes: *status = 0 and all pairs
+ *   are done, or *status = 1 + i for the first pair i refused and none is.
+ * fa_cache_reserve: room for extra[b] more keys of each row (negative: the row
+ *   is left alone).  The row's entries from its open page, seqlens[b] /
+ *   page_size, up to that of key seqlens[b] + extra[b] - 1 become its own: an
+ *   entry without a page gets a free one, and an entry whose page other
+ *   entries hold too gets a free one in its stead (copy on write: the others
+ *   keep the old page; two rows that share a page and both reserve both get
+ *   new ones).  With extra[b] = 0 that is a partly filled page, if any.
+ *   Free pages are given in ascending order to the entries in (row, entry)
+ *   order; a page given up is free from the next call on.  seqlens is not
+ *   changed.  copies int32[batch, 3] receives (old page, new page, rows) for
+ *   each row whose last keys lie in a page that was replaced, (-1, -1, 0) for
+ *   the others.  *status = 0; or, with nothing reserved (copies then hold
+ *   -1, -1, 0), the number of pages that are lacking, or -1 - b for the first
+ *   row b whose table row is too short.
+ * fa_cache_free: the rows' pages are given up (refs - 1), their entries
+ *   become -1, their lengths 0.  Rows may repeat; rows outside [0, batch) are
+ *   skipped.
+ * fa_cache_append: row r of the caches' keys seqlens[b] + i takes
+ *   k_new[b, :, i] and v_new[b, :, i] for i < n_new[b] (NULL: n; at most n),
+ *   [batch, hkv, n, head_dim] with strides of batch, head and token in
+ *   elements (multiples of 8; the last dimension is contiguous).  With copies
+ *   (as fa_cache_reserve wrote them) the copies of these rows' pages are made
+ *   in the same launch.  Keys without a page are skipped.  Rows must have
+ *   been reserved: a page that another row holds too is written as it is.
+ * fa_cache_copy: rows [0, r) of page `from` of both caches to page `to`, for
+ *   copies int32[n, 3] of (from, to, r); entries that are no page are
+ *   skipped.  No page may be written by one copy and read or written by
+ *   another.
+ * fa_cache_compact: key start[b] + a takes the rows of key start[b] +
+ *   keep[b * keep_stride + a] for a < n_keep[b] (at most keep_stride): the
+ *   accepted path of a tree moves together.  keep must ascend strictly.
+ *   Lengths and pages are the caller's to update.
+ * head_dim is a multiple of 8; caches and new rows are 16-byte aligned.
+ */
+fa_status fa_cache_fork(int *refs, int num_pages, int *block_table, int max_pages, int *seqlens,
+                        int batch, const int *src, const int *dst, int n, int *status,
+                        fa_stream_t stream);
+fa_status fa_cache_reserve(int *refs, int num_pages, int *block_table, int max_pages,
+                           const int *seqlens, int batch, const int *extra, int page_size,
+                           int *copies, int *status, fa_stream_t stream);
+fa_status fa_cache_free(int *refs, int num_pages, int *block_table, int max_pages, int *seqlens,
+                        int batch, const int *rows, int n, fa_stream_t stream);
+fa_status fa_cache_append(void *k_cache, void *v_cache, int num_pages, int hkv, int page_size,
+                          int head_dim, const int *block_table, int max_pages, const int *seqlens,
+                          int batch, const void *k_new, const long long *k_strides,
+                          const void *v_new, const long long *v_strides, int n, const int *n_new,
+                          const int *copies, fa_stream_t stream);
+fa_status fa_cache_copy(void *k_cache, void *v_cache, int num_pages, int hkv, int page_size,
+                        int head_dim, const int *copies, int n, fa_stream_t stream);
+fa_status fa_cache_compact(void *k_cache, void *v_cache, int num_pages, int hkv, int page_size,
+                           int head_dim, const int *block_table, int max_pages, const int *start,
+                           int batch, const int *keep, int keep_stride, const int *n_keep,
+                           fa_stream_t stream);
+
+/*
  * fa_fwd_decode with an explicit number of key splits (num_splits <= 0 picks
  * it automatically, exactly like fa_fwd_decode).  The splits partition
  * [0, sk) into equal chunks of a multiple of 64 keys; any split count gives
