@@ -88,6 +88,8 @@ class FaError(RuntimeError):
 def lib(path: str | None = None):
     """Load the CUDA library (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -112,13 +114,20 @@ def version() -> int:
     return lib().fa_version()
 
 
+# Handle of a device's current stream.  A small call is bound by its Python
+# half: torch.cuda.current_stream() builds a Stream object (2.9 us on the
+# host of a GB300), this call does not (0.1 us).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream_ptr(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else None
+    return t.data_ptr() if t is not None else None
 
 
 def _check_inputs(q, k, v, seqlens_k):
@@ -359,66 +368,85 @@ def decode_paged(q, k_cache, v_cache, block_table, seqlens_k, scale=None, causal
 
 
 # ------------------------------------------- trees of drafted tokens, cache pages ----
+#
+# These calls are made once per layer and step on small tensors, so their
+# checks are kept to a few attribute reads each.
 
-def _on(stream, device):
-    """The stream to launch on (the device's current one) for tensors of
-    ``device``, which has to be the current device."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device")
-    return _stream_ptr(stream)
-
-
-def _ints(name, t, dim, device):
-    """Checks an int32 tensor of ``dim`` dimensions that a kernel reads or writes in place."""
-    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {dim} dimension(s) on {device}")
-    return _ptr(t)
+_I32, _BF16 = torch.int32, torch.bfloat16
+_Strides = ctypes.c_longlong * 3
 
 
-def _tree_args(q, k, v, tree_mask, tree_lens, sinks, scale, out, lse):
-    dev = q.device
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
+def _device(name, t):
+    """Index of the CUDA device that holds t, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _on(stream, dev):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _ints(name, t, shape, dev):
+    """Address of a contiguous int32 tensor that a kernel reads or writes in place."""
+    if t.dtype is not _I32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{dev}, "
+                         f"not {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _tree_call(q, k, v, dev, mask, tree_lens, sinks, scale, out, lse):
+    """Checks and arguments that both tree calls share: (q, k, v, o, lse) and
+    (mask, shared, tree_lens, d, scale) as the library takes them, sinks, out
+    and lse."""
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not _BF16:
             raise TypeError(f"{name} must be bfloat16")
-        if t.device != dev or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 4-D tensor on {dev}")
+        if t.get_device() != dev or t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 4-D tensor on cuda:{dev}")
     B, Hq, T, d = q.shape
     if v.shape != k.shape or k.shape[3] != d:
         raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
     words = (T + 31) // 32
-    shared = tree_mask.dim() == 2
-    if tuple(tree_mask.shape) != ((T, words) if shared else (B, T, words)):
-        raise ValueError(f"tree_mask must be [{B}, {T}, {words}] or [{T}, {words}]")
-    mask = _ints("tree_mask", tree_mask, 2 if shared else 3, dev)
-    if tree_lens is not None and tree_lens.shape != (B,):
-        raise ValueError("tree_lens must be [B]")
-    if sinks is not None and sinks.device != dev:
-        raise ValueError(f"sinks must be on {dev}")
-    out, lse = _outputs(q, out, lse)
-    if out.device != dev or lse.device != dev:
-        raise ValueError(f"out and lse must be on {dev}")
-    return (mask, int(shared),
-            None if tree_lens is None else _ints("tree_lens", tree_lens, 1, dev), d,
-            1.0 / math.sqrt(d) if scale is None else float(scale)), _check_sinks(sinks, Hq), out, lse
+    shared = mask.dim() == 2
+    mask = _ints("tree_mask", mask, (T, words) if shared else (B, T, words), dev)
+    if tree_lens is not None:
+        tree_lens = _ints("tree_lens", tree_lens, (B,), dev)
+    if sinks is not None:
+        if sinks.get_device() != dev:
+            raise ValueError(f"sinks must be on cuda:{dev}")
+        sinks = _check_sinks(sinks, Hq)
+    if out is None:
+        out = torch.empty_like(q)
+    elif (out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != dev
+          or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bf16 tensor shaped like q, on its device")
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    elif (lse.shape != (B, Hq, T) or lse.dtype is not torch.float32 or lse.get_device() != dev
+          or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, T] on q's device")
+    return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr()),
+            (mask, int(shared), tree_lens, d, 1.0 / math.sqrt(d) if scale is None else float(scale)),
+            sinks, out, lse)
 
 
 def tree_mask(parents, out=None, stream=None):
     """Mask words int32 [B, T, ceil(T / 32)] of trees given by their parents
     int32 [B, T] through ``fa_tree_mask``: node i sees itself and the nodes on
     its way up (bit j % 32 of word j / 32)."""
-    if not parents.is_cuda:
-        raise ValueError("parents must be a CUDA tensor")
-    src = _ints("parents", parents, 2, parents.device)
+    dev = _device("parents", parents)
+    if parents.dim() != 2:
+        raise ValueError("parents must be [B, T]")
     B, T = parents.shape
-    words = (T + 31) // 32
+    shape = (B, T, (T + 31) // 32)
     if out is None:
-        out = torch.empty((B, T, words), dtype=torch.int32, device=parents.device)
-    dst = _ints("out", out, 3, parents.device)
-    if out.shape != (B, T, words):
-        raise ValueError(f"out must be [{B}, {T}, {words}]")
-    st = lib().fa_tree_mask(src, dst, B, T, _on(stream, parents.device))
+        out = torch.empty(shape, dtype=_I32, device=parents.device)
+    st = lib().fa_tree_mask(_ints("parents", parents, (B, T), dev), _ints("out", out, shape, dev), B, T,
+                            _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_tree_mask")
     return out
@@ -432,16 +460,17 @@ def decode_tree(q, k, v, tree_mask, scale=None, seqlens_k=None, tree_lens=None, 
     before the tree and the nodes of its mask bits, tree_mask int32
     [B, T, ceil(T / 32)] or [T, ceil(T / 32)].  Returns (o, lse); rows past a
     tree's nodes are not written."""
-    more, sinks, out, lse = _tree_args(q, k, v, tree_mask, tree_lens, sinks, scale, out, lse)
+    dev = _device("q", q)
+    tensors, more, sinks, out, lse = _tree_call(q, k, v, dev, tree_mask, tree_lens, sinks, scale,
+                                                out, lse)
     B, Hq, T, d = q.shape
-    if k.shape[0] != B:
+    Bk, Hkv, Sk, _ = k.shape
+    if Bk != B:
         raise ValueError("k and v must have q's batch")
-    if seqlens_k is not None and seqlens_k.shape != (B,):
-        raise ValueError("seqlens_k must be [B]")
-    lens = None if seqlens_k is None else _ints("seqlens_k", seqlens_k, 1, q.device)
-    st = lib().fa_fwd_decode_tree(_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq,
-                                  k.shape[1], T, k.shape[2], lens, *more, _ptr(sinks),
-                                  _on(stream, q.device))
+    if seqlens_k is not None:
+        seqlens_k = _ints("seqlens_k", seqlens_k, (B,), dev)
+    st = lib().fa_fwd_decode_tree(*tensors, B, Hq, Hkv, T, Sk, seqlens_k, *more, _ptr(sinks),
+                                  _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_decode_tree")
     return out, lse
@@ -451,40 +480,34 @@ def decode_tree_paged(q, k_cache, v_cache, block_table, seqlens_k, tree_mask, sc
                       tree_lens=None, sinks=None, out=None, lse=None, stream=None):
     """``decode_tree`` over paged caches [num_pages, Hkv, page_size, d] through
     ``fa_fwd_decode_tree_paged``; returns (o, lse)."""
-    more, sinks, out, lse = _tree_args(q, k_cache, v_cache, tree_mask, tree_lens, sinks, scale, out,
-                                       lse)
+    dev = _device("q", q)
+    tensors, more, sinks, out, lse = _tree_call(q, k_cache, v_cache, dev, tree_mask, tree_lens, sinks,
+                                                scale, out, lse)
     B, Hq, T, d = q.shape
     num_pages, Hkv, page_size, _ = k_cache.shape
-    table = _ints("block_table", block_table, 2, q.device)
-    if block_table.shape[0] != B or seqlens_k.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and seqlens_k [B]")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    width = block_table.shape[1]
     st = lib().fa_fwd_decode_tree_paged(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), B, Hq, Hkv, T,
-        _ints("seqlens_k", seqlens_k, 1, q.device), table, block_table.shape[1], page_size,
-        num_pages, *more, _ptr(sinks), _on(stream, q.device))
+        *tensors, B, Hq, Hkv, T, _ints("seqlens_k", seqlens_k, (B,), dev),
+        _ints("block_table", block_table, (B, width), dev), width, page_size, num_pages, *more,
+        _ptr(sinks), _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_decode_tree_paged")
     return out, lse
 
 
 def _table(refs, block_table, seqlens):
-    if not block_table.is_cuda:
-        raise ValueError("block_table must be a CUDA tensor")
-    dev = block_table.device
-    B, max_pages = block_table.shape if block_table.dim() == 2 else (-1, -1)
-    if seqlens.dim() != 1 or seqlens.numel() != B:
-        raise ValueError("block_table must be [B, max_pages] and seqlens [B]")
-    return (_ints("refs", refs, 1, dev), refs.numel(), _ints("block_table", block_table, 2, dev),
-            max_pages, _ints("seqlens", seqlens, 1, dev), B)
-
-
-def _status(status, device):
-    if status is None:
-        return torch.empty(1, dtype=torch.int32, device=device)
-    _ints("status", status, 1, device)
-    if status.numel() != 1:
-        raise ValueError("status must be [1]")
-    return status
+    """The device and the arguments refs, num_pages, block_table, max_pages,
+    seqlens, batch of the table calls."""
+    dev = _device("block_table", block_table)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, width = block_table.shape
+    pages = refs.numel()
+    return dev, (_ints("refs", refs, (pages,), dev), pages,
+                 _ints("block_table", block_table, (B, width), dev), width,
+                 _ints("seqlens", seqlens, (B,), dev), B)
 
 
 def cache_fork(refs, block_table, seqlens, src, dst, status=None, stream=None):
@@ -492,13 +515,12 @@ def cache_fork(refs, block_table, seqlens, src, dst, status=None, stream=None):
     refs [num_pages], block_table [B, max_pages] and seqlens [B] (int32) change
     in place.  Returns status int32 [1]: 0, or 1 + the first pair refused
     (nothing is changed then)."""
-    dev = block_table.device
-    args = _table(refs, block_table, seqlens)
-    if src.shape != dst.shape:
-        raise ValueError("src and dst must have the same length")
-    status = _status(status, dev)
-    st = lib().fa_cache_fork(*args, _ints("src", src, 1, dev), _ints("dst", dst, 1, dev),
-                             src.numel(), _ptr(status), _on(stream, dev))
+    dev, args = _table(refs, block_table, seqlens)
+    n = src.numel()
+    if status is None:
+        status = torch.empty(1, dtype=_I32, device=src.device)
+    st = lib().fa_cache_fork(*args, _ints("src", src, (n,), dev), _ints("dst", dst, (n,), dev), n,
+                             _ints("status", status, (1,), dev), _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_cache_fork")
     return status
@@ -512,18 +534,15 @@ def cache_reserve(refs, block_table, seqlens, extra, page_size, copies=None, sta
     (copy on write), in place.  Returns (copies int32 [B, 3], status int32 [1]):
     copies is for ``cache_append`` or ``cache_copy``; status is 0, the number of
     pages lacking, or -1 - b for a row too long (nothing is reserved then)."""
-    dev = block_table.device
-    args = _table(refs, block_table, seqlens)
-    B = seqlens.numel()
-    if extra.shape != (B,):
-        raise ValueError("extra must be [B]")
+    dev, args = _table(refs, block_table, seqlens)
+    B = args[5]
     if copies is None:
-        copies = torch.empty((B, 3), dtype=torch.int32, device=dev)
-    if copies.shape != (B, 3):
-        raise ValueError("copies must be [B, 3]")
-    status = _status(status, dev)
-    st = lib().fa_cache_reserve(*args, _ints("extra", extra, 1, dev), int(page_size),
-                                _ints("copies", copies, 2, dev), _ptr(status), _on(stream, dev))
+        copies = torch.empty((B, 3), dtype=_I32, device=refs.device)
+    if status is None:
+        status = torch.empty(1, dtype=_I32, device=refs.device)
+    st = lib().fa_cache_reserve(*args, _ints("extra", extra, (B,), dev), int(page_size),
+                                _ints("copies", copies, (B, 3), dev),
+                                _ints("status", status, (1,), dev), _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_cache_reserve")
     return copies, status
@@ -531,33 +550,35 @@ def cache_reserve(refs, block_table, seqlens, extra, page_size, copies=None, sta
 
 def cache_free(refs, block_table, seqlens, rows, stream=None):
     """Gives up the pages of the listed rows through ``fa_cache_free``."""
-    dev = block_table.device
-    args = _table(refs, block_table, seqlens)
-    st = lib().fa_cache_free(*args, _ints("rows", rows, 1, dev), rows.numel(), _on(stream, dev))
+    dev, args = _table(refs, block_table, seqlens)
+    n = rows.numel()
+    st = lib().fa_cache_free(*args, _ints("rows", rows, (n,), dev), n, _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_cache_free")
 
 
 def _caches(k_cache, v_cache):
-    if not k_cache.is_cuda or k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
-        raise ValueError("the caches must be CUDA bf16 tensors")
-    if (k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.device != k_cache.device
+    """The device and the arguments k_cache, v_cache, num_pages, hkv, page_size, d."""
+    dev = _device("k_cache", k_cache)
+    shape = k_cache.shape
+    if (k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16 or len(shape) != 4
+            or v_cache.shape != shape or v_cache.get_device() != dev
             or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
-        raise ValueError("the caches must share a shape [num_pages, Hkv, page_size, d], contiguous")
-    return (_ptr(k_cache), _ptr(v_cache), *k_cache.shape)
+        raise ValueError("the caches must be contiguous bf16 tensors of one shape "
+                         f"[num_pages, Hkv, page_size, d] on cuda:{dev}")
+    return dev, (k_cache.data_ptr(), v_cache.data_ptr(), *shape)
 
 
-def _new_rows(name, t, hkv, d, device):
+def _new_rows(name, t, shape, dev):
     """New rows [B, Hkv, n, d] of any strides that are multiples of 8 elements
     over a contiguous last dimension (else a copy that has them)."""
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4 or t.shape[1] != hkv \
-            or t.shape[3] != d:
-        raise ValueError(f"{name} must be a bf16 tensor [B, {hkv}, n, {d}] on {device}")
+    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
     s = t.stride()
-    if s[3] != 1 or s[0] % 8 or s[1] % 8 or s[2] % 8 or t.data_ptr() % 16:
+    if s[3] != 1 or (s[0] | s[1] | s[2]) & 7 or t.data_ptr() & 15:
         t = t.clone(memory_format=torch.contiguous_format)
         s = t.stride()
-    return t, (ctypes.c_longlong * 3)(s[0], s[1], s[2])
+    return t, _Strides(s[0], s[1], s[2])
 
 
 def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=None, copies=None,
@@ -566,23 +587,19 @@ def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=Non
     i < n_new[b] (default n), of the paged caches through ``fa_cache_append``,
     after the page copies of ``cache_reserve`` when they are given.  seqlens is
     not changed."""
-    kc = _caches(k_cache, v_cache)
-    dev = k_cache.device
-    B = seqlens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or k_new.shape != v_new.shape \
-            or k_new.shape[0] != B:
-        raise ValueError("block_table must be [B, max_pages], seqlens [B], k_new and v_new [B, Hkv, n, d]")
-    if n_new is not None and n_new.shape != (B,):
-        raise ValueError("n_new must be [B]")
-    if copies is not None and copies.shape != (B, 3):
-        raise ValueError("copies must be [B, 3]")
-    k_new, ks = _new_rows("k_new", k_new, kc[3], kc[5], dev)
-    v_new, vs = _new_rows("v_new", v_new, kc[3], kc[5], dev)
+    dev, caches = _caches(k_cache, v_cache)
+    if block_table.dim() != 2 or k_new.dim() != 4:
+        raise ValueError("block_table must be [B, max_pages], k_new and v_new [B, Hkv, n, d]")
+    B, width = block_table.shape
+    n = k_new.shape[2]
+    shape = (B, caches[3], n, caches[5])
+    k_new, ks = _new_rows("k_new", k_new, shape, dev)
+    v_new, vs = _new_rows("v_new", v_new, shape, dev)
     st = lib().fa_cache_append(
-        *kc, _ints("block_table", block_table, 2, dev), block_table.shape[1],
-        _ints("seqlens", seqlens, 1, dev), B, _ptr(k_new), ks, _ptr(v_new), vs, k_new.shape[2],
-        None if n_new is None else _ints("n_new", n_new, 1, dev),
-        None if copies is None else _ints("copies", copies, 2, dev), _on(stream, dev))
+        *caches, _ints("block_table", block_table, (B, width), dev), width,
+        _ints("seqlens", seqlens, (B,), dev), B, k_new.data_ptr(), ks, v_new.data_ptr(), vs, n,
+        None if n_new is None else _ints("n_new", n_new, (B,), dev),
+        None if copies is None else _ints("copies", copies, (B, 3), dev), _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_cache_append")
 
@@ -590,12 +607,9 @@ def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=Non
 def cache_copy(k_cache, v_cache, copies, stream=None):
     """Copies rows of pages, copies int32 [n, 3] of (from, to, rows), in both
     caches through ``fa_cache_copy``."""
-    kc = _caches(k_cache, v_cache)
-    dev = k_cache.device
-    if copies.dim() != 2 or copies.shape[1] != 3:
-        raise ValueError("copies must be [n, 3]")
-    st = lib().fa_cache_copy(*kc, _ints("copies", copies, 2, dev), copies.shape[0],
-                             _on(stream, dev))
+    dev, caches = _caches(k_cache, v_cache)
+    n = copies.shape[0] if copies.dim() == 2 else -1
+    st = lib().fa_cache_copy(*caches, _ints("copies", copies, (n, 3), dev), n, _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_cache_copy")
 
@@ -604,16 +618,15 @@ def cache_compact(k_cache, v_cache, block_table, start, keep, n_keep, stream=Non
     """Key start[b] + a takes key start[b] + keep[b, a], a < n_keep[b], of both
     caches through ``fa_cache_compact`` (keep int32 [B, n], strictly ascending):
     the accepted nodes of a tree move together."""
-    kc = _caches(k_cache, v_cache)
-    dev = k_cache.device
-    B = start.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B or keep.dim() != 2 \
-            or keep.shape[0] != B or n_keep.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages], start and n_keep [B], keep [B, n]")
+    dev, caches = _caches(k_cache, v_cache)
+    if block_table.dim() != 2 or keep.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages], keep [B, n]")
+    B, width = block_table.shape
+    n = keep.shape[1]
     st = lib().fa_cache_compact(
-        *kc, _ints("block_table", block_table, 2, dev), block_table.shape[1],
-        _ints("start", start, 1, dev), B, _ints("keep", keep, 2, dev), keep.shape[1],
-        _ints("n_keep", n_keep, 1, dev), _on(stream, dev))
+        *caches, _ints("block_table", block_table, (B, width), dev), width,
+        _ints("start", start, (B,), dev), B, _ints("keep", keep, (B, n), dev), n,
+        _ints("n_keep", n_keep, (B,), dev), _on(stream, dev))
     if st != FA_OK:
         raise FaError(st, "fa_cache_compact")
 
