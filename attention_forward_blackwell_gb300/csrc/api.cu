@@ -226,6 +226,77 @@ struct Tree {
 // 1.2-3.9x faster for every batch from 1 to 16 at 32 to 128 rows.
 constexpr int kDecodeToPrefillRows = 32;
 
+// Query rows per kv head up to which a tree runs the split-KV kernel.
+constexpr int kTreeSplitRows = 16;
+
+// A tree of query nodes on the tensor-core kernel (tree.cu).
+fa_status tree_impl(const Tree& tree, const void* q, const void* k, const void* v, void* o,
+                    float* lse, int batch, int hq, int hkv, int nodes, int sk,
+                    const int* seqlens_k, int head_dim, float scale, const float* sinks,
+                    const int* block_table, int max_pages, int page_size, int num_pages,
+                    const DeviceInfo& di, cudaStream_t s) {
+    TreeLaunch p{};
+    TreeArgs& a = p.args;
+    const unsigned long long row_bytes = (unsigned long long)head_dim * 2;
+    const long long rows = (long long)(hq / hkv) * nodes;
+    const long long tiles = (rows + 127) / 128;
+    const long long planes = block_table ? (long long)num_pages * hkv : (long long)batch * hkv;
+    if (planes >= (1ll << 31) || hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    a.box = block_table ? tree_box(head_dim, page_size) : 0;
+    const unsigned k_rows = a.box ? a.box : tree_block_keys(head_dim);
+    const unsigned v_rows = a.box ? a.box : tree_slot_keys(head_dim);
+    const int key_rows = block_table ? page_size : sk;
+    if (!encode_map_strided(&p.tm_q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
+                            row_bytes * rows) ||
+        !encode_map_strided(&p.tm_k, k, head_dim, key_rows, planes, row_bytes,
+                            row_bytes * key_rows, k_rows) ||
+        !encode_map_strided(&p.tm_v, v, head_dim, key_rows, planes, row_bytes,
+                            row_bytes * key_rows, v_rows))
+        return FA_ERR_INVALID_ARG;
+    a.o = static_cast<uint16_t*>(o);
+    a.lse = lse;
+    a.seqlens_k = seqlens_k;
+    a.tree_mask = tree.mask;
+    a.tree_lens = tree.lens;
+    a.tree_words = (nodes + 31) / 32;
+    a.tree_stride = tree.shared ? 0 : (long long)nodes * a.tree_words;
+    a.sinks = sinks;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.B = batch;
+    a.Hkv = hkv;
+    a.group = hq / hkv;
+    a.T = nodes;
+    a.Sk = sk;
+    a.rows = (int)rows;
+    a.tiles = (int)tiles;
+    a.units = hkv * (int)tiles;
+    a.min_quota = 1;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.err_word = di.err_word;
+    a.wait_limit_ns = kWaitLimitNs;
+    // one CTA per SM, or one per key block where there are fewer (of the
+    // longest the sequences can be: the host does not know their lengths)
+    const int bn = tree_block_keys(head_dim);
+    const long long most = (long long)batch * a.units * ((sk + bn - 1) / bn);
+    p.ctas = (unsigned)std::min<long long>(di.num_sms, most);
+    const size_t slots = 2ull * p.ctas;
+    const size_t bytes_o = slots * 128 * head_dim * sizeof(float);
+    const size_t bytes_ml = slots * 2 * 128 * sizeof(float);
+    char* ws = nullptr;
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes_o + bytes_ml + slots * sizeof(int4),
+                        s) != cudaSuccess)
+        return FA_ERR_CUDA;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_ml = reinterpret_cast<float*>(ws + bytes_o);
+    a.head = reinterpret_cast<int4*>(ws + bytes_o + bytes_ml);
+    const cudaError_t e = launch_tree(p, head_dim, s);
+    if (cudaFreeAsync(ws, s) != cudaSuccess) return FA_ERR_CUDA;
+    return from_cuda(e);
+}
+
 fa_status decode_impl(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
                       int hq, int hkv, int sq, int sk, const int* seqlens_k, int head_dim,
                       float scale, int causal, int window, const float* sinks, int num_splits,
@@ -259,6 +330,11 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
         (hq / hkv) * sq >= kDecodeToPrefillRows)
         return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                             causal, 0, sinks, nullptr, 0, 0, 0, stream, nullptr);
+
+    if (tree && (hq / hkv) * sq > kTreeSplitRows && sk > 0 &&
+        (!block_table || tree_box(head_dim, page_size) > 0))
+        return tree_impl(*tree, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
+                         sinks, block_table, max_pages, page_size, num_pages, *di, s);
 
     DecodeArgs a{};
     a.q = static_cast<const uint16_t*>(q);

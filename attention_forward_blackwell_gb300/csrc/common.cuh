@@ -254,6 +254,57 @@ struct DecodeArgs {
 
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, cudaStream_t s);
 
+// -------------------------------------------------------------- tree ----
+
+// The tensor-core kernel of a tree of query nodes (tree.cu).  The query rows
+// of a key/value head, group heads x T nodes, are rows of one matrix.
+struct TreeArgs {
+    uint16_t* o;                // [B, Hkv, rows, d]
+    float* lse;                 // [B, Hkv, rows]
+    const int* seqlens_k;       // [B] or nullptr (Sk)
+    const uint32_t* tree_mask;  // as in DecodeArgs
+    const int* tree_lens;
+    int tree_words;
+    long long tree_stride;
+    const float* sinks;         // [Hkv * group] or nullptr
+    const int* block_table;     // as in DecodeArgs
+    int max_pages, page_size, num_pages;
+    int box;                    // paged: rows of a tensor-map box (tree_box)
+    int B, Hkv, group, T, Sk;
+    int rows;                   // group * T
+    int tiles;                  // ceil(rows / 128)
+    int units;                  // Hkv * tiles: units of a batch entry
+    int min_quota;              // key blocks that a CTA takes at least
+    float* part_o;              // [2 CTAs][d / 4][128][4] unnormalised O of pieces
+    float* part_ml;             // [2 CTAs][2][128] their row max (log2 units) and sum
+    int4* head;                 // [2 CTAs] batch entry, unit, key blocks, and the unit's
+                                // key blocks if the piece is its first (else 0)
+    float scale_log2;
+    unsigned int* err_word;
+    unsigned long long wait_limit_ns;
+};
+struct TreeLaunch {
+    CUtensorMap tm_q;           // {d, rows, B * Hkv}, box {64, 128, 1}
+    CUtensorMap tm_k, tm_v;     // contiguous {d, Sk, B * Hkv}: boxes of a block and of a slot;
+                                // paged {d, page_size, num_pages * Hkv}: boxes of `box` rows
+    TreeArgs args;
+    unsigned ctas;
+};
+cudaError_t launch_tree(const TreeLaunch& p, int head_dim, cudaStream_t s);
+
+// Keys of a block and of a V slot of the tree kernel.
+inline int tree_block_keys(int head_dim) { return head_dim == 256 ? 128 : 256; }
+inline int tree_slot_keys(int head_dim) { return 256 * 64 / head_dim; }
+// Rows of a tensor-map box in pages of page_size rows: the largest power of
+// two that divides it, at most 128 and a V slot; 0 below 8 (the swizzle's
+// atom of 8 rows).
+inline int tree_box(int head_dim, int page_size) {
+    int box = page_size & -page_size;
+    const int most = tree_slot_keys(head_dim) < 128 ? tree_slot_keys(head_dim) : 128;
+    if (box > most) box = most;
+    return box >= 8 ? box : 0;
+}
+
 // Fills O = 0 and LSE = -inf, or the row's sink logit when sinks is not null
 // (used when there are no keys at all); rows are ordered (b, h < hq, i < sq).
 cudaError_t launch_fill_empty(uint16_t* o, float* lse, long long rows, int head_dim,
