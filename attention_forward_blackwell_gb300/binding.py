@@ -16,7 +16,7 @@ import threading
 
 import torch
 
-from .build import LIB_PATH
+from .build import BIND_PATH, LIB_PATH
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_MISALIGNED, FA_ERR_CUDA, \
     FA_ERR_TIMEOUT = range(6)
@@ -199,19 +199,23 @@ def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=
     (num_splits <= 0 lets the library choose, as ``fa_fwd_decode`` does), or
     ``fa_fwd_decode_ex`` with a sliding ``window`` > 0 or per-head ``sinks``, or
     ``fa_fwd_decode_first`` with a window whose ``first`` keys stay visible."""
+    if first:
+        if num_splits and num_splits > 0:
+            raise ValueError("num_splits cannot be combined with window or sinks")
+        r = _serving().decode_first(q, k, v, scale, causal, seqlens_k, out, lse, _handle(stream),
+                                    window or 0, sinks, first)
+        if type(r) is int:
+            raise FaError(r, "fa_fwd_decode_first")
+        return r
     B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
     out, lse = _outputs(q, out, lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
-    if first or (window and window > 0) or sinks is not None:
+    if (window and window > 0) or sinks is not None:
         if num_splits and num_splits > 0:
             raise ValueError("num_splits cannot be combined with window or sinks")
-    if first:
-        st = lib().fa_fwd_decode_first(*args, int(window or 0), int(first), _ptr(sinks),
-                                       _stream_ptr(stream))
-    elif (window and window > 0) or sinks is not None:
         st = lib().fa_fwd_decode_ex(*args, int(window or 0), _ptr(sinks), _stream_ptr(stream))
     elif num_splits and num_splits > 0:
         st = lib().fa_fwd_decode_splits(*args, int(num_splits), _stream_ptr(stream))
@@ -222,8 +226,7 @@ def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=
     return out, lse
 
 
-def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out, lse, stream,
-           *more):
+def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out, lse, stream):
     if not (q.is_cuda and k_cache.is_cuda and v_cache.is_cuda):
         raise ValueError("q and the caches must be CUDA tensors")
     if q.dtype != torch.bfloat16 or k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
@@ -244,7 +247,7 @@ def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     st = getattr(lib(), name)(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), B, Hq,
                               Hkv, Sq, _ptr(seqlens_k), _ptr(block_table), block_table.shape[1],
-                              page_size, num_pages, d, scale, int(bool(causal)), *more,
+                              page_size, num_pages, d, scale, int(bool(causal)),
                               _stream_ptr(stream))
     if st != FA_OK:
         raise FaError(st, name)
@@ -360,96 +363,49 @@ def decode_paged(q, k_cache, v_cache, block_table, seqlens_k, scale=None, causal
     (``fa_fwd_decode_paged_first`` with a sliding ``window`` > 0, whose
     ``first`` keys stay visible, or per-head ``sinks``); returns (o, lse)."""
     if first or (window and window > 0) or sinks is not None:
-        sinks = _check_sinks(sinks, q.shape[1])
-        return _paged("fa_fwd_decode_paged_first", q, k_cache, v_cache, block_table, seqlens_k,
-                      scale, causal, out, lse, stream, int(window or 0), int(first), _ptr(sinks))
+        r = _serving().decode_paged_first(q, k_cache, v_cache, block_table, seqlens_k, scale, causal,
+                                          out, lse, _handle(stream), window or 0, sinks, first)
+        if type(r) is int:
+            raise FaError(r, "fa_fwd_decode_paged_first")
+        return r
     return _paged("fa_fwd_decode_paged", q, k_cache, v_cache, block_table, seqlens_k, scale,
                   causal, out, lse, stream)
 
 
 # ------------------------------------------- trees of drafted tokens, cache pages ----
 #
-# These calls are made once per layer and step on small tensors, so their
-# checks are kept to a few attribute reads each.
+# The tensors of these calls are checked in csrc/bind.cpp; what is refused
+# raises ValueError or TypeError, an error of the library FaError.
 
-_I32, _BF16 = torch.int32, torch.bfloat16
-_Strides = ctypes.c_longlong * 3
-
-
-def _device(name, t):
-    """Index of the CUDA device that holds t, which has to be the current one."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
-    return dev
+_bind = None
 
 
-def _on(stream, dev):
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
+def _serving():
+    """The module of csrc/bind.cpp (loaded once).  Raises if it has not been built."""
+    global _bind
+    if _bind is None:
+        lib()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(
+                f"{BIND_PATH} is missing: build it with attention_forward_blackwell_gb300."
+                "build.build() (there is no CPU fallback)")
+        from . import _bind as module
+        _bind = module
+    return _bind
 
 
-def _ints(name, t, shape, dev):
-    """Address of a contiguous int32 tensor that a kernel reads or writes in place."""
-    if t.dtype is not _I32 or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on cuda:{dev}, "
-                         f"not {t.dtype} {list(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _tree_call(q, k, v, dev, mask, tree_lens, sinks, scale, out, lse):
-    """Checks and arguments that both tree calls share: (q, k, v, o, lse) and
-    (mask, shared, tree_lens, d, scale) as the library takes them, sinks, out
-    and lse."""
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype is not _BF16:
-            raise TypeError(f"{name} must be bfloat16")
-        if t.get_device() != dev or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 4-D tensor on cuda:{dev}")
-    B, Hq, T, d = q.shape
-    if v.shape != k.shape or k.shape[3] != d:
-        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
-    words = (T + 31) // 32
-    shared = mask.dim() == 2
-    mask = _ints("tree_mask", mask, (T, words) if shared else (B, T, words), dev)
-    if tree_lens is not None:
-        tree_lens = _ints("tree_lens", tree_lens, (B,), dev)
-    if sinks is not None:
-        if sinks.get_device() != dev:
-            raise ValueError(f"sinks must be on cuda:{dev}")
-        sinks = _check_sinks(sinks, Hq)
-    if out is None:
-        out = torch.empty_like(q)
-    elif (out.shape != q.shape or out.dtype is not _BF16 or out.get_device() != dev
-          or not out.is_contiguous()):
-        raise ValueError("out must be a contiguous bf16 tensor shaped like q, on its device")
-    if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-    elif (lse.shape != (B, Hq, T) or lse.dtype is not torch.float32 or lse.get_device() != dev
-          or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, T] on q's device")
-    return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr()),
-            (mask, int(shared), tree_lens, d, 1.0 / math.sqrt(d) if scale is None else float(scale)),
-            sinks, out, lse)
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def tree_mask(parents, out=None, stream=None):
     """Mask words int32 [B, T, ceil(T / 32)] of trees given by their parents
     int32 [B, T] through ``fa_tree_mask``: node i sees itself and the nodes on
     its way up (bit j % 32 of word j / 32)."""
-    dev = _device("parents", parents)
-    if parents.dim() != 2:
-        raise ValueError("parents must be [B, T]")
-    B, T = parents.shape
-    shape = (B, T, (T + 31) // 32)
-    if out is None:
-        out = torch.empty(shape, dtype=_I32, device=parents.device)
-    st = lib().fa_tree_mask(_ints("parents", parents, (B, T), dev), _ints("out", out, shape, dev), B, T,
-                            _on(stream, dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_tree_mask")
-    return out
+    r = _serving().tree_mask(parents, out, _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_tree_mask")
+    return r
 
 
 def decode_tree(q, k, v, tree_mask, scale=None, seqlens_k=None, tree_lens=None, sinks=None,
@@ -460,54 +416,22 @@ def decode_tree(q, k, v, tree_mask, scale=None, seqlens_k=None, tree_lens=None, 
     before the tree and the nodes of its mask bits, tree_mask int32
     [B, T, ceil(T / 32)] or [T, ceil(T / 32)].  Returns (o, lse); rows past a
     tree's nodes are not written."""
-    dev = _device("q", q)
-    tensors, more, sinks, out, lse = _tree_call(q, k, v, dev, tree_mask, tree_lens, sinks, scale,
-                                                out, lse)
-    B, Hq, T, d = q.shape
-    Bk, Hkv, Sk, _ = k.shape
-    if Bk != B:
-        raise ValueError("k and v must have q's batch")
-    if seqlens_k is not None:
-        seqlens_k = _ints("seqlens_k", seqlens_k, (B,), dev)
-    st = lib().fa_fwd_decode_tree(*tensors, B, Hq, Hkv, T, Sk, seqlens_k, *more, _ptr(sinks),
-                                  _on(stream, dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_fwd_decode_tree")
-    return out, lse
+    r = _serving().decode_tree(q, k, v, tree_mask, scale, seqlens_k, tree_lens, sinks, out, lse,
+                               _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_fwd_decode_tree")
+    return r
 
 
 def decode_tree_paged(q, k_cache, v_cache, block_table, seqlens_k, tree_mask, scale=None,
                       tree_lens=None, sinks=None, out=None, lse=None, stream=None):
     """``decode_tree`` over paged caches [num_pages, Hkv, page_size, d] through
     ``fa_fwd_decode_tree_paged``; returns (o, lse)."""
-    dev = _device("q", q)
-    tensors, more, sinks, out, lse = _tree_call(q, k_cache, v_cache, dev, tree_mask, tree_lens, sinks,
-                                                scale, out, lse)
-    B, Hq, T, d = q.shape
-    num_pages, Hkv, page_size, _ = k_cache.shape
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    width = block_table.shape[1]
-    st = lib().fa_fwd_decode_tree_paged(
-        *tensors, B, Hq, Hkv, T, _ints("seqlens_k", seqlens_k, (B,), dev),
-        _ints("block_table", block_table, (B, width), dev), width, page_size, num_pages, *more,
-        _ptr(sinks), _on(stream, dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_fwd_decode_tree_paged")
-    return out, lse
-
-
-def _table(refs, block_table, seqlens):
-    """The device and the arguments refs, num_pages, block_table, max_pages,
-    seqlens, batch of the table calls."""
-    dev = _device("block_table", block_table)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages]")
-    B, width = block_table.shape
-    pages = refs.numel()
-    return dev, (_ints("refs", refs, (pages,), dev), pages,
-                 _ints("block_table", block_table, (B, width), dev), width,
-                 _ints("seqlens", seqlens, (B,), dev), B)
+    r = _serving().decode_tree_paged(q, k_cache, v_cache, block_table, seqlens_k, tree_mask, scale,
+                                     tree_lens, sinks, out, lse, _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_fwd_decode_tree_paged")
+    return r
 
 
 def cache_fork(refs, block_table, seqlens, src, dst, status=None, stream=None):
@@ -515,15 +439,10 @@ def cache_fork(refs, block_table, seqlens, src, dst, status=None, stream=None):
     refs [num_pages], block_table [B, max_pages] and seqlens [B] (int32) change
     in place.  Returns status int32 [1]: 0, or 1 + the first pair refused
     (nothing is changed then)."""
-    dev, args = _table(refs, block_table, seqlens)
-    n = src.numel()
-    if status is None:
-        status = torch.empty(1, dtype=_I32, device=src.device)
-    st = lib().fa_cache_fork(*args, _ints("src", src, (n,), dev), _ints("dst", dst, (n,), dev), n,
-                             _ints("status", status, (1,), dev), _on(stream, dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_fork")
-    return status
+    r = _serving().cache_fork(refs, block_table, seqlens, src, dst, status, _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_cache_fork")
+    return r
 
 
 def cache_reserve(refs, block_table, seqlens, extra, page_size, copies=None, status=None,
@@ -534,51 +453,18 @@ def cache_reserve(refs, block_table, seqlens, extra, page_size, copies=None, sta
     (copy on write), in place.  Returns (copies int32 [B, 3], status int32 [1]):
     copies is for ``cache_append`` or ``cache_copy``; status is 0, the number of
     pages lacking, or -1 - b for a row too long (nothing is reserved then)."""
-    dev, args = _table(refs, block_table, seqlens)
-    B = args[5]
-    if copies is None:
-        copies = torch.empty((B, 3), dtype=_I32, device=refs.device)
-    if status is None:
-        status = torch.empty(1, dtype=_I32, device=refs.device)
-    st = lib().fa_cache_reserve(*args, _ints("extra", extra, (B,), dev), int(page_size),
-                                _ints("copies", copies, (B, 3), dev),
-                                _ints("status", status, (1,), dev), _on(stream, dev))
-    if st != FA_OK:
-        raise FaError(st, "fa_cache_reserve")
-    return copies, status
+    r = _serving().cache_reserve(refs, block_table, seqlens, extra, page_size, copies, status,
+                                 _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_cache_reserve")
+    return r
 
 
 def cache_free(refs, block_table, seqlens, rows, stream=None):
     """Gives up the pages of the listed rows through ``fa_cache_free``."""
-    dev, args = _table(refs, block_table, seqlens)
-    n = rows.numel()
-    st = lib().fa_cache_free(*args, _ints("rows", rows, (n,), dev), n, _on(stream, dev))
+    st = _serving().cache_free(refs, block_table, seqlens, rows, _handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_cache_free")
-
-
-def _caches(k_cache, v_cache):
-    """The device and the arguments k_cache, v_cache, num_pages, hkv, page_size, d."""
-    dev = _device("k_cache", k_cache)
-    shape = k_cache.shape
-    if (k_cache.dtype is not _BF16 or v_cache.dtype is not _BF16 or len(shape) != 4
-            or v_cache.shape != shape or v_cache.get_device() != dev
-            or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
-        raise ValueError("the caches must be contiguous bf16 tensors of one shape "
-                         f"[num_pages, Hkv, page_size, d] on cuda:{dev}")
-    return dev, (k_cache.data_ptr(), v_cache.data_ptr(), *shape)
-
-
-def _new_rows(name, t, shape, dev):
-    """New rows [B, Hkv, n, d] of any strides that are multiples of 8 elements
-    over a contiguous last dimension (else a copy that has them)."""
-    if t.dtype is not _BF16 or t.shape != shape or t.get_device() != dev:
-        raise ValueError(f"{name} must be a bf16 tensor {list(shape)} on cuda:{dev}")
-    s = t.stride()
-    if s[3] != 1 or (s[0] | s[1] | s[2]) & 7 or t.data_ptr() & 15:
-        t = t.clone(memory_format=torch.contiguous_format)
-        s = t.stride()
-    return t, _Strides(s[0], s[1], s[2])
 
 
 def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=None, copies=None,
@@ -587,19 +473,8 @@ def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=Non
     i < n_new[b] (default n), of the paged caches through ``fa_cache_append``,
     after the page copies of ``cache_reserve`` when they are given.  seqlens is
     not changed."""
-    dev, caches = _caches(k_cache, v_cache)
-    if block_table.dim() != 2 or k_new.dim() != 4:
-        raise ValueError("block_table must be [B, max_pages], k_new and v_new [B, Hkv, n, d]")
-    B, width = block_table.shape
-    n = k_new.shape[2]
-    shape = (B, caches[3], n, caches[5])
-    k_new, ks = _new_rows("k_new", k_new, shape, dev)
-    v_new, vs = _new_rows("v_new", v_new, shape, dev)
-    st = lib().fa_cache_append(
-        *caches, _ints("block_table", block_table, (B, width), dev), width,
-        _ints("seqlens", seqlens, (B,), dev), B, k_new.data_ptr(), ks, v_new.data_ptr(), vs, n,
-        None if n_new is None else _ints("n_new", n_new, (B,), dev),
-        None if copies is None else _ints("copies", copies, (B, 3), dev), _on(stream, dev))
+    st = _serving().cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new, copies,
+                                 _handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_cache_append")
 
@@ -607,9 +482,7 @@ def cache_append(k_cache, v_cache, block_table, seqlens, k_new, v_new, n_new=Non
 def cache_copy(k_cache, v_cache, copies, stream=None):
     """Copies rows of pages, copies int32 [n, 3] of (from, to, rows), in both
     caches through ``fa_cache_copy``."""
-    dev, caches = _caches(k_cache, v_cache)
-    n = copies.shape[0] if copies.dim() == 2 else -1
-    st = lib().fa_cache_copy(*caches, _ints("copies", copies, (n, 3), dev), n, _on(stream, dev))
+    st = _serving().cache_copy(k_cache, v_cache, copies, _handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_cache_copy")
 
@@ -618,15 +491,7 @@ def cache_compact(k_cache, v_cache, block_table, start, keep, n_keep, stream=Non
     """Key start[b] + a takes key start[b] + keep[b, a], a < n_keep[b], of both
     caches through ``fa_cache_compact`` (keep int32 [B, n], strictly ascending):
     the accepted nodes of a tree move together."""
-    dev, caches = _caches(k_cache, v_cache)
-    if block_table.dim() != 2 or keep.dim() != 2:
-        raise ValueError("block_table must be [B, max_pages], keep [B, n]")
-    B, width = block_table.shape
-    n = keep.shape[1]
-    st = lib().fa_cache_compact(
-        *caches, _ints("block_table", block_table, (B, width), dev), width,
-        _ints("start", start, (B,), dev), B, _ints("keep", keep, (B, n), dev), n,
-        _ints("n_keep", n_keep, (B,), dev), _on(stream, dev))
+    st = _serving().cache_compact(k_cache, v_cache, block_table, start, keep, n_keep, _handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_cache_compact")
 

@@ -1,4 +1,5 @@
-"""Builds libfa_gb300.so from csrc/ with nvcc for sm_103a (in-tree).
+"""Builds libfa_gb300.so from csrc/ with nvcc for sm_103a (in-tree), and
+_bind.so, the Python module of the serving operators, from csrc/bind.cpp.
 
 Each translation unit is compiled in parallel into ``_build/`` and the objects
 are linked into ``libfa_gb300.so`` next to this file.  Objects are rebuilt
@@ -6,9 +7,11 @@ when their source or any header is newer.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import platform
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libfa_gb300.so")
+BIND_PATH = os.path.join(HERE, "_bind.so")
 SOURCES = ["prefill_d512.cu", "prefill_d128.cu", "prefill_d256.cu", "prefill_d96.cu",
            "prefill_d64.cu", "decode.cu", "selftest.cu", "api.cu", "decode_noalloc.cu", "cache.cu",
            "tree.cu"]
@@ -37,6 +41,53 @@ def _nvcc():
     return "nvcc"
 
 
+def _torch():
+    """Folder of the installed torch package and its version."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is missing")
+    root = os.path.dirname(spec.origin)
+    about = {}
+    with open(os.path.join(root, "version.py")) as f:
+        exec(f.read(), about)
+    return root, about["__version__"]
+
+
+def _cuda_home():
+    nvcc = _nvcc()
+    nvcc = os.path.realpath(nvcc) if os.path.sep in nvcc else "/usr/local/cuda/bin/nvcc"
+    return os.path.dirname(os.path.dirname(nvcc))
+
+
+def _compile_bind(force):
+    """csrc/bind.cpp against the installed torch; whether it was compiled."""
+    src, obj = os.path.join(CSRC, "bind.cpp"), os.path.join(OBJDIR, "bind.o")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "fa.h")))
+    if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
+        return False
+    include = os.path.join(_torch()[0], "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", src, "-o", obj + ".tmp",
+           "-I", include, "-I", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(_cuda_home(), "include")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(obj + ".tmp", obj)
+    return True
+
+
+def _link_bind():
+    libs = os.path.join(_torch()[0], "lib")
+    tmp = BIND_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, os.path.join(OBJDIR, "bind.o"),
+           LIB_PATH, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
+
+
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")]
     hs.append(os.path.join(INCLUDE, "fa.h"))
@@ -47,7 +98,7 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     os.makedirs(OBJDIR, exist_ok=True)
     # objects from another host architecture (or toolchain) are never reused
     stamp = os.path.join(OBJDIR, "host.txt")
-    host = f"{platform.machine()} {platform.system()} {' '.join(_options())}"
+    host = f"{platform.machine()} {platform.system()} torch {_torch()[1]} {' '.join(_options())}"
     if not os.path.exists(stamp) or open(stamp).read() != host:
         force = True
     nvcc = _nvcc()
@@ -72,20 +123,23 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
 
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        bind = ex.submit(_compile_bind, force)
         results = list(ex.map(compile_one, SOURCES))
+        relink_bind = bind.result() or not os.path.exists(BIND_PATH)
     objs = [o for o, _ in results]
     relink = (force or any(changed for _, changed in results) or not os.path.exists(LIB_PATH)
               or os.path.getmtime(LIB_PATH) < max(os.path.getmtime(o) for o in objs))
     if relink:
         tmp = LIB_PATH + f".tmp{os.getpid()}"
         cmd = [nvcc] + ARCH + ["-shared", "-cudart", "shared", "-o", tmp] + objs + [
-            "-Xlinker", "-rpath," + os.path.join(os.path.dirname(os.path.dirname(
-                os.path.realpath(nvcc) if os.path.sep in nvcc else "/usr/local/cuda/bin/nvcc")),
-                "lib64")]
+            "-Xlinker", "-soname=libfa_gb300.so",
+            "-Xlinker", "-rpath," + os.path.join(_cuda_home(), "lib64")]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB_PATH)
+    if relink_bind:
+        _link_bind()
     with open(stamp, "w") as f:
         f.write(host)
     return LIB_PATH
