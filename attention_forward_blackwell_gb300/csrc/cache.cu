@@ -14,13 +14,17 @@
 // listed twice is freed once.  Row kernels (append, copy, compact) move
 // 16-byte granules of key and value rows; they are bound by the bytes moved,
 // each read once and written once.
+#include <cooperative_groups.h>
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "../../include/fa.h"
+#include "common.cuh"
 
 namespace fa {
 namespace {
+
+namespace cg = cooperative_groups;
 
 constexpr int kTableThreads = 1024;
 
@@ -67,15 +71,28 @@ struct TableArgs {
 
 // --------------------------------------------------------------- fork ----
 
-// One CTA.  Pass 1 checks the pairs, a warp each; pass 2 (if all passed)
-// copies the rows and counts the pages.
-__global__ void __launch_bounds__(kTableThreads)
+// One cluster, a warp per pair.  Pass 1 checks the pairs; pass 2, if all
+// passed (the cluster's first CTA holds the verdict), copies the rows and
+// counts the pages.  A single CTA took 24 us for 256 pairs of 65 entries, each
+// warp walking 8 of them; with more than 32 pairs eight CTAs share them.
+template <bool CLUSTER>
+__global__ void __cluster_dims__(CLUSTER ? 8 : 1, 1, 1) __launch_bounds__(kTableThreads)
     cache_fork_kernel(const TableArgs t, const int* src, const int* dst, int n) {
     __shared__ int bad;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    cg::cluster_group cluster = cg::this_cluster();
+    auto sync = [&] {
+        if constexpr (CLUSTER) cluster.sync();
+        else __syncthreads();
+    };
+    dependents_may_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
+    const int warp = blockIdx.x * (kTableThreads / 32) + (threadIdx.x >> 5);
+    const int warps = gridDim.x * (kTableThreads / 32);
     if (threadIdx.x == 0) bad = n;
-    __syncthreads();
-    for (int i = warp; i < n; i += kTableThreads / 32) {
+    sync();
+    int* verdict = CLUSTER ? cluster.map_shared_rank(&bad, 0) : &bad;
+    for (int i = warp; i < n; i += warps) {
         const int s = src[i], d = dst[i];
         bool ok = (unsigned)s < (unsigned)t.batch && (unsigned)d < (unsigned)t.batch;
         if (ok) {
@@ -85,28 +102,33 @@ __global__ void __launch_bounds__(kTableThreads)
             for (int j = lane; j < n; j += 32)   // nor is any pair's src or an earlier dst
                 if (src[j] == d || (j < i && dst[j] == d)) ok = false;
         }
-        if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicMin(&bad, i);
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicMin(verdict, i);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) *t.status = bad < n ? bad + 1 : 0;
-    if (bad < n) return;
-    for (int i = warp; i < n; i += kTableThreads / 32) {
-        const int* from = t.table + (size_t)src[i] * t.max_pages;
-        int* to = t.table + (size_t)dst[i] * t.max_pages;
-        for (int j = lane; j < t.max_pages; j += 32) {
-            const int e = from[j];
-            const bool held = is_page(e, t.num_pages);
-            to[j] = held ? e : -1;
-            if (held) atomicAdd(t.refs + e, 1);
+    sync();
+    const int first_bad = *verdict;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *t.status = first_bad < n ? first_bad + 1 : 0;
+    if (first_bad == n) {
+        for (int i = warp; i < n; i += warps) {
+            const int* from = t.table + (size_t)src[i] * t.max_pages;
+            int* to = t.table + (size_t)dst[i] * t.max_pages;
+            for (int j = lane; j < t.max_pages; j += 32) {
+                const int e = from[j];
+                const bool held = is_page(e, t.num_pages);
+                to[j] = held ? e : -1;
+                if (held) atomicAdd(t.refs + e, 1);
+            }
+            if (lane == 0) t.lens[dst[i]] = t.lens[src[i]];
         }
-        if (lane == 0) t.lens[dst[i]] = t.lens[src[i]];
     }
+    sync();   // the first CTA's shared memory stays until all have read it
 }
 
 // --------------------------------------------------------------- free ----
 
 __global__ void __launch_bounds__(256)
     cache_free_kernel(const TableArgs t, const int* rows, int n) {
+    dependents_may_start();
+    wait_for_previous();
     for (int i = blockIdx.x; i < n; i += gridDim.x) {
         const int r = rows[i];
         if ((unsigned)r >= (unsigned)t.batch) continue;
@@ -138,13 +160,52 @@ __device__ __forceinline__ Span reserve_span(const TableArgs& t, const int* extr
     return s;
 }
 
+constexpr int kLongSpan = 8;     // entries of a span that a warp shares
+constexpr int kScanPages = 16;   // pages a thread looks at in one step of the free scan
+
+// Marks the needed entry j of a row (see below); whether it is one.
+__device__ __forceinline__ bool reserve_mark(const TableArgs& t, int* row, int j) {
+    const int e = row[j];
+    if (!is_page(e, t.num_pages)) {
+        row[j] = -1;
+        return true;
+    }
+    if (t.refs[e] > 1) {
+        row[j] = -2 - e;
+        return true;
+    }
+    return false;
+}
+
+// Entry j of row r, marked as needed: takes `page`, or (page < 0) its mark
+// back.
+__device__ __forceinline__ void reserve_grant(const TableArgs& t, int* row, int r, int j, int page,
+                                              int first, int used, int* copies) {
+    const int e = row[j];
+    if (page < 0) {
+        if (e <= -2) row[j] = -2 - e;
+        return;
+    }
+    row[j] = page;
+    t.refs[page] = 1;
+    if (e <= -2) {
+        atomicSub(t.refs + (-2 - e), 1);
+        if (j == first && used > 0) {
+            copies[3 * r] = -2 - e;
+            copies[3 * r + 1] = page;
+            copies[3 * r + 2] = used;
+        }
+    }
+}
+
 // One CTA.  Needed entries of a row's span are those that hold no page and
 // those whose page another entry shares (it would be written under the
 // other's eyes); in (row, entry) order they take the free pages in ascending
 // order.
-//   1  count the needed entries, a thread per row; shared ones are marked in
-//      the table as -2 - page and entries that are no page as -1, so that
-//      pass 3 sees the same set whatever it does to refs
+//   1  count the needed entries, a thread per row (a warp for a long span);
+//      shared ones are marked in the table as -2 - page and entries that are
+//      no page as -1, so that pass 3 sees the same set whatever it does to
+//      refs
 //   2  list the free pages, as many as are needed (ascending; the scan stops
 //      early)
 //   3  give them out, or take the marks back where they do not suffice
@@ -153,38 +214,56 @@ __global__ void __launch_bounds__(kTableThreads)
                          int* free_list) {
     __shared__ int scratch[33];
     __shared__ int long_row;   // first row whose span does not fit the table
+    dependents_may_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) long_row = t.batch;
     __syncthreads();
     int needed = 0;
     for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
         const int r = r0 + threadIdx.x;
+        Span s{0, 0, true};
+        if (r < t.batch) s = reserve_span(t, extra, page_size, r);
+        if (!s.fits) atomicMin(&long_row, r);
+        int* row = t.table + (size_t)r * t.max_pages;
+        const bool shared_out = s.last - s.first > kLongSpan;
         int count = 0;
-        if (r < t.batch) {
-            const Span s = reserve_span(t, extra, page_size, r);
-            if (!s.fits) atomicMin(&long_row, r);
-            int* row = t.table + (size_t)r * t.max_pages;
-            for (int j = s.first; j < s.last; ++j) {
-                const int e = row[j];
-                if (!is_page(e, t.num_pages)) {
-                    row[j] = -1;
-                    ++count;
-                } else if (t.refs[e] > 1) {
-                    row[j] = -2 - e;
-                    ++count;
-                }
-            }
+        if (!shared_out)
+            for (int j = s.first; j < s.last; ++j) count += reserve_mark(t, row, j);
+        for (unsigned todo = __ballot_sync(0xffffffffu, shared_out); todo != 0; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            const int first = __shfl_sync(0xffffffffu, s.first, from);
+            const int last = __shfl_sync(0xffffffffu, s.last, from);
+            int* its = t.table + (size_t)(r - lane + from) * t.max_pages;
+            int c = 0;
+            for (int j = first + lane; j < last; j += 32) c += reserve_mark(t, its, j);
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == from) count = c;
         }
         int total;
         block_scan(count, scratch, total);
         needed += total;
     }
+    const bool wide = (reinterpret_cast<uintptr_t>(t.refs) & 15u) == 0;
     int found = 0;
-    for (int p0 = 0; p0 < t.num_pages && found < needed; p0 += kTableThreads) {
-        const int p = p0 + threadIdx.x;
-        const int is_free = p < t.num_pages && t.refs[p] == 0;
+    for (int p0 = 0; p0 < t.num_pages && found < needed; p0 += kTableThreads * kScanPages) {
+        const int p = p0 + (int)threadIdx.x * kScanPages;
+        unsigned is_free = 0;
+        if (wide && p + kScanPages <= t.num_pages) {
+#pragma unroll
+            for (int q = 0; q < kScanPages / 4; ++q) {
+                const int4 x = *reinterpret_cast<const int4*>(t.refs + p + 4 * q);
+                is_free |= ((x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3)
+                           << (4 * q);
+            }
+        } else {
+            for (int q = 0; q < kScanPages && p + q < t.num_pages; ++q)
+                is_free |= (unsigned)(t.refs[p + q] == 0) << q;
+        }
         int total;
-        const int k = found + block_scan(is_free, scratch, total);
-        if (is_free && k < needed) free_list[k] = p;
+        int k = found + block_scan(__popc(is_free), scratch, total);
+        for (; is_free != 0 && k < needed; is_free &= is_free - 1)
+            free_list[k++] = p + __ffs(is_free) - 1;
         found += total;
     }
     const bool fits = long_row == t.batch;   // (the scans' barriers order it)
@@ -195,40 +274,54 @@ __global__ void __launch_bounds__(kTableThreads)
     for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
         const int r = r0 + threadIdx.x;
         Span s{0, 0, true};
+        if (r < t.batch) s = reserve_span(t, extra, page_size, r);
         int* row = t.table + (size_t)r * t.max_pages;
+        const bool shared_out = s.last - s.first > kLongSpan;
         int count = 0;
-        if (r < t.batch) {
-            s = reserve_span(t, extra, page_size, r);
+        if (!shared_out)
             for (int j = s.first; j < s.last; ++j) count += row[j] < 0;
+        const unsigned longs = __ballot_sync(0xffffffffu, shared_out);
+        for (unsigned todo = longs; todo != 0; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            const int first = __shfl_sync(0xffffffffu, s.first, from);
+            const int last = __shfl_sync(0xffffffffu, s.last, from);
+            const int* its = t.table + (size_t)(r - lane + from) * t.max_pages;
+            int c = 0;
+            for (int j = first + lane; j < last; j += 32) c += its[j] < 0;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (lane == from) count = c;
         }
         int total;
         int k = base + block_scan(count, scratch, total);
         base += total;
-        if (r >= t.batch) continue;
-        int from = -1, to = -1, rows = 0;
-        for (int j = s.first; j < s.last; ++j) {
-            const int e = row[j];
-            if (e >= 0) continue;
-            if (!grant) {
-                if (e <= -2) row[j] = -2 - e;
-                continue;
-            }
-            const int page = free_list[k++];
-            row[j] = page;
-            t.refs[page] = 1;
-            if (e <= -2) {
-                atomicSub(t.refs + (-2 - e), 1);
-                const int used = t.lens[r] % page_size;
-                if (j == s.first && used > 0) {   // (lens[r] > 0 here)
-                    from = -2 - e;
-                    to = page;
-                    rows = used;
-                }
+        const int used = r < t.batch ? max(t.lens[r], 0) % page_size : 0;
+        if (r < t.batch) {
+            copies[3 * r] = copies[3 * r + 1] = -1;
+            copies[3 * r + 2] = 0;
+        }
+        __syncwarp();   // before a warp fills in a long row's copy
+        if (!shared_out)
+            for (int j = s.first; j < s.last; ++j)
+                if (row[j] < 0)
+                    reserve_grant(t, row, r, j, grant ? free_list[k++] : -1, s.first, used, copies);
+        for (unsigned todo = longs; todo != 0; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            const int first = __shfl_sync(0xffffffffu, s.first, from);
+            const int last = __shfl_sync(0xffffffffu, s.last, from);
+            const int its_used = __shfl_sync(0xffffffffu, used, from);
+            int at = __shfl_sync(0xffffffffu, k, from);
+            int* its = t.table + (size_t)(r - lane + from) * t.max_pages;
+            for (int j0 = first; j0 < last; j0 += 32) {
+                const int j = j0 + lane;
+                const bool take = j < last && its[j] < 0;
+                const unsigned who = __ballot_sync(0xffffffffu, take);
+                if (take)
+                    reserve_grant(t, its, r - lane + from, j,
+                                  grant ? free_list[at + __popc(who & ((1u << lane) - 1u))] : -1,
+                                  first, its_used, copies);
+                at += __popc(who);
             }
         }
-        copies[3 * r] = from;
-        copies[3 * r + 1] = to;
-        copies[3 * r + 2] = rows;
     }
 }
 
@@ -257,6 +350,8 @@ constexpr int kRowChunk = 64;   // rows of a head that one CTA moves
 // [0, c) of a page, c the third number of copies[b]), then its new rows;
 // the two never touch the same row.
 __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const RowArgs a) {
+    dependents_may_start();
+    wait_for_previous();
     const int b = blockIdx.z, h = blockIdx.y, r0 = blockIdx.x * kRowChunk;
     const int G = a.granules;
     if (a.copies != nullptr) {
@@ -296,6 +391,8 @@ __global__ void __launch_bounds__(kRowThreads) cache_append_kernel(const RowArgs
 __global__ void __launch_bounds__(kRowThreads)
     cache_compact_kernel(const RowArgs a, const int* start, const int* keep, int stride,
                          const int* n_keep) {
+    dependents_may_start();
+    wait_for_previous();
     const int b = blockIdx.y, h = blockIdx.x;
     const int G = a.granules;
     const int n = min(n_keep[b], stride);
@@ -340,6 +437,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // so a cycle cannot be followed).  A thread per (tree, node, word).
 __global__ void __launch_bounds__(256)
     tree_mask_kernel(const int* parents, unsigned int* mask, int batch, int nodes, int words) {
+    dependents_may_start();
+    wait_for_previous();
     const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (e >= (long long)batch * nodes * words) return;
     const int w = (int)(e % words), i = (int)(e / words % nodes);
@@ -359,7 +458,7 @@ __global__ void __launch_bounds__(256)
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-fa_status launched() { return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 // The kernels of this library are compiled for sm_103 only.
 fa_status device_ok() {
@@ -415,9 +514,12 @@ fa_status fa_cache_fork(int* refs, int num_pages, int* block_table, int max_page
     if (n < 0 || (n > 0 && (!src || !dst))) return FA_ERR_INVALID_ARG;
     if (!aligned4(src) || !aligned4(dst)) return FA_ERR_MISALIGNED;
     if ((st = device_ok()) != FA_OK) return st;
-    cache_fork_kernel<<<1, kTableThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(t, src, dst,
-                                                                                       n);
-    return launched();
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (n <= kTableThreads / 32)
+        return launched(launch_dependent(cache_fork_kernel<false>, dim3(1), dim3(kTableThreads), 0, s,
+                                         t, src, dst, n));
+    return launched(launch_dependent(cache_fork_kernel<true>, dim3(8), dim3(kTableThreads), 0, s, t,
+                                     src, dst, n));
 }
 
 fa_status fa_cache_free(int* refs, int num_pages, int* block_table, int max_pages, int* seqlens,
@@ -429,9 +531,8 @@ fa_status fa_cache_free(int* refs, int num_pages, int* block_table, int max_page
     if (!aligned4(rows)) return FA_ERR_MISALIGNED;
     if (n == 0 || batch == 0) return FA_OK;
     if ((st = device_ok()) != FA_OK) return st;
-    cache_free_kernel<<<n < 4096 ? n : 4096, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        t, rows, n);
-    return launched();
+    return launched(launch_dependent(cache_free_kernel, dim3(n < 4096 ? n : 4096), dim3(256), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), t, rows, n));
 }
 
 fa_status fa_cache_reserve(int* refs, int num_pages, int* block_table, int max_pages,
@@ -451,9 +552,8 @@ fa_status fa_cache_reserve(int* refs, int num_pages, int* block_table, int max_p
     void* list = nullptr;
     if (entries > 0 && cudaMallocAsync(&list, entries * sizeof(int), s) != cudaSuccess)
         return FA_ERR_CUDA;
-    cache_reserve_kernel<<<1, kTableThreads, 0, s>>>(t, extra, page_size, copies,
-                                                     static_cast<int*>(list));
-    st = launched();
+    st = launched(launch_dependent(cache_reserve_kernel, dim3(1), dim3(kTableThreads), 0, s, t, extra,
+                                   page_size, copies, static_cast<int*>(list)));
     if (list != nullptr && cudaFreeAsync(list, s) != cudaSuccess) return FA_ERR_CUDA;
     return st;
 }
@@ -497,8 +597,8 @@ fa_status fa_cache_append(void* k_cache, void* v_cache, int num_pages, int hkv, 
     int rows = n;
     if (copies && page_size > rows) rows = page_size;
     const dim3 grid((unsigned)((rows + kRowChunk - 1) / kRowChunk), (unsigned)hkv, (unsigned)batch);
-    cache_append_kernel<<<grid, kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    return launched();
+    return launched(launch_dependent(cache_append_kernel, grid, dim3(kRowThreads), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), a));
 }
 
 fa_status fa_cache_copy(void* k_cache, void* v_cache, int num_pages, int hkv, int page_size,
@@ -519,8 +619,8 @@ fa_status fa_cache_copy(void* k_cache, void* v_cache, int num_pages, int hkv, in
     if ((st = device_ok()) != FA_OK) return st;
     const dim3 grid((unsigned)((page_size + kRowChunk - 1) / kRowChunk), (unsigned)hkv,
                     (unsigned)n);
-    cache_append_kernel<<<grid, kRowThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-    return launched();
+    return launched(launch_dependent(cache_append_kernel, grid, dim3(kRowThreads), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), a));
 }
 
 fa_status fa_cache_compact(void* k_cache, void* v_cache, int num_pages, int hkv, int page_size,
@@ -545,10 +645,9 @@ fa_status fa_cache_compact(void* k_cache, void* v_cache, int num_pages, int hkv,
     if (!keep || !n_keep) return FA_ERR_INVALID_ARG;
     if (!aligned4(keep) || !aligned4(n_keep)) return FA_ERR_MISALIGNED;
     if ((st = device_ok()) != FA_OK) return st;
-    cache_compact_kernel<<<dim3((unsigned)hkv, (unsigned)batch), kRowThreads, 0,
-                           reinterpret_cast<cudaStream_t>(stream)>>>(a, start, keep, keep_stride,
-                                                                     n_keep);
-    return launched();
+    return launched(launch_dependent(cache_compact_kernel, dim3((unsigned)hkv, (unsigned)batch),
+                                     dim3(kRowThreads), 0, reinterpret_cast<cudaStream_t>(stream), a,
+                                     start, keep, keep_stride, n_keep));
 }
 
 fa_status fa_tree_mask(const int* parents, unsigned int* mask, int batch, int nodes,
@@ -562,9 +661,9 @@ fa_status fa_tree_mask(const int* parents, unsigned int* mask, int batch, int no
     if (blocks >= (1ll << 31)) return FA_ERR_INVALID_ARG;
     fa_status st = device_ok();
     if (st != FA_OK) return st;
-    tree_mask_kernel<<<(unsigned)blocks, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        parents, mask, batch, nodes, words);
-    return launched();
+    return launched(launch_dependent(tree_mask_kernel, dim3((unsigned)blocks), dim3(256), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), parents, mask, batch,
+                                     nodes, words));
 }
 
 }  // extern "C"

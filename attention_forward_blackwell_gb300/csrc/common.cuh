@@ -16,6 +16,42 @@ constexpr unsigned int kErrWaitTimeout = 0x1000u;
 // microseconds; the limit only bounds how long a broken pipeline can stall.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 
+// --------------------------------------------------- dependent launches ----
+//
+// The serving kernels are a few microseconds long and follow one another, so
+// the launch of each overlaps the end of the one before it in its stream
+// (programmatic dependent launch): its CTAs may start once every CTA of the
+// one before has called dependents_may_start() or returned, and each of them
+// calls wait_for_previous() before it touches global memory, which returns
+// when the kernel before has completed and its writes are visible.  Every CTA
+// calls it, so that completion is transitive along the stream.  Measured on
+// GB300: about 1.5 us less per kernel of a chain.
+
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t s, A&&... args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = grid;
+    config.blockDim = block;
+    config.dynamicSmemBytes = smem;
+    config.stream = s;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, kernel, static_cast<P>(args)...);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void dependents_may_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // ----------------------------------------------------------- prefill ----
 
 struct PrefillArgs {

@@ -91,6 +91,10 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     decode_split_kernel(const DecodeArgs a) {
     using T = DecodeTraits<D>;
     extern __shared__ __align__(128) uint8_t smem[];
+    if constexpr (MODE != kModePlain) {
+        dependents_may_start();
+        wait_for_previous();
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x;
     const int hkv = blockIdx.y / a.n_mtiles;
@@ -386,6 +390,10 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
 // normaliser without a value) if there is one.
 template <int D, int MODE>
 __global__ void __launch_bounds__(256) decode_combine_kernel(const DecodeArgs a) {
+    if constexpr (MODE != kModePlain) {
+        dependents_may_start();
+        wait_for_previous();
+    }
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const long long n_rows = (long long)a.B * a.Hq * a.Sq;
@@ -452,11 +460,18 @@ cudaError_t launch_decode_mode(const DecodeArgs& a, cudaStream_t s) {
                                          T::SMEM);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)a.n_splits, (unsigned)(a.Hkv * a.n_mtiles), (unsigned)a.B);
+    const long long rows = (long long)a.B * a.Hq * a.Sq;
+    const unsigned combine_ctas = (unsigned)((rows + 7) / 8);
+    if constexpr (MODE != kModePlain) {
+        e = launch_dependent(split, grid, dim3(T::THREADS), T::SMEM, s, a);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(decode_combine_kernel<D, MODE>, dim3(combine_ctas), dim3(256), 0, s,
+                                a);
+    }
     split<<<grid, T::THREADS, T::SMEM, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long long rows = (long long)a.B * a.Hq * a.Sq;
-    decode_combine_kernel<D, MODE><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
+    decode_combine_kernel<D, MODE><<<combine_ctas, 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 

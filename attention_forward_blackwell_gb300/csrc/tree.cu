@@ -680,6 +680,7 @@ __global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
     auto* aux = reinterpret_cast<TreeAux*>(smem_raw + (sQ - raw) + T::SMEM_Q + T::SMEM_RING);
     const int warp = threadIdx.x >> 5;
     const int wg = warp >> 2;
+    dependents_may_start();
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&aux->bar_q), 1);
         for (int i = 0; i < T::NSLOT; ++i) {
@@ -700,13 +701,15 @@ __global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
         aux->abort_flag = 0;
         aux->start_b = 0;
         aux->start_off = 0;
-        a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
         mbar_fence_init();
     }
     if (warp == T::MMA_WARP) {
         tmem_alloc(smem_u32(&aux->tmem_base), T::TMEM_COLS);
         tmem_relinquish();
     }
+    wait_for_previous();   // (what is above overlaps the kernel before)
+    if (threadIdx.x == 0)
+        a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     tree_place<T>(a, aux);
     tc_fence_before();
     __syncthreads();
@@ -752,6 +755,8 @@ __global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
 template <int D>
 __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeArgs a) {
     using T = TreeTraits<D>;
+    dependents_may_start();
+    wait_for_previous();
     const int r = threadIdx.x, c16 = blockIdx.y, G = gridDim.x;
     for (int b = blockIdx.x; b < a.B; b += G) {
         const int nodes = tree_count(a, b);
@@ -824,10 +829,10 @@ cudaError_t launch_tree_impl(const TreeLaunch& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          T::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    kern<<<p.ctas, T::THREADS, T::SMEM_TOTAL, s>>>(p.tm_q, p.tm_k, p.tm_v, p.args);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    tree_combine_kernel<D><<<dim3(p.ctas, D / 16), T::BM, 0, s>>>(p.args);
-    return cudaGetLastError();
+    e = launch_dependent(kern, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL, s, p.tm_q, p.tm_k,
+                         p.tm_v, p.args);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(tree_combine_kernel<D>, dim3(p.ctas, D / 16), dim3(T::BM), 0, s, p.args);
 }
 
 }  // namespace
