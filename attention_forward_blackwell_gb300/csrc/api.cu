@@ -202,7 +202,12 @@ fa_status check_paged(const int* seqlens_k, const int* block_table, int max_page
     return FA_OK;
 }
 
-struct Varlen;
+// Packed variable-length sequences (see fa_fwd_prefill_varlen).
+struct Varlen {
+    const int* cu_seqlens_q;
+    const int* cu_seqlens_k;
+    int total_q, total_k;
+};
 fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
                        int hq, int hkv, int sq, int sk, const int* seqlens_k, int head_dim,
                        float scale, int causal, int window, const float* sinks,
@@ -228,60 +233,119 @@ constexpr int kDecodeToPrefillRows = 32;
 
 // Query rows per kv head up to which a tree runs the split-KV kernel.
 constexpr int kTreeSplitRows = 16;
+// Keys of all (batch entry, kv head) pairs up to which a windowed decode with
+// first keys does.
+constexpr long long kWindowSplitKeys = 100000;
 
-// A tree of query nodes on the tensor-core kernel (tree.cu).
-fa_status tree_impl(const Tree& tree, const void* q, const void* k, const void* v, void* o,
-                    float* lse, int batch, int hq, int hkv, int nodes, int sk,
-                    const int* seqlens_k, int head_dim, float scale, const float* sinks,
-                    const int* block_table, int max_pages, int page_size, int num_pages,
-                    const DeviceInfo& di, cudaStream_t s) {
-    TreeLaunch p{};
-    TreeArgs& a = p.args;
+// A tree of query nodes (tree != nullptr, sq = nodes) or a window whose first
+// keys stay visible, on the tensor-core kernel (span.cu).  vl: packed queries,
+// and packed keys unless there is a block table.
+bool span_ok(int head_dim, int group, const int* block_table, int page_size) {
+    return (head_dim == 64 || head_dim == 128 || head_dim == 256) && group <= 128 &&
+           (!block_table || span_box(head_dim, page_size, 64) > 0);
+}
+fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* v, void* o,
+                    float* lse, int batch, int hq, int hkv, int sq, int sk, const int* seqlens_k,
+                    int head_dim, float scale, int causal, int window, int first,
+                    const float* sinks, const int* block_table, int max_pages, int page_size,
+                    int num_pages, const Varlen* vl, const DeviceInfo& di, cudaStream_t s) {
+    SpanLaunch p{};
+    SpanArgs& a = p.args;
     const unsigned long long row_bytes = (unsigned long long)head_dim * 2;
-    const long long rows = (long long)(hq / hkv) * nodes;
-    const long long tiles = (rows + 127) / 128;
-    const long long planes = block_table ? (long long)num_pages * hkv : (long long)batch * hkv;
-    if (planes >= (1ll << 31) || hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-    a.box = block_table ? tree_box(head_dim, page_size) : 0;
-    const unsigned k_rows = a.box ? a.box : tree_block_keys(head_dim);
-    const unsigned v_rows = a.box ? a.box : tree_slot_keys(head_dim);
-    const int key_rows = block_table ? page_size : sk;
-    if (!encode_map_strided(&p.tm_q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
-                            row_bytes * rows) ||
-        !encode_map_strided(&p.tm_k, k, head_dim, key_rows, planes, row_bytes,
-                            row_bytes * key_rows, k_rows) ||
-        !encode_map_strided(&p.tm_v, v, head_dim, key_rows, planes, row_bytes,
-                            row_bytes * key_rows, v_rows))
+    const int group = hq / hkv;
+    const bool packed_k = vl && !block_table;
+    // boxes: a page's rows, or 64 on either side of a window's gap; a tree over
+    // contiguous keys copies whole blocks
+    a.box = block_table ? span_box(head_dim, page_size, tree ? 128 : 64) : (tree ? 0 : 64);
+    const long long planes = block_table ? (long long)num_pages * hkv
+                             : packed_k  ? hkv
+                                         : (long long)batch * hkv;
+    if (planes >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    a.planes = (int)planes;
+    long long tiles;
+    if (tree) {
+        const long long rows = (long long)group * sq;
+        tiles = (rows + 127) / 128;
+        if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+        a.tiles = (int)tiles;
+        // up to 8 tiles go side by side over the same keys
+        a.tile_groups = (a.tiles + 7) / 8;
+        a.group_ctas = (a.tiles + a.tile_groups - 1) / a.tile_groups;
+        a.q_bytes = 128 * head_dim * 2;
+        if (!encode_map_strided(&p.tm_q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
+                                row_bytes * rows))
+            return FA_ERR_INVALID_ARG;
+    } else {
+        a.P = std::min(128 / group, sq);
+        tiles = (sq + a.P - 1) / a.P;
+        if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+        a.group_ctas = 1;
+        a.q_bytes = a.P * group * head_dim * 2;
+        if (!(vl ? encode_map_strided(&p.tm_q, q, head_dim, vl->total_q, hq, row_bytes * hq,
+                                      row_bytes, a.P, group)
+                 : encode_map_strided(&p.tm_q, q, head_dim, sq, (long long)batch * hq, row_bytes,
+                                      row_bytes * sq, a.P, group)))
+            return FA_ERR_INVALID_ARG;
+    }
+    const unsigned k_rows = a.box ? a.box : span_block_keys(head_dim);
+    const unsigned v_rows = a.box ? a.box : span_slot_keys(head_dim);
+    const long long key_rows = block_table ? page_size : packed_k ? vl->total_k : sk;
+    const unsigned long long row_stride = packed_k ? row_bytes * hkv : row_bytes;
+    const unsigned long long plane_stride = packed_k ? row_bytes : row_bytes * key_rows;
+    if (!encode_map_strided(&p.tm_k, k, head_dim, key_rows, planes, row_stride, plane_stride,
+                            k_rows) ||
+        !encode_map_strided(&p.tm_v, v, head_dim, key_rows, planes, row_stride, plane_stride,
+                            v_rows))
         return FA_ERR_INVALID_ARG;
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
     a.seqlens_k = seqlens_k;
-    a.tree_mask = tree.mask;
-    a.tree_lens = tree.lens;
-    a.tree_words = (nodes + 31) / 32;
-    a.tree_stride = tree.shared ? 0 : (long long)nodes * a.tree_words;
+    const int bn = span_block_keys(head_dim);
+    long long keys = sk;   // most keys of a unit
+    if (tree) {
+        a.tree_mask = tree->mask;
+        a.tree_lens = tree->lens;
+        a.tree_words = (sq + 31) / 32;
+        a.tree_stride = tree->shared ? 0 : (long long)sq * a.tree_words;
+    } else {
+        a.causal = causal ? 1 : 0;
+        a.window = std::min(window, 1 << 30);
+        a.first = std::min(first, sk);
+        a.head_keys = (a.first + a.box - 1) / a.box * a.box;
+        // a causal tile's axis: the first keys, the window of its first row
+        // rounded down to a box, its other rows
+        a.window_keys = (int)std::min<long long>(
+            sk, (long long)a.head_keys + a.window + a.P - 1 + a.box);
+        if (causal) keys = a.window_keys;
+    }
+    if (vl) {
+        a.cu_seqlens_q = vl->cu_seqlens_q;
+        a.cu_seqlens_k = block_table ? nullptr : vl->cu_seqlens_k;
+        a.total_q = vl->total_q;
+        a.total_k = vl->total_k;
+    }
     a.sinks = sinks;
     a.block_table = block_table;
     a.max_pages = max_pages;
     a.page_size = page_size;
     a.num_pages = num_pages;
     a.B = batch;
+    a.Hq = hq;
     a.Hkv = hkv;
-    a.group = hq / hkv;
-    a.T = nodes;
+    a.group = group;
+    a.Sq = sq;
     a.Sk = sk;
-    a.rows = (int)rows;
-    a.tiles = (int)tiles;
-    a.units = hkv * (int)tiles;
-    a.min_quota = 1;
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err_word = di.err_word;
     a.wait_limit_ns = kWaitLimitNs;
     // one CTA per SM, or one per key block where there are fewer (of the
-    // longest the sequences can be: the host does not know their lengths)
-    const int bn = tree_block_keys(head_dim);
-    const long long most = (long long)batch * a.units * ((sk + bn - 1) / bn);
-    p.ctas = (unsigned)std::min<long long>(di.num_sms, most);
+    // longest the sequences can be: the host does not know their lengths), in
+    // whole groups
+    const long long units =
+        (long long)batch * hkv * (tree ? (long long)a.tile_groups : tiles);
+    const long long blocks = units * std::max<long long>(1, (keys + bn - 1) / bn);
+    const long long groups = std::max(1, di.num_sms / a.group_ctas);
+    p.ctas = (unsigned)(std::min(groups, blocks) * a.group_ctas);
     const size_t slots = 2ull * p.ctas;
     const size_t bytes_o = slots * 128 * head_dim * sizeof(float);
     const size_t bytes_ml = slots * 2 * 128 * sizeof(float);
@@ -292,7 +356,7 @@ fa_status tree_impl(const Tree& tree, const void* q, const void* k, const void* 
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_ml = reinterpret_cast<float*>(ws + bytes_o);
     a.head = reinterpret_cast<int4*>(ws + bytes_o + bytes_ml);
-    const cudaError_t e = launch_tree(p, head_dim, s);
+    const cudaError_t e = launch_span(p, head_dim, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess) return FA_ERR_CUDA;
     return from_cuda(e);
 }
@@ -331,10 +395,14 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
         return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                             causal, 0, sinks, nullptr, 0, 0, 0, stream, nullptr);
 
-    if (tree && (hq / hkv) * sq > kTreeSplitRows && sk > 0 &&
-        (!block_table || tree_box(head_dim, page_size) > 0))
-        return tree_impl(*tree, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
-                         sinks, block_table, max_pages, page_size, num_pages, *di, s);
+    const bool windowed = window > 0 && first > 0;
+    if (sk > 0 && span_ok(head_dim, hq / hkv, block_table, page_size) &&
+        (tree ? (hq / hkv) * sq > kTreeSplitRows
+              : windowed && (long long)batch * hkv * std::min<long long>(sk, (long long)window + first) >
+                                kWindowSplitKeys))
+        return span_impl(tree, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
+                         causal, window, first, sinks, block_table, max_pages, page_size, num_pages,
+                         nullptr, *di, s);
 
     DecodeArgs a{};
     a.q = static_cast<const uint16_t*>(q);
@@ -405,13 +473,6 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
 
 // Prefill on contiguous K/V (block_table == nullptr) or on paged caches
 // [num_pages, hkv, page_size, d] (sk = max_pages * page_size keys per sequence).
-// Packed variable-length sequences (see fa_fwd_prefill_varlen).
-struct Varlen {
-    const int* cu_seqlens_q;
-    const int* cu_seqlens_k;
-    int total_q, total_k;
-};
-
 // Dense, paged (block_table != nullptr) or packed (vl != nullptr; sq is then
 // the largest query length and sk the largest key length) prefill.
 fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, float* lse, int batch,
@@ -437,6 +498,10 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
         return from_cuda(launch_fill_empty(static_cast<uint16_t*>(o), lse, rows, head_dim, sinks,
                                            hq, vl ? vl->total_q : sq, s));
     }
+    if (window > 0 && first > 0 && span_ok(head_dim, hq / hkv, block_table, page_size))
+        return span_impl(nullptr, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
+                         causal, window, first, sinks, block_table, max_pages, page_size, num_pages,
+                         vl, *di, s);
     PrefillLaunch p{};
     const unsigned long long row_bytes = (unsigned long long)head_dim * 2;
     // kernel family, unit and block sizes, work split (head_dim 96 / 128,

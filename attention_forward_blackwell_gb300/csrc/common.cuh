@@ -290,27 +290,37 @@ struct DecodeArgs {
 
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, cudaStream_t s);
 
-// -------------------------------------------------------------- tree ----
+// -------------------------------------------------------------- span ----
 
-// The tensor-core kernel of a tree of query nodes (tree.cu).  The query rows
-// of a key/value head, group heads x T nodes, are rows of one matrix.
-struct TreeArgs {
-    uint16_t* o;                // [B, Hkv, rows, d]
-    float* lse;                 // [B, Hkv, rows]
+// The tensor-core kernel of token trees and of windows with first keys
+// (span.cu).
+enum SpanMode { kSpanTree = 0, kSpanWindow = 1 };
+
+struct SpanArgs {
+    uint16_t* o;                // [B, Hq, Sq, d], or packed [total_q, Hq, d]
+    float* lse;                 // [B, Hq, Sq], or packed [Hq, total_q]
     const int* seqlens_k;       // [B] or nullptr (Sk)
-    const uint32_t* tree_mask;  // as in DecodeArgs
+    const uint32_t* tree_mask;  // as in DecodeArgs; nullptr: a window
     const int* tree_lens;
     int tree_words;
     long long tree_stride;
-    const float* sinks;         // [Hkv * group] or nullptr
+    int causal, window, first;
+    int head_keys;              // first, rounded up to boxes
+    int window_keys;            // most positions of a causal tile's axis
+    const int* cu_seqlens_q;    // packed queries and keys, as in PrefillArgs
+    const int* cu_seqlens_k;
+    int total_q, total_k;
+    const float* sinks;         // [Hq] or nullptr
     const int* block_table;     // as in DecodeArgs
     int max_pages, page_size, num_pages;
-    int box;                    // paged: rows of a tensor-map box (tree_box)
-    int B, Hkv, group, T, Sk;
-    int rows;                   // group * T
-    int tiles;                  // ceil(rows / 128)
-    int units;                  // Hkv * tiles: units of a batch entry
-    int min_quota;              // key blocks that a CTA takes at least
+    int box;                    // rows of a key box (0: whole blocks and slots)
+    int planes;                 // planes of the key maps: the first that does not exist
+    int B, Hq, Hkv, group, Sq, Sk;
+    int q_bytes;                // bytes of a Q tile's copies
+    int P;                      // window: positions of a tile
+    int tiles;                  // tree: tiles of a key/value head,
+    int group_ctas;             // CTAs that walk the same keys, a tile each,
+    int tile_groups;            // ceil(tiles / group_ctas)
     float* part_o;              // [2 CTAs][d / 4][128][4] unnormalised O of pieces
     float* part_ml;             // [2 CTAs][2][128] their row max (log2 units) and sum
     int4* head;                 // [2 CTAs] batch entry, unit, key blocks, and the unit's
@@ -319,24 +329,24 @@ struct TreeArgs {
     unsigned int* err_word;
     unsigned long long wait_limit_ns;
 };
-struct TreeLaunch {
-    CUtensorMap tm_q;           // {d, rows, B * Hkv}, box {64, 128, 1}
-    CUtensorMap tm_k, tm_v;     // contiguous {d, Sk, B * Hkv}: boxes of a block and of a slot;
-                                // paged {d, page_size, num_pages * Hkv}: boxes of `box` rows
-    TreeArgs args;
+struct SpanLaunch {
+    CUtensorMap tm_q;           // tree {d, group * Sq, B * Hkv}, box {64, 128, 1}; window {d, Sq,
+                                // B * Hq} or {d, total_q, Hq}, box {64, P, group}
+    CUtensorMap tm_k, tm_v;     // boxes of `box` rows, or of a block and of a slot
+    SpanArgs args;
     unsigned ctas;
 };
-cudaError_t launch_tree(const TreeLaunch& p, int head_dim, cudaStream_t s);
+cudaError_t launch_span(const SpanLaunch& p, int head_dim, cudaStream_t s);
 
-// Keys of a block and of a V slot of the tree kernel.
-inline int tree_block_keys(int head_dim) { return head_dim == 256 ? 128 : 256; }
-inline int tree_slot_keys(int head_dim) { return 256 * 64 / head_dim; }
-// Rows of a tensor-map box in pages of page_size rows: the largest power of
-// two that divides it, at most 128 and a V slot; 0 below 8 (the swizzle's
-// atom of 8 rows).
-inline int tree_box(int head_dim, int page_size) {
+// Keys of a block and of a V slot of the span kernel.
+inline int span_block_keys(int head_dim) { return head_dim == 256 ? 128 : 256; }
+inline int span_slot_keys(int head_dim) { return 256 * 64 / head_dim; }
+// Rows of a box in pages of page_size rows: the largest power of two that
+// divides it, at most `most` and a V slot; 0 below 8 (the swizzle's atom of 8
+// rows).
+inline int span_box(int head_dim, int page_size, int most) {
     int box = page_size & -page_size;
-    const int most = tree_slot_keys(head_dim) < 128 ? tree_slot_keys(head_dim) : 128;
+    if (span_slot_keys(head_dim) < most) most = span_slot_keys(head_dim);
     if (box > most) box = most;
     return box >= 8 ? box : 0;
 }

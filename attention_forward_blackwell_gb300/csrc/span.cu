@@ -1,24 +1,37 @@
-// Attention of a tree of drafted tokens over a cache, on the tensor cores
-// (head_dim 64, 128 and 256).
+// Attention of rows that share spans of keys, on the tensor cores (head_dim
+// 64, 128 and 256): a tree of drafted tokens over a cache (MODE kSpanTree), and
+// a sliding window whose first keys stay visible (kSpanWindow; prompts, chunks
+// of prompts and single tokens).
 //
-// All query rows of a key/value head (group heads x T nodes) see the same
-// keys up to the tree, and lie side by side in memory: the rows
-// [b, hk * group .. + group, 0 .. T) of Q and O are one matrix of
-// R = group * T rows.  A tile is 128 of them, whatever T is; row r of the
-// matrix is node r % T.  Only the last keys, the nodes' own, are masked, by
-// the bits of the row's node.
+// Rows.  All query heads of a key/value head read the same keys, so a tile of
+// 128 rows holds several of them.  For a tree the rows [b, hk * group ..
+// + group, 0 .. T) of Q and O lie side by side in memory, one matrix of group *
+// T rows; a tile is 128 of them whatever T is, and row r of the matrix is node
+// r % T.  For a window a tile is `group` heads x P = 128 / group positions
+// (row r: head r / P, position r % P of the tile), so that the keys it visits,
+// window + P, grow least.
+//
+// Keys.  A tile visits positions [0, span) of an axis of its own: for a window
+// the first keys rounded up to a box of rows, then, skipping what no row sees,
+// the keys from its first row's window on, rounded down to one (span_geometry);
+// a tree visits every key.  So no block is spent on the few first keys alone,
+// and blocks of 256 keys waste less of a window than their size suggests.
+// Only the blocks at the borders are masked.
 //
 // What bounds it: per key of a key/value head 4 d bytes of K and V are read
-// and 4 d R operations done, so up to about 270 rows memory is the bound and
-// past it the tensor cores (1865 TFLOP/s over 6793 GB/s, both measured).  The
-// keys are therefore spread evenly over the SMs: with nb_b key blocks per
-// unit (batch entry, key/value head, row tile), the units' blocks, one after
-// the other, form one line of N blocks, and CTA x takes the blocks
-// [x quota, (x + 1) quota), quota = ceil(N / CTAs), whatever the sequences'
-// lengths (which only the device knows).  A unit that lies in one CTA is
-// finished there; of the others each CTA writes its piece's unnormalised O,
-// row max and row sum, and tree_combine_kernel merges the pieces, in their
-// order (the result does not depend on timing).
+// and 4 d operations per row done, so up to about 270 rows that share it
+// memory is the bound and past it the tensor cores (1865 TFLOP/s over 6793
+// GB/s, both measured).  The blocks are therefore spread evenly over the SMs:
+// the units' (batch entry, key/value head, tile) blocks, one after the other,
+// form one line of N blocks, and CTA x takes the blocks [x quota, (x + 1)
+// quota), quota = ceil(N / CTAs), whatever the sequences' lengths (which only
+// the device knows).  A unit that lies in one CTA is finished there; of the
+// others each CTA writes its piece's unnormalised O, row max and row sum, and
+// span_combine_kernel merges the pieces, in their order (the result does not
+// depend on timing).  A tree of several tiles gives each to a CTA of a group
+// that walks the same keys at the same time, so that K and V come from HBM
+// once (one tile after the other, a 64-node tree of 8 heads read them three
+// times and took 117 us instead of %GROUPED%).
 //
 // Inside a CTA: the roles and barriers of the 256-key prefill kernel (see
 // prefill_wide.cuh), which this one follows: S = Q K^T of the next block is
@@ -27,9 +40,9 @@
 // blocks are 256 keys (one N = 256 score instruction per 16 head dims), 128 at
 // head_dim 256, whose 256 O columns leave no room for more.
 //
-// Paged caches: a box of the tensor maps is as many rows of one page as the
-// page's size allows (the largest power of two that divides it, 8 at least),
-// one lane of the producer per box, the page numbers fetched a block ahead.
+// Boxes (BOXED): a box of the tensor maps is as many rows as always lie
+// together -- of one page, of one side of the window's gap -- one lane of the
+// producer per box, page numbers fetched a block ahead.
 #include "prefill.cuh"
 #include "../../include/fa.h"
 
@@ -37,7 +50,7 @@ namespace fa {
 namespace {
 
 template <int D>
-struct TreeTraits {
+struct SpanTraits {
     static constexpr int BM = 128;                  // rows of a tile = TMEM lanes
     static constexpr int BN = D == 256 ? 128 : 256; // keys of a block
     static constexpr int HK = BN / 2;               // keys of a softmax half
@@ -73,12 +86,12 @@ struct TreeTraits {
     static_assert(SMEM_TOTAL <= 232448, "shared memory per CTA exceeds the sm_103 limit");
 };
 
-constexpr int kTreeSlots = 6;
+constexpr int kSpanSlots = 6;
 
-struct TreeAux {
+struct SpanAux {
     uint64_t bar_q;
-    uint64_t bar_full[kTreeSlots];
-    uint64_t bar_empty[kTreeSlots];
+    uint64_t bar_full[kSpanSlots];
+    uint64_t bar_empty[kSpanSlots];
     uint64_t bar_s_full;
     uint64_t bar_xm[2];
     uint64_t bar_p_ready[2];
@@ -98,66 +111,159 @@ struct TreeAux {
     float mb_l[2][128];       // [half][row] row sums of a segment
 };
 
-// Keys and nodes of sequence b.
-__device__ __forceinline__ int tree_keys(const TreeArgs& a, int b) {
-    return a.seqlens_k != nullptr ? max(0, min(a.seqlens_k[b], a.Sk)) : a.Sk;
+// A sequence: query rows (nodes) and keys, in packed tensors its first query
+// and key token, and the rows that are computed (packed: at most the launch's).
+struct SpanSeq {
+    int rows, keys, q0, k0, cap;
+};
+template <int MODE>
+__device__ __forceinline__ SpanSeq span_seq(const SpanArgs& a, int b) {
+    SpanSeq q{a.Sq, a.Sk, 0, 0, 0};
+    if (MODE == kSpanTree) {
+        if (a.tree_lens != nullptr) q.rows = max(0, min(a.tree_lens[b], a.Sq));
+    } else if (a.cu_seqlens_q != nullptr) {   // (clamped: bad offsets stay inside the tensors)
+        q.q0 = min(max(a.cu_seqlens_q[b], 0), a.total_q);
+        q.rows = min(max(a.cu_seqlens_q[b + 1], q.q0), a.total_q) - q.q0;
+    }
+    if (a.seqlens_k != nullptr) {
+        q.keys = max(0, min(a.seqlens_k[b], a.Sk));
+    } else if (MODE == kSpanWindow && a.cu_seqlens_k != nullptr) {
+        q.k0 = min(max(a.cu_seqlens_k[b], 0), a.total_k);
+        q.keys = min(max(a.cu_seqlens_k[b + 1], q.k0), a.total_k) - q.k0;
+    }
+    q.cap = min(q.rows, a.Sq);
+    return q;
 }
-__device__ __forceinline__ int tree_count(const TreeArgs& a, int b) {
-    return a.tree_lens != nullptr ? max(0, min(a.tree_lens[b], a.T)) : a.T;
+// Units of a batch entry, and the key blocks each counts for on the line: a
+// bound for a window (its tiles near the start have fewer), one at least, so
+// that rows without keys are written too.
+template <int MODE>
+__device__ __forceinline__ int span_units(const SpanArgs& a, const SpanSeq& q) {
+    if (q.cap == 0) return 0;
+    return a.Hkv * (MODE == kSpanTree ? a.tile_groups : (q.cap + a.P - 1) / a.P);
 }
-// Key blocks of each of sequence b's units.
-template <class T>
-__device__ __forceinline__ int tree_blocks(const TreeArgs& a, int b) {
-    return tree_count(a, b) > 0 ? (tree_keys(a, b) + T::BN - 1) / T::BN : 0;
+template <class T, int MODE>
+__device__ __forceinline__ int span_blocks(const SpanArgs& a, const SpanSeq& q) {
+    int keys = q.keys;
+    if (MODE == kSpanWindow && a.causal) keys = min(keys, a.window_keys);
+    return max(1, (keys + T::BN - 1) / T::BN);
 }
 
 // The CTA's segments in turn: `n` consecutive key blocks from kb on of a
-// unit with nb blocks.
-struct TreeSeg {
-    int b, u;        // batch entry, unit of it: hk * tiles + tile
+// unit with nb blocks, m of them real.
+struct SpanSeg {
+    int b, u;        // batch entry, unit of it
     int kb, n, nb;
-    int L, nodes;
     int left;        // blocks of the CTA after this segment
     int index;       // segments before it
+    SpanSeq q;
+    int units;       // of the batch entry
+    // the unit's tile (see span_geometry)
+    int hk, tile, m;
+    int head, skip;  // position x of its axis: key x below head, key x + skip from there on
+    int span;        // positions that a row may see
+    int end;         // position of the sequence's end
 };
-template <class T>
-__device__ __forceinline__ bool tree_first(const TreeArgs& a, const TreeAux* aux, TreeSeg& s) {
+
+__device__ __forceinline__ int span_key(const SpanSeg& s, int x) {
+    return x < s.head ? x : x + s.skip;
+}
+
+// The tile of unit s.u and the axis of its keys.
+template <class T, int MODE>
+__device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanSeg& s) {
+    s.head = s.skip = 0;
+    if constexpr (MODE == kSpanTree) {
+        s.hk = s.u / a.tile_groups;
+        s.tile = (s.u % a.tile_groups) * a.group_ctas + (int)blockIdx.x % a.group_ctas;
+        s.span = s.end = s.tile < a.tiles ? s.q.keys : 0;
+    } else {
+        const int tiles = (s.q.cap + a.P - 1) / a.P;
+        s.hk = s.u / tiles;
+        s.tile = s.u % tiles;
+        const int off = s.q.keys - s.q.rows;   // bottom-right alignment
+        const int p0 = s.tile * a.P + off;     // keys of the tile's first and last row
+        const int p1 = min(s.tile * a.P + a.P, s.q.cap) - 1 + off;
+        const int last = a.causal ? min(s.q.keys - 1, p1) : s.q.keys - 1;
+        const int base = max(0, p0 - a.window + 1) / a.box * a.box;
+        if (a.head_keys < base) {
+            s.head = a.head_keys;
+            s.skip = base - s.head;
+        }
+        s.span = max(0, last + 1 - s.skip);
+        s.end = s.q.keys - s.skip;
+    }
+    const int real = (s.span + T::BN - 1) / T::BN;
+    s.m = max(0, min(s.kb + s.n, real) - s.kb);
+}
+
+template <class T, int MODE>
+__device__ __forceinline__ bool span_first(const SpanArgs& a, const SpanAux* aux, SpanSeg& s) {
     s.left = aux->start_n;
     if (s.left <= 0) return false;
     s.b = aux->start_b;
-    s.nb = tree_blocks<T>(a, s.b);
+    s.q = span_seq<MODE>(a, s.b);
+    s.units = span_units<MODE>(a, s.q);
+    s.nb = span_blocks<T, MODE>(a, s.q);
     s.u = (int)(aux->start_off / s.nb);
     s.kb = (int)(aux->start_off % s.nb);
-    s.L = tree_keys(a, s.b);
-    s.nodes = tree_count(a, s.b);
     s.n = min(s.nb - s.kb, s.left);
     s.left -= s.n;
     s.index = 0;
+    span_geometry<T, MODE>(a, s);
     return true;
 }
-template <class T>
-__device__ __forceinline__ bool tree_next(const TreeArgs& a, TreeSeg& s) {
+template <class T, int MODE>
+__device__ __forceinline__ bool span_next(const SpanArgs& a, SpanSeg& s) {
     if (s.left <= 0) return false;
     s.kb = 0;
-    if (++s.u == a.units) {
+    if (++s.u == s.units) {
         s.u = 0;
         do {
-            if (++s.b >= a.B) return false;   // (never: `left` counts real blocks)
-            s.nb = tree_blocks<T>(a, s.b);
-        } while (s.nb == 0);
-        s.L = tree_keys(a, s.b);
-        s.nodes = tree_count(a, s.b);
+            if (++s.b >= a.B) return false;   // (never: `left` counts blocks that are there)
+            s.q = span_seq<MODE>(a, s.b);
+            s.units = span_units<MODE>(a, s.q);
+        } while (s.units == 0);
+        s.nb = span_blocks<T, MODE>(a, s.q);
     }
     s.n = min(s.nb, s.left);
     s.left -= s.n;
     ++s.index;
+    span_geometry<T, MODE>(a, s);
     return true;
+}
+
+// Tile row r: its query head, position (node), and index among the rows of O
+// (the LSE's too, but of packed tensors); whether it is a row of the sequence.
+template <class T, int MODE>
+__device__ __forceinline__ bool span_row(const SpanArgs& a, const SpanSeq& q, int b, int hk,
+                                         int tile, int r, int& h, int& pos, size_t& o_row,
+                                         size_t& lse_at) {
+    bool real;
+    if constexpr (MODE == kSpanTree) {
+        const int row = tile * T::BM + r;
+        h = hk * a.group + row / a.Sq;
+        pos = row % a.Sq;
+        real = row < a.group * a.Sq && pos < q.cap;
+    } else {
+        const int g = r / a.P;
+        h = hk * a.group + g;
+        pos = tile * a.P + r % a.P;
+        real = g < a.group && pos < q.cap;
+        if (a.cu_seqlens_q != nullptr) {
+            o_row = (size_t)(q.q0 + pos) * a.Hq + h;
+            lse_at = (size_t)h * a.total_q + q.q0 + pos;
+            return real;
+        }
+    }
+    o_row = lse_at = ((size_t)b * a.Hq + h) * a.Sq + pos;
+    return real;
 }
 
 // Places the CTA on the line of blocks (all threads): the sequences' blocks
 // are summed, then the one that holds the CTA's first block is found.
-template <class T>
-__device__ void tree_place(const TreeArgs& a, TreeAux* aux) {
+template <class T, int MODE>
+__device__ void span_place(const SpanArgs& a, SpanAux* aux) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto scan = [&](long long v, long long& total) -> long long {   // exclusive, over the block
         long long x = v;
@@ -179,18 +285,23 @@ __device__ void tree_place(const TreeArgs& a, TreeAux* aux) {
         }
         return before + x - v;
     };
+    auto blocks_of = [&](int b) -> long long {   // of all of a batch entry's units
+        if (b >= a.B) return 0;
+        const SpanSeq q = span_seq<MODE>(a, b);
+        return (long long)span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
+    };
     long long all = 0, mine = 0, total;
-    for (int b = threadIdx.x; b < a.B; b += T::THREADS)
-        mine += (long long)tree_blocks<T>(a, b) * a.units;
+    for (int b = threadIdx.x; b < a.B; b += T::THREADS) mine += blocks_of(b);
     scan(mine, all);
-    long long quota = (all + gridDim.x - 1) / gridDim.x;
-    if (quota < a.min_quota) quota = a.min_quota;
-    const long long beg = quota * blockIdx.x;
+    const int group_ctas = MODE == kSpanTree ? a.group_ctas : 1;
+    const int groups = (int)gridDim.x / group_ctas;
+    const long long quota = (all + groups - 1) / groups;
+    const long long beg = quota * ((int)blockIdx.x / group_ctas);
     if (threadIdx.x == 0) aux->start_n = (int)max(0ll, min(quota, all - beg));
     long long base = 0;
     for (int b0 = 0; b0 < a.B && base <= beg; b0 += T::THREADS) {
         const int b = b0 + threadIdx.x;
-        const long long v = b < a.B ? (long long)tree_blocks<T>(a, b) * a.units : 0;
+        const long long v = blocks_of(b);
         const long long at = base + scan(v, total);
         if (at <= beg && beg < at + v) {
             aux->start_b = b;
@@ -202,9 +313,9 @@ __device__ void tree_place(const TreeArgs& a, TreeAux* aux) {
 }
 
 // Producer: per segment K_0, Q, then K_{j+1} and V_j for every block j.
-template <class T, bool PAGED>
-__device__ void tree_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                               const CUtensorMap* tm_v, const TreeArgs& a, TreeAux* aux,
+template <class T, int MODE, bool BOXED>
+__device__ void span_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
+                               const CUtensorMap* tm_v, const SpanArgs& a, SpanAux* aux,
                                uint32_t sQ, uint32_t sRing, const WaitCtx& wc) {
     const int lane = threadIdx.x & 31;
     const uint32_t bar_q = smem_u32(&aux->bar_q);
@@ -215,24 +326,32 @@ __device__ void tree_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
     }
     int p = 0, ntail = 0, kq = 0;
     bool ok = true;
-    TreeSeg s;
-    for (bool more = tree_first<T>(a, aux, s); more && ok; more = tree_next<T>(a, s)) {
-        const int hk = s.u / a.tiles, tile = s.u % a.tiles;
-        const int plane = s.b * a.Hkv + hk;
-        // PAGED: lane i's box of block j, rows [i box, (i + 1) box) of it: the
-        // plane of its page (past the sequence, or no page: a plane that does
-        // not exist, which reads as zeros)
-        const int boxes = PAGED ? T::BN / a.box : 0;
-        auto box_plane = [&](int j) -> int {
-            const int key = (s.kb + j) * T::BN + lane * a.box;
-            int pl = a.num_pages * a.Hkv;
-            if (lane < boxes && key < s.L) {
-                const int page = a.block_table[(size_t)s.b * a.max_pages + key / a.page_size];
-                if ((unsigned)page < (unsigned)a.num_pages) pl = page * a.Hkv + hk;
-            }
-            return pl;
+    SpanSeg s;
+    for (bool more = span_first<T, MODE>(a, aux, s); more && ok; more = span_next<T, MODE>(a, s)) {
+        if (s.m == 0) continue;
+        const int plane = (a.cu_seqlens_k != nullptr ? 0 : s.b * a.Hkv) + s.hk;
+        // BOXED: lane i's box of block j, positions [i box, (i + 1) box) of it:
+        // where it lies in the tensor map (past the span, or no page: a plane
+        // that does not exist, which reads as zeros)
+        const int boxes = BOXED ? T::BN / a.box : 0;
+        struct Box {
+            int row, plane;
         };
-        auto box_row = [&](int j) { return ((s.kb + j) * T::BN + lane * a.box) % a.page_size; };
+        auto box_of = [&](int j) -> Box {
+            const int x = (s.kb + j) * T::BN + lane * a.box;
+            Box at{0, a.planes};
+            if (lane < boxes && x < s.span) {
+                const int key = span_key(s, x);
+                if (a.block_table == nullptr) {
+                    at = Box{s.q.k0 + key, plane};
+                } else {
+                    const int page = a.block_table[(size_t)s.b * a.max_pages + key / a.page_size];
+                    if ((unsigned)page < (unsigned)a.num_pages)
+                        at = Box{key % a.page_size, page * a.Hkv + s.hk};
+                }
+            }
+            return at;
+        };
         auto acquire = [&](uint32_t& dst, uint32_t& full) -> bool {
             const uint32_t slot = ring_slot<T>(p);
             if (!mbar_wait(smem_u32(&aux->bar_empty[slot]), ring_phase<T>(p) ^ 1u, wc,
@@ -242,17 +361,17 @@ __device__ void tree_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
             full = smem_u32(&aux->bar_full[slot]);
             return true;
         };
-        auto load_k = [&](int j, int c, int pl) -> bool {
+        auto load_k = [&](int j, int c, const Box& at) -> bool {
             uint32_t dst, full;
             if (!acquire(dst, full)) return false;
             if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)T::SLOT);
-            if constexpr (PAGED) {
+            if constexpr (BOXED) {
                 __syncwarp();
                 if (lane < boxes) {
 #pragma unroll
                     for (int q = 0; q < T::KCH; ++q)
                         tma_load_3d(dst + q * T::KCHUNK + lane * a.box * 128, tm_k,
-                                    (c * T::KCH + q) * 64, box_row(j), pl, full);
+                                    (c * T::KCH + q) * 64, at.row, at.plane, full);
                 }
             } else if (lane == 0) {
 #pragma unroll
@@ -264,22 +383,22 @@ __device__ void tree_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
             ++p;
             return true;
         };
-        auto load_v = [&](int j, int hh, int pl) -> bool {
+        auto load_v = [&](int j, int hh, const Box& at) -> bool {
             uint32_t dst, full;
             if (!acquire(dst, full)) return false;
-            const int r0 = (s.kb + j) * T::BN + hh * T::VKEYS;   // first key of the slot
-            const int rv = s.L - r0;                             // its valid keys
+            const int r0 = (s.kb + j) * T::BN + hh * T::VKEYS;   // first position of the slot
+            const int rv = s.end - r0;                           // keys of the sequence in it
             const bool tail = rv < T::VKEYS;
             const uint32_t bar = tail ? smem_u32(&aux->bar_tail) : full;
             if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
-            if constexpr (PAGED) {
+            if constexpr (BOXED) {
                 __syncwarp();
                 const int per = T::VKEYS / a.box, i = lane - hh * per;
                 if (i >= 0 && i < per) {
 #pragma unroll
                     for (int q = 0; q < T::NCH; ++q)
-                        tma_load_3d(dst + q * T::VCHUNK + i * a.box * 128, tm_v, q * 64,
-                                    box_row(j), pl, bar);
+                        tma_load_3d(dst + q * T::VCHUNK + i * a.box * 128, tm_v, q * 64, at.row,
+                                    at.plane, bar);
                 }
             } else if (lane == 0) {
 #pragma unroll
@@ -308,29 +427,34 @@ __device__ void tree_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
             ++p;
             return true;
         };
-        // page planes of the block whose V is loaded next, and of the next one
-        int pl0 = PAGED ? box_plane(0) : 0;
-        int pl1 = PAGED && s.n > 1 ? box_plane(1) : 0;
-        for (int c = 0; c < T::KP && ok; ++c) ok = load_k(0, c, pl0);
+        // boxes of the block whose V is loaded next, and of the next one
+        Box at0 = box_of(0);
+        Box at1 = s.m > 1 ? box_of(1) : at0;
+        for (int c = 0; c < T::KP && ok; ++c) ok = load_k(0, c, at0);
         if (!ok) break;
         if (kq > 0 && !mbar_wait(smem_u32(&aux->bar_qfree), (uint32_t)((kq - 1) & 1), wc,
                                  kErrWaitTimeout | kSiteLoadQfree))
             break;
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar_q, (uint32_t)T::QTILE);
+            mbar_arrive_expect_tx(bar_q, (uint32_t)a.q_bytes);
+            int row = s.tile * T::BM, q_plane = s.b * a.Hkv + s.hk;   // tree: rows of the matrix
+            if (MODE == kSpanWindow) {   // positions x heads
+                row = s.q.q0 + s.tile * a.P;
+                q_plane = (a.cu_seqlens_q != nullptr ? 0 : s.b * a.Hq) + s.hk * a.group;
+            }
 #pragma unroll
             for (int q = 0; q < T::NCH; ++q)
-                tma_load_3d(sQ + q * T::CHUNK, tm_q, q * 64, tile * T::BM, plane, bar_q);
+                tma_load_3d(sQ + q * T::CHUNK, tm_q, q * 64, row, q_plane, bar_q);
         }
         __syncwarp();
         ++kq;
-        for (int j = 0; j < s.n && ok; ++j) {
-            const int pl2 = PAGED && j + 2 < s.n ? box_plane(j + 2) : 0;
-            if (j + 1 < s.n)
-                for (int c = 0; c < T::KP && ok; ++c) ok = load_k(j + 1, c, pl1);
-            for (int hh = 0; hh < T::VP && ok; ++hh) ok = load_v(j, hh, pl0);
-            pl0 = pl1;
-            pl1 = pl2;
+        for (int j = 0; j < s.m && ok; ++j) {
+            const Box at2 = j + 2 < s.m ? box_of(j + 2) : at1;
+            if (j + 1 < s.m)
+                for (int c = 0; c < T::KP && ok; ++c) ok = load_k(j + 1, c, at1);
+            for (int hh = 0; hh < T::VP && ok; ++hh) ok = load_v(j, hh, at0);
+            at0 = at1;
+            at1 = at2;
         }
     }
     // every copy issued must have landed before the CTA exits
@@ -344,8 +468,8 @@ __device__ void tree_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
 }
 
 // MMA issue (one lane): S(J+1), then PV(J), as in the 256-key prefill kernel.
-template <class T>
-__device__ void tree_mma_role(const TreeArgs& a, TreeAux* aux, uint32_t tmem, uint32_t sQ,
+template <class T, int MODE>
+__device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, uint32_t sQ,
                               uint32_t sRing, const WaitCtx& wc) {
     const int lane = threadIdx.x & 31;
     if (lane != 0) {
@@ -391,9 +515,10 @@ __device__ void tree_mma_role(const TreeArgs& a, TreeAux* aux, uint32_t tmem, ui
     };
     int J0 = 0, kq = 0;
     bool ok = true;
-    TreeSeg s;
-    for (bool more = tree_first<T>(a, aux, s); more && ok; more = tree_next<T>(a, s)) {
-        const int n = s.n;
+    SpanSeg s;
+    for (bool more = span_first<T, MODE>(a, aux, s); more && ok; more = span_next<T, MODE>(a, s)) {
+        const int n = s.m;
+        if (n == 0) continue;
         if (!mbar_wait_lane(smem_u32(&aux->bar_q), (uint32_t)(kq & 1), wc,
                             kErrWaitTimeout | kSiteMmaQ))
             break;
@@ -464,21 +589,39 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* words, int nodes, 
     return __funnelshift_r(word(w), word(w + 1), (uint32_t)o & 31u);
 }
 
+// Bits [0, n) of a word.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
 // Softmax of one segment by warpgroup h (keys [HK h, HK h + HK) of every
 // block; thread = row); see wide_softmax_unit.
-template <class T>
-__device__ bool tree_softmax_segment(int h, const TreeArgs& a, const TreeSeg& s, TreeAux* aux,
+template <class T, int MODE>
+__device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s, SpanAux* aux,
                                      uint32_t tmem, const WaitCtx& wc, int J0, int kq) {
     constexpr int HK = T::HK;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int node = ((s.u % a.tiles) * T::BM + r) % a.T;   // (rows past the last: any row's words)
-    const uint32_t* words = a.tree_mask + s.b * a.tree_stride + (long long)node * a.tree_words;
-    const int node0 = s.L - s.nodes;
+    // what the row sees: a tree's node its mask words from position node0 on,
+    // before it everything; a window's row the positions below fa and [lo, lim]
+    // (rows that do not exist: as some row)
+    const uint32_t* words = nullptr;
+    int node0 = 0, fa = 0, lo = 0, lim = 0;
+    if constexpr (MODE == kSpanTree) {
+        words = a.tree_mask + s.b * a.tree_stride +
+                (long long)((s.tile * T::BM + r) % a.Sq) * a.tree_words;
+        node0 = s.q.keys - s.q.rows;
+    } else {
+        const int p = s.tile * a.P + r % a.P + s.q.keys - s.q.rows;   // the row's key
+        const int last = a.causal ? min(s.q.keys - 1, p) : s.q.keys - 1;
+        fa = min(a.first, last + 1);
+        lim = last - s.skip;
+        lo = max(p - a.window + 1 - s.skip, s.head);
+    }
     const float sl2 = a.scale_log2;
     float m_run = -INFINITY, l_run = 0.f;
-    for (int j = 0; j < s.n; ++j) {
+    for (int j = 0; j < s.m; ++j) {
         const int J = J0 + j;
         const int sb = J & 1;
         const uint32_t par = (uint32_t)((J >> 1) & 1);
@@ -495,11 +638,18 @@ __device__ bool tree_softmax_segment(int h, const TreeArgs& a, const TreeSeg& s,
         float x[HK];
 #pragma unroll
         for (int c = 0; c < HK; ++c) x[c] = __uint_as_float(u[c >> 5][c & 31]);
-        const int kv0 = (s.kb + j) * T::BN + h * HK;   // first key of the half
-        if (kv0 + HK > node0) {                        // the nodes' own keys, or past them
+        const int x0 = (s.kb + j) * T::BN + h * HK;   // first position of the half
+        const bool masked = MODE == kSpanTree ? x0 + HK > node0   // the nodes' own keys, or past
+                                              : (x0 < lo || x0 + HK - 1 > lim) && x0 + HK > fa;
+        if (masked) {
 #pragma unroll
             for (int q = 0; q < HK / 32; ++q) {
-                const uint32_t vis = tree_bits(words, s.nodes, kv0 + 32 * q - node0);
+                const int xq = x0 + 32 * q;
+                uint32_t vis;
+                if constexpr (MODE == kSpanTree)
+                    vis = tree_bits(words, s.q.rows, xq - node0);
+                else
+                    vis = low_bits(fa - xq) | (low_bits(lim + 1 - xq) & ~low_bits(lo - xq));
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     x[32 * q + c] = ((vis >> c) & 1u) ? x[32 * q + c] : -INFINITY;
@@ -569,7 +719,7 @@ __device__ bool tree_softmax_segment(int h, const TreeArgs& a, const TreeSeg& s,
 
 // Sum and max (log2 units) of a row with its head's sink logit, one more term
 // without a value.  Returns what O (in basis m) is multiplied by.
-__device__ __forceinline__ float tree_normaliser(const float* sinks, int h, float& l, float& m) {
+__device__ __forceinline__ float span_normaliser(const float* sinks, int h, float& l, float& m) {
     float scale = 1.f;
     if (sinks != nullptr) {
         const float sg = sinks[h] * kLog2e;
@@ -585,15 +735,15 @@ __device__ __forceinline__ float tree_normaliser(const float* sinks, int h, floa
 // Correction of one segment (thread = row): rebases O when the running max
 // moved; at its end writes O and LSE of a whole unit, or the piece's
 // unnormalised O, max and sum.
-template <class T>
-__device__ bool tree_correction_segment(const TreeArgs& a, const TreeSeg& s, TreeAux* aux,
+template <class T, int MODE>
+__device__ bool span_correction_segment(const SpanArgs& a, const SpanSeg& s, SpanAux* aux,
                                         uint32_t tmem, const WaitCtx& wc, int J0, int kq) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale_log2;
     float m_run = -INFINITY;
-    for (int j = 0; j < s.n; ++j) {
+    for (int j = 0; j < s.m; ++j) {
         const int J = J0 + j;
         const int sb = J & 1;
         if (!mbar_wait(smem_u32(&aux->bar_xm[sb]), (uint32_t)((J >> 1) & 1), wc,
@@ -624,23 +774,26 @@ __device__ bool tree_correction_segment(const TreeArgs& a, const TreeSeg& s, Tre
         tc_fence_before();
         mbar_arrive_warp(smem_u32(&aux->bar_p_ready[sb]));
     }
-    if (!mbar_wait(smem_u32(&aux->bar_fin), (uint32_t)(kq & 1), wc, kErrWaitTimeout | kSiteEpiMbox))
-        return false;
-    float l = aux->mb_l[0][r] + aux->mb_l[1][r];
-    float m = m_run;
-    const int Jl = J0 + s.n - 1;
-    if (!mbar_wait(smem_u32(&aux->bar_pv_done[Jl & 1]), (uint32_t)((Jl >> 1) & 1), wc,
-                   kErrWaitTimeout | kSiteEpiPv))
-        return false;
-    tc_fence_after();
-    const int row = (s.u % a.tiles) * T::BM + r;   // of the key/value head's rows
-    const int hk = s.u / a.tiles;
-    const bool real = row < a.rows && row % a.T < s.nodes;
+    float l = 0.f, m = m_run;
+    if (s.m > 0) {   // (else a unit, or a piece of one, without keys)
+        if (!mbar_wait(smem_u32(&aux->bar_fin), (uint32_t)(kq & 1), wc,
+                       kErrWaitTimeout | kSiteEpiMbox))
+            return false;
+        l = aux->mb_l[0][r] + aux->mb_l[1][r];
+        const int Jl = J0 + s.m - 1;
+        if (!mbar_wait(smem_u32(&aux->bar_pv_done[Jl & 1]), (uint32_t)((Jl >> 1) & 1), wc,
+                       kErrWaitTimeout | kSiteEpiPv))
+            return false;
+        tc_fence_after();
+    }
+    int head, pos;
+    size_t o_row, lse_at;
+    const bool real = span_row<T, MODE>(a, s.q, s.b, s.hk, s.tile, r, head, pos, o_row, lse_at);
     if (s.n < s.nb) {   // a piece
         const int slot = 2 * (int)blockIdx.x + (s.index > 0);
         float4* po = reinterpret_cast<float4*>(a.part_o + (size_t)slot * (T::D_COLS * T::BM));
 #pragma unroll 1
-        for (int c32 = 0; c32 < T::D_COLS / 32; ++c32) {
+        for (int c32 = 0; c32 < (s.m > 0 ? T::D_COLS / 32 : 0); ++c32) {
             uint32_t v[32];
             tmem_ld32(lane_base + T::O_COL + c32 * 32, v);
             tmem_wait_ld();
@@ -656,28 +809,29 @@ __device__ bool tree_correction_segment(const TreeArgs& a, const TreeSeg& s, Tre
         ml[T::BM + r] = l;
         if (r == 0) a.head[slot] = make_int4(s.b, s.u, s.n, s.kb == 0 ? s.nb : 0);
     } else {
-        const float inv_l = tree_normaliser(a.sinks, hk * a.group + row / a.T, l, m);
-        const size_t at = ((size_t)s.b * a.Hkv + hk) * a.rows + row;
-        store_o_rows_direct<T>(lane_base, T::O_COL, a.o + at * T::D_COLS, real, s.n, inv_l, 0,
+        const float inv_l = span_normaliser(real ? a.sinks : nullptr, head, l, m);
+        store_o_rows_direct<T>(lane_base, T::O_COL, a.o + o_row * T::D_COLS, real, s.m, inv_l, 0,
                                T::D_COLS / 32);
-        if (real) a.lse[at] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
+        if (real) a.lse[lse_at] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
     }
-    tc_fence_before();
-    mbar_arrive_warp(smem_u32(&aux->bar_odrained));
+    if (s.m > 0) {
+        tc_fence_before();
+        mbar_arrive_warp(smem_u32(&aux->bar_odrained));
+    }
     return true;
 }
 
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const TreeArgs a) {
-    using T = TreeTraits<D>;
-    static_assert(sizeof(TreeAux) <= T::SMEM_AUX && T::NSLOT <= kTreeSlots, "auxiliary block");
+template <int D, int MODE, bool BOXED>
+__global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
+    span_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const SpanArgs a) {
+    using T = SpanTraits<D>;
+    static_assert(sizeof(SpanAux) <= T::SMEM_AUX && T::NSLOT <= kSpanSlots, "auxiliary block");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sQ = (raw + 1023u) & ~1023u;
     const uint32_t sRing = sQ + T::SMEM_Q;
-    auto* aux = reinterpret_cast<TreeAux*>(smem_raw + (sQ - raw) + T::SMEM_Q + T::SMEM_RING);
+    auto* aux = reinterpret_cast<SpanAux*>(smem_raw + (sQ - raw) + T::SMEM_Q + T::SMEM_RING);
     const int warp = threadIdx.x >> 5;
     const int wg = warp >> 2;
     dependents_may_start();
@@ -710,7 +864,7 @@ __global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
     wait_for_previous();   // (what is above overlaps the kernel before)
     if (threadIdx.x == 0)
         a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-    tree_place<T>(a, aux);
+    span_place<T, MODE>(a, aux);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -719,27 +873,29 @@ __global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
     if (wg < 2) {
         setmaxnreg_inc<T::SOFTMAX_REGS>();
         int J0 = 0, kq = 0;
-        TreeSeg s;
-        for (bool more = tree_first<T>(a, aux, s); more; more = tree_next<T>(a, s)) {
-            if (!tree_softmax_segment<T>(wg, a, s, aux, tmem, wc, J0, kq)) break;
-            J0 += s.n;
+        SpanSeg s;
+        for (bool more = span_first<T, MODE>(a, aux, s); more; more = span_next<T, MODE>(a, s)) {
+            if (s.m == 0) continue;
+            if (!span_softmax_segment<T, MODE>(wg, a, s, aux, tmem, wc, J0, kq)) break;
+            J0 += s.m;
             ++kq;
         }
     } else if (wg == T::CORR_WG) {
         setmaxnreg_dec<T::CORR_REGS>();
         int J0 = 0, kq = 0;
-        TreeSeg s;
-        for (bool more = tree_first<T>(a, aux, s); more; more = tree_next<T>(a, s)) {
-            if (!tree_correction_segment<T>(a, s, aux, tmem, wc, J0, kq)) break;
-            J0 += s.n;
-            ++kq;
+        SpanSeg s;
+        for (bool more = span_first<T, MODE>(a, aux, s); more; more = span_next<T, MODE>(a, s)) {
+            if (MODE == kSpanTree && s.tile >= a.tiles) continue;   // a group's spare CTA
+            if (!span_correction_segment<T, MODE>(a, s, aux, tmem, wc, J0, kq)) break;
+            J0 += s.m;
+            kq += s.m > 0;
         }
     } else {
         setmaxnreg_dec<T::OTHER_REGS>();
         if (warp == T::MMA_WARP)
-            tree_mma_role<T>(a, aux, tmem, sQ, sRing, wc);
+            span_mma_role<T, MODE>(a, aux, tmem, sQ, sRing, wc);
         else if (warp == T::LOAD_WARP)
-            tree_load_role<T, PAGED>(&tm_q, &tm_k, &tm_v, a, aux, sQ, sRing, wc);
+            span_load_role<T, MODE, BOXED>(&tm_q, &tm_k, &tm_v, a, aux, sQ, sRing, wc);
     }
     tc_fence_before();
     __syncthreads();
@@ -750,41 +906,36 @@ __global__ void __launch_bounds__(TreeTraits<D>::THREADS, 1)
 }
 
 // Merges the pieces of the unit that starts in CTA blockIdx.x of the split
-// kernel and goes on in the next ones (16 columns per CTA here, thread = row),
-// and writes the rows of sequences without keys.
-template <int D>
-__global__ void __launch_bounds__(128) tree_combine_kernel(const TreeArgs a) {
-    using T = TreeTraits<D>;
+// kernel and goes on in the next ones of its place in the groups (16 columns
+// per CTA here, thread = row).
+template <int D, int MODE>
+__global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
+    using T = SpanTraits<D>;
     dependents_may_start();
     wait_for_previous();
     const int r = threadIdx.x, c16 = blockIdx.y, G = gridDim.x;
-    for (int b = blockIdx.x; b < a.B; b += G) {
-        const int nodes = tree_count(a, b);
-        if (nodes == 0 || tree_keys(a, b) > 0) continue;
-        for (long long i = r; i < (long long)a.Hkv * a.rows; i += T::BM) {
-            if (i % a.T >= nodes) continue;
-            const size_t at = (size_t)b * a.Hkv * a.rows + i;
-            uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + c16 * 16);
-            dst[0] = dst[1] = make_uint4(0, 0, 0, 0);
-            float l = 0.f, m = -INFINITY;
-            tree_normaliser(a.sinks, (int)(i / a.T), l, m);
-            if (c16 == 0) a.lse[at] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
-        }
-    }
+    const int step = MODE == kSpanTree ? a.group_ctas : 1;
     int slot = 2 * blockIdx.x;
     int4 hd = a.head[slot];
     if (!(hd.z > 0 && hd.w > hd.z)) hd = a.head[++slot];
     if (!(hd.z > 0 && hd.w > hd.z)) return;
     const int b = hd.x, u = hd.y, nb = hd.w;
-    if ((unsigned)b >= (unsigned)a.B || (unsigned)u >= (unsigned)a.units) return;
-    const int row = (u % a.tiles) * T::BM + r;
-    if (row >= a.rows || row % a.T >= tree_count(a, b)) return;
+    if ((unsigned)b >= (unsigned)a.B) return;
+    const SpanSeq seq = span_seq<MODE>(a, b);
+    if ((unsigned)u >= (unsigned)span_units<MODE>(a, seq)) return;
+    const int tiles = MODE == kSpanTree ? a.tile_groups : (seq.cap + a.P - 1) / a.P;
+    const int tile = MODE == kSpanTree
+                         ? u % tiles * a.group_ctas + (int)blockIdx.x % a.group_ctas
+                         : u % tiles;
+    int h, pos;
+    size_t o_row, lse_at;
+    if (!span_row<T, MODE>(a, seq, b, u / tiles, tile, r, h, pos, o_row, lse_at)) return;
     float M = -INFINITY, L = 0.f;
     float acc[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
     int x = blockIdx.x;
-    for (int done = 0; done < nb && x < G; ++x) {
+    for (int done = 0; done < nb && x < G; x += step) {
         if (x > (int)blockIdx.x) slot = 2 * x;   // it goes on as the next CTA's first segment
         const int n = a.head[slot].z;
         if (n <= 0) break;
@@ -809,39 +960,45 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(const TreeArgs a) {
             acc[4 * q + 3] = fmaf(acc[4 * q + 3], sc, wk * v[q].w);
         }
     }
-    const int hk = u / a.tiles;
-    const float inv_l = tree_normaliser(a.sinks, hk * a.group + row / a.T, L, M);
-    const size_t at = ((size_t)b * a.Hkv + hk) * a.rows + row;
-    uint4* dst = reinterpret_cast<uint4*>(a.o + at * D + c16 * 16);
+    const float inv_l = span_normaliser(a.sinks, h, L, M);
+    uint4* dst = reinterpret_cast<uint4*>(a.o + o_row * D + c16 * 16);
 #pragma unroll
     for (int g = 0; g < 2; ++g)
         dst[g] = make_uint4(pack_bf16x2(acc[8 * g + 0] * inv_l, acc[8 * g + 1] * inv_l),
                             pack_bf16x2(acc[8 * g + 2] * inv_l, acc[8 * g + 3] * inv_l),
                             pack_bf16x2(acc[8 * g + 4] * inv_l, acc[8 * g + 5] * inv_l),
                             pack_bf16x2(acc[8 * g + 6] * inv_l, acc[8 * g + 7] * inv_l));
-    if (c16 == 0) a.lse[at] = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
+    if (c16 == 0) a.lse[lse_at] = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
+}
+
+template <int D, int MODE, bool BOXED>
+cudaError_t launch_span_mode(const SpanLaunch& p, cudaStream_t s) {
+    using T = SpanTraits<D>;
+    cudaError_t e = cudaFuncSetAttribute(span_kernel<D, MODE, BOXED>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         T::SMEM_TOTAL);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(span_kernel<D, MODE, BOXED>, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL,
+                         s, p.tm_q, p.tm_k, p.tm_v, p.args);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(span_combine_kernel<D, MODE>, dim3(p.ctas, D / 16), dim3(T::BM), 0, s,
+                            p.args);
 }
 
 template <int D>
-cudaError_t launch_tree_impl(const TreeLaunch& p, cudaStream_t s) {
-    using T = TreeTraits<D>;
-    const auto kern = p.args.block_table != nullptr ? tree_kernel<D, true> : tree_kernel<D, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         T::SMEM_TOTAL);
-    if (e != cudaSuccess) return e;
-    e = launch_dependent(kern, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL, s, p.tm_q, p.tm_k,
-                         p.tm_v, p.args);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(tree_combine_kernel<D>, dim3(p.ctas, D / 16), dim3(T::BM), 0, s, p.args);
+cudaError_t launch_span_impl(const SpanLaunch& p, cudaStream_t s) {
+    if (p.args.tree_mask == nullptr) return launch_span_mode<D, kSpanWindow, true>(p, s);
+    return p.args.box > 0 ? launch_span_mode<D, kSpanTree, true>(p, s)
+                          : launch_span_mode<D, kSpanTree, false>(p, s);
 }
 
 }  // namespace
 
-cudaError_t launch_tree(const TreeLaunch& p, int head_dim, cudaStream_t s) {
+cudaError_t launch_span(const SpanLaunch& p, int head_dim, cudaStream_t s) {
     switch (head_dim) {
-        case 64: return launch_tree_impl<64>(p, s);
-        case 128: return launch_tree_impl<128>(p, s);
-        case 256: return launch_tree_impl<256>(p, s);
+        case 64: return launch_span_impl<64>(p, s);
+        case 128: return launch_span_impl<128>(p, s);
+        case 256: return launch_span_impl<256>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }
