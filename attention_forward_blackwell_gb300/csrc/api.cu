@@ -254,9 +254,8 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
     const unsigned long long row_bytes = (unsigned long long)head_dim * 2;
     const int group = hq / hkv;
     const bool packed_k = vl && !block_table;
-    // boxes: a page's rows, or 64 on either side of a window's gap; a tree over
-    // contiguous keys copies whole blocks
-    a.box = block_table ? span_box(head_dim, page_size, tree ? 128 : 64) : (tree ? 0 : 64);
+    // boxes: a page's rows, or 64 on either side of a window's gap
+    a.box = block_table ? span_box(head_dim, page_size, tree ? 128 : 64) : 64;
     const long long planes = block_table ? (long long)num_pages * hkv
                              : packed_k  ? hkv
                                          : (long long)batch * hkv;
@@ -272,7 +271,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         a.tile_groups = (a.tiles + 7) / 8;
         a.group_ctas = (a.tiles + a.tile_groups - 1) / a.tile_groups;
         a.q_bytes = 128 * head_dim * 2;
-        if (!encode_map_strided(&p.tm_q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
+        if (!encode_map_strided(&p.maps.q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
                                 row_bytes * rows))
             return FA_ERR_INVALID_ARG;
     } else {
@@ -281,21 +280,24 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
         a.group_ctas = 1;
         a.q_bytes = a.P * group * head_dim * 2;
-        if (!(vl ? encode_map_strided(&p.tm_q, q, head_dim, vl->total_q, hq, row_bytes * hq,
+        if (!(vl ? encode_map_strided(&p.maps.q, q, head_dim, vl->total_q, hq, row_bytes * hq,
                                       row_bytes, a.P, group)
-                 : encode_map_strided(&p.tm_q, q, head_dim, sq, (long long)batch * hq, row_bytes,
+                 : encode_map_strided(&p.maps.q, q, head_dim, sq, (long long)batch * hq, row_bytes,
                                       row_bytes * sq, a.P, group)))
             return FA_ERR_INVALID_ARG;
     }
-    const unsigned k_rows = a.box ? a.box : span_block_keys(head_dim);
-    const unsigned v_rows = a.box ? a.box : span_slot_keys(head_dim);
     const long long key_rows = block_table ? page_size : packed_k ? vl->total_k : sk;
     const unsigned long long row_stride = packed_k ? row_bytes * hkv : row_bytes;
     const unsigned long long plane_stride = packed_k ? row_bytes : row_bytes * key_rows;
-    if (!encode_map_strided(&p.tm_k, k, head_dim, key_rows, planes, row_stride, plane_stride,
-                            k_rows) ||
-        !encode_map_strided(&p.tm_v, v, head_dim, key_rows, planes, row_stride, plane_stride,
-                            v_rows))
+    auto key_map = [&](CUtensorMap* m, const void* base, int rows) {
+        return encode_map_strided(m, base, head_dim, key_rows, planes, row_stride, plane_stride,
+                                  rows);
+    };
+    // (a tree over contiguous keys has no gap: no boxes)
+    if (!(block_table || (key_map(&p.maps.k, k, span_block_keys(head_dim)) &&
+                          key_map(&p.maps.v, v, span_slot_keys(head_dim)))) ||
+        !((tree && !block_table) ||
+          (key_map(&p.maps.k_box, k, a.box) && key_map(&p.maps.v_box, v, a.box))))
         return FA_ERR_INVALID_ARG;
     a.o = static_cast<uint16_t*>(o);
     a.lse = lse;
@@ -338,6 +340,8 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
     a.scale_log2 = scale * 1.4426950408889634f;
     a.err_word = di.err_word;
     a.wait_limit_ns = kWaitLimitNs;
+    a.trace = g_trace_buf;
+    a.trace_block = g_trace_block;
     // one CTA per SM, or one per key block where there are fewer (of the
     // longest the sequences can be: the host does not know their lengths), in
     // whole groups

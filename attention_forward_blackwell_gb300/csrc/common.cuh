@@ -313,7 +313,8 @@ struct SpanArgs {
     const float* sinks;         // [Hq] or nullptr
     const int* block_table;     // as in DecodeArgs
     int max_pages, page_size, num_pages;
-    int box;                    // rows of a key box (0: whole blocks and slots)
+    int box;                    // rows that lie together at least: of a page, or of one side
+                                // of a window's gap
     int planes;                 // planes of the key maps: the first that does not exist
     int B, Hq, Hkv, group, Sq, Sk;
     int q_bytes;                // bytes of a Q tile's copies
@@ -328,11 +329,17 @@ struct SpanArgs {
     float scale_log2;
     unsigned int* err_word;
     unsigned long long wait_limit_ns;
+    unsigned long long* trace;  // debug trace, as in PrefillArgs
+    int trace_block;
+};
+struct SpanMaps {
+    CUtensorMap q;              // tree {d, group * Sq, B * Hkv}, box {64, 128, 1}; window {d, Sq,
+                                // B * Hq} or {d, total_q, Hq}, box {64, P, group}
+    CUtensorMap k, v;           // contiguous keys: boxes of a block's and a V slot's rows
+    CUtensorMap k_box, v_box;   // boxes of SpanArgs::box rows
 };
 struct SpanLaunch {
-    CUtensorMap tm_q;           // tree {d, group * Sq, B * Hkv}, box {64, 128, 1}; window {d, Sq,
-                                // B * Hq} or {d, total_q, Hq}, box {64, P, group}
-    CUtensorMap tm_k, tm_v;     // boxes of `box` rows, or of a block and of a slot
+    SpanMaps maps;
     SpanArgs args;
     unsigned ctas;
 };

@@ -40,9 +40,8 @@
 // blocks are 256 keys (one N = 256 score instruction per 16 head dims), 128 at
 // head_dim 256, whose 256 O columns leave no room for more.
 //
-// Boxes (BOXED): a box of the tensor maps is as many rows as always lie
-// together -- of one page, of one side of the window's gap -- one lane of the
-// producer per box, page numbers fetched a block ahead.
+#include <type_traits>
+
 #include "prefill.cuh"
 #include "../../include/fa.h"
 
@@ -69,6 +68,8 @@ struct SpanTraits {
     static constexpr int CORR_WG = 2;
     static constexpr int MMA_WARP = 12;
     static constexpr int LOAD_WARP = 13;
+    static constexpr int ITEM_WARP = 14;
+    static constexpr int LOAD2_WARP = 15;
     static constexpr int D_COLS = D;
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t S_COL = 0;
@@ -77,7 +78,8 @@ struct SpanTraits {
     static constexpr int SMEM_Q = QTILE;
     static constexpr int SMEM_RING = NSLOT * SLOT;
     static constexpr int SMEM_AUX = 8192;
-    static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_RING + SMEM_AUX;
+    static constexpr int STAGE = 2048;              // O staging per correction warp
+    static constexpr int SMEM_TOTAL = 1024 + SMEM_Q + SMEM_RING + SMEM_AUX + 4 * STAGE;
     static constexpr uint32_t SOFTMAX_REGS = 168, CORR_REGS = 96, OTHER_REGS = 80;
     static_assert(8 * 32 * SOFTMAX_REGS + 4 * 32 * CORR_REGS + 4 * 32 * OTHER_REGS <= THREADS * 128,
                   "register split exceeds the launch allocation");
@@ -88,7 +90,29 @@ struct SpanTraits {
 
 constexpr int kSpanSlots = 6;
 
+// Wait sites of the segment queue (after those of the other kernels).
+constexpr unsigned kSiteItem = 64, kSiteItemRead = 65;
+
+// A segment of a CTA: consecutive key blocks of a unit, one tile's share of a
+// (batch entry, key/value head).
+struct SpanItem {
+    int b, u;        // batch entry, unit of it
+    int kb, n, nb;   // first block, blocks on the line (0: the CTA has no more), the unit's
+    int m;           // blocks that hold keys of the tile
+    int index;       // segments before it
+    int hk, tile;
+    int head, skip;  // position x of its axis: key x below head, key x + skip from there on
+    int span;        // positions that a row may see
+    int end;         // position of the sequence's end
+    int rows, keys;  // the sequence's (see SpanSeq)
+    int q0, k0, cap;
+};
+constexpr int kItems = 4;    // segments known ahead
+
 struct SpanAux {
+    SpanItem items[kItems];
+    uint64_t bar_item[kItems];        // segment written (scheduler)
+    uint64_t bar_item_read[kItems];   // and read by every warp that works on it
     uint64_t bar_q;
     uint64_t bar_full[kSpanSlots];
     uint64_t bar_empty[kSpanSlots];
@@ -149,110 +173,178 @@ __device__ __forceinline__ int span_blocks(const SpanArgs& a, const SpanSeq& q) 
     return max(1, (keys + T::BN - 1) / T::BN);
 }
 
-// The CTA's segments in turn: `n` consecutive key blocks from kb on of a
-// unit with nb blocks, m of them real.
-struct SpanSeg {
-    int b, u;        // batch entry, unit of it
-    int kb, n, nb;
-    int left;        // blocks of the CTA after this segment
-    int index;       // segments before it
-    SpanSeq q;
-    int units;       // of the batch entry
-    // the unit's tile (see span_geometry)
-    int hk, tile, m;
-    int head, skip;  // position x of its axis: key x below head, key x + skip from there on
-    int span;        // positions that a row may see
-    int end;         // position of the sequence's end
-};
-
-__device__ __forceinline__ int span_key(const SpanSeg& s, int x) {
+__device__ __forceinline__ int span_key(const SpanItem& s, int x) {
     return x < s.head ? x : x + s.skip;
 }
 
-// The tile of unit s.u and the axis of its keys.
+// The axis of the keys of tile s.tile.
 template <class T, int MODE>
-__device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanSeg& s) {
+__device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanItem& s) {
     s.head = s.skip = 0;
     if constexpr (MODE == kSpanTree) {
-        s.hk = s.u / a.tile_groups;
-        s.tile = (s.u % a.tile_groups) * a.group_ctas + (int)blockIdx.x % a.group_ctas;
-        s.span = s.end = s.tile < a.tiles ? s.q.keys : 0;
+        s.span = s.end = s.tile < a.tiles ? s.keys : 0;
     } else {
-        const int tiles = (s.q.cap + a.P - 1) / a.P;
-        s.hk = s.u / tiles;
-        s.tile = s.u % tiles;
-        const int off = s.q.keys - s.q.rows;   // bottom-right alignment
+        const int off = s.keys - s.rows;       // bottom-right alignment
         const int p0 = s.tile * a.P + off;     // keys of the tile's first and last row
-        const int p1 = min(s.tile * a.P + a.P, s.q.cap) - 1 + off;
-        const int last = a.causal ? min(s.q.keys - 1, p1) : s.q.keys - 1;
-        const int base = max(0, p0 - a.window + 1) / a.box * a.box;
+        const int p1 = min(s.tile * a.P + a.P, s.cap) - 1 + off;
+        const int last = a.causal ? min(s.keys - 1, p1) : s.keys - 1;
+        const int base = max(0, p0 - a.window + 1) & -a.box;
         if (a.head_keys < base) {
             s.head = a.head_keys;
             s.skip = base - s.head;
         }
         s.span = max(0, last + 1 - s.skip);
-        s.end = s.q.keys - s.skip;
+        s.end = s.keys - s.skip;
     }
     const int real = (s.span + T::BN - 1) / T::BN;
     s.m = max(0, min(s.kb + s.n, real) - s.kb);
 }
 
+// Scheduler (one lane): walks the CTA's blocks of the line, writes its
+// segments ahead, and loads each one's Q as soon as the segment before has
+// issued its last score MMA (the producers, busy with slots, would come to it
+// later).
 template <class T, int MODE>
-__device__ __forceinline__ bool span_first(const SpanArgs& a, const SpanAux* aux, SpanSeg& s) {
-    s.left = aux->start_n;
-    if (s.left <= 0) return false;
-    s.b = aux->start_b;
-    s.q = span_seq<MODE>(a, s.b);
-    s.units = span_units<MODE>(a, s.q);
-    s.nb = span_blocks<T, MODE>(a, s.q);
-    s.u = (int)(aux->start_off / s.nb);
-    s.kb = (int)(aux->start_off % s.nb);
-    s.n = min(s.nb - s.kb, s.left);
-    s.left -= s.n;
-    s.index = 0;
-    span_geometry<T, MODE>(a, s);
-    return true;
-}
-template <class T, int MODE>
-__device__ __forceinline__ bool span_next(const SpanArgs& a, SpanSeg& s) {
-    if (s.left <= 0) return false;
-    s.kb = 0;
-    if (++s.u == s.units) {
-        s.u = 0;
-        do {
-            if (++s.b >= a.B) return false;   // (never: `left` counts blocks that are there)
-            s.q = span_seq<MODE>(a, s.b);
-            s.units = span_units<MODE>(a, s.q);
-        } while (s.units == 0);
-        s.nb = span_blocks<T, MODE>(a, s.q);
+__device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* aux, uint32_t sQ,
+                               const WaitCtx& wc) {
+    if ((threadIdx.x & 31) == 0) {
+        int left = aux->start_n, tiles = 0, step = 1, first = 0;   // tile numbers of the units
+        int kq = 0;
+        const uint32_t bar_q = smem_u32(&aux->bar_q);
+        SpanItem s{};
+        s.b = aux->start_b - 1;
+        s.hk = a.Hkv;      // (the line starts with a batch entry)
+        s.n = 1;
+#pragma unroll 1
+        for (int i = 0;; ++i) {
+            if (s.n > 0) {   // segment i
+                s.kb = 0;
+                if (left > 0) {
+                    s.tile += step;
+                    ++s.u;
+                    if (s.tile >= tiles) {
+                        s.tile = first;
+                        ++s.hk;
+                    }
+                    if (s.hk >= a.Hkv) {   // the next batch entry that has units
+                        int units;
+#pragma unroll 1
+                        do {
+                            const SpanSeq q = span_seq<MODE>(a, ++s.b);
+                            units = span_units<MODE>(a, q);
+                            s.nb = span_blocks<T, MODE>(a, q);
+                            s.rows = q.rows;
+                            s.keys = q.keys;
+                            s.q0 = q.q0;
+                            s.k0 = q.k0;
+                            s.cap = q.cap;
+                        } while (units == 0 && s.b + 1 < a.B);
+                        s.u = s.hk = 0;
+                        if constexpr (MODE == kSpanTree) {
+                            step = a.group_ctas;
+                            tiles = a.tile_groups * a.group_ctas;
+                            first = (int)blockIdx.x % a.group_ctas;
+                        } else {
+                            tiles = (s.cap + a.P - 1) / a.P;
+                        }
+                        s.tile = first;
+                        if (i == 0) {   // where on the line the CTA starts
+                            s.u = (int)(aux->start_off / s.nb);
+                            s.kb = (int)(aux->start_off - (long long)s.u * s.nb);
+                            const int per = tiles / step;
+                            s.hk = s.u / per;
+                            s.tile += (s.u - s.hk * per) * step;
+                        }
+                    }
+                }
+                s.n = max(0, min(s.nb - s.kb, left));
+                left -= s.n;
+                s.index = i;
+                span_geometry<T, MODE>(a, s);
+                const int slot = i % kItems;
+                if (i >= kItems && !mbar_wait_lane(smem_u32(&aux->bar_item_read[slot]),
+                                                   (uint32_t)((i / kItems - 1) & 1), wc,
+                                                   kErrWaitTimeout | kSiteItemRead))
+                    break;
+                aux->items[slot] = s;
+                mbar_arrive(smem_u32(&aux->bar_item[slot]));
+            }
+            // Q of segment i into L2, and of segment i - 1 into shared memory
+#pragma unroll 1
+            for (int behind = 0; behind < 2; ++behind) {
+                const SpanItem& g = aux->items[(i + kItems - behind) % kItems];
+                if (i < behind || g.n == 0 || g.m == 0 || (behind == 0 && s.n == 0)) continue;
+                int row = g.tile * T::BM;   // tree: rows of the matrix
+                int q_plane = g.b * a.Hkv + g.hk;
+                if (MODE == kSpanWindow) {   // positions x heads
+                    row = g.q0 + g.tile * a.P;
+                    q_plane = (a.cu_seqlens_q != nullptr ? 0 : g.b * a.Hq) + g.hk * a.group;
+                }
+                if (behind > 0) {
+                    if (kq > 0 && !mbar_wait_lane(smem_u32(&aux->bar_qfree), (uint32_t)((kq - 1) & 1),
+                                                  wc, kErrWaitTimeout | kSiteLoadQfree)) {
+                        s.n = 0;   // given up
+                        left = -1;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(bar_q, (uint32_t)a.q_bytes);
+                    ++kq;
+                }
+#pragma unroll 1
+                for (int q = 0; q < T::NCH; ++q) {
+                    if (behind > 0)
+                        tma_load_3d(sQ + q * T::CHUNK, &tm.q, q * 64, row, q_plane, bar_q);
+                    else
+                        tma_prefetch_l2_3d(&tm.q, q * 64, row, q_plane);
+                }
+            }
+            if (left < 0 || (i >= 1 && aux->items[(i + kItems - 1) % kItems].n == 0)) break;
+        }
+        if (kq > 0) mbar_wait_drain(bar_q, (uint32_t)((kq - 1) & 1), a.wait_limit_ns);
     }
-    s.n = min(s.nb, s.left);
-    s.left -= s.n;
-    ++s.index;
-    span_geometry<T, MODE>(a, s);
-    return true;
+    __syncwarp();
 }
 
-// Tile row r: its query head, position (node), and index among the rows of O
-// (the LSE's too, but of packed tensors); whether it is a row of the sequence.
+// Segment i, for one lane (the caller then counts it as read) or a warp.
+// False at the end, or if the wait gave up.
+__device__ __forceinline__ bool span_item_lane(SpanAux* aux, int i, const WaitCtx& wc, SpanItem& s) {
+    if (!mbar_wait_lane(smem_u32(&aux->bar_item[i % kItems]), (uint32_t)((i / kItems) & 1), wc,
+                        kErrWaitTimeout | kSiteItem))
+        return false;
+    s = aux->items[i % kItems];
+    return s.n > 0;
+}
+__device__ __forceinline__ bool span_item(SpanAux* aux, int i, const WaitCtx& wc, SpanItem& s) {
+    if (!mbar_wait(smem_u32(&aux->bar_item[i % kItems]), (uint32_t)((i / kItems) & 1), wc,
+                   kErrWaitTimeout | kSiteItem))
+        return false;
+    s = aux->items[i % kItems];
+    mbar_arrive_warp(smem_u32(&aux->bar_item_read[i % kItems]));
+    return s.n > 0;
+}
+
+// Tile row r (window: head g = r / P of the group, position gp = r % P of the
+// tile): its query head, and its index among the rows of O and in the LSE;
+// whether it is a row of the sequence.
 template <class T, int MODE>
-__device__ __forceinline__ bool span_row(const SpanArgs& a, const SpanSeq& q, int b, int hk,
-                                         int tile, int r, int& h, int& pos, size_t& o_row,
+__device__ __forceinline__ bool span_row(const SpanArgs& a, int cap, int q0, int b, int hk, int tile,
+                                         int r, int g, int gp, int& h, size_t& o_row,
                                          size_t& lse_at) {
     bool real;
+    int pos;
     if constexpr (MODE == kSpanTree) {
         const int row = tile * T::BM + r;
-        h = hk * a.group + row / a.Sq;
-        pos = row % a.Sq;
-        real = row < a.group * a.Sq && pos < q.cap;
+        h = row / a.Sq;
+        pos = row - h * a.Sq;
+        h += hk * a.group;
+        real = row < a.group * a.Sq && pos < cap;
     } else {
-        const int g = r / a.P;
         h = hk * a.group + g;
-        pos = tile * a.P + r % a.P;
-        real = g < a.group && pos < q.cap;
+        pos = tile * a.P + gp;
+        real = g < a.group && pos < cap;
         if (a.cu_seqlens_q != nullptr) {
-            o_row = (size_t)(q.q0 + pos) * a.Hq + h;
-            lse_at = (size_t)h * a.total_q + q.q0 + pos;
+            o_row = (size_t)(q0 + pos) * a.Hq + h;
+            lse_at = (size_t)h * a.total_q + q0 + pos;
             return real;
         }
     }
@@ -261,205 +353,178 @@ __device__ __forceinline__ bool span_row(const SpanArgs& a, const SpanSeq& q, in
 }
 
 // Places the CTA on the line of blocks (all threads): the sequences' blocks
-// are summed, then the one that holds the CTA's first block is found.
+// are summed, then the one that holds the CTA's first block is found.  (One
+// copy of the code for both: instructions fetched at the start of a kernel of
+// a few microseconds count.)
 template <class T, int MODE>
 __device__ void span_place(const SpanArgs& a, SpanAux* aux) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto scan = [&](long long v, long long& total) -> long long {   // exclusive, over the block
-        long long x = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) aux->scan[warp] = x;
-        __syncthreads();
-        long long before = 0;
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < T::THREADS / 32; ++w) {
-            const long long y = aux->scan[w];
-            if (w < warp) before += y;
-            total += y;
-        }
-        return before + x - v;
-    };
-    auto blocks_of = [&](int b) -> long long {   // of all of a batch entry's units
-        if (b >= a.B) return 0;
-        const SpanSeq q = span_seq<MODE>(a, b);
-        return (long long)span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
-    };
-    long long all = 0, mine = 0, total;
-    for (int b = threadIdx.x; b < a.B; b += T::THREADS) mine += blocks_of(b);
-    scan(mine, all);
     const int group_ctas = MODE == kSpanTree ? a.group_ctas : 1;
-    const int groups = (int)gridDim.x / group_ctas;
-    const long long quota = (all + groups - 1) / groups;
-    const long long beg = quota * ((int)blockIdx.x / group_ctas);
-    if (threadIdx.x == 0) aux->start_n = (int)max(0ll, min(quota, all - beg));
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B && base <= beg; b0 += T::THREADS) {
-        const int b = b0 + threadIdx.x;
-        const long long v = blocks_of(b);
-        const long long at = base + scan(v, total);
-        if (at <= beg && beg < at + v) {
-            aux->start_b = b;
-            aux->start_off = beg - at;
+    long long v = 0, at = 0, all = 0, beg = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        long long base = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < a.B; b0 += T::THREADS) {
+            const int b = b0 + threadIdx.x;
+            if (pass == 0 || a.B > T::THREADS) {
+                // blocks on the line of all of b's units, and their prefix sum
+                v = 0;
+                if (b < a.B) {
+                    const SpanSeq q = span_seq<MODE>(a, b);
+                    v = (long long)span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
+                }
+                long long x = v;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o) x += y;
+                }
+                __syncthreads();   // the sums of the step before have been read
+                if (lane == 31) aux->scan[warp] = x;
+                __syncthreads();
+                long long w = lane < T::THREADS / 32 ? aux->scan[lane] : 0;
+                long long before = lane < warp ? w : 0;
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) {
+                    w += __shfl_xor_sync(0xffffffffu, w, o);
+                    before += __shfl_xor_sync(0xffffffffu, before, o);
+                }
+                at = base + before + x - v;
+                base += w;
+            }
+            if (pass == 1 && at <= beg && beg < at + v) {
+                aux->start_b = b;
+                aux->start_off = beg - at;
+            }
         }
-        base += total;
+        if (pass == 0) {
+            all = base;
+            const int groups = (int)gridDim.x / group_ctas;
+            const long long quota = (all + groups - 1) / groups;
+            beg = quota * ((int)blockIdx.x / group_ctas);
+            if (threadIdx.x == 0) aux->start_n = (int)max(0ll, min(quota, all - beg));
+        }
     }
     __syncthreads();
 }
 
-// Producer: per segment K_0, Q, then K_{j+1} and V_j for every block j.
-template <class T, int MODE, bool BOXED>
-__device__ void span_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
-                               const CUtensorMap* tm_v, const SpanArgs& a, SpanAux* aux,
-                               uint32_t sQ, uint32_t sRing, const WaitCtx& wc) {
+// Producers: per segment K_0, then K_{j+1} and V_j for every block j, slot
+// after slot of one ring, by one piece of code.  Keys that lie together come
+// as one copy per chunk of a slot; those of pages, and of a slot on both sides
+// of a window's gap, as boxes of a.box rows, a lane per box.  With pages of 16
+// keys a block has 64 boxes, and issuing them keeps a warp busy for 5,000
+// cycles (a copy is issued by one lane at a time); paged kernels share them
+// between two warps (part 0 and 1): both walk all slots, part 0 alone counts
+// their bytes and does what else there is.
+template <class T, int MODE, bool PAGED>
+__device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, SpanAux* aux,
+                               uint32_t sRing, const WaitCtx& wc,
+                               unsigned long long* tr) {
     const int lane = threadIdx.x & 31;
-    const uint32_t bar_q = smem_u32(&aux->bar_q);
-    if (lane == 0) {
-        tma_prefetch_desc(tm_q);
-        tma_prefetch_desc(tm_k);
-        tma_prefetch_desc(tm_v);
-    }
-    int p = 0, ntail = 0, kq = 0;
+    const int box_shift = __ffs(a.box) - 1;   // (a power of two)
+    struct Box {
+        int row, plane;
+    };
+    int p = 0, ntail = 0;
     bool ok = true;
-    SpanSeg s;
-    for (bool more = span_first<T, MODE>(a, aux, s); more && ok; more = span_next<T, MODE>(a, s)) {
+    SpanItem s;
+    for (int i = 0; ok && span_item(aux, i, wc, s); ++i) {
         if (s.m == 0) continue;
         const int plane = (a.cu_seqlens_k != nullptr ? 0 : s.b * a.Hkv) + s.hk;
-        // BOXED: lane i's box of block j, positions [i box, (i + 1) box) of it:
-        // where it lies in the tensor map (past the span, or no page: a plane
-        // that does not exist, which reads as zeros)
-        const int boxes = BOXED ? T::BN / a.box : 0;
-        struct Box {
-            int row, plane;
-        };
-        auto box_of = [&](int j) -> Box {
-            const int x = (s.kb + j) * T::BN + lane * a.box;
-            Box at{0, a.planes};
-            if (lane < boxes && x < s.span) {
-                const int key = span_key(s, x);
-                if (a.block_table == nullptr) {
-                    at = Box{s.q.k0 + key, plane};
+        // lane l's box of a block, positions [l box, (l + 1) box) of it: where it
+        // lies in the tensor map (past the span, or no page: a plane that does
+        // not exist, which reads as zeros).  at_v: of block j, at_k: of j + 1
+        Box at_v{0, 0}, at_k{0, 0};
+#pragma unroll 1
+        for (int j = -2; j < s.m && ok; ++j) {
+            // page numbers are fetched a block ahead
+            Box next{0, a.planes};
+            const int xb = (s.kb + j + 2) * T::BN + (lane << box_shift);
+            if (j + 2 < s.m && lane << box_shift < T::BN && xb < s.span) {
+                const int key = span_key(s, xb);
+                if (!PAGED) {
+                    next = Box{s.k0 + key, plane};
                 } else {
                     const int page = a.block_table[(size_t)s.b * a.max_pages + key / a.page_size];
                     if ((unsigned)page < (unsigned)a.num_pages)
-                        at = Box{key % a.page_size, page * a.Hkv + s.hk};
+                        next = Box{key % a.page_size, page * a.Hkv + s.hk};
                 }
             }
-            return at;
-        };
-        auto acquire = [&](uint32_t& dst, uint32_t& full) -> bool {
-            const uint32_t slot = ring_slot<T>(p);
-            if (!mbar_wait(smem_u32(&aux->bar_empty[slot]), ring_phase<T>(p) ^ 1u, wc,
-                           kErrWaitTimeout | kSiteLoadEmpty))
-                return false;
-            dst = sRing + slot * T::SLOT;
-            full = smem_u32(&aux->bar_full[slot]);
-            return true;
-        };
-        auto load_k = [&](int j, int c, const Box& at) -> bool {
-            uint32_t dst, full;
-            if (!acquire(dst, full)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)T::SLOT);
-            if constexpr (BOXED) {
-                __syncwarp();
-                if (lane < boxes) {
-#pragma unroll
-                    for (int q = 0; q < T::KCH; ++q)
-                        tma_load_3d(dst + q * T::KCHUNK + lane * a.box * 128, tm_k,
-                                    (c * T::KCH + q) * 64, at.row, at.plane, full);
+            // slots: the K block j + 1 in KP, then the V block j in VP
+            const int end = j < 0 ? T::KP : T::KP + T::VP;
+#pragma unroll 1
+            for (int c = j + 1 < s.m ? 0 : T::KP; c < end && j >= -1; ++c) {
+                const bool is_v = c >= T::KP;
+                const int x0 = (s.kb + (is_v ? j : j + 1)) * T::BN + (is_v ? (c - T::KP) * T::VKEYS : 0);
+                const int rows = is_v ? T::VKEYS : T::BN, chunks = is_v ? T::NCH : T::KCH;
+                const int chunk_bytes = is_v ? T::VCHUNK : T::KCHUNK;
+                const int col = is_v ? 0 : c * T::KCH * 64;
+                const bool tail = is_v && s.end - x0 < rows;   // it ends past the sequence
+                const uint32_t slot = ring_slot<T>(p);
+                if (!mbar_wait(smem_u32(&aux->bar_empty[slot]), ring_phase<T>(p) ^ 1u, wc,
+                               kErrWaitTimeout | kSiteLoadEmpty)) {
+                    ok = false;
+                    break;
                 }
-            } else if (lane == 0) {
-#pragma unroll
-                for (int q = 0; q < T::KCH; ++q)
-                    tma_load_3d(dst + q * T::KCHUNK, tm_k, (c * T::KCH + q) * 64,
-                                (s.kb + j) * T::BN, plane, full);
-            }
-            __syncwarp();
-            ++p;
-            return true;
-        };
-        auto load_v = [&](int j, int hh, const Box& at) -> bool {
-            uint32_t dst, full;
-            if (!acquire(dst, full)) return false;
-            const int r0 = (s.kb + j) * T::BN + hh * T::VKEYS;   // first position of the slot
-            const int rv = s.end - r0;                           // keys of the sequence in it
-            const bool tail = rv < T::VKEYS;
-            const uint32_t bar = tail ? smem_u32(&aux->bar_tail) : full;
-            if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
-            if constexpr (BOXED) {
+                if (part == 0 && lane == 0) trace_mark(tr, kTrLoad, p >> 4, p & 15);
+                ++p;
+                if (part == 1 && tail) continue;   // (part 0 copies it all)
+                const uint32_t dst = sRing + slot * T::SLOT;
+                const uint32_t full = smem_u32(&aux->bar_full[slot]);
+                const uint32_t bar = tail ? smem_u32(&aux->bar_tail) : full;
+                if (part == 0 && lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
                 __syncwarp();
-                const int per = T::VKEYS / a.box, i = lane - hh * per;
-                if (i >= 0 && i < per) {
-#pragma unroll
+                if (PAGED || (MODE == kSpanWindow && x0 < s.head && x0 + rows > s.head)) {
+                    // lanes [l0, l1) have the slot's boxes
+                    const int l0 = (x0 % T::BN) >> box_shift, l1 = l0 + (rows >> box_shift);
+                    const int mid = PAGED && !tail ? (l0 + l1 + 1) / 2 : l1;
+                    if (part == 0 ? lane >= l0 && lane < mid : lane >= mid && lane < l1) {
+                        const Box at = is_v ? at_v : at_k;
+#pragma unroll 1
+                        for (int q = 0; q < chunks; ++q)
+                            tma_load_3d(dst + q * chunk_bytes + (((lane - l0) << box_shift) << 7),
+                                        is_v ? &tm.v_box : &tm.k_box, col + q * 64, at.row, at.plane,
+                                        bar);
+                    }
+                } else if (lane == 0) {
+                    const int row = s.k0 + span_key(s, x0);
+#pragma unroll 1
+                    for (int q = 0; q < chunks; ++q)
+                        tma_load_3d(dst + q * chunk_bytes, is_v ? &tm.v : &tm.k, col + q * 64, row,
+                                    plane, bar);
+                }
+                __syncwarp();
+                if (tail) {
+                    // rows past the sequence may hold anything, and zero times a
+                    // non-finite value would poison O: zeroed before publication
+                    if (!mbar_wait(bar, (uint32_t)(ntail & 1), wc,
+                                   kErrWaitTimeout | kSiteLoadTail)) {
+                        ok = false;
+                        break;
+                    }
+                    ++ntail;
+#pragma unroll 1
                     for (int q = 0; q < T::NCH; ++q)
-                        tma_load_3d(dst + q * T::VCHUNK + i * a.box * 128, tm_v, q * 64, at.row,
-                                    at.plane, bar);
+#pragma unroll 1
+                        for (int g = max(s.end - x0, 0) * 8 + lane; g < T::VKEYS * 8; g += 32)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             dst + q * T::VCHUNK + g * 16),
+                                         "r"(0)
+                                         : "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
+                    __syncwarp();
                 }
-            } else if (lane == 0) {
-#pragma unroll
-                for (int q = 0; q < T::NCH; ++q)
-                    tma_load_3d(dst + q * T::VCHUNK, tm_v, q * 64, r0, plane, bar);
             }
-            if (tail) {
-                // rows past the sequence may hold anything, and zero times a
-                // non-finite value would poison O: zeroed before publication
-                if (!mbar_wait(bar, (uint32_t)(ntail & 1), wc, kErrWaitTimeout | kSiteLoadTail))
-                    return false;
-                ++ntail;
-                const int z0 = rv > 0 ? rv : 0;
-#pragma unroll
-                for (int q = 0; q < T::NCH; ++q)
-                    for (int g = z0 * 8 + lane; g < T::VKEYS * 8; g += 32)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         dst + q * T::VCHUNK + g * 16),
-                                     "r"(0)
-                                     : "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
-            }
-            __syncwarp();
-            ++p;
-            return true;
-        };
-        // boxes of the block whose V is loaded next, and of the next one
-        Box at0 = box_of(0);
-        Box at1 = s.m > 1 ? box_of(1) : at0;
-        for (int c = 0; c < T::KP && ok; ++c) ok = load_k(0, c, at0);
-        if (!ok) break;
-        if (kq > 0 && !mbar_wait(smem_u32(&aux->bar_qfree), (uint32_t)((kq - 1) & 1), wc,
-                                 kErrWaitTimeout | kSiteLoadQfree))
-            break;
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar_q, (uint32_t)a.q_bytes);
-            int row = s.tile * T::BM, q_plane = s.b * a.Hkv + s.hk;   // tree: rows of the matrix
-            if (MODE == kSpanWindow) {   // positions x heads
-                row = s.q.q0 + s.tile * a.P;
-                q_plane = (a.cu_seqlens_q != nullptr ? 0 : s.b * a.Hq) + s.hk * a.group;
-            }
-#pragma unroll
-            for (int q = 0; q < T::NCH; ++q)
-                tma_load_3d(sQ + q * T::CHUNK, tm_q, q * 64, row, q_plane, bar_q);
-        }
-        __syncwarp();
-        ++kq;
-        for (int j = 0; j < s.m && ok; ++j) {
-            const Box at2 = j + 2 < s.m ? box_of(j + 2) : at1;
-            if (j + 1 < s.m)
-                for (int c = 0; c < T::KP && ok; ++c) ok = load_k(j + 1, c, at1);
-            for (int hh = 0; hh < T::VP && ok; ++hh) ok = load_v(j, hh, at0);
-            at0 = at1;
-            at1 = at2;
+            at_v = at_k;
+            at_k = next;
         }
     }
-    // every copy issued must have landed before the CTA exits
-    if (lane == 0) {
-        if (kq > 0) mbar_wait_drain(bar_q, (uint32_t)((kq - 1) & 1), a.wait_limit_ns);
+    // every copy issued must have landed before the CTA exits (part 0 counts
+    // the bytes of both)
+    if (part == 0 && lane == 0) {
         for (int q = p > T::NSLOT ? p - T::NSLOT : 0; q < p; ++q)
             mbar_wait_drain(smem_u32(&aux->bar_full[ring_slot<T>(q)]), ring_phase<T>(q),
                             a.wait_limit_ns);
@@ -470,7 +535,7 @@ __device__ void span_load_role(const CUtensorMap* tm_q, const CUtensorMap* tm_k,
 // MMA issue (one lane): S(J+1), then PV(J), as in the 256-key prefill kernel.
 template <class T, int MODE>
 __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, uint32_t sQ,
-                              uint32_t sRing, const WaitCtx& wc) {
+                              uint32_t sRing, const WaitCtx& wc, unsigned long long* tr) {
     const int lane = threadIdx.x & 31;
     if (lane != 0) {
         __syncwarp();
@@ -490,76 +555,81 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
         return true;
     };
     auto slot_desc = [&](uint32_t d0) { return d0 + (uint32_t)((ring_slot<T>(p) * T::SLOT) >> 4); };
-    auto score = [&](int J) -> bool {
-        if (J > 0) {   // the softmax has read S(J-1) out of the buffer
-            if (!mbar_wait_lane(smem_u32(&aux->bar_xm[(J - 1) & 1]), (uint32_t)(((J - 1) >> 1) & 1),
-                                wc, kErrWaitTimeout | kSiteMmaSfree))
-                return false;
-            tc_fence_after();
-        }
-        for (int c = 0; c < T::KP; ++c) {
-            if (!next_slot(kSiteMmaK)) return false;
-            const uint32_t kd = slot_desc(kd0);
-#pragma unroll
-            for (int kin = 0; kin < 4 * T::KCH; ++kin) {
-                const int kk = c * 4 * T::KCH + kin;
-                umma_ss_lo(tmem + T::S_COL, qd0 + kstep_off(kk),
-                           kd + (uint32_t)(((kin >> 2) * T::KCHUNK + (kin & 3) * 32) >> 4), idesc_s,
-                           kk > 0 ? 1u : 0u);
-            }
-            tc_commit(smem_u32(&aux->bar_empty[ring_slot<T>(p)]));
-            ++p;
-        }
-        tc_commit(smem_u32(&aux->bar_s_full));
-        return true;
-    };
     int J0 = 0, kq = 0;
     bool ok = true;
-    SpanSeg s;
-    for (bool more = span_first<T, MODE>(a, aux, s); more && ok; more = span_next<T, MODE>(a, s)) {
+    SpanItem s;
+    for (int i = 0; ok && span_item_lane(aux, i, wc, s); ++i) {
         const int n = s.m;
+        mbar_arrive(smem_u32(&aux->bar_item_read[i % kItems]));
         if (n == 0) continue;
         if (!mbar_wait_lane(smem_u32(&aux->bar_q), (uint32_t)(kq & 1), wc,
                             kErrWaitTimeout | kSiteMmaQ))
             break;
         tc_fence_after();
-        if (!score(J0)) break;
-        if (n == 1) tc_commit(smem_u32(&aux->bar_qfree));   // Q no longer read
-        for (int j = 0; j < n && ok; ++j) {
-            const int J = J0 + j;
-            if (j + 1 < n) {
-                if (!score(J + 1)) {
+#pragma unroll 1
+        for (int j = -1; j < n && ok; ++j) {
+            if (j + 1 < n) {   // S(J + 1)
+                const int J = J0 + j + 1;
+                trace_mark(tr, kTrMma, J, 0);
+                // the softmax has read S(J) out of the buffer
+                if (J > 0 &&
+                    !mbar_wait_lane(smem_u32(&aux->bar_xm[(J - 1) & 1]),
+                                    (uint32_t)(((J - 1) >> 1) & 1), wc,
+                                    kErrWaitTimeout | kSiteMmaSfree)) {
                     ok = false;
                     break;
                 }
-                if (j + 2 == n) tc_commit(smem_u32(&aux->bar_qfree));
+                tc_fence_after();
+                trace_mark(tr, kTrMma, J, 1);
+#pragma unroll 1
+                for (int c = 0; c < T::KP && ok; ++c) {
+                    if (!next_slot(kSiteMmaK)) {
+                        ok = false;
+                        break;
+                    }
+                    trace_mark(tr, kTrMma, J, 2 + c);
+                    const uint32_t kd = slot_desc(kd0), qd = qd0 + c * kstep_off(4 * T::KCH);
+#pragma unroll
+                    for (int kin = 0; kin < 4 * T::KCH; ++kin)
+                        umma_ss_lo(tmem + T::S_COL, qd + kstep_off(kin),
+                                   kd + (uint32_t)(((kin >> 2) * T::KCHUNK + (kin & 3) * 32) >> 4),
+                                   idesc_s, (c | kin) > 0 ? 1u : 0u);
+                    tc_commit(smem_u32(&aux->bar_empty[ring_slot<T>(p)]));
+                    ++p;
+                }
+                if (!ok) break;
+                tc_commit(smem_u32(&aux->bar_s_full));
+                if (j + 2 == n) tc_commit(smem_u32(&aux->bar_qfree));   // Q no longer read
             }
+            if (j < 0) continue;
+            const int J = J0 + j;   // PV(J)
             if (!mbar_wait_lane(smem_u32(&aux->bar_p_ready[J & 1]), (uint32_t)((J >> 1) & 1), wc,
                                 kErrWaitTimeout | kSiteMmaP)) {
                 ok = false;
                 break;
             }
-            tc_fence_after();
-            if (j == 0 && kq > 0) {   // the previous segment's O has been read out
-                if (!mbar_wait_lane(smem_u32(&aux->bar_odrained), (uint32_t)((kq - 1) & 1), wc,
-                                    kErrWaitTimeout | kSiteMmaOdrained)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+            trace_mark(tr, kTrMma, J, 4);
+            if (j == 0 && kq > 0 &&   // the previous segment's O has been read out
+                !mbar_wait_lane(smem_u32(&aux->bar_odrained), (uint32_t)((kq - 1) & 1), wc,
+                                kErrWaitTimeout | kSiteMmaOdrained)) {
+                ok = false;
+                break;
             }
+            tc_fence_after();
+            trace_mark(tr, kTrMma, J, 5);
+#pragma unroll 1
             for (int hh = 0; hh < T::VP; ++hh) {
                 if (!next_slot(kSiteMmaV)) {
                     ok = false;
                     break;
                 }
+                trace_mark(tr, kTrMma, J, 6 + hh);
                 const uint32_t vd = slot_desc(vd0);
+                const uint32_t pcol = tmem + T::P_COL + (uint32_t)(hh * (T::VKEYS / 2));
 #pragma unroll
                 for (int kk = 0; kk < T::VKEYS / 16; ++kk)
-                    umma_ts_lo(tmem + T::O_COL,
-                               tmem + T::P_COL + (uint32_t)((hh * (T::VKEYS / 16) + kk) * 8),
-                               vd + (uint32_t)((kk * 2048) >> 4), idesc_v,
-                               (j > 0 || hh > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts_lo(tmem + T::O_COL, pcol + kk * 8, vd + (uint32_t)((kk * 2048) >> 4),
+                               idesc_v, (j | hh | kk) > 0 ? 1u : 0u);
                 tc_commit(smem_u32(&aux->bar_empty[ring_slot<T>(p)]));
                 ++p;
             }
@@ -597,10 +667,13 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 // Softmax of one segment by warpgroup h (keys [HK h, HK h + HK) of every
 // block; thread = row); see wide_softmax_unit.
 template <class T, int MODE>
-__device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s, SpanAux* aux,
-                                     uint32_t tmem, const WaitCtx& wc, int J0, int kq) {
+__device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanItem& s, int gp, SpanAux* aux,
+                                     uint32_t tmem, const WaitCtx& wc, int J0, int kq,
+                                     unsigned long long* tr) {
     constexpr int HK = T::HK;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((warp & 3) != 0 || lane != 0) tr = nullptr;
+    const int trole = h == 0 ? kTrSoftmax0 : kTrSoftmax1;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     // what the row sees: a tree's node its mask words from position node0 on,
@@ -611,10 +684,10 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s,
     if constexpr (MODE == kSpanTree) {
         words = a.tree_mask + s.b * a.tree_stride +
                 (long long)((s.tile * T::BM + r) % a.Sq) * a.tree_words;
-        node0 = s.q.keys - s.q.rows;
+        node0 = s.keys - s.rows;
     } else {
-        const int p = s.tile * a.P + r % a.P + s.q.keys - s.q.rows;   // the row's key
-        const int last = a.causal ? min(s.q.keys - 1, p) : s.q.keys - 1;
+        const int p = s.tile * a.P + gp + s.keys - s.rows;   // the row's key
+        const int last = a.causal ? min(s.keys - 1, p) : s.keys - 1;
         fa = min(a.first, last + 1);
         lim = last - s.skip;
         lo = max(p - a.window + 1 - s.skip, s.head);
@@ -629,32 +702,42 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s,
         if (!mbar_wait(smem_u32(&aux->bar_s_full), (uint32_t)(J & 1), wc,
                        kErrWaitTimeout | kSiteSmS))
             return false;
+        trace_mark(tr, trole, J, 0);
         tc_fence_after();
+        const int x0 = (s.kb + j) * T::BN + h * HK;   // first position of the half
+        const bool masked = MODE == kSpanTree ? x0 + HK > node0   // the nodes' own keys, or past
+                                              : (x0 < lo || x0 + HK - 1 > lim) && x0 + HK > fa;
+        if (__any_sync(0xffffffffu, masked)) {
+            // a block at the border: scores that the row does not see become
+            // -inf in tensor memory, 32 at a time (a loop of a kilobyte of
+            // instructions; selects on the 128 registers below take five, which
+            // the instruction cache has no room for: %MASK%)
+#pragma unroll 1
+            for (int q = 0; q < HK / 32; ++q) {
+                const int xq = x0 + 32 * q;
+                uint32_t vis, w[32];
+                if constexpr (MODE == kSpanTree)
+                    vis = tree_bits(words, s.rows, xq - node0);
+                else
+                    vis = low_bits(fa - xq) | (low_bits(lim + 1 - xq) & ~low_bits(lo - xq));
+                const uint32_t col = lane_base + T::S_COL + h * HK + q * 32;
+                tmem_ld32(col, w);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) w[c] = ((vis >> c) & 1u) ? w[c] : 0xff800000u;
+                tmem_st32(col, w);
+            }
+            tmem_wait_st();
+        }
 #pragma unroll
         for (int q = 0; q < HK / 64; ++q)
             tmem_ld64(lane_base + T::S_COL + h * HK + q * 64,
                       *reinterpret_cast<uint32_t(*)[2][32]>(&u[2 * q][0]));
         tmem_wait_ld();
+        trace_mark(tr, trole, J, 1);
         float x[HK];
 #pragma unroll
         for (int c = 0; c < HK; ++c) x[c] = __uint_as_float(u[c >> 5][c & 31]);
-        const int x0 = (s.kb + j) * T::BN + h * HK;   // first position of the half
-        const bool masked = MODE == kSpanTree ? x0 + HK > node0   // the nodes' own keys, or past
-                                              : (x0 < lo || x0 + HK - 1 > lim) && x0 + HK > fa;
-        if (masked) {
-#pragma unroll
-            for (int q = 0; q < HK / 32; ++q) {
-                const int xq = x0 + 32 * q;
-                uint32_t vis;
-                if constexpr (MODE == kSpanTree)
-                    vis = tree_bits(words, s.q.rows, xq - node0);
-                else
-                    vis = low_bits(fa - xq) | (low_bits(lim + 1 - xq) & ~low_bits(lo - xq));
-#pragma unroll
-                for (int c = 0; c < 32; ++c)
-                    x[32 * q + c] = ((vis >> c) & 1u) ? x[32 * q + c] : -INFINITY;
-            }
-        }
         float mq[HK / 32];
 #pragma unroll
         for (int q = 0; q < HK / 32; ++q) {
@@ -665,11 +748,13 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s,
         }
         float mx_h = fmaxf(mq[0], mq[1]);
         if constexpr (HK == 128) mx_h = fmaxf(fmax3(mx_h, mq[2], mq[3]), mx_h);
+        trace_mark(tr, trole, J, 2);
         aux->xm[sb][h][r] = mx_h;
         tc_fence_before();
         mbar_arrive_warp(smem_u32(&aux->bar_xm[sb]));
         if (!mbar_wait(smem_u32(&aux->bar_xm[sb]), par, wc, kErrWaitTimeout | kSiteSmXm))
             return false;
+        trace_mark(tr, trole, J, 3);
         const float m_new = fmaxf(m_run, fmaxf(mx_h, aux->xm[sb][h ^ 1][r]) * sl2);
         float alpha = 1.f;
         if (m_new > m_run + kRescaleThreshold) {
@@ -689,6 +774,7 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s,
             const float2 pv = make_float2(ex2_approx(xv.x), ex2_approx(xv.y));
             rs[c & 3] = fadd2(rs[c & 3], pv);
             pk[c >> 5][c & 31] = pack_bf16x2(pv.x, pv.y);
+            if (c == 31) trace_mark(tr, trole, J, 4);
             if (c == 31) {   // P(J) overwrites P(J-1) once PV(J-1) has read it
                 if (J > 0) {
                     if (!mbar_wait(smem_u32(&aux->bar_pv_done[(J - 1) & 1]),
@@ -697,6 +783,7 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s,
                         return false;
                     tc_fence_after();
                 }
+                trace_mark(tr, trole, J, 5);
                 tmem_st32(pcol, pk[0]);
             }
         }
@@ -707,6 +794,7 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanSeg& s,
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive_warp(smem_u32(&aux->bar_p_ready[sb]));
+        trace_mark(tr, trole, J, 6);
     }
     // the previous segment's statistics must have been read
     if (kq > 0 && !mbar_wait(smem_u32(&aux->bar_odrained), (uint32_t)((kq - 1) & 1), wc,
@@ -732,13 +820,66 @@ __device__ __forceinline__ float span_normaliser(const float* sinks, int h, floa
     return l > 0.f ? scale / l : 0.f;
 }
 
+// Writes the calling warp's 32 rows of O (times inv_l, bf16; have false:
+// zeros) to the rows o_row of each lane's own row, 32 columns at a time through
+// the warp's 2 KB staging area: a lane writes its row's 64 bytes in 16-byte
+// granules, XOR-ed with the row against bank conflicts, and each store
+// instruction writes 64 bytes of 8 rows.
+template <class T>
+__device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs& a, bool have,
+                                             bool real, size_t o_row, float inv_l,
+                                             uint32_t stage) {
+    const int lane = threadIdx.x & 31;
+    const unsigned rows = __ballot_sync(0xffffffffu, real);
+#pragma unroll 1
+    for (int c0 = 0; c0 < T::D_COLS; c0 += 32) {
+        uint32_t v[32];
+        if (have) {
+            tmem_ld32(lane_base + T::O_COL + c0, v);
+            tmem_wait_ld();
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                pk[e] = pack_bf16x2(__uint_as_float(v[g * 8 + 2 * e]) * inv_l,
+                                    __uint_as_float(v[g * 8 + 2 * e + 1]) * inv_l);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             stage + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                         : "memory");
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            const int rr = k * 8 + (lane >> 2), g = lane & 3;
+            const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)o_row, rr);
+            uint32_t x0, x1, x2, x3;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                         : "r"(stage + rr * 64 + ((g ^ ((rr >> 1) & 3)) << 4))
+                         : "memory");
+            if ((rows >> rr) & 1u)
+                *reinterpret_cast<uint4*>(a.o + to * T::D_COLS + c0 + g * 8) =
+                    make_uint4(x0, x1, x2, x3);
+        }
+        __syncwarp();
+    }
+}
+
 // Correction of one segment (thread = row): rebases O when the running max
 // moved; at its end writes O and LSE of a whole unit, or the piece's
 // unnormalised O, max and sum.
 template <class T, int MODE>
-__device__ bool span_correction_segment(const SpanArgs& a, const SpanSeg& s, SpanAux* aux,
-                                        uint32_t tmem, const WaitCtx& wc, int J0, int kq) {
+__device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, int g, int gp, SpanAux* aux,
+                                        uint32_t tmem, uint32_t stage, const WaitCtx& wc, int J0,
+                                        int kq, unsigned long long* tr) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((warp & 3) != 0 || lane != 0) tr = nullptr;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sl2 = a.scale_log2;
@@ -785,10 +926,12 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanSeg& s, Spa
                        kErrWaitTimeout | kSiteEpiPv))
             return false;
         tc_fence_after();
+        trace_mark(tr, kTrCorr, Jl, 0);
     }
-    int head, pos;
+    int head;
     size_t o_row, lse_at;
-    const bool real = span_row<T, MODE>(a, s.q, s.b, s.hk, s.tile, r, head, pos, o_row, lse_at);
+    const bool real =
+        span_row<T, MODE>(a, s.cap, s.q0, s.b, s.hk, s.tile, r, g, gp, head, o_row, lse_at);
     if (s.n < s.nb) {   // a piece
         const int slot = 2 * (int)blockIdx.x + (s.index > 0);
         float4* po = reinterpret_cast<float4*>(a.part_o + (size_t)slot * (T::D_COLS * T::BM));
@@ -810,21 +953,20 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanSeg& s, Spa
         if (r == 0) a.head[slot] = make_int4(s.b, s.u, s.n, s.kb == 0 ? s.nb : 0);
     } else {
         const float inv_l = span_normaliser(real ? a.sinks : nullptr, head, l, m);
-        store_o_rows_direct<T>(lane_base, T::O_COL, a.o + o_row * T::D_COLS, real, s.m, inv_l, 0,
-                               T::D_COLS / 32);
+        span_store_o<T>(lane_base, a, s.m > 0, real, o_row, inv_l, stage + (warp & 3) * T::STAGE);
         if (real) a.lse[lse_at] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
     }
     if (s.m > 0) {
         tc_fence_before();
         mbar_arrive_warp(smem_u32(&aux->bar_odrained));
+        trace_mark(tr, kTrCorr, J0 + s.m - 1, 1);
     }
     return true;
 }
 
-template <int D, int MODE, bool BOXED>
+template <int D, int MODE, bool PAGED>
 __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
-    span_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const SpanArgs a) {
+    span_kernel(const __grid_constant__ SpanMaps tm, const SpanArgs a) {
     using T = SpanTraits<D>;
     static_assert(sizeof(SpanAux) <= T::SMEM_AUX && T::NSLOT <= kSpanSlots, "auxiliary block");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -837,6 +979,10 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
     dependents_may_start();
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&aux->bar_q), 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(smem_u32(&aux->bar_item[i]), 1);
+            mbar_init(smem_u32(&aux->bar_item_read[i]), PAGED ? 15 : 14);   // warps that read it
+        }
         for (int i = 0; i < T::NSLOT; ++i) {
             mbar_init(smem_u32(&aux->bar_full[i]), 1);
             mbar_init(smem_u32(&aux->bar_empty[i]), 1);
@@ -870,32 +1016,40 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = aux->tmem_base;
     const WaitCtx wc{smem_u32(&aux->abort_flag), (uint32_t)a.wait_limit_ns, a.err_word};
+    unsigned long long* tr =
+        FA_PREFILL_TRACE && a.trace != nullptr && (int)blockIdx.x == a.trace_block ? a.trace : nullptr;
     if (wg < 2) {
         setmaxnreg_inc<T::SOFTMAX_REGS>();
         int J0 = 0, kq = 0;
-        SpanSeg s;
-        for (bool more = span_first<T, MODE>(a, aux, s); more; more = span_next<T, MODE>(a, s)) {
+        const int gp = MODE == kSpanWindow ? (int)(threadIdx.x & 127) % a.P : 0;
+        SpanItem s;
+        for (int i = 0; span_item(aux, i, wc, s); ++i) {
             if (s.m == 0) continue;
-            if (!span_softmax_segment<T, MODE>(wg, a, s, aux, tmem, wc, J0, kq)) break;
+            if (!span_softmax_segment<T, MODE>(wg, a, s, gp, aux, tmem, wc, J0, kq, tr)) break;
             J0 += s.m;
             ++kq;
         }
     } else if (wg == T::CORR_WG) {
         setmaxnreg_dec<T::CORR_REGS>();
         int J0 = 0, kq = 0;
-        SpanSeg s;
-        for (bool more = span_first<T, MODE>(a, aux, s); more; more = span_next<T, MODE>(a, s)) {
+        const int g = MODE == kSpanWindow ? (int)(threadIdx.x & 127) / a.P : 0;
+        const int gp = MODE == kSpanWindow ? (int)(threadIdx.x & 127) % a.P : 0;
+        SpanItem s;
+        for (int i = 0; span_item(aux, i, wc, s); ++i) {
             if (MODE == kSpanTree && s.tile >= a.tiles) continue;   // a group's spare CTA
-            if (!span_correction_segment<T, MODE>(a, s, aux, tmem, wc, J0, kq)) break;
+            if (!span_correction_segment<T, MODE>(a, s, g, gp, aux, tmem,
+                                                  sRing + T::SMEM_RING + T::SMEM_AUX, wc, J0, kq, tr)) break;
             J0 += s.m;
             kq += s.m > 0;
         }
     } else {
         setmaxnreg_dec<T::OTHER_REGS>();
         if (warp == T::MMA_WARP)
-            span_mma_role<T, MODE>(a, aux, tmem, sQ, sRing, wc);
-        else if (warp == T::LOAD_WARP)
-            span_load_role<T, MODE, BOXED>(&tm_q, &tm_k, &tm_v, a, aux, sQ, sRing, wc);
+            span_mma_role<T, MODE>(a, aux, tmem, sQ, sRing, wc, tr);
+        else if (warp == T::ITEM_WARP)
+            span_item_role<T, MODE>(tm, a, aux, sQ, wc);
+        else if (warp == T::LOAD_WARP || (PAGED && warp == T::LOAD2_WARP))
+            span_load_role<T, MODE, PAGED>(warp == T::LOAD_WARP ? 0 : 1, tm, a, aux, sRing, wc, tr);
     }
     tc_fence_before();
     __syncthreads();
@@ -927,9 +1081,11 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     const int tile = MODE == kSpanTree
                          ? u % tiles * a.group_ctas + (int)blockIdx.x % a.group_ctas
                          : u % tiles;
-    int h, pos;
+    int h;
     size_t o_row, lse_at;
-    if (!span_row<T, MODE>(a, seq, b, u / tiles, tile, r, h, pos, o_row, lse_at)) return;
+    const int g = MODE == kSpanWindow ? r / a.P : 0, gp = MODE == kSpanWindow ? r % a.P : 0;
+    if (!span_row<T, MODE>(a, seq.cap, seq.q0, b, u / tiles, tile, r, g, gp, h, o_row, lse_at))
+        return;
     float M = -INFINITY, L = 0.f;
     float acc[16];
 #pragma unroll
@@ -971,15 +1127,15 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     if (c16 == 0) a.lse[lse_at] = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
 }
 
-template <int D, int MODE, bool BOXED>
+template <int D, int MODE, bool PAGED>
 cudaError_t launch_span_mode(const SpanLaunch& p, cudaStream_t s) {
     using T = SpanTraits<D>;
-    cudaError_t e = cudaFuncSetAttribute(span_kernel<D, MODE, BOXED>,
+    cudaError_t e = cudaFuncSetAttribute(span_kernel<D, MODE, PAGED>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          T::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(span_kernel<D, MODE, BOXED>, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL,
-                         s, p.tm_q, p.tm_k, p.tm_v, p.args);
+    e = launch_dependent(span_kernel<D, MODE, PAGED>, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL,
+                         s, p.maps, p.args);
     if (e != cudaSuccess) return e;
     return launch_dependent(span_combine_kernel<D, MODE>, dim3(p.ctas, D / 16), dim3(T::BM), 0, s,
                             p.args);
@@ -987,9 +1143,12 @@ cudaError_t launch_span_mode(const SpanLaunch& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_span_impl(const SpanLaunch& p, cudaStream_t s) {
-    if (p.args.tree_mask == nullptr) return launch_span_mode<D, kSpanWindow, true>(p, s);
-    return p.args.box > 0 ? launch_span_mode<D, kSpanTree, true>(p, s)
-                          : launch_span_mode<D, kSpanTree, false>(p, s);
+    const bool paged = p.args.block_table != nullptr;
+    if (p.args.tree_mask == nullptr)
+        return paged ? launch_span_mode<D, kSpanWindow, true>(p, s)
+                     : launch_span_mode<D, kSpanWindow, false>(p, s);
+    return paged ? launch_span_mode<D, kSpanTree, true>(p, s)
+                 : launch_span_mode<D, kSpanTree, false>(p, s);
 }
 
 }  // namespace
