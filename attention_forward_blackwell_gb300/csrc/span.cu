@@ -581,7 +581,7 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
                 }
                 tc_fence_after();
                 trace_mark(tr, kTrMma, J, 1);
-#pragma unroll 1
+#pragma unroll
                 for (int c = 0; c < T::KP && ok; ++c) {
                     if (!next_slot(kSiteMmaK)) {
                         ok = false;
@@ -617,7 +617,7 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
             }
             tc_fence_after();
             trace_mark(tr, kTrMma, J, 5);
-#pragma unroll 1
+#pragma unroll
             for (int hh = 0; hh < T::VP; ++hh) {
                 if (!next_slot(kSiteMmaV)) {
                     ok = false;
