@@ -354,7 +354,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
     const size_t bytes_o = slots * 128 * head_dim * sizeof(float);
     const size_t bytes_ml = slots * 2 * 128 * sizeof(float);
     char* ws = nullptr;
-    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes_o + bytes_ml + slots * sizeof(int4),
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes_o + bytes_ml + (slots + 1) * sizeof(int4),
                         s) != cudaSuccess)
         return FA_ERR_CUDA;
     a.part_o = reinterpret_cast<float*>(ws);

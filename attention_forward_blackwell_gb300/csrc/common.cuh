@@ -325,7 +325,8 @@ struct SpanArgs {
     float* part_o;              // [2 CTAs][d / 4][128][4] unnormalised O of pieces
     float* part_ml;             // [2 CTAs][2][128] their row max (log2 units) and sum
     int4* head;                 // [2 CTAs] batch entry, unit, key blocks, and the unit's
-                                // key blocks if the piece is its first (else 0)
+                                // key blocks if the piece is its first (else 0); then one more:
+                                // the key blocks of a CTA
     float scale_log2;
     unsigned int* err_word;
     unsigned long long wait_limit_ns;

@@ -40,6 +40,7 @@
 // blocks are 256 keys (one N = 256 score instruction per 16 head dims), 128 at
 // head_dim 256, whose 256 O columns leave no room for more.
 //
+#include <climits>
 #include <type_traits>
 
 #include "prefill.cuh"
@@ -123,14 +124,11 @@ struct SpanAux {
     uint64_t bar_fin;
     uint64_t bar_qfree;
     uint64_t bar_odrained;
-    uint64_t bar_tail;
     uint64_t bar_drain;
     uint32_t tmem_base;
     int abort_flag;
-    int start_b;              // the CTA's first unit: batch entry,
-    int start_n;              // (the CTA's blocks in all)
-    long long start_off;      // and blocks of that entry's units before its own
-    long long scan[16];
+    int start_b;              // the CTA's first block: its batch entry,
+    long long start_off;      // and blocks of that entry's units before it
     float xm[2][2][128];      // [J & 1][half][row] block maxima
     float mb_l[2][128];       // [half][row] row sums of a segment
 };
@@ -200,6 +198,51 @@ __device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanItem& s) {
     s.m = max(0, min(s.kb + s.n, real) - s.kb);
 }
 
+// Places the CTA on the line of blocks (the scheduler's warp): each lane sums
+// the blocks of its share of the batch, and the lane whose share holds the
+// CTA's first block finds it there.  Writes start_b and start_off, returns the
+// CTA's blocks.
+template <class T, int MODE>
+__device__ int span_place(const SpanArgs& a, SpanAux* aux) {
+    const int lane = threadIdx.x & 31;
+    auto blocks_of = [&](int b) -> long long {   // of all of a batch entry's units
+        const SpanSeq q = span_seq<MODE>(a, b);
+        return (long long)span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
+    };
+    const int per = (a.B + 31) / 32;
+    const int b0 = lane * per, b1 = min(b0 + per, a.B);
+    long long mine = 0;
+#pragma unroll 4
+    for (int b = b0; b < b1; ++b) mine += blocks_of(b);
+    long long at = mine;   // (inclusive prefix sum over the lanes)
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += y;
+    }
+    const long long all = __shfl_sync(0xffffffffu, at, 31);
+    at -= mine;
+    const int group_ctas = MODE == kSpanTree ? a.group_ctas : 1;
+    const int groups = (int)gridDim.x / group_ctas;
+    const long long up = all + groups - 1;
+    const long long quota = up <= 0xffffffffll ? (long long)((unsigned)up / (unsigned)groups) : up / groups;
+    const long long beg = quota * ((int)blockIdx.x / group_ctas);
+    if (blockIdx.x == 0 && lane == 0)   // (for the combine kernel)
+        a.head[2 * gridDim.x] = make_int4((int)min(quota, (long long)INT_MAX), 0, 0, 0);
+    if (at <= beg && beg < at + mine) {
+        int b = b0;
+        for (;; ++b) {
+            const long long v = blocks_of(b);
+            if (beg < at + v) break;
+            at += v;
+        }
+        aux->start_b = b;
+        aux->start_off = beg - at;
+    }
+    __syncwarp();
+    return (int)max(0ll, min(quota, all - beg));
+}
+
 // Scheduler (one lane): walks the CTA's blocks of the line, writes its
 // segments ahead, and loads each one's Q as soon as the segment before has
 // issued its last score MMA (the producers, busy with slots, would come to it
@@ -207,8 +250,9 @@ __device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanItem& s) {
 template <class T, int MODE>
 __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* aux, uint32_t sQ,
                                const WaitCtx& wc) {
+    int left = span_place<T, MODE>(a, aux);
     if ((threadIdx.x & 31) == 0) {
-        int left = aux->start_n, tiles = 0, step = 1, first = 0;   // tile numbers of the units
+        int tiles = 0, step = 1, first = 0;   // tile numbers of the units
         int kq = 0;
         const uint32_t bar_q = smem_u32(&aux->bar_q);
         SpanItem s{};
@@ -249,8 +293,10 @@ __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* a
                         }
                         s.tile = first;
                         if (i == 0) {   // where on the line the CTA starts
-                            s.u = (int)(aux->start_off / s.nb);
-                            s.kb = (int)(aux->start_off - (long long)s.u * s.nb);
+                            const long long off = aux->start_off;
+                            s.u = off <= 0xffffffffll ? (int)((unsigned)off / (unsigned)s.nb)
+                                                      : (int)(off / s.nb);
+                            s.kb = (int)(off - (long long)s.u * s.nb);
                             const int per = tiles / step;
                             s.hk = s.u / per;
                             s.tile += (s.u - s.hk * per) * step;
@@ -352,63 +398,6 @@ __device__ __forceinline__ bool span_row(const SpanArgs& a, int cap, int q0, int
     return real;
 }
 
-// Places the CTA on the line of blocks (all threads): the sequences' blocks
-// are summed, then the one that holds the CTA's first block is found.  (One
-// copy of the code for both: instructions fetched at the start of a kernel of
-// a few microseconds count.)
-template <class T, int MODE>
-__device__ void span_place(const SpanArgs& a, SpanAux* aux) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int group_ctas = MODE == kSpanTree ? a.group_ctas : 1;
-    long long v = 0, at = 0, all = 0, beg = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        long long base = 0;
-#pragma unroll 1
-        for (int b0 = 0; b0 < a.B; b0 += T::THREADS) {
-            const int b = b0 + threadIdx.x;
-            if (pass == 0 || a.B > T::THREADS) {
-                // blocks on the line of all of b's units, and their prefix sum
-                v = 0;
-                if (b < a.B) {
-                    const SpanSeq q = span_seq<MODE>(a, b);
-                    v = (long long)span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
-                }
-                long long x = v;
-#pragma unroll 1
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-                    if (lane >= o) x += y;
-                }
-                __syncthreads();   // the sums of the step before have been read
-                if (lane == 31) aux->scan[warp] = x;
-                __syncthreads();
-                long long w = lane < T::THREADS / 32 ? aux->scan[lane] : 0;
-                long long before = lane < warp ? w : 0;
-#pragma unroll 1
-                for (int o = 16; o > 0; o >>= 1) {
-                    w += __shfl_xor_sync(0xffffffffu, w, o);
-                    before += __shfl_xor_sync(0xffffffffu, before, o);
-                }
-                at = base + before + x - v;
-                base += w;
-            }
-            if (pass == 1 && at <= beg && beg < at + v) {
-                aux->start_b = b;
-                aux->start_off = beg - at;
-            }
-        }
-        if (pass == 0) {
-            all = base;
-            const int groups = (int)gridDim.x / group_ctas;
-            const long long quota = (all + groups - 1) / groups;
-            beg = quota * ((int)blockIdx.x / group_ctas);
-            if (threadIdx.x == 0) aux->start_n = (int)max(0ll, min(quota, all - beg));
-        }
-    }
-    __syncthreads();
-}
-
 // Producers: per segment K_0, then K_{j+1} and V_j for every block j, slot
 // after slot of one ring, by one piece of code.  Keys that lie together come
 // as one copy per chunk of a slot; those of pages, and of a slot on both sides
@@ -426,7 +415,7 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
     struct Box {
         int row, plane;
     };
-    int p = 0, ntail = 0;
+    int p = 0;
     bool ok = true;
     SpanItem s;
     for (int i = 0; ok && span_item(aux, i, wc, s); ++i) {
@@ -460,7 +449,6 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                 const int rows = is_v ? T::VKEYS : T::BN, chunks = is_v ? T::NCH : T::KCH;
                 const int chunk_bytes = is_v ? T::VCHUNK : T::KCHUNK;
                 const int col = is_v ? 0 : c * T::KCH * 64;
-                const bool tail = is_v && s.end - x0 < rows;   // it ends past the sequence
                 const uint32_t slot = ring_slot<T>(p);
                 if (!mbar_wait(smem_u32(&aux->bar_empty[slot]), ring_phase<T>(p) ^ 1u, wc,
                                kErrWaitTimeout | kSiteLoadEmpty)) {
@@ -469,16 +457,14 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                 }
                 if (part == 0 && lane == 0) trace_mark(tr, kTrLoad, p >> 4, p & 15);
                 ++p;
-                if (part == 1 && tail) continue;   // (part 0 copies it all)
                 const uint32_t dst = sRing + slot * T::SLOT;
-                const uint32_t full = smem_u32(&aux->bar_full[slot]);
-                const uint32_t bar = tail ? smem_u32(&aux->bar_tail) : full;
+                const uint32_t bar = smem_u32(&aux->bar_full[slot]);
                 if (part == 0 && lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
                 __syncwarp();
                 if (PAGED || (MODE == kSpanWindow && x0 < s.head && x0 + rows > s.head)) {
                     // lanes [l0, l1) have the slot's boxes
                     const int l0 = (x0 % T::BN) >> box_shift, l1 = l0 + (rows >> box_shift);
-                    const int mid = PAGED && !tail ? (l0 + l1 + 1) / 2 : l1;
+                    const int mid = PAGED ? (l0 + l1 + 1) / 2 : l1;
                     if (part == 0 ? lane >= l0 && lane < mid : lane >= mid && lane < l1) {
                         const Box at = is_v ? at_v : at_k;
 #pragma unroll 1
@@ -495,28 +481,6 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                                     plane, bar);
                 }
                 __syncwarp();
-                if (tail) {
-                    // rows past the sequence may hold anything, and zero times a
-                    // non-finite value would poison O: zeroed before publication
-                    if (!mbar_wait(bar, (uint32_t)(ntail & 1), wc,
-                                   kErrWaitTimeout | kSiteLoadTail)) {
-                        ok = false;
-                        break;
-                    }
-                    ++ntail;
-#pragma unroll 1
-                    for (int q = 0; q < T::NCH; ++q)
-#pragma unroll 1
-                        for (int g = max(s.end - x0, 0) * 8 + lane; g < T::VKEYS * 8; g += 32)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             dst + q * T::VCHUNK + g * 16),
-                                         "r"(0)
-                                         : "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full);
-                    __syncwarp();
-                }
             }
             at_v = at_k;
             at_k = next;
@@ -876,8 +840,8 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
 // unnormalised O, max and sum.
 template <class T, int MODE>
 __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, int g, int gp, SpanAux* aux,
-                                        uint32_t tmem, uint32_t stage, const WaitCtx& wc, int J0,
-                                        int kq, unsigned long long* tr) {
+                                        uint32_t tmem, uint32_t sRing, const WaitCtx& wc, int J0,
+                                        int kq, int p_end, unsigned long long* tr) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((warp & 3) != 0 || lane != 0) tr = nullptr;
     const int r = (warp & 3) * 32 + lane;
@@ -911,6 +875,32 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, in
                 tmem_st32(lane_base + T::O_COL + c * 32, v);
             }
             tmem_wait_st();
+        }
+        // value rows past the sequence's end may hold anything, and zero times a
+        // non-finite value would poison O: zeroed here, before PV(J) is let go
+        const int x0 = (s.kb + j) * T::BN;
+        if (s.end < x0 + T::BN) {
+            bool landed = true;
+#pragma unroll 1
+            for (int hh = 0; hh < T::VP && landed; ++hh) {
+                const int z0 = max(s.end - x0 - hh * T::VKEYS, 0);
+                if (z0 >= T::VKEYS) continue;
+                // (V of a segment's last block fills its last VP slots)
+                const int pv = p_end - T::VP + hh;
+                landed = mbar_wait(smem_u32(&aux->bar_full[ring_slot<T>(pv)]), ring_phase<T>(pv), wc,
+                                   kErrWaitTimeout | kSiteLoadTail);
+                const uint32_t slot = sRing + ring_slot<T>(pv) * T::SLOT;
+#pragma unroll 1
+                for (int g = z0 * 8 + r; g < T::VKEYS * 8; g += T::BM)
+#pragma unroll 1
+                    for (int q = 0; q < T::NCH; ++q)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         slot + q * T::VCHUNK + g * 16),
+                                     "r"(0)
+                                     : "memory");
+            }
+            if (!landed) return false;
+            fence_proxy_async_smem();
         }
         tc_fence_before();
         mbar_arrive_warp(smem_u32(&aux->bar_p_ready[sb]));
@@ -953,7 +943,8 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, in
         if (r == 0) a.head[slot] = make_int4(s.b, s.u, s.n, s.kb == 0 ? s.nb : 0);
     } else {
         const float inv_l = span_normaliser(real ? a.sinks : nullptr, head, l, m);
-        span_store_o<T>(lane_base, a, s.m > 0, real, o_row, inv_l, stage + (warp & 3) * T::STAGE);
+        span_store_o<T>(lane_base, a, s.m > 0, real, o_row, inv_l, 
+                        sRing + T::SMEM_RING + T::SMEM_AUX + (warp & 3) * T::STAGE);
         if (real) a.lse[lse_at] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
     }
     if (s.m > 0) {
@@ -996,7 +987,6 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         mbar_init(smem_u32(&aux->bar_fin), 8);
         mbar_init(smem_u32(&aux->bar_qfree), 1);
         mbar_init(smem_u32(&aux->bar_odrained), 4);
-        mbar_init(smem_u32(&aux->bar_tail), 1);
         mbar_init(smem_u32(&aux->bar_drain), 1);
         aux->abort_flag = 0;
         aux->start_b = 0;
@@ -1007,15 +997,21 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         tmem_alloc(smem_u32(&aux->tmem_base), T::TMEM_COLS);
         tmem_relinquish();
     }
+    if (warp == T::LOAD_WARP && (threadIdx.x & 31) == 0) {
+        tma_prefetch_desc(&tm.q);
+        tma_prefetch_desc(PAGED ? &tm.k_box : &tm.k);
+        tma_prefetch_desc(PAGED ? &tm.v_box : &tm.v);
+    }
     wait_for_previous();   // (what is above overlaps the kernel before)
     if (threadIdx.x == 0)
         a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-    span_place<T, MODE>(a, aux);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = aux->tmem_base;
     const WaitCtx wc{smem_u32(&aux->abort_flag), (uint32_t)a.wait_limit_ns, a.err_word};
+    if (FA_PREFILL_TRACE && a.trace != nullptr && (int)blockIdx.x == a.trace_block && threadIdx.x == 0)
+        trace_mark(a.trace, kTrCorr, 250, 0);
     unsigned long long* tr =
         FA_PREFILL_TRACE && a.trace != nullptr && (int)blockIdx.x == a.trace_block ? a.trace : nullptr;
     if (wg < 2) {
@@ -1038,7 +1034,8 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         for (int i = 0; span_item(aux, i, wc, s); ++i) {
             if (MODE == kSpanTree && s.tile >= a.tiles) continue;   // a group's spare CTA
             if (!span_correction_segment<T, MODE>(a, s, g, gp, aux, tmem,
-                                                  sRing + T::SMEM_RING + T::SMEM_AUX, wc, J0, kq, tr)) break;
+                                                  sRing, wc, J0, kq, (J0 + s.m) * (T::KP + T::VP), tr))
+                break;
             J0 += s.m;
             kq += s.m > 0;
         }
@@ -1090,30 +1087,40 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     float acc[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-    int x = blockIdx.x;
-    for (int done = 0; done < nb && x < G; x += step) {
-        if (x > (int)blockIdx.x) slot = 2 * x;   // it goes on as the next CTA's first segment
-        const int n = a.head[slot].z;
-        if (n <= 0) break;
-        done += n;
-        const float* ml = a.part_ml + (size_t)slot * 2 * T::BM;
-        const float4* po = reinterpret_cast<const float4*>(a.part_o + (size_t)slot * (D * T::BM));
-        const float mk = ml[r], lk = ml[T::BM + r];
-        float4 v[4];
+    // the pieces: hd.z blocks here, then a full CTA's share each, as the first
+    // segments of the next CTAs (their number is known without reading them,
+    // so that four at a time are in flight)
+    const int quota = a.head[2 * G].x;
+    const int pieces = min(1 + (nb - hd.z + quota - 1) / max(quota, 1), (G - (int)blockIdx.x + step - 1) / step);
+    for (int k0 = 0; k0 < pieces; k0 += 4) {
+        float mk[4], lk[4];
+        float4 v[4][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = po[(size_t)(c16 * 4 + q) * T::BM + r];
-        if (mk == -INFINITY) continue;
-        const float m2 = fmaxf(M, mk);
-        const float sc = (M == -INFINITY) ? 0.f : ex2_approx(M - m2);
-        const float wk = ex2_approx(mk - m2);
-        M = m2;
-        L = fmaf(L, sc, wk * lk);
+        for (int e = 0; e < 4; ++e) {
+            const int k = min(k0 + e, pieces - 1);
+            const int at = k == 0 ? slot : 2 * ((int)blockIdx.x + k * step);
+            const float* ml = a.part_ml + (size_t)at * 2 * T::BM;
+            const float4* po = reinterpret_cast<const float4*>(a.part_o + (size_t)at * (D * T::BM));
+            mk[e] = k0 + e < pieces ? ml[r] : -INFINITY;
+            lk[e] = ml[T::BM + r];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            acc[4 * q + 0] = fmaf(acc[4 * q + 0], sc, wk * v[q].x);
-            acc[4 * q + 1] = fmaf(acc[4 * q + 1], sc, wk * v[q].y);
-            acc[4 * q + 2] = fmaf(acc[4 * q + 2], sc, wk * v[q].z);
-            acc[4 * q + 3] = fmaf(acc[4 * q + 3], sc, wk * v[q].w);
+            for (int q = 0; q < 4; ++q) v[e][q] = po[(size_t)(c16 * 4 + q) * T::BM + r];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (mk[e] == -INFINITY) continue;   // no keys, or no piece
+            const float m2 = fmaxf(M, mk[e]);
+            const float sc = (M == -INFINITY) ? 0.f : ex2_approx(M - m2);
+            const float wk = ex2_approx(mk[e] - m2);
+            M = m2;
+            L = fmaf(L, sc, wk * lk[e]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                acc[4 * q + 0] = fmaf(acc[4 * q + 0], sc, wk * v[e][q].x);
+                acc[4 * q + 1] = fmaf(acc[4 * q + 1], sc, wk * v[e][q].y);
+                acc[4 * q + 2] = fmaf(acc[4 * q + 2], sc, wk * v[e][q].z);
+                acc[4 * q + 3] = fmaf(acc[4 * q + 3], sc, wk * v[e][q].w);
+            }
         }
     }
     const float inv_l = span_normaliser(a.sinks, h, L, M);
