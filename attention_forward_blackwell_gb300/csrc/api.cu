@@ -240,9 +240,15 @@ constexpr long long kWindowSplitKeys = 100000;
 // A tree of query nodes (tree != nullptr, sq = nodes) or a window whose first
 // keys stay visible, on the tensor-core kernel (span.cu).  vl: packed queries,
 // and packed keys unless there is a block table.
-bool span_ok(int head_dim, int group, const int* block_table, int page_size) {
-    return (head_dim == 64 || head_dim == 128 || head_dim == 256) && group <= 128 &&
-           (!block_table || span_box(head_dim, page_size, 64) > 0);
+bool span_ok(int head_dim, int batch, int hq, int hkv, int sq, int sk, const int* block_table,
+             int page_size) {
+    const int group = hq / hkv;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || group > 128 ||
+        (block_table && span_box(head_dim, page_size, 64) == 0))
+        return false;
+    // (the kernel counts key blocks of all tiles in 32 bits)
+    const long long tiles = (sq + 128 / group - 1) / (128 / group) + 8;
+    return (double)batch * hkv * tiles * (sk / 128 + 1) < 2147483647.0;
 }
 fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* v, void* o,
                     float* lse, int batch, int hq, int hkv, int sq, int sk, const int* seqlens_k,
@@ -266,10 +272,12 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         const long long rows = (long long)group * sq;
         tiles = (rows + 127) / 128;
         if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-        a.tiles = (int)tiles;
-        // up to 8 tiles go side by side over the same keys
-        a.tile_groups = (a.tiles + 7) / 8;
-        a.group_ctas = (a.tiles + a.tile_groups - 1) / a.tile_groups;
+        // up to 8 tiles go side by side over the same keys, in clusters of two
+        // (a group of three stays single: a fourth CTA would idle)
+        a.tile_groups = ((int)tiles + 7) / 8;
+        a.group_ctas = ((int)tiles + a.tile_groups - 1) / a.tile_groups;
+        a.cluster = a.group_ctas == 1 || a.group_ctas == 3 ? 1 : 2;
+        if (a.cluster == 2) a.group_ctas += a.group_ctas & 1;
         a.q_bytes = 128 * head_dim * 2;
         if (!encode_map_strided(&p.maps.q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
                                 row_bytes * rows))
@@ -278,7 +286,8 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         a.P = std::min(128 / group, sq);
         tiles = (sq + a.P - 1) / a.P;
         if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-        a.group_ctas = 1;
+        // neighbouring tiles' windows overlap: clusters of two
+        a.cluster = a.group_ctas = tiles > 1 ? 2 : 1;
         a.q_bytes = a.P * group * head_dim * 2;
         if (!(vl ? encode_map_strided(&p.maps.q, q, head_dim, vl->total_q, hq, row_bytes * hq,
                                       row_bytes, a.P, group)
@@ -293,10 +302,10 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         return encode_map_strided(m, base, head_dim, key_rows, planes, row_stride, plane_stride,
                                   rows);
     };
-    // (a tree over contiguous keys has no gap: no boxes)
+    // (a single tile of a tree over contiguous keys has no use for boxes)
     if (!(block_table || (key_map(&p.maps.k, k, span_block_keys(head_dim)) &&
                           key_map(&p.maps.v, v, span_slot_keys(head_dim)))) ||
-        !((tree && !block_table) ||
+        !((tree && !block_table && a.cluster == 1) ||
           (key_map(&p.maps.k_box, k, a.box) && key_map(&p.maps.v_box, v, a.box))))
         return FA_ERR_INVALID_ARG;
     a.o = static_cast<uint16_t*>(o);
@@ -317,7 +326,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         // a causal tile's axis: the first keys, the window of its first row
         // rounded down to a box, its other rows
         a.window_keys = (int)std::min<long long>(
-            sk, (long long)a.head_keys + a.window + a.P - 1 + a.box);
+            sk, (long long)a.head_keys + a.window + a.P * a.group_ctas - 1 + a.box);
         if (causal) keys = a.window_keys;
     }
     if (vl) {
@@ -345,11 +354,12 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
     // one CTA per SM, or one per key block where there are fewer (of the
     // longest the sequences can be: the host does not know their lengths), in
     // whole groups
-    const long long units =
-        (long long)batch * hkv * (tree ? (long long)a.tile_groups : tiles);
-    const long long blocks = units * std::max<long long>(1, (keys + bn - 1) / bn);
-    const long long groups = std::max(1, di.num_sms / a.group_ctas);
-    p.ctas = (unsigned)(std::min(groups, blocks) * a.group_ctas);
+    const long long groups = tree ? a.tile_groups : (tiles + a.group_ctas - 1) / a.group_ctas;
+    const long long blocks = (long long)batch * hkv * groups * std::max<long long>(1, (keys + bn - 1) / bn);
+    if (blocks >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    const int ctas = a.cluster > 1 ? span_paired_ctas(head_dim, di.num_sms) : di.num_sms;
+    if (ctas < a.group_ctas) return FA_ERR_CUDA;
+    p.ctas = (unsigned)(std::min<long long>(ctas / a.group_ctas, blocks) * a.group_ctas);
     const size_t slots = 2ull * p.ctas;
     const size_t bytes_o = slots * 128 * head_dim * sizeof(float);
     const size_t bytes_ml = slots * 2 * 128 * sizeof(float);
@@ -400,7 +410,7 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
                             causal, 0, sinks, nullptr, 0, 0, 0, stream, nullptr);
 
     const bool windowed = window > 0 && first > 0;
-    if (sk > 0 && span_ok(head_dim, hq / hkv, block_table, page_size) &&
+    if (sk > 0 && span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size) &&
         (tree ? (hq / hkv) * sq > kTreeSplitRows
               : windowed && (long long)batch * hkv * std::min<long long>(sk, (long long)window + first) >
                                 kWindowSplitKeys))
@@ -502,7 +512,8 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
         return from_cuda(launch_fill_empty(static_cast<uint16_t*>(o), lse, rows, head_dim, sinks,
                                            hq, vl ? vl->total_q : sq, s));
     }
-    if (window > 0 && first > 0 && span_ok(head_dim, hq / hkv, block_table, page_size))
+    if (window > 0 && first > 0 &&
+        span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size))
         return span_impl(nullptr, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,
                          vl, *di, s);

@@ -27,20 +27,29 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;
 // calls it, so that completion is transitive along the stream.  Measured on
 // GB300: about 1.5 us less per kernel of a chain.
 
+// (clusters of `cluster` CTAs along x)
 template <class... P, class... A>
-inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
-                                    cudaStream_t s, A&&... args) {
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+inline cudaError_t launch_dependent_clusters(void (*kernel)(P...), unsigned cluster, dim3 grid,
+                                             dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+    cudaLaunchAttribute attrs[2] = {};
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t config{};
     config.gridDim = grid;
     config.blockDim = block;
     config.dynamicSmemBytes = smem;
     config.stream = s;
-    config.attrs = &attr;
-    config.numAttrs = 1;
+    config.attrs = attrs;
+    config.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&config, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t s, A&&... args) {
+    return launch_dependent_clusters(kernel, 1, grid, block, smem, s, static_cast<A&&>(args)...);
 }
 
 #ifdef __CUDACC__
@@ -319,9 +328,10 @@ struct SpanArgs {
     int B, Hq, Hkv, group, Sq, Sk;
     int q_bytes;                // bytes of a Q tile's copies
     int P;                      // window: positions of a tile
-    int tiles;                  // tree: tiles of a key/value head,
-    int group_ctas;             // CTAs that walk the same keys, a tile each,
-    int tile_groups;            // ceil(tiles / group_ctas)
+    int group_ctas;             // CTAs that walk the same keys, a tile each
+    int cluster;                // CTAs of a cluster (1 or 2, dividing group_ctas), which
+                                // load each key once for both
+    int tile_groups;            // tree: groups of tiles of a key/value head
     float* part_o;              // [2 CTAs][d / 4][128][4] unnormalised O of pieces
     float* part_ml;             // [2 CTAs][2][128] their row max (log2 units) and sum
     int4* head;                 // [2 CTAs] batch entry, unit, key blocks, and the unit's
@@ -345,6 +355,8 @@ struct SpanLaunch {
     unsigned ctas;
 };
 cudaError_t launch_span(const SpanLaunch& p, int head_dim, cudaStream_t s);
+// CTAs of clusters of two that the current device holds at a time.
+int span_paired_ctas(int head_dim, int num_sms);
 
 // Keys of a block and of a V slot of the span kernel.
 inline int span_block_keys(int head_dim) { return head_dim == 256 ? 128 : 256; }

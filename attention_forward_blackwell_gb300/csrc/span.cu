@@ -40,8 +40,7 @@
 // blocks are 256 keys (one N = 256 score instruction per 16 head dims), 128 at
 // head_dim 256, whose 256 O columns leave no room for more.
 //
-#include <climits>
-#include <type_traits>
+#include <atomic>
 
 #include "prefill.cuh"
 #include "../../include/fa.h"
@@ -128,7 +127,7 @@ struct SpanAux {
     uint32_t tmem_base;
     int abort_flag;
     int start_b;              // the CTA's first block: its batch entry,
-    long long start_off;      // and blocks of that entry's units before it
+    int start_off;            // and blocks of that entry's units before it
     float xm[2][2][128];      // [J & 1][half][row] block maxima
     float mb_l[2][128];       // [half][row] row sums of a segment
 };
@@ -156,13 +155,20 @@ __device__ __forceinline__ SpanSeq span_seq(const SpanArgs& a, int b) {
     q.cap = min(q.rows, a.Sq);
     return q;
 }
-// Units of a batch entry, and the key blocks each counts for on the line: a
-// bound for a window (its tiles near the start have fewer), one at least, so
-// that rows without keys are written too.
+// Units of a batch entry -- groups of group_ctas tiles of a key/value head --
+// and the key blocks each counts for on the line: a bound for a window (its
+// tiles near the start have fewer), one at least, so that rows without keys
+// are written too.
+template <int MODE>
+__device__ __forceinline__ int span_groups(const SpanArgs& a, const SpanSeq& q) {
+    if (q.cap == 0) return 0;
+    if (MODE == kSpanTree) return a.tile_groups;
+    const int rows = a.P * a.group_ctas;
+    return (int)((unsigned)(q.cap + rows - 1) / (unsigned)rows);
+}
 template <int MODE>
 __device__ __forceinline__ int span_units(const SpanArgs& a, const SpanSeq& q) {
-    if (q.cap == 0) return 0;
-    return a.Hkv * (MODE == kSpanTree ? a.tile_groups : (q.cap + a.P - 1) / a.P);
+    return a.Hkv * span_groups<MODE>(a, q);
 }
 template <class T, int MODE>
 __device__ __forceinline__ int span_blocks(const SpanArgs& a, const SpanSeq& q) {
@@ -175,16 +181,16 @@ __device__ __forceinline__ int span_key(const SpanItem& s, int x) {
     return x < s.head ? x : x + s.skip;
 }
 
-// The axis of the keys of tile s.tile.
+// The axis of the keys of the unit whose first tile is t0.
 template <class T, int MODE>
-__device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanItem& s) {
+__device__ __forceinline__ void span_geometry(const SpanArgs& a, int t0, SpanItem& s) {
     s.head = s.skip = 0;
     if constexpr (MODE == kSpanTree) {
-        s.span = s.end = s.tile < a.tiles ? s.keys : 0;
+        s.span = s.end = s.keys;
     } else {
-        const int off = s.keys - s.rows;       // bottom-right alignment
-        const int p0 = s.tile * a.P + off;     // keys of the tile's first and last row
-        const int p1 = min(s.tile * a.P + a.P, s.cap) - 1 + off;
+        const int off = s.keys - s.rows;   // bottom-right alignment
+        const int p0 = t0 * a.P + off;     // keys of the unit's first and last row
+        const int p1 = min((t0 + a.group_ctas) * a.P, s.cap) - 1 + off;
         const int last = a.causal ? min(s.keys - 1, p1) : s.keys - 1;
         const int base = max(0, p0 - a.window + 1) & -a.box;
         if (a.head_keys < base) {
@@ -198,62 +204,58 @@ __device__ __forceinline__ void span_geometry(const SpanArgs& a, SpanItem& s) {
     s.m = max(0, min(s.kb + s.n, real) - s.kb);
 }
 
-// Places the CTA on the line of blocks (the scheduler's warp): each lane sums
-// the blocks of its share of the batch, and the lane whose share holds the
-// CTA's first block finds it there.  Writes start_b and start_off, returns the
-// CTA's blocks.
-template <class T, int MODE>
-__device__ int span_place(const SpanArgs& a, SpanAux* aux) {
-    const int lane = threadIdx.x & 31;
-    auto blocks_of = [&](int b) -> long long {   // of all of a batch entry's units
-        const SpanSeq q = span_seq<MODE>(a, b);
-        return (long long)span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
-    };
-    const int per = (a.B + 31) / 32;
-    const int b0 = lane * per, b1 = min(b0 + per, a.B);
-    long long mine = 0;
-#pragma unroll 4
-    for (int b = b0; b < b1; ++b) mine += blocks_of(b);
-    long long at = mine;   // (inclusive prefix sum over the lanes)
-#pragma unroll 1
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, at, o);
-        if (lane >= o) at += y;
-    }
-    const long long all = __shfl_sync(0xffffffffu, at, 31);
-    at -= mine;
-    const int group_ctas = MODE == kSpanTree ? a.group_ctas : 1;
-    const int groups = (int)gridDim.x / group_ctas;
-    const long long up = all + groups - 1;
-    const long long quota = up <= 0xffffffffll ? (long long)((unsigned)up / (unsigned)groups) : up / groups;
-    const long long beg = quota * ((int)blockIdx.x / group_ctas);
-    if (blockIdx.x == 0 && lane == 0)   // (for the combine kernel)
-        a.head[2 * gridDim.x] = make_int4((int)min(quota, (long long)INT_MAX), 0, 0, 0);
-    if (at <= beg && beg < at + mine) {
-        int b = b0;
-        for (;; ++b) {
-            const long long v = blocks_of(b);
-            if (beg < at + v) break;
-            at += v;
-        }
-        aux->start_b = b;
-        aux->start_off = beg - at;
-    }
-    __syncwarp();
-    return (int)max(0ll, min(quota, all - beg));
-}
-
-// Scheduler (one lane): walks the CTA's blocks of the line, writes its
-// segments ahead, and loads each one's Q as soon as the segment before has
-// issued its last score MMA (the producers, busy with slots, would come to it
-// later).
+// Scheduler's warp: places the CTA on the line of blocks -- each lane sums the
+// blocks of its share of the batch, and the lane whose share holds the CTA's
+// first block finds it there -- then (one lane) walks the CTA's blocks, writes
+// its segments ahead of the roles and loads each one's Q as soon as the segment
+// before has issued its last score MMA (the producers, busy with slots, would
+// come to it later).  Numbers of blocks are below 2^31 (span_impl sees to it).
 template <class T, int MODE>
 __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* aux, uint32_t sQ,
                                const WaitCtx& wc) {
-    int left = span_place<T, MODE>(a, aux);
-    if ((threadIdx.x & 31) == 0) {
-        int tiles = 0, step = 1, first = 0;   // tile numbers of the units
-        int kq = 0;
+    const int lane = threadIdx.x & 31;
+    const int per = (a.B + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, a.B);
+    int mine = 0, at = 0, beg = 0, left = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        // pass 0: the lane's blocks; pass 1: the batch entry that holds block beg
+#pragma unroll 4
+        for (int b = b0; b < b1; ++b) {
+            const SpanSeq q = span_seq<MODE>(a, b);
+            const int v = span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
+            if (pass == 0) {
+                mine += v;
+            } else {
+                if (at <= beg && beg < at + v) {
+                    aux->start_b = b;
+                    aux->start_off = beg - at;
+                }
+                at += v;
+            }
+        }
+        if (pass == 0) {
+            at = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, at, o);
+                if (lane >= o) at += y;
+            }
+            const int all = __shfl_sync(0xffffffffu, at, 31);
+            at -= mine;
+            const unsigned groups = (unsigned)gridDim.x / (unsigned)a.group_ctas;
+            const int quota = (int)(((unsigned)all + groups - 1) / groups);
+            // (below all where the CTA has blocks; large products stay in range)
+            const long long from = (long long)quota * (int)(blockIdx.x / (unsigned)a.group_ctas);
+            beg = (int)min(from, (long long)all);
+            left = min(quota, all - beg);
+            if (blockIdx.x == 0 && lane == 0)   // (for the combine kernel)
+                a.head[2 * gridDim.x] = make_int4(quota, 0, 0, 0);
+        }
+    }
+    __syncwarp();
+    if (lane == 0) {
+        int tiles = 0, kq = 0;   // tile numbers of a key/value head's units
+        const int first = (int)(blockIdx.x % (unsigned)a.group_ctas);
         const uint32_t bar_q = smem_u32(&aux->bar_q);
         SpanItem s{};
         s.b = aux->start_b - 1;
@@ -264,49 +266,40 @@ __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* a
             if (s.n > 0) {   // segment i
                 s.kb = 0;
                 if (left > 0) {
-                    s.tile += step;
+                    s.tile += a.group_ctas;
                     ++s.u;
                     if (s.tile >= tiles) {
                         s.tile = first;
                         ++s.hk;
                     }
                     if (s.hk >= a.Hkv) {   // the next batch entry that has units
-                        int units;
+                        int groups;
 #pragma unroll 1
                         do {
                             const SpanSeq q = span_seq<MODE>(a, ++s.b);
-                            units = span_units<MODE>(a, q);
+                            groups = span_groups<MODE>(a, q);
                             s.nb = span_blocks<T, MODE>(a, q);
                             s.rows = q.rows;
                             s.keys = q.keys;
                             s.q0 = q.q0;
                             s.k0 = q.k0;
                             s.cap = q.cap;
-                        } while (units == 0 && s.b + 1 < a.B);
+                        } while (groups == 0 && s.b + 1 < a.B);
                         s.u = s.hk = 0;
-                        if constexpr (MODE == kSpanTree) {
-                            step = a.group_ctas;
-                            tiles = a.tile_groups * a.group_ctas;
-                            first = (int)blockIdx.x % a.group_ctas;
-                        } else {
-                            tiles = (s.cap + a.P - 1) / a.P;
-                        }
+                        tiles = groups * a.group_ctas;
                         s.tile = first;
                         if (i == 0) {   // where on the line the CTA starts
-                            const long long off = aux->start_off;
-                            s.u = off <= 0xffffffffll ? (int)((unsigned)off / (unsigned)s.nb)
-                                                      : (int)(off / s.nb);
-                            s.kb = (int)(off - (long long)s.u * s.nb);
-                            const int per = tiles / step;
-                            s.hk = s.u / per;
-                            s.tile += (s.u - s.hk * per) * step;
+                            s.u = (int)((unsigned)aux->start_off / (unsigned)s.nb);
+                            s.kb = aux->start_off - s.u * s.nb;
+                            s.hk = (int)((unsigned)s.u / (unsigned)groups);
+                            s.tile += (s.u - s.hk * groups) * a.group_ctas;
                         }
                     }
                 }
                 s.n = max(0, min(s.nb - s.kb, left));
                 left -= s.n;
                 s.index = i;
-                span_geometry<T, MODE>(a, s);
+                span_geometry<T, MODE>(a, s.tile - first, s);
                 const int slot = i % kItems;
                 if (i >= kItems && !mbar_wait_lane(smem_u32(&aux->bar_item_read[slot]),
                                                    (uint32_t)((i / kItems - 1) & 1), wc,
@@ -412,6 +405,7 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                                unsigned long long* tr) {
     const int lane = threadIdx.x & 31;
     const int box_shift = __ffs(a.box) - 1;   // (a power of two)
+    const int rank = (int)cluster_ctarank();
     struct Box {
         int row, plane;
     };
@@ -461,17 +455,24 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                 const uint32_t bar = smem_u32(&aux->bar_full[slot]);
                 if (part == 0 && lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
                 __syncwarp();
-                if (PAGED || (MODE == kSpanWindow && x0 < s.head && x0 + rows > s.head)) {
-                    // lanes [l0, l1) have the slot's boxes
+                if (PAGED || a.cluster > 1 ||
+                    (MODE == kSpanWindow && x0 < s.head && x0 + rows > s.head)) {
+                    // lanes [l0, l1) have the slot's boxes; of a cluster each CTA
+                    // copies every other piece, to both
                     const int l0 = (x0 % T::BN) >> box_shift, l1 = l0 + (rows >> box_shift);
                     const int mid = PAGED ? (l0 + l1 + 1) / 2 : l1;
                     if (part == 0 ? lane >= l0 && lane < mid : lane >= mid && lane < l1) {
                         const Box at = is_v ? at_v : at_k;
 #pragma unroll 1
-                        for (int q = 0; q < chunks; ++q)
-                            tma_load_3d(dst + q * chunk_bytes + (((lane - l0) << box_shift) << 7),
-                                        is_v ? &tm.v_box : &tm.k_box, col + q * 64, at.row, at.plane,
-                                        bar);
+                        for (int q = 0; q < chunks; ++q) {
+                            const uint32_t to =
+                                dst + q * chunk_bytes + (((lane - l0) << box_shift) << 7);
+                            const CUtensorMap* m = is_v ? &tm.v_box : &tm.k_box;
+                            if (a.cluster == 1)
+                                tma_load_3d(to, m, col + q * 64, at.row, at.plane, bar);
+                            else if ((((lane - l0) * chunks + q) & 1) == rank)
+                                tma_load_3d_multicast(to, m, col + q * 64, at.row, at.plane, bar, 3);
+                        }
                     }
                 } else if (lane == 0) {
                     const int row = s.k0 + span_key(s, x0);
@@ -491,6 +492,10 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
     if (part == 0 && lane == 0) {
         for (int q = p > T::NSLOT ? p - T::NSLOT : 0; q < p; ++q)
             mbar_wait_drain(smem_u32(&aux->bar_full[ring_slot<T>(q)]), ring_phase<T>(q),
+                            a.wait_limit_ns);
+        // and every arrival from the other CTA of the cluster
+        for (int q = p > T::NSLOT ? p - T::NSLOT : 0; a.cluster > 1 && q < p; ++q)
+            mbar_wait_drain(smem_u32(&aux->bar_empty[ring_slot<T>(q)]), ring_phase<T>(q),
                             a.wait_limit_ns);
     }
     __syncwarp();
@@ -519,6 +524,14 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
         return true;
     };
     auto slot_desc = [&](uint32_t d0) { return d0 + (uint32_t)((ring_slot<T>(p) * T::SLOT) >> 4); };
+    auto release_slot = [&] {   // in every CTA that fills it
+        const uint32_t bar = smem_u32(&aux->bar_empty[ring_slot<T>(p)]);
+        if (a.cluster > 1)
+            tc_commit_multicast(bar, 3);
+        else
+            tc_commit(bar);
+        ++p;
+    };
     int J0 = 0, kq = 0;
     bool ok = true;
     SpanItem s;
@@ -558,8 +571,7 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
                         umma_ss_lo(tmem + T::S_COL, qd + kstep_off(kin),
                                    kd + (uint32_t)(((kin >> 2) * T::KCHUNK + (kin & 3) * 32) >> 4),
                                    idesc_s, (c | kin) > 0 ? 1u : 0u);
-                    tc_commit(smem_u32(&aux->bar_empty[ring_slot<T>(p)]));
-                    ++p;
+                    release_slot();
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(&aux->bar_s_full));
@@ -594,8 +606,7 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
                 for (int kk = 0; kk < T::VKEYS / 16; ++kk)
                     umma_ts_lo(tmem + T::O_COL, pcol + kk * 8, vd + (uint32_t)((kk * 2048) >> 4),
                                idesc_v, (j | hh | kk) > 0 ? 1u : 0u);
-                tc_commit(smem_u32(&aux->bar_empty[ring_slot<T>(p)]));
-                ++p;
+                release_slot();
             }
             if (ok) tc_commit(smem_u32(&aux->bar_pv_done[J & 1]));
         }
@@ -795,6 +806,13 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
                                              uint32_t stage) {
     const int lane = threadIdx.x & 31;
     const unsigned rows = __ballot_sync(0xffffffffu, real);
+    uint16_t* to[4];   // the rows (and columns) that this lane stores
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        to[k] = a.o +
+                (size_t)__shfl_sync(0xffffffffu, (unsigned long long)o_row, k * 8 + (lane >> 2)) *
+                    T::D_COLS +
+                (lane & 3) * 8;
 #pragma unroll 1
     for (int c0 = 0; c0 < T::D_COLS; c0 += 32) {
         uint32_t v[32];
@@ -818,19 +836,19 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
                          : "memory");
         }
         __syncwarp();
-#pragma unroll 1
+        uint4 x[4];
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int rr = k * 8 + (lane >> 2), g = lane & 3;
-            const size_t to = __shfl_sync(0xffffffffu, (unsigned long long)o_row, rr);
-            uint32_t x0, x1, x2, x3;
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x0), "=r"(x1), "=r"(x2), "=r"(x3)
+                         : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
                          : "r"(stage + rr * 64 + ((g ^ ((rr >> 1) & 3)) << 4))
                          : "memory");
-            if ((rows >> rr) & 1u)
-                *reinterpret_cast<uint4*>(a.o + to * T::D_COLS + c0 + g * 8) =
-                    make_uint4(x0, x1, x2, x3);
         }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if ((rows >> (k * 8 + (lane >> 2))) & 1u)
+                *reinterpret_cast<uint4*>(to[k] + c0) = x[k];
         __syncwarp();
     }
 }
@@ -976,7 +994,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         }
         for (int i = 0; i < T::NSLOT; ++i) {
             mbar_init(smem_u32(&aux->bar_full[i]), 1);
-            mbar_init(smem_u32(&aux->bar_empty[i]), 1);
+            mbar_init(smem_u32(&aux->bar_empty[i]), a.cluster);
         }
         mbar_init(smem_u32(&aux->bar_s_full), 1);
         for (int i = 0; i < 2; ++i) {
@@ -1007,6 +1025,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     tc_fence_before();
     __syncthreads();
+    if (a.cluster > 1) cluster_sync_all();   // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = aux->tmem_base;
     const WaitCtx wc{smem_u32(&aux->abort_flag), (uint32_t)a.wait_limit_ns, a.err_word};
@@ -1032,7 +1051,6 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         const int gp = MODE == kSpanWindow ? (int)(threadIdx.x & 127) % a.P : 0;
         SpanItem s;
         for (int i = 0; span_item(aux, i, wc, s); ++i) {
-            if (MODE == kSpanTree && s.tile >= a.tiles) continue;   // a group's spare CTA
             if (!span_correction_segment<T, MODE>(a, s, g, gp, aux, tmem,
                                                   sRing, wc, J0, kq, (J0 + s.m) * (T::KP + T::VP), tr))
                 break;
@@ -1054,6 +1072,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, T::TMEM_COLS);
     }
+    if (a.cluster > 1) cluster_sync_all();   // none leaves while the other may write to it
 }
 
 // Merges the pieces of the unit that starts in CTA blockIdx.x of the split
@@ -1065,7 +1084,7 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     dependents_may_start();
     wait_for_previous();
     const int r = threadIdx.x, c16 = blockIdx.y, G = gridDim.x;
-    const int step = MODE == kSpanTree ? a.group_ctas : 1;
+    const int step = a.group_ctas;
     int slot = 2 * blockIdx.x;
     int4 hd = a.head[slot];
     if (!(hd.z > 0 && hd.w > hd.z)) hd = a.head[++slot];
@@ -1074,14 +1093,12 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     if ((unsigned)b >= (unsigned)a.B) return;
     const SpanSeq seq = span_seq<MODE>(a, b);
     if ((unsigned)u >= (unsigned)span_units<MODE>(a, seq)) return;
-    const int tiles = MODE == kSpanTree ? a.tile_groups : (seq.cap + a.P - 1) / a.P;
-    const int tile = MODE == kSpanTree
-                         ? u % tiles * a.group_ctas + (int)blockIdx.x % a.group_ctas
-                         : u % tiles;
+    const int groups = span_groups<MODE>(a, seq);
+    const int tile = u % groups * step + (int)blockIdx.x % step;
     int h;
     size_t o_row, lse_at;
     const int g = MODE == kSpanWindow ? r / a.P : 0, gp = MODE == kSpanWindow ? r % a.P : 0;
-    if (!span_row<T, MODE>(a, seq.cap, seq.q0, b, u / tiles, tile, r, g, gp, h, o_row, lse_at))
+    if (!span_row<T, MODE>(a, seq.cap, seq.q0, b, u / groups, tile, r, g, gp, h, o_row, lse_at))
         return;
     float M = -INFINITY, L = 0.f;
     float acc[16];
@@ -1141,8 +1158,8 @@ cudaError_t launch_span_mode(const SpanLaunch& p, cudaStream_t s) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          T::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(span_kernel<D, MODE, PAGED>, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL,
-                         s, p.maps, p.args);
+    e = launch_dependent_clusters(span_kernel<D, MODE, PAGED>, (unsigned)p.args.cluster,
+                                  dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL, s, p.maps, p.args);
     if (e != cudaSuccess) return e;
     return launch_dependent(span_combine_kernel<D, MODE>, dim3(p.ctas, D / 16), dim3(T::BM), 0, s,
                             p.args);
@@ -1158,7 +1175,46 @@ cudaError_t launch_span_impl(const SpanLaunch& p, cudaStream_t s) {
                  : launch_span_mode<D, kSpanTree, false>(p, s);
 }
 
+// (the kernels of a head dimension take the same shared memory, and all the
+// registers of an SM)
+template <int D>
+int paired_ctas(int num_sms) {
+    using T = SpanTraits<D>;
+    const auto kernel = span_kernel<D, kSpanTree, true>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_TOTAL) !=
+        cudaSuccess)
+        return 0;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(num_sms / 2 * 2);
+    config.blockDim = dim3(T::THREADS);
+    config.dynamicSmemBytes = T::SMEM_TOTAL;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &config) != cudaSuccess) return 0;
+    return clusters * 2 < num_sms ? clusters * 2 : num_sms / 2 * 2;
+}
+
 }  // namespace
+
+int span_paired_ctas(int head_dim, int num_sms) {
+    // asked once per head dimension and device
+    static std::atomic<int> known[3][64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::atomic<int>& k = known[head_dim == 64 ? 0 : (head_dim == 128 ? 1 : 2)][dev];
+    int n = k.load();
+    if (n == 0) {
+        n = head_dim == 64 ? paired_ctas<64>(num_sms)
+                           : (head_dim == 128 ? paired_ctas<128>(num_sms) : paired_ctas<256>(num_sms));
+        k.store(n);
+    }
+    return n;
+}
 
 cudaError_t launch_span(const SpanLaunch& p, int head_dim, cudaStream_t s) {
     switch (head_dim) {
