@@ -233,6 +233,8 @@ constexpr int kDecodeToPrefillRows = 32;
 
 // Query rows per kv head up to which a tree runs the split-KV kernel.
 constexpr int kTreeSplitRows = 16;
+// Keys of a window (and its first keys) from which a dense prompt does not.
+constexpr long long kWindowDenseKeys = 512;
 // Keys of all (batch entry, kv head) pairs up to which a windowed decode with
 // first keys does.
 constexpr long long kWindowSplitKeys = 100000;
@@ -286,8 +288,13 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         a.P = std::min(128 / group, sq);
         tiles = (sq + a.P - 1) / a.P;
         if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-        // neighbouring tiles' windows overlap: clusters of two
-        a.cluster = a.group_ctas = tiles > 1 ? 2 : 1;
+        // neighbouring tiles' windows overlap: clusters of two, where a pair's
+        // union of keys is not much longer than a tile's span (8 chunks of
+        // prompts over 3,600 keys, window 512: 106 -> 91 us with 8 heads per kv
+        // head, 126 -> 111 with one; window 256, one head: 60 -> 69; head_dim
+        // 64, one head: 83 -> 95)
+        const bool pair = tiles > 1 && head_dim >= 128 && 4ll * a.P <= (long long)window + first;
+        a.cluster = a.group_ctas = pair ? 2 : 1;
         a.q_bytes = a.P * group * head_dim * 2;
         if (!(vl ? encode_map_strided(&p.maps.q, q, head_dim, vl->total_q, hq, row_bytes * hq,
                                       row_bytes, a.P, group)
@@ -302,10 +309,14 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         return encode_map_strided(m, base, head_dim, key_rows, planes, row_stride, plane_stride,
                                   rows);
     };
-    // (a single tile of a tree over contiguous keys has no use for boxes)
-    if (!(block_table || (key_map(&p.maps.k, k, span_block_keys(head_dim)) &&
-                          key_map(&p.maps.v, v, span_slot_keys(head_dim)))) ||
-        !((tree && !block_table && a.cluster == 1) ||
+    // contiguous keys: a block's and a slot's rows, or a cluster CTA's half (of
+    // a V slot the half is of its chunks where it has several); a tree has no
+    // gap, so no boxes
+    const int k_rows = span_block_keys(head_dim) / a.cluster;
+    const int v_rows = span_slot_keys(head_dim) / (head_dim == 64 ? a.cluster : 1);
+    if (!(block_table || (key_map(&p.maps.k, k, k_rows) &&
+                          key_map(&p.maps.v, v, v_rows))) ||
+        !((tree && !block_table) ||
           (key_map(&p.maps.k_box, k, a.box) && key_map(&p.maps.v_box, v, a.box))))
         return FA_ERR_INVALID_ARG;
     a.o = static_cast<uint16_t*>(o);
@@ -512,7 +523,11 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
         return from_cuda(launch_fill_empty(static_cast<uint16_t*>(o), lse, rows, head_dim, sinks,
                                            hq, vl ? vl->total_q : sq, s));
     }
-    if (window > 0 && first > 0 &&
+    // (dense prompts with longer windows: the two-tile and one-tile kernels
+    // below, whose units are longer, are faster -- 2 x 16 x 4,096 rows at head_dim
+    // 128, window 1,024: 88 against 94 us, at head_dim 256 67 against 90; window
+    // 256: 68 against 60)
+    if (window > 0 && first > 0 && (vl || (long long)window + first < kWindowDenseKeys) &&
         span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size))
         return span_impl(nullptr, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,

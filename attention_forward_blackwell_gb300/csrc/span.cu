@@ -204,12 +204,24 @@ __device__ __forceinline__ void span_geometry(const SpanArgs& a, int t0, SpanIte
     s.m = max(0, min(s.kb + s.n, real) - s.kb);
 }
 
+// Where a segment's Q tile lies in its tensor map.
+template <class T, int MODE>
+__device__ __forceinline__ void span_q_at(const SpanArgs& a, const SpanItem& s, int& row,
+                                          int& plane) {
+    row = s.tile * T::BM;   // tree: rows of the matrix; window: positions x heads
+    plane = s.b * a.Hkv + s.hk;
+    if (MODE == kSpanWindow) {
+        row = s.q0 + s.tile * a.P;
+        plane = (a.cu_seqlens_q != nullptr ? 0 : s.b * a.Hq) + s.hk * a.group;
+    }
+}
+
 // Scheduler's warp: places the CTA on the line of blocks -- each lane sums the
 // blocks of its share of the batch, and the lane whose share holds the CTA's
 // first block finds it there -- then (one lane) walks the CTA's blocks, writes
 // its segments ahead of the roles and loads each one's Q as soon as the segment
 // before has issued its last score MMA (the producers, busy with slots, would
-// come to it later).  Numbers of blocks are below 2^31 (span_impl sees to it).
+// come to it later).  Numbers of blocks are below 2^31 (span_ok sees to it).
 template <class T, int MODE>
 __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* aux, uint32_t sQ,
                                const WaitCtx& wc) {
@@ -219,7 +231,7 @@ __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* a
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         // pass 0: the lane's blocks; pass 1: the batch entry that holds block beg
-#pragma unroll 4
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const SpanSeq q = span_seq<MODE>(a, b);
             const int v = span_units<MODE>(a, q) * span_blocks<T, MODE>(a, q);
@@ -308,18 +320,17 @@ __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* a
                 aux->items[slot] = s;
                 mbar_arrive(smem_u32(&aux->bar_item[slot]));
             }
-            // Q of segment i into L2, and of segment i - 1 into shared memory
+            // Q of segment i into L2, and of segment i - 1 into shared memory (the
+            // first at once)
 #pragma unroll 1
             for (int behind = 0; behind < 2; ++behind) {
                 const SpanItem& g = aux->items[(i + kItems - behind) % kItems];
-                if (i < behind || g.n == 0 || g.m == 0 || (behind == 0 && s.n == 0)) continue;
-                int row = g.tile * T::BM;   // tree: rows of the matrix
-                int q_plane = g.b * a.Hkv + g.hk;
-                if (MODE == kSpanWindow) {   // positions x heads
-                    row = g.q0 + g.tile * a.P;
-                    q_plane = (a.cu_seqlens_q != nullptr ? 0 : g.b * a.Hq) + g.hk * a.group;
-                }
-                if (behind > 0) {
+                const bool load = behind > 0 || i == 0;
+                if ((behind > 0 && i < 2) || g.n == 0 || g.m == 0 || (behind == 0 && s.n == 0))
+                    continue;
+                int row, q_plane;
+                span_q_at<T, MODE>(a, g, row, q_plane);
+                if (load) {
                     if (kq > 0 && !mbar_wait_lane(smem_u32(&aux->bar_qfree), (uint32_t)((kq - 1) & 1),
                                                   wc, kErrWaitTimeout | kSiteLoadQfree)) {
                         s.n = 0;   // given up
@@ -331,7 +342,7 @@ __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* a
                 }
 #pragma unroll 1
                 for (int q = 0; q < T::NCH; ++q) {
-                    if (behind > 0)
+                    if (load)
                         tma_load_3d(sQ + q * T::CHUNK, &tm.q, q * 64, row, q_plane, bar_q);
                     else
                         tma_prefetch_l2_3d(&tm.q, q * 64, row, q_plane);
@@ -392,111 +403,168 @@ __device__ __forceinline__ bool span_row(const SpanArgs& a, int cap, int q0, int
 }
 
 // Producers: per segment K_0, then K_{j+1} and V_j for every block j, slot
-// after slot of one ring, by one piece of code.  Keys that lie together come
-// as one copy per chunk of a slot; those of pages, and of a slot on both sides
-// of a window's gap, as boxes of a.box rows, a lane per box.  With pages of 16
-// keys a block has 64 boxes, and issuing them keeps a warp busy for 5,000
-// cycles (a copy is issued by one lane at a time); paged kernels share them
-// between two warps (part 0 and 1): both walk all slots, part 0 alone counts
-// their bytes and does what else there is.
+// after slot of one ring.  Keys that lie together come as one copy per chunk
+// of a slot (a cluster's CTAs copy half of it each, to both); those of pages,
+// and of a block on both sides of a window's gap, as boxes of a.box rows, a
+// lane per box.  What a slot costs here is instructions, which the softmax's
+// straight code keeps evicting (about 0.3 cycles a byte): the loop over slots
+// is kept to a few hundred bytes, with everything that does not change from
+// slot to slot in registers (1,000 -> %SLOT% cycles a slot).  Paged kernels
+// share a slot's boxes between two warps (part 0 and 1): both walk all slots,
+// part 0 alone counts their bytes.
 template <class T, int MODE, bool PAGED>
 __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, SpanAux* aux,
-                               uint32_t sRing, const WaitCtx& wc,
-                               unsigned long long* tr) {
+                               uint32_t sRing, const WaitCtx& wc, unsigned long long* tr) {
     const int lane = threadIdx.x & 31;
     const int box_shift = __ffs(a.box) - 1;   // (a power of two)
     const int rank = (int)cluster_ctarank();
-    struct Box {
-        int row, plane;
+    const bool paired = a.cluster > 1;
+    // the boxes of a block, lane l's the l-th: K slots hold all of them, one
+    // chunk or more each; V slot h the boxes [h vboxes, (h + 1) vboxes)
+    const int boxes = T::BN >> box_shift, vboxes = T::VKEYS >> box_shift;
+    const int v_slot = lane >> (__ffs(vboxes) - 1);
+    const uint32_t k_off = (uint32_t)(lane << box_shift) << 7;
+    const uint32_t v_off = (uint32_t)((lane & (vboxes - 1)) << box_shift) << 7;
+    // whose they are: of a cluster, every other piece (box x chunk); of the two
+    // warps, half of the boxes
+    const bool k_mine = lane < boxes && (!PAGED || (lane < (boxes + 1) / 2) == (part == 0));
+    const bool v_mine =
+        lane < boxes && (!PAGED || ((lane & (vboxes - 1)) < (vboxes + 1) / 2) == (part == 0));
+    const uint32_t bars = smem_u32(&aux->bar_full[0]);
+    const uint32_t empty_off = smem_u32(&aux->bar_empty[0]) - bars;
+    int slot = 0, used = 0;
+    uint32_t phase = 1;   // parity of the phase in which the slot's last contents are released
+    // the next slot, once it is free: its bytes are counted here
+    uint32_t dst, bar;
+    auto acquire = [&]() -> bool {
+        bar = bars + slot * 8;
+        dst = sRing + slot * T::SLOT;
+        if (!mbar_wait(bar + empty_off, phase, wc, kErrWaitTimeout | kSiteLoadEmpty)) return false;
+        if (part == 0 && lane == 0) {
+            trace_mark(tr, kTrLoad, used >> 4, used & 15);
+            mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
+        }
+        ++used;
+        if (++slot == T::NSLOT) {
+            slot = 0;
+            phase ^= 1u;
+        }
+        __syncwarp();
+        return true;
     };
-    int p = 0;
     bool ok = true;
     SpanItem s;
     for (int i = 0; ok && span_item(aux, i, wc, s); ++i) {
         if (s.m == 0) continue;
         const int plane = (a.cu_seqlens_k != nullptr ? 0 : s.b * a.Hkv) + s.hk;
-        // lane l's box of a block, positions [l box, (l + 1) box) of it: where it
-        // lies in the tensor map (past the span, or no page: a plane that does
-        // not exist, which reads as zeros).  at_v: of block j, at_k: of j + 1
-        Box at_v{0, 0}, at_k{0, 0};
+        // where the lane's box of a block lies in the tensor map (past the span,
+        // or no page: a plane that does not exist, which reads as zeros); v: of
+        // block j, k: of j + 1
+        int k_row = 0, k_plane = 0, v_row = 0, v_plane = 0;
 #pragma unroll 1
-        for (int j = -2; j < s.m && ok; ++j) {
+        for (int j = -2; j < s.m; ++j) {
             // page numbers are fetched a block ahead
-            Box next{0, a.planes};
+            int n_row = 0, n_plane = a.planes;
             const int xb = (s.kb + j + 2) * T::BN + (lane << box_shift);
-            if (j + 2 < s.m && lane << box_shift < T::BN && xb < s.span) {
+            if (lane < boxes && xb < s.span) {
                 const int key = span_key(s, xb);
-                if (!PAGED) {
-                    next = Box{s.k0 + key, plane};
-                } else {
-                    const int page = a.block_table[(size_t)s.b * a.max_pages + key / a.page_size];
-                    if ((unsigned)page < (unsigned)a.num_pages)
-                        next = Box{key % a.page_size, page * a.Hkv + s.hk};
+                n_row = s.k0 + key;
+                n_plane = plane;
+                if (PAGED) {
+                    const unsigned at = (unsigned)key / (unsigned)a.page_size;
+                    const int page = a.block_table[(size_t)s.b * a.max_pages + at];
+                    n_row = key - (int)at * a.page_size;
+                    n_plane = (unsigned)page < (unsigned)a.num_pages ? page * a.Hkv + s.hk : a.planes;
                 }
             }
-            // slots: the K block j + 1 in KP, then the V block j in VP
-            const int end = j < 0 ? T::KP : T::KP + T::VP;
+            if (j >= -1) {
+                const int x0 = (s.kb + j) * T::BN;   // block j
+                if (j + 1 < s.m) {
+                    const int x1 = x0 + T::BN;
+                    const bool in_boxes = PAGED || (MODE == kSpanWindow && x1 < s.head && x1 + T::BN > s.head);
 #pragma unroll 1
-            for (int c = j + 1 < s.m ? 0 : T::KP; c < end && j >= -1; ++c) {
-                const bool is_v = c >= T::KP;
-                const int x0 = (s.kb + (is_v ? j : j + 1)) * T::BN + (is_v ? (c - T::KP) * T::VKEYS : 0);
-                const int rows = is_v ? T::VKEYS : T::BN, chunks = is_v ? T::NCH : T::KCH;
-                const int chunk_bytes = is_v ? T::VCHUNK : T::KCHUNK;
-                const int col = is_v ? 0 : c * T::KCH * 64;
-                const uint32_t slot = ring_slot<T>(p);
-                if (!mbar_wait(smem_u32(&aux->bar_empty[slot]), ring_phase<T>(p) ^ 1u, wc,
-                               kErrWaitTimeout | kSiteLoadEmpty)) {
-                    ok = false;
-                    break;
-                }
-                if (part == 0 && lane == 0) trace_mark(tr, kTrLoad, p >> 4, p & 15);
-                ++p;
-                const uint32_t dst = sRing + slot * T::SLOT;
-                const uint32_t bar = smem_u32(&aux->bar_full[slot]);
-                if (part == 0 && lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
-                __syncwarp();
-                if (PAGED || a.cluster > 1 ||
-                    (MODE == kSpanWindow && x0 < s.head && x0 + rows > s.head)) {
-                    // lanes [l0, l1) have the slot's boxes; of a cluster each CTA
-                    // copies every other piece, to both
-                    const int l0 = (x0 % T::BN) >> box_shift, l1 = l0 + (rows >> box_shift);
-                    const int mid = PAGED ? (l0 + l1 + 1) / 2 : l1;
-                    if (part == 0 ? lane >= l0 && lane < mid : lane >= mid && lane < l1) {
-                        const Box at = is_v ? at_v : at_k;
-#pragma unroll 1
-                        for (int q = 0; q < chunks; ++q) {
-                            const uint32_t to =
-                                dst + q * chunk_bytes + (((lane - l0) << box_shift) << 7);
-                            const CUtensorMap* m = is_v ? &tm.v_box : &tm.k_box;
-                            if (a.cluster == 1)
-                                tma_load_3d(to, m, col + q * 64, at.row, at.plane, bar);
-                            else if ((((lane - l0) * chunks + q) & 1) == rank)
-                                tma_load_3d_multicast(to, m, col + q * 64, at.row, at.plane, bar, 3);
+                    for (int c = 0; c < T::KP; ++c) {
+                        if (!(ok = acquire())) break;
+                        if (in_boxes) {
+                            if (k_mine) {
+#pragma unroll
+                                for (int q = 0; q < T::KCH; ++q) {
+                                    const int col = (c * T::KCH + q) * 64;
+                                    const uint32_t to = dst + k_off + q * T::KCHUNK;
+                                    if (!paired)
+                                        tma_load_3d(to, &tm.k_box, col, k_row, k_plane, bar);
+                                    else if (((lane * T::KCH + q) & 1) == rank)
+                                        tma_load_3d_multicast(to, &tm.k_box, col, k_row, k_plane, bar, 3);
+                                }
+                            }
+                        } else if (lane == 0) {
+                            const int row = s.k0 + span_key(s, x1);
+#pragma unroll
+                            for (int q = 0; q < T::KCH; ++q) {
+                                const int col = (c * T::KCH + q) * 64;
+                                const uint32_t to = dst + q * T::KCHUNK;
+                                if (!paired)
+                                    tma_load_3d(to, &tm.k, col, row, plane, bar);
+                                else   // half of the rows
+                                    tma_load_3d_multicast(to + rank * (T::BN / 2 * 128), &tm.k, col,
+                                                          row + rank * (T::BN / 2), plane, bar, 3);
+                            }
                         }
                     }
-                } else if (lane == 0) {
-                    const int row = s.k0 + span_key(s, x0);
-#pragma unroll 1
-                    for (int q = 0; q < chunks; ++q)
-                        tma_load_3d(dst + q * chunk_bytes, is_v ? &tm.v : &tm.k, col + q * 64, row,
-                                    plane, bar);
+                    if (!ok) break;
                 }
-                __syncwarp();
+                if (j >= 0) {
+#pragma unroll 1
+                    for (int h = 0; h < T::VP; ++h) {
+                        const int xv = x0 + h * T::VKEYS;
+                        if (!(ok = acquire())) break;
+                        if (PAGED || (MODE == kSpanWindow && xv < s.head && xv + T::VKEYS > s.head)) {
+                            if (v_mine && v_slot == h) {
+#pragma unroll
+                                for (int q = 0; q < T::NCH; ++q) {
+                                    const uint32_t to = dst + v_off + q * T::VCHUNK;
+                                    if (!paired)
+                                        tma_load_3d(to, &tm.v_box, q * 64, v_row, v_plane, bar);
+                                    else if (((lane * T::NCH + q) & 1) == rank)
+                                        tma_load_3d_multicast(to, &tm.v_box, q * 64, v_row, v_plane, bar, 3);
+                                }
+                            }
+                        } else if (lane == 0) {
+                            const int row = s.k0 + span_key(s, xv);
+                            if (!paired) {
+#pragma unroll
+                                for (int q = 0; q < T::NCH; ++q)
+                                    tma_load_3d(dst + q * T::VCHUNK, &tm.v, q * 64, row, plane, bar);
+                            } else if (T::NCH == 1) {   // half of the rows
+                                tma_load_3d_multicast(dst + rank * (T::VKEYS / 2 * 128), &tm.v, 0,
+                                                      row + rank * (T::VKEYS / 2), plane, bar, 3);
+                            } else {                    // half of the chunks
+#pragma unroll
+                                for (int q = 0; q < T::NCH / 2; ++q)
+                                    tma_load_3d_multicast(dst + (2 * q + rank) * T::VCHUNK, &tm.v,
+                                                          (2 * q + rank) * 64, row, plane, bar, 3);
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                }
             }
-            at_v = at_k;
-            at_k = next;
+            v_row = k_row;
+            v_plane = k_plane;
+            k_row = n_row;
+            k_plane = n_plane;
         }
     }
     // every copy issued must have landed before the CTA exits (part 0 counts
-    // the bytes of both)
+    // the bytes of both), and every arrival from the other CTA of a cluster
     if (part == 0 && lane == 0) {
-        for (int q = p > T::NSLOT ? p - T::NSLOT : 0; q < p; ++q)
-            mbar_wait_drain(smem_u32(&aux->bar_full[ring_slot<T>(q)]), ring_phase<T>(q),
-                            a.wait_limit_ns);
-        // and every arrival from the other CTA of the cluster
-        for (int q = p > T::NSLOT ? p - T::NSLOT : 0; a.cluster > 1 && q < p; ++q)
-            mbar_wait_drain(smem_u32(&aux->bar_empty[ring_slot<T>(q)]), ring_phase<T>(q),
-                            a.wait_limit_ns);
+#pragma unroll 1
+        for (int q = used > T::NSLOT ? used - T::NSLOT : 0; q < used; ++q) {
+            mbar_wait_drain(bars + ring_slot<T>(q) * 8, ring_phase<T>(q), a.wait_limit_ns);
+            if (paired)
+                mbar_wait_drain(bars + empty_off + ring_slot<T>(q) * 8, ring_phase<T>(q),
+                                a.wait_limit_ns);
+        }
     }
     __syncwarp();
 }
@@ -695,6 +763,7 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanItem& s
                     vis = tree_bits(words, s.rows, xq - node0);
                 else
                     vis = low_bits(fa - xq) | (low_bits(lim + 1 - xq) & ~low_bits(lo - xq));
+                if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
                 const uint32_t col = lane_base + T::S_COL + h * HK + q * 32;
                 tmem_ld32(col, w);
                 tmem_wait_ld();
@@ -827,9 +896,12 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
         for (int g = 0; g < 4; ++g) {
             uint32_t pk[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                pk[e] = pack_bf16x2(__uint_as_float(v[g * 8 + 2 * e]) * inv_l,
-                                    __uint_as_float(v[g * 8 + 2 * e + 1]) * inv_l);
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = ffma2(make_float2(__uint_as_float(v[g * 8 + 2 * e]),
+                                                   __uint_as_float(v[g * 8 + 2 * e + 1])),
+                                       make_float2(inv_l, inv_l), make_float2(0.f, 0.f));
+                pk[e] = pack_bf16x2(y.x, y.y);
+            }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                              stage + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
                          "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
