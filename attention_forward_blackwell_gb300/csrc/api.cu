@@ -231,13 +231,41 @@ struct Tree {
 // 1.2-3.9x faster for every batch from 1 to 16 at 32 to 128 rows.
 constexpr int kDecodeToPrefillRows = 32;
 
-// Query rows per kv head up to which a tree runs the split-KV kernel.
-constexpr int kTreeSplitRows = 16;
-// Keys of a window (and its first keys) from which a dense prompt does not.
+// Keys of a window (and its first keys) from which a dense prompt does not run
+// the span kernel.
 constexpr long long kWindowDenseKeys = 512;
-// Keys of all (batch entry, kv head) pairs up to which a windowed decode with
-// first keys does.
-constexpr long long kWindowSplitKeys = 100000;
+
+// Whether a tree, or a decode window with first keys, runs the span kernel
+// (true) or the split-KV kernel; `rows` query rows per kv head read `keys` keys
+// each, of `heads` (batch entry, kv head) pairs.  The split-KV kernel starts
+// faster and its tensor instructions take 16 rows at a time, so it wins where
+// both the rows and the bytes are few.  us, split-KV / span, pages of 64:
+//                       d 64          d 128         d 256
+//  tree, 8 heads x 1,024 keys
+//    4 rows          10.0 /  12.7  11.9 /  14.0  16.9 /  15.6
+//    16 rows         11.9 /  12.7  15.8 /  14.0  23.2 /  15.4
+//    64 rows         13.8 /  12.9  17.5 /  14.3  36.1 /  16.0
+//  tree, 64 heads x 8,192 keys
+//    4 rows          48.2 /  35.9  78.3 /  53.2   218 /  92.1
+//    64 rows          131 /  35.7   245 /  54.2   750 /  96.3
+//  window of 1,024, 32 heads
+//    4 rows          11.2 /  16.2  12.7 /  18.5  23.5 /  20.3
+//    16 rows         13.5 /  16.1  16.1 /  18.4  35.0 /  19.0
+//  window of 4,096, 64 heads
+//    4 rows          26.8 /  26.7  42.9 /  35.8   108 /  56.7
+//  window of 256, 512 heads (most of a block masked)
+//    4 rows          19.5 /  32.8  31.7 /  42.7  77.7 /  51.7
+// Small boxes (of the largest power of two that divides the page size) slow the
+// span kernel's loads: 16 sequences x 8 heads of 1K to 16K keys at head_dim 128,
+// 16 rows 137 / 97 in pages of 64, 140 / 112 in pages of 40, 139 / 160 in pages
+// of 100 (boxes of 4), 128 rows of those 689 / 163.
+constexpr long long kSpanElements = 8 << 20;   // keys x head_dim of all heads
+bool span_wins(bool tree, int head_dim, int rows, long long heads, long long keys, int box) {
+    const bool small = box < 8;
+    if ((long long)rows * head_dim >= (tree ? 2048 : 8192) << small) return true;
+    return heads * keys * head_dim >= kSpanElements && !small &&
+           (tree || head_dim == 256 || keys >= 512);
+}
 
 // A tree of query nodes (tree != nullptr, sq = nodes) or a window whose first
 // keys stay visible, on the tensor-core kernel (span.cu).  vl: packed queries,
@@ -256,7 +284,8 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
                     float* lse, int batch, int hq, int hkv, int sq, int sk, const int* seqlens_k,
                     int head_dim, float scale, int causal, int window, int first,
                     const float* sinks, const int* block_table, int max_pages, int page_size,
-                    int num_pages, const Varlen* vl, const DeviceInfo& di, cudaStream_t s) {
+                    int num_pages, const Varlen* vl, bool decode, const DeviceInfo& di,
+                    cudaStream_t s) {
     SpanLaunch p{};
     SpanArgs& a = p.args;
     const unsigned long long row_bytes = (unsigned long long)head_dim * 2;
@@ -331,6 +360,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         a.tree_stride = tree->shared ? 0 : (long long)sq * a.tree_words;
     } else {
         a.causal = causal ? 1 : 0;
+        a.decode = decode ? 1 : 0;
         a.window = std::min(window, 1 << 30);
         a.first = std::min(first, sk);
         a.head_keys = (a.first + a.box - 1) / a.box * a.box;
@@ -422,12 +452,13 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
 
     const bool windowed = window > 0 && first > 0;
     if (sk > 0 && span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size) &&
-        (tree ? (hq / hkv) * sq > kTreeSplitRows
-              : windowed && (long long)batch * hkv * std::min<long long>(sk, (long long)window + first) >
-                                kWindowSplitKeys))
+        (tree || windowed) &&
+        span_wins(tree != nullptr, head_dim, hq / hkv * sq, (long long)batch * hkv,
+                  tree ? sk : std::min<long long>(sk, (long long)window + first),
+                  block_table ? span_box(head_dim, page_size, 64) : 64))
         return span_impl(tree, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,
-                         nullptr, *di, s);
+                         nullptr, true, *di, s);
 
     DecodeArgs a{};
     a.q = static_cast<const uint16_t*>(q);
@@ -531,7 +562,7 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
         span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size))
         return span_impl(nullptr, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,
-                         vl, *di, s);
+                         vl, false, *di, s);
     PrefillLaunch p{};
     const unsigned long long row_bytes = (unsigned long long)head_dim * 2;
     // kernel family, unit and block sizes, work split (head_dim 96 / 128,

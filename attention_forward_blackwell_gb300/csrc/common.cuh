@@ -314,6 +314,7 @@ struct SpanArgs {
     int tree_words;
     long long tree_stride;
     int causal, window, first;
+    int decode;                 // keys that no row sees may hold anything
     int head_keys;              // first, rounded up to boxes
     int window_keys;            // most positions of a causal tile's axis
     const int* cu_seqlens_q;    // packed queries and keys, as in PrefillArgs
@@ -362,13 +363,14 @@ int span_paired_ctas(int head_dim, int num_sms);
 inline int span_block_keys(int head_dim) { return head_dim == 256 ? 128 : 256; }
 inline int span_slot_keys(int head_dim) { return 256 * 64 / head_dim; }
 // Rows of a box in pages of page_size rows: the largest power of two that
-// divides it, at most `most` and a V slot; 0 below 8 (the swizzle's atom of 8
-// rows).
+// divides it, at most `most` and a V slot; 0 below 4 (the producer's 64 lanes
+// hold a block's 64 boxes; a box of 4 rows is half an atom of the 128-byte
+// swizzle, whose pattern goes by the address).
 inline int span_box(int head_dim, int page_size, int most) {
     int box = page_size & -page_size;
     if (span_slot_keys(head_dim) < most) most = span_slot_keys(head_dim);
     if (box > most) box = most;
-    return box >= 8 ? box : 0;
+    return box >= 4 ? box : 0;
 }
 
 // Fills O = 0 and LSE = -inf, or the row's sink logit when sinks is not null

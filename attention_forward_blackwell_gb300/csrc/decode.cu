@@ -200,6 +200,14 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
         const uint32_t sk = wbase + stage * 2 * T::SLICE;
         const uint32_t sv = sk + T::SLICE;
         const size_t slice_off = slice_pages ? row_off(fs.key(key0)) : 0;
+        // pages of other sizes: a lane per row looks its row up, and the row's
+        // granules take it from there (one division and table entry per row
+        // instead of one per granule)
+        size_t lane_off = 0;
+        if (PAGED && !slice_pages) {
+            const int x = key0 + (lane & (T::KB - 1));
+            lane_off = row_off(fs.key(x < k_hi ? x : k_lo));
+        }
 #pragma unroll
         for (int e = lane; e < T::KB * T::GRAN; e += 32) {
             const int kr = e / T::GRAN, g = e % T::GRAN;
@@ -209,8 +217,14 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
                 const int x = fs.key(key);
                 valid = valid && (x >= lo_all || x < a.first);
             }
-            const size_t src = (slice_pages ? slice_off + (size_t)(valid ? kr : 0) * D
-                                            : row_off(fs.key(valid ? key : k_lo))) + g * 8;
+            size_t row;
+            if (!PAGED)
+                row = row_off(fs.key(valid ? key : k_lo));
+            else if (slice_pages)
+                row = slice_off + (size_t)(valid ? kr : 0) * D;
+            else
+                row = __shfl_sync(0xffffffffu, (unsigned long long)lane_off, kr);
+            const size_t src = row + g * 8;
             cp_async_16(sk + swz<D>(kr, g), a.k + src, valid ? 16u : 0u);
             cp_async_16(sv + swz<D>(kr, g), a.v + src, valid ? 16u : 0u);
         }

@@ -31,7 +31,7 @@
 // depend on timing).  A tree of several tiles gives each to a CTA of a group
 // that walks the same keys at the same time, so that K and V come from HBM
 // once (one tile after the other, a 64-node tree of 8 heads read them three
-// times and took 117 us instead of %GROUPED%).
+// times and took 117 us instead of 98).
 //
 // Inside a CTA: the roles and barriers of the 256-key prefill kernel (see
 // prefill_wide.cuh), which this one follows: S = Q K^T of the next block is
@@ -104,6 +104,7 @@ struct SpanItem {
     int head, skip;  // position x of its axis: key x below head, key x + skip from there on
     int span;        // positions that a row may see
     int end;         // position of the sequence's end
+    int gap;         // decode: no row sees a position from `first` up to here
     int rows, keys;  // the sequence's (see SpanSeq)
     int q0, k0, cap;
 };
@@ -184,7 +185,7 @@ __device__ __forceinline__ int span_key(const SpanItem& s, int x) {
 // The axis of the keys of the unit whose first tile is t0.
 template <class T, int MODE>
 __device__ __forceinline__ void span_geometry(const SpanArgs& a, int t0, SpanItem& s) {
-    s.head = s.skip = 0;
+    s.head = s.skip = s.gap = 0;
     if constexpr (MODE == kSpanTree) {
         s.span = s.end = s.keys;
     } else {
@@ -192,11 +193,12 @@ __device__ __forceinline__ void span_geometry(const SpanArgs& a, int t0, SpanIte
         const int p0 = t0 * a.P + off;     // keys of the unit's first and last row
         const int p1 = min((t0 + a.group_ctas) * a.P, s.cap) - 1 + off;
         const int last = a.causal ? min(s.keys - 1, p1) : s.keys - 1;
-        const int base = max(0, p0 - a.window + 1) & -a.box;
+        const int lo = max(0, p0 - a.window + 1), base = lo & -a.box;
         if (a.head_keys < base) {
             s.head = a.head_keys;
             s.skip = base - s.head;
         }
+        if (a.decode) s.gap = lo - s.skip;
         s.span = max(0, last + 1 - s.skip);
         s.end = s.keys - s.skip;
     }
@@ -409,7 +411,7 @@ __device__ __forceinline__ bool span_row(const SpanArgs& a, int cap, int q0, int
 // lane per box.  What a slot costs here is instructions, which the softmax's
 // straight code keeps evicting (about 0.3 cycles a byte): the loop over slots
 // is kept to a few hundred bytes, with everything that does not change from
-// slot to slot in registers (1,000 -> %SLOT% cycles a slot).  Paged kernels
+// slot to slot in registers (1,000 -> 700 cycles a slot).  Paged kernels
 // share a slot's boxes between two warps (part 0 and 1): both walk all slots,
 // part 0 alone counts their bytes.
 template <class T, int MODE, bool PAGED>
@@ -419,17 +421,22 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
     const int box_shift = __ffs(a.box) - 1;   // (a power of two)
     const int rank = (int)cluster_ctarank();
     const bool paired = a.cluster > 1;
-    // the boxes of a block, lane l's the l-th: K slots hold all of them, one
-    // chunk or more each; V slot h the boxes [h vboxes, (h + 1) vboxes)
+    // the boxes of a block, lane l's the l-th (of 64, a warp has half): K slots
+    // hold all of them, one chunk or more each; V slot h the boxes [h vboxes,
+    // (h + 1) vboxes)
     const int boxes = T::BN >> box_shift, vboxes = T::VKEYS >> box_shift;
-    const int v_slot = lane >> (__ffs(vboxes) - 1);
-    const uint32_t k_off = (uint32_t)(lane << box_shift) << 7;
-    const uint32_t v_off = (uint32_t)((lane & (vboxes - 1)) << box_shift) << 7;
+    const bool many = boxes > 32;
+    const int mine = many ? part * 32 + lane : lane;
+    const int v_slot = mine >> (__ffs(vboxes) - 1);
+    const uint32_t k_off = (uint32_t)(mine << box_shift) << 7;
+    const uint32_t v_off = (uint32_t)((mine & (vboxes - 1)) << box_shift) << 7;
     // whose they are: of a cluster, every other piece (box x chunk); of the two
     // warps, half of the boxes
-    const bool k_mine = lane < boxes && (!PAGED || (lane < (boxes + 1) / 2) == (part == 0));
+    const bool k_mine =
+        mine < boxes && (!PAGED || many || (mine < (boxes + 1) / 2) == (part == 0));
     const bool v_mine =
-        lane < boxes && (!PAGED || ((lane & (vboxes - 1)) < (vboxes + 1) / 2) == (part == 0));
+        mine < boxes &&
+        (!PAGED || many || ((mine & (vboxes - 1)) < (vboxes + 1) / 2) == (part == 0));
     const uint32_t bars = smem_u32(&aux->bar_full[0]);
     const uint32_t empty_off = smem_u32(&aux->bar_empty[0]) - bars;
     int slot = 0, used = 0;
@@ -465,8 +472,8 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
         for (int j = -2; j < s.m; ++j) {
             // page numbers are fetched a block ahead
             int n_row = 0, n_plane = a.planes;
-            const int xb = (s.kb + j + 2) * T::BN + (lane << box_shift);
-            if (lane < boxes && xb < s.span) {
+            const int xb = (s.kb + j + 2) * T::BN + (mine << box_shift);
+            if (mine < boxes && xb < s.span) {
                 const int key = span_key(s, xb);
                 n_row = s.k0 + key;
                 n_plane = plane;
@@ -493,7 +500,7 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                                     const uint32_t to = dst + k_off + q * T::KCHUNK;
                                     if (!paired)
                                         tma_load_3d(to, &tm.k_box, col, k_row, k_plane, bar);
-                                    else if (((lane * T::KCH + q) & 1) == rank)
+                                    else if (((mine * T::KCH + q) & 1) == rank)
                                         tma_load_3d_multicast(to, &tm.k_box, col, k_row, k_plane, bar, 3);
                                 }
                             }
@@ -525,7 +532,7 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                                     const uint32_t to = dst + v_off + q * T::VCHUNK;
                                     if (!paired)
                                         tma_load_3d(to, &tm.v_box, q * 64, v_row, v_plane, bar);
-                                    else if (((lane * T::NCH + q) & 1) == rank)
+                                    else if (((mine * T::NCH + q) & 1) == rank)
                                         tma_load_3d_multicast(to, &tm.v_box, q * 64, v_row, v_plane, bar, 3);
                                 }
                             }
@@ -754,7 +761,8 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanItem& s
             // a block at the border: scores that the row does not see become
             // -inf in tensor memory, 32 at a time (a loop of a kilobyte of
             // instructions; selects on the 128 registers below take five, which
-            // the instruction cache has no room for: %MASK%)
+            // the instruction cache has no room for; with the scheduler warp this
+            // took a window's prompts from 123 to 99 us)
 #pragma unroll 1
             for (int q = 0; q < HK / 32; ++q) {
                 const int xq = x0 + 32 * q;
@@ -931,7 +939,7 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
 template <class T, int MODE>
 __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, int g, int gp, SpanAux* aux,
                                         uint32_t tmem, uint32_t sRing, const WaitCtx& wc, int J0,
-                                        int kq, int p_end, unsigned long long* tr) {
+                                        int kq, int p0, unsigned long long* tr) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((warp & 3) != 0 || lane != 0) tr = nullptr;
     const int r = (warp & 3) * 32 + lane;
@@ -966,28 +974,31 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, in
             }
             tmem_wait_st();
         }
-        // value rows past the sequence's end may hold anything, and zero times a
+        // value rows past the sequence's end, and (decode) those between the
+        // first keys and the window, may hold anything, and zero times a
         // non-finite value would poison O: zeroed here, before PV(J) is let go
         const int x0 = (s.kb + j) * T::BN;
-        if (s.end < x0 + T::BN) {
+        if (s.end < x0 + T::BN || (x0 < s.gap && x0 + T::BN > a.first)) {
+            // (V_j's slots come after K_{j+1}'s)
+            int pv = p0 + j * (T::KP + T::VP) + (j + 1 < s.m ? 2 : 1) * T::KP;
             bool landed = true;
 #pragma unroll 1
-            for (int hh = 0; hh < T::VP && landed; ++hh) {
-                const int z0 = max(s.end - x0 - hh * T::VKEYS, 0);
-                if (z0 >= T::VKEYS) continue;
-                // (V of a segment's last block fills its last VP slots)
-                const int pv = p_end - T::VP + hh;
+            for (int hh = 0; hh < T::VP && landed; ++hh, ++pv) {
+                const int xv = x0 + hh * T::VKEYS;   // first position of the slot
                 landed = mbar_wait(smem_u32(&aux->bar_full[ring_slot<T>(pv)]), ring_phase<T>(pv), wc,
                                    kErrWaitTimeout | kSiteLoadTail);
                 const uint32_t slot = sRing + ring_slot<T>(pv) * T::SLOT;
 #pragma unroll 1
-                for (int g = z0 * 8 + r; g < T::VKEYS * 8; g += T::BM)
+                for (int g = r; g < T::VKEYS * 8; g += T::BM) {
+                    const int x = xv + (g >> 3);
+                    if (x < s.end && (x < a.first || x >= s.gap)) continue;
 #pragma unroll 1
                     for (int q = 0; q < T::NCH; ++q)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                          slot + q * T::VCHUNK + g * 16),
                                      "r"(0)
                                      : "memory");
+                }
             }
             if (!landed) return false;
             fence_proxy_async_smem();
@@ -1124,7 +1135,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         SpanItem s;
         for (int i = 0; span_item(aux, i, wc, s); ++i) {
             if (!span_correction_segment<T, MODE>(a, s, g, gp, aux, tmem,
-                                                  sRing, wc, J0, kq, (J0 + s.m) * (T::KP + T::VP), tr))
+                                                  sRing, wc, J0, kq, J0 * (T::KP + T::VP), tr))
                 break;
             J0 += s.m;
             kq += s.m > 0;

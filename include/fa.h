@@ -258,10 +258,10 @@ fa_status fa_fwd_decode_ex(const void *q, const void *k, const void *v, void *o,
  * (fa_fwd_decode_paged_first: paged decode with a window and sinks).  Only the
  * key blocks that hold the first keys and those of the window are visited, so
  * time and traffic do not grow with the sequence.  The prefill kernels read
- * whole blocks of 128 keys: within the first block(s) and the blocks of the
+ * whole blocks of up to 256 keys: within the first block(s) and the blocks of the
  * window, keys j < L_b must be finite even where they are masked (a masked
- * key's probability, zero, multiplies its value row).  Decode reads only keys
- * that some query row of the sequence sees.  first < 0: FA_ERR_INVALID_ARG.
+ * key's probability, zero, multiplies its value row).  In decode, keys that no
+ * query row of the sequence sees may hold anything.  first < 0: FA_ERR_INVALID_ARG.
  */
 fa_status fa_fwd_prefill_first(const void *q, const void *k, const void *v, void *o,
                                float *lse, int batch, int hq, int hkv, int sq, int sk,
