@@ -235,36 +235,69 @@ constexpr int kDecodeToPrefillRows = 32;
 // the span kernel.
 constexpr long long kWindowDenseKeys = 512;
 
-// Whether a tree, or a decode window with first keys, runs the span kernel
-// (true) or the split-KV kernel; `rows` query rows per kv head read `keys` keys
-// each, of `heads` (batch entry, kv head) pairs.  The split-KV kernel starts
-// faster and its tensor instructions take 16 rows at a time, so it wins where
-// both the rows and the bytes are few.  us, split-KV / span, pages of 64:
-//                       d 64          d 128         d 256
+// Splits of the split-KV kernel over `span` keys of `pairs` (batch entry, kv
+// head, 16 query rows): enough CTAs to keep in flight, of at least 256 keys.
+// A tree or a window with first keys may join: splits of 64 keys or more in one
+// wave of CTAs, the splits of a pair a cluster, which merges them without a
+// second kernel and a workspace (7 query heads x 1,000 keys at head_dim 64: 8.8
+// -> 6.9 us; a window of 1,024 at 128: 8.8 -> 7.5).  Past 8 x 256 keys more
+// splits gain more (4,096 keys at head_dim 128: 15.2 us / 16.9 joined), and past
+// a wave the wait for the others costs more (512 pairs x 256 keys at 64: 19.6 /
+// 25.3).  With one CTA per SM (head_dim 256) few clusters of 7 or 8 find their
+// SMs in one GPC: 16 pairs x 8 splits took 28 us, two waves, 32 x 4 took 18.
+struct SplitPlan {
+    int splits;
+    bool joined;
+    long long wave;   // CTAs that run at once
+};
+SplitPlan split_plan(bool may_join, int head_dim, long long pairs, long long span, int num_sms) {
+    SplitPlan p{};
+    const long long target = 24ll * num_sms;
+    const long long most = (span + 255) / 256;
+    p.splits = (int)std::max(1ll, std::min((target + pairs - 1) / pairs, most));
+    p.wave = (head_dim == 256 ? 1ll : head_dim == 128 ? 2ll : 3ll) * num_sms;
+    if (may_join && most <= kJoinSplits) {
+        const long long fine = std::min<long long>((span + 63) / 64, kJoinSplits);
+        long long join = std::min(fine, p.wave / pairs);
+        if (head_dim == 256 && 2 * join * pairs > p.wave) join = std::min(join, 4ll);
+        p.joined = join >= std::min(2ll, fine);
+        if (p.joined) p.splits = (int)join;
+    }
+    return p;
+}
+
+// Whether a tree, or a decode window with first keys, of `tiles` x 16 query
+// rows per (batch entry, kv head), `heads` of those, over `span` keys each runs
+// the span kernel (true) or the split-KV kernel as planned.  The split-KV kernel
+// starts faster and reads the keys once per 16 rows, so it wins where what it
+// reads is little.  us, split-KV / span, pages of 64:
+//                           d 64          d 128         d 256
 //  tree, 8 heads x 1,024 keys
-//    4 rows          10.0 /  12.7  11.9 /  14.0  16.9 /  15.6
-//    16 rows         11.9 /  12.7  15.8 /  14.0  23.2 /  15.4
-//    64 rows         13.8 /  12.9  17.5 /  14.3  36.1 /  16.0
+//    4 rows              7.1 /  12.6   9.1 /  13.9  12.3 /  15.9
+//    64 rows             9.7 /  12.8  11.9 /  14.3  19.8 /  16.0
+//  tree, 128 heads x 300 keys
+//    4 rows              7.5 /  11.9   9.4 /  13.9  24.1 /  16.0
+//    24 rows            15.0 /  11.9  20.3 /  13.9  49.9 /  16.0
 //  tree, 64 heads x 8,192 keys
-//    4 rows          48.2 /  35.9  78.3 /  53.2   218 /  92.1
-//    64 rows          131 /  35.7   245 /  54.2   750 /  96.3
-//  window of 1,024, 32 heads
-//    4 rows          11.2 /  16.2  12.7 /  18.5  23.5 /  20.3
-//    16 rows         13.5 /  16.1  16.1 /  18.4  35.0 /  19.0
-//  window of 4,096, 64 heads
-//    4 rows          26.8 /  26.7  42.9 /  35.8   108 /  56.7
-//  window of 256, 512 heads (most of a block masked)
-//    4 rows          19.5 /  32.8  31.7 /  42.7  77.7 /  51.7
+//    4 rows             48.2 /  35.9  78.3 /  53.2   218 /  92.1
+//  window of 2,048, 32 heads
+//    4 rows             11.8 /  16.7  12.6 /  19.6  31.1 /  26.1
+//    64 rows            26.2 /  17.4  41.3 /  20.1   117 /  26.6
+//  window of 256, 512 heads (the span kernel masks most of a block)
+//    4 rows             19.2 /  32.7  29.4 /  42.4  74.4 /  51.4
+//    32 rows            42.5 /  32.9  69.2 /  42.2   188 /  56.5
 // Small boxes (of the largest power of two that divides the page size) slow the
 // span kernel's loads: 16 sequences x 8 heads of 1K to 16K keys at head_dim 128,
 // 16 rows 137 / 97 in pages of 64, 140 / 112 in pages of 40, 139 / 160 in pages
 // of 100 (boxes of 4), 128 rows of those 689 / 163.
-constexpr long long kSpanElements = 8 << 20;   // keys x head_dim of all heads
-bool span_wins(bool tree, int head_dim, int rows, long long heads, long long keys, int box) {
-    const bool small = box < 8;
-    if ((long long)rows * head_dim >= (tree ? 2048 : 8192) << small) return true;
-    return heads * keys * head_dim >= kSpanElements && !small &&
-           (tree || head_dim == 256 || keys >= 512);
+bool span_wins(const SplitPlan& plan, int head_dim, long long heads, long long tiles,
+               long long span, int box) {
+    constexpr long long M = 1 << 20;
+    // elements of K that the split-KV kernel reads, against those it may
+    const long long read = heads * tiles * span * head_dim / (box < 8 ? 2 : 1);
+    if (plan.joined) return read >= (tiles == 1 ? 24 * M : head_dim == 256 ? 4 * M : 12 * M);
+    if (tiles > 1) return read >= 8 * M || 2 * heads * tiles > plan.wave;
+    return read >= (head_dim == 256 ? 8 * M : 12 * M) && (head_dim == 256 || span >= 512);
 }
 
 // A tree of query nodes (tree != nullptr, sq = nodes) or a window whose first
@@ -450,16 +483,30 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
         return prefill_impl(q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                             causal, 0, sinks, nullptr, 0, 0, 0, stream, nullptr);
 
+    const int rows = hq / hkv * sq;
+    const long long tiles = (rows + 15) / 16, pairs = (long long)batch * hkv * tiles;
+    // equal chunks of a multiple of 64 keys over the keys a sequence's rows can
+    // see: all sk, or with a sliding window the last window + sq - 1 (the splits
+    // start at each sequence's first visible key, rounded down to a multiple of
+    // 64: up to 63 more), plus the first keys rounded up to one where they stay
+    // visible; at least 1 (a tree over no keys: the split kernel does nothing,
+    // the combine writes the rows)
     const bool windowed = window > 0 && first > 0;
-    if (sk > 0 && span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size) &&
-        (tree || windowed) &&
-        span_wins(tree != nullptr, head_dim, hq / hkv * sq, (long long)batch * hkv,
-                  tree ? sk : std::min<long long>(sk, (long long)window + first),
+    const long long heads_first = windowed ? (std::min(first, sk) + 63ll) / 64 * 64 : 0;
+    const long long window_keys = (long long)window + sq + 62 + heads_first;
+    const long long span =
+        std::max<long long>(1, window > 0 ? std::min<long long>(sk, window_keys) : (long long)sk);
+    SplitPlan plan = split_plan(tree || windowed, head_dim, pairs, span, di->num_sms);
+    if (num_splits > 0) plan = {num_splits, false, plan.wave};
+    if ((tree || windowed) && sk > 0 &&
+        span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size) &&
+        span_wins(plan, head_dim, (long long)batch * hkv, tiles, span,
                   block_table ? span_box(head_dim, page_size, 64) : 64))
         return span_impl(tree, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,
                          nullptr, true, *di, s);
 
+    if (hkv * tiles > 65535) return FA_ERR_INVALID_ARG;
     DecodeArgs a{};
     a.q = static_cast<const uint16_t*>(q);
     a.k = static_cast<const uint16_t*>(k);
@@ -473,8 +520,8 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     a.Sq = sq;
     a.Sk = sk;
     a.group = hq / hkv;
-    a.rows = a.group * sq;
-    a.n_mtiles = (a.rows + 15) / 16;
+    a.rows = rows;
+    a.n_mtiles = (int)tiles;
     a.causal = causal ? 1 : 0;
     a.window = window > 0 ? window : 0;
     a.first = window > 0 ? std::min(first, sk) : 0;
@@ -490,33 +537,15 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     a.page_size = page_size;
     a.num_pages = num_pages;
     a.scale_log2 = scale * 1.4426950408889634f;
-    if ((long long)hkv * a.n_mtiles > 65535) return FA_ERR_INVALID_ARG;
-    // split planning: equal chunks of a multiple of 64 keys over the keys a
-    // sequence's rows can see: all sk, or with a sliding window the last
-    // window + sq - 1 (the splits start at each sequence's first visible key,
-    // rounded down to a multiple of 64: up to 63 more), plus the first keys
-    // rounded up to one where they stay visible; at least 1 (a tree over no
-    // keys: the split kernel does nothing, the combine writes the rows)
-    const long long window_keys = (long long)a.window + sq + 62 + (a.first + 63ll) / 64 * 64;
-    const long long span =
-        std::max<long long>(1, a.window > 0 ? std::min<long long>(sk, window_keys) : (long long)sk);
-    int splits = num_splits;
-    if (splits <= 0) {
-        const long long pairs = (long long)batch * hkv * a.n_mtiles;
-        const long long target = 24ll * di->num_sms;   // CTAs worth keeping in flight
-        long long want = (target + pairs - 1) / pairs;
-        const long long max_splits = (span + 255) / 256;  // at least 256 keys per split
-        if (want > max_splits) want = max_splits;
-        if (want < 1) want = 1;
-        splits = (int)want;
-    }
-    long long chunk = (span + splits - 1) / splits;
+    long long chunk = (span + plan.splits - 1) / plan.splits;
     chunk = (chunk + 63) / 64 * 64;
     a.chunk = (int)chunk;
     a.n_splits = (int)((span + chunk - 1) / chunk);
-    const size_t rows = (size_t)batch * hq * sq;
-    const size_t bytes_o = (size_t)a.n_splits * rows * head_dim * sizeof(float);
-    const size_t bytes_l = (size_t)a.n_splits * rows * sizeof(float);
+    a.joined = plan.joined ? 1 : 0;
+    if (a.joined) return from_cuda(launch_decode(a, head_dim, s));
+    const size_t parts = (size_t)a.n_splits * batch * hq * sq;
+    const size_t bytes_o = parts * head_dim * sizeof(float);
+    const size_t bytes_l = parts * sizeof(float);
     void* ws = nullptr;
     if (cudaMallocAsync(&ws, bytes_o + bytes_l, s) != cudaSuccess) return FA_ERR_CUDA;
     a.part_o = static_cast<float*>(ws);

@@ -274,6 +274,7 @@ struct DecodeArgs {
     int n_mtiles;               // ceil(rows / 16)
     int n_splits;
     int chunk;                  // keys per split (multiple of 64)
+    int joined;                 // the splits are a cluster, which merges them (no combine)
     int causal;
     int window;                 // sliding window in keys (<= 0: none)
     int first;                  // with a window: keys [0, first) stay visible (0: none)
@@ -297,6 +298,7 @@ struct DecodeArgs {
     float scale_log2;
 };
 
+constexpr int kJoinSplits = 8;   // most splits of a joined call (CTAs of a cluster)
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, cudaStream_t s);
 
 // -------------------------------------------------------------- span ----

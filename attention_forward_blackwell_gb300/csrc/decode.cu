@@ -20,7 +20,11 @@
 // The four warps' states are merged in shared memory and the CTA writes one
 // normalised partial (O_s, LSE_s in log2 units).
 //
-// decode_combine_kernel: one warp per query row merges its splits.
+// decode_combine_kernel: one warp per query row merges its splits.  Of a tree
+// or a window with first keys, few splits are one cluster instead, which reads
+// its parts from each other's shared memory and writes the rows itself
+// (DecodeArgs::joined): such calls are bound by latencies, of the launches and
+// of the chain of loads, not by bytes.
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -46,6 +50,7 @@ struct DecodeTraits {
     static constexpr int SMEM = (WARPS * WARP_BYTES > MERGE_BYTES) ? WARPS * WARP_BYTES
                                                                    : MERGE_BYTES;
     static constexpr int NT = D / 8;                    // n8 tiles of O
+    static_assert(MERGE_BYTES + 16 * (D + 1) * 4 <= SMEM, "a joined split's rows must fit");
 };
 
 // byte offset of granule g of key row `key` inside a slice (XOR swizzle keeps
@@ -112,11 +117,13 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     const int k_base =
         (MODE == kModePlain && a.window > 0) ? (max(0, L - a.Sq - a.window + 1) & ~63) : 0;
     const int k_lo = k_base + split * a.chunk;
-    if (k_lo >= fs.span) return;                 // nothing of this sequence here
+    // a joined split stays for its cluster's barriers
+    const bool joined = MODE != kModePlain && a.joined;
+    if (k_lo >= fs.span && !joined) return;      // nothing of this sequence here
     const int k_hi = min(k_lo + a.chunk, fs.span);
     const int nodes = MODE == kModeTree ? tree_nodes(a, b) : 0;
     const int node0 = L - nodes;                 // key of node 0
-    const int nblk = (k_hi - k_lo + T::KB - 1) / T::KB;
+    const int nblk = max(0, k_hi - k_lo + T::KB - 1) / T::KB;
     const int my_blocks = nblk > warp ? (nblk - warp + T::WARPS - 1) / T::WARPS : 0;
 
     // query rows of this thread's fragment: rq0 = lane/4, rq1 = lane/4 + 8
@@ -372,7 +379,9 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     }
     __syncthreads();
     const int valid_rows = min(16, a.rows - rbase);
-    for (int e = threadIdx.x; e < valid_rows * D; e += T::THREADS) {
+    float* jl = reinterpret_cast<float*>(smem + T::MERGE_BYTES);   // joined: [16] LSE,
+    float* jo = jl + 16;                                           // [16][D] O
+    for (int e = threadIdx.x * 4; e < valid_rows * D; e += T::THREADS * 4) {
         const int r = e / D, c = e % D;
         float M = -INFINITY;
 #pragma unroll
@@ -382,20 +391,73 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
         if (MODE == kModeTree && qi_ >= nodes) continue;
         const size_t row_id = ((size_t)b * a.Hq + hkv * a.group + g) * a.Sq + qi_;
         const size_t part = (size_t)split * a.B * a.Hq * a.Sq + row_id;
-        float o = 0.f, lse2 = -INFINITY;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lse2 = -INFINITY;
         if (M != -INFINITY) {
-            float wsum = 0.f, acc = 0.f;
+            float wsum = 0.f;
 #pragma unroll
             for (int w = 0; w < T::WARPS; ++w) {
                 const float f = ex2_approx(wm[w * 16 + r] - M);   // 0 for empty warps
+                const float4 x = *reinterpret_cast<const float4*>(wo + (w * 16 + r) * D + c);
                 wsum = fmaf(f, wl[w * 16 + r], wsum);
-                acc = fmaf(f, wo[(w * 16 + r) * D + c], acc);
+                o.x = fmaf(f, x.x, o.x);
+                o.y = fmaf(f, x.y, o.y);
+                o.z = fmaf(f, x.z, o.z);
+                o.w = fmaf(f, x.w, o.w);
             }
-            o = acc / wsum;
+            o = make_float4(o.x / wsum, o.y / wsum, o.z / wsum, o.w / wsum);
             lse2 = M + lg2_approx(wsum);
         }
-        a.part_o[part * D + c] = o;
-        if (c == 0) a.part_lse[part] = lse2;
+        *reinterpret_cast<float4*>(joined ? jo + e : a.part_o + part * D + c) = o;
+        if (c == 0) *(joined ? jl + r : a.part_lse + part) = lse2;
+    }
+    if constexpr (MODE != kModePlain) {
+        if (!joined) return;
+        // the splits of these rows are the CTAs of the cluster: each finishes a
+        // share of the elements from all of them, in the order of the splits
+        cluster_sync_all();
+        const uint32_t jl_at = smem_u32(jl), jo_at = smem_u32(jo);
+        for (int e = (split * T::THREADS + threadIdx.x) * 4; e < valid_rows * D;
+             e += T::THREADS * a.n_splits * 4) {
+            const int r = e / D, c = e % D;
+            const int pr = rbase + r;
+            const int h = hkv * a.group + pr / a.Sq, qi_ = pr % a.Sq;
+            if (MODE == kModeTree && qi_ >= nodes) continue;
+            float x[kJoinSplits];
+            float4 y[kJoinSplits];
+#pragma unroll
+            for (int s = 0; s < kJoinSplits; ++s) {
+                x[s] = -INFINITY;
+                y[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s < a.n_splits) {
+                    x[s] = cluster_read(jl_at + 4 * r, s);
+                    y[s] = cluster_read4(jo_at + 4 * e, s);
+                }
+            }
+            const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
+            float M = sg, wsum = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int s = 0; s < kJoinSplits; ++s) M = fmaxf(M, x[s]);
+            if (M != -INFINITY) {
+                wsum = ex2_approx(sg - M);
+#pragma unroll
+                for (int s = 0; s < kJoinSplits; ++s) {
+                    const float f = ex2_approx(x[s] - M);
+                    wsum += f;
+                    o.x = fmaf(f, y[s].x, o.x);
+                    o.y = fmaf(f, y[s].y, o.y);
+                    o.z = fmaf(f, y[s].z, o.z);
+                    o.w = fmaf(f, y[s].w, o.w);
+                }
+            }
+            const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+            const size_t row = ((size_t)b * a.Hq + h) * a.Sq + qi_;
+            *reinterpret_cast<uint2*>(a.o + row * D + c) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (c == 0) a.lse[row] = wsum > 0.f ? (M + lg2_approx(wsum)) * kLn2f : -INFINITY;
+        }
+        cluster_sync_all();   // shared memory stays until all have read it
     }
 }
 
@@ -477,6 +539,9 @@ cudaError_t launch_decode_mode(const DecodeArgs& a, cudaStream_t s) {
     const long long rows = (long long)a.B * a.Hq * a.Sq;
     const unsigned combine_ctas = (unsigned)((rows + 7) / 8);
     if constexpr (MODE != kModePlain) {
+        if (a.joined)
+            return launch_dependent_clusters(split, (unsigned)a.n_splits, grid, dim3(T::THREADS),
+                                             T::SMEM, s, a);
         e = launch_dependent(split, grid, dim3(T::THREADS), T::SMEM, s, a);
         if (e != cudaSuccess) return e;
         return launch_dependent(decode_combine_kernel<D, MODE>, dim3(combine_ctas), dim3(256), 0, s,

@@ -193,6 +193,25 @@ __device__ __forceinline__ void cluster_sync_all() {
         "barrier.cluster.arrive.release.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The float that CTA `rank` of the cluster has at this CTA's address `addr`.
+__device__ __forceinline__ float cluster_read(uint32_t addr, int rank) {
+    float x;
+    asm volatile(
+        "{\n\t.reg .b32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [at];\n\t}"
+        : "=f"(x) : "r"(addr), "r"(rank) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 cluster_read4(uint32_t addr, int rank) {
+    float4 x;
+    asm volatile(
+        "{\n\t.reg .b32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [at];\n\t}"
+        : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr), "r"(rank) : "memory");
+    return x;
+}
 
 // Prefetch of a tile (the tensor map's box at these coordinates) into L2:
 // no shared memory, no completion; a later tiled load of the same box then
