@@ -106,6 +106,17 @@ __device__ __forceinline__ void record_error(const WaitCtx& w, unsigned int code
     atomicCAS(w.err_word, 0u, (code & 0xFFFFu) | ((cta & 0xFFFFu) << 16));
 }
 
+// True in one lane of a converged warp (the same one each time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
 // One lane's bounded wait for the phase of `bar` with the given parity.
 // Returns false (without having observed the phase) if the CTA was aborted or
 // the wait exceeded the time limit; the latter records `code`.

@@ -580,8 +580,7 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
 template <class T, int MODE>
 __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, uint32_t sQ,
                               uint32_t sRing, const WaitCtx& wc, unsigned long long* tr) {
-    const int lane = threadIdx.x & 31;
-    if (lane != 0) {
+    if (!elect_one()) {
         __syncwarp();
         return;
     }
