@@ -780,25 +780,17 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanItem& s
             }
             tmem_wait_st();
         }
+        float mq[HK / 64];
 #pragma unroll
         for (int q = 0; q < HK / 64; ++q)
-            tmem_ld64(lane_base + T::S_COL + h * HK + q * 64,
-                      *reinterpret_cast<uint32_t(*)[2][32]>(&u[2 * q][0]));
+            mq[q] = tmem_ld64_max(lane_base + T::S_COL + h * HK + q * 64,
+                                  *reinterpret_cast<uint32_t(*)[2][32]>(&u[2 * q][0]));
         tmem_wait_ld();
         trace_mark(tr, trole, J, 1);
         float x[HK];
 #pragma unroll
         for (int c = 0; c < HK; ++c) x[c] = __uint_as_float(u[c >> 5][c & 31]);
-        float mq[HK / 32];
-#pragma unroll
-        for (int q = 0; q < HK / 32; ++q) {
-            float m = fmax3(x[32 * q], x[32 * q + 1], x[32 * q + 2]);
-#pragma unroll
-            for (int c = 3; c < 31; c += 2) m = fmax3(m, x[32 * q + c], x[32 * q + c + 1]);
-            mq[q] = fmaxf(m, x[32 * q + 31]);
-        }
-        float mx_h = fmaxf(mq[0], mq[1]);
-        if constexpr (HK == 128) mx_h = fmaxf(fmax3(mx_h, mq[2], mq[3]), mx_h);
+        const float mx_h = fmaxf(mq[0], mq[HK / 64 - 1]);
         trace_mark(tr, trole, J, 2);
         aux->xm[sb][h][r] = mx_h;
         tc_fence_before();
