@@ -120,6 +120,7 @@ struct SpanAux {
     uint64_t bar_s_full;
     uint64_t bar_xm[2];
     uint64_t bar_p_ready[2];
+    uint64_t bar_corrected[2];
     uint64_t bar_pv_done[2];
     uint64_t bar_fin;
     uint64_t bar_qfree;
@@ -405,51 +406,45 @@ __device__ __forceinline__ bool span_row(const SpanArgs& a, int cap, int q0, int
 }
 
 // Producers: per segment K_0, then K_{j+1} and V_j for every block j, slot
-// after slot of one ring.  Keys that lie together come as one copy per chunk
-// of a slot (a cluster's CTAs copy half of it each, to both); those of pages,
-// and of a block on both sides of a window's gap, as boxes of a.box rows, a
-// lane per box.  What a slot costs here is instructions, which the softmax's
-// straight code keeps evicting (about 0.3 cycles a byte): the loop over slots
-// is kept to a few hundred bytes, with everything that does not change from
-// slot to slot in registers (1,000 -> 700 cycles a slot).  Paged kernels
-// share a slot's boxes between two warps (part 0 and 1): both walk all slots,
-// part 0 alone counts their bytes.
+// after slot of one ring, two warps in turn (each waits a slot free, counts its
+// bytes and copies).  Keys that lie together come as one copy per chunk of a
+// slot (a cluster's CTAs copy half of it each, to both); those of pages, and of
+// a block on both sides of a window's gap, as boxes of a.box rows, one or two
+// per lane.  A slot takes its warp 500 to 700 cycles of waits and issue one
+// after the other: one warp for the four slots of a block took as long as the
+// block's softmax.  The code is kept to a few hundred bytes, with what does not
+// change from slot to slot in registers: the softmax's straight code keeps
+// evicting it (about 0.3 cycles a byte).
 template <class T, int MODE, bool PAGED>
 __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, SpanAux* aux,
                                uint32_t sRing, const WaitCtx& wc, unsigned long long* tr) {
     const int lane = threadIdx.x & 31;
     const int box_shift = __ffs(a.box) - 1;   // (a power of two)
     const int rank = (int)cluster_ctarank();
-    const bool paired = a.cluster > 1;
-    // the boxes of a block, lane l's the l-th (of 64, a warp has half): K slots
-    // hold all of them, one chunk or more each; V slot h the boxes [h vboxes,
-    // (h + 1) vboxes)
-    const int boxes = T::BN >> box_shift, vboxes = T::VKEYS >> box_shift;
-    const bool many = boxes > 32;
-    const int mine = many ? part * 32 + lane : lane;
-    const int v_slot = mine >> (__ffs(vboxes) - 1);
-    const uint32_t k_off = (uint32_t)(mine << box_shift) << 7;
-    const uint32_t v_off = (uint32_t)((mine & (vboxes - 1)) << box_shift) << 7;
-    // whose they are: of a cluster, every other piece (box x chunk); of the two
-    // warps, half of the boxes
-    const bool k_mine =
-        mine < boxes && (!PAGED || many || (mine < (boxes + 1) / 2) == (part == 0));
-    const bool v_mine =
-        mine < boxes &&
-        (!PAGED || many || ((mine & (vboxes - 1)) < (vboxes + 1) / 2) == (part == 0));
+    const bool paired = a.cluster > 1, one = elect_one();
+    // the boxes of a block, lane l's the l-th and the (l + 32)-th: K slots hold
+    // all of them, one chunk or more each; V slot h the boxes [h vboxes, (h + 1)
+    // vboxes)
+    const int boxes = T::BN >> box_shift, vboxes_shift = __ffs(T::VKEYS >> box_shift) - 1;
     const uint32_t bars = smem_u32(&aux->bar_full[0]);
     const uint32_t empty_off = smem_u32(&aux->bar_empty[0]) - bars;
-    int slot = 0, used = 0;
+    int slot = 0, used = 0;   // the next slot, slots before it
     uint32_t phase = 1;   // parity of the phase in which the slot's last contents are released
-    // the next slot, once it is free: its bytes are counted here
     uint32_t dst, bar;
+    // the next slot: false where it is the other warp's, else it is free and its
+    // bytes are counted
+    bool ok = true;
     auto acquire = [&]() -> bool {
+        const bool its = (used & 1) == part;
         bar = bars + slot * 8;
         dst = sRing + slot * T::SLOT;
-        if (!mbar_wait(bar + empty_off, phase, wc, kErrWaitTimeout | kSiteLoadEmpty)) return false;
-        if (part == 0 && lane == 0) {
-            trace_mark(tr, kTrLoad, used >> 4, used & 15);
-            mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
+        if (its) {
+            ok = ok && mbar_wait(bar + empty_off, phase, wc, kErrWaitTimeout | kSiteLoadEmpty);
+            if (!ok) return false;
+            if (one) {
+                trace_mark(tr, kTrLoad, slot, 0);
+                mbar_arrive_expect_tx(bar, (uint32_t)T::SLOT);
+            }
         }
         ++used;
         if (++slot == T::NSLOT) {
@@ -457,31 +452,35 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
             phase ^= 1u;
         }
         __syncwarp();
-        return true;
+        return its;
     };
-    bool ok = true;
     SpanItem s;
     for (int i = 0; ok && span_item(aux, i, wc, s); ++i) {
         if (s.m == 0) continue;
         const int plane = (a.cu_seqlens_k != nullptr ? 0 : s.b * a.Hkv) + s.hk;
-        // where the lane's box of a block lies in the tensor map (past the span,
+        // where the lane's boxes of a block lie in the tensor map (past the span,
         // or no page: a plane that does not exist, which reads as zeros); v: of
         // block j, k: of j + 1
-        int k_row = 0, k_plane = 0, v_row = 0, v_plane = 0;
+        int k_row[2] = {0, 0}, k_plane[2] = {0, 0}, v_row[2], v_plane[2];
 #pragma unroll 1
-        for (int j = -2; j < s.m; ++j) {
+        for (int j = -2; j < s.m && ok; ++j) {
             // page numbers are fetched a block ahead
-            int n_row = 0, n_plane = a.planes;
-            const int xb = (s.kb + j + 2) * T::BN + (mine << box_shift);
-            if (mine < boxes && xb < s.span) {
-                const int key = span_key(s, xb);
-                n_row = s.k0 + key;
-                n_plane = plane;
-                if (PAGED) {
-                    const unsigned at = (unsigned)key / (unsigned)a.page_size;
-                    const int page = a.block_table[(size_t)s.b * a.max_pages + at];
-                    n_row = key - (int)at * a.page_size;
-                    n_plane = (unsigned)page < (unsigned)a.num_pages ? page * a.Hkv + s.hk : a.planes;
+            int n_row[2] = {0, 0}, n_plane[2] = {a.planes, a.planes};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int box = lane + 32 * e;
+                const int xb = (s.kb + j + 2) * T::BN + (box << box_shift);
+                if (box < boxes && xb < s.span) {
+                    const int key = span_key(s, xb);
+                    n_row[e] = s.k0 + key;
+                    n_plane[e] = plane;
+                    if (PAGED) {
+                        const unsigned at = (unsigned)key / (unsigned)a.page_size;
+                        const int page = a.block_table[(size_t)s.b * a.max_pages + at];
+                        n_row[e] = key - (int)at * a.page_size;
+                        n_plane[e] =
+                            (unsigned)page < (unsigned)a.num_pages ? page * a.Hkv + s.hk : a.planes;
+                    }
                 }
             }
             if (j >= -1) {
@@ -490,21 +489,24 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                     const int x1 = x0 + T::BN;
                     const bool in_boxes = PAGED || (MODE == kSpanWindow && x1 < s.head && x1 + T::BN > s.head);
 #pragma unroll 1
-                    for (int c = 0; c < T::KP; ++c) {
-                        if (!(ok = acquire())) break;
+                    for (int c = 0; c < T::KP && ok; ++c) {
+                        if (!acquire()) continue;
                         if (in_boxes) {
-                            if (k_mine) {
+#pragma unroll 1
+                            for (int box = lane; box < boxes; box += 32) {
+                                const uint32_t to = dst + ((uint32_t)(box << box_shift) << 7);
+                                const int y = box < 32 ? k_row[0] : k_row[1];
+                                const int z = box < 32 ? k_plane[0] : k_plane[1];
 #pragma unroll
                                 for (int q = 0; q < T::KCH; ++q) {
                                     const int col = (c * T::KCH + q) * 64;
-                                    const uint32_t to = dst + k_off + q * T::KCHUNK;
                                     if (!paired)
-                                        tma_load_3d(to, &tm.k_box, col, k_row, k_plane, bar);
-                                    else if (((mine * T::KCH + q) & 1) == rank)
-                                        tma_load_3d_multicast(to, &tm.k_box, col, k_row, k_plane, bar, 3);
+                                        tma_load_3d(to + q * T::KCHUNK, &tm.k_box, col, y, z, bar);
+                                    else if (((box * T::KCH + q) & 1) == rank)
+                                        tma_load_3d_multicast(to + q * T::KCHUNK, &tm.k_box, col, y, z, bar, 3);
                                 }
                             }
-                        } else if (lane == 0) {
+                        } else if (one) {
                             const int row = s.k0 + span_key(s, x1);
 #pragma unroll
                             for (int q = 0; q < T::KCH; ++q) {
@@ -518,25 +520,29 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                             }
                         }
                     }
-                    if (!ok) break;
                 }
                 if (j >= 0) {
 #pragma unroll 1
-                    for (int h = 0; h < T::VP; ++h) {
+                    for (int h = 0; h < T::VP && ok; ++h) {
                         const int xv = x0 + h * T::VKEYS;
-                        if (!(ok = acquire())) break;
+                        if (!acquire()) continue;
                         if (PAGED || (MODE == kSpanWindow && xv < s.head && xv + T::VKEYS > s.head)) {
-                            if (v_mine && v_slot == h) {
+#pragma unroll 1
+                            for (int box = lane; box < boxes; box += 32) {
+                                if (box >> vboxes_shift != h) continue;
+                                const uint32_t to =
+                                    dst + ((uint32_t)((box - (h << vboxes_shift)) << box_shift) << 7);
+                                const int y = box < 32 ? v_row[0] : v_row[1];
+                                const int z = box < 32 ? v_plane[0] : v_plane[1];
 #pragma unroll
                                 for (int q = 0; q < T::NCH; ++q) {
-                                    const uint32_t to = dst + v_off + q * T::VCHUNK;
                                     if (!paired)
-                                        tma_load_3d(to, &tm.v_box, q * 64, v_row, v_plane, bar);
-                                    else if (((mine * T::NCH + q) & 1) == rank)
-                                        tma_load_3d_multicast(to, &tm.v_box, q * 64, v_row, v_plane, bar, 3);
+                                        tma_load_3d(to + q * T::VCHUNK, &tm.v_box, q * 64, y, z, bar);
+                                    else if (((box * T::NCH + q) & 1) == rank)
+                                        tma_load_3d_multicast(to + q * T::VCHUNK, &tm.v_box, q * 64, y, z, bar, 3);
                                 }
                             }
-                        } else if (lane == 0) {
+                        } else if (one) {
                             const int row = s.k0 + span_key(s, xv);
                             if (!paired) {
 #pragma unroll
@@ -553,20 +559,23 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                             }
                         }
                     }
-                    if (!ok) break;
                 }
             }
-            v_row = k_row;
-            v_plane = k_plane;
-            k_row = n_row;
-            k_plane = n_plane;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                v_row[e] = k_row[e];
+                v_plane[e] = k_plane[e];
+                k_row[e] = n_row[e];
+                k_plane[e] = n_plane[e];
+            }
         }
     }
-    // every copy issued must have landed before the CTA exits (part 0 counts
-    // the bytes of both), and every arrival from the other CTA of a cluster
-    if (part == 0 && lane == 0) {
+    // every copy issued must have landed before the CTA exits, and every arrival
+    // from the other CTA of a cluster (of the last use of each slot)
+    if (one) {
 #pragma unroll 1
         for (int q = used > T::NSLOT ? used - T::NSLOT : 0; q < used; ++q) {
+            if ((q & 1) != part) continue;
             mbar_wait_drain(bars + ring_slot<T>(q) * 8, ring_phase<T>(q), a.wait_limit_ns);
             if (paired)
                 mbar_wait_drain(bars + empty_off + ring_slot<T>(q) * 8, ring_phase<T>(q),
@@ -574,6 +583,12 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
         }
     }
     __syncwarp();
+}
+
+// Whether the block of positions x0 on holds values that must be zeroed.
+template <class T>
+__device__ __forceinline__ bool span_zeroes(const SpanArgs& a, const SpanItem& s, int x0) {
+    return s.end < x0 + T::BN || (x0 < s.gap && x0 + T::BN > a.first);
 }
 
 // MMA issue (one lane): S(J+1), then PV(J), as in the 256-key prefill kernel.
@@ -630,6 +645,15 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
                     ok = false;
                     break;
                 }
+                // the correction warps have the row maxima of S(J - 2), in whose
+                // place those of S(J) will be written
+                if (J > 1 &&
+                    !mbar_wait_lane(smem_u32(&aux->bar_corrected[J & 1]),
+                                    (uint32_t)(((J - 2) >> 1) & 1), wc,
+                                    kErrWaitTimeout | kSiteMmaSfree)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 trace_mark(tr, kTrMma, J, 1);
 #pragma unroll
@@ -659,6 +683,15 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
                 break;
             }
             trace_mark(tr, kTrMma, J, 4);
+            // O rebased, values zeroed (the first block of a segment needs
+            // neither as a rule, and the correction warps may still be busy with
+            // the last segment's end; its odrained orders their arrivals)
+            if ((j > 0 || span_zeroes<T>(a, s, s.kb * T::BN)) &&
+                !mbar_wait_lane(smem_u32(&aux->bar_corrected[J & 1]), (uint32_t)((J >> 1) & 1), wc,
+                                kErrWaitTimeout | kSiteMmaP)) {
+                ok = false;
+                break;
+            }
             if (j == 0 && kq > 0 &&   // the previous segment's O has been read out
                 !mbar_wait_lane(smem_u32(&aux->bar_odrained), (uint32_t)((kq - 1) & 1), wc,
                                 kErrWaitTimeout | kSiteMmaOdrained)) {
@@ -850,10 +883,11 @@ __device__ bool span_softmax_segment(int h, const SpanArgs& a, const SpanItem& s
 
 // Sum and max (log2 units) of a row with its head's sink logit, one more term
 // without a value.  Returns what O (in basis m) is multiplied by.
-__device__ __forceinline__ float span_normaliser(const float* sinks, int h, float& l, float& m) {
+// (sink: the logit of the row's head, -inf without sinks).
+__device__ __forceinline__ float span_normaliser(float sink, float& l, float& m) {
     float scale = 1.f;
-    if (sinks != nullptr) {
-        const float sg = sinks[h] * kLog2e;
+    if (sink != -INFINITY) {
+        const float sg = sink * kLog2e;
         const float m2 = fmaxf(m, sg);
         if (m2 == -INFINITY) return 0.f;
         scale = (m == -INFINITY) ? 0.f : ex2_approx(m - m2);
@@ -871,7 +905,7 @@ __device__ __forceinline__ float span_normaliser(const float* sinks, int h, floa
 template <class T>
 __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs& a, bool have,
                                              bool real, size_t o_row, float inv_l,
-                                             uint32_t stage) {
+                                             uint32_t stage, uint32_t drained) {
     const int lane = threadIdx.x & 31;
     const unsigned rows = __ballot_sync(0xffffffffu, real);
     uint16_t* to[4];   // the rows (and columns) that this lane stores
@@ -881,31 +915,30 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
                 (size_t)__shfl_sync(0xffffffffu, (unsigned long long)o_row, k * 8 + (lane >> 2)) *
                     T::D_COLS +
                 (lane & 3) * 8;
+    uint32_t v[32];
+    tmem_ld32(lane_base + T::O_COL, v);
 #pragma unroll 1
     for (int c0 = 0; c0 < T::D_COLS; c0 += 32) {
-        uint32_t v[32];
-        if (have) {
-            tmem_ld32(lane_base + T::O_COL + c0, v);
-            tmem_wait_ld();
-        } else {
+        tmem_wait_ld();
+        uint32_t pk[16];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0u;
+        for (int e = 0; e < 16; ++e) {
+            const float2 y = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                                   make_float2(inv_l, inv_l), make_float2(0.f, 0.f));
+            pk[e] = have ? pack_bf16x2(y.x, y.y) : 0u;
+        }
+        if (c0 + 32 < T::D_COLS) {
+            tmem_ld32(lane_base + T::O_COL + c0 + 32, v);   // lands meanwhile
+        } else if (have) {   // O is free for the next segment
+            tc_fence_before();
+            mbar_arrive_warp(drained);
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 y = ffma2(make_float2(__uint_as_float(v[g * 8 + 2 * e]),
-                                                   __uint_as_float(v[g * 8 + 2 * e + 1])),
-                                       make_float2(inv_l, inv_l), make_float2(0.f, 0.f));
-                pk[e] = pack_bf16x2(y.x, y.y);
-            }
+        for (int g = 0; g < 4; ++g)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                              stage + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)),
-                         "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                         "r"(pk[4 * g]), "r"(pk[4 * g + 1]), "r"(pk[4 * g + 2]), "r"(pk[4 * g + 3])
                          : "memory");
-        }
         __syncwarp();
         uint4 x[4];
 #pragma unroll
@@ -969,10 +1002,14 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, in
         // first keys and the window, may hold anything, and zero times a
         // non-finite value would poison O: zeroed here, before PV(J) is let go
         const int x0 = (s.kb + j) * T::BN;
-        if (s.end < x0 + T::BN || (x0 < s.gap && x0 + T::BN > a.first)) {
+        if (span_zeroes<T>(a, s, x0)) {
             // (V_j's slots come after K_{j+1}'s)
             int pv = p0 + j * (T::KP + T::VP) + (j + 1 < s.m ? 2 : 1) * T::KP;
-            bool landed = true;
+            // (the slots' contents before V_j are at most V_{j-1}: past that, full
+            // means V_j)
+            bool landed = j == 0 || mbar_wait(smem_u32(&aux->bar_pv_done[(J - 1) & 1]),
+                                              (uint32_t)(((J - 1) >> 1) & 1), wc,
+                                              kErrWaitTimeout | kSiteCorrPv);
 #pragma unroll 1
             for (int hh = 0; hh < T::VP && landed; ++hh, ++pv) {
                 const int xv = x0 + hh * T::VKEYS;   // first position of the slot
@@ -995,55 +1032,60 @@ __device__ bool span_correction_segment(const SpanArgs& a, const SpanItem& s, in
             fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive_warp(smem_u32(&aux->bar_p_ready[sb]));
+        mbar_arrive_warp(smem_u32(&aux->bar_corrected[sb]));
     }
+    // (what the end needs from memory, while the last PV runs)
+    int head;
+    size_t o_row, lse_at;
+    const bool real =
+        span_row<T, MODE>(a, s.cap, s.q0, s.b, s.hk, s.tile, r, g, gp, head, o_row, lse_at);
+    const float sink = a.sinks != nullptr && real ? a.sinks[head] : -INFINITY;
     float l = 0.f, m = m_run;
+    const int Jl = J0 + s.m - 1;
     if (s.m > 0) {   // (else a unit, or a piece of one, without keys)
         if (!mbar_wait(smem_u32(&aux->bar_fin), (uint32_t)(kq & 1), wc,
                        kErrWaitTimeout | kSiteEpiMbox))
             return false;
         l = aux->mb_l[0][r] + aux->mb_l[1][r];
-        const int Jl = J0 + s.m - 1;
         if (!mbar_wait(smem_u32(&aux->bar_pv_done[Jl & 1]), (uint32_t)((Jl >> 1) & 1), wc,
                        kErrWaitTimeout | kSiteEpiPv))
             return false;
         tc_fence_after();
         trace_mark(tr, kTrCorr, Jl, 0);
     }
-    int head;
-    size_t o_row, lse_at;
-    const bool real =
-        span_row<T, MODE>(a, s.cap, s.q0, s.b, s.hk, s.tile, r, g, gp, head, o_row, lse_at);
+    const uint32_t drained = smem_u32(&aux->bar_odrained);
     if (s.n < s.nb) {   // a piece
         const int slot = 2 * (int)blockIdx.x + (s.index > 0);
         float4* po = reinterpret_cast<float4*>(a.part_o + (size_t)slot * (T::D_COLS * T::BM));
 #pragma unroll 1
-        for (int c32 = 0; c32 < (s.m > 0 ? T::D_COLS / 32 : 0); ++c32) {
-            uint32_t v[32];
-            tmem_ld32(lane_base + T::O_COL + c32 * 32, v);
+        for (int c64 = 0; c64 < (s.m > 0 ? T::D_COLS / 64 : 0); ++c64) {
+            uint32_t v[2][32];
+            tmem_ld64(lane_base + T::O_COL + c64 * 64, v);
             tmem_wait_ld();
+            if (c64 == T::D_COLS / 64 - 1) {
+                tc_fence_before();
+                mbar_arrive_warp(drained);
+            }
             if (!real) continue;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                po[(size_t)(c32 * 8 + q) * T::BM + r] =
-                    make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+            for (int q = 0; q < 16; ++q) {
+                const uint32_t* x = &v[q >> 3][4 * (q & 7)];
+                po[(size_t)(c64 * 16 + q) * T::BM + r] =
+                    make_float4(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
+                                __uint_as_float(x[3]));
+            }
         }
         float* ml = a.part_ml + (size_t)slot * 2 * T::BM;
         ml[r] = m;
         ml[T::BM + r] = l;
         if (r == 0) a.head[slot] = make_int4(s.b, s.u, s.n, s.kb == 0 ? s.nb : 0);
     } else {
-        const float inv_l = span_normaliser(real ? a.sinks : nullptr, head, l, m);
-        span_store_o<T>(lane_base, a, s.m > 0, real, o_row, inv_l, 
-                        sRing + T::SMEM_RING + T::SMEM_AUX + (warp & 3) * T::STAGE);
+        const float inv_l = span_normaliser(sink, l, m);
+        span_store_o<T>(lane_base, a, s.m > 0, real, o_row, inv_l,
+                        sRing + T::SMEM_RING + T::SMEM_AUX + (warp & 3) * T::STAGE, drained);
         if (real) a.lse[lse_at] = l > 0.f ? (m + lg2_approx(l)) * kLn2 : -INFINITY;
     }
-    if (s.m > 0) {
-        tc_fence_before();
-        mbar_arrive_warp(smem_u32(&aux->bar_odrained));
-        trace_mark(tr, kTrCorr, J0 + s.m - 1, 1);
-    }
+    if (s.m > 0) trace_mark(tr, kTrCorr, Jl, 1);
     return true;
 }
 
@@ -1064,7 +1106,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         mbar_init(smem_u32(&aux->bar_q), 1);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(smem_u32(&aux->bar_item[i]), 1);
-            mbar_init(smem_u32(&aux->bar_item_read[i]), PAGED ? 15 : 14);   // warps that read it
+            mbar_init(smem_u32(&aux->bar_item_read[i]), 15);   // warps that read it
         }
         for (int i = 0; i < T::NSLOT; ++i) {
             mbar_init(smem_u32(&aux->bar_full[i]), 1);
@@ -1073,7 +1115,8 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         mbar_init(smem_u32(&aux->bar_s_full), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&aux->bar_xm[i]), 8);
-            mbar_init(smem_u32(&aux->bar_p_ready[i]), 12);
+            mbar_init(smem_u32(&aux->bar_p_ready[i]), 8);
+            mbar_init(smem_u32(&aux->bar_corrected[i]), 4);
             mbar_init(smem_u32(&aux->bar_pv_done[i]), 1);
         }
         mbar_init(smem_u32(&aux->bar_fin), 8);
@@ -1137,7 +1180,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
             span_mma_role<T, MODE>(a, aux, tmem, sQ, sRing, wc, tr);
         else if (warp == T::ITEM_WARP)
             span_item_role<T, MODE>(tm, a, aux, sQ, wc);
-        else if (warp == T::LOAD_WARP || (PAGED && warp == T::LOAD2_WARP))
+        else if (warp == T::LOAD_WARP || warp == T::LOAD2_WARP)
             span_load_role<T, MODE, PAGED>(warp == T::LOAD_WARP ? 0 : 1, tm, a, aux, sRing, wc, tr);
     }
     tc_fence_before();
@@ -1214,7 +1257,7 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
             }
         }
     }
-    const float inv_l = span_normaliser(a.sinks, h, L, M);
+    const float inv_l = span_normaliser(a.sinks != nullptr ? a.sinks[h] : -INFINITY, L, M);
     uint4* dst = reinterpret_cast<uint4*>(a.o + o_row * D + c16 * 16);
 #pragma unroll
     for (int g = 0; g < 2; ++g)
