@@ -1202,21 +1202,17 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     wait_for_previous();
     const int r = threadIdx.x, c16 = blockIdx.y, G = gridDim.x;
     const int step = a.group_ctas;
+    // (what the pieces' addresses need, in one latency)
     int slot = 2 * blockIdx.x;
-    int4 hd = a.head[slot];
-    if (!(hd.z > 0 && hd.w > hd.z)) hd = a.head[++slot];
+    const int4 h0 = a.head[slot], h1 = a.head[slot + 1];
+    const int quota = a.head[2 * G].x;
+    const bool second = !(h0.z > 0 && h0.w > h0.z);
+    const int4 hd = second ? h1 : h0;
+    slot += second;
     if (!(hd.z > 0 && hd.w > hd.z)) return;
     const int b = hd.x, u = hd.y, nb = hd.w;
     if ((unsigned)b >= (unsigned)a.B) return;
-    const SpanSeq seq = span_seq<MODE>(a, b);
-    if ((unsigned)u >= (unsigned)span_units<MODE>(a, seq)) return;
-    const int groups = span_groups<MODE>(a, seq);
-    const int tile = u % groups * step + (int)blockIdx.x % step;
-    int h;
-    size_t o_row, lse_at;
-    const int g = MODE == kSpanWindow ? r / a.P : 0, gp = MODE == kSpanWindow ? r % a.P : 0;
-    if (!span_row<T, MODE>(a, seq.cap, seq.q0, b, u / groups, tile, r, g, gp, h, o_row, lse_at))
-        return;
+    const SpanSeq seq = span_seq<MODE>(a, b);   // (its loads run with the pieces')
     float M = -INFINITY, L = 0.f;
     float acc[16];
 #pragma unroll
@@ -1224,7 +1220,6 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
     // the pieces: hd.z blocks here, then a full CTA's share each, as the first
     // segments of the next CTAs (their number is known without reading them,
     // so that four at a time are in flight)
-    const int quota = a.head[2 * G].x;
     const int pieces = min(1 + (nb - hd.z + quota - 1) / max(quota, 1), (G - (int)blockIdx.x + step - 1) / step);
     for (int k0 = 0; k0 < pieces; k0 += 4) {
         float mk[4], lk[4];
@@ -1257,6 +1252,14 @@ __global__ void __launch_bounds__(128) span_combine_kernel(const SpanArgs a) {
             }
         }
     }
+    if ((unsigned)u >= (unsigned)span_units<MODE>(a, seq)) return;
+    const int groups = span_groups<MODE>(a, seq);
+    const int tile = u % groups * step + (int)blockIdx.x % step;
+    int h;
+    size_t o_row, lse_at;
+    const int g = MODE == kSpanWindow ? r / a.P : 0, gp = MODE == kSpanWindow ? r % a.P : 0;
+    if (!span_row<T, MODE>(a, seq.cap, seq.q0, b, u / groups, tile, r, g, gp, h, o_row, lse_at))
+        return;
     const float inv_l = span_normaliser(a.sinks != nullptr ? a.sinks[h] : -INFINITY, L, M);
     uint4* dst = reinterpret_cast<uint4*>(a.o + o_row * D + c16 * 16);
 #pragma unroll
