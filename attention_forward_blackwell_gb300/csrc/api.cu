@@ -231,9 +231,24 @@ struct Tree {
 // 1.2-3.9x faster for every batch from 1 to 16 at 32 to 128 rows.
 constexpr int kDecodeToPrefillRows = 32;
 
-// Keys of a window (and its first keys) from which a dense prompt does not run
-// the span kernel.
-constexpr long long kWindowDenseKeys = 512;
+// Whether a dense prompt of a window whose first keys stay visible runs the span
+// kernel (true) or the two-tile and one-tile kernels, whose units are longer: a
+// key/value head's query heads share the span kernel's tiles and their keys, so
+// it wins where the window is short or the group large, in long work.  us,
+// two-tile / span, window 256, 512, 1,024, 2,048 of 4 first keys:
+//  2 x 16 heads x 4,096, group 1
+//    d 64     60 /  46    68 /  56    77 /  79    96 / 110
+//    d 128    68 /  60    77 /  84    89 / 103   112 / 138
+//    d 256    86 /  94    96 / 114   124 / 161   169 / 230   (100: 86 / 69)
+//  32 heads x 8,192, group 4
+//    d 64    107 /  93   130 / 109   157 / 141   208 / 205
+//    d 128   120 /  96   144 / 119   179 / 156   241 / 230
+//    d 256   169 / 107   178 / 142   238 / 219   354 / 353
+//  4 x 8 heads x 1,000, group 8 (less than a wave)
+//    d 128    21 /  23    24 /  24    23 /  32    24 /  32
+bool span_wins_prompt(int head_dim, int group, long long rows, long long keys) {
+    return rows >= (64 << 10) && keys < (group >= 4 ? 1100 : 49152 / head_dim);
+}
 
 // Splits of the split-KV kernel over `span` keys of `pairs` (batch entry, kv
 // head, 16 query rows): enough CTAs to keep in flight, of at least 256 keys.
@@ -583,11 +598,9 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
         return from_cuda(launch_fill_empty(static_cast<uint16_t*>(o), lse, rows, head_dim, sinks,
                                            hq, vl ? vl->total_q : sq, s));
     }
-    // (dense prompts with longer windows: the two-tile and one-tile kernels
-    // below, whose units are longer, are faster -- 2 x 16 x 4,096 rows at head_dim
-    // 128, window 1,024: 88 against 94 us, at head_dim 256 67 against 90; window
-    // 256: 68 against 60)
-    if (window > 0 && first > 0 && (vl || (long long)window + first < kWindowDenseKeys) &&
+    if (window > 0 && first > 0 &&
+        (vl || span_wins_prompt(head_dim, hq / hkv, (long long)batch * hq * sq,
+                                (long long)window + first)) &&
         span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size))
         return span_impl(nullptr, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,

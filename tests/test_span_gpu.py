@@ -100,6 +100,10 @@ PREFILL = [
     (1, 4, 1, 150, 600, 128, 64, 16, False),
     (40, 2, 1, 30, 60, 64, 10, 3, True),           # many sequences
     (1, 2, 1, 4000, 4000, 64, 128, 64, True),      # a long line of blocks
+    (70, 8, 2, 120, 1300, 128, 50, 20, True),      # many rows
+    (12, 8, 2, 700, 700, 64, 100, 4, True),
+    (41, 16, 1, 110, 300, 256, 33, 3, True),
+    (66, 16, 1, 70, 300, 128, 130, 40, False),
 ]
 
 
