@@ -246,8 +246,20 @@ constexpr int kDecodeToPrefillRows = 32;
 //    d 256   169 / 107   178 / 142   238 / 219   354 / 353
 //  4 x 8 heads x 1,000, group 8 (less than a wave)
 //    d 128    21 /  23    24 /  24    23 /  32    24 /  32
-bool span_wins_prompt(int head_dim, int group, long long rows, long long keys) {
-    return rows >= (64 << 10) && keys < (group >= 4 ? 1100 : 49152 / head_dim);
+// Packed prompts of other lengths leave the two-tile kernels' units idle:
+//  8 x 16 heads x 200 to 1,024 after 0 to 3,000 keys, group 1
+//    d 64     51 /  41 *  63 /  46    73 /  60    86 /  70   (* window 100)
+//    d 128    58 /  52 *  72 /  69    85 /  78   100 /  89
+//    d 256    73 /  65 * 107 /  93   137 / 124   183 / 157
+//  2 x 32 heads x 4,000 to 8,000, group 4, pages of 128
+//    d 128   170 /  95 * 215 / 155   266 / 211   350 / 322
+//  4 x 8 heads x 200 to 1,000, group 8
+//    d 128    25 /  33 *  25 /  31    25 /  33    24 /  33
+bool span_wins_prompt(int head_dim, int group, long long rows, long long keys, bool packed,
+                      bool short_prompts) {
+    if (rows < (packed ? 32 << 10 : 64 << 10)) return false;
+    if (packed && (group >= 4 || short_prompts)) return true;
+    return keys < (group >= 4 ? 1100 : 49152 / head_dim);
 }
 
 // Splits of the split-KV kernel over `span` keys of `pairs` (batch entry, kv
@@ -599,8 +611,9 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
                                            hq, vl ? vl->total_q : sq, s));
     }
     if (window > 0 && first > 0 &&
-        (vl || span_wins_prompt(head_dim, hq / hkv, (long long)batch * hq * sq,
-                                (long long)window + first)) &&
+        span_wins_prompt(head_dim, hq / hkv, hq * (vl ? (long long)vl->total_q : (long long)batch * sq),
+                         (long long)window + first, vl != nullptr,
+                         vl && vl->total_q < 2048ll * batch) &&
         span_ok(head_dim, batch, hq, hkv, sq, sk, block_table, page_size))
         return span_impl(nullptr, q, k, v, o, lse, batch, hq, hkv, sq, sk, seqlens_k, head_dim, scale,
                          causal, window, first, sinks, block_table, max_pages, page_size, num_pages,

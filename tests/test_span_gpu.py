@@ -134,6 +134,11 @@ PACKED = [
     (4, 1, [(1, 50 + i) for i in range(60)] + [(90, 90)], 128, 128, 40, 6),
     (2, 2, [(3, 3 + i) for i in range(530)], 64, 0, 40, 6),
     (12, 4, [(300, 300), (41, 600)], 64, 128, 1000, 2000),
+    (32, 4, [(1100, 1400), (0, 5), (33, 900)], 128, 128, 300, 20),             # many rows
+    (32, 4, [(700, 700), (5, 900), (401, 555)], 128, 0, 30, 70),
+    (16, 16, [(513, 700), (300, 300), (1, 40), (900, 901), (500, 1300)], 64, 0, 200, 9),
+    (32, 8, [(300, 600), (290, 1000), (310, 310), (250, 400)], 256, 256, 90, 200),
+    (32, 16, [(300, 600), (290, 1000), (310, 310), (250, 400)], 256, 0, 500, 130),
 ]
 
 
