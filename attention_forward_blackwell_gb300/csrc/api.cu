@@ -423,7 +423,8 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         a.decode = decode ? 1 : 0;
         a.window = std::min(window, 1 << 30);
         a.first = std::min(first, sk);
-        a.head_keys = (a.first + a.box - 1) / a.box * a.box;
+        a.head_keys = (int)std::min<long long>(((long long)a.first + a.box - 1) / a.box * a.box,
+                                               0x7fffffff & -a.box);
         // a causal tile's axis: the first keys, the window of its first row
         // rounded down to a box, its other rows
         a.window_keys = (int)std::min<long long>(

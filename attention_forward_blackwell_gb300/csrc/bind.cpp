@@ -13,6 +13,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
@@ -111,6 +112,15 @@ float scale_of(PyObject* o, int64_t d) {
         throw BadType("scale must be a number");
     }
     return static_cast<float>(x);
+}
+
+int truth(const char* name, PyObject* o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) {
+        PyErr_Clear();
+        throw BadType(std::string(name) + " must be true or false");
+    }
+    return x;
 }
 
 void need_args(Py_ssize_t n, Py_ssize_t want) {
@@ -260,7 +270,7 @@ PyObject* decode_first(PyObject* const* a, Py_ssize_t n) {
     return c.result(fa_fwd_decode_first(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
         small(c.k.size(1)), c.n, small(c.k.size(2)), ints_or_null("seqlens_k", a[5], {c.B}, c.dev),
-        c.d, scale_of(a[3], c.d), PyObject_IsTrue(a[4]) == 1, whole("window", a[9]),
+        c.d, scale_of(a[3], c.d), truth("causal", a[4]), whole("window", a[9]),
         whole("first", a[11]), c.sinks, stream_of(a[8], c.dev)));
 }
 
@@ -274,7 +284,7 @@ PyObject* decode_paged_first(PyObject* const* a, Py_ssize_t n) {
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
         p.hkv, c.n, ints("seqlens_k", tensor("seqlens_k", a[4]), {c.B}, c.dev), p.table,
         p.max_pages, p.page_size, p.num_pages, c.d, scale_of(a[5], c.d),
-        PyObject_IsTrue(a[6]) == 1, whole("window", a[10]), whole("first", a[12]), c.sinks,
+        truth("causal", a[6]), whole("window", a[10]), whole("first", a[12]), c.sinks,
         stream_of(a[9], c.dev)));
 }
 
@@ -385,12 +395,14 @@ struct Caches {
 };
 
 // New rows [B, Hkv, n, d] of any strides that are multiples of 8 elements over
-// a contiguous last dimension; others are copied first.
+// a contiguous last dimension; others are copied first, on the call's stream
+// (whose pool the copy then belongs to: it may go as soon as the call is
+// enqueued).
 struct Rows {
     Tensor t;
     long long strides[3];
 
-    Rows(const char* name, PyObject* o, const Caches& c, int64_t B, int64_t n)
+    Rows(const char* name, PyObject* o, const Caches& c, int64_t B, int64_t n, fa_stream_t stream)
         : t(tensor(name, o)) {
         if (t.scalar_type() != at::kBFloat16 || !has_shape(t, {B, c.hkv, n, c.d}) || !on(t, c.dev))
             throw BadValue(std::string(name) + " must be a bf16 tensor " +
@@ -398,7 +410,14 @@ struct Rows {
         const bool fits = t.stride(3) == 1 &&
                           ((t.stride(0) | t.stride(1) | t.stride(2)) & 7) == 0 &&
                           (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0;
-        if (!fits) t = t.clone(at::MemoryFormat::Contiguous);
+        if (!fits) {
+            auto* const raw = reinterpret_cast<cudaStream_t>(stream);
+            const auto current = c10::cuda::getCurrentCUDAStream(c.dev);
+            const c10::cuda::CUDAStreamGuard guard(
+                raw == current.stream() ? current
+                                        : c10::cuda::getStreamFromExternal(raw, c.dev));
+            t = t.clone(at::MemoryFormat::Contiguous);
+        }
         for (int i = 0; i < 3; ++i) strides[i] = t.stride(i);
     }
 };
@@ -412,13 +431,14 @@ PyObject* cache_append(PyObject* const* a, Py_ssize_t n) {
     if (table.dim() != 2 || kn.dim() != 4)
         throw BadValue("block_table must be [B, max_pages], k_new and v_new [B, Hkv, n, d]");
     const int64_t B = table.size(0), m = kn.size(2);
-    const Rows k("k_new", a[4], c, B, m), v("v_new", a[5], c, B, m);
+    const fa_stream_t stream = stream_of(a[8], c.dev);
+    const Rows k("k_new", a[4], c, B, m, stream), v("v_new", a[5], c, B, m, stream);
     return PyLong_FromLong(fa_cache_append(
         c.k, c.v, c.num_pages, c.hkv, c.page_size, c.d,
         ints("block_table", table, {B, table.size(1)}, c.dev), small(table.size(1)),
         ints("seqlens", tensor("seqlens", a[3]), {B}, c.dev), small(B), k.t.data_ptr(), k.strides,
         v.t.data_ptr(), v.strides, small(m), ints_or_null("n_new", a[6], {B}, c.dev),
-        ints_or_null("copies", a[7], {B, 3}, c.dev), stream_of(a[8], c.dev)));
+        ints_or_null("copies", a[7], {B, 3}, c.dev), stream));
 }
 
 // k_cache, v_cache, copies, stream
