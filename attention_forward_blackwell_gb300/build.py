@@ -80,7 +80,7 @@ def _link_bind():
     libs = os.path.join(_torch()[0], "lib")
     tmp = BIND_PATH + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, os.path.join(OBJDIR, "bind.o"),
-           LIB_PATH, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           LIB_PATH, "-L", libs, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda",
            "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

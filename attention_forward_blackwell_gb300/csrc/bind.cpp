@@ -11,8 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -88,6 +87,13 @@ fa_stream_t stream_of(PyObject* handle, int dev) {
         throw BadType("stream must be a CUDA stream");
     }
     return static_cast<fa_stream_t>(p);
+}
+
+// A new contiguous tensor on the current device (without the dispatcher: 0.5 us
+// where at::empty takes 1.5).
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
+    return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)),
+                                  std::nullopt);
 }
 
 // Sizes beyond int are refused here rather than cut.
@@ -185,13 +191,13 @@ struct Attention {
             sinks = static_cast<const float*>(
                 dense("sinks", tensor("sinks", sinks_), at::kFloat, {Hq}, dev));
         if (out_ == Py_None) {
-            out = at::empty_like(q);
+            out = fresh(q.sizes(), at::kBFloat16, dev);
         } else {
             out = tensor("out", out_);
             dense("out", out, at::kBFloat16, {B, Hq, n, d}, dev);
         }
         if (lse_ == Py_None) {
-            lse = at::empty({B, Hq, n}, q.options().dtype(at::kFloat));
+            lse = fresh({B, Hq, n}, at::kFloat, dev);
         } else {
             lse = tensor("lse", lse_);
             dense("lse", lse, at::kFloat, {B, Hq, n}, dev);
@@ -295,7 +301,7 @@ PyObject* tree_mask(PyObject* const* a, Py_ssize_t n) {
     const int dev = device_of("parents", parents);
     if (parents.dim() != 2) throw BadValue("parents must be [B, T]");
     const int64_t B = parents.size(0), T = parents.size(1), W = (T + 31) / 32;
-    Tensor out = a[1] == Py_None ? at::empty({B, T, W}, parents.options().dtype(at::kInt))
+    Tensor out = a[1] == Py_None ? fresh({B, T, W}, at::kInt, dev)
                                  : tensor("out", a[1]);
     const fa_status st = fa_tree_mask(
         ints("parents", parents, {B, T}, dev),
@@ -309,7 +315,6 @@ PyObject* tree_mask(PyObject* const* a, Py_ssize_t n) {
 struct Table {
     int dev, num_pages, max_pages, batch;
     int *refs, *table, *lens;
-    at::TensorOptions options;
 
     Table(PyObject* refs_, PyObject* table_, PyObject* lens_) {
         const Tensor& t = tensor("block_table", table_);
@@ -322,10 +327,9 @@ struct Table {
         refs = ints("refs", r, {num_pages}, dev);
         table = ints("block_table", t, {batch, max_pages}, dev);
         lens = ints("seqlens", tensor("seqlens", lens_), {batch}, dev);
-        options = t.options().dtype(at::kInt);
     }
     Tensor status(PyObject* o) const {
-        Tensor t = o == Py_None ? at::empty({1}, options) : tensor("status", o);
+        Tensor t = o == Py_None ? fresh({1}, at::kInt, dev) : tensor("status", o);
         ints("status", t, {1}, dev);
         return t;
     }
@@ -351,7 +355,7 @@ PyObject* cache_reserve(PyObject* const* a, Py_ssize_t n) {
     const Table t(a[0], a[1], a[2]);
     const Tensor status = t.status(a[6]);
     const Tensor copies =
-        a[5] == Py_None ? at::empty({t.batch, 3}, t.options) : tensor("copies", a[5]);
+        a[5] == Py_None ? fresh({t.batch, 3}, at::kInt, t.dev) : tensor("copies", a[5]);
     const fa_status st = fa_cache_reserve(
         t.refs, t.num_pages, t.table, t.max_pages, t.lens, t.batch,
         ints("extra", tensor("extra", a[3]), {t.batch}, t.dev), whole("page_size", a[4]),
