@@ -71,6 +71,8 @@ struct TableArgs {
 
 // --------------------------------------------------------------- fork ----
 
+constexpr int kForkHeld = 4;   // table entries a lane keeps from pass 1 to pass 2
+
 // One cluster, a warp per pair.  Pass 1 checks the pairs; pass 2, if all
 // passed (the cluster's first CTA holds the verdict), copies the rows and
 // counts the pages.  A single CTA took 24 us for 256 pairs of 65 entries, each
@@ -92,15 +94,28 @@ __global__ void __cluster_dims__(CLUSTER ? 8 : 1, 1, 1) __launch_bounds__(kTable
     if (threadIdx.x == 0) bad = n;
     sync();
     int* verdict = CLUSTER ? cluster.map_shared_rank(&bad, 0) : &bad;
+    int held[kForkHeld];   // the first entries of the warp's first pair, for pass 2
+    int held_len = 0;
     for (int i = warp; i < n; i += warps) {
         const int s = src[i], d = dst[i];
         bool ok = (unsigned)s < (unsigned)t.batch && (unsigned)d < (unsigned)t.batch;
         if (ok) {
+            if (i == warp) {
+                const int* from = t.table + (size_t)s * t.max_pages;
+                held_len = t.lens[s];
+#pragma unroll
+                for (int k = 0; k < kForkHeld; ++k)
+                    held[k] = lane + 32 * k < t.max_pages ? from[lane + 32 * k] : -1;
+            }
             if (t.lens[d] > 0) ok = false;
+#pragma unroll 4
             for (int j = lane; j < t.max_pages; j += 32)   // dst holds nothing
-                if (is_page(t.table[(size_t)d * t.max_pages + j], t.num_pages)) ok = false;
-            for (int j = lane; j < n; j += 32)   // nor is any pair's src or an earlier dst
-                if (src[j] == d || (j < i && dst[j] == d)) ok = false;
+                ok &= !is_page(t.table[(size_t)d * t.max_pages + j], t.num_pages);
+#pragma unroll 4
+            for (int j = lane; j < n; j += 32) {   // nor is any pair's src or an earlier dst
+                const int sj = src[j], dj = dst[j];
+                ok &= sj != d && (j >= i || dj != d);
+            }
         }
         if (!__all_sync(0xffffffffu, ok) && lane == 0) atomicMin(verdict, i);
     }
@@ -111,13 +126,20 @@ __global__ void __cluster_dims__(CLUSTER ? 8 : 1, 1, 1) __launch_bounds__(kTable
         for (int i = warp; i < n; i += warps) {
             const int* from = t.table + (size_t)src[i] * t.max_pages;
             int* to = t.table + (size_t)dst[i] * t.max_pages;
-            for (int j = lane; j < t.max_pages; j += 32) {
-                const int e = from[j];
-                const bool held = is_page(e, t.num_pages);
-                to[j] = held ? e : -1;
-                if (held) atomicAdd(t.refs + e, 1);
+            auto share = [&](int j, int e) {
+                const bool page = is_page(e, t.num_pages);
+                to[j] = page ? e : -1;
+                if (page) atomicAdd(t.refs + e, 1);
+            };
+            int j0 = lane;
+            if (i == warp) {
+#pragma unroll
+                for (int k = 0; k < kForkHeld; ++k)
+                    if (lane + 32 * k < t.max_pages) share(lane + 32 * k, held[k]);
+                j0 += 32 * kForkHeld;
             }
-            if (lane == 0) t.lens[dst[i]] = t.lens[src[i]];
+            for (int j = j0; j < t.max_pages; j += 32) share(j, from[j]);
+            if (lane == 0) t.lens[dst[i]] = i == warp ? held_len : t.lens[src[i]];
         }
     }
     sync();   // the first CTA's shared memory stays until all have read it
@@ -151,11 +173,12 @@ struct Span {
 __device__ __forceinline__ Span reserve_span(const TableArgs& t, const int* extra, int page_size,
                                              int r) {
     Span s{0, 0, true};
-    const long long len = max(t.lens[r], 0), more = extra[r];
+    const unsigned len = (unsigned)max(t.lens[r], 0), page = (unsigned)page_size;
+    const int more = extra[r];
     if (more < 0) return s;
-    const long long last = (len + more + page_size - 1) / page_size;
-    s.fits = last <= t.max_pages;
-    s.first = (int)min(len / page_size, (long long)t.max_pages);
+    const unsigned end = len + (unsigned)more, last = end / page + (end % page != 0);   // (below 2^32)
+    s.fits = last <= (unsigned)t.max_pages;
+    s.first = (int)min(len / page, (unsigned)t.max_pages);
     s.last = s.fits ? (int)last : s.first;
     return s;
 }
@@ -221,6 +244,25 @@ __global__ void __launch_bounds__(kTableThreads)
     wait_for_previous();
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) long_row = t.batch;
+    // which of the kScanPages pages from p on are free
+    const bool wide = (reinterpret_cast<uintptr_t>(t.refs) & 15u) == 0;
+    auto free_pages = [&](int p) {
+        unsigned is_free = 0;
+        if (wide && p + kScanPages <= t.num_pages) {
+#pragma unroll
+            for (int q = 0; q < kScanPages / 4; ++q) {
+                const int4 x = *reinterpret_cast<const int4*>(t.refs + p + 4 * q);
+                is_free |= ((x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3)
+                           << (4 * q);
+            }
+        } else {
+            for (int q = 0; q < kScanPages && p + q < t.num_pages; ++q)
+                is_free |= (unsigned)(t.refs[p + q] == 0) << q;
+        }
+        return is_free;
+    };
+    // (the first ones with the rows' loads: nothing changes refs before pass 3)
+    const unsigned first_free = free_pages((int)threadIdx.x * kScanPages);
     __syncthreads();
     int needed = 0;
     for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
@@ -247,22 +289,10 @@ __global__ void __launch_bounds__(kTableThreads)
         block_scan(count, scratch, total);
         needed += total;
     }
-    const bool wide = (reinterpret_cast<uintptr_t>(t.refs) & 15u) == 0;
     int found = 0;
     for (int p0 = 0; p0 < t.num_pages && found < needed; p0 += kTableThreads * kScanPages) {
         const int p = p0 + (int)threadIdx.x * kScanPages;
-        unsigned is_free = 0;
-        if (wide && p + kScanPages <= t.num_pages) {
-#pragma unroll
-            for (int q = 0; q < kScanPages / 4; ++q) {
-                const int4 x = *reinterpret_cast<const int4*>(t.refs + p + 4 * q);
-                is_free |= ((x.x == 0) | (x.y == 0) << 1 | (x.z == 0) << 2 | (x.w == 0) << 3)
-                           << (4 * q);
-            }
-        } else {
-            for (int q = 0; q < kScanPages && p + q < t.num_pages; ++q)
-                is_free |= (unsigned)(t.refs[p + q] == 0) << q;
-        }
+        unsigned is_free = p0 == 0 ? first_free : free_pages(p);
         int total;
         int k = found + block_scan(__popc(is_free), scratch, total);
         for (; is_free != 0 && k < needed; is_free &= is_free - 1)
