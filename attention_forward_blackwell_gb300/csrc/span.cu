@@ -907,6 +907,13 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
                                              bool real, size_t o_row, float inv_l,
                                              uint32_t stage, uint32_t drained) {
     const int lane = threadIdx.x & 31;
+    if (!have) {   // a unit without keys
+        if (real)
+#pragma unroll 1
+            for (int c = 0; c < T::D_COLS; c += 8)
+                *reinterpret_cast<uint4*>(a.o + o_row * T::D_COLS + c) = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const unsigned rows = __ballot_sync(0xffffffffu, real);
     uint16_t* to[4];   // the rows (and columns) that this lane stores
 #pragma unroll
@@ -925,11 +932,11 @@ __device__ __forceinline__ void span_store_o(uint32_t lane_base, const SpanArgs&
         for (int e = 0; e < 16; ++e) {
             const float2 y = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
                                    make_float2(inv_l, inv_l), make_float2(0.f, 0.f));
-            pk[e] = have ? pack_bf16x2(y.x, y.y) : 0u;
+            pk[e] = pack_bf16x2(y.x, y.y);
         }
         if (c0 + 32 < T::D_COLS) {
             tmem_ld32(lane_base + T::O_COL + c0 + 32, v);   // lands meanwhile
-        } else if (have) {   // O is free for the next segment
+        } else {   // O is free for the next segment
             tc_fence_before();
             mbar_arrive_warp(drained);
         }
