@@ -685,7 +685,7 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
             trace_mark(tr, kTrMma, J, 4);
             // O rebased, values zeroed (the first block of a segment needs
             // neither as a rule, and the correction warps may still be busy with
-            // the last segment's end; its odrained orders their arrivals)
+            // the last segment's end)
             if ((j > 0 || span_zeroes<T>(a, s, s.kb * T::BN)) &&
                 !mbar_wait_lane(smem_u32(&aux->bar_corrected[J & 1]), (uint32_t)((J >> 1) & 1), wc,
                                 kErrWaitTimeout | kSiteMmaP)) {
