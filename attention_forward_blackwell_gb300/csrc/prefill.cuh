@@ -1322,11 +1322,23 @@ __device__ void prefill_softmax_role(int t, const CUtensorMap* tm_o, const Prefi
         if (masked) {
             const int nvis = lim - kv0 + 1;                  // visible columns [c0, nvis)
             const int c0 = WINDOW ? lo - kv0 : 0;
-            const int cf = WINDOW == 2 ? a.first - kv0 : 0;   // columns below it: first keys
+            [[maybe_unused]] const int cf = a.first - kv0;    // columns below it: first keys
+            if constexpr (WINDOW == 2) {
+                // 32 columns' visibility as a word: half the instructions of
+                // three comparisons a column
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-                s[c] = (c < nvis && (!WINDOW || c >= c0 || (WINDOW == 2 && c < cf))) ? s[c]
-                                                                                     : -INFINITY;
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t vis = low_bits(nvis - 32 * q) &
+                                         (low_bits(cf - 32 * q) | ~low_bits(c0 - 32 * q));
+#pragma unroll
+                    for (int c = 0; c < 32; ++c)
+                        s[32 * q + c] = ((vis >> c) & 1u) ? s[32 * q + c] : -INFINITY;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    s[c] = (c < nvis && (!WINDOW || c >= c0)) ? s[c] : -INFINITY;
+            }
         }
         // row max: four independent 3-input-max chains, then combine
         float mq[4];

@@ -483,6 +483,11 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Bits [0, n) of a word.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
 // ------------------------------------------------------- float helpers ----
 
 __device__ __forceinline__ float ex2_approx(float x) {

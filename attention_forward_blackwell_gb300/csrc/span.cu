@@ -741,11 +741,6 @@ __device__ __forceinline__ uint32_t tree_bits(const uint32_t* words, int nodes, 
     return __funnelshift_r(word(w), word(w + 1), (uint32_t)o & 31u);
 }
 
-// Bits [0, n) of a word.
-__device__ __forceinline__ uint32_t low_bits(int n) {
-    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
-}
-
 // Softmax of one segment by warpgroup h (keys [HK h, HK h + HK) of every
 // block; thread = row); see wide_softmax_unit.
 template <class T, int MODE>
