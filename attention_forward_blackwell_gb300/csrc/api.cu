@@ -231,35 +231,42 @@ struct Tree {
 // 1.2-3.9x faster for every batch from 1 to 16 at 32 to 128 rows.
 constexpr int kDecodeToPrefillRows = 32;
 
-// Whether a dense prompt of a window whose first keys stay visible runs the span
-// kernel (true) or the two-tile and one-tile kernels, whose units are longer: a
-// key/value head's query heads share the span kernel's tiles and their keys, so
-// it wins where the window is short or the group large, in long work.  us,
-// two-tile / span, window 256, 512, 1,024, 2,048 of 4 first keys:
+// Whether a prompt of a window whose first keys stay visible, of `rows` query
+// rows of all heads and `keys` keys of window and first keys, runs the span
+// kernel (true) or the two-tile and one-tile kernels.  A key/value head's query
+// heads share the span kernel's tiles and their keys, so it wins where the group
+// is large and the window short, and where packed prompts of other lengths leave
+// the other kernels' units idle; their units are longer, and start faster, so
+// they win in long windows and in little work.  us, two-tile / span, window 100,
+// 512, 1,024, 2,048 of 4 first keys:
 //  2 x 16 heads x 4,096, group 1
-//    d 64     60 /  46    68 /  56    77 /  79    96 / 110
-//    d 128    68 /  60    77 /  84    89 / 103   112 / 138
-//    d 256    86 /  94    96 / 114   124 / 161   169 / 230   (100: 86 / 69)
+//    d 64     47 /  48    56 /  55    66 /  79    87 / 110
+//    d 128    54 /  61    67 /  84    80 / 104   103 / 138
+//    d 256    69 /  69    89 / 113   120 / 161   165 / 230
 //  32 heads x 8,192, group 4
-//    d 64    107 /  93   130 / 109   157 / 141   208 / 205
-//    d 128   120 /  96   144 / 119   179 / 156   241 / 230
-//    d 256   169 / 107   178 / 142   238 / 219   354 / 353
-//  4 x 8 heads x 1,000, group 8 (less than a wave)
-//    d 128    21 /  23    24 /  24    23 /  32    24 /  32
-// Packed prompts of other lengths leave the two-tile kernels' units idle:
-//  8 x 16 heads x 200 to 1,024 after 0 to 3,000 keys, group 1
-//    d 64     51 /  41 *  63 /  46    73 /  60    86 /  70   (* window 100)
-//    d 128    58 /  52 *  72 /  69    85 /  78   100 /  89
-//    d 256    73 /  65 * 107 /  93   137 / 124   183 / 157
-//  2 x 32 heads x 4,000 to 8,000, group 4, pages of 128
-//    d 128   170 /  95 * 215 / 155   266 / 211   350 / 322
-//  4 x 8 heads x 200 to 1,000, group 8
-//    d 128    25 /  33 *  25 /  31    25 /  33    24 /  33
+//    d 64     79 /  65   103 / 111   135 / 140   186 / 204
+//    d 128    92 /  79   122 / 119   159 / 157   221 / 230
+//    d 256   112 / 111   154 / 142   219 / 218   333 / 355   (256: 124 / 107)
+//  packed, 8 x 32 heads x 200 to 1,024 after 0 to 3,000 keys, group 8, pages
+//    d 64     71 /  40    89 /  74   108 /  91   132 / 113
+//    d 128    84 /  54   106 /  83   127 / 108   156 / 129
+//    d 256   123 /  68   161 / 109   196 / 160   244 / 212
+//  packed, 2 x 32 heads x 4,000 to 8,000, group 4, pages
+//    d 64    121 /  81   157 / 143   202 / 203   278 / 299
+//    d 128   141 /  94   184 / 156   237 / 212   326 / 325
+//    d 256   217 / 141   293 / 196   389 / 346   553 / 582
+//  packed, 8 x 16 heads x 200 to 1,024 after 0 to 3,000 keys, group 1
+//    d 64     41 /  41    51 /  46    63 /  59    77 /  70
+//    d 128    49 /  53    61 /  68    75 /  78    92 /  89
+//    d 256    69 /  65   104 /  93   135 / 123   182 / 157
+//  4 x 8 heads x 1,000, group 8 (less than a wave); packed, 200 to 1,000
+//    d 128    20 /  26    21 /  27    23 /  32    22 /  32
+//    d 128    23 /  28    21 /  27    22 /  26    24 /  28
 bool span_wins_prompt(int head_dim, int group, long long rows, long long keys, bool packed,
                       bool short_prompts) {
-    if (rows < (packed ? 32 << 10 : 64 << 10)) return false;
-    if (packed && (group >= 4 || short_prompts)) return true;
-    return keys < (group >= 4 ? 1100 : 49152 / head_dim);
+    if (!packed) return rows >= (64 << 10) && group >= 4 && keys < (head_dim == 64 ? 200 : 600);
+    if (rows < (32 << 10)) return false;
+    return group >= 4 ? short_prompts || keys < 1100 : short_prompts && head_dim != 128;
 }
 
 // Splits of the split-KV kernel over `span` keys of `pairs` (batch entry, kv
