@@ -515,25 +515,43 @@ __global__ void __launch_bounds__(kRowThreads)
 
 // ---------------------------------------------------------- tree mask ----
 
+constexpr int kMaskThreads = 256;
+
 // Words of a tree's ancestor mask: node i sees itself and every node on the
 // way up, parent after parent (parents[i] < i; anything else ends the walk,
-// so a cycle cannot be followed).  A thread per (tree, node, word).
-__global__ void __launch_bounds__(256)
-    tree_mask_kernel(const int* parents, unsigned int* mask, int batch, int nodes, int words) {
+// so a cycle cannot be followed).  A thread per node walks once, word after word,
+// over parents in shared memory; a warp's rows are then written together.  Bound
+// by the walk of the deepest node: 64 trees of 1,024 nodes 9.1 us, chains 32
+// (a thread per word, each with a walk of its own in global memory: 15 and 739;
+// words written as the walk leaves them: 31 and 168).
+__global__ void __launch_bounds__(kMaskThreads)
+    tree_mask_kernel(const int* parents, unsigned int* mask, int nodes, int words) {
+    __shared__ int up[FA_TREE_MAX_NODES];
+    __shared__ unsigned int tile[kMaskThreads / 32][32][33];
     dependents_may_start();
     wait_for_previous();
-    const long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= (long long)batch * nodes * words) return;
-    const int w = (int)(e % words), i = (int)(e / words % nodes);
-    const int* p = parents + e / words / nodes * nodes;
-    unsigned int bits = 0;
-    for (int x = i; x >= 0;) {
-        if ((x >> 5) == w) bits |= 1u << (x & 31);
-        if ((x >> 5) < w) break;
-        const int up = p[x];
-        x = up < x ? up : -1;
+    const int* p = parents + (size_t)blockIdx.x * nodes;
+    const int i = blockIdx.y * blockDim.x + threadIdx.x;
+    const int last = min(nodes, (int)((blockIdx.y + 1) * blockDim.x));
+    for (int x = threadIdx.x; x < last; x += blockDim.x) {
+        const int v = p[x];
+        up[x] = v < x ? v : -1;
     }
-    mask[e] = bits;
+    __syncthreads();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int x = i < nodes ? i : -1;
+    for (int w = words - 1; w >= 0; --w) {
+        unsigned int bits = 0;
+        while (x >= w * 32) {
+            bits |= 1u << (x & 31);
+            x = up[x];
+        }
+        tile[warp][lane][w] = bits;
+    }
+    __syncwarp();
+    const int row0 = i - lane, n = min(32, nodes - row0) * words;
+    unsigned int* rows = mask + ((size_t)blockIdx.x * nodes + row0) * words;
+    for (int e = lane; e < n; e += 32) rows[e] = tile[warp][e / words][e % words];
 }
 
 // -------------------------------------------------------------- host ----
@@ -743,13 +761,13 @@ fa_status fa_tree_mask(const int* parents, unsigned int* mask, int batch, int no
     if (!parents || !mask) return FA_ERR_INVALID_ARG;
     if (!aligned4(parents) || !aligned4(mask)) return FA_ERR_MISALIGNED;
     const int words = (nodes + 31) / 32;
-    const long long blocks = ((long long)batch * nodes * words + 255) / 256;
-    if (blocks >= (1ll << 31)) return FA_ERR_INVALID_ARG;
     fa_status st = device_ok();
     if (st != FA_OK) return st;
-    return launched(launch_dependent(tree_mask_kernel, dim3((unsigned)blocks), dim3(256), 0,
-                                     reinterpret_cast<cudaStream_t>(stream), parents, mask, batch,
-                                     nodes, words));
+    const int threads = nodes < kMaskThreads ? (nodes + 31) / 32 * 32 : kMaskThreads;
+    return launched(launch_dependent(tree_mask_kernel,
+                                     dim3((unsigned)batch, (unsigned)((nodes + threads - 1) / threads)),
+                                     dim3((unsigned)threads), 0, reinterpret_cast<cudaStream_t>(stream),
+                                     parents, mask, nodes, words));
 }
 
 }  // extern "C"
