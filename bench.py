@@ -63,12 +63,12 @@ KERNEL_SOURCES = {
 
 CAPTURED_TRAFFIC = {
     # kernel: (sources sha256, workload, bytes per launch)
-    "prefill": ("2c87fe4f574f485b478774c76ac76c261f8ae7a5bb32e1582f47bd86ef6e07af",
-                "long_prefill_b1_h16_s8192_d128", 115617024),
-    # captured at batch 16 (463.73 MB, 1.017 x its algorithmic bytes) and
+    "prefill": ("3b5eb7e0547fd752e15fc60fff58d954f16dec0773c5746a899918cfa3512c5f",
+                "long_prefill_b1_h16_s8192_d128", 115342336),
+    # captured at batch 16 (463.42 MB, 1.016 x its algorithmic bytes) and
     # scaled to batch 64 by the algorithmic bytes of the two batches
-    "decode": ("4f0491259b04d4788454cb2e2704a1707995117770ea3398451eb287333e470e",
-               "decode_gqa_b64_hq64_hkv8_d128", 2205759804),
+    "decode": ("cca474b083978c75ce978c5524dfb2d6ca97959d2615b3fc7ab45f432f85a2a1",
+               "decode_gqa_b64_hq64_hkv8_d128", 2204292120),
 }
 
 
