@@ -51,7 +51,11 @@ struct DecodeTraits {
     static constexpr int SMEM = (WARPS * WARP_BYTES > MERGE_BYTES) ? WARPS * WARP_BYTES
                                                                    : MERGE_BYTES;
     static constexpr int NT = D / 8;                    // n8 tiles of O
-    static_assert(MERGE_BYTES + 16 * (D + 1) * 4 <= SMEM, "a joined split's rows must fit");
+    // joined splits: n of them give ceil(16 / n) rows each to every other, at
+    // most 21 rows in all; behind the ring, which a slower split still fills
+    static constexpr int JOIN_ROWS = 21;
+    static constexpr int JOIN_LSE = 128;                // bytes of the rows' LSE
+    static constexpr int JOIN_BYTES = JOIN_LSE + JOIN_ROWS * D * 4;
 };
 
 // byte offset of granule g of key row `key` inside a slice (XOR swizzle keeps
@@ -120,6 +124,7 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     const int k_lo = k_base + split * a.chunk;
     // a joined split stays for its cluster's barriers
     const bool joined = MODE != kModePlain && a.joined;
+    if (joined) cluster_arrive();   // (waited for before the first write to another)
     if (k_lo >= fs.span && !joined) return;      // nothing of this sequence here
     const int k_hi = min(k_lo + a.chunk, fs.span);
     const int nodes = MODE == kModeTree ? tree_nodes(a, b) : 0;
@@ -380,8 +385,11 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
     }
     __syncthreads();
     const int valid_rows = min(16, a.rows - rbase);
-    float* jl = reinterpret_cast<float*>(smem + T::MERGE_BYTES);   // joined: [16] LSE,
-    float* jo = jl + 16;                                           // [16][D] O
+    // joined: split s finishes the rows [s * own, (s + 1) * own); the others write
+    // theirs of them into its shared memory, [split][own] LSE and [split][own][D] O
+    const int own = joined ? (16 + a.n_splits - 1) / a.n_splits : 1;
+    const uint32_t jl = smem_u32(smem) + T::SMEM, jo = jl + T::JOIN_LSE;
+    if (joined) cluster_wait();
     for (int e = threadIdx.x * 4; e < valid_rows * D; e += T::THREADS * 4) {
         const int r = e / D, c = e % D;
         float M = -INFINITY;
@@ -409,18 +417,21 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
             o = make_float4(o.x / wsum, o.y / wsum, o.z / wsum, o.w / wsum);
             lse2 = M + lg2_approx(wsum);
         }
-        *reinterpret_cast<float4*>(joined ? jo + e : a.part_o + part * D + c) = o;
-        if (c == 0) *(joined ? jl + r : a.part_lse + part) = lse2;
+        if (joined) {
+            const int to = r / own, at = split * own + r - to * own;
+            cluster_write4(jo + (at * D + c) * 4, to, o);
+            if (c == 0) cluster_write(jl + at * 4, to, lse2);
+            continue;
+        }
+        *reinterpret_cast<float4*>(a.part_o + part * D + c) = o;
+        if (c == 0) a.part_lse[part] = lse2;
     }
     if constexpr (MODE != kModePlain) {
         if (!joined) return;
-        // the splits of these rows are the CTAs of the cluster: each finishes a
-        // share of the elements from all of them, in the order of the splits
         cluster_sync_all();
-        const uint32_t jl_at = smem_u32(jl), jo_at = smem_u32(jo);
-        for (int e = (split * T::THREADS + threadIdx.x) * 4; e < valid_rows * D;
-             e += T::THREADS * a.n_splits * 4) {
-            const int r = e / D, c = e % D;
+        for (int e = threadIdx.x * 4; e < own * D; e += T::THREADS * 4) {
+            const int q = e / D, c = e % D, r = split * own + q;
+            if (r >= valid_rows) break;
             const int pr = rbase + r;
             const int h = hkv * a.group + pr / a.Sq, qi_ = pr % a.Sq;
             if (MODE == kModeTree && qi_ >= nodes) continue;
@@ -431,8 +442,9 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
                 x[s] = -INFINITY;
                 y[s] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (s < a.n_splits) {
-                    x[s] = cluster_read(jl_at + 4 * r, s);
-                    y[s] = cluster_read4(jo_at + 4 * e, s);
+                    const uint8_t* from = smem + T::SMEM;
+                    x[s] = *reinterpret_cast<const float*>(from + (s * own + q) * 4);
+                    y[s] = *reinterpret_cast<const float4*>(from + T::JOIN_LSE + ((s * own + q) * D + c) * 4);
                 }
             }
             const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
@@ -458,7 +470,6 @@ __global__ void __launch_bounds__(DecodeTraits<D>::THREADS)
                 make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
             if (c == 0) a.lse[row] = wsum > 0.f ? (M + lg2_approx(wsum)) * kLn2f : -INFINITY;
         }
-        cluster_sync_all();   // shared memory stays until all have read it
     }
 }
 
@@ -533,8 +544,8 @@ cudaError_t launch_decode_mode(const DecodeArgs& a, cudaStream_t s) {
     using T = DecodeTraits<D>;
     void (*split)(DecodeArgs) = a.block_table != nullptr ? decode_split_kernel<D, true, MODE>
                                                          : decode_split_kernel<D, false, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         T::SMEM);
+    const int smem = T::SMEM + (MODE != kModePlain ? T::JOIN_BYTES : 0);
+    cudaError_t e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)a.n_splits, (unsigned)(a.Hkv * a.n_mtiles), (unsigned)a.B);
     const long long rows = (long long)a.B * a.Hq * a.Sq;
@@ -542,7 +553,7 @@ cudaError_t launch_decode_mode(const DecodeArgs& a, cudaStream_t s) {
     if constexpr (MODE != kModePlain) {
         if (a.joined)
             return launch_dependent_clusters(split, (unsigned)a.n_splits, grid, dim3(T::THREADS),
-                                             T::SMEM, s, a);
+                                             smem, s, a);
         e = launch_dependent(split, grid, dim3(T::THREADS), T::SMEM, s, a);
         if (e != cudaSuccess) return e;
         return launch_dependent(decode_combine_kernel<D, MODE>, dim3(combine_ctas), dim3(256), 0, s,

@@ -204,24 +204,27 @@ __device__ __forceinline__ void cluster_sync_all() {
         "barrier.cluster.arrive.release.aligned;\n\t"
         "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// The float that CTA `rank` of the cluster has at this CTA's address `addr`.
-__device__ __forceinline__ float cluster_read(uint32_t addr, int rank) {
-    float x;
-    asm volatile(
-        "{\n\t.reg .b32 at;\n\t"
-        "mapa.shared::cluster.u32 at, %1, %2;\n\t"
-        "ld.shared::cluster.f32 %0, [at];\n\t}"
-        : "=f"(x) : "r"(addr), "r"(rank) : "memory");
-    return x;
+// The same in two halves; the arrival orders nothing.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float4 cluster_read4(uint32_t addr, int rank) {
-    float4 x;
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// Writes to what lies at this CTA's address `addr` in CTA `rank` of the cluster.
+__device__ __forceinline__ void cluster_write(uint32_t addr, int rank, float x) {
     asm volatile(
         "{\n\t.reg .b32 at;\n\t"
-        "mapa.shared::cluster.u32 at, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [at];\n\t}"
-        : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(addr), "r"(rank) : "memory");
-    return x;
+        "mapa.shared::cluster.u32 at, %0, %1;\n\t"
+        "st.shared::cluster.f32 [at], %2;\n\t}" ::"r"(addr), "r"(rank), "f"(x) : "memory");
+}
+__device__ __forceinline__ void cluster_write4(uint32_t addr, int rank, float4 x) {
+    asm volatile(
+        "{\n\t.reg .b32 at;\n\t"
+        "mapa.shared::cluster.u32 at, %0, %1;\n\t"
+        "st.shared::cluster.v4.f32 [at], {%2, %3, %4, %5};\n\t}" ::"r"(addr), "r"(rank),
+        "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+        : "memory");
 }
 
 // Prefetch of a tile (the tensor map's box at these coordinates) into L2:
