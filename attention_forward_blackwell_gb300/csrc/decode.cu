@@ -21,11 +21,13 @@
 // normalised partial (O_s, LSE_s in log2 units).
 //
 // decode_combine_kernel: one warp per query row merges its splits.  Of a tree
-// or a window with first keys, few splits are one cluster instead, which reads
-// its parts from each other's shared memory and writes the rows itself
-// (DecodeArgs::joined): such calls are bound by latencies, of the launches and
-// of the chain of loads, not by bytes (a tree of 7 nodes over 1,000 keys x 16
-// heads at head_dim 64 6.5 us, 4.2 MB; a window of 1,024 over 8 heads at 128 6.5).
+// or a window with first keys, few splits are one cluster instead, in which each
+// CTA hands its parts of the others' rows over to their shared memory and writes
+// its own share of the rows (DecodeArgs::joined): such calls are bound by
+// latencies, of the launch, the chain of loads and one barrier of the cluster,
+// not by bytes (7 query heads x 1,000 keys x 16 heads at head_dim 64 6.2 us a
+// call, 4.2 MB; a window of 1,024 over 8 heads at 128 6.7; with parts read from
+// the others between two barriers 6.8 and 7.2).
 #include "common.cuh"
 #include "ptx.cuh"
 
