@@ -265,6 +265,13 @@ __device__ void span_item_role(const SpanMaps& tm, const SpanArgs& a, SpanAux* a
             left = min(quota, all - beg);
             if (blockIdx.x == 0 && lane == 0)   // (for the combine kernel)
                 a.head[2 * gridDim.x] = make_int4(quota, 0, 0, 0);
+            if (per == 1) {   // (no second pass)
+                if (at <= beg && beg < at + mine) {
+                    aux->start_b = b0;
+                    aux->start_off = beg - at;
+                }
+                break;
+            }
         }
     }
     __syncwarp();
