@@ -63,12 +63,12 @@ KERNEL_SOURCES = {
 
 CAPTURED_TRAFFIC = {
     # kernel: (sources sha256, workload, bytes per launch)
-    "prefill": ("3b5eb7e0547fd752e15fc60fff58d954f16dec0773c5746a899918cfa3512c5f",
-                "long_prefill_b1_h16_s8192_d128", 115342336),
-    # captured at batch 16 (463.42 MB, 1.016 x its algorithmic bytes) and
+    "prefill": ("ca8ce4fc495c8cf639e592fa7e41c5f9bc1c7ab5cd3e756b10f5caf1d1e82c4a",
+                "long_prefill_b1_h16_s8192_d128", 115318784),
+    # captured at batch 16 (463.37 MB, 1.016 x its algorithmic bytes) and
     # scaled to batch 64 by the algorithmic bytes of the two batches
-    "decode": ("cca474b083978c75ce978c5524dfb2d6ca97959d2615b3fc7ab45f432f85a2a1",
-               "decode_gqa_b64_hq64_hkv8_d128", 2204292120),
+    "decode": ("ccd599648da5bf7362660bbc0cec8064d7d58bbb3bbbf9b740dd3e00fb8d8580",
+               "decode_gqa_b64_hq64_hkv8_d128", 2204044931),
 }
 
 
