@@ -62,6 +62,9 @@ DECODE = [
     (8, 4, 1, spread(40, 0, 900), 128, 16, 600, 4, True, False),
     (8, 4, 2, spread(520, 0, 700), 64, 0, 600, 4, True, False),
     (128, 1, 2, [300, 77], 64, 0, 90, 33, True, False),           # one position a tile
+    (12, 2, 8, [700, 5, 410], 256, 32, 120, 10, True, True),      # six heads, 21 positions
+    (33, 3, 16, [1200, 333], 128, 0, 333, 1, True, False),
+    (7, 1, 16, [2000, 1, 0], 64, 48, 64, 200, False, False),
 ]
 
 
@@ -139,6 +142,9 @@ PACKED = [
     (16, 16, [(513, 700), (300, 300), (1, 40), (900, 901), (500, 1300)], 64, 0, 200, 9),
     (32, 8, [(300, 600), (290, 1000), (310, 310), (250, 400)], 256, 256, 90, 200),
     (32, 16, [(300, 600), (290, 1000), (310, 310), (250, 400)], 256, 0, 500, 130),
+    (24, 8, [(700, 900), (690, 700)], 64, 0, 150, 20),        # three heads a tile, 42 positions
+    (21, 7, [(800, 800), (1, 300), (777, 1000)], 256, 128, 90, 150),
+    (40, 8, [(500, 800), (420, 430)], 128, 128, 64, 5),       # five heads, 25 positions
 ]
 
 
