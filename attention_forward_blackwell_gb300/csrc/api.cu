@@ -189,6 +189,11 @@ fa_status check_common(const void* q, const void* k, const void* v, void* o, flo
 
 fa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
+// The window as the kernels take it: 0 without one, and no longer than the keys,
+// past which it hides nothing (a row stands at most at the last key), so that
+// first keys of windows stay in 32 bits.
+int window_of(int window, int keys) { return window > 0 ? std::max(1, std::min(window, keys)) : 0; }
+
 // Checks of the paged-cache arguments shared by prefill and decode.
 fa_status check_paged(const int* seqlens_k, const int* block_table, int max_pages, int page_size,
                       int num_pages, int batch, int hq, int sq) {
@@ -428,7 +433,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
     } else {
         a.causal = causal ? 1 : 0;
         a.decode = decode ? 1 : 0;
-        a.window = std::min(window, 1 << 30);
+        a.window = window_of(window, packed_k ? std::max(sk, vl->total_k) : sk);
         a.first = std::min(first, sk);
         a.head_keys = (int)std::min<long long>(((long long)a.first + a.box - 1) / a.box * a.box,
                                                0x7fffffff & -a.box);
@@ -558,7 +563,7 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     a.rows = rows;
     a.n_mtiles = (int)tiles;
     a.causal = causal ? 1 : 0;
-    a.window = window > 0 ? window : 0;
+    a.window = window_of(window, sk);
     a.first = window > 0 ? std::min(first, sk) : 0;
     if (tree) {
         a.tree_mask = tree->mask;
@@ -704,7 +709,7 @@ fa_status prefill_impl(const void* q, const void* k, const void* v, void* o, flo
     // whose 2048 short units each start with a DRAM round trip of a 64 KB Q
     // tile; no gain measured at the other head dimensions)
     a.q_prefetch = head_dim == 256 ? di->num_sms : 0;
-    a.window = window > 0 ? window : 0;
+    a.window = window_of(window, vl && !block_table ? std::max(sk, vl->total_k) : sk);
     a.first = window > 0 ? first : 0;
     a.sinks = sinks;
     a.block_table = block_table;

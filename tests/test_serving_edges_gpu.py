@@ -151,6 +151,32 @@ def test_wide_numbers(rows):
     assert status.item() == -2 and refs.tolist() == [1, 1, 0, 0]
 
 
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_windows_past_32_bits(d):
+    """The longest window a call can name, rows that stand before the first key."""
+    from attention_forward_blackwell_gb300 import binding
+    g = torch.Generator().manual_seed(d)
+    big = 2 ** 31 - 1
+    lens = [40, 3, 1, 0]
+    q, k, v = (torch.randn(*s, generator=g).bfloat16()
+               for s in ((4, 2, 40, d), (4, 1, 40, d), (4, 1, 40, d)))
+    want = ref.attention64(q, k, v, ref.window_seen(40, lens, 40, 0, 0, True), d ** -0.5)
+    for first in (0, 1, big):
+        o, lse = binding.prefill(q.cuda(), k.cuda(), v.cuda(), causal=True, seqlens_k=i32(lens),
+                                 window=big, first=first)
+        torch.cuda.synchronize()
+        ref.check(o, lse, want, f"prefill {first}")
+        if d == 512:
+            continue
+        qs = q[:, :, :9].contiguous()
+        o, lse = binding.decode(qs.cuda(), k.cuda(), v.cuda(), causal=True, seqlens_k=i32(lens),
+                                window=big, first=first)
+        torch.cuda.synchronize()
+        short = ref.attention64(qs, k, v, ref.window_seen(9, lens, 40, 0, 0, True), d ** -0.5)
+        ref.check(o, lse, short, f"decode {first}")
+    check_device_error()
+
+
 def test_another_device_is_refused():
     from attention_forward_blackwell_gb300 import binding
     q = torch.zeros(1, 2, 1, 64).bfloat16()
