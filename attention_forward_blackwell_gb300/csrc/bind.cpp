@@ -12,6 +12,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -78,22 +79,39 @@ int* ints_or_null(const char* name, PyObject* o, std::initializer_list<int64_t> 
     return o == Py_None ? nullptr : ints(name, tensor(name, o), shape, dev);
 }
 
-fa_stream_t stream_of(PyObject* handle, int dev) {
-    if (handle == Py_None)
-        return reinterpret_cast<fa_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
+// The stream of a call, and whether it is another than the current one.
+struct Stream {
+    fa_stream_t handle;
+    bool other;
+    operator fa_stream_t() const { return handle; }
+};
+Stream stream_of(PyObject* handle, int dev) {
+    const cudaStream_t current =
+        c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
+    if (handle == Py_None) return {reinterpret_cast<fa_stream_t>(current), false};
     void* p = PyLong_AsVoidPtr(handle);
     if (p == nullptr && PyErr_Occurred()) {
         PyErr_Clear();
         throw BadType("stream must be a CUDA stream");
     }
-    return static_cast<fa_stream_t>(p);
+    return {static_cast<fa_stream_t>(p), p != reinterpret_cast<void*>(current)};
 }
 
-// A new contiguous tensor on the current device (without the dispatcher: 0.5 us
-// where at::empty takes 1.5).
-Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev) {
-    return at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)),
-                                  std::nullopt);
+c10::cuda::CUDAStream torch_stream(const Stream& s, int dev) {
+    const auto d = static_cast<c10::DeviceIndex>(dev);
+    return s.other ? c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(s.handle), d)
+                   : c10::cuda::getCurrentCUDAStream(d);
+}
+
+// A new contiguous tensor for a call on `stream` (without the dispatcher: 0.5 us
+// where at::empty takes 1.5).  On a stream other than the current one the
+// allocator is told, so that the memory outlives that stream's work on it.
+Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev, const Stream& stream) {
+    Tensor t = at::detail::empty_cuda(
+        shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
+    if (stream.other && t.numel() > 0)
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), torch_stream(stream, dev));
+    return t;
 }
 
 // Sizes beyond int are refused here rather than cut.
@@ -171,9 +189,12 @@ struct Attention {
     int dev;
     int B, Hq, n, d;
 
+    Stream stream;
+
     Attention(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* sinks_, PyObject* out_,
-              PyObject* lse_)
-        : q(tensor("q", q_)), k(tensor("k", k_)), v(tensor("v", v_)), dev(device_of("q", q)) {
+              PyObject* lse_, PyObject* stream_)
+        : q(tensor("q", q_)), k(tensor("k", k_)), v(tensor("v", v_)), dev(device_of("q", q)),
+          stream(stream_of(stream_, dev)) {
         const char* names[3] = {"q", "k", "v"};
         const Tensor* all[3] = {&q, &k, &v};
         for (int i = 0; i < 3; ++i) {
@@ -191,13 +212,13 @@ struct Attention {
             sinks = static_cast<const float*>(
                 dense("sinks", tensor("sinks", sinks_), at::kFloat, {Hq}, dev));
         if (out_ == Py_None) {
-            out = fresh(q.sizes(), at::kBFloat16, dev);
+            out = fresh(q.sizes(), at::kBFloat16, dev, stream);
         } else {
             out = tensor("out", out_);
             dense("out", out, at::kBFloat16, {B, Hq, n, d}, dev);
         }
         if (lse_ == Py_None) {
-            lse = fresh({B, Hq, n}, at::kFloat, dev);
+            lse = fresh({B, Hq, n}, at::kFloat, dev, stream);
         } else {
             lse = tensor("lse", lse_);
             dense("lse", lse, at::kFloat, {B, Hq, n}, dev);
@@ -245,53 +266,52 @@ void same_batch(const Attention& c) {
 // q, k, v, tree_mask, scale, seqlens_k, tree_lens, sinks, out, lse, stream
 PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 11);
-    const Attention c(a[0], a[1], a[2], a[7], a[8], a[9]);
+    const Attention c(a[0], a[1], a[2], a[7], a[8], a[9], a[10]);
     same_batch(c);
     const TreeMask m(c, a[3], a[6]);
     return c.result(fa_fwd_decode_tree(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
         small(c.k.size(1)), c.n, small(c.k.size(2)), ints_or_null("seqlens_k", a[5], {c.B}, c.dev),
-        m.words, m.shared, m.lens, c.d, scale_of(a[4], c.d), c.sinks, stream_of(a[10], c.dev)));
+        m.words, m.shared, m.lens, c.d, scale_of(a[4], c.d), c.sinks, c.stream));
 }
 
 // q, k_cache, v_cache, block_table, seqlens_k, tree_mask, scale, tree_lens,
 // sinks, out, lse, stream
 PyObject* decode_tree_paged(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 12);
-    const Attention c(a[0], a[1], a[2], a[8], a[9], a[10]);
+    const Attention c(a[0], a[1], a[2], a[8], a[9], a[10], a[11]);
     const Pages p(c, a[3]);
     const TreeMask m(c, a[5], a[7]);
     return c.result(fa_fwd_decode_tree_paged(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
         p.hkv, c.n, ints("seqlens_k", tensor("seqlens_k", a[4]), {c.B}, c.dev), p.table,
         p.max_pages, p.page_size, p.num_pages, m.words, m.shared, m.lens, c.d,
-        scale_of(a[6], c.d), c.sinks, stream_of(a[11], c.dev)));
+        scale_of(a[6], c.d), c.sinks, c.stream));
 }
 
 // q, k, v, scale, causal, seqlens_k, out, lse, stream, window, sinks, first
 PyObject* decode_first(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 12);
-    const Attention c(a[0], a[1], a[2], a[10], a[6], a[7]);
+    const Attention c(a[0], a[1], a[2], a[10], a[6], a[7], a[8]);
     same_batch(c);
     return c.result(fa_fwd_decode_first(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
         small(c.k.size(1)), c.n, small(c.k.size(2)), ints_or_null("seqlens_k", a[5], {c.B}, c.dev),
         c.d, scale_of(a[3], c.d), truth("causal", a[4]), whole("window", a[9]),
-        whole("first", a[11]), c.sinks, stream_of(a[8], c.dev)));
+        whole("first", a[11]), c.sinks, c.stream));
 }
 
 // q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out, lse, stream,
 // window, sinks, first
 PyObject* decode_paged_first(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 13);
-    const Attention c(a[0], a[1], a[2], a[11], a[7], a[8]);
+    const Attention c(a[0], a[1], a[2], a[11], a[7], a[8], a[9]);
     const Pages p(c, a[3]);
     return c.result(fa_fwd_decode_paged_first(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
         p.hkv, c.n, ints("seqlens_k", tensor("seqlens_k", a[4]), {c.B}, c.dev), p.table,
         p.max_pages, p.page_size, p.num_pages, c.d, scale_of(a[5], c.d),
-        truth("causal", a[6]), whole("window", a[10]), whole("first", a[12]), c.sinks,
-        stream_of(a[9], c.dev)));
+        truth("causal", a[6]), whole("window", a[10]), whole("first", a[12]), c.sinks, c.stream));
 }
 
 // parents, out, stream
@@ -301,12 +321,12 @@ PyObject* tree_mask(PyObject* const* a, Py_ssize_t n) {
     const int dev = device_of("parents", parents);
     if (parents.dim() != 2) throw BadValue("parents must be [B, T]");
     const int64_t B = parents.size(0), T = parents.size(1), W = (T + 31) / 32;
-    Tensor out = a[1] == Py_None ? fresh({B, T, W}, at::kInt, dev)
+    const Stream stream = stream_of(a[2], dev);
+    Tensor out = a[1] == Py_None ? fresh({B, T, W}, at::kInt, dev, stream)
                                  : tensor("out", a[1]);
     const fa_status st = fa_tree_mask(
         ints("parents", parents, {B, T}, dev),
-        reinterpret_cast<unsigned int*>(ints("out", out, {B, T, W}, dev)), small(B), small(T),
-        stream_of(a[2], dev));
+        reinterpret_cast<unsigned int*>(ints("out", out, {B, T, W}, dev)), small(B), small(T), stream);
     return status_or(st, THPVariable_Wrap(out));
 }
 
@@ -328,8 +348,8 @@ struct Table {
         table = ints("block_table", t, {batch, max_pages}, dev);
         lens = ints("seqlens", tensor("seqlens", lens_), {batch}, dev);
     }
-    Tensor status(PyObject* o) const {
-        Tensor t = o == Py_None ? fresh({1}, at::kInt, dev) : tensor("status", o);
+    Tensor status(PyObject* o, const Stream& stream) const {
+        Tensor t = o == Py_None ? fresh({1}, at::kInt, dev, stream) : tensor("status", o);
         ints("status", t, {1}, dev);
         return t;
     }
@@ -340,12 +360,13 @@ PyObject* cache_fork(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 7);
     const Table t(a[0], a[1], a[2]);
     const Tensor& src = tensor("src", a[3]);
-    const Tensor status = t.status(a[5]);
+    const Stream stream = stream_of(a[6], t.dev);
+    const Tensor status = t.status(a[5], stream);
     const int64_t m = src.numel();
     const fa_status st = fa_cache_fork(
         t.refs, t.num_pages, t.table, t.max_pages, t.lens, t.batch, ints("src", src, {m}, t.dev),
         ints("dst", tensor("dst", a[4]), {m}, t.dev), small(m),
-        static_cast<int*>(status.data_ptr()), stream_of(a[6], t.dev));
+        static_cast<int*>(status.data_ptr()), stream);
     return status_or(st, THPVariable_Wrap(status));
 }
 
@@ -353,14 +374,15 @@ PyObject* cache_fork(PyObject* const* a, Py_ssize_t n) {
 PyObject* cache_reserve(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 8);
     const Table t(a[0], a[1], a[2]);
-    const Tensor status = t.status(a[6]);
+    const Stream stream = stream_of(a[7], t.dev);
+    const Tensor status = t.status(a[6], stream);
     const Tensor copies =
-        a[5] == Py_None ? fresh({t.batch, 3}, at::kInt, t.dev) : tensor("copies", a[5]);
+        a[5] == Py_None ? fresh({t.batch, 3}, at::kInt, t.dev, stream) : tensor("copies", a[5]);
     const fa_status st = fa_cache_reserve(
         t.refs, t.num_pages, t.table, t.max_pages, t.lens, t.batch,
         ints("extra", tensor("extra", a[3]), {t.batch}, t.dev), whole("page_size", a[4]),
         ints("copies", copies, {t.batch, 3}, t.dev), static_cast<int*>(status.data_ptr()),
-        stream_of(a[7], t.dev));
+        stream);
     return status_or(st, pair(copies, status));
 }
 
@@ -406,7 +428,7 @@ struct Rows {
     Tensor t;
     long long strides[3];
 
-    Rows(const char* name, PyObject* o, const Caches& c, int64_t B, int64_t n, fa_stream_t stream)
+    Rows(const char* name, PyObject* o, const Caches& c, int64_t B, int64_t n, const Stream& stream)
         : t(tensor(name, o)) {
         if (t.scalar_type() != at::kBFloat16 || !has_shape(t, {B, c.hkv, n, c.d}) || !on(t, c.dev))
             throw BadValue(std::string(name) + " must be a bf16 tensor " +
@@ -415,11 +437,7 @@ struct Rows {
                           ((t.stride(0) | t.stride(1) | t.stride(2)) & 7) == 0 &&
                           (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0;
         if (!fits) {
-            auto* const raw = reinterpret_cast<cudaStream_t>(stream);
-            const auto current = c10::cuda::getCurrentCUDAStream(c.dev);
-            const c10::cuda::CUDAStreamGuard guard(
-                raw == current.stream() ? current
-                                        : c10::cuda::getStreamFromExternal(raw, c.dev));
+            const c10::cuda::CUDAStreamGuard guard(torch_stream(stream, c.dev));
             t = t.clone(at::MemoryFormat::Contiguous);
         }
         for (int i = 0; i < 3; ++i) strides[i] = t.stride(i);
@@ -435,7 +453,7 @@ PyObject* cache_append(PyObject* const* a, Py_ssize_t n) {
     if (table.dim() != 2 || kn.dim() != 4)
         throw BadValue("block_table must be [B, max_pages], k_new and v_new [B, Hkv, n, d]");
     const int64_t B = table.size(0), m = kn.size(2);
-    const fa_stream_t stream = stream_of(a[8], c.dev);
+    const Stream stream = stream_of(a[8], c.dev);
     const Rows k("k_new", a[4], c, B, m, stream), v("v_new", a[5], c, B, m, stream);
     return PyLong_FromLong(fa_cache_append(
         c.k, c.v, c.num_pages, c.hkv, c.page_size, c.d,

@@ -125,6 +125,38 @@ def test_rows_of_other_layouts_on_another_stream():
     assert torch.equal(kc.cpu(), want) and torch.equal(vc.cpu(), want)
 
 
+def test_outputs_outlive_another_stream():
+    """What a call on another stream returns may be dropped while it is at work."""
+    from attention_forward_blackwell_gb300 import binding
+    P, Hkv, d, B = 16, 2, 64, 6
+    g = torch.Generator().manual_seed(8)
+    kc = torch.randn(40, Hkv, P, d, generator=g).bfloat16().cuda()
+    vc = torch.randn(40, Hkv, P, d, generator=g).bfloat16().cuda()
+    table = torch.full((B, 3), -1, dtype=torch.int32)
+    table[:, 0] = 7                              # one page, shared by all rows
+    lens = i32([11] * B)
+    refs = torch.zeros(40, dtype=torch.int32)
+    refs[7] = B
+    table, refs = table.cuda(), refs.cuda()
+    new = torch.randn(B, Hkv, 1, d, generator=g).bfloat16().cuda()
+    want = kc.cpu()
+    ref.append_rows(want, [[b] for b in range(B)], [11] * B, new.cpu(), [1] * B,
+                    [(7, b, 11) for b in range(B)])
+    side = torch.cuda.Stream()
+    one = i32([1] * B)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    copies, status = binding.cache_reserve(refs, table, lens, one, P, stream=side)
+    binding.cache_append(kc, vc, table, lens, new, new, copies=copies, stream=side)
+    del copies, status
+    for _ in range(20):
+        torch.full((B, 3), 1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert table[:, 0].tolist() == list(range(B)) and refs[:8].tolist() == [1] * B + [0, 0]
+    assert torch.equal(kc.cpu(), want)
+
+
 @pytest.mark.parametrize("rows", [1, 40], ids=["few rows", "many rows"])
 def test_wide_numbers(rows):
     """Windows and first keys far past the keys, extras past the table."""
