@@ -245,33 +245,38 @@ constexpr int kDecodeToPrefillRows = 32;
 // they win in long windows and in little work.  us, two-tile / span, window 100,
 // 512, 1,024, 2,048 of 4 first keys:
 //  2 x 16 heads x 4,096, group 1
-//    d 64     47 /  48    56 /  55    66 /  79    87 / 110
-//    d 128    54 /  61    67 /  84    80 / 104   103 / 138
-//    d 256    69 /  69    89 / 113   120 / 161   165 / 230
+//    d 64     46 /  46    56 /  54    67 /  78    87 / 110
+//    d 128    54 /  58    66 /  67    80 /  98   103 / 133
+//    d 256    69 /  65    89 / 136   120 / 181   165 / 233
+//  2 x 16 heads x 4,096, group 4
+//    d 64     44 /  31    54 /  52    64 /  75    85 / 107
+//    d 128    53 /  39    66 /  63    78 /  93   102 / 130
+//    d 256    60 /  50    85 /  89   114 / 117   150 / 181   (256: 68 / 72)
 //  32 heads x 8,192, group 4
-//    d 64     79 /  65   103 / 111   135 / 140   186 / 204
-//    d 128    92 /  79   122 / 119   159 / 157   221 / 230
-//    d 256   112 / 111   154 / 142   219 / 218   333 / 355   (256: 124 / 107)
+//    d 64     79 /  62   103 / 110   134 / 139   186 / 203   (256: 86 / 91)
+//    d 128    91 /  75   121 / 132   159 / 171   221 / 246   (256: 101 / 112)
+//    d 256   112 /  98   155 / 152   221 / 224   334 / 356   (256: 124 / 113)
 //  packed, 8 x 32 heads x 200 to 1,024 after 0 to 3,000 keys, group 8, pages
-//    d 64     71 /  40    89 /  74   108 /  91   132 / 113
-//    d 128    84 /  54   106 /  83   127 / 108   156 / 129
-//    d 256   123 /  68   161 / 109   196 / 160   244 / 212
+//    d 64     71 /  39    89 /  72   108 /  91   131 / 113
+//    d 128    83 /  48   106 /  90   128 / 115   156 / 141
+//    d 256   123 /  70   161 / 107   196 / 144   245 / 204
 //  packed, 2 x 32 heads x 4,000 to 8,000, group 4, pages
-//    d 64    121 /  81   157 / 143   202 / 203   278 / 299
-//    d 128   141 /  94   184 / 156   237 / 212   326 / 325
-//    d 256   217 / 141   293 / 196   389 / 346   553 / 582
+//    d 64    121 /  79   157 / 141   202 / 200   278 / 296
+//    d 128   141 /  92   184 / 162   237 / 244   326 / 352
+//    d 256   217 / 118   293 / 274   388 / 381   553 / 562
 //  packed, 8 x 16 heads x 200 to 1,024 after 0 to 3,000 keys, group 1
-//    d 64     41 /  41    51 /  46    63 /  59    77 /  70
-//    d 128    49 /  53    61 /  68    75 /  78    92 /  89
-//    d 256    69 /  65   104 /  93   135 / 123   182 / 157
+//    d 64     41 /  40    51 /  45    63 /  59    77 /  70
+//    d 128    49 /  50    61 /  59    75 /  75    92 /  90
+//    d 256    69 /  64   105 / 102   135 / 146   182 / 201
 //  4 x 8 heads x 1,000, group 8 (less than a wave); packed, 200 to 1,000
-//    d 128    20 /  26    21 /  27    23 /  32    22 /  32
-//    d 128    23 /  28    21 /  27    22 /  26    24 /  28
+//    d 128    20 /  24    21 /  30    21 /  32    22 /  31
+//    d 128    24 /  28    22 /  28    23 /  27    21 /  26
 bool span_wins_prompt(int head_dim, int group, long long rows, long long keys, bool packed,
                       bool short_prompts) {
-    if (!packed) return rows >= (64 << 10) && group >= 4 && keys < (head_dim == 64 ? 200 : 600);
+    if (!packed) return rows >= (64 << 10) && group >= 4 && keys < (head_dim == 256 ? 600 : 200);
     if (rows < (32 << 10)) return false;
-    return group >= 4 ? short_prompts || keys < 1100 : short_prompts && head_dim != 128;
+    if (group >= 4) return short_prompts || keys < 1100;
+    return short_prompts && (head_dim == 64 || (head_dim == 256 && keys < 800));
 }
 
 // Splits of the split-KV kernel over `span` keys of `pairs` (batch entry, kv
@@ -375,12 +380,9 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         const long long rows = (long long)group * sq;
         tiles = (rows + 127) / 128;
         if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-        // up to 8 tiles go side by side over the same keys, in clusters of two
-        // (a group of three stays single: a fourth CTA would idle)
+        // up to 8 tiles go side by side over the same keys
         a.tile_groups = ((int)tiles + 7) / 8;
         a.group_ctas = ((int)tiles + a.tile_groups - 1) / a.tile_groups;
-        a.cluster = a.group_ctas == 1 || a.group_ctas == 3 ? 1 : 2;
-        if (a.cluster == 2) a.group_ctas += a.group_ctas & 1;
         a.q_bytes = 128 * head_dim * 2;
         if (!encode_map_strided(&p.maps.q, q, head_dim, rows, (long long)batch * hkv, row_bytes,
                                 row_bytes * rows))
@@ -389,13 +391,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         a.P = std::min(128 / group, sq);
         tiles = (sq + a.P - 1) / a.P;
         if (hkv * tiles >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-        // neighbouring tiles' windows overlap: clusters of two, where a pair's
-        // union of keys is not much longer than a tile's span (8 chunks of
-        // prompts over 3,600 keys, window 512: 106 -> 91 us with 8 heads per kv
-        // head, 126 -> 111 with one; window 256, one head: 60 -> 69; head_dim
-        // 64, one head: 83 -> 95)
-        const bool pair = tiles > 1 && head_dim >= 128 && 4ll * a.P <= (long long)window + first;
-        a.cluster = a.group_ctas = pair ? 2 : 1;
+        a.group_ctas = 1;
         a.q_bytes = a.P * group * head_dim * 2;
         if (!(vl ? encode_map_strided(&p.maps.q, q, head_dim, vl->total_q, hq, row_bytes * hq,
                                       row_bytes, a.P, group)
@@ -410,13 +406,9 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         return encode_map_strided(m, base, head_dim, key_rows, planes, row_stride, plane_stride,
                                   rows);
     };
-    // contiguous keys: a block's and a slot's rows, or a cluster CTA's half (of
-    // a V slot the half is of its chunks where it has several); a tree has no
-    // gap, so no boxes
-    const int k_rows = span_block_keys(head_dim) / a.cluster;
-    const int v_rows = span_slot_keys(head_dim) / (head_dim == 64 ? a.cluster : 1);
-    if (!(block_table || (key_map(&p.maps.k, k, k_rows) &&
-                          key_map(&p.maps.v, v, v_rows))) ||
+    // (a tree over contiguous keys has no gap, so no boxes)
+    if (!(block_table || (key_map(&p.maps.k, k, span_block_keys(head_dim)) &&
+                          key_map(&p.maps.v, v, span_slot_keys(head_dim)))) ||
         !((tree && !block_table) ||
           (key_map(&p.maps.k_box, k, a.box) && key_map(&p.maps.v_box, v, a.box))))
         return FA_ERR_INVALID_ARG;
@@ -440,7 +432,7 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
         // a causal tile's axis: the first keys, the window of its first row
         // rounded down to a box, its other rows
         a.window_keys = (int)std::min<long long>(
-            sk, (long long)a.head_keys + a.window + a.P * a.group_ctas - 1 + a.box);
+            sk, (long long)a.head_keys + a.window + a.P - 1 + a.box);
         if (causal) keys = a.window_keys;
     }
     if (vl) {
@@ -471,9 +463,8 @@ fa_status span_impl(const Tree* tree, const void* q, const void* k, const void* 
     const long long groups = tree ? a.tile_groups : (tiles + a.group_ctas - 1) / a.group_ctas;
     const long long blocks = (long long)batch * hkv * groups * std::max<long long>(1, (keys + bn - 1) / bn);
     if (blocks >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-    const int ctas = a.cluster > 1 ? span_paired_ctas(head_dim, di.num_sms) : di.num_sms;
-    if (ctas < a.group_ctas) return FA_ERR_CUDA;
-    p.ctas = (unsigned)(std::min<long long>(ctas / a.group_ctas, blocks) * a.group_ctas);
+    if (di.num_sms < a.group_ctas) return FA_ERR_CUDA;
+    p.ctas = (unsigned)(std::min<long long>(di.num_sms / a.group_ctas, blocks) * a.group_ctas);
     const size_t slots = 2ull * p.ctas;
     const size_t bytes_o = slots * 128 * head_dim * sizeof(float);
     const size_t bytes_ml = slots * 2 * 128 * sizeof(float);

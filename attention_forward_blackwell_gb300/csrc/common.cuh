@@ -331,9 +331,7 @@ struct SpanArgs {
     int B, Hq, Hkv, group, Sq, Sk;
     int q_bytes;                // bytes of a Q tile's copies
     int P;                      // window: positions of a tile
-    int group_ctas;             // CTAs that walk the same keys, a tile each
-    int cluster;                // CTAs of a cluster (1 or 2, dividing group_ctas), which
-                                // load each key once for both
+    int group_ctas;             // CTAs that walk the same keys, a tile each (a window: 1)
     int tile_groups;            // tree: groups of tiles of a key/value head
     float* part_o;              // [2 CTAs][d / 4][128][4] unnormalised O of pieces
     float* part_ml;             // [2 CTAs][2][128] their row max (log2 units) and sum
@@ -358,8 +356,6 @@ struct SpanLaunch {
     unsigned ctas;
 };
 cudaError_t launch_span(const SpanLaunch& p, int head_dim, cudaStream_t s);
-// CTAs of clusters of two that the current device holds at a time.
-int span_paired_ctas(int head_dim, int num_sms);
 
 // Keys of a block and of a V slot of the span kernel.
 inline int span_block_keys(int head_dim) { return head_dim == 256 ? 128 : 256; }

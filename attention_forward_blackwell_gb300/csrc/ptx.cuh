@@ -182,23 +182,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
         : "memory");
 }
 
-// The same copy to every CTA of the cluster in `mask`: to the same offset of
-// its shared memory, completion counted on the barrier at bar's offset there.
-__device__ __forceinline__ void tma_load_3d_multicast(uint32_t dst, const CUtensorMap* m, int x,
-                                                      int y, int z, uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar), "h"(mask)
-        : "memory");
-}
-
-// Rank of the CTA in its cluster, and a barrier over all threads of it.
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
+// A barrier over all threads of the CTA's cluster.
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile(
         "barrier.cluster.arrive.release.aligned;\n\t"
@@ -296,16 +280,6 @@ __device__ __forceinline__ void tc_fence_after() {
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-        : "memory");
-}
-
-// The same, arriving on the barrier at bar's offset in every CTA of the cluster
-// in `mask`.
-__device__ __forceinline__ void tc_commit_multicast(uint32_t bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"(mask)
         : "memory");
 }
 

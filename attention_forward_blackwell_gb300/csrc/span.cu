@@ -30,8 +30,9 @@
 // span_combine_kernel merges the pieces, in their order (the result does not
 // depend on timing).  A tree of several tiles gives each to a CTA of a group
 // that walks the same keys at the same time, so that K and V come from HBM
-// once (one tile after the other, a 64-node tree of 8 heads read them three
-// times and took 117 us instead of 98).
+// once and from L2 after that (64 nodes x 8 heads over 8 x 4K to 8K keys at
+// head_dim 128: 95 us; one tile after the other read them three times and took
+// 20 more).
 //
 // Inside a CTA: the roles and barriers of the 256-key prefill kernel (see
 // prefill_wide.cuh), which this one follows: S = Q K^T of the next block is
@@ -40,8 +41,6 @@
 // blocks are 256 keys (one N = 256 score instruction per 16 head dims), 128 at
 // head_dim 256, whose 256 O columns leave no room for more.
 //
-#include <atomic>
-
 #include "prefill.cuh"
 #include "../../include/fa.h"
 
@@ -157,16 +156,15 @@ __device__ __forceinline__ SpanSeq span_seq(const SpanArgs& a, int b) {
     q.cap = min(q.rows, a.Sq);
     return q;
 }
-// Units of a batch entry -- groups of group_ctas tiles of a key/value head --
-// and the key blocks each counts for on the line: a bound for a window (its
-// tiles near the start have fewer), one at least, so that rows without keys
-// are written too.
+// Units of a batch entry -- a window's tiles, a tree's groups of group_ctas tiles,
+// of each key/value head -- and the key blocks each counts for on the line: a
+// bound for a window (its tiles near the start have fewer), one at least, so
+// that rows without keys are written too.
 template <int MODE>
 __device__ __forceinline__ int span_groups(const SpanArgs& a, const SpanSeq& q) {
     if (q.cap == 0) return 0;
     if (MODE == kSpanTree) return a.tile_groups;
-    const int rows = a.P * a.group_ctas;
-    return (int)((unsigned)(q.cap + rows - 1) / (unsigned)rows);
+    return (int)((unsigned)(q.cap + a.P - 1) / (unsigned)a.P);
 }
 template <int MODE>
 __device__ __forceinline__ int span_units(const SpanArgs& a, const SpanSeq& q) {
@@ -192,7 +190,7 @@ __device__ __forceinline__ void span_geometry(const SpanArgs& a, int t0, SpanIte
     } else {
         const int off = s.keys - s.rows;   // bottom-right alignment
         const int p0 = t0 * a.P + off;     // keys of the unit's first and last row
-        const int p1 = min((t0 + a.group_ctas) * a.P, s.cap) - 1 + off;
+        const int p1 = min((t0 + 1) * a.P, s.cap) - 1 + off;
         const int last = a.causal ? min(s.keys - 1, p1) : s.keys - 1;
         const int lo = max(0, p0 - a.window + 1), base = lo & -a.box;
         if (a.head_keys < base) {
@@ -415,9 +413,8 @@ __device__ __forceinline__ bool span_row(const SpanArgs& a, int cap, int q0, int
 // Producers: per segment K_0, then K_{j+1} and V_j for every block j, slot
 // after slot of one ring, two warps in turn (each waits a slot free, counts its
 // bytes and copies).  Keys that lie together come as one copy per chunk of a
-// slot (a cluster's CTAs copy half of it each, to both); those of pages, and of
-// a block on both sides of a window's gap, as boxes of a.box rows, one or two
-// per lane.  A slot takes its warp 500 to 700 cycles of waits and issue one
+// slot; those of pages, and of a block on both sides of a window's gap, as boxes
+// of a.box rows, one or two per lane.  A slot takes its warp 500 to 700 cycles of waits and issue one
 // after the other: one warp for the four slots of a block took as long as the
 // block's softmax.  The code is kept to a few hundred bytes, with what does not
 // change from slot to slot in registers: the softmax's straight code keeps
@@ -427,8 +424,7 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                                uint32_t sRing, const WaitCtx& wc, unsigned long long* tr) {
     const int lane = threadIdx.x & 31;
     const int box_shift = __ffs(a.box) - 1;   // (a power of two)
-    const int rank = (int)cluster_ctarank();
-    const bool paired = a.cluster > 1, one = elect_one();
+    const bool one = elect_one();
     // the boxes of a block, lane l's the l-th and the (l + 32)-th: K slots hold
     // all of them, one chunk or more each; V slot h the boxes [h vboxes, (h + 1)
     // vboxes)
@@ -507,24 +503,15 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
 #pragma unroll
                                 for (int q = 0; q < T::KCH; ++q) {
                                     const int col = (c * T::KCH + q) * 64;
-                                    if (!paired)
-                                        tma_load_3d(to + q * T::KCHUNK, &tm.k_box, col, y, z, bar);
-                                    else if (((box * T::KCH + q) & 1) == rank)
-                                        tma_load_3d_multicast(to + q * T::KCHUNK, &tm.k_box, col, y, z, bar, 3);
+                                    tma_load_3d(to + q * T::KCHUNK, &tm.k_box, col, y, z, bar);
                                 }
                             }
                         } else if (one) {
                             const int row = s.k0 + span_key(s, x1);
 #pragma unroll
-                            for (int q = 0; q < T::KCH; ++q) {
-                                const int col = (c * T::KCH + q) * 64;
-                                const uint32_t to = dst + q * T::KCHUNK;
-                                if (!paired)
-                                    tma_load_3d(to, &tm.k, col, row, plane, bar);
-                                else   // half of the rows
-                                    tma_load_3d_multicast(to + rank * (T::BN / 2 * 128), &tm.k, col,
-                                                          row + rank * (T::BN / 2), plane, bar, 3);
-                            }
+                            for (int q = 0; q < T::KCH; ++q)
+                                tma_load_3d(dst + q * T::KCHUNK, &tm.k, (c * T::KCH + q) * 64, row,
+                                            plane, bar);
                         }
                     }
                 }
@@ -542,28 +529,14 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
                                 const int y = box < 32 ? v_row[0] : v_row[1];
                                 const int z = box < 32 ? v_plane[0] : v_plane[1];
 #pragma unroll
-                                for (int q = 0; q < T::NCH; ++q) {
-                                    if (!paired)
-                                        tma_load_3d(to + q * T::VCHUNK, &tm.v_box, q * 64, y, z, bar);
-                                    else if (((box * T::NCH + q) & 1) == rank)
-                                        tma_load_3d_multicast(to + q * T::VCHUNK, &tm.v_box, q * 64, y, z, bar, 3);
-                                }
+                                for (int q = 0; q < T::NCH; ++q)
+                                    tma_load_3d(to + q * T::VCHUNK, &tm.v_box, q * 64, y, z, bar);
                             }
                         } else if (one) {
                             const int row = s.k0 + span_key(s, xv);
-                            if (!paired) {
 #pragma unroll
-                                for (int q = 0; q < T::NCH; ++q)
-                                    tma_load_3d(dst + q * T::VCHUNK, &tm.v, q * 64, row, plane, bar);
-                            } else if (T::NCH == 1) {   // half of the rows
-                                tma_load_3d_multicast(dst + rank * (T::VKEYS / 2 * 128), &tm.v, 0,
-                                                      row + rank * (T::VKEYS / 2), plane, bar, 3);
-                            } else {                    // half of the chunks
-#pragma unroll
-                                for (int q = 0; q < T::NCH / 2; ++q)
-                                    tma_load_3d_multicast(dst + (2 * q + rank) * T::VCHUNK, &tm.v,
-                                                          (2 * q + rank) * 64, row, plane, bar, 3);
-                            }
+                            for (int q = 0; q < T::NCH; ++q)
+                                tma_load_3d(dst + q * T::VCHUNK, &tm.v, q * 64, row, plane, bar);
                         }
                     }
                 }
@@ -577,16 +550,12 @@ __device__ void span_load_role(int part, const SpanMaps& tm, const SpanArgs& a, 
             }
         }
     }
-    // every copy issued must have landed before the CTA exits, and every arrival
-    // from the other CTA of a cluster (of the last use of each slot)
+    // every copy issued must have landed before the CTA exits
     if (one) {
 #pragma unroll 1
         for (int q = used > T::NSLOT ? used - T::NSLOT : 0; q < used; ++q) {
             if ((q & 1) != part) continue;
             mbar_wait_drain(bars + ring_slot<T>(q) * 8, ring_phase<T>(q), a.wait_limit_ns);
-            if (paired)
-                mbar_wait_drain(bars + empty_off + ring_slot<T>(q) * 8, ring_phase<T>(q),
-                                a.wait_limit_ns);
         }
     }
     __syncwarp();
@@ -620,12 +589,8 @@ __device__ void span_mma_role(const SpanArgs& a, SpanAux* aux, uint32_t tmem, ui
         return true;
     };
     auto slot_desc = [&](uint32_t d0) { return d0 + (uint32_t)((ring_slot<T>(p) * T::SLOT) >> 4); };
-    auto release_slot = [&] {   // in every CTA that fills it
-        const uint32_t bar = smem_u32(&aux->bar_empty[ring_slot<T>(p)]);
-        if (a.cluster > 1)
-            tc_commit_multicast(bar, 3);
-        else
-            tc_commit(bar);
+    auto release_slot = [&] {
+        tc_commit(smem_u32(&aux->bar_empty[ring_slot<T>(p)]));
         ++p;
     };
     int J0 = 0, kq = 0;
@@ -1119,7 +1084,7 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         }
         for (int i = 0; i < T::NSLOT; ++i) {
             mbar_init(smem_u32(&aux->bar_full[i]), 1);
-            mbar_init(smem_u32(&aux->bar_empty[i]), a.cluster);
+            mbar_init(smem_u32(&aux->bar_empty[i]), 1);
         }
         mbar_init(smem_u32(&aux->bar_s_full), 1);
         for (int i = 0; i < 2; ++i) {
@@ -1151,7 +1116,6 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
     tc_fence_before();
     __syncthreads();
-    if (a.cluster > 1) cluster_sync_all();   // the other CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = aux->tmem_base;
     const WaitCtx wc{smem_u32(&aux->abort_flag), (uint32_t)a.wait_limit_ns, a.err_word};
@@ -1198,7 +1162,6 @@ __global__ void __launch_bounds__(SpanTraits<D>::THREADS, 1)
         tc_fence_after();
         tmem_dealloc(tmem, T::TMEM_COLS);
     }
-    if (a.cluster > 1) cluster_sync_all();   // none leaves while the other may write to it
 }
 
 // Merges the pieces of the unit that starts in CTA blockIdx.x of the split
@@ -1287,8 +1250,8 @@ cudaError_t launch_span_mode(const SpanLaunch& p, cudaStream_t s) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          T::SMEM_TOTAL);
     if (e != cudaSuccess) return e;
-    e = launch_dependent_clusters(span_kernel<D, MODE, PAGED>, (unsigned)p.args.cluster,
-                                  dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL, s, p.maps, p.args);
+    e = launch_dependent(span_kernel<D, MODE, PAGED>, dim3(p.ctas), dim3(T::THREADS), T::SMEM_TOTAL,
+                         s, p.maps, p.args);
     if (e != cudaSuccess) return e;
     return launch_dependent(span_combine_kernel<D, MODE>, dim3(p.ctas, D / 16), dim3(T::BM), 0, s,
                             p.args);
@@ -1304,46 +1267,7 @@ cudaError_t launch_span_impl(const SpanLaunch& p, cudaStream_t s) {
                  : launch_span_mode<D, kSpanTree, false>(p, s);
 }
 
-// (the kernels of a head dimension take the same shared memory, and all the
-// registers of an SM)
-template <int D>
-int paired_ctas(int num_sms) {
-    using T = SpanTraits<D>;
-    const auto kernel = span_kernel<D, kSpanTree, true>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_TOTAL) !=
-        cudaSuccess)
-        return 0;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cudaLaunchConfig_t config{};
-    config.gridDim = dim3(num_sms / 2 * 2);
-    config.blockDim = dim3(T::THREADS);
-    config.dynamicSmemBytes = T::SMEM_TOTAL;
-    config.attrs = &attr;
-    config.numAttrs = 1;
-    int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &config) != cudaSuccess) return 0;
-    return clusters * 2 < num_sms ? clusters * 2 : num_sms / 2 * 2;
-}
-
 }  // namespace
-
-int span_paired_ctas(int head_dim, int num_sms) {
-    // asked once per head dimension and device
-    static std::atomic<int> known[3][64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    std::atomic<int>& k = known[head_dim == 64 ? 0 : (head_dim == 128 ? 1 : 2)][dev];
-    int n = k.load();
-    if (n == 0) {
-        n = head_dim == 64 ? paired_ctas<64>(num_sms)
-                           : (head_dim == 128 ? paired_ctas<128>(num_sms) : paired_ctas<256>(num_sms));
-        k.store(n);
-    }
-    return n;
-}
 
 cudaError_t launch_span(const SpanLaunch& p, int head_dim, cudaStream_t s) {
     switch (head_dim) {
