@@ -1,8 +1,8 @@
 """ctypes binding of libfa_gb300.so (argument marshalling only).
 
-Every function here checks tensor shapes/dtypes/devices, allocates outputs with
-torch when the caller does not pass them, and calls the C ABI declared in
-``include/fa.h`` on the current torch CUDA stream.  All arithmetic runs in the
+Every function here checks tensor shapes/dtypes/devices (all tensors lie on the
+current device), allocates outputs with torch when the caller does not pass them,
+and calls the C ABI declared in ``include/fa.h`` on the current torch CUDA stream.  All arithmetic runs in the
 library's CUDA kernels; there is no fallback path.  If the library has not
 been built, loading it raises.
 """
@@ -130,6 +130,15 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _on_current_device(**tensors):
+    """Refuses tensors of the host or of another device than the current one,
+    which the kernels run on."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
+
+
 def _check_inputs(q, k, v, seqlens_k):
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t.dtype != torch.bfloat16:
@@ -179,6 +188,7 @@ def prefill(q, k, v, scale=None, causal=False, seqlens_k=None, out=None, lse=Non
     out, lse = _outputs(q, out, lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
+    _on_current_device(q=q, k=k, v=v, seqlens_k=seqlens_k, out=out, lse=lse, sinks=sinks)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
     if first:
@@ -211,6 +221,7 @@ def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=
     out, lse = _outputs(q, out, lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
+    _on_current_device(q=q, k=k, v=v, seqlens_k=seqlens_k, out=out, lse=lse, sinks=sinks)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
     if (window and window > 0) or sinks is not None:
@@ -244,6 +255,8 @@ def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out
     q, k_cache, v_cache = q.contiguous(), k_cache.contiguous(), v_cache.contiguous()
     block_table, seqlens_k = block_table.contiguous(), seqlens_k.contiguous()
     out, lse = _outputs(q, out, lse)
+    _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                       seqlens_k=seqlens_k, out=out, lse=lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     st = getattr(lib(), name)(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), B, Hq,
                               Hkv, Sq, _ptr(seqlens_k), _ptr(block_table), block_table.shape[1],
@@ -285,6 +298,8 @@ def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
     if lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, total_q]")
     sinks = _check_sinks(sinks, Hq)
+    _on_current_device(q=q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
+                       lse=lse, sinks=sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
             _ptr(cu_seqlens_k), B, int(max_seqlen_q), int(max_seqlen_k), total_q, total_k, Hq, Hkv,
@@ -335,6 +350,8 @@ def prefill_varlen_paged(q, k_cache, v_cache, cu_seqlens_q, max_seqlen_q, block_
     if lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, total_q]")
     sinks = _check_sinks(sinks, Hq)
+    _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, cu_seqlens_q=cu_seqlens_q,
+                       seqlens_k=seqlens_k, block_table=block_table, out=out, lse=lse, sinks=sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(lse), _ptr(cu_seqlens_q),
             _ptr(seqlens_k), _ptr(block_table), block_table.shape[1], page_size, num_pages, B,
