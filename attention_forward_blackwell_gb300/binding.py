@@ -126,6 +126,28 @@ def _stream_ptr(stream=None):
     return _raw_stream(torch.cuda.current_device())
 
 
+def _other(stream):
+    """torch's stream of a call whose stream is not the current one, else None."""
+    if stream is None or stream.cuda_stream == _raw_stream(torch.cuda.current_device()):
+        return None
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream)
+
+
+def _fresh(shape, dtype, device, stream):
+    """New output of a call on `stream`.  Its memory comes from that stream's
+    pool, so that nothing still at work on the current stream uses it, and is
+    not given out again before what the current stream does with the output is
+    done: the caller may drop it at any time."""
+    other = _other(stream)
+    if other is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(other):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
+    return t
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -158,12 +180,12 @@ def _check_inputs(q, k, v, seqlens_k):
     return B, Hq, Hkv, Sq, Sk, d, seqlens_k
 
 
-def _outputs(q, out, lse):
+def _outputs(q, out, lse, stream):
     B, Hq, Sq, d = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _fresh(q.shape, torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+        lse = _fresh((B, Hq, Sq), torch.float32, q.device, stream)
     if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse.shape != (B, Hq, Sq) or lse.dtype != torch.float32 or not lse.is_contiguous():
@@ -185,7 +207,7 @@ def prefill(q, k, v, scale=None, causal=False, seqlens_k=None, out=None, lse=Non
     a sliding ``window`` > 0 or per-head ``sinks``, ``fa_fwd_prefill_first`` with
     a window whose ``first`` keys stay visible); returns (o, lse)."""
     B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
-    out, lse = _outputs(q, out, lse)
+    out, lse = _outputs(q, out, lse, stream)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
     _on_current_device(q=q, k=k, v=v, seqlens_k=seqlens_k, out=out, lse=lse, sinks=sinks)
@@ -218,7 +240,7 @@ def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=
             raise FaError(r, "fa_fwd_decode_first")
         return r
     B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
-    out, lse = _outputs(q, out, lse)
+    out, lse = _outputs(q, out, lse, stream)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     sinks = _check_sinks(sinks, q.shape[1])
     _on_current_device(q=q, k=k, v=v, seqlens_k=seqlens_k, out=out, lse=lse, sinks=sinks)
@@ -254,7 +276,7 @@ def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out
         raise ValueError("seqlens_k must be int32 [B]")
     q, k_cache, v_cache = q.contiguous(), k_cache.contiguous(), v_cache.contiguous()
     block_table, seqlens_k = block_table.contiguous(), seqlens_k.contiguous()
-    out, lse = _outputs(q, out, lse)
+    out, lse = _outputs(q, out, lse, stream)
     _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
                        seqlens_k=seqlens_k, out=out, lse=lse)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
@@ -290,9 +312,9 @@ def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
     q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
     cu_seqlens_q, cu_seqlens_k = cu_seqlens_q.contiguous(), cu_seqlens_k.contiguous()
     if out is None:
-        out = torch.empty_like(q)
+        out = _fresh(q.shape, torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty(Hq, total_q, device=q.device, dtype=torch.float32)
+        lse = _fresh((Hq, total_q), torch.float32, q.device, stream)
     if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
@@ -342,9 +364,9 @@ def prefill_varlen_paged(q, k_cache, v_cache, cu_seqlens_q, max_seqlen_q, block_
     cu_seqlens_q, seqlens_k = cu_seqlens_q.contiguous(), seqlens_k.contiguous()
     block_table = block_table.contiguous()
     if out is None:
-        out = torch.empty_like(q)
+        out = _fresh(q.shape, torch.bfloat16, q.device, stream)
     if lse is None:
-        lse = torch.empty(Hq, total_q, device=q.device, dtype=torch.float32)
+        lse = _fresh((Hq, total_q), torch.float32, q.device, stream)
     if out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():

@@ -1,0 +1,128 @@
+"""Calls on another stream than the current one: the memory of their outputs
+while either stream is busy."""
+import pytest
+import torch
+
+from gpu_parity import check_device_error, free_cuda
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 20_000_000   # cycles that a stream sleeps: far longer than any call here
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from attention_forward_blackwell_gb300 import build
+    build.build()
+    yield
+    free_cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def prompt(seed):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(*s, generator=g).bfloat16().cuda()
+            for s in ((1, 4, 200, 64), (1, 2, 256, 64), (1, 2, 256, 64))]
+
+
+def packed(t):
+    return t[0].transpose(0, 1).contiguous()
+
+
+def pages(t):   # [1, H, 256, d] as two pages of 128
+    return torch.stack([t[0, :, :128], t[0, :, 128:]]).contiguous()
+
+
+def calls():
+    """The calls over 256 keys, as f(q, k, v, **more); inputs() has their tensors."""
+    from attention_forward_blackwell_gb300 import binding
+    cu_q, cu_k, lens, table = i32([0, 200]), i32([0, 256]), i32([256]), i32([[0, 1]])
+    win = dict(causal=True, window=30, first=3)
+    return {
+        "prefill": lambda q, k, v, **m: binding.prefill(q, k, v, **win, **m),
+        "prefill, plain": lambda q, k, v, **m: binding.prefill(q, k, v, **m),
+        "prefill_varlen": lambda q, k, v, **m: binding.prefill_varlen(
+            q, k, v, cu_q, cu_k, 200, 256, **win, **m),
+        "prefill_varlen_paged": lambda q, k, v, **m: binding.prefill_varlen_paged(
+            q, k, v, cu_q, 200, table, lens, **win, **m),
+        "prefill_paged": lambda q, k, v, **m: binding.prefill_paged(q, k, v, table, lens, **m),
+        "decode": lambda q, k, v, **m: binding.decode(q, k, v, **m),
+        "decode_paged": lambda q, k, v, **m: binding.decode_paged(q, k, v, table, lens, **m),
+    }
+
+
+def inputs(name, seed):
+    q, k, v = prompt(seed)
+    if name == "prefill_varlen":
+        return packed(q), packed(k), packed(v)
+    if name == "prefill_varlen_paged":
+        return packed(q), pages(k), pages(v)
+    if name.startswith("decode"):
+        q = q[:, :, :9].contiguous()
+    if name.endswith("paged"):
+        return q, pages(k), pages(v)
+    return q, k, v
+
+
+NAMES = ["prefill", "prefill, plain", "prefill_varlen", "prefill_varlen_paged", "prefill_paged",
+         "decode", "decode_paged"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_may_be_dropped(name):
+    """Outputs dropped while the call's stream has not begun: what the current
+    stream allocates meanwhile stays as it is."""
+    call, args = calls()[name], inputs(name, 1)
+    side = torch.cuda.Stream()
+    o, lse = call(*args)
+    shapes = [(o.shape, o.dtype), (lse.shape, lse.dtype)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    o, lse = call(*args, stream=side)
+    del o, lse
+    held = [torch.full(s, 7.0, dtype=t, device="cuda") for s, t in shapes for _ in range(6)]
+    torch.cuda.synchronize()
+    check_device_error()
+    assert all(bool((t == 7).all()) for t in held)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_leave_memory_in_use_alone(name):
+    """The current stream is yet to read what was dropped just before the call."""
+    call, args = calls()[name], inputs(name, 2)
+    side = torch.cuda.Stream()
+    o, lse = call(*args)
+    kinds = [(o.shape, o.dtype), (lse.shape, lse.dtype)]
+    del o, lse
+    was = [torch.full(s, 7.0, dtype=t, device="cuda") for s, t in kinds for _ in range(3)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    now = [t.clone() for t in was]
+    del was
+    call(*args, stream=side)
+    torch.cuda.synchronize()
+    check_device_error()
+    assert all(bool((t == 7).all()) for t in now)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_outputs_stay_while_they_are_read(name):
+    """Outputs dropped before the current stream has read them, then another call."""
+    call, args, others = calls()[name], inputs(name, 3), inputs(name, 4)
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in call(*args)]
+    torch.cuda.synchronize()
+    o, lse = call(*args, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(BUSY)
+    got = [o.clone(), lse.clone()]
+    del o, lse
+    for _ in range(3):
+        call(*others, stream=side)
+    torch.cuda.synchronize()
+    check_device_error()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
