@@ -148,6 +148,19 @@ def _fresh(shape, dtype, device, stream):
     return t
 
 
+def _dense(t, stream):
+    """An input as a kernel on `stream` reads it: copied there where it is not
+    contiguous (the copy's memory is of that stream's pool too, so that it may go
+    as soon as the call is enqueued)."""
+    if t.is_contiguous():
+        return t
+    other = _other(stream)
+    if other is None:
+        return t.contiguous()
+    with torch.cuda.stream(other):
+        return t.contiguous()
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -161,7 +174,7 @@ def _on_current_device(**tensors):
             raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
 
 
-def _check_inputs(q, k, v, seqlens_k):
+def _check_inputs(q, k, v, seqlens_k, stream):
     for name, t in (("q", q), ("k", k), ("v", v)):
         if t.dtype != torch.bfloat16:
             raise TypeError(f"{name} must be bfloat16")
@@ -176,7 +189,7 @@ def _check_inputs(q, k, v, seqlens_k):
     if seqlens_k is not None:
         if seqlens_k.dtype != torch.int32 or not seqlens_k.is_cuda or seqlens_k.shape != (B,):
             raise ValueError("seqlens_k must be a CUDA int32 tensor of shape [B]")
-        seqlens_k = seqlens_k.contiguous()
+        seqlens_k = _dense(seqlens_k, stream)
     return B, Hq, Hkv, Sq, Sk, d, seqlens_k
 
 
@@ -193,12 +206,12 @@ def _outputs(q, out, lse, stream):
     return out, lse
 
 
-def _check_sinks(sinks, hq):
+def _check_sinks(sinks, hq, stream):
     if sinks is None:
         return None
     if sinks.dtype != torch.float32 or sinks.shape != (hq,) or not sinks.is_cuda:
         raise ValueError("sinks must be a CUDA fp32 tensor of shape [Hq]")
-    return sinks.contiguous()
+    return _dense(sinks, stream)
 
 
 def prefill(q, k, v, scale=None, causal=False, seqlens_k=None, out=None, lse=None,
@@ -206,10 +219,10 @@ def prefill(q, k, v, scale=None, causal=False, seqlens_k=None, out=None, lse=Non
     """Attention forward through ``fa_fwd_prefill`` (``fa_fwd_prefill_ex`` with
     a sliding ``window`` > 0 or per-head ``sinks``, ``fa_fwd_prefill_first`` with
     a window whose ``first`` keys stay visible); returns (o, lse)."""
-    B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
+    B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k, stream)
     out, lse = _outputs(q, out, lse, stream)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    sinks = _check_sinks(sinks, q.shape[1])
+    sinks = _check_sinks(sinks, q.shape[1], stream)
     _on_current_device(q=q, k=k, v=v, seqlens_k=seqlens_k, out=out, lse=lse, sinks=sinks)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
@@ -239,10 +252,10 @@ def decode(q, k, v, scale=None, causal=False, seqlens_k=None, num_splits=0, out=
         if type(r) is int:
             raise FaError(r, "fa_fwd_decode_first")
         return r
-    B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k)
+    B, Hq, Hkv, Sq, Sk, d, seqlens_k = _check_inputs(q, k, v, seqlens_k, stream)
     out, lse = _outputs(q, out, lse, stream)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    sinks = _check_sinks(sinks, q.shape[1])
+    sinks = _check_sinks(sinks, q.shape[1], stream)
     _on_current_device(q=q, k=k, v=v, seqlens_k=seqlens_k, out=out, lse=lse, sinks=sinks)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), B, Hq, Hkv, Sq, Sk,
             _ptr(seqlens_k), d, scale, int(bool(causal)))
@@ -274,8 +287,8 @@ def _paged(name, q, k_cache, v_cache, block_table, seqlens_k, scale, causal, out
         raise ValueError("block_table must be int32 [B, max_pages]")
     if seqlens_k is None or seqlens_k.dtype != torch.int32 or seqlens_k.shape != (B,):
         raise ValueError("seqlens_k must be int32 [B]")
-    q, k_cache, v_cache = q.contiguous(), k_cache.contiguous(), v_cache.contiguous()
-    block_table, seqlens_k = block_table.contiguous(), seqlens_k.contiguous()
+    q, k_cache, v_cache, block_table, seqlens_k = (
+        _dense(t, stream) for t in (q, k_cache, v_cache, block_table, seqlens_k))
     out, lse = _outputs(q, out, lse, stream)
     _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
                        seqlens_k=seqlens_k, out=out, lse=lse)
@@ -309,8 +322,8 @@ def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
     if cu_seqlens_q.shape != cu_seqlens_k.shape or cu_seqlens_q.numel() < 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_k must both be [B + 1]")
     B = cu_seqlens_q.numel() - 1
-    q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
-    cu_seqlens_q, cu_seqlens_k = cu_seqlens_q.contiguous(), cu_seqlens_k.contiguous()
+    q, k, v, cu_seqlens_q, cu_seqlens_k = (
+        _dense(t, stream) for t in (q, k, v, cu_seqlens_q, cu_seqlens_k))
     if out is None:
         out = _fresh(q.shape, torch.bfloat16, q.device, stream)
     if lse is None:
@@ -319,7 +332,7 @@ def prefill_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, total_q]")
-    sinks = _check_sinks(sinks, Hq)
+    sinks = _check_sinks(sinks, Hq, stream)
     _on_current_device(q=q, k=k, v=v, cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k, out=out,
                        lse=lse, sinks=sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
@@ -360,9 +373,8 @@ def prefill_varlen_paged(q, k_cache, v_cache, cu_seqlens_q, max_seqlen_q, block_
         raise ValueError("seqlens_k must be [B] with B + 1 query offsets")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be int32 [B, max_pages]")
-    q, k_cache, v_cache = q.contiguous(), k_cache.contiguous(), v_cache.contiguous()
-    cu_seqlens_q, seqlens_k = cu_seqlens_q.contiguous(), seqlens_k.contiguous()
-    block_table = block_table.contiguous()
+    q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table = (
+        _dense(t, stream) for t in (q, k_cache, v_cache, cu_seqlens_q, seqlens_k, block_table))
     if out is None:
         out = _fresh(q.shape, torch.bfloat16, q.device, stream)
     if lse is None:
@@ -371,7 +383,7 @@ def prefill_varlen_paged(q, k_cache, v_cache, cu_seqlens_q, max_seqlen_q, block_
         raise ValueError("out must be a contiguous bf16 tensor shaped like q")
     if lse.shape != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [Hq, total_q]")
-    sinks = _check_sinks(sinks, Hq)
+    sinks = _check_sinks(sinks, Hq, stream)
     _on_current_device(q=q, k_cache=k_cache, v_cache=v_cache, cu_seqlens_q=cu_seqlens_q,
                        seqlens_k=seqlens_k, block_table=block_table, out=out, lse=lse, sinks=sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)

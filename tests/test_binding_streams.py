@@ -71,3 +71,30 @@ def test_outputs_come_from_the_calls_stream(call, i, stream, at, monkeypatch):
     else:   # (and kept until what the current stream does with them is done)
         assert made.outputs == [OTHER] * 2 and used == [CURRENT] * 2
     assert made.copies == [] and at == [CURRENT]
+
+
+# inputs that each call takes in other layouts
+LAID_OUT = {"prefill": ["seqlens_k", "sinks"], "decode": ["seqlens_k", "sinks"],
+            "prefill_paged": ["q", "k_cache", "v_cache", "block_table", "seqlens_k"],
+            "decode_paged": ["q", "k_cache", "v_cache", "block_table", "seqlens_k"],
+            "prefill_varlen": ["q", "k", "v", "cu_seqlens_q", "cu_seqlens_k", "sinks"],
+            "prefill_varlen_paged": ["q", "k_cache", "v_cache", "cu_seqlens_q", "seqlens_k",
+                                     "block_table", "sinks"]}
+
+
+@pytest.mark.parametrize("stream", [None, Side], ids=["current", "other"])
+@pytest.mark.parametrize("call,i", CASES)
+def test_inputs_are_laid_out_on_the_calls_stream(call, i, stream, at, monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    tensors, more = CALLS[call]
+    with FakeTensorMode():
+        args, copied = {}, 0
+        for n, (shape, dtype) in tensors.items():
+            args[n] = torch.empty(shape, dtype=dtype, device="cuda:0")
+            if n in LAID_OUT[call] and args[n].numel() > 1:   # every other element of a wider one
+                args[n] = torch.empty((*shape[:-1], 2 * shape[-1]), dtype=dtype, device="cuda:0")[..., ::2]
+                copied += 1
+        with Allocations(at) as made:
+            getattr(binding, call)(**args, **more[i], stream=stream)
+    assert made.copies == [CURRENT if stream is None else OTHER] * copied and copied > 0
+    assert at == [CURRENT]

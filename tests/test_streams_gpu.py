@@ -126,3 +126,31 @@ def test_outputs_stay_while_they_are_read(name):
     torch.cuda.synchronize()
     check_device_error()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def strided(t):
+    wide = torch.empty(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype, device="cuda")
+    wide[..., ::2] = t
+    return wide[..., ::2]
+
+
+def test_inputs_of_other_layouts_are_copied_on_the_calls_stream():
+    """The current stream is busy: copies made there would come after the kernel."""
+    from attention_forward_blackwell_gb300 import binding
+    q, k, v = prompt(5)
+    q, k, v = (t.expand(3, -1, -1, -1).contiguous() for t in (q, k, v))
+    lens, sinks = i32([256, 40, 0]), torch.randn(4, device="cuda")
+    win = dict(causal=True, window=30, first=3)
+    want = binding.prefill(q, k, v, seqlens_k=lens, sinks=sinks, **win)
+    wide = strided(lens), strided(sinks)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    got = binding.prefill(q, k, v, seqlens_k=wide[0], sinks=wide[1], stream=side, **win)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()   # still busy
+    with torch.cuda.stream(side):
+        got = [t.cpu() for t in got]
+    torch.cuda.synchronize()
+    check_device_error()
+    assert all(torch.equal(a, b.cpu()) for a, b in zip(got, want))
