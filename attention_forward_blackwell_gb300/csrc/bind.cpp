@@ -104,13 +104,21 @@ c10::cuda::CUDAStream torch_stream(const Stream& s, int dev) {
 }
 
 // A new contiguous tensor for a call on `stream` (without the dispatcher: 0.5 us
-// where at::empty takes 1.5).  On a stream other than the current one the
-// allocator is told, so that the memory outlives that stream's work on it.
+// where at::empty takes 1.5).  Its memory comes from that stream's pool, so that
+// nothing still at work on the current stream uses it; and where that is another
+// stream the allocator is told of the current one, which is to read it: the
+// caller may drop it at any time.
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev, const Stream& stream) {
-    Tensor t = at::detail::empty_cuda(
-        shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev)), std::nullopt);
-    if (stream.other && t.numel() > 0)
-        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), torch_stream(stream, dev));
+    const c10::Device device(c10::kCUDA, static_cast<c10::DeviceIndex>(dev));
+    if (!stream.other) return at::detail::empty_cuda(shape, type, device, std::nullopt);
+    Tensor t;
+    {
+        const c10::cuda::CUDAStreamGuard guard(torch_stream(stream, dev));
+        t = at::detail::empty_cuda(shape, type, device, std::nullopt);
+    }
+    if (t.numel() > 0)
+        c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(),
+                                                      c10::cuda::getCurrentCUDAStream(device.index()));
     return t;
 }
 

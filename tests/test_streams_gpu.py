@@ -154,3 +154,68 @@ def test_inputs_of_other_layouts_are_copied_on_the_calls_stream():
     torch.cuda.synchronize()
     check_device_error()
     assert all(torch.equal(a, b.cpu()) for a, b in zip(got, want))
+
+
+def serving():
+    """The serving calls that make their outputs, as name -> f(**more)."""
+    from attention_forward_blackwell_gb300 import binding
+    q, k, v = prompt(6)
+    q = q[:, :, :9].contiguous()
+    kc, vc, table, lens = pages(k), pages(v), i32([[0, 1]]), i32([256])
+    parents = torch.arange(-1, 8, dtype=torch.int32, device="cuda")[None]
+    mask = binding.tree_mask(parents)
+    refs, none = i32([1, 1]), torch.empty(0, dtype=torch.int32, device="cuda")
+    return {
+        "tree_mask": lambda **m: (binding.tree_mask(parents, **m),),
+        "decode_tree": lambda **m: binding.decode_tree(q, k, v, mask, **m),
+        "decode_tree_paged": lambda **m: binding.decode_tree_paged(q, kc, vc, table, lens, mask, **m),
+        "decode": lambda **m: binding.decode(q, k, v, window=30, first=3, **m),
+        "decode_paged": lambda **m: binding.decode_paged(q, kc, vc, table, lens, window=30, first=3, **m),
+        "cache_fork": lambda **m: (binding.cache_fork(refs, table, lens, none, none, **m),),
+        "cache_reserve": lambda **m: binding.cache_reserve(refs, table, lens, i32([0]), 128, **m),
+    }
+
+
+SERVING = ["tree_mask", "decode_tree", "decode_tree_paged", "decode", "decode_paged", "cache_fork",
+           "cache_reserve"]
+
+
+@pytest.mark.parametrize("name", SERVING)
+def test_serving_outputs_come_from_the_calls_stream(name):
+    """By the allocator's own account: each stream's memory is its own, and an
+    output that the current stream may read is kept until it has."""
+    call = serving()[name]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for out in call(stream=side):
+        owners = [s["stream"] for s in torch.cuda.memory_snapshot()
+                  if s["address"] <= out.data_ptr() < s["address"] + s["total_size"]]
+        assert owners == [side.cuda_stream]
+    torch.cuda.synchronize()
+    out = call(stream=side)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(BUSY)
+    at = out.data_ptr()
+    del out
+    states = [b["state"] for s in torch.cuda.memory_snapshot() for b in s["blocks"]
+              if b["address"] <= at < b["address"] + b["size"]]
+    torch.cuda.synchronize()
+    check_device_error()
+    assert states == ["active_pending_free"]
+
+
+@pytest.mark.parametrize("name", SERVING)
+def test_serving_outputs_leave_memory_in_use_alone(name):
+    """The current stream is yet to read what was dropped just before the call."""
+    call = serving()[name]
+    side = torch.cuda.Stream()
+    kinds = [(t.shape, t.dtype) for t in call()]
+    was = [torch.full(s, 7, dtype=t, device="cuda") for s, t in kinds for _ in range(3)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    now = [t.clone() for t in was]
+    del was
+    call(stream=side)
+    torch.cuda.synchronize()
+    check_device_error()
+    assert all(bool((t == 7).all()) for t in now)
