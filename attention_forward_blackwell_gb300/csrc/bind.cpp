@@ -8,6 +8,7 @@
 // (None where an optional one is absent), raises ValueError or TypeError for
 // tensors that do not fit, and returns the outputs, or the status of the C
 // call as an int where it is not FA_OK.
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
@@ -17,6 +18,7 @@
 #include <c10/cuda/CUDAStream.h>
 
 #include <cmath>
+#include <exception>
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
@@ -181,8 +183,8 @@ PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const BadType& e) {
         PyErr_SetString(PyExc_TypeError, e.what());
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {   // torch's own (out of memory, ...) as what torch raises for them
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
