@@ -60,11 +60,11 @@ def _cuda_home():
 
 
 def _compile_bind(force):
-    """csrc/bind.cpp against the installed torch; whether it was compiled."""
+    """csrc/bind.cpp against the installed torch."""
     src, obj = os.path.join(CSRC, "bind.cpp"), os.path.join(OBJDIR, "bind.o")
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "fa.h")))
     if not force and os.path.exists(obj) and os.path.getmtime(obj) >= newest:
-        return False
+        return
     include = os.path.join(_torch()[0], "include")
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-c", src, "-o", obj + ".tmp",
            "-I", include, "-I", os.path.join(include, "torch", "csrc", "api", "include"),
@@ -73,7 +73,6 @@ def _compile_bind(force):
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(obj + ".tmp", obj)
-    return True
 
 
 def _link_bind():
@@ -125,7 +124,10 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         bind = ex.submit(_compile_bind, force)
         results = list(ex.map(compile_one, SOURCES))
-        relink_bind = bind.result() or not os.path.exists(BIND_PATH)
+        bind.result()
+    # (by age, as the library: an earlier build may have failed after bind.o)
+    relink_bind = (not os.path.exists(BIND_PATH)
+                   or os.path.getmtime(BIND_PATH) < os.path.getmtime(os.path.join(OBJDIR, "bind.o")))
     objs = [o for o, _ in results]
     relink = (force or any(changed for _, changed in results) or not os.path.exists(LIB_PATH)
               or os.path.getmtime(LIB_PATH) < max(os.path.getmtime(o) for o in objs))
@@ -137,6 +139,9 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        # a module of other arguments is never left beside the new library
+        if relink_bind and os.path.exists(BIND_PATH):
+            os.remove(BIND_PATH)
         os.replace(tmp, LIB_PATH)
     if relink_bind:
         _link_bind()
