@@ -1,5 +1,5 @@
 """Builds libfa_gb300.so from csrc/ with nvcc for sm_103a (in-tree), and
-_bind.so, the Python module of the serving operators, from csrc/bind.cpp.
+_bind, the Python module of the serving operators, from csrc/bind.cpp.
 
 Each translation unit is compiled in parallel into ``_build/`` and the objects
 are linked into ``libfa_gb300.so`` next to this file.  Objects are rebuilt
@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libfa_gb300.so")
-BIND_PATH = os.path.join(HERE, "_bind.so")
+BIND_PATH = os.path.join(HERE, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["prefill_d512.cu", "prefill_d128.cu", "prefill_d256.cu", "prefill_d96.cu",
            "prefill_d64.cu", "decode.cu", "selftest.cu", "api.cu", "decode_noalloc.cu", "cache.cu",
            "span.cu"]
@@ -95,9 +95,10 @@ def _headers():
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
-    # objects from another host architecture (or toolchain) are never reused
+    # objects for another host architecture, Python or torch are never reused
     stamp = os.path.join(OBJDIR, "host.txt")
-    host = f"{platform.machine()} {platform.system()} torch {_torch()[1]} {' '.join(_options())}"
+    host = (f"{platform.machine()} {platform.system()} {sysconfig.get_config_var('SOABI')} "
+            f"torch {_torch()[1]} {' '.join(_options())}")
     if not os.path.exists(stamp) or open(stamp).read() != host:
         force = True
     nvcc = _nvcc()

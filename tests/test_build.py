@@ -76,3 +76,15 @@ def test_a_build_that_failed_leaves_no_stale_module(tree, failing):
     assert tree.bind in again
     assert os.path.getmtime(tree.bind_path) >= os.path.getmtime(tree.bind_obj)
     assert made(tree) == []
+
+
+def test_the_module_is_of_one_python(tree, monkeypatch):
+    """A CPython extension: another interpreter neither finds it nor keeps it."""
+    import sysconfig
+    assert real.BIND_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    made(tree)
+    of = sysconfig.get_config_var
+    monkeypatch.setattr(real.sysconfig, "get_config_var",
+                        lambda name: "cpython-399-other" if name == "SOABI" else of(name))
+    assert tree.bind in made(tree)
+    assert made(tree) == []
