@@ -1,5 +1,6 @@
 """Builds libfa_gb300.so from csrc/ with nvcc for sm_103a (in-tree), and
-_bind, the Python module of the serving operators, from csrc/bind.cpp.
+_bind, the Python module of the serving operators, from csrc/bind.cpp (where torch
+is installed: the library itself needs none).
 
 Each translation unit is compiled in parallel into ``_build/`` and the objects
 are linked into ``libfa_gb300.so`` next to this file.  Objects are rebuilt
@@ -42,10 +43,10 @@ def _nvcc():
 
 
 def _torch():
-    """Folder of the installed torch package and its version."""
+    """Folder of the installed torch package and its version; None, None without torch."""
     spec = importlib.util.find_spec("torch")
     if spec is None:
-        raise RuntimeError("torch is missing")
+        return None, None
     root = os.path.dirname(spec.origin)
     about = {}
     with open(os.path.join(root, "version.py")) as f:
@@ -95,6 +96,7 @@ def _headers():
 
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
+    with_bind = _torch()[0] is not None
     # objects for another host architecture, Python or torch are never reused
     stamp = os.path.join(OBJDIR, "host.txt")
     host = (f"{platform.machine()} {platform.system()} {sysconfig.get_config_var('SOABI')} "
@@ -123,12 +125,14 @@ def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -
 
     jobs = jobs or min(len(SOURCES), os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
-        bind = ex.submit(_compile_bind, force)
+        bind = ex.submit(_compile_bind, force) if with_bind else None
         results = list(ex.map(compile_one, SOURCES))
-        bind.result()
+        if bind is not None:
+            bind.result()
     # (by age, as the library: an earlier build may have failed after bind.o)
-    relink_bind = (not os.path.exists(BIND_PATH)
-                   or os.path.getmtime(BIND_PATH) < os.path.getmtime(os.path.join(OBJDIR, "bind.o")))
+    relink_bind = with_bind and (
+        not os.path.exists(BIND_PATH)
+        or os.path.getmtime(BIND_PATH) < os.path.getmtime(os.path.join(OBJDIR, "bind.o")))
     objs = [o for o, _ in results]
     relink = (force or any(changed for _, changed in results) or not os.path.exists(LIB_PATH)
               or os.path.getmtime(LIB_PATH) < max(os.path.getmtime(o) for o in objs))

@@ -88,3 +88,13 @@ def test_the_module_is_of_one_python(tree, monkeypatch):
                         lambda name: "cpython-399-other" if name == "SOABI" else of(name))
     assert tree.bind in made(tree)
     assert made(tree) == []
+
+
+def test_the_library_needs_no_torch(tree, monkeypatch):
+    """Users of the C ABI build the library without torch; with it, the module follows."""
+    with monkeypatch.context() as m:
+        m.setattr(real.importlib.util, "find_spec", lambda name: None)
+        first = made(tree)
+        assert tree.lib in first and "bind.o" not in first and tree.bind not in first
+        assert made(tree) == []
+    assert tree.bind in made(tree)
