@@ -574,6 +574,7 @@ fa_status device_ok() {
 fa_status check_table(const TableArgs& t, bool need_status) {
     if (t.num_pages < 0 || t.max_pages < 0 || t.batch < 0) return FA_ERR_INVALID_ARG;
     if (t.batch > 0 && (!t.table || !t.lens || !t.refs)) return FA_ERR_INVALID_ARG;
+    if (t.num_pages > 0 && !t.refs) return FA_ERR_INVALID_ARG;   // (reserve reads them at once)
     if (need_status && !t.status) return FA_ERR_INVALID_ARG;
     if (!aligned4(t.refs) || !aligned4(t.table) || !aligned4(t.lens) || !aligned4(t.status))
         return FA_ERR_MISALIGNED;

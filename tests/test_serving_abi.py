@@ -158,3 +158,17 @@ def test_plain_page_operators():
     assert pool.reserve([0, 4, 0], 4) == ([[-1, -1, 0]] * 3, 1)
     pool.free([1, 1])
     assert pool.refs == [1, 0, 2, 1, 1] and pool.lens[1] == 0
+
+
+def test_pages_need_their_counts(lib):
+    """Counts may be absent only where there are no pages, whatever the rows: the
+    kernel that reserves looks for free pages before it knows what is needed."""
+    # refs pages table max_pages lens B extra P copies status stream
+    call = variants([None, 8, None, 4, None, 0, None, 16, None, P16, None])
+    assert call(lib.fa_cache_reserve) == 1
+    # refs pages table max_pages lens B src dst n status stream
+    call = variants([None, 8, None, 4, None, 0, None, None, 0, P16, None])
+    assert call(lib.fa_cache_fork) == 1
+    # refs pages table max_pages lens B rows n stream
+    call = variants([None, 8, None, 4, None, 0, None, 0, None])
+    assert call(lib.fa_cache_free) == 1
