@@ -190,29 +190,24 @@ constexpr int kLongSpan = 8;     // entries of a span that a warp shares
 constexpr int kSharedList = 8192;   // most entries of a list in shared memory
 constexpr int kScanPages = 16;   // pages a thread looks at in one step of the free scan
 
-// Marks the needed entry j of a row (see below); whether it is one.
-__device__ __forceinline__ bool reserve_mark(const TableArgs& t, int* row, int j) {
+// Whether entry j of a row is needed (see below).
+__device__ __forceinline__ bool reserve_needs(const TableArgs& t, const int* row, int j) {
     const int e = row[j];
-    if (!is_page(e, t.num_pages)) {
-        row[j] = -1;
-        return true;
-    }
-    if (t.refs[e] > 1) {
-        row[j] = -2 - e;
-        return true;
-    }
-    return false;
+    return !is_page(e, t.num_pages) || t.refs[e] > 1;
 }
 
-// Entry j of row r, marked as needed: takes `page`, or (page < 0) its mark
-// back.
+// Marks entry j of a row if it is needed.
+__device__ __forceinline__ bool reserve_mark(const TableArgs& t, int* row, int j) {
+    if (!reserve_needs(t, row, j)) return false;
+    const int e = row[j];
+    row[j] = is_page(e, t.num_pages) ? -2 - e : -1;
+    return true;
+}
+
+// Entry j of row r, marked as needed, takes `page`.
 __device__ __forceinline__ void reserve_grant(const TableArgs& t, int* row, int r, int j, int page,
                                               int first, int used, int* copies) {
     const int e = row[j];
-    if (page < 0) {
-        if (e <= -2) row[j] = -2 - e;
-        return;
-    }
     row[j] = page;
     t.refs[page] = 1;
     if (e <= -2) {
@@ -229,16 +224,16 @@ __device__ __forceinline__ void reserve_grant(const TableArgs& t, int* row, int 
 // those whose page another entry shares (it would be written under the
 // other's eyes); in (row, entry) order they take the free pages in ascending
 // order.
-//   1  count the needed entries, a thread per row (a warp for a long span);
-//      shared ones are marked in the table as -2 - page and entries that are
-//      no page as -1, so that pass 3 sees the same set whatever it does to
-//      refs
+//   1  count the needed entries, a thread per row (a warp for a long span)
 //   2  list the free pages, as many as are needed (ascending; the scan stops
-//      early)
-//   3  give them out, or take the marks back where they do not suffice
+//      early); where they do not suffice that is all
+//   3  mark the needed entries: shared ones as -2 - page and entries that are
+//      no page as -1, so that pass 4 sees the same set whatever it does to
+//      refs (what pass 1 read is still in the L1 cache)
+//   4  give the pages out
 // The order of the pages makes it one scan over the rows and one over the pages;
 // bound by the latencies of its chain (length, entry, count; scan; entry, page):
-// 6.0 us for 288 rows over 17,000 pages, 5 for 5 rows.
+// 5.3 us for 288 rows over 17,000 pages, 4.0 for 5 rows.
 __global__ void __launch_bounds__(kTableThreads)
     cache_reserve_kernel(const TableArgs t, const int* extra, int page_size, int* copies,
                          int* free_list) {
@@ -267,30 +262,36 @@ __global__ void __launch_bounds__(kTableThreads)
         }
         return is_free;
     };
-    // (the first ones with the rows' loads: nothing changes refs before pass 3)
+    // (the first ones with the rows' loads: nothing changes refs before pass 4)
     const unsigned first_free = free_pages((int)threadIdx.x * kScanPages);
     __syncthreads();
-    int needed = 0;
-    for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
-        const int r = r0 + threadIdx.x;
-        Span s{0, 0, true};
-        if (r < t.batch) s = reserve_span(t, extra, page_size, r);
-        if (!s.fits) atomicMin(&long_row, r);
+    // sum of f(row, entry) over the span of each lane's row r, by the lanes of the
+    // warp together where a span is long
+    auto over_span = [&](int r, const Span& s, auto&& f) -> int {
         int* row = t.table + (size_t)r * t.max_pages;
         const bool shared_out = s.last - s.first > kLongSpan;
         int count = 0;
         if (!shared_out)
-            for (int j = s.first; j < s.last; ++j) count += reserve_mark(t, row, j);
+            for (int j = s.first; j < s.last; ++j) count += f(row, j);
         for (unsigned todo = __ballot_sync(0xffffffffu, shared_out); todo != 0; todo &= todo - 1) {
             const int from = __ffs(todo) - 1;
             const int first = __shfl_sync(0xffffffffu, s.first, from);
             const int last = __shfl_sync(0xffffffffu, s.last, from);
             int* its = t.table + (size_t)(r - lane + from) * t.max_pages;
             int c = 0;
-            for (int j = first + lane; j < last; j += 32) c += reserve_mark(t, its, j);
+            for (int j = first + lane; j < last; j += 32) c += f(its, j);
             c = __reduce_add_sync(0xffffffffu, c);
             if (lane == from) count = c;
         }
+        return count;
+    };
+    int needed = 0;
+    for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
+        const int r = r0 + threadIdx.x;
+        Span s{0, 0, true};
+        if (r < t.batch) s = reserve_span(t, extra, page_size, r);
+        if (!s.fits) atomicMin(&long_row, r);
+        const int count = over_span(r, s, [&](int* row, int j) { return reserve_needs(t, row, j); });
         int total;
         block_scan(count, scratch, total);
         needed += total;
@@ -308,7 +309,22 @@ __global__ void __launch_bounds__(kTableThreads)
     const bool fits = long_row == t.batch;   // (the scans' barriers order it)
     const bool grant = fits && found >= needed;
     if (threadIdx.x == 0) *t.status = !fits ? -1 - long_row : (grant ? 0 : needed - found);
-    __syncthreads();   // free_list
+    // (the rows of one step are marked as they are counted: the scan's barriers
+    // come before refs change)
+    const bool at_once = t.batch <= kTableThreads;
+    auto mark = [&](int* row, int j) { return reserve_mark(t, row, j); };
+    for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
+        const int r = r0 + threadIdx.x;
+        Span s{0, 0, true};
+        if (r < t.batch) {
+            copies[3 * r] = copies[3 * r + 1] = -1;
+            copies[3 * r + 2] = 0;
+            if (grant && !at_once) s = reserve_span(t, extra, page_size, r);
+        }
+        if (!at_once) over_span(r, s, mark);
+    }
+    if (!grant) return;
+    if (!at_once) __syncthreads();   // every mark is there before refs change
     int base = 0;
     for (int r0 = 0; r0 < t.batch; r0 += kTableThreads) {
         const int r = r0 + threadIdx.x;
@@ -316,33 +332,17 @@ __global__ void __launch_bounds__(kTableThreads)
         if (r < t.batch) s = reserve_span(t, extra, page_size, r);
         int* row = t.table + (size_t)r * t.max_pages;
         const bool shared_out = s.last - s.first > kLongSpan;
-        int count = 0;
-        if (!shared_out)
-            for (int j = s.first; j < s.last; ++j) count += row[j] < 0;
         const unsigned longs = __ballot_sync(0xffffffffu, shared_out);
-        for (unsigned todo = longs; todo != 0; todo &= todo - 1) {
-            const int from = __ffs(todo) - 1;
-            const int first = __shfl_sync(0xffffffffu, s.first, from);
-            const int last = __shfl_sync(0xffffffffu, s.last, from);
-            const int* its = t.table + (size_t)(r - lane + from) * t.max_pages;
-            int c = 0;
-            for (int j = first + lane; j < last; j += 32) c += its[j] < 0;
-            c = __reduce_add_sync(0xffffffffu, c);
-            if (lane == from) count = c;
-        }
+        const int count = at_once ? over_span(r, s, mark)
+                                  : over_span(r, s, [](const int* its, int j) { return its[j] < 0; });
         int total;
         int k = base + block_scan(count, scratch, total);
         base += total;
         const int used = r < t.batch ? max(t.lens[r], 0) % page_size : 0;
-        if (r < t.batch) {
-            copies[3 * r] = copies[3 * r + 1] = -1;
-            copies[3 * r + 2] = 0;
-        }
-        __syncwarp();   // before a warp fills in a long row's copy
         if (!shared_out)
             for (int j = s.first; j < s.last; ++j)
                 if (row[j] < 0)
-                    reserve_grant(t, row, r, j, grant ? free_list[k++] : -1, s.first, used, copies);
+                    reserve_grant(t, row, r, j, free_list[k++], s.first, used, copies);
         for (unsigned todo = longs; todo != 0; todo &= todo - 1) {
             const int from = __ffs(todo) - 1;
             const int first = __shfl_sync(0xffffffffu, s.first, from);
@@ -356,8 +356,8 @@ __global__ void __launch_bounds__(kTableThreads)
                 const unsigned who = __ballot_sync(0xffffffffu, take);
                 if (take)
                     reserve_grant(t, its, r - lane + from, j,
-                                  grant ? free_list[at + __popc(who & ((1u << lane) - 1u))] : -1,
-                                  first, its_used, copies);
+                                  free_list[at + __popc(who & ((1u << lane) - 1u))], first, its_used,
+                                  copies);
                 at += __popc(who);
             }
         }

@@ -107,6 +107,24 @@ def test_reserve_refuses_as_a_whole():
     s.reserve([0, 48, 0, 0])
 
 
+@pytest.mark.parametrize("entries,pages,extra", [(6, 12, [4, 4, 4]), (60, 16, [24, 4, 6])],
+                         ids=["short spans", "long spans"])
+def test_a_refused_reserve_leaves_entries_that_are_no_page(entries, pages, extra):
+    """Whatever they hold, that of a shared page's mark among it."""
+    s = State(3, entries, pages, 4, [6, 0, 9], seed=6)
+    assert s.fork([0], [1]) == 0
+    page = s.plain.table[0][0]
+    junk = [-2 - page, -2, pages, 2 ** 31 - 1, -2 ** 31, -1 - pages]
+    for b in range(3):
+        for j in range(3, entries):
+            s.plain.table[b][j] = junk[(b + j) % len(junk)]
+    s.table.copy_(i32(s.plain.table))
+    assert s.reserve([4 * entries - 6, 4, 4])[1] > 0     # pages are lacking
+    assert s.reserve([4, 4 * entries, 4])[1] == -2       # row 1 is too short
+    assert s.reserve(extra)[1] == 0
+    assert s.reserve([1, 1, 4 * entries])[1] == -3
+
+
 def test_long_spans_and_many_rows():
     g = torch.Generator().manual_seed(4)
     lens = torch.randint(0, 200, (1500,), generator=g).tolist()
