@@ -124,6 +124,15 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, int dev, const Stream& 
     return t;
 }
 
+// An input as a kernel on `stream` reads it: copied there where it is on the
+// device and not contiguous (the copy's memory is of that stream's pool, so that
+// it may go as soon as the call is enqueued).
+Tensor laid_out(const Tensor& t, int dev, const Stream& stream) {
+    if (!on(t, dev) || t.is_contiguous()) return t;
+    const c10::cuda::CUDAStreamGuard guard(torch_stream(stream, dev));
+    return t.clone(at::MemoryFormat::Contiguous);
+}
+
 // Sizes beyond int are refused here rather than cut.
 int small(int64_t n) {
     if (n > INT32_MAX) throw BadValue("a dimension exceeds 2^31 - 1");
@@ -192,7 +201,7 @@ PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // ---------------------------------------------------------- attention ----
 
 // q [B, Hq, n, d], keys and values of one shape [*, Hkv, m, d], sinks, out and
-// lse of an attention call.
+// lse of an attention call.  Lengths, tables and sinks come in any layout.
 struct Attention {
     Tensor q, k, v, out, lse;
     const float* sinks = nullptr;
@@ -200,16 +209,33 @@ struct Attention {
     int B, Hq, n, d;
 
     Stream stream;
+    Tensor held[4];   // copies of small inputs
+    int n_held = 0;
 
+    const Tensor& hold(const Tensor& t) {
+        if (t.is_contiguous()) return t;
+        held[n_held] = laid_out(t, dev, stream);
+        return held[n_held++];
+    }
+    int* lengths(const char* name, PyObject* o) {   // int32 [B], or nullptr for None
+        return o == Py_None ? nullptr : ints(name, hold(tensor(name, o)), {B}, dev);
+    }
+
+    // as_paged: with the contract of the paged decode call of the plain kind, which
+    // takes q and the caches in any layout too and raises ValueError for their type
     Attention(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* sinks_, PyObject* out_,
-              PyObject* lse_, PyObject* stream_)
+              PyObject* lse_, PyObject* stream_, bool as_paged = false)
         : q(tensor("q", q_)), k(tensor("k", k_)), v(tensor("v", v_)), dev(device_of("q", q)),
           stream(stream_of(stream_, dev)) {
+        if (as_paged)
+            for (Tensor* t : {&q, &k, &v}) *t = laid_out(*t, dev, stream);
         const char* names[3] = {"q", "k", "v"};
         const Tensor* all[3] = {&q, &k, &v};
         for (int i = 0; i < 3; ++i) {
-            if (all[i]->scalar_type() != at::kBFloat16)
+            if (all[i]->scalar_type() != at::kBFloat16) {
+                if (as_paged) throw BadValue("q and the caches must be bf16");
                 throw BadType(std::string(names[i]) + " must be bfloat16");
+            }
             if (!on(*all[i], dev) || all[i]->dim() != 4 || !all[i]->is_contiguous())
                 throw BadValue(std::string(names[i]) +
                                " must be a contiguous 4-D tensor on cuda:" + std::to_string(dev));
@@ -220,7 +246,7 @@ struct Attention {
         B = small(q.size(0)), Hq = small(q.size(1)), n = small(q.size(2)), d = small(q.size(3));
         if (sinks_ != Py_None)
             sinks = static_cast<const float*>(
-                dense("sinks", tensor("sinks", sinks_), at::kFloat, {Hq}, dev));
+                dense("sinks", hold(tensor("sinks", sinks_)), at::kFloat, {Hq}, dev));
         if (out_ == Py_None) {
             out = fresh(q.sizes(), at::kBFloat16, dev, stream);
         } else {
@@ -242,8 +268,8 @@ struct Pages {
     const int* table;
     int max_pages, page_size, num_pages, hkv;
 
-    Pages(const Attention& c, PyObject* table_) {
-        const Tensor& t = tensor("block_table", table_);
+    Pages(Attention& c, PyObject* table_) {
+        const Tensor& t = c.hold(tensor("block_table", table_));
         if (t.dim() != 2) throw BadValue("block_table must be [B, max_pages]");
         max_pages = small(t.size(1));
         table = ints("block_table", t, {c.B, t.size(1)}, c.dev);
@@ -258,14 +284,14 @@ struct TreeMask {
     int shared;
     const int* lens;
 
-    TreeMask(const Attention& c, PyObject* mask_, PyObject* lens_) {
+    TreeMask(Attention& c, PyObject* mask_, PyObject* lens_) {
         const Tensor& m = tensor("tree_mask", mask_);
         const int64_t w = (c.n + 31) / 32;
         shared = m.dim() == 2;
         words = reinterpret_cast<const unsigned int*>(
             shared ? ints("tree_mask", m, {c.n, w}, c.dev)
                    : ints("tree_mask", m, {c.B, c.n, w}, c.dev));
-        lens = ints_or_null("tree_lens", lens_, {c.B}, c.dev);
+        lens = c.lengths("tree_lens", lens_);
     }
 };
 
@@ -276,12 +302,12 @@ void same_batch(const Attention& c) {
 // q, k, v, tree_mask, scale, seqlens_k, tree_lens, sinks, out, lse, stream
 PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 11);
-    const Attention c(a[0], a[1], a[2], a[7], a[8], a[9], a[10]);
+    Attention c(a[0], a[1], a[2], a[7], a[8], a[9], a[10]);
     same_batch(c);
     const TreeMask m(c, a[3], a[6]);
     return c.result(fa_fwd_decode_tree(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
-        small(c.k.size(1)), c.n, small(c.k.size(2)), ints_or_null("seqlens_k", a[5], {c.B}, c.dev),
+        small(c.k.size(1)), c.n, small(c.k.size(2)), c.lengths("seqlens_k", a[5]),
         m.words, m.shared, m.lens, c.d, scale_of(a[4], c.d), c.sinks, c.stream));
 }
 
@@ -289,12 +315,12 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
 // sinks, out, lse, stream
 PyObject* decode_tree_paged(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 12);
-    const Attention c(a[0], a[1], a[2], a[8], a[9], a[10], a[11]);
+    Attention c(a[0], a[1], a[2], a[8], a[9], a[10], a[11]);
     const Pages p(c, a[3]);
     const TreeMask m(c, a[5], a[7]);
     return c.result(fa_fwd_decode_tree_paged(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
-        p.hkv, c.n, ints("seqlens_k", tensor("seqlens_k", a[4]), {c.B}, c.dev), p.table,
+        p.hkv, c.n, ints("seqlens_k", c.hold(tensor("seqlens_k", a[4])), {c.B}, c.dev), p.table,
         p.max_pages, p.page_size, p.num_pages, m.words, m.shared, m.lens, c.d,
         scale_of(a[6], c.d), c.sinks, c.stream));
 }
@@ -302,11 +328,11 @@ PyObject* decode_tree_paged(PyObject* const* a, Py_ssize_t n) {
 // q, k, v, scale, causal, seqlens_k, out, lse, stream, window, sinks, first
 PyObject* decode_first(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 12);
-    const Attention c(a[0], a[1], a[2], a[10], a[6], a[7], a[8]);
+    Attention c(a[0], a[1], a[2], a[10], a[6], a[7], a[8]);
     same_batch(c);
     return c.result(fa_fwd_decode_first(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
-        small(c.k.size(1)), c.n, small(c.k.size(2)), ints_or_null("seqlens_k", a[5], {c.B}, c.dev),
+        small(c.k.size(1)), c.n, small(c.k.size(2)), c.lengths("seqlens_k", a[5]),
         c.d, scale_of(a[3], c.d), truth("causal", a[4]), whole("window", a[9]),
         whole("first", a[11]), c.sinks, c.stream));
 }
@@ -315,11 +341,11 @@ PyObject* decode_first(PyObject* const* a, Py_ssize_t n) {
 // window, sinks, first
 PyObject* decode_paged_first(PyObject* const* a, Py_ssize_t n) {
     need_args(n, 13);
-    const Attention c(a[0], a[1], a[2], a[11], a[7], a[8], a[9]);
+    Attention c(a[0], a[1], a[2], a[11], a[7], a[8], a[9], true);
     const Pages p(c, a[3]);
     return c.result(fa_fwd_decode_paged_first(
         c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), c.out.data_ptr(), c.lse_ptr(), c.B, c.Hq,
-        p.hkv, c.n, ints("seqlens_k", tensor("seqlens_k", a[4]), {c.B}, c.dev), p.table,
+        p.hkv, c.n, ints("seqlens_k", c.hold(tensor("seqlens_k", a[4])), {c.B}, c.dev), p.table,
         p.max_pages, p.page_size, p.num_pages, c.d, scale_of(a[5], c.d),
         truth("causal", a[6]), whole("window", a[10]), whole("first", a[12]), c.sinks, c.stream));
 }
