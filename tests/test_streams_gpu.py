@@ -219,3 +219,41 @@ def test_serving_outputs_leave_memory_in_use_alone(name):
     torch.cuda.synchronize()
     check_device_error()
     assert all(bool((t == 7).all()) for t in now)
+
+
+def test_captured_calls_on_a_forked_stream():
+    """A captured step whose calls run on a stream of their own, their outputs
+    dropped inside the capture; replayed over other inputs."""
+    from attention_forward_blackwell_gb300 import binding
+    q, k, v = prompt(7)
+    q = q[:, :, :9].contiguous()
+    lens = i32([256])
+    parents = torch.arange(-1, 8, dtype=torch.int32, device="cuda")[None].contiguous()
+    win = dict(causal=True, window=30, first=3)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        mask = binding.tree_mask(parents, stream=side)
+        a = binding.decode_tree(q, k, v, mask, seqlens_k=lens, stream=side)[0]
+        b = binding.decode(q, k, v, seqlens_k=lens, stream=side, **win)[0]
+        c = binding.prefill(q, k, v, seqlens_k=lens, stream=side, **win)[0]
+        main.wait_stream(side)
+        return a + b + c
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed, n in ((8, 256), (9, 100)):
+        for t, new in zip((q, k, v), prompt(seed)):
+            t.copy_(new[:, :, :t.shape[2]])
+        lens.fill_(n)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, step())
+    torch.cuda.synchronize()
+    check_device_error()
