@@ -284,10 +284,10 @@ bool span_wins_prompt(int head_dim, int group, long long rows, long long keys, b
 // A tree or a window with first keys may join: splits of 64 keys or more in one
 // wave of CTAs, the splits of a pair a cluster, which merges them without a
 // second kernel and a workspace (7 query heads x 1,000 keys at head_dim 64: 8.8
-// -> 6.2 us; a window of 1,024 at 128: 8.8 -> 6.7).  Past 8 x 256 keys more
-// splits gain more (4,096 keys at head_dim 128: 15.2 us / 16.9 joined), and past
-// a wave the wait for the others costs more (512 pairs x 256 keys at 64: 19.6 /
-// 25.3).  With one CTA per SM (head_dim 256) few clusters of 7 or 8 find their
+// -> 6.2 us; a window of 1,024 at 128, keys in L2: 8.8 -> 6.7).  Past 8 x 256
+// keys more splits gain more (4,096 keys at head_dim 128: 15.2 us / 16.9 joined),
+// and past a wave the wait for the others costs more (512 pairs x 256 keys at 64:
+// 19.6 / 25.3).  With one CTA per SM (head_dim 256) few clusters of 7 or 8 find their
 // SMs in one GPC: 16 pairs x 8 splits took 28 us, two waves, 32 x 4 took 18.
 struct SplitPlan {
     int splits;

@@ -25,9 +25,9 @@
 // CTA hands its parts of the others' rows over to their shared memory and writes
 // its own share of the rows (DecodeArgs::joined): such calls are bound by
 // latencies, of the launch, the chain of loads and one barrier of the cluster,
-// not by bytes (7 query heads x 1,000 keys x 16 heads at head_dim 64 6.2 us a
-// call, 4.2 MB; a window of 1,024 over 8 heads at 128 6.7; with parts read from
-// the others between two barriers 6.8 and 7.2).
+// not by bytes (7 query heads x 1,000 keys x 16 heads at head_dim 64 6.1 us a
+// call, 4.2 MB; a window of 1,024 over 8 heads at 128 7.5, 6.7 with its keys in
+// L2; with parts read from the others between two barriers 0.5 to 0.6 more).
 #include "common.cuh"
 #include "ptx.cuh"
 

@@ -34,6 +34,10 @@
  *             and LSE = -infinity.
  *   Scale     must be finite and > 0 (typically 1/sqrt(head_dim)).
  *   LSE units natural log of the sum of exp(scaled score).
+ *   Precision scores, row maxima, sums and O are held in fp32.  A probability is
+ *             rounded to bf16 for the product with its value row (its place in
+ *             the sum is not), and O once at the end: with a = sum_j p_j |v_j|,
+ *             O is off by at most 2^-8 (|O| + a), plus terms of fp32 rounding.
  *   Streams   work is enqueued on `stream` (NULL = legacy default stream);
  *             the calls are asynchronous and never synchronise the device.
  *   Errors    argument checks run on the host before anything is enqueued;
@@ -313,7 +317,8 @@ fa_status fa_fwd_decode_paged_first(const void *q, const void *k_cache, const vo
  * they are masked.  head_dim 64, 128 or 256; nodes <= FA_TREE_MAX_NODES;
  * batch * hq * nodes * head_dim < 2^31.  Scratch is stream-ordered, as in
  * fa_fwd_decode.  The paged call takes the caches, block table and page sizes
- * of fa_fwd_decode_paged.
+ * of fa_fwd_decode_paged; as in fa_fwd_decode_paged_first, keys j < L_b whose
+ * entry is no page read as zeros or as rows of some page of the caches.
  */
 fa_status fa_fwd_decode_tree(const void *q, const void *k, const void *v, void *o, float *lse,
                              int batch, int hq, int hkv, int nodes, int sk, const int *seqlens_k,
