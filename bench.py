@@ -63,12 +63,12 @@ KERNEL_SOURCES = {
 
 CAPTURED_TRAFFIC = {
     # kernel: (sources sha256, workload, bytes per launch)
-    "prefill": ("ca8ce4fc495c8cf639e592fa7e41c5f9bc1c7ab5cd3e756b10f5caf1d1e82c4a",
-                "long_prefill_b1_h16_s8192_d128", 115318784),
-    # captured at batch 16 (463.37 MB, 1.016 x its algorithmic bytes) and
+    "prefill": ("aba11ed3790bfc31511b50a6997222cd977da230d2d64aeccd516d2f6be093a9",
+                "long_prefill_b1_h16_s8192_d128", 115373312),
+    # captured at batch 16 (463.35 MB, 1.016 x its algorithmic bytes) and
     # scaled to batch 64 by the algorithmic bytes of the two batches
-    "decode": ("ccd599648da5bf7362660bbc0cec8064d7d58bbb3bbbf9b740dd3e00fb8d8580",
-               "decode_gqa_b64_hq64_hkv8_d128", 2204044931),
+    "decode": ("1d4b712e6b279783506827cb0a91e71a38f90a602712c861342c3b02dd0fc90b",
+               "decode_gqa_b64_hq64_hkv8_d128", 2203971027),
 }
 
 
