@@ -40,7 +40,7 @@ def same(call, args, kw, wide_args, wide_kw, **more):
     got = call(*wide_args, **wide_kw, **more)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    torch.cuda._sleep(20_000_000)
+    torch.cuda._sleep(100_000_000)
     late = call(*wide_args, **wide_kw, **more, stream=side)
     side.synchronize()
     assert not torch.cuda.current_stream().query()

@@ -7,7 +7,7 @@ from gpu_parity import check_device_error, free_cuda
 
 pytestmark = pytest.mark.gpu
 
-BUSY = 20_000_000   # cycles that a stream sleeps: far longer than any call here
+BUSY = 100_000_000   # cycles that a stream sleeps: far longer than any call here
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -143,6 +143,7 @@ def test_inputs_of_other_layouts_are_copied_on_the_calls_stream():
     win = dict(causal=True, window=30, first=3)
     want = binding.prefill(q, k, v, seqlens_k=lens, sinks=sinks, **win)
     wide = strided(lens), strided(sinks)
+    binding.prefill(q, k, v, seqlens_k=wide[0], sinks=wide[1], **win)   # (every kernel loaded)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
     torch.cuda._sleep(BUSY)
@@ -257,3 +258,22 @@ def test_captured_calls_on_a_forked_stream():
         assert torch.equal(got, step())
     torch.cuda.synchronize()
     check_device_error()
+
+
+@pytest.mark.parametrize("name", NAMES + ["tree_mask", "decode_tree_paged"])
+def test_calls_on_the_default_stream_from_another(name):
+    """The call's stream is the legacy default one, the current one is not."""
+    if name in NAMES:
+        args = inputs(name, 10)
+        call = lambda **m: calls()[name](*args, **m)
+    else:
+        call = serving()[name]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = call(stream=torch.cuda.default_stream())
+        torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+        got = [t.clone() for t in got]
+    torch.cuda.synchronize()
+    check_device_error()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
