@@ -61,6 +61,16 @@ SIGNATURES = {
                              _VP, _VP, _VP]),
     "fa_cache_copy": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I, _VP]),
     "fa_cache_compact": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I, _VP, _I, _VP, _I, _VP, _VP]),
+    "fa_rope": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _LL, _VP, _I,
+                     _I, _I, _F, _VP]),
+    "fa_cache_append_rope": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I, _VP, _I, _VP, _VP, _VP, _VP, _I,
+                                  _VP, _VP, _VP, _VP]),
+    "fa_cache_append_q8": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _I, _VP, _I, _VP, _VP, _VP,
+                                _VP, _I, _VP, _VP, _VP, _VP]),
+    "fa_cache_read_q8": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _VP, _I, _VP, _I, _I, _I, _VP,
+                              _VP, _VP]),
+    "fa_fwd_decode_paged_q8": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _I, _I,
+                                    _I, _I, _I, _F, _I, _I, _I, _VP, _VP]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_get_device_error": (_I, [_VP]),
     "fa_get_device_error_word": (_I, [_VP, ctypes.POINTER(ctypes.c_uint)]),
@@ -545,6 +555,128 @@ def cache_compact(k_cache, v_cache, block_table, start, keep, n_keep, stream=Non
     st = _serving().cache_compact(k_cache, v_cache, block_table, start, keep, n_keep, _handle(stream))
     if st != FA_OK:
         raise FaError(st, "fa_cache_compact")
+
+
+# ------------------------------------------------- rotated positions, 8-bit caches ----
+
+class Turn(ctypes.Structure):
+    """``fa_turn`` (see fa.h), for callers of the C ABI."""
+    _fields_ = [("freqs", _VP), ("rot", _I), ("interleaved", _I), ("factor", _F), ("positions", _VP),
+                ("position_stride", _LL), ("q", _VP), ("q_strides", _VP), ("q_out", _VP), ("hq", _I)]
+
+
+def rope_inv_freq(rot, base=10000.0, method=None, stretch=1.0, original=None, fast=32.0, slow=1.0):
+    """Radians a position of the rot / 2 pairs of a rotation, float64 on the host, and the factor
+    that ``rope`` and the appends take with them: (inv_freq, factor).
+
+    w_i = base^(-2 i / rot), for contexts ``stretch`` times as long as the original:
+      None      w_i
+      "linear"  w_i / stretch: every position interpolated
+      "ntk"     with the base times stretch^(rot / (rot - 2)): the slowest pair interpolated, the
+                fastest kept
+      "yarn"    pairs that turn ``fast`` times or more in ``original`` positions keep w_i, those that
+                turn ``slow`` times or less take w_i / stretch, linearly in the number of turns in
+                between; factor 0.1 ln(stretch) + 1
+    """
+    if rot <= 0 or rot % 2:
+        raise ValueError("rot must be positive and even")
+    if not base > 0 or not stretch > 0:
+        raise ValueError("base and stretch must be positive")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if method == "ntk":
+        if rot < 4:
+            raise ValueError('"ntk" needs two pairs')
+        base = base * stretch ** (rot / (rot - 2))
+    w = float(base) ** (-2.0 * i / rot)
+    if method is None or method == "ntk":
+        return w, 1.0
+    if method == "linear":
+        return w / stretch, 1.0
+    if method == "yarn":
+        if original is None or not original > 0 or not fast > slow:
+            raise ValueError('"yarn" needs the original context and fast > slow')
+        keep = ((original * w / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        return w * (keep + (1.0 - keep) / stretch), 0.1 * math.log(stretch) + 1.0 if stretch > 1 else 1.0
+    raise ValueError(f"unknown method {method!r}")
+
+
+def rope_freqs(inv_freq, device="cuda"):
+    """The table that ``rope`` and the appends take, int64 [rot / 2]: radians a position (numbers or a
+    float64 tensor) in units of 2^-64 of a turn, so that the angle of a far position is exact modulo a
+    turn."""
+    values = inv_freq.tolist() if isinstance(inv_freq, torch.Tensor) else [float(w) for w in inv_freq]
+    if not all(math.isfinite(w) for w in values):
+        raise ValueError("inv_freq must be finite")
+    turns = [round(math.fmod(w / (2 * math.pi), 1.0) * 2 ** 64) % 2 ** 64 for w in values]
+    return torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64,
+                        device=device)
+
+
+def rope(q, k, positions, freqs, interleaved=False, inverse=False, factor=1.0, q_out=None, k_out=None,
+         stream=None):
+    """Queries and keys turned by their positions through ``fa_rope``: q and k (or None) bf16
+    [T, heads, d] with int32 positions [T], or [B, heads, n, d] with positions [B, n] or [n]; the first
+    2 freqs.numel() elements of a row are turned (``rope_freqs``), as pairs (i, i + rot / 2) or, with
+    ``interleaved``, (2 i, 2 i + 1), times ``factor``.  Any strides; an output may be its input.
+    ``inverse`` turns back: the gradient of the inputs from that of the outputs.  Returns (q_out,
+    k_out)."""
+    r = _serving().rope(q, k, positions, freqs, interleaved, inverse, factor, q_out, k_out, _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_rope")
+    return r
+
+
+def cache_append_rope(k_cache, v_cache, block_table, seqlens, k_new, v_new, freqs, n_new=None, copies=None,
+                      positions=None, q=None, q_out=None, interleaved=False, factor=1.0, stream=None):
+    """``cache_append`` with keys turned on the way through ``fa_cache_append_rope``: row i of sequence b
+    by position seqlens[b] + i, or positions int32 [B, n] or [n] (a tree's nodes by their depth); see
+    ``rope``.  Queries q [B, Hq, n, d] of the same rows are turned in the same launch: returns q_out
+    [B, Hq, n, d], whose rows past n_new[b] are not written (None without q)."""
+    r = _serving().cache_append_rope(k_cache, v_cache, block_table, seqlens, k_new, v_new, freqs, n_new, copies,
+                                     positions, q, q_out, interleaved, factor, _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_cache_append_rope")
+    return r
+
+
+def cache_append_q8(k_cache, v_cache, k_scale, v_scale, block_table, seqlens, k_new, v_new, freqs=None,
+                    n_new=None, copies=None, positions=None, q=None, q_out=None, interleaved=False,
+                    factor=1.0, stream=None):
+    """Appends to a paged cache held in 8 bits through ``fa_cache_append_q8``: k_cache, v_cache
+    [num_pages, Hkv, page_size, d] float8_e4m3fn, k_scale, v_scale fp32 [num_pages, Hkv, page_size /
+    block].  Rows and keys as in ``cache_append``; keys are turned where freqs is given, and q beside
+    them, as in ``cache_append_rope``.  Scales are powers of two that grow with their block's rows; codes
+    written before are taken along.  Returns q_out (None without q)."""
+    r = _serving().cache_append_q8(k_cache, v_cache, k_scale, v_scale, block_table, seqlens, k_new, v_new,
+                                   freqs, n_new, copies, positions, q, q_out, interleaved, factor,
+                                   _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_cache_append_q8")
+    return r
+
+
+def cache_read_q8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, total, max_seqlen,
+                  k_out=None, v_out=None, stream=None):
+    """The first cu_seqlens[b + 1] - cu_seqlens[b] keys and values of every sequence of an 8-bit cache as
+    bf16, packed [total, Hkv, d] (what ``prefill_varlen`` takes), through ``fa_cache_read_q8``; returns
+    (k, v).  max_seqlen is at least the longest length."""
+    r = _serving().cache_read_q8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, total, max_seqlen,
+                                 k_out, v_out, _handle(stream))
+    if type(r) is int:
+        raise FaError(r, "fa_cache_read_q8")
+    return r
+
+
+def decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, scale=None, causal=False,
+                    out=None, lse=None, stream=None, window=0, sinks=None, first=0):
+    """``decode_paged`` over a paged cache held in 8 bits (see ``cache_append_q8``) through
+    ``fa_fwd_decode_paged_q8``: q [B, Hq, n, d] bf16, n <= 16, optionally with a sliding ``window`` > 0,
+    whose ``first`` keys stay visible, and per-head ``sinks``; returns (o, lse)."""
+    r = _serving().decode_paged_q8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, scale, causal,
+                                   out, lse, _handle(stream), window or 0, sinks, first)
+    if type(r) is int:
+        raise FaError(r, "fa_fwd_decode_paged_q8")
+    return r
 
 
 def get_device_error(stream=None) -> int:

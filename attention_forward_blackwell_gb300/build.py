@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(HERE, "libfa_gb300.so")
 BIND_PATH = os.path.join(HERE, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ["prefill_d512.cu", "prefill_d128.cu", "prefill_d256.cu", "prefill_d96.cu",
            "prefill_d64.cu", "decode.cu", "selftest.cu", "api.cu", "decode_noalloc.cu", "cache.cu",
-           "span.cu"]
+           "span.cu", "rope.cu", "cache_q8.cu", "decode_q8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
                 "-I", CSRC, "-I", INCLUDE]

@@ -587,6 +587,82 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     return FA_OK;
 }
 
+// Decode over a paged cache of 8 bits (decode_q8.cu): equal splits as those of
+// the split-KV kernel, of the positions that a sequence's rows can see.
+fa_status decode_q8_impl(const void* q, const void* k, const void* v, const float* k_scale,
+                         const float* v_scale, void* o, float* lse, int batch, int hq, int hkv, int sq,
+                         const int* seqlens_k, const int* block_table, int max_pages, int page_size,
+                         int num_pages, int block, int head_dim, float scale, int causal, int window,
+                         int first, const float* sinks, fa_stream_t stream) {
+    fa_status st = check_paged(seqlens_k, block_table, max_pages, page_size, num_pages, batch, hq, sq);
+    if (st != FA_OK) return st;
+    Common c;
+    const int sk = max_pages * page_size;
+    st = check_common(q, k, v, o, lse, batch, hq, hkv, sq, sk, scale, c);
+    if (st != FA_OK || c.noop) return st;
+    if (sq > FA_DECODE_MAX_SQ || first < 0) return FA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FA_ERR_UNSUPPORTED;
+    if (!k_scale || !v_scale || block <= 0 || page_size % block != 0) return FA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(k_scale), static_cast<const void*>(v_scale),
+                          static_cast<const void*>(sinks)})
+        if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_MISALIGNED;
+    // (rows of the cache, and of the outputs, are counted in 32 bits)
+    if ((double)num_pages * hkv * page_size >= 4294967296.0) return FA_ERR_INVALID_ARG;
+    if ((long long)batch * hq * sq >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    const DeviceInfo* di = device_info();
+    if (!di) return FA_ERR_CUDA;
+    if (!di->supported) return FA_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    DecodeQ8Args a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint8_t*>(k);
+    a.v = static_cast<const uint8_t*>(v);
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.o = static_cast<uint16_t*>(o);
+    a.lse = lse;
+    a.seqlens_k = seqlens_k;
+    a.B = batch;
+    a.Hq = hq;
+    a.Hkv = hkv;
+    a.Sq = sq;
+    a.Sk = sk;
+    a.group = hq / hkv;
+    a.rows = a.group * sq;
+    const int tile = decode_q8_tile(head_dim, a.rows);
+    a.tiles = (a.rows + tile - 1) / tile;
+    if ((long long)hkv * a.tiles > 65535) return FA_ERR_INVALID_ARG;
+    a.causal = causal ? 1 : 0;
+    a.window = window_of(window, sk);
+    a.first = window > 0 ? std::min(first, sk) : 0;
+    a.sinks = sinks;
+    a.block_table = block_table;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.block = block;
+    a.blocks = page_size / block;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const long long heads_first = (a.first + 63ll) / 64 * 64;
+    const long long span = window > 0 ? std::min<long long>(sk, (long long)window + sq + 62 + heads_first) : sk;
+    const long long pairs = (long long)batch * hkv * a.tiles;
+    const SplitPlan plan = split_plan(true, head_dim, pairs, span, di->num_sms);
+    a.chunk = (int)(((span + plan.splits - 1) / plan.splits + 63) / 64 * 64);
+    a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
+    a.joined = plan.joined ? 1 : 0;
+    if (a.joined) return from_cuda(launch_decode_q8(a, head_dim, s));
+    const size_t parts = (size_t)a.n_splits * batch * hq * sq;
+    char* ws = nullptr;
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), parts * (head_dim + 1) * sizeof(float), s) !=
+        cudaSuccess)
+        return FA_ERR_CUDA;
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.part_lse = a.part_o + parts * head_dim;
+    const cudaError_t e = launch_decode_q8(a, head_dim, s);
+    if (cudaFreeAsync(ws, s) != cudaSuccess) return FA_ERR_CUDA;
+    return from_cuda(e);
+}
+
 // Prefill on contiguous K/V (block_table == nullptr) or on paged caches
 // [num_pages, hkv, page_size, d] (sk = max_pages * page_size keys per sequence).
 // Dense, paged (block_table != nullptr) or packed (vl != nullptr; sq is then
@@ -932,6 +1008,17 @@ fa_status fa_fwd_decode_tree_paged(const void* q, const void* k_cache, const voi
     return decode_impl(q, k_cache, v_cache, o, lse, batch, hq, hkv, nodes, max_pages * page_size,
                        seqlens_k, head_dim, scale, 0, 0, sinks, 0, stream, block_table, max_pages,
                        page_size, num_pages, 0, &tree);
+}
+
+fa_status fa_fwd_decode_paged_q8(const void* q, const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale, void* o, float* lse,
+                                 int batch, int hq, int hkv, int sq, const int* seqlens_k,
+                                 const int* block_table, int max_pages, int page_size, int num_pages,
+                                 int block, int head_dim, float scale, int causal, int window,
+                                 int first, const float* sinks, fa_stream_t stream) {
+    return decode_q8_impl(q, k_cache, v_cache, k_scale, v_scale, o, lse, batch, hq, hkv, sq, seqlens_k,
+                          block_table, max_pages, page_size, num_pages, block, head_dim, scale, causal,
+                          window, first, sinks, stream);
 }
 
 fa_status fa_fwd_decode_splits(const void* q, const void* k, const void* v, void* o, float* lse,

@@ -20,8 +20,10 @@
 #include <cmath>
 #include <exception>
 #include <initializer_list>
+#include <optional>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/fa.h"
 
@@ -223,8 +225,10 @@ struct Attention {
 
     // as_paged: with the contract of the paged decode call of the plain kind, which
     // takes q and the caches in any layout too and raises ValueError for their type
+    // kv: type of the keys and values
     Attention(PyObject* q_, PyObject* k_, PyObject* v_, PyObject* sinks_, PyObject* out_,
-              PyObject* lse_, PyObject* stream_, bool as_paged = false)
+              PyObject* lse_, PyObject* stream_, bool as_paged = false,
+              at::ScalarType kv = at::kBFloat16)
         : q(tensor("q", q_)), k(tensor("k", k_)), v(tensor("v", v_)), dev(device_of("q", q)),
           stream(stream_of(stream_, dev)) {
         if (as_paged)
@@ -232,7 +236,9 @@ struct Attention {
         const char* names[3] = {"q", "k", "v"};
         const Tensor* all[3] = {&q, &k, &v};
         for (int i = 0; i < 3; ++i) {
-            if (all[i]->scalar_type() != at::kBFloat16) {
+            if (all[i]->scalar_type() != (i == 0 ? at::kBFloat16 : kv)) {
+                if (kv != at::kBFloat16)
+                    throw BadValue("q must be bf16 and the caches " + std::string(c10::toString(kv)));
                 if (as_paged) throw BadValue("q and the caches must be bf16");
                 throw BadType(std::string(names[i]) + " must be bfloat16");
             }
@@ -439,15 +445,16 @@ struct Caches {
     int dev, num_pages, hkv, page_size, d;
     void *k, *v;
 
-    Caches(PyObject* k_, PyObject* v_) {
+    Caches(PyObject* k_, PyObject* v_, at::ScalarType type = at::kBFloat16) {
         const Tensor& kc = tensor("k_cache", k_);
         const Tensor& vc = tensor("v_cache", v_);
         dev = device_of("k_cache", kc);
-        if (kc.scalar_type() != at::kBFloat16 || vc.scalar_type() != at::kBFloat16 ||
+        if (kc.scalar_type() != type || vc.scalar_type() != type ||
             kc.dim() != 4 || vc.sizes() != kc.sizes() || !on(vc, dev) || !kc.is_contiguous() ||
             !vc.is_contiguous())
-            throw BadValue("the caches must be contiguous bf16 tensors of one shape "
-                           "[num_pages, Hkv, page_size, d] on cuda:" +
+            throw BadValue(std::string("the caches must be contiguous ") +
+                           (type == at::kBFloat16 ? "bf16" : c10::toString(type)) +
+                           " tensors of one shape [num_pages, Hkv, page_size, d] on cuda:" +
                            std::to_string(dev));
         num_pages = small(kc.size(0)), hkv = small(kc.size(1));
         page_size = small(kc.size(2)), d = small(kc.size(3));
@@ -460,19 +467,23 @@ struct Caches {
 // a contiguous last dimension; others are copied first, on the call's stream
 // (whose pool the copy then belongs to: it may go as soon as the call is
 // enqueued).
+bool rows_fit(const Tensor& t) {
+    const int64_t last = t.dim() - 1;
+    int64_t all = 0;
+    for (int64_t i = 0; i < last; ++i) all |= t.stride(i);
+    return t.stride(last) == 1 && (all & 7) == 0 && (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0;
+}
 struct Rows {
     Tensor t;
     long long strides[3];
 
-    Rows(const char* name, PyObject* o, const Caches& c, int64_t B, int64_t n, const Stream& stream)
+    Rows(const char* name, PyObject* o, const Caches& c, int64_t heads, int64_t B, int64_t n,
+         const Stream& stream)
         : t(tensor(name, o)) {
-        if (t.scalar_type() != at::kBFloat16 || !has_shape(t, {B, c.hkv, n, c.d}) || !on(t, c.dev))
+        if (t.scalar_type() != at::kBFloat16 || !has_shape(t, {B, heads, n, c.d}) || !on(t, c.dev))
             throw BadValue(std::string(name) + " must be a bf16 tensor " +
-                           text({B, c.hkv, n, c.d}) + " on cuda:" + std::to_string(c.dev));
-        const bool fits = t.stride(3) == 1 &&
-                          ((t.stride(0) | t.stride(1) | t.stride(2)) & 7) == 0 &&
-                          (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15) == 0;
-        if (!fits) {
+                           text({B, heads, n, c.d}) + " on cuda:" + std::to_string(c.dev));
+        if (!rows_fit(t)) {
             const c10::cuda::CUDAStreamGuard guard(torch_stream(stream, c.dev));
             t = t.clone(at::MemoryFormat::Contiguous);
         }
@@ -490,7 +501,7 @@ PyObject* cache_append(PyObject* const* a, Py_ssize_t n) {
         throw BadValue("block_table must be [B, max_pages], k_new and v_new [B, Hkv, n, d]");
     const int64_t B = table.size(0), m = kn.size(2);
     const Stream stream = stream_of(a[8], c.dev);
-    const Rows k("k_new", a[4], c, B, m, stream), v("v_new", a[5], c, B, m, stream);
+    const Rows k("k_new", a[4], c, c.hkv, B, m, stream), v("v_new", a[5], c, c.hkv, B, m, stream);
     return PyLong_FromLong(fa_cache_append(
         c.k, c.v, c.num_pages, c.hkv, c.page_size, c.d,
         ints("block_table", table, {B, table.size(1)}, c.dev), small(table.size(1)),
@@ -528,12 +539,284 @@ PyObject* cache_compact(PyObject* const* a, Py_ssize_t n) {
         ints("n_keep", tensor("n_keep", a[5]), {B}, c.dev), stream_of(a[6], c.dev)));
 }
 
+// ---------------------------------------------------- rotated positions ----
+
+float factor_of(PyObject* o) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        throw BadType("factor must be a number");
+    }
+    return static_cast<float>(x);
+}
+
+// Frequencies int64 [rot / 2], or none.
+struct Freqs {
+    Tensor t;
+    const long long* p = nullptr;
+    int rot = 0;
+
+    Freqs(PyObject* o, int dev, const Stream& stream, bool optional) {
+        if (o == Py_None && optional) return;
+        t = laid_out(tensor("freqs", o), dev, stream);
+        if (t.dim() != 1) throw BadValue("freqs must be [rot / 2]");
+        p = static_cast<const long long*>(dense("freqs", t, at::kLong, {t.size(0)}, dev));
+        rot = small(2 * t.size(0));
+    }
+};
+
+// Positions int32 [B, n], or [n] for every batch entry.
+struct Positions {
+    Tensor t;
+    const int* p = nullptr;
+    long long stride = 0;
+
+    Positions(PyObject* o, int64_t B, int64_t n, int dev, const Stream& stream) {
+        t = laid_out(tensor("positions", o), dev, stream);
+        if (t.dim() == 2) {
+            p = ints("positions", t, {B, n}, dev);
+            stride = n;
+        } else {
+            p = ints("positions", t, {n}, dev);
+        }
+    }
+    Positions() = default;
+};
+
+// Rows to turn: [T, heads, d] or [B, heads, n, d] with the strides of batch, head
+// and token; and where they go.
+struct Turned {
+    Tensor in, out;
+    long long is[3], os[3];
+    int heads = 0;
+
+    static void strides_of(const Tensor& t, long long (&s)[3]) {
+        const bool packed = t.dim() == 3;
+        s[0] = packed ? 0 : t.stride(0);
+        s[1] = t.stride(1);
+        s[2] = packed ? t.stride(0) : t.stride(2);
+    }
+    static std::pair<uintptr_t, uintptr_t> range(const Tensor& t) {   // of addresses
+        uintptr_t lo = reinterpret_cast<uintptr_t>(t.data_ptr()), hi = lo + 2;
+        for (int64_t i = 0; i < t.dim(); ++i) hi += 2 * (t.size(i) - 1) * t.stride(i);
+        return {lo, hi};
+    }
+
+    Turned(const char* name, PyObject* in_, const char* out_name, PyObject* out_, int dev,
+           const Stream& stream)
+        : in(tensor(name, in_)) {
+        if (in.scalar_type() != at::kBFloat16) throw BadType(std::string(name) + " must be bfloat16");
+        if (!on(in, dev) || (in.dim() != 3 && in.dim() != 4))
+            throw BadValue(std::string(name) + " must be [T, heads, d] or [B, heads, n, d] on cuda:" +
+                           std::to_string(dev));
+        heads = small(in.size(1));
+        if (out_ == Py_None) {
+            out = fresh(in.sizes(), at::kBFloat16, dev, stream);
+        } else {
+            out = tensor(out_name, out_);
+            if (out.scalar_type() != at::kBFloat16 || out.sizes() != in.sizes() || !on(out, dev))
+                throw BadValue(std::string(out_name) + " must be a bf16 tensor " + text(in.sizes()) +
+                               " on cuda:" + std::to_string(dev));
+            bool apart = rows_fit(out);   // (no element twice)
+            for (int64_t i = 0; i < out.dim(); ++i) apart &= out.size(i) < 2 || out.stride(i) != 0;
+            if (!apart)
+                throw BadValue(std::string(out_name) + " must have contiguous, 16-byte aligned rows");
+            if (in.numel() > 0 && (in.data_ptr() != out.data_ptr() || in.strides() != out.strides())) {
+                const auto x = range(in), y = range(out);
+                if (x.first < y.second && y.first < x.second)
+                    throw BadValue(std::string(out_name) + " must be " + name + " itself or lie apart from it");
+            }
+        }
+        if (!rows_fit(in)) {
+            const c10::cuda::CUDAStreamGuard guard(torch_stream(stream, dev));
+            in = in.clone(at::MemoryFormat::Contiguous);
+        }
+        strides_of(in, is);
+        strides_of(out, os);
+    }
+};
+
+// q, k, positions, freqs, interleaved, inverse, factor, q_out, k_out, stream
+PyObject* rope(PyObject* const* a, Py_ssize_t n) {
+    need_args(n, 10);
+    const int dev = device_of("q", tensor("q", a[0]));
+    const Stream stream = stream_of(a[9], dev);
+    const Turned q("q", a[0], "q_out", a[7], dev, stream);
+    std::optional<Turned> k;
+    if (a[1] != Py_None) k.emplace("k", a[1], "k_out", a[8], dev, stream);
+    const Tensor& x = q.in;
+    const bool packed = x.dim() == 3;
+    if (k && (k->in.dim() != x.dim() || k->in.size(0) != x.size(0) ||
+              k->in.size(x.dim() - 1) != x.size(x.dim() - 1) || (!packed && k->in.size(2) != x.size(2))))
+        throw BadValue("k " + text(k->in.sizes()) + " does not go with q " + text(x.sizes()));
+    const int64_t B = packed ? 1 : x.size(0), rows = packed ? x.size(0) : x.size(2);
+    const Positions at(a[2], B, rows, dev, stream);
+    const Freqs f(a[3], dev, stream, false);
+    const fa_status st = fa_rope(
+        x.data_ptr(), q.is, q.out.data_ptr(), q.os, q.heads, k ? k->in.data_ptr() : nullptr,
+        k ? k->is : nullptr, k ? k->out.data_ptr() : nullptr, k ? k->os : nullptr, k ? k->heads : 0,
+        small(B), small(rows), small(x.size(x.dim() - 1)), at.p, at.stride, f.p, f.rot,
+        truth("interleaved", a[4]), truth("inverse", a[5]), factor_of(a[6]), stream);
+    if (st != FA_OK) return PyLong_FromLong(st);
+    PyObject* qo = THPVariable_Wrap(q.out);
+    PyObject* ko = k ? THPVariable_Wrap(k->out) : Py_NewRef(Py_None);
+    PyObject* both = PyTuple_Pack(2, qo, ko);
+    Py_DECREF(qo);
+    Py_DECREF(ko);
+    return both;
+}
+
+// What the appends of turned rows share: block_table, seqlens, k_new, v_new,
+// freqs, n_new, copies, positions, q, q_out, interleaved, factor from a[0] on.
+struct Append {
+    int64_t B, n;
+    int max_pages;
+    const int *table, *lens, *n_new, *copies;
+    std::optional<Rows> k, v, q;
+    std::optional<Freqs> freqs;
+    Positions at;
+    Tensor q_out;
+    fa_turn turn{};
+
+    Append(PyObject* const* a, const Caches& c, const Stream& stream, bool freqs_optional) {
+        const Tensor& t = tensor("block_table", a[0]);
+        const Tensor& kn = tensor("k_new", a[2]);
+        if (t.dim() != 2 || kn.dim() != 4)
+            throw BadValue("block_table must be [B, max_pages], k_new and v_new [B, Hkv, n, d]");
+        B = t.size(0), n = kn.size(2);
+        max_pages = small(t.size(1));
+        table = ints("block_table", t, {B, t.size(1)}, c.dev);
+        lens = ints("seqlens", tensor("seqlens", a[1]), {B}, c.dev);
+        k.emplace("k_new", a[2], c, c.hkv, B, n, stream);
+        v.emplace("v_new", a[3], c, c.hkv, B, n, stream);
+        freqs.emplace(a[4], c.dev, stream, freqs_optional);
+        n_new = ints_or_null("n_new", a[5], {B}, c.dev);
+        copies = ints_or_null("copies", a[6], {B, 3}, c.dev);
+        if (a[7] != Py_None) at = Positions(a[7], B, n, c.dev, stream);
+        if (a[8] != Py_None) {
+            const Tensor& qn = tensor("q", a[8]);
+            if (qn.dim() != 4) throw BadValue("q must be [B, Hq, n, d]");
+            q.emplace("q", a[8], c, qn.size(1), B, n, stream);
+            turn.hq = small(qn.size(1));
+            if (a[9] == Py_None) {
+                q_out = fresh({B, qn.size(1), n, c.d}, at::kBFloat16, c.dev, stream);
+            } else {
+                q_out = tensor("q_out", a[9]);
+                dense("q_out", q_out, at::kBFloat16, {B, qn.size(1), n, c.d}, c.dev);
+            }
+            turn.q = q->t.data_ptr();
+            turn.q_strides = q->strides;
+            turn.q_out = q_out.data_ptr();
+        } else if (a[9] != Py_None) {
+            throw BadValue("q_out without q");
+        }
+        turn.freqs = freqs->p;
+        turn.rot = freqs->rot;
+        turn.interleaved = truth("interleaved", a[10]);
+        turn.factor = factor_of(a[11]);
+        turn.positions = at.p;
+        turn.position_stride = at.stride;
+    }
+    PyObject* result(fa_status st) const {
+        if (st != FA_OK) return PyLong_FromLong(st);
+        return q ? THPVariable_Wrap(q_out) : Py_NewRef(Py_None);
+    }
+};
+
+// k_cache, v_cache, then Append's twelve, stream
+PyObject* cache_append_rope(PyObject* const* a, Py_ssize_t n) {
+    need_args(n, 15);
+    const Caches c(a[0], a[1]);
+    const Stream stream = stream_of(a[14], c.dev);
+    const Append x(a + 2, c, stream, false);
+    return x.result(fa_cache_append_rope(
+        c.k, c.v, c.num_pages, c.hkv, c.page_size, c.d, x.table, x.max_pages, x.lens, small(x.B),
+        x.k->t.data_ptr(), x.k->strides, x.v->t.data_ptr(), x.v->strides, small(x.n), x.n_new,
+        x.copies, &x.turn, stream));
+}
+
+// -------------------------------------------------------- 8-bit caches ----
+
+// Scales fp32 [num_pages, Hkv, page_size / block] of both caches.
+struct Scales {
+    float *k, *v;
+    int block;
+
+    Scales(PyObject* k_, PyObject* v_, const Tensor& cache, int dev) {
+        const Tensor& ks = tensor("k_scale", k_);
+        const Tensor& vs = tensor("v_scale", v_);
+        const int64_t blocks = ks.dim() == 3 ? ks.size(2) : 0, page = cache.size(2);
+        if (blocks < 1 || page % blocks != 0)
+            throw BadValue("k_scale must be [num_pages, Hkv, page_size / block]");
+        k = static_cast<float*>(dense("k_scale", ks, at::kFloat, {cache.size(0), cache.size(1), blocks}, dev));
+        v = static_cast<float*>(dense("v_scale", vs, at::kFloat, {cache.size(0), cache.size(1), blocks}, dev));
+        block = small(page / blocks);
+    }
+};
+
+// k_cache, v_cache, k_scale, v_scale, then Append's twelve, stream
+PyObject* cache_append_q8(PyObject* const* a, Py_ssize_t n) {
+    need_args(n, 17);
+    const Caches c(a[0], a[1], at::kFloat8_e4m3fn);
+    const Scales s(a[2], a[3], tensor("k_cache", a[0]), c.dev);
+    const Stream stream = stream_of(a[16], c.dev);
+    const Append x(a + 4, c, stream, true);
+    return x.result(fa_cache_append_q8(
+        c.k, c.v, s.k, s.v, c.num_pages, c.hkv, c.page_size, s.block, c.d, x.table, x.max_pages, x.lens,
+        small(x.B), x.k->t.data_ptr(), x.k->strides, x.v->t.data_ptr(), x.v->strides, small(x.n), x.n_new,
+        x.copies, &x.turn, stream));
+}
+
+// k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, total, max_seqlen,
+// k_out, v_out, stream
+PyObject* cache_read_q8(PyObject* const* a, Py_ssize_t n) {
+    need_args(n, 11);
+    const Caches c(a[0], a[1], at::kFloat8_e4m3fn);
+    const Scales s(a[2], a[3], tensor("k_cache", a[0]), c.dev);
+    const Stream stream = stream_of(a[10], c.dev);
+    const Tensor table = laid_out(tensor("block_table", a[4]), c.dev, stream);
+    const Tensor cu = laid_out(tensor("cu_seqlens", a[5]), c.dev, stream);
+    if (table.dim() != 2) throw BadValue("block_table must be [B, max_pages]");
+    const int64_t B = table.size(0);
+    const int total = whole("total", a[6]), longest = whole("max_seqlen", a[7]);
+    if (total < 0) throw BadValue("total must not be negative");
+    Tensor out[2];
+    const char* names[2] = {"k_out", "v_out"};
+    for (int i = 0; i < 2; ++i) {
+        out[i] = a[8 + i] == Py_None ? fresh({total, c.hkv, c.d}, at::kBFloat16, c.dev, stream)
+                                     : tensor(names[i], a[8 + i]);
+        dense(names[i], out[i], at::kBFloat16, {total, c.hkv, c.d}, c.dev);
+    }
+    return status_or(fa_cache_read_q8(c.k, c.v, s.k, s.v, c.num_pages, c.hkv, c.page_size, s.block, c.d,
+                                      ints("block_table", table, {B, table.size(1)}, c.dev),
+                                      small(table.size(1)), ints("cu_seqlens", cu, {B + 1}, c.dev),
+                                      small(B), longest, total, out[0].data_ptr(), out[1].data_ptr(),
+                                      stream),
+                     pair(out[0], out[1]));
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, scale, causal,
+// out, lse, stream, window, sinks, first
+PyObject* decode_paged_q8(PyObject* const* a, Py_ssize_t n) {
+    need_args(n, 15);
+    Attention c(a[0], a[1], a[2], a[13], a[9], a[10], a[11], true, at::kFloat8_e4m3fn);
+    const Scales s(a[3], a[4], c.k, c.dev);
+    const Pages p(c, a[5]);
+    return c.result(fa_fwd_decode_paged_q8(
+        c.q.data_ptr(), c.k.data_ptr(), c.v.data_ptr(), s.k, s.v, c.out.data_ptr(), c.lse_ptr(), c.B,
+        c.Hq, p.hkv, c.n, ints("seqlens_k", c.hold(tensor("seqlens_k", a[6])), {c.B}, c.dev), p.table,
+        p.max_pages, p.page_size, p.num_pages, s.block, c.d, scale_of(a[7], c.d),
+        truth("causal", a[8]), whole("window", a[12]), whole("first", a[14]), c.sinks, c.stream));
+}
+
 #define ENTRY(f) \
     {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {
     ENTRY(decode_tree), ENTRY(decode_tree_paged), ENTRY(decode_first), ENTRY(decode_paged_first),
     ENTRY(tree_mask),   ENTRY(cache_fork),        ENTRY(cache_reserve), ENTRY(cache_free),
-    ENTRY(cache_append), ENTRY(cache_copy),       ENTRY(cache_compact), {nullptr, nullptr, 0, nullptr}};
+    ENTRY(cache_append), ENTRY(cache_copy),       ENTRY(cache_compact), ENTRY(rope),
+    ENTRY(cache_append_rope), ENTRY(cache_append_q8), ENTRY(cache_read_q8), ENTRY(decode_paged_q8),
+    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, kMethods,
                        nullptr,               nullptr, nullptr, nullptr};
 

@@ -301,6 +301,35 @@ struct DecodeArgs {
 constexpr int kJoinSplits = 8;   // most splits of a joined call (CTAs of a cluster)
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, cudaStream_t s);
 
+// Decode over paged caches of 8 bits (decode_q8.cu).
+struct DecodeQ8Args {
+    const uint16_t* q;          // [B, Hq, Sq, d] bf16 bits
+    const uint8_t* k;           // [num_pages, Hkv, page_size, d] e4m3 codes
+    const uint8_t* v;
+    const float* k_scale;       // [num_pages, Hkv, blocks]
+    const float* v_scale;
+    uint16_t* o;                // [B, Hq, Sq, d]
+    float* lse;                 // [B, Hq, Sq]
+    const int* seqlens_k;       // [B]
+    float* part_o;              // as in DecodeArgs
+    float* part_lse;
+    int B, Hq, Hkv, Sq, Sk;     // Sk = max_pages * page_size
+    int group, rows;            // Hq / Hkv, group * Sq
+    int tiles;                  // of query rows of a key/value head
+    int n_splits, chunk, joined;
+    int causal, window, first;
+    const float* sinks;
+    const int* block_table;
+    int max_pages, page_size, num_pages;
+    int block, blocks;          // keys of a scale, scales of a page and head
+    float scale_log2;
+};
+// Rows of a tile: 8, 16 or, up to head_dim 128, 32.
+inline int decode_q8_tile(int head_dim, int rows) {
+    return rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
+}
+cudaError_t launch_decode_q8(const DecodeQ8Args& a, int head_dim, cudaStream_t s);
+
 // -------------------------------------------------------------- span ----
 
 // The tensor-core kernel of token trees and of windows with first keys

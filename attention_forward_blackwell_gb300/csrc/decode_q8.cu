@@ -1,0 +1,575 @@
+// Decode attention over a paged cache held in 8 bits, for sm_103a.
+//
+// Half the bytes of decode.cu's caches for a key, so that twice as many keys a
+// second have to be turned into operands: what decides is how few instructions
+// that takes.  The split over the keys, the merge by LSE and the joined splits
+// are decode.cu's; what differs:
+//
+//   - The keys are the M side of the products: S^T [16 keys x 8 rows] = K Q^T and
+//     O^T [16 dims x 8 rows] += V^T P^T, so that 8 query rows (a group of 8 heads)
+//     fill the instruction, where rows on M would leave half of it empty.
+//   - A sum may be taken in any order, so the operands are laid out for the loads:
+//     a lane's 16 codes of a key (16 bytes) are its share of 4 steps of the score
+//     product, the rows of Q permuted alike; a lane's 16 dims of four keys are its
+//     share of 8 tiles of O^T, two byte permutes for two pairs of keys.  A
+//     conversion (two codes to fp16, exact) per register of an operand is all the
+//     rest.  e4m3 values and fp16 P and Q multiply exactly into fp32 sums.
+//   - Q in fp16: each row times a power of two that brings its largest element
+//     into [1, 2), so 8 bits of fraction stay of every element down to 2^-14 of
+//     it; below, the error is 2^-25 of the largest, that of an fp32 sum.
+//   - Scales.  A key's score is multiplied by its scale.  A value's scale goes into
+//     its probability, p_j v_j = (p_j s_j) code_j, and fp16 has to hold that
+//     product whatever the scales are: it is exp2(score_j + log2 s_j - m'), with a
+//     running maximum m' of its own beside that of the softmax's sum, so that
+//     the largest terms of O always lie in the upper binades; 2^6 of headroom is
+//     used (kLift), 2^8 of growth allowed before both are moved on (kGrow).
+//   - The row maxima of a slice are never taken: lanes check their own scores
+//     against the bounds and vote; a shuffle tree follows only where one is over.
+//
+// A warp walks 16-key slices of its split (keys 16 w + 64 i) through a ring of
+// its own, filled by cp.async with zeros where a key is not there or seen by no
+// row; the page numbers of a slice are fetched while the one before is issued.
+#include "common.cuh"
+#include "ptx.cuh"
+#include "q8.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kLn2f = 0.69314718055994530942f;
+constexpr float kLog2ef = 1.44269504088896340736f;
+constexpr float kGrow = 8.0f;   // log2
+constexpr float kLift = 6.0f;
+
+template <int D, int NR>
+struct Q8Traits {
+    static constexpr int WARPS = 4;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int R = 8 * NR;                    // rows of a tile
+    static constexpr int KB = 16;                       // keys of a slice
+    static constexpr int GRAN = D / 16;                 // 16-byte granules of a key
+    static constexpr int SLICE = KB * D;                // bytes of a slice of keys, or of values
+    static constexpr int STAGE = 2 * SLICE + 128;       // and the scales of both
+    static constexpr int STAGES = D == 64 ? 6 : D == 128 ? 4 : 3;
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int ROW = D + 4;                   // floats of a row of the merge
+    static constexpr int MERGE = WARPS * R * (ROW + 2) * 4;
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int JOIN_ROWS = R + kJoinSplits;   // n splits, ceil(R / n) rows each
+    static constexpr int JOIN_LSE = JOIN_ROWS * 4 + (-JOIN_ROWS * 4 & 15);
+    static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
+    static constexpr int MT = D / 16;                   // tiles of O^T
+    static constexpr int MIN_CTAS = NR == 4 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
+};
+
+// Places of granule g of a key in a slice of keys, and of values (no two lanes of
+// a quarter warp that read together share a bank).
+template <int D>
+__device__ __forceinline__ uint32_t k_place(int key, int g) {
+    return (uint32_t)(key * D + ((D == 64 ? g : g ^ ((key & 1) << 2)) << 4));
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_place(int key, int g) {
+    return (uint32_t)(key * D + ((g ^ (D == 64 ? ((key >> 1) & 1) << 1 : ((key >> 1) & 3) << 1)) << 4));
+}
+
+// Keys that a sequence's splits walk, as in decode.cu: positions [0, span) stand
+// for the keys [0, head) and [base, L); lo: the first key of some row's window.
+struct Axis {
+    int head, base, span, lo;
+    __device__ __forceinline__ int key(int x) const { return x < head ? x : x - head + base; }
+};
+__device__ __forceinline__ Axis key_axis(const DecodeQ8Args& a, int L) {
+    Axis s{0, 0, L, 0};
+    if (a.window <= 0) return s;
+    s.lo = max(0, L - a.Sq - a.window + 1);
+    s.base = s.lo & ~63;
+    if (a.first > 0) s.head = ((a.first - 1) | 63) + 1;
+    if (a.first > L || s.head >= s.base) {
+        if (a.first > 0) s.base = 0;
+        s.head = 0;
+    }
+    s.span = s.head + L - s.base;
+    return s;
+}
+
+__device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN_CTAS)
+    decode_q8_kernel(const DecodeQ8Args a) {
+    using T = Q8Traits<D, NR>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    dependents_may_start();
+    wait_for_previous();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x, hkv = blockIdx.y / a.tiles, rbase = blockIdx.y % a.tiles * T::R;
+    const int b = blockIdx.z;
+    const int L = max(0, min(a.seqlens_k[b], a.Sk));
+    const Axis axis = key_axis(a, L);
+    const int x_lo = split * a.chunk, x_hi = min(x_lo + a.chunk, axis.span);
+    const bool joined = a.joined != 0;
+    if (joined) cluster_arrive();   // (waited for before the first write to another)
+    if (x_lo >= axis.span && !joined) return;
+    const int n_slices = max(0, x_hi - x_lo + T::KB - 1) / T::KB;
+    const int mine = n_slices > warp ? (n_slices - warp + T::WARPS - 1) / T::WARPS : 0;
+
+    // ------------------------------------------------ ring
+    const uint32_t ring = smem_u32(smem) + warp * T::STAGES * T::STAGE;
+    const int* table = a.block_table + (size_t)b * a.max_pages;
+    // This lane's key (lane & 15) of a slice: its page, -1 where it is not loaded,
+    // and its row there.  Nothing waits for the page before the slice is issued.
+    int page = -1;
+    unsigned page_row = 0;
+    auto look_up = [&](int i) {
+        const int x = x_lo + T::KB * (warp + T::WARPS * i) + (lane & 15);
+        const int key = axis.key(x);
+        page = -1;
+        if (x >= x_hi || (key < axis.lo && key >= a.first)) return;
+        const unsigned p = (unsigned)key / (unsigned)a.page_size;
+        page_row = (unsigned)key - p * (unsigned)a.page_size;
+        page = table[p];
+    };
+    auto load_slice = [&](int i) {
+        const uint32_t to = ring + (i % T::STAGES) * T::STAGE;
+        const bool there = (unsigned)page < (unsigned)a.num_pages;   // (no page: reads as zeros)
+        const uint32_t head = (uint32_t)page * (uint32_t)a.Hkv + (uint32_t)hkv;
+        // its row among all rows of the cache (below 2^32), and its scale
+        const uint32_t at_row = head * (uint32_t)a.page_size + page_row;
+        const uint32_t at_scale = head * (uint32_t)a.blocks + page_row / (unsigned)a.block;
+        const unsigned rows = __ballot_sync(0xffffffffu, there);
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+            const int e = lane + 32 * u, key = e / T::GRAN, gr = e % T::GRAN;
+            const bool have = (rows >> key) & 1u;
+            const uint32_t row = __shfl_sync(0xffffffffu, at_row, key);
+            const size_t src = have ? (size_t)row * D + gr * 16 : 0;
+            cp_async_16(to + k_place<D>(key, gr), a.k + src, have ? 16u : 0u);
+            cp_async_16(to + T::SLICE + v_place<D>(key, gr), a.v + src, have ? 16u : 0u);
+        }
+        cp_async_4(to + 2 * T::SLICE + lane * 4,
+                   (lane < 16 ? a.k_scale : a.v_scale) + (there ? at_scale : 0), there ? 4u : 0u);
+    };
+    if (mine > 0) look_up(0);
+#pragma unroll
+    for (int s = 0; s < T::STAGES - 1; ++s) {
+        if (s < mine) {
+            load_slice(s);
+            if (s + 1 < mine) look_up(s + 1);
+        }
+        cp_async_commit();
+    }
+
+    // ------------------------------------------------ queries
+    // B fragments: lane (g, t) has row nr 8 + g, of each 64 dims the 16 from 16 t on
+    uint32_t qb[NR][D / 16][2];
+    float unit[NR][2];   // scores of rows 2 t, 2 t + 1 are sums times this (log2 units)
+    int place[NR][2];    // the rows' keys
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+        const int pr = rbase + nr * 8 + g;
+        uint32_t w[D / 64][8];
+        float most = 0.f;
+        if (pr < a.rows) {
+            const int h = hkv * a.group + pr / a.Sq;
+            const uint16_t* q = a.q + (((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq) * D + t * 16;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(q + c * 64);
+                const uint4 y = *reinterpret_cast<const uint4*>(q + c * 64 + 8);
+                w[c][0] = x.x, w[c][1] = x.y, w[c][2] = x.z, w[c][3] = x.w;
+                w[c][4] = y.x, w[c][5] = y.y, w[c][6] = y.z, w[c][7] = y.w;
+            }
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[c][e] << 16)),
+                                             fabsf(__uint_as_float(w[c][e] & 0xffff0000u))));
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[c][e] = 0;
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // 2^-e of the largest element's exponent (1 for a row of zeros; exponents
+        // at which it would not be a normal number stay short of them)
+        int ex = (int)(__float_as_uint(most) >> 23) - 127;
+        ex = most == 0.f ? 0 : max(-125, min(ex, 125));
+        const float by = __uint_as_float((uint32_t)(127 - ex) << 23);
+        const float back = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t x = w[c][2 * s + e];
+                    qb[nr][c * 4 + s][e] =
+                        pack_halves(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
+                }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            unit[nr][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
+            place[nr][e] = (rbase + nr * 8 + 2 * t + e) % a.Sq + L - a.Sq;
+        }
+    }
+    // keys [all_lo, all_hi) are seen by every row of the sequence, as those below
+    // all_first are
+    const int all_hi = a.causal ? L - a.Sq + 1 : L;
+    const int all_lo = a.window > 0 ? L - a.window : 0;
+    const int all_first = min(a.first, all_hi);
+
+    float oacc[NR][T::MT][4];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int j = 0; j < T::MT; ++j)
+            oacc[nr][j][0] = oacc[nr][j][1] = oacc[nr][j][2] = oacc[nr][j][3] = 0.f;
+    // of rows 2 t + e: bases of the sum and of O (the same in all lanes of a row),
+    // and this lane's part of the sum
+    float m[NR][2], mv[NR][2], l[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            m[nr][e] = mv[nr][e] = -INFINITY;
+            l[nr][e] = 0.f;
+        }
+
+    for (int i = 0; i < mine; ++i) {
+        cp_async_wait<T::STAGES - 2>();
+        __syncwarp();
+        const uint32_t sk = ring + (i % T::STAGES) * T::STAGE, sv = sk + T::SLICE, sc = sv + T::SLICE;
+        const int x0 = x_lo + T::KB * (warp + T::WARPS * i);
+
+        float sacc[NR][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) sacc[nr][0] = sacc[nr][1] = sacc[nr][2] = sacc[nr][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            const uint4 u = lds128(sk + k_place<D>(g, c * 4 + t));
+            const uint4 w = lds128(sk + k_place<D>(g + 8, c * 4 + t));
+            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t a0 = q8_halves(uu[s]), a1 = q8_halves(ww[s]);
+                const uint32_t a2 = q8_halves_up(uu[s]), a3 = q8_halves_up(ww[s]);
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+                    mma_f16_16816(sacc[nr], a0, a1, a2, a3, qb[nr][c * 4 + s][0], qb[nr][c * 4 + s][1]);
+            }
+        }
+        const float ks[2] = {lds32(sc + g * 4), lds32(sc + 32 + g * 4)};
+        const float lv[2] = {lg2_approx(lds32(sc + 64 + g * 4)), lg2_approx(lds32(sc + 96 + g * 4))};
+        // scores, in place: sacc[nr][2 f + e] is that of key g + 8 f in row 2 t + e
+        const int key0 = axis.key(x0);
+        const bool whole = x0 + T::KB <= x_hi && key0 + T::KB <= all_hi &&
+                           (key0 >= all_lo || key0 + T::KB <= all_first);
+        bool over = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float top = m[nr][e] + kGrow, top_v = mv[nr][e] + kGrow;
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    float& s = sacc[nr][2 * f + e];
+                    s *= unit[nr][e] * ks[f];
+                    if (!whole) {
+                        const int key = key0 + g + 8 * f, p = place[nr][e];
+                        const bool seen = x0 + g + 8 * f < x_hi && (!a.causal || key <= p) &&
+                                          (a.window <= 0 || key > p - a.window || key < a.first);
+                        s = seen ? s : -INFINITY;
+                    }
+                    over |= s > top || s + lv[f] > top_v;
+                }
+            }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = fmaxf(sacc[nr][e], sacc[nr][2 + e]);
+                    float y = fmaxf(sacc[nr][e] + lv[0], sacc[nr][2 + e] + lv[1]);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+                    }
+                    x = fmaxf(x, m[nr][e]);
+                    y = fmaxf(y, mv[nr][e]);
+                    if (x > m[nr][e]) l[nr][e] *= ex2_approx(m[nr][e] - x);   // (0 from -inf)
+                    const float by = y > mv[nr][e] ? ex2_approx(mv[nr][e] - y) : 1.f;
+                    m[nr][e] = x;
+                    mv[nr][e] = y;
+#pragma unroll
+                    for (int j = 0; j < T::MT; ++j) {
+                        oacc[nr][j][e] *= by;
+                        oacc[nr][j][2 + e] *= by;
+                    }
+                }
+        }
+        uint32_t pb[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            float pv[2][2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float base = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
+                const float base_v = mv[nr][e] == -INFINITY ? 0.f : mv[nr][e] - kLift;
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const float s = sacc[nr][2 * f + e];
+                    l[nr][e] += ex2_approx(s - base);
+                    pv[f][e] = ex2_approx(s + lv[f] - base_v);
+                }
+            }
+#pragma unroll
+            for (int f = 0; f < 2; ++f) pb[nr][f] = movmatrix_trans(pack_halves(pv[f][0], pv[f][1]));
+        }
+        // O^T += V^T P^T: lane (g, t) has 16 dims (64: 8) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
+            // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
+            const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
+            const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
+            const uint32_t a0 = q8_halves(xl), a1 = q8_halves_up(xl), a2 = q8_halves(yl), a3 = q8_halves_up(yl);
+            const uint32_t b0 = q8_halves(xh), b1 = q8_halves_up(xh), b2 = q8_halves(yh), b3 = q8_halves_up(yh);
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) {
+                mma_f16_16816(oacc[nr][j], a0, a1, a2, a3, pb[nr][0], pb[nr][1]);
+                mma_f16_16816(oacc[nr][j + 1], b0, b1, b2, b3, pb[nr][0], pb[nr][1]);
+            }
+        };
+        if constexpr (D == 64) {
+            const uint32_t half = (g & 1) * 8;
+            const uint2 x0_ = lds64(sv + v_place<D>(2 * t, g >> 1) + half);
+            const uint2 x1_ = lds64(sv + v_place<D>(2 * t + 1, g >> 1) + half);
+            const uint2 y0_ = lds64(sv + v_place<D>(2 * t + 8, g >> 1) + half);
+            const uint2 y1_ = lds64(sv + v_place<D>(2 * t + 9, g >> 1) + half);
+            add(0, x0_.x, x1_.x, y0_.x, y1_.x);
+            add(2, x0_.y, x1_.y, y0_.y, y1_.y);
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 128; ++c) {
+                const uint4 x0_ = lds128(sv + v_place<D>(2 * t, c * 8 + g));
+                const uint4 x1_ = lds128(sv + v_place<D>(2 * t + 1, c * 8 + g));
+                const uint4 y0_ = lds128(sv + v_place<D>(2 * t + 8, c * 8 + g));
+                const uint4 y1_ = lds128(sv + v_place<D>(2 * t + 9, c * 8 + g));
+                add(c * 8, x0_.x, x1_.x, y0_.x, y1_.x);
+                add(c * 8 + 2, x0_.y, x1_.y, y0_.y, y1_.y);
+                add(c * 8 + 4, x0_.z, x1_.z, y0_.z, y1_.z);
+                add(c * 8 + 6, x0_.w, x1_.w, y0_.w, y1_.w);
+            }
+        }
+        __syncwarp();
+        const int next = i + T::STAGES - 1;
+        if (next < mine) {
+            load_slice(next);
+            if (next + 1 < mine) look_up(next + 1);
+        }
+        cp_async_commit();
+    }
+    cp_async_wait<0>();
+    __syncthreads();   // every warp is done with its ring
+
+    // ------------------------------------------------ merge of the warps
+    float* wm = reinterpret_cast<float*>(smem);   // [WARPS][R]
+    float* wl = wm + T::WARPS * T::R;
+    float* wo = wl + T::WARPS * T::R;             // [WARPS][R][ROW]
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[nr][e];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const int r = nr * 8 + 2 * t + e;
+            if (g == 0) {
+                wm[warp * T::R + r] = m[nr][e];
+                wl[warp * T::R + r] = sum;
+            }
+            // O of the base of the sum (0 where the warp saw no key of the row, or
+            // values of scale 0)
+            const float by = mv[nr][e] == -INFINITY ? 0.f : ex2_approx(mv[nr][e] - kLift - m[nr][e]);
+            float* row = wo + (warp * T::R + r) * T::ROW;
+#pragma unroll
+            for (int j = 0; j < T::MT; ++j) {
+                const int dim = D == 64 ? g * 8 + 2 * j : (j >> 3) * 128 + g * 16 + 2 * (j & 7);
+                *reinterpret_cast<float2*>(row + dim) =
+                    make_float2(oacc[nr][j][e] * by, oacc[nr][j][2 + e] * by);
+            }
+        }
+    __syncthreads();
+    const int valid_rows = min(T::R, a.rows - rbase);
+    // joined: split s finishes the rows [s own, (s + 1) own) (see decode.cu)
+    const int own = joined ? (T::R + a.n_splits - 1) / a.n_splits : 1;
+    const uint32_t jl = smem_u32(smem) + T::SMEM, jo = jl + T::JOIN_LSE;
+    if (joined) cluster_wait();
+    auto row_id = [&](int r) {
+        const int pr = rbase + r;
+        return ((size_t)b * a.Hq + hkv * a.group + pr / a.Sq) * a.Sq + pr % a.Sq;
+    };
+    for (int e = threadIdx.x * 4; e < valid_rows * D; e += T::THREADS * 4) {
+        const int r = e / D, c = e % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < T::WARPS; ++w) M = fmaxf(M, wm[w * T::R + r]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lse2 = -INFINITY;
+        if (M != -INFINITY) {
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < T::WARPS; ++w) {
+                const float f = ex2_approx(wm[w * T::R + r] - M);   // 0 for warps without keys
+                const float4 x = *reinterpret_cast<const float4*>(wo + (w * T::R + r) * T::ROW + c);
+                sum = fmaf(f, wl[w * T::R + r], sum);
+                o.x = fmaf(f, x.x, o.x);
+                o.y = fmaf(f, x.y, o.y);
+                o.z = fmaf(f, x.z, o.z);
+                o.w = fmaf(f, x.w, o.w);
+            }
+            const float inv = 1.f / sum;
+            o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+            lse2 = M + lg2_approx(sum);
+        }
+        if (joined) {
+            const int to = r / own, at = split * own + r - to * own;
+            cluster_write4(jo + (at * D + c) * 4, to, o);
+            if (c == 0) cluster_write(jl + at * 4, to, lse2);
+            continue;
+        }
+        const size_t part = (size_t)split * a.B * a.Hq * a.Sq + row_id(r);
+        *reinterpret_cast<float4*>(a.part_o + part * D + c) = o;
+        if (c == 0) a.part_lse[part] = lse2;
+    }
+    if (!joined) return;
+    cluster_sync_all();
+    for (int e = threadIdx.x * 4; e < own * D; e += T::THREADS * 4) {
+        const int k = e / D, c = e % D, r = split * own + k;
+        if (r >= valid_rows) break;
+        const int h = hkv * a.group + (rbase + r) / a.Sq;
+        const uint8_t* from = smem + T::SMEM;
+        const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
+        float x[kJoinSplits], M = sg, sum = 0.f;
+        float4 y[kJoinSplits], o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kJoinSplits; ++s) {
+            x[s] = -INFINITY;
+            y[s] = o;
+            if (s < a.n_splits) {
+                x[s] = *reinterpret_cast<const float*>(from + (s * own + k) * 4);
+                y[s] = *reinterpret_cast<const float4*>(from + T::JOIN_LSE + ((s * own + k) * D + c) * 4);
+            }
+            M = fmaxf(M, x[s]);
+        }
+        if (M != -INFINITY) {
+            sum = ex2_approx(sg - M);
+#pragma unroll
+            for (int s = 0; s < kJoinSplits; ++s) {
+                const float f = ex2_approx(x[s] - M);
+                sum += f;
+                o.x = fmaf(f, y[s].x, o.x);
+                o.y = fmaf(f, y[s].y, o.y);
+                o.z = fmaf(f, y[s].z, o.z);
+                o.w = fmaf(f, y[s].w, o.w);
+            }
+        }
+        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const size_t row = row_id(r);
+        *reinterpret_cast<uint2*>(a.o + row * D + c) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
+    }
+}
+
+// A warp per query row: merges its splits by their LSE, with the head's sink.
+template <int D>
+__global__ void __launch_bounds__(256) combine_q8_kernel(const DecodeQ8Args a) {
+    dependents_may_start();
+    wait_for_previous();
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long n_rows = (long long)a.B * a.Hq * a.Sq;
+    if (row >= n_rows) return;
+    const int b = (int)(row / ((long long)a.Hq * a.Sq)), h = (int)(row / a.Sq % a.Hq);
+    const int L = max(0, min(a.seqlens_k[b], a.Sk));
+    const int ns = (key_axis(a, L).span + a.chunk - 1) / a.chunk;
+    const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
+    float M = sg;
+    for (int s = lane; s < ns; s += 32) M = fmaxf(M, a.part_lse[s * n_rows + row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    constexpr int PER = D / 64;   // pairs of columns of a lane
+    float2 acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = make_float2(0.f, 0.f);
+    float sum = 0.f;
+    if (M != -INFINITY) {
+        sum = ex2_approx(sg - M);
+#pragma unroll 4
+        for (int s = 0; s < ns; ++s) {
+            const float f = ex2_approx(a.part_lse[s * n_rows + row] - M);
+            const float2* po = reinterpret_cast<const float2*>(a.part_o + (s * n_rows + row) * D);
+            sum += f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const float2 x = po[lane + 32 * e];
+                acc[e].x = fmaf(f, x.x, acc[e].x);
+                acc[e].y = fmaf(f, x.y, acc[e].y);
+            }
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    uint32_t* o = reinterpret_cast<uint32_t*>(a.o + row * D);
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
+    if (lane == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
+}
+
+template <int D, int NR>
+cudaError_t launch_tile(const DecodeQ8Args& a, cudaStream_t s) {
+    using T = Q8Traits<D, NR>;
+    const int smem = T::SMEM + (a.joined ? T::JOIN : 0);
+    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, NR>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM + T::JOIN);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)a.n_splits, (unsigned)(a.Hkv * a.tiles), (unsigned)a.B);
+    if (a.joined)
+        return launch_dependent_clusters(decode_q8_kernel<D, NR>, (unsigned)a.n_splits, grid,
+                                         dim3(T::THREADS), smem, s, a);
+    e = launch_dependent(decode_q8_kernel<D, NR>, grid, dim3(T::THREADS), smem, s, a);
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)a.B * a.Hq * a.Sq;
+    return launch_dependent(combine_q8_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+}
+
+template <int D>
+cudaError_t launch_dim(const DecodeQ8Args& a, cudaStream_t s) {
+    switch (decode_q8_tile(D, a.rows)) {
+        case 8: return launch_tile<D, 1>(a, s);
+        case 16: return launch_tile<D, 2>(a, s);
+        default:
+            if constexpr (D <= 128) return launch_tile<D, 4>(a, s);
+            else return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_q8(const DecodeQ8Args& a, int head_dim, cudaStream_t s) {
+    switch (head_dim) {
+        case 64: return launch_dim<64>(a, s);
+        case 128: return launch_dim<128>(a, s);
+        case 256: return launch_dim<256>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace fa

@@ -413,6 +413,112 @@ fa_status fa_cache_compact(void *k_cache, void *v_cache, int num_pages, int hkv,
                            fa_stream_t stream);
 
 /*
+ * Rotation of positions.  The first `rot` elements of a row of head_dim are
+ * pairs (x, y), and a row at position p has pair i turned by the angle t = p w_i:
+ *     x' = factor (x cos t - y sin t),   y' = factor (y cos t + x sin t)
+ * Elements past rot stay as they are.  The pairs are (i, i + rot / 2) or, with
+ * interleaved nonzero, (2 i, 2 i + 1).  freqs: device int64[rot / 2], 16-byte
+ * aligned, w_i / (2 pi) in units of 2^-64 of a turn (modulo 2^64), so that the
+ * angle of any int32 position, negative ones too, is exact modulo a turn.  rot and
+ * head_dim are multiples of 16.  Angles, products and sums are fp32, rounded once to
+ * the output's type.
+ *
+ * fa_rope: rows of q (hq heads) and k (hk heads; either may be 0), [batch, heads,
+ *   n, head_dim] bf16 with strides of batch, head and token in elements (multiples
+ *   of 8; the last dimension is contiguous), 16-byte aligned; row i of batch entry b
+ *   stands at positions[b * position_stride + i].  An output may be its input
+ *   (in place); else it must not overlap an input.  inverse nonzero: by the angle
+ *   -t, the transpose: the gradient of the inputs from that of the outputs.
+ *   batch <= 65535, hq + hk <= 65535.
+ * fa_turn: how an append turns keys, and the queries that it turns beside them.
+ *   positions NULL: row i of entry b stands at seqlens[b] + i, its key; else
+ *   at positions[b * position_stride + i].  q: hq heads (0: none) [batch, hq, n,
+ *   head_dim] with q_strides as above; q_out [batch, hq, n, head_dim] contiguous, its
+ *   rows i >= n_new[b] are not written.
+ * fa_cache_append_rope: fa_cache_append with keys turned (values are not).
+ */
+typedef struct fa_turn {
+    const long long *freqs;
+    int rot;
+    int interleaved;
+    float factor;                  /* > 0; 1 leaves lengths as they are */
+    const int *positions;
+    long long position_stride;
+    const void *q;
+    const long long *q_strides;
+    void *q_out;
+    int hq;
+} fa_turn;
+
+fa_status fa_rope(const void *q, const long long *q_strides, void *q_out,
+                  const long long *q_out_strides, int hq, const void *k, const long long *k_strides,
+                  void *k_out, const long long *k_out_strides, int hk, int batch, int n, int head_dim,
+                  const int *positions, long long position_stride, const long long *freqs, int rot,
+                  int interleaved, int inverse, float factor, fa_stream_t stream);
+fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int hkv, int page_size,
+                               int head_dim, const int *block_table, int max_pages,
+                               const int *seqlens, int batch, const void *k_new,
+                               const long long *k_strides, const void *v_new,
+                               const long long *v_strides, int n, const int *n_new,
+                               const int *copies, const fa_turn *turn, fa_stream_t stream);
+
+/*
+ * Paged caches held in 8 bits:
+ *     k_cache, v_cache : [num_pages, hkv, page_size, head_dim] e4m3 codes,
+ *                        16-byte aligned
+ *     k_scale, v_scale : [num_pages, hkv, page_size / block] fp32; a value is its
+ *                        code times the scale of its block of keys.  `block`
+ *                        divides page_size.
+ * with the block tables and lengths of the other paged calls; fa_cache_fork, _reserve
+ * and _free serve them as they are.  Contiguous caches are pages of one sequence each.
+ *
+ * fa_cache_append_q8: as fa_cache_append, with keys turned where turn is given (its
+ *   rot may be 0: only queries are copied then).  A block that receives rows takes the
+ *   scale s = 2^e, the smallest with -54 <= e <= 54 and 448 s no less than the rows'
+ *   reach, or the scale it has if that is larger and the block holds earlier rows of
+ *   the sequence (keys below seqlens[b]); earlier rows are then rounded anew to codes
+ *   of s, which between powers of two changes only what falls below 2^-6 s.  The
+ *   reach is the largest length factor * sqrt(x^2 + y^2) of a turned pair and
+ *   magnitude of the other elements, so it does not depend on positions.  A code is
+ *   its element over s, rounded to the nearest code, ties to even; beyond 448 it is
+ *   448.  New rows must be finite.  With copies, blocks and scales of replaced
+ *   pages come along; n may be 0.  A page that another row holds must not be
+ *   appended to.  cache_copy and cache_compact do not take these caches.
+ * fa_cache_read_q8: keys j < cu_seqlens[b + 1] - cu_seqlens[b] of each sequence as
+ *   bf16 rows cu_seqlens[b] + j of k_out, v_out [total, hkv, head_dim] (16-byte
+ *   aligned), rounded once; the layout of fa_fwd_prefill_varlen.  max_seqlen is at
+ *   least every length (rows beyond it are not written); keys without a page read as
+ *   zeros.  Offsets are clamped to [0, total].
+ * head_dim of both is a multiple of 16.
+ *
+ * fa_fwd_decode_paged_q8: fa_fwd_decode_paged_first over such a cache: causal or
+ *   not, window <= 0 or a window with `first` visible first keys (0: none), sinks or
+ *   NULL.  Queries, probabilities and values are multiplied in fp16 with fp32 sums:
+ *   codes exactly, queries to 2^-11 (elements below 2^-14 of their row's largest to
+ *   2^-25 of that), a probability times its value's scale to 2^-11.  Scales must
+ *   be finite and not negative; keys that no query row of the sequence sees may hold
+ *   anything, their scales too.  Keys whose entry is no page read as zeros.
+ *   head_dim 64, 128 or 256; num_pages * hkv * page_size < 2^32.
+ */
+fa_status fa_cache_append_q8(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
+                             int num_pages, int hkv, int page_size, int block, int head_dim,
+                             const int *block_table, int max_pages, const int *seqlens, int batch,
+                             const void *k_new, const long long *k_strides, const void *v_new,
+                             const long long *v_strides, int n, const int *n_new,
+                             const int *copies, const fa_turn *turn, fa_stream_t stream);
+fa_status fa_cache_read_q8(const void *k_cache, const void *v_cache, const float *k_scale,
+                           const float *v_scale, int num_pages, int hkv, int page_size, int block,
+                           int head_dim, const int *block_table, int max_pages,
+                           const int *cu_seqlens, int batch, int max_seqlen, int total,
+                           void *k_out, void *v_out, fa_stream_t stream);
+fa_status fa_fwd_decode_paged_q8(const void *q, const void *k_cache, const void *v_cache,
+                                 const float *k_scale, const float *v_scale, void *o, float *lse,
+                                 int batch, int hq, int hkv, int sq, const int *seqlens_k,
+                                 const int *block_table, int max_pages, int page_size,
+                                 int num_pages, int block, int head_dim, float scale, int causal,
+                                 int window, int first, const float *sinks, fa_stream_t stream);
+
+/*
  * fa_fwd_decode with an explicit number of key splits (num_splits <= 0 picks
  * it automatically, exactly like fa_fwd_decode).  The splits partition
  * [0, sk) into equal chunks of a multiple of 64 keys; any split count gives
