@@ -647,17 +647,25 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     const long long span = window > 0 ? std::min<long long>(sk, (long long)window + sq + 62 + heads_first) : sk;
     const long long pairs = (long long)batch * hkv * a.tiles;
     const SplitPlan plan = split_plan(true, head_dim, pairs, span, di->num_sms);
-    a.chunk = (int)(((span + plan.splits - 1) / plan.splits + 63) / 64 * 64);
-    a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
     a.joined = plan.joined ? 1 : 0;
-    if (a.joined) return from_cuda(launch_decode_q8(a, head_dim, s));
-    const size_t parts = (size_t)a.n_splits * batch * hq * sq;
+    if (a.joined) {
+        a.chunk = (int)(((span + plan.splits - 1) / plan.splits + 63) / 64 * 64);
+        a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
+        return from_cuda(launch_decode_q8(a, head_dim, s));
+    }
+    // (the kernel counts the blocks of all units in 32 bits)
+    const double blocks = (double)pairs * (double)((span + 63) / 64);
+    if (blocks >= 2147483648.0) return FA_ERR_INVALID_ARG;
+    a.n_splits = (int)std::min<double>((double)di->num_sms * decode_q8_ctas(head_dim, tile), blocks);
+    const size_t parts = 2ull * a.n_splits * tile;
+    const size_t bytes_o = parts * head_dim * sizeof(float), bytes_l = parts * sizeof(float);
     char* ws = nullptr;
-    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), parts * (head_dim + 1) * sizeof(float), s) !=
-        cudaSuccess)
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes_o + bytes_l + (2ull * a.n_splits + 1) * sizeof(int4),
+                        s) != cudaSuccess)
         return FA_ERR_CUDA;
     a.part_o = reinterpret_cast<float*>(ws);
-    a.part_lse = a.part_o + parts * head_dim;
+    a.part_lse = reinterpret_cast<float*>(ws + bytes_o);
+    a.head = reinterpret_cast<int4*>(ws + bytes_o + bytes_l);
     const cudaError_t e = launch_decode_q8(a, head_dim, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess) return FA_ERR_CUDA;
     return from_cuda(e);

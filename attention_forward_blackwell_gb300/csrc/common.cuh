@@ -311,12 +311,18 @@ struct DecodeQ8Args {
     uint16_t* o;                // [B, Hq, Sq, d]
     float* lse;                 // [B, Hq, Sq]
     const int* seqlens_k;       // [B]
-    float* part_o;              // as in DecodeArgs
+    // pieces of units, two of a CTA at most: O [2 CTAs][tile][d] and LSE (log2
+    // units) [2 CTAs][tile]; head [2 CTAs] batch entry, unit, its blocks in the piece,
+    // and the unit's blocks if the piece is its first (else 0); then one more: the
+    // blocks of a CTA
+    float* part_o;
     float* part_lse;
+    int4* head;
     int B, Hq, Hkv, Sq, Sk;     // Sk = max_pages * page_size
     int group, rows;            // Hq / Hkv, group * Sq
     int tiles;                  // of query rows of a key/value head
-    int n_splits, chunk, joined;
+    int joined;                 // the splits of a unit are a cluster, `chunk` keys each
+    int n_splits, chunk;        // (not joined: CTAs)
     int causal, window, first;
     const float* sinks;
     const int* block_table;
@@ -328,6 +334,7 @@ struct DecodeQ8Args {
 inline int decode_q8_tile(int head_dim, int rows) {
     return rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
 }
+int decode_q8_ctas(int head_dim, int tile);   // CTAs that an SM holds at once
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, int head_dim, cudaStream_t s);
 
 // -------------------------------------------------------------- span ----

@@ -26,9 +26,22 @@
 //   - The row maxima of a slice are never taken: lanes check their own scores
 //     against the bounds and vote; a shuffle tree follows only where one is over.
 //
-// A warp walks 16-key slices of its split (keys 16 w + 64 i) through a ring of
-// its own, filled by cp.async with zeros where a key is not there or seen by no
-// row; the page numbers of a slice are fetched while the one before is issued.
+// Work.  The sequences' lengths are known to the device only, and differ.  A unit
+// (batch entry, key/value head, tile of query rows) counts its blocks of 64 keys;
+// the units' blocks, one after the other, form a line that is cut into equal
+// pieces, one per CTA, as many CTAs as fit the SMs at once (as in span.cu).  A
+// unit that lies in one piece is finished there; of the others each CTA writes
+// what it has, normalised, with its LSE, and combine_q8_kernel merges them in
+// their order.  (The split kernel's grid, one CTA of 256 keys and more for every
+// piece of the longest possible sequence, took 195 us for 64 x 1K to 16K keys x 8
+// heads and 213 for one of 130,000 keys x 2 heads at head_dim 256.)
+// Short caches are split over the CTAs of a cluster instead, which merge without a
+// second kernel, as decode.cu's joined splits.
+//
+// A warp takes 16 keys of every block through a ring of its own, filled by
+// cp.async with zeros where a key is not there or seen by no row; copies run
+// ahead over the ends of units, and the page numbers of a slice are fetched while
+// the one before is issued.
 #include "common.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -41,25 +54,28 @@ constexpr float kLog2ef = 1.44269504088896340736f;
 constexpr float kGrow = 8.0f;   // log2
 constexpr float kLift = 6.0f;
 
+constexpr int kBlock = 64;      // keys of a block
+constexpr int kLeastBlocks = 4; // of a piece
+
 template <int D, int NR>
 struct Q8Traits {
     static constexpr int WARPS = 4;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int R = 8 * NR;                    // rows of a tile
-    static constexpr int KB = 16;                       // keys of a slice
+    static constexpr int KB = kBlock / WARPS;           // keys of a slice
     static constexpr int GRAN = D / 16;                 // 16-byte granules of a key
     static constexpr int SLICE = KB * D;                // bytes of a slice of keys, or of values
     static constexpr int STAGE = 2 * SLICE + 128;       // and the scales of both
     static constexpr int STAGES = D == 64 ? 6 : D == 128 ? 4 : 3;
-    static constexpr int RING = WARPS * STAGES * STAGE;
-    static constexpr int ROW = D + 4;                   // floats of a row of the merge
-    static constexpr int MERGE = WARPS * R * (ROW + 2) * 4;
-    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int WARP_RING = STAGES * STAGE;
+    static constexpr int RING = WARPS * WARP_RING;
     static constexpr int JOIN_ROWS = R + kJoinSplits;   // n splits, ceil(R / n) rows each
     static constexpr int JOIN_LSE = JOIN_ROWS * 4 + (-JOIN_ROWS * 4 & 15);
     static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
     static constexpr int MT = D / 16;                   // tiles of O^T
     static constexpr int MIN_CTAS = NR == 4 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
+    // the merge of 8 rows goes through the slot that was read last
+    static_assert(8 * (D + 2) * 4 <= STAGE, "merge buffer");
 };
 
 // Places of granule g of a key in a slice of keys, and of values (no two lanes of
@@ -99,6 +115,52 @@ __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     return r;
 }
 
+__device__ __forceinline__ int unit_blocks(int span) { return max(1, (span + kBlock - 1) / kBlock); }
+__device__ __forceinline__ int keys_of(const DecodeQ8Args& a, int b) {
+    return max(0, min(a.seqlens_k[b], a.Sk));
+}
+
+// Where on the line piece `x` lies: its first block's batch entry, unit of it and
+// block of that; the blocks of the piece, 0 past the end.  A warp together: each
+// lane sums its share of the batch.
+struct Piece {
+    int b, u, kb, blocks, quota;
+};
+__device__ __forceinline__ Piece place_piece(const DecodeQ8Args& a, int x, int pieces) {
+    const int lane = threadIdx.x & 31, units = a.Hkv * a.tiles;
+    const int per = (a.B + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, a.B);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units * unit_blocks(key_axis(a, keys_of(a, b)).span);
+    int end = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, end, o);
+        if (lane >= o) end += y;
+    }
+    const int all = __shfl_sync(0xffffffffu, end, 31);
+    Piece p;
+    p.quota = max((int)(((unsigned)all + (unsigned)pieces - 1) / (unsigned)pieces), kLeastBlocks);
+    const long long from = (long long)p.quota * x;
+    p.blocks = from < all ? min(p.quota, all - (int)from) : 0;
+    const int beg = (int)min(from, (long long)all - 1);
+    const unsigned who = __ballot_sync(0xffffffffu, end - mine <= beg && beg < end);
+    int at = end - mine, b = b0, nb = 1;
+    if (end - mine <= beg && beg < end) {
+        for (;; ++b) {
+            nb = unit_blocks(key_axis(a, keys_of(a, b)).span);
+            if (beg < at + units * nb) break;
+            at += units * nb;
+        }
+    }
+    const int from_lane = __ffs(who) - 1;
+    p.b = __shfl_sync(0xffffffffu, b, from_lane);
+    nb = __shfl_sync(0xffffffffu, nb, from_lane);
+    const int off = beg - __shfl_sync(0xffffffffu, at, from_lane);
+    p.u = off / nb;
+    p.kb = off - p.u * nb;
+    return p;
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN_CTAS)
     decode_q8_kernel(const DecodeQ8Args a) {
@@ -107,37 +169,59 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     dependents_may_start();
     wait_for_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int split = blockIdx.x, hkv = blockIdx.y / a.tiles, rbase = blockIdx.y % a.tiles * T::R;
-    const int b = blockIdx.z;
-    const int L = max(0, min(a.seqlens_k[b], a.Sk));
-    const Axis axis = key_axis(a, L);
-    const int x_lo = split * a.chunk, x_hi = min(x_lo + a.chunk, axis.span);
     const bool joined = a.joined != 0;
-    if (joined) cluster_arrive();   // (waited for before the first write to another)
-    if (x_lo >= axis.span && !joined) return;
-    const int n_slices = max(0, x_hi - x_lo + T::KB - 1) / T::KB;
-    const int mine = n_slices > warp ? (n_slices - warp + T::WARPS - 1) / T::WARPS : 0;
+    const int units = a.Hkv * a.tiles;
+    Piece piece;
+    if (joined) {   // grid (splits of a unit, units, batch entries), the splits a cluster
+        cluster_arrive();   // (waited for before the first write to another)
+        const int nb = unit_blocks(key_axis(a, keys_of(a, blockIdx.z)).span), n = a.chunk / kBlock;
+        piece.b = blockIdx.z;
+        piece.u = blockIdx.y;
+        piece.kb = (int)blockIdx.x * n;
+        piece.blocks = max(0, min(n, nb - piece.kb));
+        piece.quota = n;
+    } else {
+        piece = place_piece(a, blockIdx.x, gridDim.x);
+        if (threadIdx.x == 0) {
+            a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
+            if (blockIdx.x == 0) a.head[2 * gridDim.x] = make_int4(piece.quota, 0, 0, 0);
+        }
+        if (piece.blocks == 0) return;
+    }
 
     // ------------------------------------------------ ring
-    const uint32_t ring = smem_u32(smem) + warp * T::STAGES * T::STAGE;
-    const int* table = a.block_table + (size_t)b * a.max_pages;
-    // This lane's key (lane & 15) of a slice: its page, -1 where it is not loaded,
-    // and its row there.  Nothing waits for the page before the slice is issued.
-    int page = -1;
+    const uint32_t ring = smem_u32(smem) + warp * T::WARP_RING;
+    // The producer's place on the line: unit lu of batch entry lb, block lk; and
+    // this lane's key (lane & 15) of the slice looked up last: its page, -1 where
+    // it is not loaded, and its row there.  Nothing waits for the page before the
+    // slice is issued.
+    int lb = piece.b, lu = piece.u, lk = piece.kb, l_head = 0;
+    Axis la = key_axis(a, keys_of(a, lb));
+    int page = -1, page_head = 0;
     unsigned page_row = 0;
-    auto look_up = [&](int i) {
-        const int x = x_lo + T::KB * (warp + T::WARPS * i) + (lane & 15);
-        const int key = axis.key(x);
+    l_head = lu / a.tiles;
+    auto look_up = [&]() {
+        if (lk * kBlock >= la.span && lk > 0) {   // the next unit
+            lk = 0;
+            if (++lu == units) {
+                lu = 0;
+                la = key_axis(a, keys_of(a, ++lb));
+            }
+            l_head = lu / a.tiles;
+        }
+        const int x = lk * kBlock + T::KB * warp + (lane & 15);
+        const int key = la.key(x);
         page = -1;
-        if (x >= x_hi || (key < axis.lo && key >= a.first)) return;
+        page_head = l_head;
+        ++lk;
+        if (x >= la.span || (key < la.lo && key >= a.first)) return;
         const unsigned p = (unsigned)key / (unsigned)a.page_size;
         page_row = (unsigned)key - p * (unsigned)a.page_size;
-        page = table[p];
+        page = a.block_table[(size_t)lb * a.max_pages + p];
     };
-    auto load_slice = [&](int i) {
-        const uint32_t to = ring + (i % T::STAGES) * T::STAGE;
+    auto load_slice = [&](uint32_t to) {
         const bool there = (unsigned)page < (unsigned)a.num_pages;   // (no page: reads as zeros)
-        const uint32_t head = (uint32_t)page * (uint32_t)a.Hkv + (uint32_t)hkv;
+        const uint32_t head = (uint32_t)page * (uint32_t)a.Hkv + (uint32_t)page_head;
         // its row among all rows of the cache (below 2^32), and its scale
         const uint32_t at_row = head * (uint32_t)a.page_size + page_row;
         const uint32_t at_scale = head * (uint32_t)a.blocks + page_row / (unsigned)a.block;
@@ -154,400 +238,462 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         cp_async_4(to + 2 * T::SLICE + lane * 4,
                    (lane < 16 ? a.k_scale : a.v_scale) + (there ? at_scale : 0), there ? 4u : 0u);
     };
-    if (mine > 0) look_up(0);
-#pragma unroll
-    for (int s = 0; s < T::STAGES - 1; ++s) {
-        if (s < mine) {
-            load_slice(s);
-            if (s + 1 < mine) look_up(s + 1);
+    int issued = 0, in_slot = 0, out_slot = 0;
+    auto issue = [&]() {   // the slice looked up, and the look-up of the next
+        if (issued < piece.blocks) {
+            load_slice(ring + in_slot * T::STAGE);
+            if (++issued < piece.blocks) look_up();
         }
         cp_async_commit();
-    }
+        if (++in_slot == T::STAGES) in_slot = 0;
+    };
+    if (piece.blocks > 0) look_up();
+#pragma unroll 1
+    for (int s = 0; s < T::STAGES - 1; ++s) issue();
 
-    // ------------------------------------------------ queries
-    // B fragments: lane (g, t) has row nr 8 + g, of each 64 dims the 16 from 16 t on
-    uint32_t qb[NR][D / 16][2];
-    float unit[NR][2];   // scores of rows 2 t, 2 t + 1 are sums times this (log2 units)
-    int place[NR][2];    // the rows' keys
+    // ------------------------------------------------ segments: a unit's blocks here
+    int left = piece.blocks, b = piece.b, at_unit = piece.u, kb = piece.kb, index = 0;
+#pragma unroll 1
+    do {
+        const int L = keys_of(a, b);
+        const Axis axis = key_axis(a, L);
+        const int nb = unit_blocks(axis.span), n = min(nb - kb, left);
+        const int hkv = at_unit / a.tiles, rbase = (at_unit - hkv * a.tiles) * T::R;
+        // ------------------------------------------------ queries
+        // B fragments: lane (g, t) has row nr 8 + g, of each 64 dims the 16 from 16 t on
+        uint32_t qb[NR][D / 16][2];
+        float unit[NR][2];   // scores of rows 2 t, 2 t + 1 are sums times this (log2 units)
+        int place[NR][2];    // the rows' keys
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-        const int pr = rbase + nr * 8 + g;
-        uint32_t w[D / 64][8];
-        float most = 0.f;
-        if (pr < a.rows) {
-            const int h = hkv * a.group + pr / a.Sq;
-            const uint16_t* q = a.q + (((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq) * D + t * 16;
+        for (int nr = 0; nr < NR; ++nr) {
+            const int pr = rbase + nr * 8 + g;
+            uint32_t w[D / 64][8];
+            float most = 0.f;
+            if (pr < a.rows) {
+                const int h = hkv * a.group + pr / a.Sq;
+                const uint16_t* q = a.q + (((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq) * D + t * 16;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const uint4 x = *reinterpret_cast<const uint4*>(q + c * 64);
-                const uint4 y = *reinterpret_cast<const uint4*>(q + c * 64 + 8);
-                w[c][0] = x.x, w[c][1] = x.y, w[c][2] = x.z, w[c][3] = x.w;
-                w[c][4] = y.x, w[c][5] = y.y, w[c][6] = y.z, w[c][7] = y.w;
-            }
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[c][e] << 16)),
-                                             fabsf(__uint_as_float(w[c][e] & 0xffff0000u))));
-        } else {
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[c][e] = 0;
-        }
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // 2^-e of the largest element's exponent (1 for a row of zeros; exponents
-        // at which it would not be a normal number stay short of them)
-        int ex = (int)(__float_as_uint(most) >> 23) - 127;
-        ex = most == 0.f ? 0 : max(-125, min(ex, 125));
-        const float by = __uint_as_float((uint32_t)(127 - ex) << 23);
-        const float back = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t x = w[c][2 * s + e];
-                    qb[nr][c * 4 + s][e] =
-                        pack_halves(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(q + c * 64);
+                    const uint4 y = *reinterpret_cast<const uint4*>(q + c * 64 + 8);
+                    w[c][0] = x.x, w[c][1] = x.y, w[c][2] = x.z, w[c][3] = x.w;
+                    w[c][4] = y.x, w[c][5] = y.y, w[c][6] = y.z, w[c][7] = y.w;
                 }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            unit[nr][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
-            place[nr][e] = (rbase + nr * 8 + 2 * t + e) % a.Sq + L - a.Sq;
-        }
-    }
-    // keys [all_lo, all_hi) are seen by every row of the sequence, as those below
-    // all_first are
-    const int all_hi = a.causal ? L - a.Sq + 1 : L;
-    const int all_lo = a.window > 0 ? L - a.window : 0;
-    const int all_first = min(a.first, all_hi);
-
-    float oacc[NR][T::MT][4];
+                for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
+                    for (int e = 0; e < 8; ++e)
+                        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[c][e] << 16)),
+                                                 fabsf(__uint_as_float(w[c][e] & 0xffff0000u))));
+            } else {
 #pragma unroll
-        for (int j = 0; j < T::MT; ++j)
-            oacc[nr][j][0] = oacc[nr][j][1] = oacc[nr][j][2] = oacc[nr][j][3] = 0.f;
-    // of rows 2 t + e: bases of the sum and of O (the same in all lanes of a row),
-    // and this lane's part of the sum
-    float m[NR][2], mv[NR][2], l[NR][2];
+                for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
+                    for (int e = 0; e < 8; ++e) w[c][e] = 0;
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            // 2^-e of the largest element's exponent (1 for a row of zeros; exponents
+            // at which it would not be a normal number stay short of them)
+            int ex = (int)(__float_as_uint(most) >> 23) - 127;
+            ex = most == 0.f ? 0 : max(-125, min(ex, 125));
+            const float by = __uint_as_float((uint32_t)(127 - ex) << 23);
+            const float back = __uint_as_float((uint32_t)(127 + ex) << 23) * a.scale_log2;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            m[nr][e] = mv[nr][e] = -INFINITY;
-            l[nr][e] = 0.f;
-        }
-
-    for (int i = 0; i < mine; ++i) {
-        cp_async_wait<T::STAGES - 2>();
-        __syncwarp();
-        const uint32_t sk = ring + (i % T::STAGES) * T::STAGE, sv = sk + T::SLICE, sc = sv + T::SLICE;
-        const int x0 = x_lo + T::KB * (warp + T::WARPS * i);
-
-        float sacc[NR][4];
+            for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) sacc[nr][0] = sacc[nr][1] = sacc[nr][2] = sacc[nr][3] = 0.f;
+                for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            const uint4 u = lds128(sk + k_place<D>(g, c * 4 + t));
-            const uint4 w = lds128(sk + k_place<D>(g + 8, c * 4 + t));
-            const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t x = w[c][2 * s + e];
+                        qb[nr][c * 4 + s][e] =
+                            pack_halves(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
+                    }
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const uint32_t a0 = q8_halves(uu[s]), a1 = q8_halves(ww[s]);
-                const uint32_t a2 = q8_halves_up(uu[s]), a3 = q8_halves_up(ww[s]);
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-                    mma_f16_16816(sacc[nr], a0, a1, a2, a3, qb[nr][c * 4 + s][0], qb[nr][c * 4 + s][1]);
+            for (int e = 0; e < 2; ++e) {
+                unit[nr][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
+                place[nr][e] = (rbase + nr * 8 + 2 * t + e) % a.Sq + L - a.Sq;
             }
         }
-        const float ks[2] = {lds32(sc + g * 4), lds32(sc + 32 + g * 4)};
-        const float lv[2] = {lg2_approx(lds32(sc + 64 + g * 4)), lg2_approx(lds32(sc + 96 + g * 4))};
-        // scores, in place: sacc[nr][2 f + e] is that of key g + 8 f in row 2 t + e
-        const int key0 = axis.key(x0);
-        const bool whole = x0 + T::KB <= x_hi && key0 + T::KB <= all_hi &&
-                           (key0 >= all_lo || key0 + T::KB <= all_first);
-        bool over = false;
+        // keys [all_lo, all_hi) are seen by every row of the sequence, as those below
+        // all_first are
+        const int all_hi = a.causal ? L - a.Sq + 1 : L;
+        const int all_lo = a.window > 0 ? L - a.window : 0;
+        const int all_first = min(a.first, all_hi);
+
+        float oacc[NR][T::MT][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int j = 0; j < T::MT; ++j)
+                oacc[nr][j][0] = oacc[nr][j][1] = oacc[nr][j][2] = oacc[nr][j][3] = 0.f;
+        // of rows 2 t + e: bases of the sum and of O (the same in all lanes of a row),
+        // and this lane's part of the sum
+        float m[NR][2], mv[NR][2], l[NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float top = m[nr][e] + kGrow, top_v = mv[nr][e] + kGrow;
+                m[nr][e] = mv[nr][e] = -INFINITY;
+                l[nr][e] = 0.f;
+            }
+
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            cp_async_wait<T::STAGES - 2>();
+            __syncwarp();
+            const uint32_t sk = ring + out_slot * T::STAGE, sv = sk + T::SLICE, sc = sv + T::SLICE;
+            const int x0 = (kb + i) * kBlock + T::KB * warp;
+
+            float sacc[NR][4];
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    float& s = sacc[nr][2 * f + e];
-                    s *= unit[nr][e] * ks[f];
-                    if (!whole) {
-                        const int key = key0 + g + 8 * f, p = place[nr][e];
-                        const bool seen = x0 + g + 8 * f < x_hi && (!a.causal || key <= p) &&
-                                          (a.window <= 0 || key > p - a.window || key < a.first);
-                        s = seen ? s : -INFINITY;
-                    }
-                    over |= s > top || s + lv[f] > top_v;
+            for (int nr = 0; nr < NR; ++nr) sacc[nr][0] = sacc[nr][1] = sacc[nr][2] = sacc[nr][3] = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                const uint4 u = lds128(sk + k_place<D>(g, c * 4 + t));
+                const uint4 w = lds128(sk + k_place<D>(g + 8, c * 4 + t));
+                const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t a0 = q8_halves(uu[s]), a1 = q8_halves(ww[s]);
+                    const uint32_t a2 = q8_halves_up(uu[s]), a3 = q8_halves_up(ww[s]);
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+                        mma_f16_16816(sacc[nr], a0, a1, a2, a3, qb[nr][c * 4 + s][0], qb[nr][c * 4 + s][1]);
                 }
             }
-        if (__any_sync(0xffffffffu, over)) {
+            const float ks[2] = {lds32(sc + g * 4), lds32(sc + 32 + g * 4)};
+            const float lv[2] = {lg2_approx(lds32(sc + 64 + g * 4)), lg2_approx(lds32(sc + 96 + g * 4))};
+            // scores, in place: sacc[nr][2 f + e] is that of key g + 8 f in row 2 t + e
+            const int key0 = axis.key(x0);
+            const bool whole = x0 + T::KB <= axis.span && key0 + T::KB <= all_hi &&
+                               (key0 >= all_lo || key0 + T::KB <= all_first);
+            bool over = false;
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = fmaxf(sacc[nr][e], sacc[nr][2 + e]);
-                    float y = fmaxf(sacc[nr][e] + lv[0], sacc[nr][2 + e] + lv[1]);
+                    const float top = m[nr][e] + kGrow, top_v = mv[nr][e] + kGrow;
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                        y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-                    }
-                    x = fmaxf(x, m[nr][e]);
-                    y = fmaxf(y, mv[nr][e]);
-                    if (x > m[nr][e]) l[nr][e] *= ex2_approx(m[nr][e] - x);   // (0 from -inf)
-                    const float by = y > mv[nr][e] ? ex2_approx(mv[nr][e] - y) : 1.f;
-                    m[nr][e] = x;
-                    mv[nr][e] = y;
-#pragma unroll
-                    for (int j = 0; j < T::MT; ++j) {
-                        oacc[nr][j][e] *= by;
-                        oacc[nr][j][2 + e] *= by;
+                    for (int f = 0; f < 2; ++f) {
+                        float& s = sacc[nr][2 * f + e];
+                        s *= unit[nr][e] * ks[f];
+                        if (!whole) {
+                            const int key = key0 + g + 8 * f, p = place[nr][e];
+                            const bool seen = x0 + g + 8 * f < axis.span && (!a.causal || key <= p) &&
+                                              (a.window <= 0 || key > p - a.window || key < a.first);
+                            s = seen ? s : -INFINITY;
+                        }
+                        over |= s > top || s + lv[f] > top_v;
                     }
                 }
-        }
-        uint32_t pb[NR][2];
+            if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-            float pv[2][2];
+                for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float base = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
-                const float base_v = mv[nr][e] == -INFINITY ? 0.f : mv[nr][e] - kLift;
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(sacc[nr][e], sacc[nr][2 + e]);
+                        float y = fmaxf(sacc[nr][e] + lv[0], sacc[nr][2 + e] + lv[1]);
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const float s = sacc[nr][2 * f + e];
-                    l[nr][e] += ex2_approx(s - base);
-                    pv[f][e] = ex2_approx(s + lv[f] - base_v);
-                }
+                        for (int o = 4; o < 32; o <<= 1) {
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+                        }
+                        x = fmaxf(x, m[nr][e]);
+                        y = fmaxf(y, mv[nr][e]);
+                        if (x > m[nr][e]) l[nr][e] *= ex2_approx(m[nr][e] - x);   // (0 from -inf)
+                        const float by = y > mv[nr][e] ? ex2_approx(mv[nr][e] - y) : 1.f;
+                        m[nr][e] = x;
+                        mv[nr][e] = y;
+#pragma unroll
+                        for (int j = 0; j < T::MT; ++j) {
+                            oacc[nr][j][e] *= by;
+                            oacc[nr][j][2 + e] *= by;
+                        }
+                    }
             }
-#pragma unroll
-            for (int f = 0; f < 2; ++f) pb[nr][f] = movmatrix_trans(pack_halves(pv[f][0], pv[f][1]));
-        }
-        // O^T += V^T P^T: lane (g, t) has 16 dims (64: 8) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-        auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
-            // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
-            const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
-            const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
-            const uint32_t a0 = q8_halves(xl), a1 = q8_halves_up(xl), a2 = q8_halves(yl), a3 = q8_halves_up(yl);
-            const uint32_t b0 = q8_halves(xh), b1 = q8_halves_up(xh), b2 = q8_halves(yh), b3 = q8_halves_up(yh);
+            uint32_t pb[NR][2];
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) {
-                mma_f16_16816(oacc[nr][j], a0, a1, a2, a3, pb[nr][0], pb[nr][1]);
-                mma_f16_16816(oacc[nr][j + 1], b0, b1, b2, b3, pb[nr][0], pb[nr][1]);
-            }
-        };
-        if constexpr (D == 64) {
-            const uint32_t half = (g & 1) * 8;
-            const uint2 x0_ = lds64(sv + v_place<D>(2 * t, g >> 1) + half);
-            const uint2 x1_ = lds64(sv + v_place<D>(2 * t + 1, g >> 1) + half);
-            const uint2 y0_ = lds64(sv + v_place<D>(2 * t + 8, g >> 1) + half);
-            const uint2 y1_ = lds64(sv + v_place<D>(2 * t + 9, g >> 1) + half);
-            add(0, x0_.x, x1_.x, y0_.x, y1_.x);
-            add(2, x0_.y, x1_.y, y0_.y, y1_.y);
-        } else {
+                float pv[2][2];
 #pragma unroll
-            for (int c = 0; c < D / 128; ++c) {
-                const uint4 x0_ = lds128(sv + v_place<D>(2 * t, c * 8 + g));
-                const uint4 x1_ = lds128(sv + v_place<D>(2 * t + 1, c * 8 + g));
-                const uint4 y0_ = lds128(sv + v_place<D>(2 * t + 8, c * 8 + g));
-                const uint4 y1_ = lds128(sv + v_place<D>(2 * t + 9, c * 8 + g));
-                add(c * 8, x0_.x, x1_.x, y0_.x, y1_.x);
-                add(c * 8 + 2, x0_.y, x1_.y, y0_.y, y1_.y);
-                add(c * 8 + 4, x0_.z, x1_.z, y0_.z, y1_.z);
-                add(c * 8 + 6, x0_.w, x1_.w, y0_.w, y1_.w);
+                for (int e = 0; e < 2; ++e) {
+                    const float base = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
+                    const float base_v = mv[nr][e] == -INFINITY ? 0.f : mv[nr][e] - kLift;
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const float s = sacc[nr][2 * f + e];
+                        l[nr][e] += ex2_approx(s - base);
+                        pv[f][e] = ex2_approx(s + lv[f] - base_v);
+                    }
+                }
+#pragma unroll
+                for (int f = 0; f < 2; ++f) pb[nr][f] = movmatrix_trans(pack_halves(pv[f][0], pv[f][1]));
             }
+            // O^T += V^T P^T: lane (g, t) has 16 dims (64: 8) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
+                // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
+                const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
+                const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
+                const uint32_t a0 = q8_halves(xl), a1 = q8_halves_up(xl), a2 = q8_halves(yl), a3 = q8_halves_up(yl);
+                const uint32_t b0 = q8_halves(xh), b1 = q8_halves_up(xh), b2 = q8_halves(yh), b3 = q8_halves_up(yh);
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    mma_f16_16816(oacc[nr][j], a0, a1, a2, a3, pb[nr][0], pb[nr][1]);
+                    mma_f16_16816(oacc[nr][j + 1], b0, b1, b2, b3, pb[nr][0], pb[nr][1]);
+                }
+            };
+            if constexpr (D == 64) {
+                const uint32_t half = (g & 1) * 8;
+                const uint2 x0_ = lds64(sv + v_place<D>(2 * t, g >> 1) + half);
+                const uint2 x1_ = lds64(sv + v_place<D>(2 * t + 1, g >> 1) + half);
+                const uint2 y0_ = lds64(sv + v_place<D>(2 * t + 8, g >> 1) + half);
+                const uint2 y1_ = lds64(sv + v_place<D>(2 * t + 9, g >> 1) + half);
+                add(0, x0_.x, x1_.x, y0_.x, y1_.x);
+                add(2, x0_.y, x1_.y, y0_.y, y1_.y);
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 128; ++c) {
+                    const uint4 x0_ = lds128(sv + v_place<D>(2 * t, c * 8 + g));
+                    const uint4 x1_ = lds128(sv + v_place<D>(2 * t + 1, c * 8 + g));
+                    const uint4 y0_ = lds128(sv + v_place<D>(2 * t + 8, c * 8 + g));
+                    const uint4 y1_ = lds128(sv + v_place<D>(2 * t + 9, c * 8 + g));
+                    add(c * 8, x0_.x, x1_.x, y0_.x, y1_.x);
+                    add(c * 8 + 2, x0_.y, x1_.y, y0_.y, y1_.y);
+                    add(c * 8 + 4, x0_.z, x1_.z, y0_.z, y1_.z);
+                    add(c * 8 + 6, x0_.w, x1_.w, y0_.w, y1_.w);
+                }
+            }
+            __syncwarp();
+            issue();
+            if (++out_slot == T::STAGES) out_slot = 0;
         }
-        __syncwarp();
-        const int next = i + T::STAGES - 1;
-        if (next < mine) {
-            load_slice(next);
-            if (next + 1 < mine) look_up(next + 1);
-        }
-        cp_async_commit();
-    }
-    cp_async_wait<0>();
-    __syncthreads();   // every warp is done with its ring
 
-    // ------------------------------------------------ merge of the warps
-    float* wm = reinterpret_cast<float*>(smem);   // [WARPS][R]
-    float* wl = wm + T::WARPS * T::R;
-    float* wo = wl + T::WARPS * T::R;             // [WARPS][R][ROW]
+        // ------------------------------------------------ merge of the warps
+        // eight rows at a time through the slot that was read last, which is free until
+        // the block after the next is issued: [8][D] O (columns turned by the row
+        // against bank conflicts), row maxima, row sums
+        const int last_slot = (out_slot == 0 ? T::STAGES : out_slot) - 1;
+        const float* merge0 = reinterpret_cast<const float*>(smem + last_slot * T::STAGE);
+        float* mine = reinterpret_cast<float*>(smem + warp * T::WARP_RING + last_slot * T::STAGE);
+        constexpr int WF = T::WARP_RING / 4;   // floats from warp to warp
+        const int valid_rows = min(T::R, a.rows - rbase);
+        const bool whole_unit = n == nb;
+        // joined: split s finishes the rows [s own, (s + 1) own) (see decode.cu)
+        const int split = blockIdx.x;
+        const int own = joined ? (T::R + a.n_splits - 1) / a.n_splits : 1;
+        const uint32_t jl = smem_u32(smem) + T::RING, jo = jl + T::JOIN_LSE;
+        auto row_id = [&](int r) {
+            const int pr = rbase + r;
+            return ((size_t)b * a.Hq + hkv * a.group + pr / a.Sq) * a.Sq + pr % a.Sq;
+        };
+        const int part = 2 * (int)blockIdx.x + (index > 0);
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float sum = l[nr][e];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const int r = nr * 8 + 2 * t + e;
-            if (g == 0) {
-                wm[warp * T::R + r] = m[nr][e];
-                wl[warp * T::R + r] = sum;
+        for (int nr = 0; nr < NR; ++nr) {
+            if (nr * 8 >= valid_rows) break;
+            // (not joined: every warp has read its slot, for copies into this one are not
+            // issued before all have passed the barriers below)
+            if (joined && nr == 0) {
+                cp_async_wait<0>();
+                __syncthreads();
+                cluster_wait();
             }
-            // O of the base of the sum (0 where the warp saw no key of the row, or
-            // values of scale 0)
-            const float by = mv[nr][e] == -INFINITY ? 0.f : ex2_approx(mv[nr][e] - kLift - m[nr][e]);
-            float* row = wo + (warp * T::R + r) * T::ROW;
 #pragma unroll
-            for (int j = 0; j < T::MT; ++j) {
-                const int dim = D == 64 ? g * 8 + 2 * j : (j >> 3) * 128 + g * 16 + 2 * (j & 7);
-                *reinterpret_cast<float2*>(row + dim) =
-                    make_float2(oacc[nr][j][e] * by, oacc[nr][j][2 + e] * by);
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nr][e];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const int r = 2 * t + e;
+                if (g == 0) {
+                    mine[8 * D + r] = m[nr][e];
+                    mine[8 * D + 8 + r] = sum;
+                }
+                // O of the base of the sum (0 where the warp saw no key of the row, or
+                // values of scale 0)
+                const float by = mv[nr][e] == -INFINITY ? 0.f : ex2_approx(mv[nr][e] - kLift - m[nr][e]);
+#pragma unroll
+                for (int j = 0; j < T::MT; ++j) {
+                    const int dim = D == 64 ? g * 8 + 2 * j : (j >> 3) * 128 + g * 16 + 2 * (j & 7);
+                    *reinterpret_cast<float2*>(mine + r * D + ((dim + 4 * r) & (D - 1))) =
+                        make_float2(oacc[nr][j][e] * by, oacc[nr][j][2 + e] * by);
+                }
             }
-        }
-    __syncthreads();
-    const int valid_rows = min(T::R, a.rows - rbase);
-    // joined: split s finishes the rows [s own, (s + 1) own) (see decode.cu)
-    const int own = joined ? (T::R + a.n_splits - 1) / a.n_splits : 1;
-    const uint32_t jl = smem_u32(smem) + T::SMEM, jo = jl + T::JOIN_LSE;
-    if (joined) cluster_wait();
-    auto row_id = [&](int r) {
-        const int pr = rbase + r;
-        return ((size_t)b * a.Hq + hkv * a.group + pr / a.Sq) * a.Sq + pr % a.Sq;
-    };
-    for (int e = threadIdx.x * 4; e < valid_rows * D; e += T::THREADS * 4) {
-        const int r = e / D, c = e % D;
-        float M = -INFINITY;
+            __syncthreads();
+#pragma unroll 1
+            for (int e = threadIdx.x * 4; e < 8 * D; e += T::THREADS * 4) {
+                const int r8 = e / D, c = e % D, r = nr * 8 + r8;
+                if (r >= valid_rows) break;
+                float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < T::WARPS; ++w) M = fmaxf(M, wm[w * T::R + r]);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float lse2 = -INFINITY;
-        if (M != -INFINITY) {
-            float sum = 0.f;
+                for (int w = 0; w < T::WARPS; ++w) M = fmaxf(M, merge0[w * WF + 8 * D + r8]);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                float sum = 0.f, lse2 = -INFINITY;
+                const size_t row = row_id(r);
+                const bool sink = whole_unit && !joined && a.sinks != nullptr;
+                const float sg = sink ? a.sinks[hkv * a.group + (rbase + r) / a.Sq] * kLog2ef : -INFINITY;
+                const float base = fmaxf(M, sg);
+                if (base != -INFINITY) {
+                    sum = ex2_approx(sg - base);
 #pragma unroll
-            for (int w = 0; w < T::WARPS; ++w) {
-                const float f = ex2_approx(wm[w * T::R + r] - M);   // 0 for warps without keys
-                const float4 x = *reinterpret_cast<const float4*>(wo + (w * T::R + r) * T::ROW + c);
-                sum = fmaf(f, wl[w * T::R + r], sum);
-                o.x = fmaf(f, x.x, o.x);
-                o.y = fmaf(f, x.y, o.y);
-                o.z = fmaf(f, x.z, o.z);
-                o.w = fmaf(f, x.w, o.w);
+                    for (int w = 0; w < T::WARPS; ++w) {
+                        const float f = ex2_approx(merge0[w * WF + 8 * D + r8] - base);   // 0 for warps without keys
+                        const float4 x = *reinterpret_cast<const float4*>(merge0 + w * WF + r8 * D +
+                                                                          ((c + 4 * r8) & (D - 1)));
+                        sum = fmaf(f, merge0[w * WF + 8 * D + 8 + r8], sum);
+                        o.x = fmaf(f, x.x, o.x);
+                        o.y = fmaf(f, x.y, o.y);
+                        o.z = fmaf(f, x.z, o.z);
+                        o.w = fmaf(f, x.w, o.w);
+                    }
+                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                    lse2 = sum > 0.f ? base + lg2_approx(sum) : -INFINITY;
+                }
+                if (joined) {
+                    const int to = r / own, at = split * own + r - to * own;
+                    cluster_write4(jo + (at * D + c) * 4, to, o);
+                    if (c == 0) cluster_write(jl + at * 4, to, lse2);
+                } else if (whole_unit) {
+                    *reinterpret_cast<uint2*>(a.o + row * D + c) =
+                        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+                    if (c == 0) a.lse[row] = lse2 * kLn2f;
+                } else {
+                    *reinterpret_cast<float4*>(a.part_o + ((size_t)part * T::R + r) * D + c) = o;
+                    if (c == 0) a.part_lse[(size_t)part * T::R + r] = lse2;
+                }
             }
-            const float inv = 1.f / sum;
-            o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-            lse2 = M + lg2_approx(sum);
+            __syncthreads();
         }
         if (joined) {
-            const int to = r / own, at = split * own + r - to * own;
-            cluster_write4(jo + (at * D + c) * 4, to, o);
-            if (c == 0) cluster_write(jl + at * 4, to, lse2);
-            continue;
-        }
-        const size_t part = (size_t)split * a.B * a.Hq * a.Sq + row_id(r);
-        *reinterpret_cast<float4*>(a.part_o + part * D + c) = o;
-        if (c == 0) a.part_lse[part] = lse2;
-    }
-    if (!joined) return;
-    cluster_sync_all();
-    for (int e = threadIdx.x * 4; e < own * D; e += T::THREADS * 4) {
-        const int k = e / D, c = e % D, r = split * own + k;
-        if (r >= valid_rows) break;
-        const int h = hkv * a.group + (rbase + r) / a.Sq;
-        const uint8_t* from = smem + T::SMEM;
-        const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
-        float x[kJoinSplits], M = sg, sum = 0.f;
-        float4 y[kJoinSplits], o = make_float4(0.f, 0.f, 0.f, 0.f);
+            cluster_sync_all();
+#pragma unroll 1
+            for (int e = threadIdx.x * 4; e < own * D; e += T::THREADS * 4) {
+                const int k = e / D, c = e % D, r = split * own + k;
+                if (r >= valid_rows) break;
+                const uint8_t* from = smem + T::RING;
+                const float sg = a.sinks != nullptr ? a.sinks[hkv * a.group + (rbase + r) / a.Sq] * kLog2ef : -INFINITY;
+                float x[kJoinSplits], M = sg, sum = 0.f;
+                float4 y[kJoinSplits], o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int s = 0; s < kJoinSplits; ++s) {
-            x[s] = -INFINITY;
-            y[s] = o;
-            if (s < a.n_splits) {
-                x[s] = *reinterpret_cast<const float*>(from + (s * own + k) * 4);
-                y[s] = *reinterpret_cast<const float4*>(from + T::JOIN_LSE + ((s * own + k) * D + c) * 4);
-            }
-            M = fmaxf(M, x[s]);
-        }
-        if (M != -INFINITY) {
-            sum = ex2_approx(sg - M);
+                for (int s = 0; s < kJoinSplits; ++s) {
+                    x[s] = -INFINITY;
+                    y[s] = o;
+                    if (s < a.n_splits) {
+                        x[s] = *reinterpret_cast<const float*>(from + (s * own + k) * 4);
+                        y[s] = *reinterpret_cast<const float4*>(from + T::JOIN_LSE + ((s * own + k) * D + c) * 4);
+                    }
+                    M = fmaxf(M, x[s]);
+                }
+                if (M != -INFINITY) {
+                    sum = ex2_approx(sg - M);
 #pragma unroll
-            for (int s = 0; s < kJoinSplits; ++s) {
-                const float f = ex2_approx(x[s] - M);
-                sum += f;
-                o.x = fmaf(f, y[s].x, o.x);
-                o.y = fmaf(f, y[s].y, o.y);
-                o.z = fmaf(f, y[s].z, o.z);
-                o.w = fmaf(f, y[s].w, o.w);
+                    for (int s = 0; s < kJoinSplits; ++s) {
+                        const float f = ex2_approx(x[s] - M);
+                        sum += f;
+                        o.x = fmaf(f, y[s].x, o.x);
+                        o.y = fmaf(f, y[s].y, o.y);
+                        o.z = fmaf(f, y[s].z, o.z);
+                        o.w = fmaf(f, y[s].w, o.w);
+                    }
+                }
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                const size_t row = row_id(r);
+                *reinterpret_cast<uint2*>(a.o + row * D + c) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
             }
+            return;
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
-        const size_t row = row_id(r);
-        *reinterpret_cast<uint2*>(a.o + row * D + c) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
-    }
+        if (!whole_unit && threadIdx.x == 0) a.head[part] = make_int4(b, at_unit, n, kb == 0 ? nb : 0);
+        left -= n;
+        kb = 0;
+        ++index;
+        if (++at_unit == units) {
+            at_unit = 0;
+            ++b;
+        }
+    } while (left > 0);
+    cp_async_wait<0>();
 }
 
-// A warp per query row: merges its splits by their LSE, with the head's sink.
+// Merges the pieces of the unit that starts in CTA blockIdx.x of the kernel before
+// and goes on in the next ones: row blockIdx.y of its tile, eight warps over the
+// pieces, lanes over the columns.
 template <int D>
-__global__ void __launch_bounds__(256) combine_q8_kernel(const DecodeQ8Args a) {
+__global__ void __launch_bounds__(256) combine_q8_kernel(const DecodeQ8Args a, int tile) {
+    constexpr int PER = D / 32;   // columns of a lane
+    __shared__ float other[8][D], weight[8];
     dependents_may_start();
     wait_for_previous();
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const long long n_rows = (long long)a.B * a.Hq * a.Sq;
-    if (row >= n_rows) return;
-    const int b = (int)(row / ((long long)a.Hq * a.Sq)), h = (int)(row / a.Sq % a.Hq);
-    const int L = max(0, min(a.seqlens_k[b], a.Sk));
-    const int ns = (key_axis(a, L).span + a.chunk - 1) / a.chunk;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = gridDim.x, r = blockIdx.y;
+    const int4 h0 = a.head[2 * blockIdx.x], h1 = a.head[2 * blockIdx.x + 1];
+    const int quota = a.head[2 * G].x;
+    const bool second = h0.w == 0;   // (.w: the unit's blocks where a piece is its first)
+    const int4 hd = second ? h1 : h0;
+    if (hd.w == 0) return;
+    const int b = hd.x, hkv = hd.y / a.tiles, rbase = (hd.y - hkv * a.tiles) * tile;
+    if (rbase + r >= a.rows) return;
+    const int pieces = 1 + (hd.w - hd.z + quota - 1) / quota;
+    auto slot = [&](int k) { return k == 0 ? 2 * (int)blockIdx.x + second : 2 * ((int)blockIdx.x + k); };
+    const int h = hkv * a.group + (rbase + r) / a.Sq;
     const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
     float M = sg;
-    for (int s = lane; s < ns; s += 32) M = fmaxf(M, a.part_lse[s * n_rows + row]);
+    for (int k = lane; k < pieces; k += 32) M = fmaxf(M, a.part_lse[(size_t)slot(k) * tile + r]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    constexpr int PER = D / 64;   // pairs of columns of a lane
-    float2 acc[PER];
+    float acc[PER], sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = make_float2(0.f, 0.f);
-    float sum = 0.f;
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
     if (M != -INFINITY) {
-        sum = ex2_approx(sg - M);
 #pragma unroll 4
-        for (int s = 0; s < ns; ++s) {
-            const float f = ex2_approx(a.part_lse[s * n_rows + row] - M);
-            const float2* po = reinterpret_cast<const float2*>(a.part_o + (s * n_rows + row) * D);
+        for (int k = warp; k < pieces; k += 8) {
+            const size_t at = (size_t)slot(k) * tile + r;
+            const float f = ex2_approx(a.part_lse[at] - M);
             sum += f;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                const float2 x = po[lane + 32 * e];
-                acc[e].x = fmaf(f, x.x, acc[e].x);
-                acc[e].y = fmaf(f, x.y, acc[e].y);
+            for (int e = 0; e < PER; e += 2) {
+                const float2 x = *reinterpret_cast<const float2*>(a.part_o + at * D + e * 32 + 2 * lane);
+                acc[e] = fmaf(f, x.x, acc[e]);
+                acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
             }
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    uint32_t* o = reinterpret_cast<uint32_t*>(a.o + row * D);
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[lane + 32 * e] = pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
-    if (lane == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
+    for (int e = 0; e < PER; e += 2)
+        *reinterpret_cast<float2*>(&other[warp][e * 32 + 2 * lane]) = make_float2(acc[e], acc[e + 1]);
+    if (lane == 0) weight[warp] = sum;
+    __syncthreads();
+    const int c = threadIdx.x * 2;
+    if (c >= D) return;
+    sum = M != -INFINITY ? ex2_approx(sg - M) : 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        sum += weight[w];
+        o.x += other[w][c];
+        o.y += other[w][c + 1];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const size_t row = ((size_t)b * a.Hq + h) * a.Sq + (rbase + r) % a.Sq;
+    *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o.x * inv, o.y * inv);
+    if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
 }
 
 template <int D, int NR>
 cudaError_t launch_tile(const DecodeQ8Args& a, cudaStream_t s) {
     using T = Q8Traits<D, NR>;
-    const int smem = T::SMEM + (a.joined ? T::JOIN : 0);
     cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, NR>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM + T::JOIN);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, T::RING + T::JOIN);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)a.n_splits, (unsigned)(a.Hkv * a.tiles), (unsigned)a.B);
     if (a.joined)
-        return launch_dependent_clusters(decode_q8_kernel<D, NR>, (unsigned)a.n_splits, grid,
-                                         dim3(T::THREADS), smem, s, a);
-    e = launch_dependent(decode_q8_kernel<D, NR>, grid, dim3(T::THREADS), smem, s, a);
+        return launch_dependent_clusters(
+            decode_q8_kernel<D, NR>, (unsigned)a.n_splits,
+            dim3((unsigned)a.n_splits, (unsigned)(a.Hkv * a.tiles), (unsigned)a.B), dim3(T::THREADS),
+            T::RING + T::JOIN, s, a);
+    e = launch_dependent(decode_q8_kernel<D, NR>, dim3((unsigned)a.n_splits), dim3(T::THREADS), T::RING, s, a);
     if (e != cudaSuccess) return e;
-    const long long rows = (long long)a.B * a.Hq * a.Sq;
-    return launch_dependent(combine_q8_kernel<D>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, a);
+    return launch_dependent(combine_q8_kernel<D>, dim3((unsigned)a.n_splits, (unsigned)T::R), dim3(256), 0, s,
+                            a, (int)T::R);
 }
 
 template <int D>
@@ -562,6 +708,12 @@ cudaError_t launch_dim(const DecodeQ8Args& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int decode_q8_ctas(int head_dim, int tile) {
+    if (head_dim == 64) return tile == 32 ? Q8Traits<64, 4>::MIN_CTAS : Q8Traits<64, 1>::MIN_CTAS;
+    if (head_dim == 128) return tile == 32 ? Q8Traits<128, 4>::MIN_CTAS : Q8Traits<128, 1>::MIN_CTAS;
+    return Q8Traits<256, 1>::MIN_CTAS;
+}
 
 cudaError_t launch_decode_q8(const DecodeQ8Args& a, int head_dim, cudaStream_t s) {
     switch (head_dim) {
