@@ -159,6 +159,21 @@ bool prefill_load_map(CUtensorMap* m, const void* base, int d, long long rows, l
     return encode_map_strided(m, base, d, rows, planes, row_stride, plane_stride);
 }
 
+// 3-D map of bytes {d, rows, planes} with a {min(d, 128), box_rows, 1} box, swizzled
+// over the 64 or 128 bytes of a box's row.
+bool encode_map8(CUtensorMap* m, const void* base, int d, long long rows, long long planes,
+                 unsigned box_rows) {
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)d * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {(cuuint32_t)std::min(d, 128), box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                    estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_map(CUtensorMap* m, const void* base, int d, int rows, long long planes) {
     return encode_map_strided(m, base, d, rows, planes, (unsigned long long)d * 2,
                               (unsigned long long)rows * d * 2);
@@ -606,17 +621,25 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     for (const void* p : {static_cast<const void*>(k_scale), static_cast<const void*>(v_scale),
                           static_cast<const void*>(sinks)})
         if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_MISALIGNED;
-    // (rows of the cache, and of the outputs, are counted in 32 bits)
-    if ((double)num_pages * hkv * page_size >= 4294967296.0) return FA_ERR_INVALID_ARG;
+    // (planes of the cache, its scales and rows of the outputs are counted in 32 bits)
+    if ((long long)num_pages * hkv >= (1ll << 31) ||
+        (double)num_pages * hkv * (page_size / block) >= 4294967296.0)
+        return FA_ERR_INVALID_ARG;
     if ((long long)batch * hq * sq >= (1ll << 31)) return FA_ERR_INVALID_ARG;
     const DeviceInfo* di = device_info();
     if (!di) return FA_ERR_CUDA;
     if (!di->supported) return FA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    DecodeQ8Args a{};
+    DecodeQ8Launch p{};
+    DecodeQ8Args& a = p.args;
     a.q = static_cast<const uint16_t*>(q);
     a.k = static_cast<const uint8_t*>(k);
     a.v = static_cast<const uint8_t*>(v);
+    a.box = std::min(page_size & -page_size, 16);
+    a.planes = num_pages * hkv;
+    if (!encode_map8(&p.maps.k, k, head_dim, page_size, a.planes, (unsigned)a.box) ||
+        !encode_map8(&p.maps.v, v, head_dim, page_size, a.planes, (unsigned)a.box))
+        return FA_ERR_INVALID_ARG;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
     a.o = static_cast<uint16_t*>(o);
@@ -640,8 +663,11 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.max_pages = max_pages;
     a.page_size = page_size;
     a.num_pages = num_pages;
-    a.block = block;
     a.blocks = page_size / block;
+    a.by_page = fast_div(page_size);
+    a.by_block = fast_div(block);
+    a.err_word = di->err_word;
+    a.wait_limit_ns = kWaitLimitNs;
     a.scale_log2 = scale * 1.4426950408889634f;
     const long long heads_first = (a.first + 63ll) / 64 * 64;
     const long long span = window > 0 ? std::min<long long>(sk, (long long)window + sq + 62 + heads_first) : sk;
@@ -651,7 +677,7 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     if (a.joined) {
         a.chunk = (int)(((span + plan.splits - 1) / plan.splits + 63) / 64 * 64);
         a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
-        return from_cuda(launch_decode_q8(a, head_dim, s));
+        return from_cuda(launch_decode_q8(p, head_dim, s));
     }
     // (the kernel counts the blocks of all units in 32 bits)
     const double blocks = (double)pairs * (double)((span + 63) / 64);
@@ -666,7 +692,7 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + bytes_o);
     a.head = reinterpret_cast<int4*>(ws + bytes_o + bytes_l);
-    const cudaError_t e = launch_decode_q8(a, head_dim, s);
+    const cudaError_t e = launch_decode_q8(p, head_dim, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess) return FA_ERR_CUDA;
     return from_cuda(e);
 }

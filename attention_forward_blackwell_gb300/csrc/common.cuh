@@ -301,11 +301,27 @@ struct DecodeArgs {
 constexpr int kJoinSplits = 8;   // most splits of a joined call (CTAs of a cluster)
 cudaError_t launch_decode(const DecodeArgs& a, int head_dim, cudaStream_t s);
 
+// Division of 0 <= n < 2^31 by a number that the host knows: with 2^shift >= d and
+// mul = floor(2^(31 + shift) / d) + 1, n mul exceeds 2^(31 + shift) n / d by at most
+// n d / d < 2^31, too little to reach the next quotient.
+struct FastDiv {
+    uint32_t mul, shift;
+#ifdef __CUDACC__
+    __device__ __forceinline__ unsigned operator()(unsigned n) const { return __umulhi(2u * n, mul) >> shift; }
+#endif
+};
+inline FastDiv fast_div(int d) {
+    FastDiv f{0, 0};
+    while ((1ll << f.shift) < d) ++f.shift;
+    f.mul = (uint32_t)((1ull << (31 + f.shift)) / (unsigned)d + 1);
+    return f;
+}
+
 // Decode over paged caches of 8 bits (decode_q8.cu).
 struct DecodeQ8Args {
     const uint16_t* q;          // [B, Hq, Sq, d] bf16 bits
-    const uint8_t* k;           // [num_pages, Hkv, page_size, d] e4m3 codes
-    const uint8_t* v;
+    const uint8_t* k;           // [num_pages, Hkv, page_size, d] e4m3 codes (read by the maps of
+    const uint8_t* v;           // DecodeQ8Launch, but for single rows of 64 bytes)
     const float* k_scale;       // [num_pages, Hkv, blocks]
     const float* v_scale;
     uint16_t* o;                // [B, Hq, Sq, d]
@@ -327,15 +343,28 @@ struct DecodeQ8Args {
     const float* sinks;
     const int* block_table;
     int max_pages, page_size, num_pages;
-    int block, blocks;          // keys of a scale, scales of a page and head
+    int blocks;                 // scales of a page and head
+    FastDiv by_page, by_block;  // keys / page_size, keys / keys of a scale
+    int box;                    // rows of a copy: the largest power of two up to 16 that
+                                // divides page_size
+    int planes;                 // num_pages * Hkv: the first plane that does not exist
     float scale_log2;
+    unsigned int* err_word;
+    unsigned long long wait_limit_ns;
+};
+struct DecodeQ8Maps {
+    CUtensorMap k, v;           // bytes {d, page_size, planes}, box {min(d, 128), box, 1}
+};
+struct DecodeQ8Launch {
+    DecodeQ8Maps maps;
+    DecodeQ8Args args;
 };
 // Rows of a tile: 8, 16 or, up to head_dim 128, 32.
 inline int decode_q8_tile(int head_dim, int rows) {
     return rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
 }
 int decode_q8_ctas(int head_dim, int tile);   // CTAs that an SM holds at once
-cudaError_t launch_decode_q8(const DecodeQ8Args& a, int head_dim, cudaStream_t s);
+cudaError_t launch_decode_q8(const DecodeQ8Launch& p, int head_dim, cudaStream_t s);
 
 // -------------------------------------------------------------- span ----
 

@@ -23,8 +23,9 @@
 //     running maximum m' of its own beside that of the softmax's sum, so that
 //     the largest terms of O always lie in the upper binades; 2^6 of headroom is
 //     used (kLift), 2^8 of growth allowed before both are moved on (kGrow).
-//   - The row maxima of a slice are never taken: lanes check their own scores
+//   - The row maxima of a slice are never taken: lanes check their own exponents
 //     against the bounds and vote; a shuffle tree follows only where one is over.
+//     Scores and exponents are computed two rows an instruction.
 //
 // Work.  The sequences' lengths are known to the device only, and differ.  A unit
 // (batch entry, key/value head, tile of query rows) counts its blocks of 64 keys;
@@ -38,10 +39,13 @@
 // Short caches are split over the CTAs of a cluster instead, which merge without a
 // second kernel, as decode.cu's joined splits.
 //
-// A warp takes 16 keys of every block through a ring of its own, filled by
-// cp.async with zeros where a key is not there or seen by no row; copies run
-// ahead over the ends of units, and the page numbers of a slice are fetched while
-// the one before is issued.
+// A warp takes 16 keys of every block through a ring of its own.  Tensor copies
+// fill it, one lane for every box of rows that lie together (a page's, up to 16),
+// so that a slice costs the warp a few instructions where 16-byte copies by all
+// lanes took a third of all it issues; copies run ahead over the ends of units,
+// and the page numbers of a slice are fetched while the one before is issued.
+// What a box brings beside keys that some row sees may be anything: scores are
+// replaced, values zeroed in registers, at the borders alone.
 #include "common.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -53,6 +57,9 @@ constexpr float kLn2f = 0.69314718055994530942f;
 constexpr float kLog2ef = 1.44269504088896340736f;
 constexpr float kGrow = 8.0f;   // log2
 constexpr float kLift = 6.0f;
+constexpr float kFar = 3.0e38f;  // minus a base of a row that has seen nothing
+
+constexpr unsigned kSiteQ8 = 72; // wait site of the ring
 
 constexpr int kBlock = 64;      // keys of a block
 constexpr int kLeastBlocks = 4; // of a piece
@@ -63,30 +70,36 @@ struct Q8Traits {
     static constexpr int THREADS = WARPS * 32;
     static constexpr int R = 8 * NR;                    // rows of a tile
     static constexpr int KB = kBlock / WARPS;           // keys of a slice
-    static constexpr int GRAN = D / 16;                 // 16-byte granules of a key
     static constexpr int SLICE = KB * D;                // bytes of a slice of keys, or of values
-    static constexpr int STAGE = 2 * SLICE + 128;       // and the scales of both
+    static constexpr int CHUNK = D == 64 ? 1024 : 2048; // 16 rows of a box
+    static constexpr int STAGE = 2 * SLICE;
     static constexpr int STAGES = D == 64 ? 6 : D == 128 ? 4 : 3;
     static constexpr int WARP_RING = STAGES * STAGE;
-    static constexpr int RING = WARPS * WARP_RING;
+    static constexpr int SCALES = WARPS * WARP_RING;    // behind the ring: scales of both, [32] a slot,
+    static constexpr int WARP_SCALES = STAGES * 128;
+    static constexpr int BARS = SCALES + WARPS * WARP_SCALES;   // a barrier a slot, the abort flag
+    static constexpr int RING = BARS + (WARPS * STAGES + 1) * 8 + (8 & -(WARPS * STAGES + 1 & 1));
     static constexpr int JOIN_ROWS = R + kJoinSplits;   // n splits, ceil(R / n) rows each
     static constexpr int JOIN_LSE = JOIN_ROWS * 4 + (-JOIN_ROWS * 4 & 15);
     static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
     static constexpr int MT = D / 16;                   // tiles of O^T
     static constexpr int MIN_CTAS = NR == 4 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
     // the merge of 8 rows goes through the slot that was read last
-    static_assert(8 * (D + 2) * 4 <= STAGE, "merge buffer");
+    static_assert(8 * D * 4 <= STAGE && RING % 16 == 0, "merge buffer");
 };
 
-// Places of granule g of a key in a slice of keys, and of values (no two lanes of
-// a quarter warp that read together share a bank).
+// Place of granule g (16 bytes) of key row `key` in a slice: the copies' swizzle.
+// S^T row g holds key slice_key(g), whose order lets the lanes of a quarter warp that
+// read together hit all banks, in keys (rows of two lanes' groups) and in values
+// (rows of four lanes).
 template <int D>
-__device__ __forceinline__ uint32_t k_place(int key, int g) {
-    return (uint32_t)(key * D + ((D == 64 ? g : g ^ ((key & 1) << 2)) << 4));
+__device__ __forceinline__ uint32_t place_of(int key, int g) {
+    if (D == 64) return (uint32_t)(key * 64 + ((g ^ ((key >> 1) & 3)) << 4));
+    return (uint32_t)((g >> 3) * 2048 + key * 128 + (((g & 7) ^ (key & 7)) << 4));
 }
 template <int D>
-__device__ __forceinline__ uint32_t v_place(int key, int g) {
-    return (uint32_t)(key * D + ((g ^ (D == 64 ? ((key >> 1) & 1) << 1 : ((key >> 1) & 3) << 1)) << 4));
+__device__ __forceinline__ int slice_key(int g) {
+    return D == 64 ? g : g ^ ((g & 1) << 2);
 }
 
 // Keys that a sequence's splits walk, as in decode.cu: positions [0, span) stand
@@ -163,12 +176,23 @@ __device__ __forceinline__ Piece place_piece(const DecodeQ8Args& a, int x, int p
 
 template <int D, int NR>
 __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN_CTAS)
-    decode_q8_kernel(const DecodeQ8Args a) {
+    decode_q8_kernel(const __grid_constant__ DecodeQ8Maps tm, const DecodeQ8Args a) {
     using T = Q8Traits<D, NR>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
     dependents_may_start();
-    wait_for_previous();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t base = smem_u32(smem), bars = base + T::BARS + warp * T::STAGES * 8;
+    const WaitCtx wc{base + T::BARS + T::WARPS * T::STAGES * 8, (uint32_t)a.wait_limit_ns, a.err_word};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T::WARPS * T::STAGES; ++i) mbar_init(base + T::BARS + i * 8, 1);
+        st_volatile_shared(wc.abort_flag, 0);
+        mbar_fence_init();
+        tma_prefetch_desc(&tm.k);
+        tma_prefetch_desc(&tm.v);
+    }
+    __syncthreads();
+    wait_for_previous();   // (what is above overlaps the kernel before)
     const bool joined = a.joined != 0;
     const int units = a.Hkv * a.tiles;
     Piece piece;
@@ -190,16 +214,15 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     }
 
     // ------------------------------------------------ ring
-    const uint32_t ring = smem_u32(smem) + warp * T::WARP_RING;
+    const uint32_t ring = base + warp * T::WARP_RING, scales = base + T::SCALES + warp * T::WARP_SCALES;
     // The producer's place on the line: unit lu of batch entry lb, block lk; and
-    // this lane's key (lane & 15) of the slice looked up last: its page, -1 where
-    // it is not loaded, and its row there.  Nothing waits for the page before the
-    // slice is issued.
-    int lb = piece.b, lu = piece.u, lk = piece.kb, l_head = 0;
+    // this lane's key (lane & 15) of the slice looked up last: its page, -1 where no
+    // row sees it, and its row there.  Nothing waits for the page before the slice is
+    // issued.
+    int lb = piece.b, lu = piece.u, lk = piece.kb, l_head = lu / a.tiles;
     Axis la = key_axis(a, keys_of(a, lb));
     int page = -1, page_head = 0;
     unsigned page_row = 0;
-    l_head = lu / a.tiles;
     auto look_up = [&]() {
         if (lk * kBlock >= la.span && lk > 0) {   // the next unit
             lk = 0;
@@ -214,34 +237,50 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         page = -1;
         page_head = l_head;
         ++lk;
-        if (x >= la.span || (key < la.lo && key >= a.first)) return;
-        const unsigned p = (unsigned)key / (unsigned)a.page_size;
+        // (a box whose first key no row sees may hold some that a row does)
+        const int last = key | (a.box - 1);
+        if (x >= la.span || (last < la.lo && key >= a.first)) return;
+        const unsigned p = a.by_page((unsigned)key);
         page_row = (unsigned)key - p * (unsigned)a.page_size;
         page = a.block_table[(size_t)lb * a.max_pages + p];
     };
-    auto load_slice = [&](uint32_t to) {
-        const bool there = (unsigned)page < (unsigned)a.num_pages;   // (no page: reads as zeros)
-        const uint32_t head = (uint32_t)page * (uint32_t)a.Hkv + (uint32_t)page_head;
-        // its row among all rows of the cache (below 2^32), and its scale
-        const uint32_t at_row = head * (uint32_t)a.page_size + page_row;
-        const uint32_t at_scale = head * (uint32_t)a.blocks + page_row / (unsigned)a.block;
-        const unsigned rows = __ballot_sync(0xffffffffu, there);
-#pragma unroll
-        for (int u = 0; u < D / 32; ++u) {
-            const int e = lane + 32 * u, key = e / T::GRAN, gr = e % T::GRAN;
-            const bool have = (rows >> key) & 1u;
-            const uint32_t row = __shfl_sync(0xffffffffu, at_row, key);
-            const size_t src = have ? (size_t)row * D + gr * 16 : 0;
-            cp_async_16(to + k_place<D>(key, gr), a.k + src, have ? 16u : 0u);
-            cp_async_16(to + T::SLICE + v_place<D>(key, gr), a.v + src, have ? 16u : 0u);
-        }
-        cp_async_4(to + 2 * T::SLICE + lane * 4,
-                   (lane < 16 ? a.k_scale : a.v_scale) + (there ? at_scale : 0), there ? 4u : 0u);
-    };
+    const bool copies = lane < 16 && (lane & (a.box - 1)) == 0 && (D != 64 || a.box > 1);
     int issued = 0, in_slot = 0, out_slot = 0;
+    uint32_t out_phase = 0;
+    bool ok = true;
     auto issue = [&]() {   // the slice looked up, and the look-up of the next
-        if (issued < piece.blocks) {
-            load_slice(ring + in_slot * T::STAGE);
+        if (ok && issued < piece.blocks) {
+            const bool there = (unsigned)page < (unsigned)a.num_pages;   // (no page: reads as zeros)
+            const int plane = page * a.Hkv + page_head;
+            const uint32_t bar = bars + in_slot * 8, to = ring + in_slot * T::STAGE;
+            if (D == 64 && a.box == 1) {
+                // single rows of 64 bytes: shorter than a tensor copy's alignment
+                if (lane == 0) mbar_arrive(bar);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int key = (lane + 32 * u) >> 2, gr = lane & 3;
+                    const int z = __shfl_sync(0xffffffffu, there ? plane : -1, key);
+                    const unsigned y = __shfl_sync(0xffffffffu, page_row, key);
+                    const size_t src = z < 0 ? 0 : ((size_t)z * a.page_size + y) * 64 + gr * 16;
+                    cp_async_16(to + place_of<64>(key, gr), a.k + src, z < 0 ? 0u : 16u);
+                    cp_async_16(to + T::SLICE + place_of<64>(key, gr), a.v + src, z < 0 ? 0u : 16u);
+                }
+            } else if (lane == 0) {
+                mbar_arrive_expect_tx(bar, T::STAGE);
+            }
+            __syncwarp();
+            if (copies) {
+                const int z = there ? plane : a.planes, y = there ? (int)page_row : 0;
+                const uint32_t row = to + lane * (D == 64 ? 64 : 128);
+#pragma unroll
+                for (int c = 0; c < (D + 127) / 128; ++c) {
+                    tma_load_3d(row + c * T::CHUNK, &tm.k, c * 128, y, z, bar);
+                    tma_load_3d(row + T::SLICE + c * T::CHUNK, &tm.v, c * 128, y, z, bar);
+                }
+            }
+            const size_t at = there ? (size_t)plane * a.blocks + a.by_block(page_row) : 0;
+            cp_async_4(scales + in_slot * 128 + lane * 4, (lane < 16 ? a.k_scale : a.v_scale) + at,
+                       there ? 4u : 0u);
             if (++issued < piece.blocks) look_up();
         }
         cp_async_commit();
@@ -262,7 +301,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         // ------------------------------------------------ queries
         // B fragments: lane (g, t) has row nr 8 + g, of each 64 dims the 16 from 16 t on
         uint32_t qb[NR][D / 16][2];
-        float unit[NR][2];   // scores of rows 2 t, 2 t + 1 are sums times this (log2 units)
+        float2 unit[NR];     // scores of rows 2 t, 2 t + 1 are sums times this (log2 units)
         int place[NR][2];    // the rows' keys
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
@@ -309,9 +348,10 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                         qb[nr][c * 4 + s][e] =
                             pack_halves(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
                     }
+            unit[nr].x = __shfl_sync(0xffffffffu, back, 8 * t);
+            unit[nr].y = __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                unit[nr][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
                 place[nr][e] = (rbase + nr * 8 + 2 * t + e) % a.Sq + L - a.Sq;
             }
         }
@@ -327,31 +367,31 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
 #pragma unroll
             for (int j = 0; j < T::MT; ++j)
                 oacc[nr][j][0] = oacc[nr][j][1] = oacc[nr][j][2] = oacc[nr][j][3] = 0.f;
-        // of rows 2 t + e: bases of the sum and of O (the same in all lanes of a row),
-        // and this lane's part of the sum
-        float m[NR][2], mv[NR][2], l[NR][2];
+        // of rows 2 t, 2 t + 1: minus the base of the sum, kLift minus that of O (both the
+        // same in all lanes of a row), and this lane's part of the sum
+        float2 nm[NR], qv[NR], l[NR];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[nr][e] = mv[nr][e] = -INFINITY;
-                l[nr][e] = 0.f;
-            }
+        for (int nr = 0; nr < NR; ++nr) {
+            nm[nr] = qv[nr] = make_float2(kFar, kFar);
+            l[nr] = make_float2(0.f, 0.f);
+        }
 
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
             cp_async_wait<T::STAGES - 2>();
+            ok = ok && mbar_wait(bars + out_slot * 8, out_phase, wc, kErrWaitTimeout | kSiteQ8);
             __syncwarp();
-            const uint32_t sk = ring + out_slot * T::STAGE, sv = sk + T::SLICE, sc = sv + T::SLICE;
+            const uint32_t sk = ring + out_slot * T::STAGE, sv = sk + T::SLICE, sc = scales + out_slot * 128;
             const int x0 = (kb + i) * kBlock + T::KB * warp;
+            const int kg = slice_key<D>(g);   // this lane's keys: kg, kg + 8
 
             float sacc[NR][4];
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) sacc[nr][0] = sacc[nr][1] = sacc[nr][2] = sacc[nr][3] = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
-                const uint4 u = lds128(sk + k_place<D>(g, c * 4 + t));
-                const uint4 w = lds128(sk + k_place<D>(g + 8, c * 4 + t));
+                const uint4 u = lds128(sk + place_of<D>(kg, c * 4 + t));
+                const uint4 w = lds128(sk + place_of<D>(kg + 8, c * 4 + t));
                 const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                 for (int s = 0; s < 4; ++s) {
@@ -362,49 +402,74 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                         mma_f16_16816(sacc[nr], a0, a1, a2, a3, qb[nr][c * 4 + s][0], qb[nr][c * 4 + s][1]);
                 }
             }
-            const float ks[2] = {lds32(sc + g * 4), lds32(sc + 32 + g * 4)};
-            const float lv[2] = {lg2_approx(lds32(sc + 64 + g * 4)), lg2_approx(lds32(sc + 96 + g * 4))};
-            // scores, in place: sacc[nr][2 f + e] is that of key g + 8 f in row 2 t + e
+            const float ks[2] = {lds32(sc + kg * 4), lds32(sc + 32 + kg * 4)};
+            float lv[2] = {lg2_approx(lds32(sc + 64 + kg * 4)), lg2_approx(lds32(sc + 96 + kg * 4))};
+            // scores: s[nr][f] those of key kg + 8 f in rows 2 t, 2 t + 1
             const int key0 = axis.key(x0);
             const bool whole = x0 + T::KB <= axis.span && key0 + T::KB <= all_hi &&
                                (key0 >= all_lo || key0 + T::KB <= all_first);
-            bool over = false;
+            float2 s[NR][2];
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float top = m[nr][e] + kGrow, top_v = mv[nr][e] + kGrow;
+                for (int f = 0; f < 2; ++f)
+                    s[nr][f] = fmul2(make_float2(sacc[nr][2 * f], sacc[nr][2 * f + 1]),
+                                     fmul2(unit[nr], make_float2(ks[f], ks[f])));
+            if (!whole) {
+                // (a scale that belongs to no key of some row may be anything)
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        float& s = sacc[nr][2 * f + e];
-                        s *= unit[nr][e] * ks[f];
-                        if (!whole) {
-                            const int key = key0 + g + 8 * f, p = place[nr][e];
-                            const bool seen = x0 + g + 8 * f < axis.span && (!a.causal || key <= p) &&
-                                              (a.window <= 0 || key > p - a.window || key < a.first);
-                            s = seen ? s : -INFINITY;
-                        }
-                        over |= s > top || s + lv[f] > top_v;
-                    }
+                for (int f = 0; f < 2; ++f) {
+                    const int key = key0 + kg + 8 * f;
+                    if (x0 + kg + 8 * f >= axis.span || (key < axis.lo && key >= a.first)) lv[f] = 0.f;
                 }
-            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = key0 + kg + 8 * f, p = place[nr][e];
+                            const bool seen = x0 + kg + 8 * f < axis.span && (!a.causal || key <= p) &&
+                                              (a.window <= 0 || key > p - a.window || key < a.first);
+                            float& x = e == 0 ? s[nr][f].x : s[nr][f].y;
+                            x = seen ? x : -INFINITY;
+                        }
+            }
+            // exponents of the probabilities, and of those times the values' scales
+            auto exponents = [&](int nr, int f, float2& x, float2& y) {
+                x = fadd2(s[nr][f], nm[nr]);
+                y = fadd2(s[nr][f], fadd2(qv[nr], make_float2(lv[f], lv[f])));
+            };
+            float most = -INFINITY, most_v = -INFINITY;
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    float2 x, y;
+                    exponents(nr, f, x, y);
+                    most = fmax3(most, x.x, x.y);
+                    most_v = fmax3(most_v, y.x, y.y);
+                }
+            if (__any_sync(0xffffffffu, most > kGrow || most_v > kGrow + kLift)) {
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float x = fmaxf(sacc[nr][e], sacc[nr][2 + e]);
-                        float y = fmaxf(sacc[nr][e] + lv[0], sacc[nr][2 + e] + lv[1]);
+                        const float s0 = e == 0 ? s[nr][0].x : s[nr][0].y, s1 = e == 0 ? s[nr][1].x : s[nr][1].y;
+                        float x = fmaxf(s0, s1), y = fmaxf(s0 + lv[0], s1 + lv[1]);
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) {
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
                         }
-                        x = fmaxf(x, m[nr][e]);
-                        y = fmaxf(y, mv[nr][e]);
-                        if (x > m[nr][e]) l[nr][e] *= ex2_approx(m[nr][e] - x);   // (0 from -inf)
-                        const float by = y > mv[nr][e] ? ex2_approx(mv[nr][e] - y) : 1.f;
-                        m[nr][e] = x;
-                        mv[nr][e] = y;
+                        float& old = e == 0 ? nm[nr].x : nm[nr].y;
+                        float& old_v = e == 0 ? qv[nr].x : qv[nr].y;
+                        const float now = fminf(old, -x), now_v = fminf(old_v, kLift - y);
+                        float& sum = e == 0 ? l[nr].x : l[nr].y;
+                        sum *= ex2_approx(now - old);
+                        const float by = ex2_approx(now_v - old_v);
+                        old = now;
+                        old_v = now_v;
 #pragma unroll
                         for (int j = 0; j < T::MT; ++j) {
                             oacc[nr][j][e] *= by;
@@ -414,24 +479,34 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             }
             uint32_t pb[NR][2];
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-                float pv[2][2];
+            for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float base = m[nr][e] == -INFINITY ? 0.f : m[nr][e];
-                    const float base_v = mv[nr][e] == -INFINITY ? 0.f : mv[nr][e] - kLift;
-#pragma unroll
-                    for (int f = 0; f < 2; ++f) {
-                        const float s = sacc[nr][2 * f + e];
-                        l[nr][e] += ex2_approx(s - base);
-                        pv[f][e] = ex2_approx(s + lv[f] - base_v);
-                    }
+                for (int f = 0; f < 2; ++f) {
+                    float2 x, y;
+                    exponents(nr, f, x, y);
+                    l[nr] = fadd2(l[nr], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                    pb[nr][f] = movmatrix_trans(pack_halves(ex2_approx(y.x), ex2_approx(y.y)));
                 }
+            // values: lane (g, t) has 16 dims (64: 8) of four keys, of S^T rows 2 t, 2 t + 1,
+            // 2 t + 8, 2 t + 9; those that no row sees become zeros
+            const int v0 = slice_key<D>(2 * t), v1 = slice_key<D>(2 * t + 1);
+            uint32_t have[4] = {~0u, ~0u, ~0u, ~0u};
+            if (!whole) {
+                const int at[4] = {v0, v1, v0 + 8, v1 + 8};
 #pragma unroll
-                for (int f = 0; f < 2; ++f) pb[nr][f] = movmatrix_trans(pack_halves(pv[f][0], pv[f][1]));
+                for (int k = 0; k < 4; ++k) {
+                    const int key = key0 + at[k];
+                    if (x0 + at[k] >= axis.span || (key < axis.lo && key >= a.first)) have[k] = 0;
+                }
             }
-            // O^T += V^T P^T: lane (g, t) has 16 dims (64: 8) of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            // O^T += V^T P^T
             auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
+                if (!whole) {
+                    x0_ &= have[0];
+                    x1_ &= have[1];
+                    y0_ &= have[2];
+                    y1_ &= have[3];
+                }
                 // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
                 const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
                 const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
@@ -445,19 +520,19 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             };
             if constexpr (D == 64) {
                 const uint32_t half = (g & 1) * 8;
-                const uint2 x0_ = lds64(sv + v_place<D>(2 * t, g >> 1) + half);
-                const uint2 x1_ = lds64(sv + v_place<D>(2 * t + 1, g >> 1) + half);
-                const uint2 y0_ = lds64(sv + v_place<D>(2 * t + 8, g >> 1) + half);
-                const uint2 y1_ = lds64(sv + v_place<D>(2 * t + 9, g >> 1) + half);
+                const uint2 x0_ = lds64(sv + place_of<D>(v0, g >> 1) + half);
+                const uint2 x1_ = lds64(sv + place_of<D>(v1, g >> 1) + half);
+                const uint2 y0_ = lds64(sv + place_of<D>(v0 + 8, g >> 1) + half);
+                const uint2 y1_ = lds64(sv + place_of<D>(v1 + 8, g >> 1) + half);
                 add(0, x0_.x, x1_.x, y0_.x, y1_.x);
                 add(2, x0_.y, x1_.y, y0_.y, y1_.y);
             } else {
 #pragma unroll
                 for (int c = 0; c < D / 128; ++c) {
-                    const uint4 x0_ = lds128(sv + v_place<D>(2 * t, c * 8 + g));
-                    const uint4 x1_ = lds128(sv + v_place<D>(2 * t + 1, c * 8 + g));
-                    const uint4 y0_ = lds128(sv + v_place<D>(2 * t + 8, c * 8 + g));
-                    const uint4 y1_ = lds128(sv + v_place<D>(2 * t + 9, c * 8 + g));
+                    const uint4 x0_ = lds128(sv + place_of<D>(v0, c * 8 + g));
+                    const uint4 x1_ = lds128(sv + place_of<D>(v1, c * 8 + g));
+                    const uint4 y0_ = lds128(sv + place_of<D>(v0 + 8, c * 8 + g));
+                    const uint4 y1_ = lds128(sv + place_of<D>(v1 + 8, c * 8 + g));
                     add(c * 8, x0_.x, x1_.x, y0_.x, y1_.x);
                     add(c * 8 + 2, x0_.y, x1_.y, y0_.y, y1_.y);
                     add(c * 8 + 4, x0_.z, x1_.z, y0_.z, y1_.z);
@@ -466,17 +541,22 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             }
             __syncwarp();
             issue();
-            if (++out_slot == T::STAGES) out_slot = 0;
+            if (++out_slot == T::STAGES) {
+                out_slot = 0;
+                out_phase ^= 1u;
+            }
         }
 
         // ------------------------------------------------ merge of the warps
         // eight rows at a time through the slot that was read last, which is free until
         // the block after the next is issued: [8][D] O (columns turned by the row
-        // against bank conflicts), row maxima, row sums
+        // against bank conflicts), and row maxima and sums through its scales
         const int last_slot = (out_slot == 0 ? T::STAGES : out_slot) - 1;
         const float* merge0 = reinterpret_cast<const float*>(smem + last_slot * T::STAGE);
         float* mine = reinterpret_cast<float*>(smem + warp * T::WARP_RING + last_slot * T::STAGE);
-        constexpr int WF = T::WARP_RING / 4;   // floats from warp to warp
+        constexpr int WF = T::WARP_RING / 4, WS = T::WARP_SCALES / 4;   // floats from warp to warp
+        const float* ml0 = reinterpret_cast<const float*>(smem + T::SCALES + last_slot * 128);
+        float* ml = reinterpret_cast<float*>(smem + T::SCALES + warp * T::WARP_SCALES + last_slot * 128);
         const int valid_rows = min(T::R, a.rows - rbase);
         const bool whole_unit = n == nb;
         // joined: split s finishes the rows [s own, (s + 1) own) (see decode.cu)
@@ -491,26 +571,20 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             if (nr * 8 >= valid_rows) break;
-            // (not joined: every warp has read its slot, for copies into this one are not
-            // issued before all have passed the barriers below)
-            if (joined && nr == 0) {
-                cp_async_wait<0>();
-                __syncthreads();
-                cluster_wait();
-            }
+            if (joined && nr == 0) cluster_wait();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float sum = l[nr][e];
+                float sum = e == 0 ? l[nr].x : l[nr].y;
+                const float to_m = e == 0 ? nm[nr].x : nm[nr].y, to_v = e == 0 ? qv[nr].x : qv[nr].y;
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 const int r = 2 * t + e;
                 if (g == 0) {
-                    mine[8 * D + r] = m[nr][e];
-                    mine[8 * D + 8 + r] = sum;
+                    ml[r] = -to_m;
+                    ml[8 + r] = sum;
                 }
-                // O of the base of the sum (0 where the warp saw no key of the row, or
-                // values of scale 0)
-                const float by = mv[nr][e] == -INFINITY ? 0.f : ex2_approx(mv[nr][e] - kLift - m[nr][e]);
+                // O in the base of the sum (a row without keys: 0 times 1 or 0)
+                const float by = ex2_approx(to_m - to_v);
 #pragma unroll
                 for (int j = 0; j < T::MT; ++j) {
                     const int dim = D == 64 ? g * 8 + 2 * j : (j >> 3) * 128 + g * 16 + 2 * (j & 7);
@@ -525,30 +599,27 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                 if (r >= valid_rows) break;
                 float M = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < T::WARPS; ++w) M = fmaxf(M, merge0[w * WF + 8 * D + r8]);
+                for (int w = 0; w < T::WARPS; ++w) M = fmaxf(M, ml0[w * WS + r8]);
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                float sum = 0.f, lse2 = -INFINITY;
                 const size_t row = row_id(r);
                 const bool sink = whole_unit && !joined && a.sinks != nullptr;
                 const float sg = sink ? a.sinks[hkv * a.group + (rbase + r) / a.Sq] * kLog2ef : -INFINITY;
-                const float base = fmaxf(M, sg);
-                if (base != -INFINITY) {
-                    sum = ex2_approx(sg - base);
+                M = fmaxf(M, sg);   // (finite: at least -kFar)
+                float sum = ex2_approx(sg - M);
 #pragma unroll
-                    for (int w = 0; w < T::WARPS; ++w) {
-                        const float f = ex2_approx(merge0[w * WF + 8 * D + r8] - base);   // 0 for warps without keys
-                        const float4 x = *reinterpret_cast<const float4*>(merge0 + w * WF + r8 * D +
-                                                                          ((c + 4 * r8) & (D - 1)));
-                        sum = fmaf(f, merge0[w * WF + 8 * D + 8 + r8], sum);
-                        o.x = fmaf(f, x.x, o.x);
-                        o.y = fmaf(f, x.y, o.y);
-                        o.z = fmaf(f, x.z, o.z);
-                        o.w = fmaf(f, x.w, o.w);
-                    }
-                    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-                    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-                    lse2 = sum > 0.f ? base + lg2_approx(sum) : -INFINITY;
+                for (int w = 0; w < T::WARPS; ++w) {
+                    const float f = ex2_approx(ml0[w * WS + r8] - M);
+                    const float4 x = *reinterpret_cast<const float4*>(merge0 + w * WF + r8 * D +
+                                                                      ((c + 4 * r8) & (D - 1)));
+                    sum = fmaf(f, ml0[w * WS + 8 + r8], sum);
+                    o.x = fmaf(f, x.x, o.x);
+                    o.y = fmaf(f, x.y, o.y);
+                    o.z = fmaf(f, x.z, o.z);
+                    o.w = fmaf(f, x.w, o.w);
                 }
+                const float inv = sum > 0.f ? 1.f / sum : 0.f;
+                o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                const float lse2 = sum > 0.f ? M + lg2_approx(sum) : -INFINITY;
                 if (joined) {
                     const int to = r / own, at = split * own + r - to * own;
                     cluster_write4(jo + (at * D + c) * 4, to, o);
@@ -562,6 +633,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                     if (c == 0) a.part_lse[(size_t)part * T::R + r] = lse2;
                 }
             }
+            fence_proxy_async_smem();   // (copies will write here)
             __syncthreads();
         }
         if (joined) {
@@ -602,7 +674,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
                 if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
             }
-            return;
+            break;
         }
         if (!whole_unit && threadIdx.x == 0) a.head[part] = make_int4(b, at_unit, n, kb == 0 ? nb : 0);
         left -= n;
@@ -614,6 +686,11 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         }
     } while (left > 0);
     cp_async_wait<0>();
+    if (!ok) {   // given up: what was asked for must have landed before the CTA exits
+#pragma unroll 1
+        for (int q = max(0, issued - T::STAGES); q < issued; ++q)
+            mbar_wait_drain(bars + q % T::STAGES * 8, (uint32_t)(q / T::STAGES) & 1u, a.wait_limit_ns);
+    }
 }
 
 // Merges the pieces of the unit that starts in CTA blockIdx.x of the kernel before
@@ -680,29 +757,32 @@ __global__ void __launch_bounds__(256) combine_q8_kernel(const DecodeQ8Args a, i
 }
 
 template <int D, int NR>
-cudaError_t launch_tile(const DecodeQ8Args& a, cudaStream_t s) {
+cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
     using T = Q8Traits<D, NR>;
-    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, NR>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, T::RING + T::JOIN);
+    const DecodeQ8Args& a = p.args;
+    constexpr int kAlign = 1024;
+    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kAlign + T::RING + T::JOIN);
     if (e != cudaSuccess) return e;
     if (a.joined)
         return launch_dependent_clusters(
             decode_q8_kernel<D, NR>, (unsigned)a.n_splits,
             dim3((unsigned)a.n_splits, (unsigned)(a.Hkv * a.tiles), (unsigned)a.B), dim3(T::THREADS),
-            T::RING + T::JOIN, s, a);
-    e = launch_dependent(decode_q8_kernel<D, NR>, dim3((unsigned)a.n_splits), dim3(T::THREADS), T::RING, s, a);
+            kAlign + T::RING + T::JOIN, s, p.maps, a);
+    e = launch_dependent(decode_q8_kernel<D, NR>, dim3((unsigned)a.n_splits), dim3(T::THREADS),
+                         kAlign + T::RING, s, p.maps, a);
     if (e != cudaSuccess) return e;
     return launch_dependent(combine_q8_kernel<D>, dim3((unsigned)a.n_splits, (unsigned)T::R), dim3(256), 0, s,
                             a, (int)T::R);
 }
 
 template <int D>
-cudaError_t launch_dim(const DecodeQ8Args& a, cudaStream_t s) {
-    switch (decode_q8_tile(D, a.rows)) {
-        case 8: return launch_tile<D, 1>(a, s);
-        case 16: return launch_tile<D, 2>(a, s);
+cudaError_t launch_dim(const DecodeQ8Launch& p, cudaStream_t s) {
+    switch (decode_q8_tile(D, p.args.rows)) {
+        case 8: return launch_tile<D, 1>(p, s);
+        case 16: return launch_tile<D, 2>(p, s);
         default:
-            if constexpr (D <= 128) return launch_tile<D, 4>(a, s);
+            if constexpr (D <= 128) return launch_tile<D, 4>(p, s);
             else return cudaErrorInvalidValue;
     }
 }
@@ -715,11 +795,11 @@ int decode_q8_ctas(int head_dim, int tile) {
     return Q8Traits<256, 1>::MIN_CTAS;
 }
 
-cudaError_t launch_decode_q8(const DecodeQ8Args& a, int head_dim, cudaStream_t s) {
+cudaError_t launch_decode_q8(const DecodeQ8Launch& p, int head_dim, cudaStream_t s) {
     switch (head_dim) {
-        case 64: return launch_dim<64>(a, s);
-        case 128: return launch_dim<128>(a, s);
-        case 256: return launch_dim<256>(a, s);
+        case 64: return launch_dim<64>(p, s);
+        case 128: return launch_dim<128>(p, s);
+        case 256: return launch_dim<256>(p, s);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -89,7 +89,8 @@ SHAPES = [  # lens, hq, hkv, n, d, page, block
     ([1000, 3], 4, 4, 1, 64, 48, 16), ([513, 511, 512], 16, 2, 1, 256, 128, 32), ([77, 2000], 16, 1, 1, 128, 100, 25),
     ([250, 31], 24, 1, 1, 64, 32, 32), ([1500], 32, 1, 1, 256, 256, 256), ([900, 128], 40, 2, 2, 128, 64, 16),
     ([129, 640], 8, 1, 16, 64, 16, 16), ([70, 3], 7, 7, 5, 128, 1, 1), ([333], 5, 1, 3, 256, 7, 7),
-    ([2100, 90], 33, 1, 1, 128, 64, 64)]
+    ([2100, 90], 33, 1, 1, 128, 64, 64), ([77, 300], 4, 2, 1, 64, 7, 7), ([130, 5], 2, 1, 2, 64, 1, 1),
+    ([400], 8, 1, 1, 64, 6, 3), ([90, 33], 4, 1, 1, 128, 10, 5), ([1300, 0, 7], 20, 1, 1, 64, 20, 10)]
 
 
 @pytest.mark.parametrize("causal", [False, True])
@@ -108,7 +109,8 @@ WINDOWS = [  # lens, hq, hkv, n, d, page, block, window, first, width
     ([300, 40, 0], 4, 1, 1, 128, 16, 16, 64, 0, None), ([300, 40, 5], 4, 2, 3, 64, 48, 12, 50, 4, None),
     ([3000, 900], 8, 1, 1, 128, 64, 64, 256, 130, 200), ([3000, 64], 16, 2, 4, 256, 128, 64, 1, 1, None),
     ([700], 2, 2, 16, 64, 32, 32, 33, 300, 300), ([2500, 2499], 8, 8, 1, 128, 100, 50, 2 ** 31 - 1, 3, None),
-    ([1200], 6, 1, 2, 128, 16, 16, 500, 2 ** 31 - 1, None)]
+    ([1200], 6, 1, 2, 128, 16, 16, 500, 2 ** 31 - 1, None), ([990, 300], 4, 2, 2, 64, 15, 5, 100, 3, 400),
+    ([400, 5000], 12, 2, 1, 64, 16, 4, 200, 70, None)]
 
 
 @pytest.mark.parametrize("causal", [False, True])
