@@ -635,7 +635,9 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.q = static_cast<const uint16_t*>(q);
     a.k = static_cast<const uint8_t*>(k);
     a.v = static_cast<const uint8_t*>(v);
-    a.box = std::min(page_size & -page_size, 16);
+    const int slice = decode_q8_block(head_dim) / 4;
+    a.box = std::min(page_size & -page_size, slice);
+    a.flat = block % slice == 0 ? 1 : 0;
     a.planes = num_pages * hkv;
     if (!encode_map8(&p.maps.k, k, head_dim, page_size, a.planes, (unsigned)a.box) ||
         !encode_map8(&p.maps.v, v, head_dim, page_size, a.planes, (unsigned)a.box))
@@ -675,23 +677,27 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     const SplitPlan plan = split_plan(true, head_dim, pairs, span, di->num_sms);
     a.joined = plan.joined ? 1 : 0;
     if (a.joined) {
-        a.chunk = (int)(((span + plan.splits - 1) / plan.splits + 63) / 64 * 64);
+        const long long keys = decode_q8_block(head_dim);
+        a.chunk = (int)(((span + plan.splits - 1) / plan.splits + keys - 1) / keys * keys);
         a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
         return from_cuda(launch_decode_q8(p, head_dim, s));
     }
     // (the kernel counts the blocks of all units in 32 bits)
-    const double blocks = (double)pairs * (double)((span + 63) / 64);
-    if (blocks >= 2147483648.0) return FA_ERR_INVALID_ARG;
-    a.n_splits = (int)std::min<double>((double)di->num_sms * decode_q8_ctas(head_dim, tile), blocks);
+    const int keys = decode_q8_block(head_dim);
+    const double blocks = (double)pairs * (double)((span + keys - 1) / keys);
+    if (blocks >= 2147483647.0 - 65536) return FA_ERR_INVALID_ARG;
+    a.slots = (int)std::min<double>((double)di->num_sms * decode_q8_ctas(head_dim, tile), blocks);
+    // pieces for every SM to take when it is done with its own, where there may be much
+    a.levels = blocks >= 48.0 * a.slots ? 2 : 0;
+    a.n_splits = a.slots * (1 + a.levels);
     const size_t parts = 2ull * a.n_splits * tile;
-    const size_t bytes_o = parts * head_dim * sizeof(float), bytes_l = parts * sizeof(float);
+    const size_t bytes_o = parts * head_dim * sizeof(float), bytes_l = (parts * sizeof(float) + 15) / 16 * 16;
     char* ws = nullptr;
-    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes_o + bytes_l + (2ull * a.n_splits + 1) * sizeof(int4),
-                        s) != cudaSuccess)
+    if (cudaMallocAsync(reinterpret_cast<void**>(&ws), bytes_o + bytes_l + a.n_splits * sizeof(int4), s) != cudaSuccess)
         return FA_ERR_CUDA;
     a.part_o = reinterpret_cast<float*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + bytes_o);
-    a.head = reinterpret_cast<int4*>(ws + bytes_o + bytes_l);
+    if (4 * pairs > a.slots) a.head = reinterpret_cast<int4*>(ws + bytes_o + bytes_l);
     const cudaError_t e = launch_decode_q8(p, head_dim, s);
     if (cudaFreeAsync(ws, s) != cudaSuccess) return FA_ERR_CUDA;
     return from_cuda(e);

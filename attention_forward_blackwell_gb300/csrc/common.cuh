@@ -327,26 +327,29 @@ struct DecodeQ8Args {
     uint16_t* o;                // [B, Hq, Sq, d]
     float* lse;                 // [B, Hq, Sq]
     const int* seqlens_k;       // [B]
-    // pieces of units, two of a CTA at most: O [2 CTAs][tile][d] and LSE (log2
-    // units) [2 CTAs][tile]; head [2 CTAs] batch entry, unit, its blocks in the piece,
-    // and the unit's blocks if the piece is its first (else 0); then one more: the
-    // blocks of a CTA
+    // pieces of units, two of a CTA at most: O [2 CTAs][tile][d] and LSE (log2 units)
+    // [2 CTAs][tile]
     float* part_o;
     float* part_lse;
+    // [CTAs] batch entry, unit, pieces, slot of the first (0 or 1) of the unit that starts
+    // in a CTA and goes on in the next (no pieces: none does); nullptr: units are looked
+    // for one by one (few, in many pieces)
     int4* head;
     int B, Hq, Hkv, Sq, Sk;     // Sk = max_pages * page_size
     int group, rows;            // Hq / Hkv, group * Sq
     int tiles;                  // of query rows of a key/value head
     int joined;                 // the splits of a unit are a cluster, `chunk` keys each
     int n_splits, chunk;        // (not joined: CTAs)
+    int slots, levels;          // CTAs that run at once; further ones for each, with small pieces
     int causal, window, first;
     const float* sinks;
     const int* block_table;
     int max_pages, page_size, num_pages;
     int blocks;                 // scales of a page and head
     FastDiv by_page, by_block;  // keys / page_size, keys / keys of a scale
-    int box;                    // rows of a copy: the largest power of two up to 16 that
-                                // divides page_size
+    int box;                    // rows of a copy: the largest power of two up to a slice's
+                                // keys that divides page_size
+    int flat;                   // a slice's keys have one scale
     int planes;                 // num_pages * Hkv: the first plane that does not exist
     float scale_log2;
     unsigned int* err_word;
@@ -363,6 +366,7 @@ struct DecodeQ8Launch {
 inline int decode_q8_tile(int head_dim, int rows) {
     return rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
 }
+int decode_q8_block(int head_dim);   // keys of a block, four slices
 int decode_q8_ctas(int head_dim, int tile);   // CTAs that an SM holds at once
 cudaError_t launch_decode_q8(const DecodeQ8Launch& p, int head_dim, cudaStream_t s);
 

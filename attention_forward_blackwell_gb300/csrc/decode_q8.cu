@@ -9,11 +9,14 @@
 //     O^T [16 dims x 8 rows] += V^T P^T, so that 8 query rows (a group of 8 heads)
 //     fill the instruction, where rows on M would leave half of it empty.
 //   - A sum may be taken in any order, so the operands are laid out for the loads:
-//     a lane's 16 codes of a key (16 bytes) are its share of 4 steps of the score
+//     a lane's 16 codes of a key (16 bytes) are its share of four steps of the score
 //     product, the rows of Q permuted alike; a lane's 16 dims of four keys are its
-//     share of 8 tiles of O^T, two byte permutes for two pairs of keys.  A
-//     conversion (two codes to fp16, exact) per register of an operand is all the
-//     rest.  e4m3 values and fp16 P and Q multiply exactly into fp32 sums.
+//     share of 8 tiles of O^T, two byte permutes for two pairs of keys.
+//     A conversion (two codes to fp16, exact) per register of an operand is all the
+//     rest; products of e4m3 values with fp16 P and Q are exact, their sums fp32.
+//     (Scores by e4m3 products, each query as two codes, need no conversion of keys,
+//     but products of both kinds in one loop cost more than that: 202 us where fp16
+//     alone took 194.)
 //   - Q in fp16: each row times a power of two that brings its largest element
 //     into [1, 2), so 8 bits of fraction stay of every element down to 2^-14 of
 //     it; below, the error is 2^-25 of the largest, that of an fp32 sum.
@@ -28,19 +31,22 @@
 //     Scores and exponents are computed two rows an instruction.
 //
 // Work.  The sequences' lengths are known to the device only, and differ.  A unit
-// (batch entry, key/value head, tile of query rows) counts its blocks of 64 keys;
-// the units' blocks, one after the other, form a line that is cut into equal
-// pieces, one per CTA, as many CTAs as fit the SMs at once (as in span.cu).  A
-// unit that lies in one piece is finished there; of the others each CTA writes
-// what it has, normalised, with its LSE, and combine_q8_kernel merges them in
+// (batch entry, key/value head, tile of query rows) counts its blocks of keys; the
+// units' blocks, one after the other, form a line that is cut into equal pieces, one
+// per CTA, as many CTAs as fit the SMs at once (as in span.cu; cut_line has the
+// choices).  A unit that lies in one piece is finished there; of the others each CTA
+// writes what it has, normalised, with its LSE, and a second kernel merges them in
 // their order.  (The split kernel's grid, one CTA of 256 keys and more for every
 // piece of the longest possible sequence, took 195 us for 64 x 1K to 16K keys x 8
-// heads and 213 for one of 130,000 keys x 2 heads at head_dim 256.)
+// heads at head_dim 128, now 177, 6.5 TB/s, and 213 for one of 130,000 keys x 2 heads
+// at 256, now 35.  Merged by the CTA that writes a unit's last piece, without a second
+// kernel: 189, for the fences and counts stop its ring.)  Neither kernel lets the
+// next start early: its CTAs would take the places of this one's later pieces (195).
 // Short caches are split over the CTAs of a cluster instead, which merge without a
-// second kernel, as decode.cu's joined splits.
+// second kernel, as decode.cu's joined splits (2,000 keys x 8 heads 6.9 us).
 //
-// A warp takes 16 keys of every block through a ring of its own.  Tensor copies
-// fill it, one lane for every box of rows that lie together (a page's, up to 16),
+// A warp takes a slice of every block through a ring of its own.  Tensor copies
+// fill it, one lane for every box of rows that lie together (a page's, up to 32),
 // so that a slice costs the warp a few instructions where 16-byte copies by all
 // lanes took a third of all it issues; copies run ahead over the ends of units,
 // and the page numbers of a slice are fetched while the one before is issued.
@@ -61,31 +67,38 @@ constexpr float kFar = 3.0e38f;  // minus a base of a row that has seen nothing
 
 constexpr unsigned kSiteQ8 = 72; // wait site of the ring
 
-constexpr int kBlock = 64;      // keys of a block
-constexpr int kLeastBlocks = 4; // of a piece
+constexpr int kLeastKeys = 256;  // of a piece
+constexpr int kSegmentBlocks = 2; // what a segment's set-up and merge are worth
+constexpr int kManyBlocks = 48;  // a CTA's share from which part of it goes in small pieces
 
 template <int D, int NR>
 struct Q8Traits {
     static constexpr int WARPS = 4;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int R = 8 * NR;                    // rows of a tile
-    static constexpr int KB = kBlock / WARPS;           // keys of a slice
+    static constexpr int SUB = D == 256 ? 1 : 2;        // 16-key parts of a slice
+    static constexpr int KB = 16 * SUB;                 // keys of a slice
+    static constexpr int BLOCK = WARPS * KB;            // keys of a block
+    static constexpr int SW = NR == 1 ? SUB : 1;        // parts worked on together
+    static constexpr int PITCH = D == 64 ? 64 : 128;    // bytes of a box's row
+    static constexpr int CHUNK = KB * PITCH;            // a box of a slice's rows
     static constexpr int SLICE = KB * D;                // bytes of a slice of keys, or of values
-    static constexpr int CHUNK = D == 64 ? 1024 : 2048; // 16 rows of a box
     static constexpr int STAGE = 2 * SLICE;
-    static constexpr int STAGES = D == 64 ? 6 : D == 128 ? 4 : 3;
+    static constexpr int STAGES = D == 64 ? 3 : 2;
     static constexpr int WARP_RING = STAGES * STAGE;
-    static constexpr int SCALES = WARPS * WARP_RING;    // behind the ring: scales of both, [32] a slot,
-    static constexpr int WARP_SCALES = STAGES * 128;
+    static constexpr int SCALE_BYTES = 2 * KB * 4;      // of a slot's keys and values
+    static constexpr int SCALES = WARPS * WARP_RING;    // behind the ring
+    static constexpr int WARP_SCALES = STAGES * SCALE_BYTES;
     static constexpr int BARS = SCALES + WARPS * WARP_SCALES;   // a barrier a slot, the abort flag
-    static constexpr int RING = BARS + (WARPS * STAGES + 1) * 8 + (8 & -(WARPS * STAGES + 1 & 1));
+    static constexpr int LINE = BARS + (WARPS * STAGES + 1) * 8;
+    static constexpr int RING = (LINE + 32 + 15) / 16 * 16;
     static constexpr int JOIN_ROWS = R + kJoinSplits;   // n splits, ceil(R / n) rows each
-    static constexpr int JOIN_LSE = JOIN_ROWS * 4 + (-JOIN_ROWS * 4 & 15);
+    static constexpr int JOIN_LSE = (JOIN_ROWS * 4 + 15) / 16 * 16;
     static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
     static constexpr int MT = D / 16;                   // tiles of O^T
     static constexpr int MIN_CTAS = NR == 4 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
     // the merge of 8 rows goes through the slot that was read last
-    static_assert(8 * D * 4 <= STAGE && RING % 16 == 0, "merge buffer");
+    static_assert(8 * D * 4 <= STAGE && 16 * 4 <= SCALE_BYTES, "merge buffer");
 };
 
 // Place of granule g (16 bytes) of key row `key` in a slice: the copies' swizzle.
@@ -95,7 +108,7 @@ struct Q8Traits {
 template <int D>
 __device__ __forceinline__ uint32_t place_of(int key, int g) {
     if (D == 64) return (uint32_t)(key * 64 + ((g ^ ((key >> 1) & 3)) << 4));
-    return (uint32_t)((g >> 3) * 2048 + key * 128 + (((g & 7) ^ (key & 7)) << 4));
+    return (uint32_t)((g >> 3) * Q8Traits<D, 1>::CHUNK + key * 128 + (((g & 7) ^ (key & 7)) << 4));
 }
 template <int D>
 __device__ __forceinline__ int slice_key(int g) {
@@ -128,49 +141,123 @@ __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ int unit_blocks(int span) { return max(1, (span + kBlock - 1) / kBlock); }
+template <int BLOCK>
+__device__ __forceinline__ int unit_blocks(int span) {
+    return max(1, (span + BLOCK - 1) / BLOCK);
+}
 __device__ __forceinline__ int keys_of(const DecodeQ8Args& a, int b) {
     return max(0, min(a.seqlens_k[b], a.Sk));
 }
 
-// Where on the line piece `x` lies: its first block's batch entry, unit of it and
-// block of that; the blocks of the piece, 0 past the end.  A warp together: each
-// lane sums its share of the batch.
-struct Piece {
-    int b, u, kb, blocks, quota;
+// How the units' blocks, one unit after the other on a line of `all`, are cut: into
+// `slots` pieces of `big` blocks, then `small` ones up to the line's end; or, with
+// `aligned` blocks to a piece, unit by unit (the line then counts pieces).
+struct Line {
+    int all, slots, big, small, aligned;
+    __device__ __forceinline__ int of_unit(int nb) const {   // what a unit of nb blocks takes of the line
+        return aligned > 0 ? (nb + aligned - 1) / aligned : nb;
+    }
+    __device__ __forceinline__ int from(int x) const {   // where piece x starts
+        if (aligned > 0) return min(x, all);
+        const long long at = x < slots ? (long long)x * big
+                                       : (long long)slots * big + (long long)(x - slots) * small;
+        return (int)min(at, (long long)all);
+    }
+    __device__ __forceinline__ int piece_of(int pos) const {
+        if (aligned > 0) return pos;
+        // (slots * big < all + slots + big: within 32 bits as unsigned)
+        const unsigned bigs = (unsigned)slots * (unsigned)big;
+        return (unsigned)pos < bigs ? pos / big : slots + (int)(((unsigned)pos - bigs) / (unsigned)small);
+    }
 };
-__device__ __forceinline__ Piece place_piece(const DecodeQ8Args& a, int x, int pieces) {
+
+// Sum of f(blocks of a unit of entry b) over the entries [b0, b1).
+template <int BLOCK, class F>
+__device__ __forceinline__ int sum_blocks(const DecodeQ8Args& a, int b0, int b1, F&& f) {
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) sum += f(unit_blocks<BLOCK>(key_axis(a, keys_of(a, b)).span));
+    return sum;
+}
+
+// The line's cut, by a warp together, each lane with its share of the batch.  Pieces
+// that end with their units save the set-up and merge of a second segment, worth
+// about two blocks: taken where such pieces, one for every CTA at most, are no more
+// than that much longer.  A long line leaves a quarter of itself to small pieces, for
+// the SMs that are done with their own first (equal shares alone ended 12% apart: 64 x
+// 1K to 16K keys x 8 heads 188 us, so 181).
+template <int BLOCK>
+__device__ __forceinline__ Line cut_line(const DecodeQ8Args& a, int& mine) {
     const int lane = threadIdx.x & 31, units = a.Hkv * a.tiles;
-    const int per = (a.B + 31) >> 5, b0 = lane * per, b1 = min(b0 + per, a.B);
-    int mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units * unit_blocks(key_axis(a, keys_of(a, b)).span);
+    const int per = (a.B + 31) >> 5, b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
+    Line line;
+    line.slots = a.slots;
+    line.aligned = 0;
+    mine = units * sum_blocks<BLOCK>(a, b0, b1, [](int nb) { return nb; });
+    line.all = __reduce_add_sync(0xffffffffu, mine);
+    const int share = (int)(((unsigned)line.all + (unsigned)a.slots - 1) / (unsigned)a.slots);
+    const int least = max(1, kLeastKeys / BLOCK), cut = max(share, least);
+    line.small = a.levels > 0 && share >= kManyBlocks ? share / (4 * a.levels) : 0;
+    line.big = max(share - a.levels * line.small, least);
+    if (line.small == 0 && a.B * units <= a.slots) {
+        for (int s = cut; s <= cut + kSegmentBlocks && line.aligned == 0; ++s) {
+            const int count = units * sum_blocks<BLOCK>(a, b0, b1, [&](int nb) { return (nb + s - 1) / s; });
+            const int all = __reduce_add_sync(0xffffffffu, count);
+            if (all <= a.slots) {
+                line.aligned = s;
+                line.all = all;
+                mine = count;
+            }
+        }
+    }
+    line.small = max(line.small, 1);
+    return line;
+}
+
+// Where position pos < line.all lies: batch entry, its units' start on the line, unit,
+// place in it, and the unit's blocks.  (A warp together; mine: of cut_line.)
+struct Spot {
+    int b, start, u, at, nb;
+};
+template <int BLOCK>
+__device__ __forceinline__ Spot find_on_line(const DecodeQ8Args& a, const Line& line, int mine, int pos) {
+    const int lane = threadIdx.x & 31, units = a.Hkv * a.tiles;
     int end = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, end, o);
         if (lane >= o) end += y;
     }
-    const int all = __shfl_sync(0xffffffffu, end, 31);
-    Piece p;
-    p.quota = max((int)(((unsigned)all + (unsigned)pieces - 1) / (unsigned)pieces), kLeastBlocks);
-    const long long from = (long long)p.quota * x;
-    p.blocks = from < all ? min(p.quota, all - (int)from) : 0;
-    const int beg = (int)min(from, (long long)all - 1);
-    const unsigned who = __ballot_sync(0xffffffffu, end - mine <= beg && beg < end);
-    int at = end - mine, b = b0, nb = 1;
-    if (end - mine <= beg && beg < end) {
+    const bool here = end - mine <= pos && pos < end;
+    const int from_lane = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    int at = end - mine, b = lane * ((a.B + 31) >> 5), nb = 1;
+    if (here) {
         for (;; ++b) {
-            nb = unit_blocks(key_axis(a, keys_of(a, b)).span);
-            if (beg < at + units * nb) break;
-            at += units * nb;
+            nb = unit_blocks<BLOCK>(key_axis(a, keys_of(a, b)).span);
+            if (pos < at + units * line.of_unit(nb)) break;
+            at += units * line.of_unit(nb);
         }
     }
-    const int from_lane = __ffs(who) - 1;
+    Spot p;
     p.b = __shfl_sync(0xffffffffu, b, from_lane);
-    nb = __shfl_sync(0xffffffffu, nb, from_lane);
-    const int off = beg - __shfl_sync(0xffffffffu, at, from_lane);
-    p.u = off / nb;
-    p.kb = off - p.u * nb;
+    p.nb = __shfl_sync(0xffffffffu, nb, from_lane);
+    p.start = __shfl_sync(0xffffffffu, at, from_lane);
+    const int len = line.of_unit(p.nb);
+    p.u = (pos - p.start) / len;
+    p.at = pos - p.start - p.u * len;
+    return p;
+}
+
+// The pieces of a unit that takes [from, from + len) of the line: the first one,
+// their number, and whether the first is its CTA's second slot.
+struct Pieces {
+    int first, count, second;
+    __device__ __forceinline__ int slot(int k) const { return k == 0 ? 2 * first + second : 2 * (first + k); }
+};
+__device__ __forceinline__ Pieces pieces_of(const Line& line, int from, int len) {
+    Pieces p;
+    p.first = line.piece_of(from);
+    p.count = line.piece_of(from + len - 1) - p.first + 1;
+    p.second = from > line.from(p.first) ? 1 : 0;
     return p;
 }
 
@@ -180,7 +267,6 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     using T = Q8Traits<D, NR>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023u);
-    dependents_may_start();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t base = smem_u32(smem), bars = base + T::BARS + warp * T::STAGES * 8;
     const WaitCtx wc{base + T::BARS + T::WARPS * T::STAGES * 8, (uint32_t)a.wait_limit_ns, a.err_word};
@@ -195,36 +281,45 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     wait_for_previous();   // (what is above overlaps the kernel before)
     const bool joined = a.joined != 0;
     const int units = a.Hkv * a.tiles;
-    Piece piece;
+    Spot spot;
+    int blocks;   // of this CTA
+    auto* const kept = reinterpret_cast<Line*>(smem + T::LINE);   // (for the end of segments)
     if (joined) {   // grid (splits of a unit, units, batch entries), the splits a cluster
         cluster_arrive();   // (waited for before the first write to another)
-        const int nb = unit_blocks(key_axis(a, keys_of(a, blockIdx.z)).span), n = a.chunk / kBlock;
-        piece.b = blockIdx.z;
-        piece.u = blockIdx.y;
-        piece.kb = (int)blockIdx.x * n;
-        piece.blocks = max(0, min(n, nb - piece.kb));
-        piece.quota = n;
+        const int nb = unit_blocks<T::BLOCK>(key_axis(a, keys_of(a, blockIdx.z)).span), n = a.chunk / T::BLOCK;
+        spot.b = blockIdx.z;
+        spot.u = blockIdx.y;
+        spot.at = (int)blockIdx.x * n;
+        blocks = max(0, min(n, nb - spot.at));
     } else {
-        piece = place_piece(a, blockIdx.x, gridDim.x);
-        if (threadIdx.x == 0) {
-            a.head[2 * blockIdx.x] = a.head[2 * blockIdx.x + 1] = make_int4(0, 0, 0, 0);
-            if (blockIdx.x == 0) a.head[2 * gridDim.x] = make_int4(piece.quota, 0, 0, 0);
+        int mine;
+        if (a.head != nullptr && threadIdx.x == 0) a.head[blockIdx.x] = make_int4(0, 0, 0, 0);
+        const Line line = cut_line<T::BLOCK>(a, mine);
+        const int begin = line.from(blockIdx.x);
+        if (begin >= line.all) return;
+        spot = find_on_line<T::BLOCK>(a, line, mine, begin);
+        if (line.aligned > 0) {
+            spot.at *= line.aligned;
+            blocks = min(line.aligned, spot.nb - spot.at);
+        } else {
+            blocks = line.from(blockIdx.x + 1) - begin;
         }
-        if (piece.blocks == 0) return;
+        if (threadIdx.x == 0) *kept = line;
     }
 
     // ------------------------------------------------ ring
     const uint32_t ring = base + warp * T::WARP_RING, scales = base + T::SCALES + warp * T::WARP_SCALES;
     // The producer's place on the line: unit lu of batch entry lb, block lk; and
-    // this lane's key (lane & 15) of the slice looked up last: its page, -1 where no
-    // row sees it, and its row there.  Nothing waits for the page before the slice is
-    // issued.
-    int lb = piece.b, lu = piece.u, lk = piece.kb, l_head = lu / a.tiles;
+    // this lane's key (lane, of 16: lane & 15) of the slice looked up last: its page,
+    // -1 where no row sees it, and its row there.  Nothing waits for the page before
+    // the slice is issued.
+    int lb = spot.b, lu = spot.u, lk = spot.at, l_head = lu / a.tiles;
     Axis la = key_axis(a, keys_of(a, lb));
+    const int lane_key = lane & (T::KB - 1);
     int page = -1, page_head = 0;
     unsigned page_row = 0;
     auto look_up = [&]() {
-        if (lk * kBlock >= la.span && lk > 0) {   // the next unit
+        if (lk * T::BLOCK >= la.span && lk > 0) {   // the next unit
             lk = 0;
             if (++lu == units) {
                 lu = 0;
@@ -232,7 +327,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             }
             l_head = lu / a.tiles;
         }
-        const int x = lk * kBlock + T::KB * warp + (lane & 15);
+        const int x = lk * T::BLOCK + T::KB * warp + lane_key;
         const int key = la.key(x);
         page = -1;
         page_head = l_head;
@@ -244,21 +339,22 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         page_row = (unsigned)key - p * (unsigned)a.page_size;
         page = a.block_table[(size_t)lb * a.max_pages + p];
     };
-    const bool copies = lane < 16 && (lane & (a.box - 1)) == 0 && (D != 64 || a.box > 1);
+    const int box = min(a.box, T::KB);
+    const bool copies = lane < T::KB && (lane & (box - 1)) == 0 && (D != 64 || box > 1);
     int issued = 0, in_slot = 0, out_slot = 0;
     uint32_t out_phase = 0;
     bool ok = true;
     auto issue = [&]() {   // the slice looked up, and the look-up of the next
-        if (ok && issued < piece.blocks) {
+        if (ok && issued < blocks) {
             const bool there = (unsigned)page < (unsigned)a.num_pages;   // (no page: reads as zeros)
             const int plane = page * a.Hkv + page_head;
             const uint32_t bar = bars + in_slot * 8, to = ring + in_slot * T::STAGE;
-            if (D == 64 && a.box == 1) {
+            if (D == 64 && box == 1) {
                 // single rows of 64 bytes: shorter than a tensor copy's alignment
                 if (lane == 0) mbar_arrive(bar);
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int key = (lane + 32 * u) >> 2, gr = lane & 3;
+                for (int u = 0; u < T::KB / 8; ++u) {
+                    const int key = (lane >> 2) + 8 * u, gr = lane & 3;
                     const int z = __shfl_sync(0xffffffffu, there ? plane : -1, key);
                     const unsigned y = __shfl_sync(0xffffffffu, page_row, key);
                     const size_t src = z < 0 ? 0 : ((size_t)z * a.page_size + y) * 64 + gr * 16;
@@ -271,36 +367,49 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             __syncwarp();
             if (copies) {
                 const int z = there ? plane : a.planes, y = there ? (int)page_row : 0;
-                const uint32_t row = to + lane * (D == 64 ? 64 : 128);
+                const uint32_t row = to + lane * T::PITCH;
 #pragma unroll
                 for (int c = 0; c < (D + 127) / 128; ++c) {
                     tma_load_3d(row + c * T::CHUNK, &tm.k, c * 128, y, z, bar);
                     tma_load_3d(row + T::SLICE + c * T::CHUNK, &tm.v, c * 128, y, z, bar);
                 }
             }
-            const size_t at = there ? (size_t)plane * a.blocks + a.by_block(page_row) : 0;
-            cp_async_4(scales + in_slot * 128 + lane * 4, (lane < 16 ? a.k_scale : a.v_scale) + at,
-                       there ? 4u : 0u);
-            if (++issued < piece.blocks) look_up();
+            // scales: one of the slice's keys and one of its values where they have no
+            // more (every key's to the same place would be one after the other)
+            if (!a.flat || lane_key == 0) {
+                const size_t at = there ? (size_t)plane * a.blocks + a.by_block(page_row) : 0;
+                const uint32_t slot = scales + in_slot * T::SCALE_BYTES + lane_key * 4, size = there ? 4u : 0u;
+                if (T::KB == 32 || lane < 16) cp_async_4(slot, a.k_scale + at, size);
+                if (T::KB == 32 || lane >= 16) cp_async_4(slot + T::KB * 4, a.v_scale + at, size);
+            }
+            if (++issued < blocks) look_up();
         }
         cp_async_commit();
         if (++in_slot == T::STAGES) in_slot = 0;
     };
-    if (piece.blocks > 0) look_up();
+    if (blocks > 0) look_up();
 #pragma unroll 1
     for (int s = 0; s < T::STAGES - 1; ++s) issue();
+    // places in a slot that this lane reads: keys kg, kg + 8 (16-byte granules, 64 dims
+    // on: ^ 64), values of S^T rows 2 t, 2 t + 1 (and + 8)
+    const int kg = slice_key<D>(g), v0 = slice_key<D>(2 * t), v1 = slice_key<D>(2 * t + 1);
+    const uint32_t k_at = place_of<D>(kg, t);
+    const uint32_t v0_at = D == 64 ? place_of<64>(v0, g >> 1) + (g & 1) * 8 : place_of<D>(v0, g);
+    const uint32_t v1_at = D == 64 ? place_of<64>(v1, g >> 1) + (g & 1) * 8 : place_of<D>(v1, g);
+    const uint32_t scale_at = a.flat ? 0 : kg * 4;
+    const uint32_t scale_step = a.flat ? 0 : 32;   // eight keys on
 
     // ------------------------------------------------ segments: a unit's blocks here
-    int left = piece.blocks, b = piece.b, at_unit = piece.u, kb = piece.kb, index = 0;
+    int left = blocks, b = spot.b, at_unit = spot.u, kb = spot.at, index = 0;
 #pragma unroll 1
     do {
         const int L = keys_of(a, b);
         const Axis axis = key_axis(a, L);
-        const int nb = unit_blocks(axis.span), n = min(nb - kb, left);
+        const int nb = unit_blocks<T::BLOCK>(axis.span), n = min(nb - kb, left);
         const int hkv = at_unit / a.tiles, rbase = (at_unit - hkv * a.tiles) * T::R;
         // ------------------------------------------------ queries
         // B fragments: lane (g, t) has row nr 8 + g, of each 64 dims the 16 from 16 t on
-        uint32_t qb[NR][D / 16][2];
+        uint32_t qb[NR][D / 64][8];
         float2 unit[NR];     // scores of rows 2 t, 2 t + 1 are sums times this (log2 units)
         int place[NR][2];    // the rows' keys
 #pragma unroll
@@ -308,6 +417,10 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             const int pr = rbase + nr * 8 + g;
             uint32_t w[D / 64][8];
             float most = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[c][e] = 0;
             if (pr < a.rows) {
                 const int h = hkv * a.group + pr / a.Sq;
                 const uint16_t* q = a.q + (((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq) * D + t * 16;
@@ -318,22 +431,17 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                     w[c][0] = x.x, w[c][1] = x.y, w[c][2] = x.z, w[c][3] = x.w;
                     w[c][4] = y.x, w[c][5] = y.y, w[c][6] = y.z, w[c][7] = y.w;
                 }
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[c][e] << 16)),
-                                                 fabsf(__uint_as_float(w[c][e] & 0xffff0000u))));
-            } else {
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[c][e] = 0;
             }
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    most = fmax3(most, fabsf(__uint_as_float(w[c][e] << 16)),
+                                 fabsf(__uint_as_float(w[c][e] & 0xffff0000u)));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            // 2^-e of the largest element's exponent (1 for a row of zeros; exponents
-            // at which it would not be a normal number stay short of them)
+            // the largest element into [1, 2) (a row of zeros: as it is; exponents whose
+            // power would not be a normal number stay short of that)
             int ex = (int)(__float_as_uint(most) >> 23) - 127;
             ex = most == 0.f ? 0 : max(-125, min(ex, 125));
             const float by = __uint_as_float((uint32_t)(127 - ex) << 23);
@@ -341,19 +449,13 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t x = w[c][2 * s + e];
-                        qb[nr][c * 4 + s][e] =
-                            pack_halves(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
-                    }
+                for (int e = 0; e < 8; ++e)
+                    qb[nr][c][e] = pack_halves(__uint_as_float(w[c][e] << 16) * by,
+                                               __uint_as_float(w[c][e] & 0xffff0000u) * by);
             unit[nr].x = __shfl_sync(0xffffffffu, back, 8 * t);
             unit[nr].y = __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                place[nr][e] = (rbase + nr * 8 + 2 * t + e) % a.Sq + L - a.Sq;
-            }
+            for (int e = 0; e < 2; ++e) place[nr][e] = (rbase + nr * 8 + 2 * t + e) % a.Sq + L - a.Sq;
         }
         // keys [all_lo, all_hi) are seen by every row of the sequence, as those below
         // all_first are
@@ -378,169 +480,188 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
 
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            cp_async_wait<T::STAGES - 2>();
+            issue();   // (into the slot of the block before this one, which every lane has read)
+            cp_async_wait<T::STAGES - 1>();
             ok = ok && mbar_wait(bars + out_slot * 8, out_phase, wc, kErrWaitTimeout | kSiteQ8);
             __syncwarp();
-            const uint32_t sk = ring + out_slot * T::STAGE, sv = sk + T::SLICE, sc = scales + out_slot * 128;
-            const int x0 = (kb + i) * kBlock + T::KB * warp;
-            const int kg = slice_key<D>(g);   // this lane's keys: kg, kg + 8
-
-            float sacc[NR][4];
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) sacc[nr][0] = sacc[nr][1] = sacc[nr][2] = sacc[nr][3] = 0.f;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const uint4 u = lds128(sk + place_of<D>(kg, c * 4 + t));
-                const uint4 w = lds128(sk + place_of<D>(kg + 8, c * 4 + t));
-                const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t a0 = q8_halves(uu[s]), a1 = q8_halves(ww[s]);
-                    const uint32_t a2 = q8_halves_up(uu[s]), a3 = q8_halves_up(ww[s]);
-#pragma unroll
-                    for (int nr = 0; nr < NR; ++nr)
-                        mma_f16_16816(sacc[nr], a0, a1, a2, a3, qb[nr][c * 4 + s][0], qb[nr][c * 4 + s][1]);
-                }
-            }
-            const float ks[2] = {lds32(sc + kg * 4), lds32(sc + 32 + kg * 4)};
-            float lv[2] = {lg2_approx(lds32(sc + 64 + kg * 4)), lg2_approx(lds32(sc + 96 + kg * 4))};
-            // scores: s[nr][f] those of key kg + 8 f in rows 2 t, 2 t + 1
+            const uint32_t sk0 = ring + out_slot * T::STAGE + k_at, sv0 = ring + out_slot * T::STAGE + T::SLICE;
+            const uint32_t sc0 = scales + out_slot * T::SCALE_BYTES + scale_at;
+            const int x0 = (kb + i) * T::BLOCK + T::KB * warp;   // the slice's first position, and key
             const int key0 = axis.key(x0);
             const bool whole = x0 + T::KB <= axis.span && key0 + T::KB <= all_hi &&
                                (key0 >= all_lo || key0 + T::KB <= all_first);
-            float2 s[NR][2];
+#pragma unroll 1
+            for (int part = 0; part < T::SUB; part += T::SW) {
+                float2 s[T::SW][NR][2];   // scores: of key kg + 8 f in rows 2 t, 2 t + 1
+                float lv[T::SW][2];       // log2 of the values' scales
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+                for (int w = 0; w < T::SW; ++w) {
+                    const int u16 = 16 * (part + w);
+                    float sum[NR][4];
 #pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    s[nr][f] = fmul2(make_float2(sacc[nr][2 * f], sacc[nr][2 * f + 1]),
-                                     fmul2(unit[nr], make_float2(ks[f], ks[f])));
-            if (!whole) {
-                // (a scale that belongs to no key of some row may be anything)
+                    for (int nr = 0; nr < NR; ++nr) sum[nr][0] = sum[nr][1] = sum[nr][2] = sum[nr][3] = 0.f;
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const int key = key0 + kg + 8 * f;
-                    if (x0 + kg + 8 * f >= axis.span || (key < axis.lo && key >= a.first)) lv[f] = 0.f;
-                }
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint32_t at = (sk0 ^ ((c & 1) * 64)) + (c >> 1) * T::CHUNK + u16 * T::PITCH;
+                        const uint4 x = lds128(at), y = lds128(at + 8 * T::PITCH);
+                        const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t a0 = q8_halves(xx[e]), a1 = q8_halves(yy[e]);
+                            const uint32_t a2 = q8_halves_up(xx[e]), a3 = q8_halves_up(yy[e]);
 #pragma unroll
-                    for (int f = 0; f < 2; ++f)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = key0 + kg + 8 * f, p = place[nr][e];
-                            const bool seen = x0 + kg + 8 * f < axis.span && (!a.causal || key <= p) &&
-                                              (a.window <= 0 || key > p - a.window || key < a.first);
-                            float& x = e == 0 ? s[nr][f].x : s[nr][f].y;
-                            x = seen ? x : -INFINITY;
-                        }
-            }
-            // exponents of the probabilities, and of those times the values' scales
-            auto exponents = [&](int nr, int f, float2& x, float2& y) {
-                x = fadd2(s[nr][f], nm[nr]);
-                y = fadd2(s[nr][f], fadd2(qv[nr], make_float2(lv[f], lv[f])));
-            };
-            float most = -INFINITY, most_v = -INFINITY;
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    float2 x, y;
-                    exponents(nr, f, x, y);
-                    most = fmax3(most, x.x, x.y);
-                    most_v = fmax3(most_v, y.x, y.y);
-                }
-            if (__any_sync(0xffffffffu, most > kGrow || most_v > kGrow + kLift)) {
-#pragma unroll
-                for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float s0 = e == 0 ? s[nr][0].x : s[nr][0].y, s1 = e == 0 ? s[nr][1].x : s[nr][1].y;
-                        float x = fmaxf(s0, s1), y = fmaxf(s0 + lv[0], s1 + lv[1]);
-#pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) {
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-                        }
-                        float& old = e == 0 ? nm[nr].x : nm[nr].y;
-                        float& old_v = e == 0 ? qv[nr].x : qv[nr].y;
-                        const float now = fminf(old, -x), now_v = fminf(old_v, kLift - y);
-                        float& sum = e == 0 ? l[nr].x : l[nr].y;
-                        sum *= ex2_approx(now - old);
-                        const float by = ex2_approx(now_v - old_v);
-                        old = now;
-                        old_v = now_v;
-#pragma unroll
-                        for (int j = 0; j < T::MT; ++j) {
-                            oacc[nr][j][e] *= by;
-                            oacc[nr][j][2 + e] *= by;
+                            for (int nr = 0; nr < NR; ++nr)
+                                mma_f16_16816(sum[nr], a0, a1, a2, a3, qb[nr][c][2 * e], qb[nr][c][2 * e + 1]);
                         }
                     }
-            }
-            uint32_t pb[NR][2];
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr)
+                    for (int f = 0; f < 2; ++f) {
+                        const uint32_t at = sc0 + (2 * (part + w) + f) * scale_step;
+                        const float ks = lds32(at);
+                        lv[w][f] = lg2_approx(lds32(at + T::KB * 4));
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    float2 x, y;
-                    exponents(nr, f, x, y);
-                    l[nr] = fadd2(l[nr], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
-                    pb[nr][f] = movmatrix_trans(pack_halves(ex2_approx(y.x), ex2_approx(y.y)));
+                        for (int nr = 0; nr < NR; ++nr)
+                            s[w][nr][f] = fmul2(make_float2(sum[nr][2 * f], sum[nr][2 * f + 1]),
+                                                fmul2(unit[nr], make_float2(ks, ks)));
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const int at = u16 + kg + 8 * f, key = key0 + at;
+                            const bool real = x0 + at < axis.span;
+                            // (a scale that belongs to no key of some row may be anything)
+                            if (!real || (key < axis.lo && key >= a.first)) lv[w][f] = 0.f;
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int p = place[nr][e];
+                                    const bool seen = real && (!a.causal || key <= p) &&
+                                                      (a.window <= 0 || key > p - a.window || key < a.first);
+                                    float& x = e == 0 ? s[w][nr][f].x : s[w][nr][f].y;
+                                    x = seen ? x : -INFINITY;
+                                }
+                        }
+                    }
                 }
-            // values: lane (g, t) has 16 dims (64: 8) of four keys, of S^T rows 2 t, 2 t + 1,
-            // 2 t + 8, 2 t + 9; those that no row sees become zeros
-            const int v0 = slice_key<D>(2 * t), v1 = slice_key<D>(2 * t + 1);
-            uint32_t have[4] = {~0u, ~0u, ~0u, ~0u};
-            if (!whole) {
-                const int at[4] = {v0, v1, v0 + 8, v1 + 8};
+                // exponents of the probabilities, and of those times the values' scales
+                auto exponents = [&](int w, int nr, int f, float2& x, float2& y) {
+                    x = fadd2(s[w][nr][f], nm[nr]);
+                    y = fadd2(s[w][nr][f], fadd2(qv[nr], make_float2(lv[w][f], lv[w][f])));
+                };
+                float most = -INFINITY, most_v = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = key0 + at[k];
-                    if (x0 + at[k] >= axis.span || (key < axis.lo && key >= a.first)) have[k] = 0;
-                }
-            }
-            // O^T += V^T P^T
-            auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
-                if (!whole) {
-                    x0_ &= have[0];
-                    x1_ &= have[1];
-                    y0_ &= have[2];
-                    y1_ &= have[3];
-                }
-                // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
-                const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
-                const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
-                const uint32_t a0 = q8_halves(xl), a1 = q8_halves_up(xl), a2 = q8_halves(yl), a3 = q8_halves_up(yl);
-                const uint32_t b0 = q8_halves(xh), b1 = q8_halves_up(xh), b2 = q8_halves(yh), b3 = q8_halves_up(yh);
+                for (int w = 0; w < T::SW; ++w)
 #pragma unroll
-                for (int nr = 0; nr < NR; ++nr) {
-                    mma_f16_16816(oacc[nr][j], a0, a1, a2, a3, pb[nr][0], pb[nr][1]);
-                    mma_f16_16816(oacc[nr][j + 1], b0, b1, b2, b3, pb[nr][0], pb[nr][1]);
-                }
-            };
-            if constexpr (D == 64) {
-                const uint32_t half = (g & 1) * 8;
-                const uint2 x0_ = lds64(sv + place_of<D>(v0, g >> 1) + half);
-                const uint2 x1_ = lds64(sv + place_of<D>(v1, g >> 1) + half);
-                const uint2 y0_ = lds64(sv + place_of<D>(v0 + 8, g >> 1) + half);
-                const uint2 y1_ = lds64(sv + place_of<D>(v1 + 8, g >> 1) + half);
-                add(0, x0_.x, x1_.x, y0_.x, y1_.x);
-                add(2, x0_.y, x1_.y, y0_.y, y1_.y);
-            } else {
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int c = 0; c < D / 128; ++c) {
-                    const uint4 x0_ = lds128(sv + place_of<D>(v0, c * 8 + g));
-                    const uint4 x1_ = lds128(sv + place_of<D>(v1, c * 8 + g));
-                    const uint4 y0_ = lds128(sv + place_of<D>(v0 + 8, c * 8 + g));
-                    const uint4 y1_ = lds128(sv + place_of<D>(v1 + 8, c * 8 + g));
-                    add(c * 8, x0_.x, x1_.x, y0_.x, y1_.x);
-                    add(c * 8 + 2, x0_.y, x1_.y, y0_.y, y1_.y);
-                    add(c * 8 + 4, x0_.z, x1_.z, y0_.z, y1_.z);
-                    add(c * 8 + 6, x0_.w, x1_.w, y0_.w, y1_.w);
+                        for (int f = 0; f < 2; ++f) {
+                            float2 x, y;
+                            exponents(w, nr, f, x, y);
+                            most = fmax3(most, x.x, x.y);
+                            most_v = fmax3(most_v, y.x, y.y);
+                        }
+                if (__any_sync(0xffffffffu, most > kGrow || most_v > kGrow + kLift)) {
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+                            for (int w = 0; w < T::SW; ++w)
+#pragma unroll
+                                for (int f = 0; f < 2; ++f) {
+                                    const float z = e == 0 ? s[w][nr][f].x : s[w][nr][f].y;
+                                    x = fmaxf(x, z);
+                                    y = fmaxf(y, z + lv[w][f]);
+                                }
+#pragma unroll
+                            for (int o = 4; o < 32; o <<= 1) {
+                                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+                            }
+                            float& old = e == 0 ? nm[nr].x : nm[nr].y;
+                            float& old_v = e == 0 ? qv[nr].x : qv[nr].y;
+                            const float now = fminf(old, -x), now_v = fminf(old_v, kLift - y);
+                            float& sum = e == 0 ? l[nr].x : l[nr].y;
+                            sum *= ex2_approx(now - old);
+                            const float by = ex2_approx(now_v - old_v);
+                            old = now;
+                            old_v = now_v;
+#pragma unroll
+                            for (int j = 0; j < T::MT; ++j) {
+                                oacc[nr][j][e] *= by;
+                                oacc[nr][j][2 + e] *= by;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int w = 0; w < T::SW; ++w) {
+                    const int u16 = 16 * (part + w);
+                    uint32_t pb[NR][2];
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            float2 x, y;
+                            exponents(w, nr, f, x, y);
+                            l[nr] = fadd2(l[nr], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
+                            pb[nr][f] = movmatrix_trans(pack_halves(ex2_approx(y.x), ex2_approx(y.y)));
+                        }
+                    // values: lane (g, t) has 16 dims (64: 8) of four keys; those that no row
+                    // sees become zeros
+                    uint32_t have[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (!whole) {
+                        const int at[4] = {v0, v1, v0 + 8, v1 + 8};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int key = key0 + u16 + at[k];
+                            if (x0 + u16 + at[k] >= axis.span || (key < axis.lo && key >= a.first)) have[k] = 0;
+                        }
+                    }
+                    // O^T += V^T P^T
+                    auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
+                        if (!whole) {
+                            x0_ &= have[0];
+                            x1_ &= have[1];
+                            y0_ &= have[2];
+                            y1_ &= have[3];
+                        }
+                        // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
+                        const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
+                        const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
+                        const uint32_t a0 = q8_halves(xl), a1 = q8_halves_up(xl);
+                        const uint32_t a2 = q8_halves(yl), a3 = q8_halves_up(yl);
+                        const uint32_t b0 = q8_halves(xh), b1 = q8_halves_up(xh);
+                        const uint32_t b2 = q8_halves(yh), b3 = q8_halves_up(yh);
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            mma_f16_16816(oacc[nr][j], a0, a1, a2, a3, pb[nr][0], pb[nr][1]);
+                            mma_f16_16816(oacc[nr][j + 1], b0, b1, b2, b3, pb[nr][0], pb[nr][1]);
+                        }
+                    };
+                    const uint32_t sv = sv0 + u16 * T::PITCH;
+                    if constexpr (D == 64) {
+                        const uint2 x0_ = lds64(sv + v0_at), x1_ = lds64(sv + v1_at);
+                        const uint2 y0_ = lds64(sv + v0_at + 8 * T::PITCH), y1_ = lds64(sv + v1_at + 8 * T::PITCH);
+                        add(0, x0_.x, x1_.x, y0_.x, y1_.x);
+                        add(2, x0_.y, x1_.y, y0_.y, y1_.y);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < D / 128; ++c) {
+                            const uint32_t at = sv + c * T::CHUNK;
+                            const uint4 x0_ = lds128(at + v0_at), x1_ = lds128(at + v1_at);
+                            const uint4 y0_ = lds128(at + v0_at + 8 * T::PITCH);
+                            const uint4 y1_ = lds128(at + v1_at + 8 * T::PITCH);
+                            add(c * 8, x0_.x, x1_.x, y0_.x, y1_.x);
+                            add(c * 8 + 2, x0_.y, x1_.y, y0_.y, y1_.y);
+                            add(c * 8 + 4, x0_.z, x1_.z, y0_.z, y1_.z);
+                            add(c * 8 + 6, x0_.w, x1_.w, y0_.w, y1_.w);
+                        }
+                    }
                 }
             }
             __syncwarp();
-            issue();
             if (++out_slot == T::STAGES) {
                 out_slot = 0;
                 out_phase ^= 1u;
@@ -549,14 +670,15 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
 
         // ------------------------------------------------ merge of the warps
         // eight rows at a time through the slot that was read last, which is free until
-        // the block after the next is issued: [8][D] O (columns turned by the row
+        // the next block is begun: [8][D] O (columns turned by the row
         // against bank conflicts), and row maxima and sums through its scales
         const int last_slot = (out_slot == 0 ? T::STAGES : out_slot) - 1;
         const float* merge0 = reinterpret_cast<const float*>(smem + last_slot * T::STAGE);
         float* mine = reinterpret_cast<float*>(smem + warp * T::WARP_RING + last_slot * T::STAGE);
         constexpr int WF = T::WARP_RING / 4, WS = T::WARP_SCALES / 4;   // floats from warp to warp
-        const float* ml0 = reinterpret_cast<const float*>(smem + T::SCALES + last_slot * 128);
-        float* ml = reinterpret_cast<float*>(smem + T::SCALES + warp * T::WARP_SCALES + last_slot * 128);
+        const float* ml0 = reinterpret_cast<const float*>(smem + T::SCALES + last_slot * T::SCALE_BYTES);
+        float* ml = reinterpret_cast<float*>(smem + T::SCALES + warp * T::WARP_SCALES +
+                                             last_slot * T::SCALE_BYTES);
         const int valid_rows = min(T::R, a.rows - rbase);
         const bool whole_unit = n == nb;
         // joined: split s finishes the rows [s own, (s + 1) own) (see decode.cu)
@@ -676,7 +798,13 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             }
             break;
         }
-        if (!whole_unit && threadIdx.x == 0) a.head[part] = make_int4(b, at_unit, n, kb == 0 ? nb : 0);
+        // (the unit starts here and goes on: what the merge by pieces has to know)
+        if (kb == 0 && !whole_unit && a.head != nullptr && threadIdx.x == 0) {
+            const Line cut = *kept;
+            const Pieces pc = cut.aligned > 0 ? Pieces{(int)blockIdx.x, cut.of_unit(nb), 0}
+                                              : pieces_of(cut, cut.from(blockIdx.x) + (blocks - left), nb);
+            a.head[blockIdx.x] = make_int4(b, at_unit, pc.count, pc.second);
+        }
         left -= n;
         kb = 0;
         ++index;
@@ -693,65 +821,136 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     }
 }
 
-// Merges the pieces of the unit that starts in CTA blockIdx.x of the kernel before
-// and goes on in the next ones: row blockIdx.y of its tile, eight warps over the
-// pieces, lanes over the columns.
+// Merge of units in a few pieces: CTA (piece that such a unit starts in, eight rows
+// of its tile), a warp per row.
 template <int D>
-__global__ void __launch_bounds__(256) combine_q8_kernel(const DecodeQ8Args a, int tile) {
-    constexpr int PER = D / 32;   // columns of a lane
-    __shared__ float other[8][D], weight[8];
-    dependents_may_start();
+__global__ void __launch_bounds__(256) combine_few_kernel(const DecodeQ8Args a, int tile) {
+    constexpr int PER = D / 32;   // columns of a lane, two side by side
     wait_for_previous();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = gridDim.x, r = blockIdx.y;
-    const int4 h0 = a.head[2 * blockIdx.x], h1 = a.head[2 * blockIdx.x + 1];
-    const int quota = a.head[2 * G].x;
-    const bool second = h0.w == 0;   // (.w: the unit's blocks where a piece is its first)
-    const int4 hd = second ? h1 : h0;
-    if (hd.w == 0) return;
-    const int b = hd.x, hkv = hd.y / a.tiles, rbase = (hd.y - hkv * a.tiles) * tile;
-    if (rbase + r >= a.rows) return;
-    const int pieces = 1 + (hd.w - hd.z + quota - 1) / quota;
-    auto slot = [&](int k) { return k == 0 ? 2 * (int)blockIdx.x + second : 2 * ((int)blockIdx.x + k); };
-    const int h = hkv * a.group + (rbase + r) / a.Sq;
+    const int4 hd = a.head[blockIdx.x];   // batch entry, unit, pieces, the first's slot
+    if (hd.z < 2) return;
+    const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int hkv = hd.y / a.tiles, pr = (hd.y - hkv * a.tiles) * tile + r;
+    if (pr >= a.rows) return;
+    const Pieces pc{(int)blockIdx.x, hd.z, hd.w};
+    const int h = hkv * a.group + pr / a.Sq;
     const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
-    float M = sg;
-    for (int k = lane; k < pieces; k += 32) M = fmaxf(M, a.part_lse[(size_t)slot(k) * tile + r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float acc[PER], sum = 0.f;
+    float M = sg, sum = sg == -INFINITY ? 0.f : 1.f, acc[PER];   // (the sink's own term)
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int k = warp; k < pieces; k += 8) {
-            const size_t at = (size_t)slot(k) * tile + r;
-            const float f = ex2_approx(a.part_lse[at] - M);
+    for (int k0 = 0; k0 < pc.count; k0 += 4) {   // (four in flight)
+        float x[4];
+        float2 y[4][PER / 2];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const size_t at = (size_t)pc.slot(min(k0 + k, pc.count - 1)) * tile + r;
+            x[k] = k0 + k < pc.count ? a.part_lse[at] : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e)
+                y[k][e] = *reinterpret_cast<const float2*>(a.part_o + at * D + e * 64 + 2 * lane);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (x[k] == -INFINITY) continue;
+            const float top = fmaxf(M, x[k]), old = ex2_approx(M - top), f = ex2_approx(x[k] - top);
+            M = top;
+            sum = fmaf(sum, old, f);
+#pragma unroll
+            for (int e = 0; e < PER / 2; ++e) {
+                acc[2 * e] = fmaf(acc[2 * e], old, f * y[k][e].x);
+                acc[2 * e + 1] = fmaf(acc[2 * e + 1], old, f * y[k][e].y);
+            }
+        }
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const size_t row = ((size_t)hd.x * a.Hq + h) * a.Sq + pr % a.Sq;
+#pragma unroll
+    for (int e = 0; e < PER / 2; ++e)
+        *reinterpret_cast<uint32_t*>(a.o + row * D + e * 64 + 2 * lane) =
+            pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    if (lane == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
+}
+
+// Merge of few units in many pieces: CTA (unit, row), sixteen warps over the pieces, each
+// with a base of its own, merged at the end.
+constexpr int kCombineWarps = 16;
+template <int D, int BLOCK>
+__global__ void __launch_bounds__(kCombineWarps * 32) combine_q8_kernel(const DecodeQ8Args a, int tile) {
+    constexpr int PER = D / 32;   // columns of a lane, two side by side
+    __shared__ float other[kCombineWarps][D], base[kCombineWarps], weight[kCombineWarps];
+    wait_for_previous();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+    const int units = a.Hkv * a.tiles, b = (int)blockIdx.x / units, u = (int)blockIdx.x - b * units;
+    const int hkv = u / a.tiles, pr = (u - hkv * a.tiles) * tile + r;
+    if (pr >= a.rows) return;
+    int mine;
+    const Line line = cut_line<BLOCK>(a, mine);
+    const int nb = unit_blocks<BLOCK>(key_axis(a, keys_of(a, b)).span), len = line.of_unit(nb);
+    int before = 0;   // its batch entry's place on the line
+    for (int i = lane; i < b; i += 32)
+        before += units * line.of_unit(unit_blocks<BLOCK>(key_axis(a, keys_of(a, i)).span));
+    before = __reduce_add_sync(0xffffffffu, before);
+    const Pieces pc = pieces_of(line, before + u * len, len);
+    if (pc.count < 2) return;
+    const int h = hkv * a.group + pr / a.Sq;
+    auto at = [&](int k) { return (size_t)pc.slot(k) * tile + r; };
+    // the warp's pieces: warp, warp + 16, ...; lane l has the weight of the l-th
+    float M = -INFINITY, sum = 0.f, acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int k0 = warp; k0 < pc.count; k0 += 32 * kCombineWarps) {
+        const int its = k0 + lane * kCombineWarps;
+        const float x = its < pc.count ? a.part_lse[at(its)] : -INFINITY;
+        float top = fmaxf(x, M);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (top == -INFINITY) continue;
+        const float old = ex2_approx(M - top), w = ex2_approx(x - top);
+        M = top;
+        sum *= old;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] *= old;
+        const int n = min(32, (pc.count - k0 + kCombineWarps - 1) / kCombineWarps);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float f = __shfl_sync(0xffffffffu, w, k);
+            const float* po = a.part_o + at(k0 + k * kCombineWarps) * D + 2 * lane;
             sum += f;
 #pragma unroll
             for (int e = 0; e < PER; e += 2) {
-                const float2 x = *reinterpret_cast<const float2*>(a.part_o + at * D + e * 32 + 2 * lane);
-                acc[e] = fmaf(f, x.x, acc[e]);
-                acc[e + 1] = fmaf(f, x.y, acc[e + 1]);
+                const float2 y = *reinterpret_cast<const float2*>(po + e * 32);
+                acc[e] = fmaf(f, y.x, acc[e]);
+                acc[e + 1] = fmaf(f, y.y, acc[e + 1]);
             }
         }
     }
 #pragma unroll
     for (int e = 0; e < PER; e += 2)
         *reinterpret_cast<float2*>(&other[warp][e * 32 + 2 * lane]) = make_float2(acc[e], acc[e + 1]);
-    if (lane == 0) weight[warp] = sum;
+    if (lane == 0) {
+        base[warp] = M;
+        weight[warp] = sum;
+    }
     __syncthreads();
     const int c = threadIdx.x * 2;
     if (c >= D) return;
-    sum = M != -INFINITY ? ex2_approx(sg - M) : 0.f;
+    const float sg = a.sinks != nullptr ? a.sinks[h] * kLog2ef : -INFINITY;
+    M = sg;
+    for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, base[w]);
     float2 o = make_float2(0.f, 0.f);
+    sum = 0.f;
+    if (M != -INFINITY) {
+        sum = ex2_approx(sg - M);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        sum += weight[w];
-        o.x += other[w][c];
-        o.y += other[w][c + 1];
+        for (int w = 0; w < kCombineWarps; ++w) {
+            const float f = ex2_approx(base[w] - M);
+            sum = fmaf(f, weight[w], sum);
+            o.x = fmaf(f, other[w][c], o.x);
+            o.y = fmaf(f, other[w][c + 1], o.y);
+        }
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const size_t row = ((size_t)b * a.Hq + h) * a.Sq + (rbase + r) % a.Sq;
+    const size_t row = ((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq;
     *reinterpret_cast<uint32_t*>(a.o + row * D + c) = pack_bf16x2(o.x * inv, o.y * inv);
     if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
 }
@@ -772,8 +971,12 @@ cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
     e = launch_dependent(decode_q8_kernel<D, NR>, dim3((unsigned)a.n_splits), dim3(T::THREADS),
                          kAlign + T::RING, s, p.maps, a);
     if (e != cudaSuccess) return e;
-    return launch_dependent(combine_q8_kernel<D>, dim3((unsigned)a.n_splits, (unsigned)T::R), dim3(256), 0, s,
-                            a, (int)T::R);
+    if (a.head != nullptr)
+        return launch_dependent(combine_few_kernel<D>, dim3((unsigned)a.n_splits, (unsigned)(T::R / 8)), dim3(256),
+                                0, s, a, (int)T::R);
+    return launch_dependent(combine_q8_kernel<D, T::BLOCK>,
+                            dim3((unsigned)(a.B * a.Hkv * a.tiles), (unsigned)T::R), dim3(kCombineWarps * 32), 0,
+                            s, a, (int)T::R);
 }
 
 template <int D>
@@ -789,6 +992,7 @@ cudaError_t launch_dim(const DecodeQ8Launch& p, cudaStream_t s) {
 
 }  // namespace
 
+int decode_q8_block(int head_dim) { return head_dim == 256 ? Q8Traits<256, 1>::BLOCK : Q8Traits<128, 1>::BLOCK; }
 int decode_q8_ctas(int head_dim, int tile) {
     if (head_dim == 64) return tile == 32 ? Q8Traits<64, 4>::MIN_CTAS : Q8Traits<64, 1>::MIN_CTAS;
     if (head_dim == 128) return tile == 32 ? Q8Traits<128, 4>::MIN_CTAS : Q8Traits<128, 1>::MIN_CTAS;
