@@ -362,9 +362,11 @@ struct DecodeQ8Launch {
     DecodeQ8Maps maps;
     DecodeQ8Args args;
 };
-// Rows of a tile: 8, 16 or, up to head_dim 128, 32.
+// Rows of a tile: 8, 16 or, at head_dim 64, 32.  Wider tiles read and convert the keys
+// less often but hold more registers a warp (us, tiles of 16 / 32 for 16 x 1K to 16K
+// keys x 8 heads, 64 rows: head_dim 64 152 / 134; 32 rows: head_dim 128 109 / 124).
 inline int decode_q8_tile(int head_dim, int rows) {
-    return rows <= 8 ? 8 : rows <= 16 || head_dim == 256 ? 16 : 32;
+    return rows <= 8 ? 8 : rows <= 16 || head_dim > 64 ? 16 : 32;
 }
 int decode_q8_block(int head_dim);   // keys of a block, four slices
 int decode_q8_ctas(int head_dim, int tile);   // CTAs that an SM holds at once

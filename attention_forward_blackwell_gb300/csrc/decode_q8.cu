@@ -51,7 +51,7 @@
 // lanes took a third of all it issues; copies run ahead over the ends of units,
 // and the page numbers of a slice are fetched while the one before is issued.
 // What a box brings beside keys that some row sees may be anything: scores are
-// replaced, values zeroed in registers, at the borders alone.
+// replaced, values zeroed, at the borders alone.
 #include "common.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -79,7 +79,8 @@ struct Q8Traits {
     static constexpr int SUB = D == 256 ? 1 : 2;        // 16-key parts of a slice
     static constexpr int KB = 16 * SUB;                 // keys of a slice
     static constexpr int BLOCK = WARPS * KB;            // keys of a block
-    static constexpr int SW = NR == 1 ? SUB : 1;        // parts worked on together
+    static constexpr int SW = NR <= 2 ? SUB : 1;        // parts worked on together
+    static constexpr bool KEEP = D != 256 || NR == 1;   // exponents kept over the vote
     static constexpr int PITCH = D == 64 ? 64 : 128;    // bytes of a box's row
     static constexpr int CHUNK = KB * PITCH;            // a box of a slice's rows
     static constexpr int SLICE = KB * D;                // bytes of a slice of keys, or of values
@@ -96,7 +97,10 @@ struct Q8Traits {
     static constexpr int JOIN_LSE = (JOIN_ROWS * 4 + 15) / 16 * 16;
     static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
     static constexpr int MT = D / 16;                   // tiles of O^T
-    static constexpr int MIN_CTAS = NR == 4 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
+    // CTAs of an SM: what the registers of a warp leave.  16 rows with two parts in
+    // hand and two CTAs at head_dim 128 take 66 us where one part and three take 76
+    // (16 x 1K to 16K keys x 8 heads; at 64, three for four, 43 for 65).
+    static constexpr int MIN_CTAS = D == 256 ? 2 : (D == 64 ? 5 : 4) - (NR == 4 ? 3 : NR);
     // the merge of 8 rows goes through the slot that was read last
     static_assert(8 * D * 4 <= STAGE && 16 * 4 <= SCALE_BYTES, "merge buffer");
 };
@@ -490,6 +494,24 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             const int key0 = axis.key(x0);
             const bool whole = x0 + T::KB <= axis.span && key0 + T::KB <= all_hi &&
                                (key0 >= all_lo || key0 + T::KB <= all_first);
+            if (!whole) {
+                // values that no row sees may be anything, and zero times that would
+                // poison O: zeros in their place (a lane per key, a row's granules)
+                if (lane < T::KB) {
+                    const int key = key0 + lane;
+                    if (x0 + lane >= axis.span || (key < axis.lo && key >= a.first)) {
+                        const uint32_t at = ring + out_slot * T::STAGE + T::SLICE + lane * T::PITCH;
+#pragma unroll 1
+                        for (int e = 0; e < D / 16; ++e)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             at + e / (T::PITCH / 16) * T::CHUNK + e % (T::PITCH / 16) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                }
+                fence_proxy_async_smem();   // (copies will write here)
+                __syncwarp();
+            }
 #pragma unroll 1
             for (int part = 0; part < T::SUB; part += T::SW) {
                 float2 s[T::SW][NR][2];   // scores: of key kg + 8 f in rows 2 t, 2 t + 1
@@ -545,9 +567,11 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                     }
                 }
                 // exponents of the probabilities, and of those times the values' scales
-                auto exponents = [&](int w, int nr, int f, float2& x, float2& y) {
-                    x = fadd2(s[w][nr][f], nm[nr]);
-                    y = fadd2(s[w][nr][f], fadd2(qv[nr], make_float2(lv[w][f], lv[w][f])));
+                // (kept over the vote where registers allow, else computed again)
+                float2 px[T::SW][NR][2], py[T::SW][NR][2];
+                auto exponents = [&](int w, int nr, int f) {
+                    px[w][nr][f] = fadd2(s[w][nr][f], nm[nr]);
+                    py[w][nr][f] = fadd2(s[w][nr][f], fadd2(qv[nr], make_float2(lv[w][f], lv[w][f])));
                 };
                 float most = -INFINITY, most_v = -INFINITY;
 #pragma unroll
@@ -556,10 +580,9 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                         for (int f = 0; f < 2; ++f) {
-                            float2 x, y;
-                            exponents(w, nr, f, x, y);
-                            most = fmax3(most, x.x, x.y);
-                            most_v = fmax3(most_v, y.x, y.y);
+                            exponents(w, nr, f);
+                            most = fmax3(most, px[w][nr][f].x, px[w][nr][f].y);
+                            most_v = fmax3(most_v, py[w][nr][f].x, py[w][nr][f].y);
                         }
                 if (__any_sync(0xffffffffu, most > kGrow || most_v > kGrow + kLift)) {
 #pragma unroll
@@ -594,6 +617,15 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                                 oacc[nr][j][2 + e] *= by;
                             }
                         }
+                    if (T::KEEP) {
+#pragma unroll
+                        for (int w = 0; w < T::SW; ++w)
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr) {
+                                exponents(w, nr, 0);
+                                exponents(w, nr, 1);
+                            }
+                    }
                 }
 #pragma unroll
                 for (int w = 0; w < T::SW; ++w) {
@@ -603,30 +635,13 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
                         for (int f = 0; f < 2; ++f) {
-                            float2 x, y;
-                            exponents(w, nr, f, x, y);
+                            if (!T::KEEP) exponents(w, nr, f);
+                            const float2 x = px[w][nr][f], y = py[w][nr][f];
                             l[nr] = fadd2(l[nr], make_float2(ex2_approx(x.x), ex2_approx(x.y)));
                             pb[nr][f] = movmatrix_trans(pack_halves(ex2_approx(y.x), ex2_approx(y.y)));
                         }
-                    // values: lane (g, t) has 16 dims (64: 8) of four keys; those that no row
-                    // sees become zeros
-                    uint32_t have[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (!whole) {
-                        const int at[4] = {v0, v1, v0 + 8, v1 + 8};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int key = key0 + u16 + at[k];
-                            if (x0 + u16 + at[k] >= axis.span || (key < axis.lo && key >= a.first)) have[k] = 0;
-                        }
-                    }
-                    // O^T += V^T P^T
+                    // O^T += V^T P^T: lane (g, t) has 16 dims (64: 8) of four keys
                     auto add = [&](int j, uint32_t x0_, uint32_t x1_, uint32_t y0_, uint32_t y1_) {
-                        if (!whole) {
-                            x0_ &= have[0];
-                            x1_ &= have[1];
-                            y0_ &= have[2];
-                            y1_ &= have[3];
-                        }
                         // words of four dims of the keys: tiles j (dims 0, 1) and j + 1 (dims 2, 3)
                         const uint32_t xl = __byte_perm(x0_, x1_, 0x5140), xh = __byte_perm(x0_, x1_, 0x7362);
                         const uint32_t yl = __byte_perm(y0_, y1_, 0x5140), yh = __byte_perm(y0_, y1_, 0x7362);
@@ -985,7 +1000,7 @@ cudaError_t launch_dim(const DecodeQ8Launch& p, cudaStream_t s) {
         case 8: return launch_tile<D, 1>(p, s);
         case 16: return launch_tile<D, 2>(p, s);
         default:
-            if constexpr (D <= 128) return launch_tile<D, 4>(p, s);
+            if constexpr (D == 64) return launch_tile<D, 4>(p, s);
             else return cudaErrorInvalidValue;
     }
 }
@@ -994,9 +1009,14 @@ cudaError_t launch_dim(const DecodeQ8Launch& p, cudaStream_t s) {
 
 int decode_q8_block(int head_dim) { return head_dim == 256 ? Q8Traits<256, 1>::BLOCK : Q8Traits<128, 1>::BLOCK; }
 int decode_q8_ctas(int head_dim, int tile) {
-    if (head_dim == 64) return tile == 32 ? Q8Traits<64, 4>::MIN_CTAS : Q8Traits<64, 1>::MIN_CTAS;
-    if (head_dim == 128) return tile == 32 ? Q8Traits<128, 4>::MIN_CTAS : Q8Traits<128, 1>::MIN_CTAS;
-    return Q8Traits<256, 1>::MIN_CTAS;
+    switch (head_dim) {
+        case 64:
+            return tile == 8    ? Q8Traits<64, 1>::MIN_CTAS
+                   : tile == 16 ? Q8Traits<64, 2>::MIN_CTAS
+                                : Q8Traits<64, 4>::MIN_CTAS;
+        case 128: return tile == 8 ? Q8Traits<128, 1>::MIN_CTAS : Q8Traits<128, 2>::MIN_CTAS;
+        default: return Q8Traits<256, 1>::MIN_CTAS;
+    }
 }
 
 cudaError_t launch_decode_q8(const DecodeQ8Launch& p, int head_dim, cudaStream_t s) {
