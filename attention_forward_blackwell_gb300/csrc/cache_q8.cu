@@ -19,10 +19,10 @@ namespace {
 struct Q8Cache {
     uint8_t* codes[2];         // of keys and values
     float* scales[2];
-    int num_pages, hkv, page_size, block;
+    PageTable pages;
+    int hkv, block;
     int blocks;                // of a page
-    const int* table;
-    int max_pages;
+    FastDiv by_block;          // by block
 };
 
 // ------------------------------------------------------------ append ----
@@ -41,48 +41,48 @@ struct AppendArgs {
     long long ss[3][3];
     int hq;
     uint4* q_out;              // [batch, hq, n, d]
+    FastDiv by_tasks, by_hq;
     int units;                 // blocks that an entry's new rows may lie in
+    int kv_ctas;               // CTAs along y that append; the rest turn queries
 };
 
 // Granules of a row that a thread keeps between the two passes over a block.
 constexpr int kKept = 4;
 
-// Codes of 16 elements in two granules' places (8 bytes each).
+// Codes of a task's two granules.
 __device__ __forceinline__ void store_codes(uint8_t* row, const TaskAt& at, const float (&x)[8],
                                             const float (&y)[8], float inv) {
-    const uint2 u = make_uint2(q8_codes(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                               q8_codes(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-    const uint2 w = make_uint2(q8_codes(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                               q8_codes(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-    if (at.b == at.a + 8) {
-        *reinterpret_cast<uint4*>(row + at.a) = make_uint4(u.x, u.y, w.x, w.y);
-    } else {
-        *reinterpret_cast<uint2*>(row + at.a) = u;
-        *reinterpret_cast<uint2*>(row + at.b) = w;
-    }
+    *reinterpret_cast<uint2*>(row + at.a) =
+        make_uint2(q8_codes(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                   q8_codes(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
+    *reinterpret_cast<uint2*>(row + at.b) =
+        make_uint2(q8_codes(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                   q8_codes(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
 }
 
 // Queries of batch entry b: as in rope.cu, a task a thread.
 template <bool INTERLEAVED>
 __device__ void append_queries(const AppendArgs& a, int b, int len, int n) {
-    const long long all = (long long)n * a.hq * a.tasks;
-    for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < all;
-         e += (long long)gridDim.x * blockDim.x) {
-        const int j = (int)(e % a.tasks);
-        const long long r = e / a.tasks;
-        const int i = (int)(r % n), h = (int)(r / n);
-        const TaskAt at = task_at(a.turn, j);
-        const uint4* from = a.src[2] + b * a.ss[2][0] + h * a.ss[2][1] + i * a.ss[2][2];
-        uint4* to = a.q_out + (((long long)b * a.hq + h) * a.n + i) * (2 * a.tasks);
+    const unsigned all = (unsigned)n * (unsigned)(a.hq * a.tasks);   // (below 2^31: the host sees to it)
+    const unsigned cta = (blockIdx.y - a.kv_ctas) * gridDim.x + blockIdx.x;
+    const unsigned step = (gridDim.y - a.kv_ctas) * gridDim.x * blockDim.x;
+    for (unsigned e = cta * blockDim.x + threadIdx.x; e < all; e += step) {
+        const unsigned r = a.by_tasks(e), i = a.by_hq(r);
+        const int j = (int)(e - r * (unsigned)a.tasks), h = (int)(r - i * (unsigned)a.hq);
+        const TaskAt at = task_at<INTERLEAVED>(a.turn.rot, a.tasks, j);
+        const uint4* from = a.src[2] + b * a.ss[2][0] + h * a.ss[2][1] + (long long)i * a.ss[2][2];
+        uint4* to = a.q_out + (((long long)b * a.hq + h) * a.n + (int)i) * (2 * a.tasks);
         uint4 u = from[at.a >> 3], w = from[at.b >> 3];
-        if (at.turned) {
+        if (at.turned_a || at.turned_b) {
             Angles g;
-            angles_of(a.turn, j,
-                      a.positions != nullptr ? a.positions[b * a.position_stride + i] : (int)((unsigned)len + i), g);
+            angles_of<INTERLEAVED>(a.turn, at,
+                                   a.positions != nullptr ? a.positions[b * a.position_stride + i]
+                                                          : (int)((unsigned)len + i),
+                                   g);
             float x[8], y[8];
             unpack8(u, x);
             unpack8(w, y);
-            turn_task(INTERLEAVED, g, x, y);
+            turn_task<INTERLEAVED>(at, g, x, y);
             u = pack8(x);
             w = pack8(y);
         }
@@ -91,174 +91,176 @@ __device__ void append_queries(const AppendArgs& a, int b, int len, int n) {
     }
 }
 
-// CTA (block of an entry, head and keys or values -- the last y: queries --,
-// batch entry).  Two passes over the new rows of a block: their reach, then their
-// codes; what a thread has of them stays in registers in between, kKept tasks,
-// which covers blocks of 64 keys of 128 elements, and is read again past that
-// (from L1 or L2).  A block has one writer, so nothing is atomic.  Bound by the
-// bytes, 3 for an element, and for single tokens by a chain of loads: length,
-// page, scale and row.
-template <bool INTERLEAVED>
+// A unit is a block of an entry's keys or of its values, of a head; WARP: a warp has
+// one, four a CTA (few rows), else a CTA.  CTA (block, heads and keys or values -- past
+// kv_ctas: queries --, batch entry).  Two passes over the new rows of a block: their
+// reach, then their codes; what a thread has of them stays in registers in between,
+// kKept tasks, which covers blocks of 64 keys of 128 elements, and is read again past
+// that (from L1 or L2).  A block has one writer, so nothing is atomic.  Bound by the
+// bytes, 3 for an element, and for single tokens by a chain of loads: length, page,
+// scale; the rows, and the angles that need only the length, come beside it.
+template <bool INTERLEAVED, bool WARP>
 __global__ void append_q8_kernel(const AppendArgs a) {
     __shared__ float most[8];
     dependents_may_start();
     wait_for_previous();
-    const int b = blockIdx.z;
     const Q8Cache& c = a.c;
+    const int b = blockIdx.z;
     const int start = max(a.lens[b], 0);
     int n = max(0, min(a.n_new != nullptr ? a.n_new[b] : a.n, a.n));
-    if ((int)blockIdx.y == 2 * c.hkv) {
+    if ((int)blockIdx.y >= a.kv_ctas) {
         if (n > 0) append_queries<INTERLEAVED>(a, b, start, n);
         return;
     }
+    const int T = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+    const int which = WARP ? blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.y;
+    if (WARP && which >= 2 * c.hkv) return;
+    const int h = which >> 1, kind = which & 1;
     // (what lies behind the table has no page; len + n stays in 32 bits)
-    const int room = c.max_pages * c.page_size, len = min(start, room);
+    const int room = c.pages.max_pages * c.pages.page_size, len = min(start, room);
     n = min(n, room - len);
-    const int h = blockIdx.y >> 1, kind = blockIdx.y & 1;
-    uint8_t* const codes = c.codes[kind];
-    float* const scales = c.scales[kind];
-    const int d = a.tasks * 16;
+    uint8_t* const codes = kind == 0 ? c.codes[0] : c.codes[1];
+    float* const scales = kind == 0 ? c.scales[0] : c.scales[1];
+    const int d = a.tasks * 16, num_pages = c.pages.num_pages;
     auto row_of = [&](int page, int row) {
-        return codes + (((size_t)page * c.hkv + h) * c.page_size + row) * d;
+        return codes + (((size_t)page * c.hkv + h) * c.pages.page_size + row) * d;
     };
     auto scale_of = [&](int page, int block) {
         return scales + ((size_t)page * c.hkv + h) * c.blocks + block;
     };
+    const int first0 = (int)c.by_block((unsigned)len) * c.block;   // the open block: where the next key goes
     // the page that reserve replaced: its rows below `copied` come along
-    int from = -1, to = -1, copied = 0;
+    int from = -1, copied = 0;
+    bool moved = false;   // the open block's earlier rows are taken by the unit that fills it
     if (a.copies != nullptr) {
         from = a.copies[3 * b];
-        to = a.copies[3 * b + 1];
-        copied = min(a.copies[3 * b + 2], c.page_size);
-        if ((unsigned)from >= (unsigned)c.num_pages || (unsigned)to >= (unsigned)c.num_pages || from == to)
+        const int to = a.copies[3 * b + 1];
+        copied = min(a.copies[3 * b + 2], c.pages.page_size);
+        if ((unsigned)from >= (unsigned)num_pages || (unsigned)to >= (unsigned)num_pages || from == to)
             copied = 0;
-    }
-    // the open block: page and first row where the next key goes
-    const int first0 = len / c.block * c.block;
-    int page0 = -1, row0 = 0;
-    key_page(c.table + (size_t)b * c.max_pages, c.max_pages, c.page_size, c.num_pages, first0, page0, row0);
-    // its earlier rows are taken from the replaced page by the unit that fills it
-    const bool moved = copied > 0 && page0 == to && len > first0 && row0 + (len - first0) == copied;
-    if ((int)blockIdx.x >= a.units) {   // a whole block of a replaced page
-        const int block = blockIdx.x - a.units, at = block * c.block;
-        const int rows = min(c.block, copied - at);
-        if (rows <= 0 || (moved && at == row0)) return;
-        const uint4* s = reinterpret_cast<const uint4*>(row_of(from, at));
-        uint4* t = reinterpret_cast<uint4*>(row_of(to, at));
-        for (int e = threadIdx.x; e < rows * a.tasks; e += blockDim.x) t[e] = s[e];
-        if (threadIdx.x == 0) *scale_of(to, block) = *scale_of(from, block);
-        return;
+        int page0 = -1, row0 = 0;
+        key_page(c.pages, b, first0, page0, row0);
+        moved = copied > 0 && page0 == to && len > first0 && row0 + (len - first0) == copied;
+        if ((int)blockIdx.x >= a.units) {   // a whole block of a replaced page
+            const int block = blockIdx.x - a.units, at = block * c.block;
+            const int rows = min(c.block, copied - at);
+            if (rows <= 0 || (moved && at == row0)) return;
+            const uint4* s = reinterpret_cast<const uint4*>(row_of(from, at));
+            uint4* t = reinterpret_cast<uint4*>(row_of(to, at));
+            for (int e = tid; e < rows * a.tasks; e += T) t[e] = s[e];
+            if (tid == 0) *scale_of(to, block) = *scale_of(from, block);
+            return;
+        }
     }
     const long long first_ = first0 + (long long)blockIdx.x * c.block;
     const int first = (int)min(first_, (long long)room);
     const int lo = max(first, len), hi = (int)min(first_ + c.block, (long long)len + n);
     const bool takes_over = moved && blockIdx.x == 0;
     if (lo >= hi && !takes_over) return;
-    int page, row;   // (a block lies in one page)
-    if (!key_page(c.table + (size_t)b * c.max_pages, c.max_pages, c.page_size, c.num_pages, first, page, row))
-        return;
-    const int block = row / c.block;
-    const int old_page = takes_over ? from : page;
-    const float before = lo > first ? *scale_of(old_page, block) : 0.f;
-    const uint4* src = a.src[kind] + b * a.ss[kind][0] + h * a.ss[kind][1];
+    const uint4* src = (kind == 0 ? a.src[0] : a.src[1]) + b * a.ss[kind][0] + h * a.ss[kind][1];
     const long long step = a.ss[kind][2];
-    const bool turns = kind == 0 && a.turn.rot > 0;
+    const int rot = kind == 0 ? a.turn.rot : 0;
     const int all = max(0, hi - lo) * a.tasks;
     uint4 ka[kKept], kb[kKept];
+    auto load = [&](int e, uint4& u, uint4& w) {
+        const int i = (int)a.by_tasks((unsigned)e), j = e - i * a.tasks;
+        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, j);
+        const uint4* r = src + (lo - len + i) * step;
+        u = r[at.a >> 3];
+        w = r[at.b >> 3];
+    };
+    auto angles = [&](int e, Angles& g) {
+        const int i = (int)a.by_tasks((unsigned)e), j = e - i * a.tasks, row = lo - len + i;
+        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, j);
+        if (at.turned_a || at.turned_b)
+            angles_of<INTERLEAVED>(a.turn, at,
+                                   a.positions != nullptr ? a.positions[b * a.position_stride + row]
+                                                          : (int)((unsigned)start + row),
+                                   g);
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (tid + k * T < all) load(tid + k * T, ka[k], kb[k]);
+    int page, row;   // (a block lies in one page)
+    const bool there = key_page(c.pages, b, first, page, row);
+    Angles first_angles;   // of the thread's first task
+    if (rot > 0 && tid < all) angles(tid, first_angles);
+    if (!there) return;
+    const int block = (int)c.by_block((unsigned)row);
+    const int old_page = takes_over ? from : page;
+    const float before = lo > first ? *scale_of(old_page, block) : 0.f;
     float square = 0.f;
     const float f2 = a.turn.factor * a.turn.factor;
-    auto load = [&](int e, uint4& u, uint4& w) {
-        const int i = e / a.tasks, j = e - i * a.tasks;
-        const TaskAt at = task_at(a.turn, j);
-        const int ga = turns ? at.a >> 3 : 2 * j, gb = turns ? at.b >> 3 : 2 * j + 1;
-        const uint4* r = src + (lo - len + i) * step;
-        u = r[ga];
-        w = r[gb];
-    };
     auto reach = [&](int e, const uint4& u, const uint4& w) {
-        const int j = e % a.tasks;
-        float x[8], y[8], m = 0.f;
+        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, e - (int)a.by_tasks((unsigned)e) * a.tasks);
+        float x[8], y[8], turned = 0.f, rest = 0.f;
         unpack8(u, x);
         unpack8(w, y);
         // (products of bf16 values are exact in fp32, a sum of two rounds once)
-        if (turns && 16 * j < a.turn.rot) {
-            if (INTERLEAVED) {
+        if (INTERLEAVED) {
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                    m = fmaxf(m, fmaf(x[k], x[k], x[k + 1] * x[k + 1]));
-                    m = fmaxf(m, fmaf(y[k], y[k], y[k + 1] * y[k + 1]));
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaf(x[k], x[k], y[k] * y[k]));
+            for (int k = 0; k < 8; k += 2) {
+                const float p = fmaf(x[k], x[k], x[k + 1] * x[k + 1]);
+                const float q = fmaf(y[k], y[k], y[k + 1] * y[k + 1]);
+                if (at.turned_a) turned = fmaxf(turned, p);
+                else rest = fmaxf(rest, fmaxf(x[k] * x[k], x[k + 1] * x[k + 1]));
+                if (at.turned_b) turned = fmaxf(turned, q);
+                else rest = fmaxf(rest, fmaxf(y[k] * y[k], y[k + 1] * y[k + 1]));
             }
-            m *= f2;
+        } else if (at.turned_a) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) turned = fmaxf(turned, fmaf(x[k], x[k], y[k] * y[k]));
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, fmaxf(x[k] * x[k], y[k] * y[k]));
+            for (int k = 0; k < 8; ++k) rest = fmaxf(rest, fmaxf(x[k] * x[k], y[k] * y[k]));
         }
-        square = fmaxf(square, m);
+        square = fmaxf(square, fmaxf(turned * f2, rest));
     };
-    const int T = blockDim.x;
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-        const int e = threadIdx.x + k * T;
-        if (e < all) load(e, ka[k], kb[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-        const int e = threadIdx.x + k * T;
-        if (e < all) reach(e, ka[k], kb[k]);
-    }
-    for (int e = threadIdx.x + kKept * T; e < all; e += T) {
+    for (int k = 0; k < kKept; ++k)
+        if (tid + k * T < all) reach(tid + k * T, ka[k], kb[k]);
+    for (int e = tid + kKept * T; e < all; e += T) {
         uint4 u, w;
         load(e, u, w);
         reach(e, u, w);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) square = fmaxf(square, __shfl_xor_sync(0xffffffffu, square, o));
-    if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = square;
-    __syncthreads();   // (every thread has read `before` too)
-    square = most[0];
-    for (int w = 1; w < T / 32; ++w) square = fmaxf(square, most[w]);
+    if (!WARP) {
+        if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = square;
+        __syncthreads();   // (every thread has read `before` too)
+        for (int w = 0; w < T / 32; ++w) square = fmaxf(square, most[w]);
+    }
     const float now = hi > lo ? fmaxf(before, q8_scale(square)) : before;
     const float inv = 1.f / now;
-    auto store = [&](int e, const uint4& u, const uint4& w) {
-        const int i = e / a.tasks, j = e - i * a.tasks;
+    auto store = [&](int e, const uint4& u, const uint4& w, const Angles& g) {
+        const int i = (int)a.by_tasks((unsigned)e);
+        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, e - i * a.tasks);
         float x[8], y[8];
         unpack8(u, x);
         unpack8(w, y);
-        TaskAt at{16 * j, 16 * j + 8, false};
-        if (turns) {
-            at = task_at(a.turn, j);
-            if (at.turned) {
-                Angles g;
-                const int new_row = lo - len + i;
-                angles_of(a.turn, j,
-                          a.positions != nullptr ? a.positions[b * a.position_stride + new_row]
-                                                 : len + new_row,
-                          g);
-                turn_task(INTERLEAVED, g, x, y);
-            }
-        }
+        if (at.turned_a || at.turned_b) turn_task<INTERLEAVED>(at, g, x, y);
         store_codes(row_of(page, row + (lo - first) + i), at, x, y, inv);
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
-        const int e = threadIdx.x + k * T;
-        if (e < all) store(e, ka[k], kb[k]);
+        const int e = tid + k * T;
+        if (e >= all) break;
+        if (k > 0 && rot > 0) angles(e, first_angles);
+        store(e, ka[k], kb[k], first_angles);
     }
-    for (int e = threadIdx.x + kKept * T; e < all; e += T) {
+    for (int e = tid + kKept * T; e < all; e += T) {
         uint4 u, w;
         load(e, u, w);
-        store(e, u, w);
+        if (rot > 0) angles(e, first_angles);
+        store(e, u, w, first_angles);
     }
     // rows that lay in the block before
     if (lo > first && (now != before || takes_over)) {
         const uint4* s = reinterpret_cast<const uint4*>(row_of(old_page, row));
         uint4* t = reinterpret_cast<uint4*>(row_of(page, row));
         const float ratio = before * inv;
-        for (int e = threadIdx.x; e < (lo - first) * a.tasks; e += T) {
+        for (int e = tid; e < (lo - first) * a.tasks; e += T) {
             const uint4 u = s[e];
             uint32_t r[4] = {u.x, u.y, u.z, u.w};
             if (now != before) {
@@ -272,7 +274,7 @@ __global__ void append_q8_kernel(const AppendArgs a) {
             t[e] = make_uint4(r[0], r[1], r[2], r[3]);
         }
     }
-    if (threadIdx.x == 0 && (now != before || takes_over)) *scale_of(page, block) = now;
+    if (tid == 0 && (now != before || takes_over)) *scale_of(page, block) = now;
 }
 
 // -------------------------------------------------------------- read ----
@@ -280,6 +282,7 @@ __global__ void append_q8_kernel(const AppendArgs a) {
 struct ReadArgs {
     Q8Cache c;
     int tasks;
+    FastDiv by_hkv;
     const int* cu;             // [batch + 1]
     int total;
     uint4* out[2];             // [total, hkv, d] bf16
@@ -287,54 +290,61 @@ struct ReadArgs {
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTokens = 16;   // of a CTA, all heads
-constexpr int kReadFlight = 4;    // granules a thread has in flight
+constexpr int kReadFlight = 8;    // granules (8 codes) a thread has in flight
 
-// CTA (tokens of a sequence, keys or values, batch entry): 16 codes in, 32 bytes
-// out, a granule a thread, four in flight.
+// CTA (tokens of a sequence, keys or values, batch entry).  The tokens' pages are looked
+// up once, by a thread each; then granules of 8 codes in, 16 bytes out, a warp 256 and
+// 512 bytes in a row, eight granules a thread in flight.
 __global__ void __launch_bounds__(kReadThreads) read_q8_kernel(const ReadArgs a) {
+    __shared__ int page_of[kReadTokens], row_of[kReadTokens], block_of[kReadTokens];
     dependents_may_start();
     wait_for_previous();
     const Q8Cache& c = a.c;
-    const int b = blockIdx.z, kind = blockIdx.y;
+    const int b = blockIdx.z, kind = blockIdx.y, t0 = blockIdx.x * kReadTokens;
     const int q0 = min(max(a.cu[b], 0), a.total);
     const int len = min(max(a.cu[b + 1], q0), a.total) - q0;
-    const int t0 = blockIdx.x * kReadTokens, count = min(kReadTokens, len - t0);
+    const int count = min(kReadTokens, len - t0);
     if (count <= 0) return;
-    const int per = c.hkv * a.tasks;   // granules of a token
-    const int* table = c.table + (size_t)b * c.max_pages;
-    for (int e0 = threadIdx.x; e0 < count * per; e0 += kReadFlight * kReadThreads) {
-        uint4 u[kReadFlight];
+    if (threadIdx.x < kReadTokens) {
+        int page = -1, row = 0;
+        if (!key_page(c.pages, b, (long long)t0 + threadIdx.x, page, row)) page = -1;
+        page_of[threadIdx.x] = page;
+        row_of[threadIdx.x] = row;
+        block_of[threadIdx.x] = (int)c.by_block((unsigned)row);
+    }
+    __syncthreads();
+    const int G = 2 * a.tasks, slots = kReadThreads / G;   // granules of a row, rows at a time
+    const int slot = threadIdx.x / G, j = threadIdx.x - slot * G;
+    if (slot >= slots) return;
+    const uint2* const codes = reinterpret_cast<const uint2*>(kind == 0 ? c.codes[0] : c.codes[1]) + j;
+    const float* const scales = kind == 0 ? c.scales[0] : c.scales[1];
+    uint4* const out = (kind == 0 ? a.out[0] : a.out[1]) + (size_t)(q0 + t0) * c.hkv * G + j;
+    const int rows = count * c.hkv;   // (token, head), the head fastest
+    for (int r0 = slot; r0 < rows; r0 += kReadFlight * slots) {
+        uint2 u[kReadFlight];
         float s[kReadFlight];
 #pragma unroll
         for (int k = 0; k < kReadFlight; ++k) {
-            const int e = e0 + k * kReadThreads;
-            u[k] = make_uint4(0, 0, 0, 0);
+            const int r = r0 + k * slots;
+            u[k] = make_uint2(0, 0);
             s[k] = 0.f;
-            if (e >= count * per) continue;
-            const int t = e / per, r = e - t * per, h = r / a.tasks, j = r - h * a.tasks;
-            int page, row;
-            if (!key_page(table, c.max_pages, c.page_size, c.num_pages, (long long)t0 + t, page, row))
-                continue;
-            const size_t head = (size_t)page * c.hkv + h;
-            u[k] = reinterpret_cast<const uint4*>(c.codes[kind])[(head * c.page_size + row) * a.tasks + j];
-            s[k] = c.scales[kind][head * c.blocks + row / c.block];
+            if (r >= rows) continue;
+            const int t = (int)a.by_hkv((unsigned)r), page = page_of[t];
+            if (page < 0) continue;
+            const size_t head = (size_t)page * c.hkv + (r - t * c.hkv);
+            u[k] = codes[(head * c.pages.page_size + row_of[t]) * G];
+            s[k] = scales[head * c.blocks + block_of[t]];
         }
 #pragma unroll
         for (int k = 0; k < kReadFlight; ++k) {
-            const int e = e0 + k * kReadThreads;
-            if (e >= count * per) continue;
-            const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-            uint32_t o[8];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                float x[4];
-                q8_floats(w[m], x);
-                o[2 * m] = pack_bf16x2(x[0] * s[k], x[1] * s[k]);
-                o[2 * m + 1] = pack_bf16x2(x[2] * s[k], x[3] * s[k]);
-            }
-            uint4* to = a.out[kind] + ((size_t)(q0 + t0) * per + e) * 2;
-            to[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            to[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            const int r = r0 + k * slots;
+            if (r >= rows) continue;
+            float x[4], y[4];
+            q8_floats(u[k].x, x);
+            q8_floats(u[k].y, y);
+            out[(size_t)r * G] =
+                make_uint4(pack_bf16x2(x[0] * s[k], x[1] * s[k]), pack_bf16x2(x[2] * s[k], x[3] * s[k]),
+                           pack_bf16x2(y[0] * s[k], y[1] * s[k]), pack_bf16x2(y[2] * s[k], y[3] * s[k]));
         }
     }
 }
@@ -343,18 +353,19 @@ __global__ void __launch_bounds__(kReadThreads) read_q8_kernel(const ReadArgs a)
 
 // Checks of an 8-bit cache and its table.
 fa_status check_cache(const Q8Cache& c, int head_dim) {
-    if (c.num_pages < 0 || c.hkv < 0 || c.page_size < 0 || c.max_pages < 0 || c.hkv > 16000)
+    const PageTable& t = c.pages;
+    if (t.num_pages < 0 || c.hkv < 0 || t.page_size < 0 || t.max_pages < 0 || c.hkv > 16000)
         return FA_ERR_INVALID_ARG;
-    if (head_dim <= 0 || head_dim % 16 != 0) return FA_ERR_UNSUPPORTED;
-    if (c.num_pages == 0 || c.hkv == 0 || c.page_size == 0) return FA_OK;
-    if (c.block <= 0 || c.page_size % c.block != 0) return FA_ERR_INVALID_ARG;
+    if (head_dim <= 0 || head_dim % 16 != 0 || head_dim > 2048) return FA_ERR_UNSUPPORTED;
+    if (t.num_pages == 0 || c.hkv == 0 || t.page_size == 0) return FA_OK;
+    if (c.block <= 0 || t.page_size % c.block != 0) return FA_ERR_INVALID_ARG;
     for (int i = 0; i < 2; ++i) {
         if (!c.codes[i] || !c.scales[i]) return FA_ERR_INVALID_ARG;
         if (!is_aligned(c.codes[i], 16) || !is_aligned(c.scales[i], 4)) return FA_ERR_MISALIGNED;
     }
-    if (c.max_pages > 0 && !c.table) return FA_ERR_INVALID_ARG;
-    if (!is_aligned(c.table, 4)) return FA_ERR_MISALIGNED;
-    if ((long long)c.max_pages * c.page_size >= (1ll << 31) ||
+    if (t.max_pages > 0 && !t.table) return FA_ERR_INVALID_ARG;
+    if (!is_aligned(t.table, 4)) return FA_ERR_MISALIGNED;
+    if ((long long)t.max_pages * t.page_size >= (1ll << 31) ||
         (long long)c.block * (head_dim / 16) >= (1ll << 30))
         return FA_ERR_INVALID_ARG;
     return FA_OK;
@@ -367,13 +378,11 @@ Q8Cache cache_of(void* k, void* v, float* ks, float* vs, int num_pages, int hkv,
     c.codes[1] = static_cast<uint8_t*>(v);
     c.scales[0] = ks;
     c.scales[1] = vs;
-    c.num_pages = num_pages;
+    c.pages = PageTable{table, max_pages, page_size, num_pages, fast_div(page_size > 0 ? page_size : 1)};
     c.hkv = hkv;
-    c.page_size = page_size;
     c.block = block;
     c.blocks = block > 0 ? page_size / block : 0;
-    c.table = table;
-    c.max_pages = max_pages;
+    c.by_block = fast_div(block > 0 ? block : 1);
     return c;
 }
 
@@ -416,6 +425,9 @@ fa_status fa_cache_append_q8(void* k_cache, void* v_cache, float* k_scale, float
     // (keys of a sequence, new ones among them, are counted in 32 bits)
     if (n >= (1 << 30)) return FA_ERR_INVALID_ARG;
     a.tasks = head_dim / 16;
+    a.by_tasks = fast_div(a.tasks);
+    a.by_hq = fast_div(a.hq > 0 ? a.hq : 1);
+    if ((double)n * a.hq * a.tasks >= 2147483648.0) return FA_ERR_INVALID_ARG;
     if (n > 0) {
         const void* src[3] = {k_new, v_new, a.hq > 0 ? turn->q : nullptr};
         const long long* ss[3] = {k_strides, v_strides, a.hq > 0 ? turn->q_strides : nullptr};
@@ -442,12 +454,21 @@ fa_status fa_cache_append_q8(void* k_cache, void* v_cache, float* k_scale, float
     const long long x = (long long)a.units + (copies ? a.c.blocks : 0);
     if (x >= (1ll << 31)) return FA_ERR_INVALID_ARG;
     if ((st = sm103_or_status()) != FA_OK) return st;
-    const int rows = n < block ? n : block;
-    const int threads = (long long)rows * a.tasks > 128 * kKept ? 256 : 128;
-    const dim3 grid((unsigned)x, (unsigned)(2 * hkv + (a.hq > 0 && n > 0 ? 1 : 0)), (unsigned)batch);
-    const cudaError_t e =
-        launch_dependent(a.turn.interleaved ? append_q8_kernel<true> : append_q8_kernel<false>, grid,
-                         dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), a);
+    // a warp for a unit where it keeps all of its rows
+    const long long unit_tasks = (long long)(n < block ? n : block) * a.tasks;
+    const bool warp = unit_tasks <= 32 * kKept;
+    const int threads = warp || unit_tasks <= 128 * kKept ? 128 : 256;
+    a.kv_ctas = warp ? (2 * hkv + 3) / 4 : 2 * hkv;
+    long long q_ctas = 0;
+    if (a.hq > 0 && n > 0) {
+        q_ctas = ((long long)n * a.hq * a.tasks + threads * x - 1) / (threads * x);
+        if (q_ctas > 4096) q_ctas = 4096;
+    }
+    const dim3 grid((unsigned)x, (unsigned)(a.kv_ctas + q_ctas), (unsigned)batch);
+    void (*kernel)(AppendArgs) =
+        a.turn.interleaved ? (warp ? append_q8_kernel<true, true> : append_q8_kernel<true, false>)
+                           : (warp ? append_q8_kernel<false, true> : append_q8_kernel<false, false>);
+    const cudaError_t e = launch_dependent(kernel, grid, dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -468,10 +489,11 @@ fa_status fa_cache_read_q8(const void* k_cache, const void* v_cache, const float
     if (!is_aligned(cu_seqlens, 4) || !is_aligned(k_out, 16) || !is_aligned(v_out, 16))
         return FA_ERR_MISALIGNED;
     if (num_pages == 0 || page_size == 0) {   // (no page: every key reads as zeros)
-        a.c.max_pages = 0;
-        a.c.page_size = a.c.block = 1;
+        a.c.pages.max_pages = 0;
+        a.c.block = 1;
     }
     a.tasks = head_dim / 16;
+    a.by_hkv = fast_div(hkv);
     a.cu = cu_seqlens;
     a.total = total;
     a.out[0] = static_cast<uint4*>(k_out);

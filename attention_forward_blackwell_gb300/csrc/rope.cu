@@ -39,31 +39,35 @@ struct RopeArgs {
     long long position_stride;
     const int* lens;           // (positions null) at lens[b] + i
     // cache
-    int num_pages, hkv, page_size, max_pages;
-    const int* table;
+    PageTable pages;
+    int hkv;
     const int* copies;         // [batch, 3] or nullptr
     int row_ctas;              // CTAs along x that turn rows; the rest copy
+    int by_token;              // neighbouring threads take neighbouring tokens, not heads
+    FastDiv by_tasks, by_inner;   // by tasks, and by what goes round next: groups or tokens
 };
 
-// CTA (rows of an entry, batch entry), threads over (token, group of heads,
-// task), the task fastest: 8 threads read the halves of a row of 128 elements.
+// CTA (rows of an entry, batch entry), threads over (token, group of heads, task), the
+// task fastest -- 8 threads read the halves of a row of 128 elements -- then what
+// lies next in memory, the heads of a token or the tokens of a head.
 template <int HEADS, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, HEADS > 1 ? 7 : 12) rope_kernel(const RopeArgs a) {
     dependents_may_start();
     wait_for_previous();
-    const int b = blockIdx.y;
+    const int b = blockIdx.y, page_size = a.pages.page_size;
     if ((int)blockIdx.x >= a.row_ctas) {   // rows [0, c) of a page that reserve replaced
         const int src = a.copies[3 * b], dst = a.copies[3 * b + 1];
-        const int c = min(a.copies[3 * b + 2], a.page_size);
-        if ((unsigned)src >= (unsigned)a.num_pages || (unsigned)dst >= (unsigned)a.num_pages || src == dst)
+        const int c = min(a.copies[3 * b + 2], page_size);
+        if ((unsigned)src >= (unsigned)a.pages.num_pages || (unsigned)dst >= (unsigned)a.pages.num_pages ||
+            src == dst)
             return;
         const int per = a.tasks * 2, part = c * per;      // granules of a row, of a head
-        const size_t page = (size_t)a.hkv * a.page_size * per;
+        const size_t page = (size_t)a.hkv * page_size * per;
         const long long step = (long long)(gridDim.x - a.row_ctas) * kThreads;
         for (long long e = (long long)(blockIdx.x - a.row_ctas) * kThreads + threadIdx.x;
              e < (long long)part * a.hkv; e += step) {
             const int h = (int)(e / part);
-            const size_t at = (size_t)h * a.page_size * per + (size_t)(e - (long long)h * part);
+            const size_t at = (size_t)h * page_size * per + (size_t)(e - (long long)h * part);
             const uint4 k = a.rows[0].pages[src * page + at], v = a.rows[1].pages[src * page + at];
             a.rows[0].pages[dst * page + at] = k;
             a.rows[1].pages[dst * page + at] = v;
@@ -72,13 +76,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
     }
     const int n = min(a.n_new != nullptr ? a.n_new[b] : a.n, a.n);
     const int groups = (a.heads + HEADS - 1) / HEADS;
-    const int per_token = groups * a.tasks;
-    const long long x = (long long)blockIdx.x * kThreads + threadIdx.x;
-    const long long token = x / per_token;
-    if (token >= n) return;
-    const int i = (int)token, rest = (int)(x - token * per_token);
-    const int g = rest / a.tasks, j = rest - g * a.tasks;
-    const TaskAt at = task_at(a.turn, j);
+    const unsigned x = blockIdx.x * kThreads + threadIdx.x;   // (below 2^31: the host sees to it)
+    const unsigned row = a.by_tasks(x), outer = a.by_inner(row);
+    const int j = (int)(x - row * (unsigned)a.tasks);
+    const int inner = (int)(row - outer * (unsigned)(a.by_token ? a.n : groups));
+    const int i = a.by_token ? inner : (int)outer, g = a.by_token ? (int)outer : inner;
+    if (i >= n || g >= groups) return;
+    const TaskAt at = task_at<INTERLEAVED>(a.turn.rot, a.tasks, j);
     const int ga = at.a >> 3, gb = at.b >> 3;   // granules of a row
     uint4 xa[HEADS], xb[HEADS];
     uint4* to[HEADS];
@@ -97,21 +101,20 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
         const uint4* from = r.src + b * r.ss[0] + h * r.ss[1] + i * r.ss[2];
         xa[u] = from[ga];
         xb[u] = from[gb];
-        turned[u] = at.turned && r.turned;
+        turned[u] = (at.turned_a || at.turned_b) && r.turned;
         if (r.dst != nullptr) {
             to[u] = r.dst + b * r.ds[0] + h * r.ds[1] + i * r.ds[2];
         } else {
             int page, row;
-            if (key_page(a.table + (size_t)b * a.max_pages, a.max_pages, a.page_size, a.num_pages,
-                         (long long)len + i, page, row))
-                to[u] = r.pages + (((size_t)page * a.hkv + h) * a.page_size + row) * (2 * a.tasks);
+            if (key_page(a.pages, b, (long long)len + i, page, row))
+                to[u] = r.pages + (((size_t)page * a.hkv + h) * page_size + row) * (2 * a.tasks);
         }
     }
     Angles angles;
-    if (at.turned)
-        angles_of(a.turn, j, a.positions != nullptr ? a.positions[b * a.position_stride + i]
-                                                    : (int)((unsigned)len + i),
-                  angles);
+    if (at.turned_a || at.turned_b)
+        angles_of<INTERLEAVED>(a.turn, at, a.positions != nullptr ? a.positions[b * a.position_stride + i]
+                                                               : (int)((unsigned)len + i),
+                               angles);
 #pragma unroll
     for (int u = 0; u < HEADS; ++u) {
         if (to[u] == nullptr) continue;
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
             float p[8], q[8];
             unpack8(xa[u], p);
             unpack8(xb[u], q);
-            turn_task(INTERLEAVED, angles, p, q);
+            turn_task<INTERLEAVED>(at, angles, p, q);
             xa[u] = pack8(p);
             xb[u] = pack8(q);
         }
@@ -147,12 +150,15 @@ fa_status launch_rope(RopeArgs& a, int batch, cudaStream_t s) {
     const long long ctas = (rows * ((a.heads + per - 1) / per) + kThreads - 1) / kThreads;
     long long copy_ctas = 0;
     if (a.copies != nullptr) {
-        copy_ctas = ((long long)a.page_size * a.tasks * 2 * a.hkv + 4 * kThreads - 1) / (4 * kThreads);
+        copy_ctas = ((long long)a.pages.page_size * a.tasks * 2 * a.hkv + 4 * kThreads - 1) / (4 * kThreads);
         if (copy_ctas > 64) copy_ctas = 64;
     }
-    if (ctas + copy_ctas >= (1ll << 31)) return FA_ERR_INVALID_ARG;
+    if (ctas * kThreads >= (1ll << 31)) return FA_ERR_INVALID_ARG;   // (rows of one entry, 16 elements each)
     if (ctas + copy_ctas == 0) return FA_OK;
     a.row_ctas = (int)ctas;
+    a.by_token = a.n > 0 && a.rows[0].ss[2] < a.rows[0].ss[1] ? 1 : 0;
+    a.by_tasks = fast_div(a.tasks);
+    a.by_inner = fast_div(a.by_token ? a.n : (a.heads + per - 1) / per);
     void (*kernel)(RopeArgs) =
         a.turn.interleaved ? (many ? rope_kernel<kHeads, true> : rope_kernel<1, true>)
                            : (many ? rope_kernel<kHeads, false> : rope_kernel<1, false>);
@@ -267,11 +273,10 @@ fa_status fa_cache_append_rope(void* k_cache, void* v_cache, int num_pages, int 
     a.positions = turn->positions;
     a.position_stride = turn->position_stride;
     a.lens = seqlens;
-    a.num_pages = num_pages;
     a.hkv = hkv;
-    a.page_size = page_size;
-    a.max_pages = num_pages > 0 ? max_pages : 0;   // (the table may be absent then)
-    a.table = block_table;
+    // (without pages the table may be absent)
+    a.pages = PageTable{block_table, num_pages > 0 ? max_pages : 0, page_size, num_pages,
+                        fast_div(page_size > 0 ? page_size : 1)};
     a.copies = num_pages > 0 ? copies : nullptr;
     if ((st = sm103_or_status()) != FA_OK) return st;
     return launch_rope(a, batch, reinterpret_cast<cudaStream_t>(stream));

@@ -13,6 +13,7 @@
 // instructions an angle, with no range reduction and no branch.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -54,30 +55,50 @@ struct Turn {
     float factor, sign;
 };
 
-// A row is handled 16 elements a time, by tasks j < head_dim / 16: two granules
-// of 8 elements (16 bytes of bf16) that hold 8 whole pairs of the turned part, or
-// 16 elements of the rest.
+// A row is handled 16 elements a time, by tasks j < head_dim / 16: two granules of
+// 8 elements (16 bytes of bf16), of which the tasks of neighbouring lanes take
+// neighbouring ones, so that every load and store of a warp covers whole sectors
+// (with the granules of a task side by side, each instruction left every other 16 bytes to
+// the next: prompts with interleaved pairs 20 us for 15 of their bytes).  Pairs of the
+// halves lie in both granules at the same place, interleaved ones within a granule.
 struct TaskAt {
-    int a, b;      // first elements of the granules
-    bool turned;
+    int a, b;               // first elements of the granules
+    bool turned_a, turned_b;
+    int pair_a, pair_b;     // first pair: of both granules (8 of them), or of each (4)
 };
-__device__ __forceinline__ TaskAt task_at(const Turn& t, int j) {
-    TaskAt at{16 * j, 16 * j + 8, 16 * j < t.rot};
-    if (at.turned && !t.interleaved) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ TaskAt task_at(int rot, int tasks, int j) {
+    TaskAt at;
+    if (INTERLEAVED) {
         at.a = 8 * j;
-        at.b = 8 * j + (t.rot >> 1);
+        at.b = 8 * (j + tasks);
+        at.turned_a = at.a < rot;
+        at.turned_b = at.b < rot;
+        at.pair_a = 4 * j;
+        at.pair_b = 4 * (j + tasks);
+    } else {
+        const bool in = 16 * j < rot;   // (else the rest of the row, which has its own halves)
+        const int first = in ? 0 : rot, len = in ? rot : 16 * tasks - rot;
+        at.a = first + 8 * j - (first >> 1);
+        at.b = at.a + (len >> 1);
+        at.turned_a = at.turned_b = in;
+        at.pair_a = at.pair_b = 8 * j;
     }
     return at;
 }
 
-// Sines and cosines of task j's 8 pairs at a position.
+// Sines and cosines of a task's 8 pairs at a position.
 struct Angles {
     float s[8], c[8];
 };
-__device__ __forceinline__ void angles_of(const Turn& t, int j, int position, Angles& g) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ void angles_of(const Turn& t, const TaskAt& at, int position, Angles& g) {
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-        const longlong2 F = *reinterpret_cast<const longlong2*>(t.freqs + 8 * j + e);
+        const bool second = INTERLEAVED && e >= 4;
+        if (second ? !at.turned_b : !at.turned_a) continue;
+        const long long* from = t.freqs + (second ? at.pair_b + e - 4 : at.pair_a + e);
+        const longlong2 F = *reinterpret_cast<const longlong2*>(from);
         turn_sincos(position, F.x, g.s[e], g.c[e]);
         turn_sincos(position, F.y, g.s[e + 1], g.c[e + 1]);
     }
@@ -109,28 +130,33 @@ __device__ __forceinline__ void turn_pair(float& x, float& y, float s, float c) 
     y = y * c + x * s;
     x = a;
 }
-__device__ __forceinline__ void turn_task(bool interleaved, const Angles& g, float (&x)[8], float (&y)[8]) {
-    if (interleaved) {
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_task(const TaskAt& at, const Angles& g, float (&x)[8], float (&y)[8]) {
+    if (INTERLEAVED) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            turn_pair(x[2 * e], x[2 * e + 1], g.s[e], g.c[e]);
-            turn_pair(y[2 * e], y[2 * e + 1], g.s[4 + e], g.c[4 + e]);
+            if (at.turned_a) turn_pair(x[2 * e], x[2 * e + 1], g.s[e], g.c[e]);
+            if (at.turned_b) turn_pair(y[2 * e], y[2 * e + 1], g.s[4 + e], g.c[4 + e]);
         }
-    } else {
+    } else if (at.turned_a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) turn_pair(x[e], y[e], g.s[e], g.c[e]);
     }
 }
 
-// Place of key `pos` in a paged cache of `heads` heads: its page and row in it;
-// false where it has no page.
-__device__ __forceinline__ bool key_page(const int* table, int max_pages, int page_size, int num_pages,
-                                         long long pos, int& page, int& row) {
-    if (pos < 0 || pos >= (long long)max_pages * page_size) return false;   // (below 2^31)
-    const unsigned p = (unsigned)pos, j = p / (unsigned)page_size;
-    page = table[j];
-    row = (int)(p - j * (unsigned)page_size);
-    return (unsigned)page < (unsigned)num_pages;
+// Place of key `pos` in a paged cache: its page and row in it; false where it has no
+// page.
+struct PageTable {
+    const int* table;          // [batch, max_pages]
+    int max_pages, page_size, num_pages;
+    FastDiv by_page;           // by page_size
+};
+__device__ __forceinline__ bool key_page(const PageTable& t, int b, long long pos, int& page, int& row) {
+    if (pos < 0 || pos >= (long long)t.max_pages * t.page_size) return false;   // (below 2^31)
+    const unsigned p = (unsigned)pos, j = t.by_page(p);
+    page = t.table[(size_t)b * t.max_pages + j];
+    row = (int)(p - j * (unsigned)t.page_size);
+    return (unsigned)page < (unsigned)t.num_pages;
 }
 
 // ------------------------------------------------------------------ host ----
@@ -138,14 +164,23 @@ __device__ __forceinline__ bool key_page(const int* table, int max_pages, int pa
 inline bool is_aligned(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
-// The kernels of this library are compiled for sm_103 only.
+// The kernels of this library are compiled for sm_103 only.  (Asked of the runtime once
+// per device: the calls here take two microseconds.)
 inline fa_status sm103_or_status() {
+    constexpr int kDevices = 64;
+    static std::atomic<signed char> known[kDevices];   // 0: not asked yet, 1: it is, -1: it is not
     int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return FA_ERR_CUDA;
-    return major == 10 && minor == 3 ? FA_OK : FA_ERR_UNSUPPORTED;
+    if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+    const bool keep = dev >= 0 && dev < kDevices;
+    signed char is = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (is == 0) {
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            return FA_ERR_CUDA;
+        is = major == 10 && minor == 3 ? 1 : -1;
+        if (keep) known[dev].store(is, std::memory_order_relaxed);
+    }
+    return is > 0 ? FA_OK : FA_ERR_UNSUPPORTED;
 }
 // Frequencies and factor of a call that turns rows (freqs NULL: none).
 inline fa_status check_turn(const long long* freqs, int rot, int head_dim, float factor) {

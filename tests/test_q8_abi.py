@@ -121,7 +121,7 @@ def test_decode_q8(fa):
         assert call(fn, **{f"a{i}": -1}) == 1
     assert call(fn, a9=3) == 1 and call(fn, a10=17) == 1 and call(fn, a16=5) == 1 and call(fn, a18=0.0) == 1
     assert call(fn, a13=1 << 20, a14=1 << 12) == 1
-    assert call(fn, a15=1 << 29, a14=16) == 1                      # rows of the cache past 2^32
+    assert call(fn, a15=1 << 30) == 1                              # planes of the cache past 2^31
     assert call(fn, a17=96) == 2 and call(fn, a17=512) == 2
     assert call(fn, a0=P_ODD) == 3 and call(fn, a2=P_ODD) == 3 and call(fn, a3=P_MIS4) == 3
     assert call(fn, a22=P_MIS4) == 3 and call(fn, a11=P_MIS4) == 3
