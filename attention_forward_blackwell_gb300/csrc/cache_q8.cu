@@ -46,8 +46,9 @@ struct AppendArgs {
     int kv_ctas;               // CTAs along y that append; the rest turn queries
 };
 
-// Granules of a row that a thread keeps between the two passes over a block.
-constexpr int kKept = 4;
+// Tasks that a thread keeps between the two passes over a block (a unit's in a warp, in
+// a CTA).
+constexpr int kKeptWarp = 4, kKeptCta = 4;
 
 // Codes of a task's two granules.
 __device__ __forceinline__ void store_codes(uint8_t* row, const TaskAt& at, const float (&x)[8],
@@ -95,12 +96,13 @@ __device__ void append_queries(const AppendArgs& a, int b, int len, int n) {
 // one, four a CTA (few rows), else a CTA.  CTA (block, heads and keys or values -- past
 // kv_ctas: queries --, batch entry).  Two passes over the new rows of a block: their
 // reach, then their codes; what a thread has of them stays in registers in between,
-// kKept tasks, which covers blocks of 64 keys of 128 elements, and is read again past
-// that (from L1 or L2).  A block has one writer, so nothing is atomic.  Bound by the
+// which covers blocks of 64 keys of 128 elements, and is read again past that (from L1
+// or L2).  A block has one writer, so nothing is atomic.  Bound by the
 // bytes, 3 for an element, and for single tokens by a chain of loads: length, page,
 // scale; the rows, and the angles that need only the length, come beside it.
 template <bool INTERLEAVED, bool WARP>
 __global__ void append_q8_kernel(const AppendArgs a) {
+    constexpr int kKept = WARP ? kKeptWarp : kKeptCta;
     __shared__ float most[8];
     dependents_may_start();
     wait_for_previous();
@@ -290,11 +292,11 @@ struct ReadArgs {
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTokens = 16;   // of a CTA, all heads
-constexpr int kReadFlight = 8;    // granules (8 codes) a thread has in flight
+constexpr int kReadFlight = 4;    // granules (8 codes) a thread has in flight
 
 // CTA (tokens of a sequence, keys or values, batch entry).  The tokens' pages are looked
 // up once, by a thread each; then granules of 8 codes in, 16 bytes out, a warp 256 and
-// 512 bytes in a row, eight granules a thread in flight.
+// 512 bytes in a row, four granules a thread in flight.
 __global__ void __launch_bounds__(kReadThreads) read_q8_kernel(const ReadArgs a) {
     __shared__ int page_of[kReadTokens], row_of[kReadTokens], block_of[kReadTokens];
     dependents_may_start();
@@ -342,9 +344,9 @@ __global__ void __launch_bounds__(kReadThreads) read_q8_kernel(const ReadArgs a)
             float x[4], y[4];
             q8_floats(u[k].x, x);
             q8_floats(u[k].y, y);
-            out[(size_t)r * G] =
-                make_uint4(pack_bf16x2(x[0] * s[k], x[1] * s[k]), pack_bf16x2(x[2] * s[k], x[3] * s[k]),
-                           pack_bf16x2(y[0] * s[k], y[1] * s[k]), pack_bf16x2(y[2] * s[k], y[3] * s[k]));
+            __stcs(out + (size_t)r * G,
+                   make_uint4(pack_bf16x2(x[0] * s[k], x[1] * s[k]), pack_bf16x2(x[2] * s[k], x[3] * s[k]),
+                              pack_bf16x2(y[0] * s[k], y[1] * s[k]), pack_bf16x2(y[2] * s[k], y[3] * s[k])));
         }
     }
 }
@@ -456,8 +458,8 @@ fa_status fa_cache_append_q8(void* k_cache, void* v_cache, float* k_scale, float
     if ((st = sm103_or_status()) != FA_OK) return st;
     // a warp for a unit where it keeps all of its rows
     const long long unit_tasks = (long long)(n < block ? n : block) * a.tasks;
-    const bool warp = unit_tasks <= 32 * kKept;
-    const int threads = warp || unit_tasks <= 128 * kKept ? 128 : 256;
+    const bool warp = unit_tasks <= 32 * kKeptWarp;
+    const int threads = warp || unit_tasks <= 128 * kKeptCta ? 128 : 256;
     a.kv_ctas = warp ? (2 * hkv + 3) / 4 : 2 * hkv;
     long long q_ctas = 0;
     if (a.hq > 0 && n > 0) {

@@ -15,7 +15,7 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;
 constexpr int kStreams = 3;
 
 // Rows of one kind: [batch, heads, n, d] with strides in granules; dst null: to
@@ -51,7 +51,7 @@ struct RopeArgs {
 // task fastest -- 8 threads read the halves of a row of 128 elements -- then what
 // lies next in memory, the heads of a token or the tokens of a head.
 template <int HEADS, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, HEADS > 1 ? 7 : 12) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, HEADS > 1 ? 14 : 24) rope_kernel(const RopeArgs a) {
     dependents_may_start();
     wait_for_previous();
     const int b = blockIdx.y, page_size = a.pages.page_size;
@@ -99,8 +99,8 @@ __global__ void __launch_bounds__(kThreads, HEADS > 1 ? 7 : 12) rope_kernel(cons
         while (s < kStreams - 1 && h >= a.rows[s].heads) h -= a.rows[s++].heads;
         const Rows& r = a.rows[s];
         const uint4* from = r.src + b * r.ss[0] + h * r.ss[1] + i * r.ss[2];
-        xa[u] = from[ga];
-        xb[u] = from[gb];
+        xa[u] = HEADS > 1 ? __ldcs(from + ga) : from[ga];
+        xb[u] = HEADS > 1 ? __ldcs(from + gb) : from[gb];
         turned[u] = (at.turned_a || at.turned_b) && r.turned;
         if (r.dst != nullptr) {
             to[u] = r.dst + b * r.ds[0] + h * r.ds[1] + i * r.ds[2];
@@ -126,8 +126,13 @@ __global__ void __launch_bounds__(kThreads, HEADS > 1 ? 7 : 12) rope_kernel(cons
             xa[u] = pack8(p);
             xb[u] = pack8(q);
         }
-        to[u][ga] = xa[u];
-        to[u][gb] = xb[u];
+        if (HEADS > 1) {
+            __stcs(to[u] + ga, xa[u]);
+            __stcs(to[u] + gb, xb[u]);
+        } else {
+            to[u][ga] = xa[u];
+            to[u][gb] = xb[u];
+        }
     }
 }
 
