@@ -52,6 +52,8 @@
 // and the page numbers of a slice are fetched while the one before is issued.
 // What a box brings beside keys that some row sees may be anything: scores are
 // replaced, values zeroed, at the borders alone.
+#include <atomic>
+
 #include "common.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -403,6 +405,29 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     const uint32_t scale_at = a.flat ? 0 : kg * 4;
     const uint32_t scale_step = a.flat ? 0 : 32;   // eight keys on
 
+    // This lane's words of query row nr 8 + g of a tile: of each 64 dims the 16 from
+    // 16 t on (zeros where there is no such row).
+    auto load_query = [&](int b, int hkv, int rbase, int nr, uint32_t (&w)[D / 64][8]) {
+        const int pr = rbase + nr * 8 + g;
+        const bool real = pr < a.rows;
+        const int h = hkv * a.group + pr / a.Sq;
+        const uint4* q = reinterpret_cast<const uint4*>(
+            a.q + (real ? (((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq) * D : 0) + t * 16);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (real) {
+                x = q[c * 8];
+                y = q[c * 8 + 1];
+            }
+            w[c][0] = x.x, w[c][1] = x.y, w[c][2] = x.z, w[c][3] = x.w;
+            w[c][4] = y.x, w[c][5] = y.y, w[c][6] = y.z, w[c][7] = y.w;
+        }
+    };
+    // (of a tile of eight rows, the next segment's come while this one is merged)
+    uint32_t qw[D / 64][8];
+    if (NR == 1) load_query(spot.b, spot.u / a.tiles, spot.u % a.tiles * T::R, 0, qw);
+
     // ------------------------------------------------ segments: a unit's blocks here
     int left = blocks, b = spot.b, at_unit = spot.u, kb = spot.at, index = 0;
 #pragma unroll 1
@@ -418,24 +443,9 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         int place[NR][2];    // the rows' keys
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            const int pr = rbase + nr * 8 + g;
-            uint32_t w[D / 64][8];
+            if (NR > 1) load_query(b, hkv, rbase, nr, qw);
+            const uint32_t(&w)[D / 64][8] = qw;
             float most = 0.f;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[c][e] = 0;
-            if (pr < a.rows) {
-                const int h = hkv * a.group + pr / a.Sq;
-                const uint16_t* q = a.q + (((size_t)b * a.Hq + h) * a.Sq + pr % a.Sq) * D + t * 16;
-#pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(q + c * 64);
-                    const uint4 y = *reinterpret_cast<const uint4*>(q + c * 64 + 8);
-                    w[c][0] = x.x, w[c][1] = x.y, w[c][2] = x.z, w[c][3] = x.w;
-                    w[c][4] = y.x, w[c][5] = y.y, w[c][6] = y.z, w[c][7] = y.w;
-                }
-            }
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -683,6 +693,12 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
             }
         }
 
+        // the next segment
+        const bool last_unit = at_unit + 1 == units;
+        const int next_b = last_unit ? b + 1 : b, next_unit = last_unit ? 0 : at_unit + 1;
+        if (NR == 1 && left > n)
+            load_query(next_b, next_unit / a.tiles, next_unit % a.tiles * T::R, 0, qw);
+
         // ------------------------------------------------ merge of the warps
         // eight rows at a time through the slot that was read last, which is free until
         // the next block is begun: [8][D] O (columns turned by the row
@@ -823,10 +839,8 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         left -= n;
         kb = 0;
         ++index;
-        if (++at_unit == units) {
-            at_unit = 0;
-            ++b;
-        }
+        at_unit = next_unit;
+        b = next_b;
     } while (left > 0);
     cp_async_wait<0>();
     if (!ok) {   // given up: what was asked for must have landed before the CTA exits
@@ -975,9 +989,19 @@ cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
     using T = Q8Traits<D, NR>;
     const DecodeQ8Args& a = p.args;
     constexpr int kAlign = 1024;
-    cudaError_t e = cudaFuncSetAttribute(decode_q8_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kAlign + T::RING + T::JOIN);
+    // (once per device: a small call takes seven microseconds)
+    constexpr int kDevices = 64;
+    static std::atomic<bool> allowed[kDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < kDevices;
+    if (!keep || !allowed[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(decode_q8_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kAlign + T::RING + T::JOIN);
+        if (e != cudaSuccess) return e;
+        if (keep) allowed[dev].store(true, std::memory_order_relaxed);
+    }
     if (a.joined)
         return launch_dependent_clusters(
             decode_q8_kernel<D, NR>, (unsigned)a.n_splits,
