@@ -602,8 +602,16 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     return FA_OK;
 }
 
-// Decode over a paged cache of 8 bits (decode_q8.cu): equal splits as those of
-// the split-KV kernel, of the positions that a sequence's rows can see.
+// Most keys of a joined split of an 8-bit cache: past it the line's even pieces gain
+// more than their second kernel costs.  us, line / joined, 8 heads:
+//              4,000 keys     6,000 keys     8,000 keys
+//   d 64       11.1 /  8.1    12.0 /  9.7    11.8 / 11.5
+//   d 128      11.7 /  9.2    11.9 / 11.0    12.9 / 13.0
+//   d 256      14.8 / 13.6    15.6 / 17.6    15.7 / 21.6
+long long join_keys_q8(int head_dim) { return head_dim == 256 ? 512 : 768; }
+
+// Decode over a paged cache of 8 bits (decode_q8.cu): the splits of each unit a
+// cluster where they are short, else pieces of a line.
 fa_status decode_q8_impl(const void* q, const void* k, const void* v, const float* k_scale,
                          const float* v_scale, void* o, float* lse, int batch, int hq, int hkv, int sq,
                          const int* seqlens_k, const int* block_table, int max_pages, int page_size,
@@ -674,19 +682,20 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     const long long heads_first = (a.first + 63ll) / 64 * 64;
     const long long span = window > 0 ? std::min<long long>(sk, (long long)window + sq + 62 + heads_first) : sk;
     const long long pairs = (long long)batch * hkv * a.tiles;
-    const SplitPlan plan = split_plan(true, head_dim, pairs, span, di->num_sms);
-    a.joined = plan.joined ? 1 : 0;
-    if (a.joined) {
-        const long long keys = decode_q8_block(head_dim);
-        a.chunk = (int)(((span + plan.splits - 1) / plan.splits + keys - 1) / keys * keys);
+    const int keys = decode_q8_block(head_dim);
+    const long long wave = (long long)di->num_sms * decode_q8_ctas(head_dim, tile);   // CTAs at once
+    const long long fine = (span + keys - 1) / keys;
+    const long long join = std::min(std::min<long long>(fine, kJoinSplits), wave / pairs);
+    if (join >= std::min(2ll, fine) && span <= join * join_keys_q8(head_dim)) {
+        a.joined = 1;
+        a.chunk = (int)((fine + join - 1) / join * keys);
         a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
         return from_cuda(launch_decode_q8(p, head_dim, s));
     }
     // (the kernel counts the blocks of all units in 32 bits)
-    const int keys = decode_q8_block(head_dim);
     const double blocks = (double)pairs * (double)((span + keys - 1) / keys);
     if (blocks >= 2147483647.0 - 65536) return FA_ERR_INVALID_ARG;
-    a.slots = (int)std::min<double>((double)di->num_sms * decode_q8_ctas(head_dim, tile), blocks);
+    a.slots = (int)std::min<double>((double)wave, blocks);
     // pieces for every SM to take when it is done with its own, where there may be much
     a.levels = blocks >= 48.0 * a.slots ? 2 : 0;
     a.n_splits = a.slots * (1 + a.levels);
