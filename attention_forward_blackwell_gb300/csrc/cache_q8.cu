@@ -50,24 +50,38 @@ struct AppendArgs {
 // a CTA).
 constexpr int kKeptWarp = 4, kKeptCta = 4;
 
-// Codes of a task's two granules.
-__device__ __forceinline__ void store_codes(uint8_t* row, const TaskAt& at, const float (&x)[8],
-                                            const float (&y)[8], float inv) {
-    *reinterpret_cast<uint2*>(row + at.a) =
-        make_uint2(q8_codes(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
-                   q8_codes(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
-    *reinterpret_cast<uint2*>(row + at.b) =
-        make_uint2(q8_codes(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                   q8_codes(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+// Codes of a granule, its elements times inv.
+__device__ __forceinline__ uint2 codes_of(const Granule& x, float inv) {
+    const float2 i2 = both(inv);
+    float2 y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = fmul2(make_float2(x.even[i], x.odd[i]), i2);
+    return make_uint2(q8_codes(y[0].x, y[0].y, y[1].x, y[1].y), q8_codes(y[2].x, y[2].y, y[3].x, y[3].y));
+}
+// Largest square of a granule's elements, and of its interleaved pairs' lengths.
+// (Products of bf16 values are exact in fp32, a sum of two rounds once.)
+__device__ __forceinline__ float square_of(const Granule& x) {
+    float m = fmax3(fabsf(x.even[0]), fabsf(x.odd[0]), fabsf(x.even[1]));
+    m = fmax3(m, fabsf(x.odd[1]), fabsf(x.even[2]));
+    m = fmax3(m, fabsf(x.odd[2]), fabsf(x.even[3]));
+    m = fmaxf(m, fabsf(x.odd[3]));
+    return m * m;
+}
+__device__ __forceinline__ float square_of_pairs(const float (&x)[4], const float (&y)[4]) {
+    const float2 a0 = make_float2(x[0], x[1]), a1 = make_float2(x[2], x[3]);
+    const float2 b0 = make_float2(y[0], y[1]), b1 = make_float2(y[2], y[3]);
+    const float2 p = ffma2(a0, a0, fmul2(b0, b0)), q = ffma2(a1, a1, fmul2(b1, b1));
+    return fmax3(fmaxf(p.x, p.y), q.x, q.y);
 }
 
 // Queries of batch entry b: as in rope.cu, a task a thread.
 template <bool INTERLEAVED>
 __device__ void append_queries(const AppendArgs& a, int b, int len, int n) {
     const unsigned all = (unsigned)n * (unsigned)(a.hq * a.tasks);   // (below 2^31: the host sees to it)
-    const unsigned cta = (blockIdx.y - a.kv_ctas) * gridDim.x + blockIdx.x;
-    const unsigned step = (gridDim.y - a.kv_ctas) * gridDim.x * blockDim.x;
-    for (unsigned e = cta * blockDim.x + threadIdx.x; e < all; e += step) {
+    const long long cta = (long long)(blockIdx.y - a.kv_ctas) * gridDim.x + blockIdx.x;
+    const long long step = (long long)(gridDim.y - a.kv_ctas) * gridDim.x * blockDim.x;
+    for (long long e_ = cta * blockDim.x + threadIdx.x; e_ < (long long)all; e_ += step) {
+        const unsigned e = (unsigned)e_;
         const unsigned r = a.by_tasks(e), i = a.by_hq(r);
         const int j = (int)(e - r * (unsigned)a.tasks), h = (int)(r - i * (unsigned)a.hq);
         const TaskAt at = task_at<INTERLEAVED>(a.turn.rot, a.tasks, j);
@@ -80,9 +94,7 @@ __device__ void append_queries(const AppendArgs& a, int b, int len, int n) {
                                    a.positions != nullptr ? a.positions[b * a.position_stride + i]
                                                           : (int)((unsigned)len + i),
                                    g);
-            float x[8], y[8];
-            unpack8(u, x);
-            unpack8(w, y);
+            Granule x = unpack8(u), y = unpack8(w);
             turn_task<INTERLEAVED>(at, g, x, y);
             u = pack8(x);
             w = pack8(y);
@@ -195,26 +207,17 @@ __global__ void append_q8_kernel(const AppendArgs a) {
     const float f2 = a.turn.factor * a.turn.factor;
     auto reach = [&](int e, const uint4& u, const uint4& w) {
         const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, e - (int)a.by_tasks((unsigned)e) * a.tasks);
-        float x[8], y[8], turned = 0.f, rest = 0.f;
-        unpack8(u, x);
-        unpack8(w, y);
-        // (products of bf16 values are exact in fp32, a sum of two rounds once)
+        const Granule x = unpack8(u), y = unpack8(w);
+        float turned = 0.f, rest = 0.f;
         if (INTERLEAVED) {
-#pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-                const float p = fmaf(x[k], x[k], x[k + 1] * x[k + 1]);
-                const float q = fmaf(y[k], y[k], y[k + 1] * y[k + 1]);
-                if (at.turned_a) turned = fmaxf(turned, p);
-                else rest = fmaxf(rest, fmaxf(x[k] * x[k], x[k + 1] * x[k + 1]));
-                if (at.turned_b) turned = fmaxf(turned, q);
-                else rest = fmaxf(rest, fmaxf(y[k] * y[k], y[k + 1] * y[k + 1]));
-            }
+            if (at.turned_a) turned = square_of_pairs(x.even, x.odd);
+            else rest = square_of(x);
+            if (at.turned_b) turned = fmaxf(turned, square_of_pairs(y.even, y.odd));
+            else rest = fmaxf(rest, square_of(y));
         } else if (at.turned_a) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) turned = fmaxf(turned, fmaf(x[k], x[k], y[k] * y[k]));
+            turned = fmaxf(square_of_pairs(x.even, y.even), square_of_pairs(x.odd, y.odd));
         } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) rest = fmaxf(rest, fmaxf(x[k] * x[k], y[k] * y[k]));
+            rest = fmaxf(square_of(x), square_of(y));
         }
         square = fmaxf(square, fmaxf(turned * f2, rest));
     };
@@ -238,11 +241,11 @@ __global__ void append_q8_kernel(const AppendArgs a) {
     auto store = [&](int e, const uint4& u, const uint4& w, const Angles& g) {
         const int i = (int)a.by_tasks((unsigned)e);
         const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, e - i * a.tasks);
-        float x[8], y[8];
-        unpack8(u, x);
-        unpack8(w, y);
+        Granule x = unpack8(u), y = unpack8(w);
         if (at.turned_a || at.turned_b) turn_task<INTERLEAVED>(at, g, x, y);
-        store_codes(row_of(page, row + (lo - first) + i), at, x, y, inv);
+        uint8_t* const to = row_of(page, row + (lo - first) + i);
+        *reinterpret_cast<uint2*>(to + at.a) = codes_of(x, inv);
+        *reinterpret_cast<uint2*>(to + at.b) = codes_of(y, inv);
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {

@@ -51,7 +51,7 @@ struct RopeArgs {
 // task fastest -- 8 threads read the halves of a row of 128 elements -- then what
 // lies next in memory, the heads of a token or the tokens of a head.
 template <int HEADS, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, HEADS > 1 ? 14 : 24) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, HEADS > 1 ? 13 : 20) rope_kernel(const RopeArgs a) {
     dependents_may_start();
     wait_for_previous();
     const int b = blockIdx.y, page_size = a.pages.page_size;
@@ -119,9 +119,7 @@ __global__ void __launch_bounds__(kThreads, HEADS > 1 ? 14 : 24) rope_kernel(con
     for (int u = 0; u < HEADS; ++u) {
         if (to[u] == nullptr) continue;
         if (turned[u]) {
-            float p[8], q[8];
-            unpack8(xa[u], p);
-            unpack8(xb[u], q);
+            Granule p = unpack8(xa[u]), q = unpack8(xb[u]);
             turn_task<INTERLEAVED>(at, angles, p, q);
             xa[u] = pack8(p);
             xb[u] = pack8(q);

@@ -5,12 +5,13 @@
 // angle 2 pi p F_i / 2^64 of pair i: F_i counts 2^-64 of a turn, so the product
 // modulo 2^64, whole-number arithmetic, is the exact fraction of a turn however far
 // the position, where the product of two fp32 numbers is off by 0.03 radians at
-// position 10^6.  Its two highest bits, rounded, are the quarter; the rest, at
-// most an eighth of a turn, goes through two polynomials of its own (sine and
-// cosine of pi/4 w over the square of w, interpolated at Chebyshev points in 64
-// bits: off by 2.4e-9 and 4.8e-11, 8.3e-8 with the roundings of fp32).  Two
-// products, 9 fused multiply-adds and the choice of the quarter: about 25
-// instructions an angle, with no range reduction and no branch.
+// position 10^6.  Half turns change the signs; what is left, a quarter of a turn at
+// most either way, goes through two polynomials of its own (sine and cosine of
+// pi/2 w over the square of w, interpolated at Chebyshev points in 64 bits: off by
+// 6.7e-9 and 2.3e-10, 1.6e-7 with the roundings of fp32, and w itself by 2^-24).  Two
+// angles an instruction for all but the whole numbers: about 15 an angle, with no
+// range reduction, no branch and no selects, which the appends have too many of
+// (with quarter turns, whose sines and cosines change places, 8-bit chunks took 15 us).
 #pragma once
 
 #include <atomic>
@@ -22,26 +23,32 @@
 
 namespace fa {
 
-// Sine and cosine of 2 pi p F / 2^64.
-__device__ __forceinline__ void turn_sincos(int p, long long F, float& sine, float& cosine) {
+// Upper half of p F modulo 2^64.
+__device__ __forceinline__ uint32_t turn_of(int p, long long F) {
     const uint32_t lo = (uint32_t)F, up = (uint32_t)((uint64_t)F >> 32);
-    uint32_t t = __umulhi((uint32_t)p, lo) + (uint32_t)p * up;   // the product's upper half
-    if (p < 0) t -= lo;
-    const uint32_t quarter = (t + 0x20000000u) >> 30;
-    const float w = (float)(int)(t - (quarter << 30)) * 0x1p-29f;
-    const float v = w * w;
-    float s = fmaf(v, -0x1.2d9b4p-15f, 0x1.465ec4p-9f);
-    s = fmaf(v, s, -0x1.4abbbap-4f);
-    s = fmaf(v, s, 0x1.921fb6p-1f) * w;
-    float c = fmaf(v, 0x1.d9c2e8p-19f, -0x1.55c57ap-12f);
-    c = fmaf(v, c, 0x1.03c1dcp-6f);
-    c = fmaf(v, c, -0x1.3bd3ccp-2f);
-    c = fmaf(v, c, 1.0f);
-    const bool odd = (quarter & 1u) != 0;
-    sine = odd ? c : s;
-    cosine = odd ? s : c;
-    if (quarter & 2u) sine = -sine;
-    if ((quarter + 1u) & 2u) cosine = -cosine;
+    return __umulhi((uint32_t)p, lo) + (uint32_t)p * up - (lo & (uint32_t)(p >> 31));
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float with_sign(float x, uint32_t bits) {   // (bit 31 of `bits` changes it)
+    return __uint_as_float(__float_as_uint(x) ^ (bits & 0x80000000u));
+}
+// Sines and cosines of 2 pi p F / 2^64 for two F.
+__device__ __forceinline__ void turn_sincos(int p, const longlong2& F, float2& sine, float2& cosine) {
+    const uint32_t t0 = turn_of(p, F.x), t1 = turn_of(p, F.y);
+    const float2 w = fmul2(make_float2((float)(int)(t0 << 1), (float)(int)(t1 << 1)), both(0x1p-31f));
+    const float2 v = fmul2(w, w);
+    float2 s = ffma2(v, both(0x1.3e1420p-13f), both(-0x1.32531ep-8f));
+    s = ffma2(v, s, both(0x1.4668f0p-4f));
+    s = ffma2(v, s, both(-0x1.4abbc4p-1f));
+    s = fmul2(ffma2(v, s, both(0x1.921fb6p+0f)), w);
+    float2 c = ffma2(v, both(-0x1.8fb3f4p-16f), both(0x1.e126b0p-11f));
+    c = ffma2(v, c, both(-0x1.55d074p-6f));
+    c = ffma2(v, c, both(0x1.03c1e4p-2f));
+    c = ffma2(v, c, both(-0x1.3bd3ccp+0f));
+    c = ffma2(v, c, both(1.0f));
+    const uint32_t h0 = t0 + 0x40000000u, h1 = t1 + 0x40000000u;
+    sine = make_float2(with_sign(s.x, h0), with_sign(s.y, h1));
+    cosine = make_float2(with_sign(c.x, h0), with_sign(c.y, h1));
 }
 
 // How rows are turned: the first `rot` elements of a row (a multiple of 16; 0:
@@ -87,60 +94,68 @@ __device__ __forceinline__ TaskAt task_at(int rot, int tasks, int j) {
     return at;
 }
 
-// Sines and cosines of a task's 8 pairs at a position.
+// Sines and cosines of a task's 8 pairs at a position, two together.
 struct Angles {
-    float s[8], c[8];
+    float2 s[4], c[4];
 };
 template <bool INTERLEAVED>
 __device__ __forceinline__ void angles_of(const Turn& t, const TaskAt& at, int position, Angles& g) {
+    const float2 f = both(t.factor), fs = both(t.factor * t.sign);
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        const bool second = INTERLEAVED && e >= 4;
+    for (int e = 0; e < 4; ++e) {
+        const bool second = INTERLEAVED && e >= 2;
         if (second ? !at.turned_b : !at.turned_a) continue;
-        const long long* from = t.freqs + (second ? at.pair_b + e - 4 : at.pair_a + e);
-        const longlong2 F = *reinterpret_cast<const longlong2*>(from);
-        turn_sincos(position, F.x, g.s[e], g.c[e]);
-        turn_sincos(position, F.y, g.s[e + 1], g.c[e + 1]);
-    }
-    const float f = t.factor, fs = t.factor * t.sign;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        g.s[e] *= fs;
-        g.c[e] *= f;
+        const long long* from = t.freqs + (second ? at.pair_b + 2 * e - 4 : at.pair_a + 2 * e);
+        turn_sincos(position, *reinterpret_cast<const longlong2*>(from), g.s[e], g.c[e]);
+        g.s[e] = fmul2(g.s[e], fs);
+        g.c[e] = fmul2(g.c[e], f);
     }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+// A granule's eight elements, those of even and of odd place.
+struct Granule {
+    float even[4], odd[4];
+};
+__device__ __forceinline__ Granule unpack8(const uint4& u) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    Granule x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        x.even[i] = __uint_as_float(w[i] << 16);
+        x.odd[i] = __uint_as_float(w[i] & 0xffff0000u);
     }
+    return x;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack8(const Granule& x) {
+    return make_uint4(pack_bf16x2(x.even[0], x.odd[0]), pack_bf16x2(x.even[1], x.odd[1]),
+                      pack_bf16x2(x.even[2], x.odd[2]), pack_bf16x2(x.even[3], x.odd[3]));
 }
 
-// The turned pairs of a task, in place: x, y its granules' elements.  Products
-// and sums in fp32, rounded once by whoever stores them.
-__device__ __forceinline__ void turn_pair(float& x, float& y, float s, float c) {
-    const float a = x * c - y * s;
-    y = y * c + x * s;
-    x = a;
+// Two pairs (x, y), turned in place.  Products and sums in fp32, rounded once by whoever
+// stores them.
+__device__ __forceinline__ void turn_pairs(float& x0, float& x1, float& y0, float& y1, float2 s, float2 c) {
+    const float2 x = make_float2(x0, x1), y = make_float2(y0, y1);
+    const float2 a = ffma2(fmul2(y, s), both(-1.f), fmul2(x, c)), b = ffma2(y, c, fmul2(x, s));
+    x0 = a.x;
+    x1 = a.y;
+    y0 = b.x;
+    y1 = b.y;
 }
+// The turned pairs of a task, in place: x, y its granules.
 template <bool INTERLEAVED>
-__device__ __forceinline__ void turn_task(const TaskAt& at, const Angles& g, float (&x)[8], float (&y)[8]) {
+__device__ __forceinline__ void turn_task(const TaskAt& at, const Angles& g, Granule& x, Granule& y) {
     if (INTERLEAVED) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (at.turned_a) turn_pair(x[2 * e], x[2 * e + 1], g.s[e], g.c[e]);
-            if (at.turned_b) turn_pair(y[2 * e], y[2 * e + 1], g.s[4 + e], g.c[4 + e]);
+        for (int e = 0; e < 2; ++e) {
+            if (at.turned_a)
+                turn_pairs(x.even[2 * e], x.even[2 * e + 1], x.odd[2 * e], x.odd[2 * e + 1], g.s[e], g.c[e]);
+            if (at.turned_b)
+                turn_pairs(y.even[2 * e], y.even[2 * e + 1], y.odd[2 * e], y.odd[2 * e + 1], g.s[2 + e],
+                           g.c[2 + e]);
         }
     } else if (at.turned_a) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) turn_pair(x[e], y[e], g.s[e], g.c[e]);
+        for (int e = 0; e < 4; ++e) turn_pairs(x.even[e], x.odd[e], y.even[e], y.odd[e], g.s[e], g.c[e]);
     }
 }
 

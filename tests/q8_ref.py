@@ -24,15 +24,15 @@ def turn64(x, positions, inv_freq, factor=1.0, interleaved=False, inverse=False)
 
 
 def turn_bound(x, y, positions, rot, factor, interleaved):
-    """Bound of a turned row y of x in bf16 (rounding: 2^-8 of the value; before it, in fp32: a sine or
-    cosine off by 2^-23 + 2^-29 -- one rounding of the fraction of a turn to 24 bits of at most an
-    eighth, 2^-29 radians of its cut to 2^-32 of a turn, the polynomials' 2^-28 and their roundings --
-    the factor's product, and two products and a sum, 2^-24 each: 2^-21 of the pair's length
-    is over all of it), zero for elements that are not turned."""
+    """Bound of a turned row y of x in bf16: 2^-8 of the value for its rounding.  Before it, in fp32, a
+    sine or cosine is off by 2^-22: 2^-24 pi / 2 of a rounding of the fraction of half a turn to 24 bits,
+    2^-29 of its cut to 2^-32 of a turn, 1.6e-7 of the polynomials and their roundings, 2^-24 of the
+    factor's product.  A turned element is then off by sqrt(2) 2^-22 of its pair's length, and by three
+    roundings of 2^-24: 5.2e-7 of it in all, below 2^-20.  Zero for elements that are not turned."""
     x = x.double().abs()
     size = torch.zeros_like(x)
     a, b = (x[..., 0:rot:2], x[..., 1:rot:2]) if interleaved else (x[..., :rot // 2], x[..., rot // 2:rot])
-    length = factor * torch.hypot(a, b) * 2.0 ** -21
+    length = factor * torch.hypot(a, b) * 2.0 ** -20
     if interleaved:
         size[..., 0:rot:2] = size[..., 1:rot:2] = length
     else:
@@ -132,7 +132,7 @@ class Cache8:
                         z = y[h] / s
                         r0 = row + lo - p0
                         self.codes[i][page, h, r0:r0 + hi - lo] = z = round8(z)
-                        # a turned element is off by 2^-21 of its pair: the code may be the other of two
+                        # a turned element is off by 2^-20 of its pair: the code may be the other of two
                         near = torch.zeros_like(z)
                         if rot:
                             near[..., :rot] = 2 * half_step(z)[..., :rot]
