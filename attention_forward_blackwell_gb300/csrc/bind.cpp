@@ -583,6 +583,40 @@ struct Positions {
     Positions() = default;
 };
 
+bool same_memory(const Tensor& a, const Tensor& b) {
+    return a.data_ptr() == b.data_ptr() && a.sizes() == b.sizes() && a.strides() == b.strides();
+}
+// Refuses an output `a` that shares memory with another tensor `b` of rows [.., heads,
+// .., d] -- or may: the heads of one token of both lie within a common stride of the
+// tokens, as the parts of one projection do, apart from one another, or their ranges of
+// addresses do.
+void apart_from(const char* a_name, const Tensor& a, const char* b_name, const Tensor& b) {
+    if (a.numel() == 0 || b.numel() == 0) return;
+    auto extent = [](const Tensor& t) {   // elements from the first to past the last
+        int64_t n = 1;
+        for (int64_t i = 0; i < t.dim(); ++i) n += (t.size(i) - 1) * t.stride(i);
+        return n;
+    };
+    const auto pa = reinterpret_cast<uintptr_t>(a.data_ptr()), pb = reinterpret_cast<uintptr_t>(b.data_ptr());
+    if (pa + 2 * extent(a) <= pb || pb + 2 * extent(b) <= pa) return;
+    if (a.dim() == b.dim()) {
+        // the tokens' dimension; with one token to a batch entry, the entries'
+        const int64_t token = a.dim() == 3 || a.size(2) == 1 ? 0 : 2, period = a.stride(token);
+        bool grid = period > 0 && b.stride(token) == period && a.size(token) == b.size(token);
+        if (a.dim() == 4) {
+            grid &= a.size(2) == b.size(2) && a.size(0) == b.size(0);
+            if (a.size(0) > 1) grid &= a.stride(0) == b.stride(0) && a.stride(0) % period == 0;
+        }
+        // a token's heads of each, as offsets within the period
+        auto row = [](const Tensor& t) { return (t.size(1) - 1) * t.stride(1) + t.size(t.dim() - 1); };
+        if (grid && (pa - pb) % 2 == 0 && row(a) <= period && row(b) <= period) {
+            const int64_t off = ((static_cast<int64_t>(pb) - static_cast<int64_t>(pa)) / 2 % period + period) % period;
+            if (off >= row(a) && off + row(b) <= period) return;
+        }
+    }
+    throw BadValue(std::string(a_name) + " may share memory with " + b_name);
+}
+
 // Rows to turn: [T, heads, d] or [B, heads, n, d] with the strides of batch, head
 // and token; and where they go.
 struct Turned {
@@ -596,12 +630,6 @@ struct Turned {
         s[1] = t.stride(1);
         s[2] = packed ? t.stride(0) : t.stride(2);
     }
-    static std::pair<uintptr_t, uintptr_t> range(const Tensor& t) {   // of addresses
-        uintptr_t lo = reinterpret_cast<uintptr_t>(t.data_ptr()), hi = lo + 2;
-        for (int64_t i = 0; i < t.dim(); ++i) hi += 2 * (t.size(i) - 1) * t.stride(i);
-        return {lo, hi};
-    }
-
     Turned(const char* name, PyObject* in_, const char* out_name, PyObject* out_, int dev,
            const Stream& stream)
         : in(tensor(name, in_)) {
@@ -621,11 +649,7 @@ struct Turned {
             for (int64_t i = 0; i < out.dim(); ++i) apart &= out.size(i) < 2 || out.stride(i) != 0;
             if (!apart)
                 throw BadValue(std::string(out_name) + " must have contiguous, 16-byte aligned rows");
-            if (in.numel() > 0 && (in.data_ptr() != out.data_ptr() || in.strides() != out.strides())) {
-                const auto x = range(in), y = range(out);
-                if (x.first < y.second && y.first < x.second)
-                    throw BadValue(std::string(out_name) + " must be " + name + " itself or lie apart from it");
-            }
+            if (!same_memory(in, out)) apart_from(out_name, out, name, in);
         }
         if (!rows_fit(in)) {
             const c10::cuda::CUDAStreamGuard guard(torch_stream(stream, dev));
@@ -646,6 +670,12 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
     if (a[1] != Py_None) k.emplace("k", a[1], "k_out", a[8], dev, stream);
     const Tensor& x = q.in;
     const bool packed = x.dim() == 3;
+    if (k) {   // (rows of one are read while the other's are written)
+        const Tensor &q_in = tensor("q", a[0]), &k_in = tensor("k", a[1]);
+        apart_from("q_out", q.out, "k", k_in);
+        apart_from("k_out", k->out, "q", q_in);
+        apart_from("q_out", q.out, "k_out", k->out);
+    }
     if (k && (k->in.dim() != x.dim() || k->in.size(0) != x.size(0) ||
               k->in.size(x.dim() - 1) != x.size(x.dim() - 1) || (!packed && k->in.size(2) != x.size(2))))
         throw BadValue("k " + text(k->in.sizes()) + " does not go with q " + text(x.sizes()));
@@ -703,6 +733,9 @@ struct Append {
             } else {
                 q_out = tensor("q_out", a[9]);
                 dense("q_out", q_out, at::kBFloat16, {B, qn.size(1), n, c.d}, c.dev);
+                if (!same_memory(qn, q_out)) apart_from("q_out", q_out, "q", qn);
+                apart_from("q_out", q_out, "k_new", kn);
+                apart_from("q_out", q_out, "v_new", tensor("v_new", a[3]));
             }
             turn.q = q->t.data_ptr();
             turn.q_strides = q->strides;

@@ -309,6 +309,7 @@ def test_refusals(fa):
                 lambda: fa.cache_append_q8(kc, kc, ks, ks, t, lens, x, x[:, :1]),
                 lambda: fa.cache_append_q8(kc, kc, ks, ks, t, lens, x, x, freqs, q=x[0]),
                 lambda: fa.cache_append_q8(kc, kc, ks, ks, t, lens, x, x, freqs, q_out=x),
+                lambda: fa.cache_append_q8(kc, kc, ks, ks, t, lens, x, x, freqs, q=x.clone(), q_out=x),
                 lambda: fa.cache_append_q8(kc, kc, ks, ks, t, lens, x, x, freqs, positions=i32([1, 2])),
                 lambda: fa.cache_append_q8(kc, kc, ks, ks, t, lens, x, x, freqs, factor=float("nan")),
                 lambda: fa.cache_append_rope(kc, kc, t, lens, x, x, freqs),

@@ -53,7 +53,8 @@ def test_packed(fa, n, hq, hk, d, rot, start, method, interleaved):
 
 
 @pytest.mark.parametrize("per_entry", [False, True])
-@pytest.mark.parametrize("B,hq,hk,n,d,rot", [(1, 2, 1, 1, 64, 64), (3, 4, 2, 37, 128, 96), (2, 16, 16, 600, 96, 48)])
+@pytest.mark.parametrize("B,hq,hk,n,d,rot", [(1, 2, 1, 1, 64, 64), (5, 4, 2, 1, 128, 64), (3, 4, 2, 37, 128, 96),
+                                           (2, 16, 16, 600, 96, 48)])
 def test_batched_positions_strides_in_place(fa, B, hq, hk, n, d, rot, per_entry):
     inv, _ = fa.rope_inv_freq(rot)
     freqs = fa.rope_freqs(inv)
@@ -73,6 +74,15 @@ def test_batched_positions_strides_in_place(fa, B, hq, hk, n, d, rot, per_entry)
     q2, k2 = fa.rope(q, k, at, freqs, q_out=q, k_out=k)   # in place, in the projection's own memory
     assert q2.data_ptr() == q.data_ptr() and torch.equal(q, qo) and torch.equal(k, ko)
     assert torch.equal(x[:, :, hq + hk:], before[:, :, hq + hk:])
+    # side by side in memory of its own, and parts of one projection that share heads
+    wide = torch.zeros_like(x)
+    q3, k3 = fa.rope(q0, k0, at, freqs, q_out=wide[:, :, :hq].transpose(1, 2),
+                     k_out=wide[:, :, hq:hq + hk].transpose(1, 2))
+    assert torch.equal(q3, qo) and torch.equal(k3, ko) and not wide[:, :, hq + hk:].any()
+    if n > 1:
+        with pytest.raises(ValueError):
+            fa.rope(q0, k0, at, freqs, q_out=wide[:, :, :hq].transpose(1, 2),
+                    k_out=wide[:, :, hq - 1:hq - 1 + hk].transpose(1, 2))
     # an unaligned view, and an input expanded over the heads
     odd = rows(6, B, hq, n, d + 4)[..., 4:]
     near(fa.rope(odd, None, at, freqs)[0], odd, where, inv, 1.0, False, False, "unaligned")
@@ -144,6 +154,8 @@ def test_empty_and_refused(fa):
                 lambda: fa.rope(x, None, at, freqs.int()), lambda: fa.rope(x, None, at.cpu(), freqs),
                 lambda: fa.rope(x, None, at, freqs, q_out=x[:, :1].expand(4, 2, 64)),
                 lambda: fa.rope(big[:4], None, at, freqs, q_out=big[2:]),
+                lambda: fa.rope(x, big[:4], at, freqs, k_out=x), lambda: fa.rope(big[:4], x, at, freqs, q_out=x),
+                lambda: fa.rope(x, big[:4], at, freqs, q_out=big[2:], k_out=big[:4]),
                 lambda: fa.rope(x, None, at, freqs, factor=0.0),
                 lambda: fa.rope(x, None, at, fa.rope_freqs(fa.rope_inv_freq(128)[0])),
                 lambda: fa.rope(x, None, at, fa.rope_freqs(fa.rope_inv_freq(24)[0])),
@@ -166,4 +178,4 @@ def test_angles_against_cuda(fa):
     angle = torch.tensor([[v / 2 ** 64 for v in row] for row in part], dtype=torch.float64) * 2 * math.pi
     want = torch.cat([torch.cos(angle), torch.sin(angle)], 1)
     off = (y[:, 0].cpu().double() - want).abs()
-    assert torch.all(off <= 2.0 ** -8 * want.abs() + 2.0 ** -21)
+    assert torch.all(off <= 2.0 ** -8 * want.abs() + 2.0 ** -22)
