@@ -174,60 +174,63 @@ __global__ void append_q8_kernel(const AppendArgs a) {
     const uint4* src = (kind == 0 ? a.src[0] : a.src[1]) + b * a.ss[kind][0] + h * a.ss[kind][1];
     const long long step = a.ss[kind][2];
     const int rot = kind == 0 ? a.turn.rot : 0;
-    const int all = max(0, hi - lo) * a.tasks;
+    // a thread has one task of the rows i0, i0 + slots, ...: what goes by the task alone
+    // is worked out once
+    const int slots = (int)a.by_tasks((unsigned)T), slot = (int)a.by_tasks((unsigned)tid), rows = max(0, hi - lo);
+    const int i0 = slot < slots ? slot : rows;
+    const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, tid - slot * a.tasks);
+    const bool turned = at.turned_a || at.turned_b;
+    const uint4* const mine = src + (lo - len + i0) * step + (at.a >> 3);
+    const int apart = (at.b - at.a) >> 3;
+    const long long stride = slots * step;
     uint4 ka[kKept], kb[kKept];
-    auto load = [&](int e, uint4& u, uint4& w) {
-        const int i = (int)a.by_tasks((unsigned)e), j = e - i * a.tasks;
-        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, j);
-        const uint4* r = src + (lo - len + i) * step;
-        u = r[at.a >> 3];
-        w = r[at.b >> 3];
+    auto load = [&](int k, uint4& u, uint4& w) {   // of row i0 + k slots
+        const uint4* r = mine + k * stride;
+        u = r[0];
+        w = r[apart];
     };
-    auto angles = [&](int e, Angles& g) {
-        const int i = (int)a.by_tasks((unsigned)e), j = e - i * a.tasks, row = lo - len + i;
-        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, j);
-        if (at.turned_a || at.turned_b)
-            angles_of<INTERLEAVED>(a.turn, at,
-                                   a.positions != nullptr ? a.positions[b * a.position_stride + row]
-                                                          : (int)((unsigned)start + row),
-                                   g);
+    auto angles = [&](int k, Angles& g) {
+        const int new_row = lo - len + i0 + k * slots;
+        angles_of<INTERLEAVED>(a.turn, at,
+                               a.positions != nullptr ? a.positions[b * a.position_stride + new_row]
+                                                      : (int)((unsigned)start + new_row),
+                               g);
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
-        if (tid + k * T < all) load(tid + k * T, ka[k], kb[k]);
+        if (i0 + k * slots < rows) load(k, ka[k], kb[k]);
     int page, row;   // (a block lies in one page)
     const bool there = key_page(c.pages, b, first, page, row);
-    Angles first_angles;   // of the thread's first task
-    if (rot > 0 && tid < all) angles(tid, first_angles);
+    Angles g;
+    if (turned && i0 < rows) angles(0, g);
     if (!there) return;
     const int block = (int)c.by_block((unsigned)row);
     const int old_page = takes_over ? from : page;
     const float before = lo > first ? *scale_of(old_page, block) : 0.f;
     float square = 0.f;
     const float f2 = a.turn.factor * a.turn.factor;
-    auto reach = [&](int e, const uint4& u, const uint4& w) {
-        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, e - (int)a.by_tasks((unsigned)e) * a.tasks);
+    auto reach = [&](const uint4& u, const uint4& w) {
         const Granule x = unpack8(u), y = unpack8(w);
-        float turned = 0.f, rest = 0.f;
+        float turned_most = 0.f, rest = 0.f;
         if (INTERLEAVED) {
-            if (at.turned_a) turned = square_of_pairs(x.even, x.odd);
+            if (at.turned_a) turned_most = square_of_pairs(x.even, x.odd);
             else rest = square_of(x);
-            if (at.turned_b) turned = fmaxf(turned, square_of_pairs(y.even, y.odd));
+            if (at.turned_b) turned_most = fmaxf(turned_most, square_of_pairs(y.even, y.odd));
             else rest = fmaxf(rest, square_of(y));
         } else if (at.turned_a) {
-            turned = fmaxf(square_of_pairs(x.even, y.even), square_of_pairs(x.odd, y.odd));
+            turned_most = fmaxf(square_of_pairs(x.even, y.even), square_of_pairs(x.odd, y.odd));
         } else {
             rest = fmaxf(square_of(x), square_of(y));
         }
-        square = fmaxf(square, fmaxf(turned * f2, rest));
+        square = fmaxf(square, fmaxf(turned_most * f2, rest));
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
-        if (tid + k * T < all) reach(tid + k * T, ka[k], kb[k]);
-    for (int e = tid + kKept * T; e < all; e += T) {
+        if (i0 + k * slots < rows) reach(ka[k], kb[k]);
+    for (int k = kKept; i0 + k * slots < rows; ++k) {
         uint4 u, w;
-        load(e, u, w);
-        reach(e, u, w);
+        load(k, u, w);
+        reach(u, w);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) square = fmaxf(square, __shfl_xor_sync(0xffffffffu, square, o));
@@ -238,27 +241,25 @@ __global__ void append_q8_kernel(const AppendArgs a) {
     }
     const float now = hi > lo ? fmaxf(before, q8_scale(square)) : before;
     const float inv = 1.f / now;
-    auto store = [&](int e, const uint4& u, const uint4& w, const Angles& g) {
-        const int i = (int)a.by_tasks((unsigned)e);
-        const TaskAt at = task_at<INTERLEAVED>(rot, a.tasks, e - i * a.tasks);
+    uint8_t* const to = row_of(page, row + (lo - first) + i0);
+    auto store = [&](int k, const uint4& u, const uint4& w) {
         Granule x = unpack8(u), y = unpack8(w);
-        if (at.turned_a || at.turned_b) turn_task<INTERLEAVED>(at, g, x, y);
-        uint8_t* const to = row_of(page, row + (lo - first) + i);
-        *reinterpret_cast<uint2*>(to + at.a) = codes_of(x, inv);
-        *reinterpret_cast<uint2*>(to + at.b) = codes_of(y, inv);
+        if (turned) turn_task<INTERLEAVED>(at, g, x, y);
+        uint8_t* const r = to + (size_t)(k * slots) * d;
+        *reinterpret_cast<uint2*>(r + at.a) = codes_of(x, inv);
+        *reinterpret_cast<uint2*>(r + at.b) = codes_of(y, inv);
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
-        const int e = tid + k * T;
-        if (e >= all) break;
-        if (k > 0 && rot > 0) angles(e, first_angles);
-        store(e, ka[k], kb[k], first_angles);
+        if (i0 + k * slots >= rows) break;
+        if (k > 0 && turned) angles(k, g);
+        store(k, ka[k], kb[k]);
     }
-    for (int e = tid + kKept * T; e < all; e += T) {
+    for (int k = kKept; i0 + k * slots < rows; ++k) {
         uint4 u, w;
-        load(e, u, w);
-        if (rot > 0) angles(e, first_angles);
-        store(e, u, w, first_angles);
+        load(k, u, w);
+        if (turned) angles(k, g);
+        store(k, u, w);
     }
     // rows that lay in the block before
     if (lo > first && (now != before || takes_over)) {
@@ -460,9 +461,9 @@ fa_status fa_cache_append_q8(void* k_cache, void* v_cache, float* k_scale, float
     if (x >= (1ll << 31)) return FA_ERR_INVALID_ARG;
     if ((st = sm103_or_status()) != FA_OK) return st;
     // a warp for a unit where it keeps all of its rows
-    const long long unit_tasks = (long long)(n < block ? n : block) * a.tasks;
-    const bool warp = unit_tasks <= 32 * kKeptWarp;
-    const int threads = warp || unit_tasks <= 128 * kKeptCta ? 128 : 256;
+    const int unit_rows = n < block ? n : block;
+    const bool warp = unit_rows <= 32 / a.tasks * kKeptWarp;
+    const int threads = warp || unit_rows <= 128 / a.tasks * kKeptCta ? 128 : 256;
     a.kv_ctas = warp ? (2 * hkv + 3) / 4 : 2 * hkv;
     long long q_ctas = 0;
     if (a.hq > 0 && n > 0) {

@@ -82,7 +82,7 @@ struct Q8Traits {
     static constexpr int KB = 16 * SUB;                 // keys of a slice
     static constexpr int BLOCK = WARPS * KB;            // keys of a block
     static constexpr int SW = NR <= 2 ? SUB : 1;        // parts worked on together
-    static constexpr bool KEEP = D != 256 || NR == 1;   // exponents kept over the vote
+    static constexpr bool KEEP = NR == 1 || (D != 256 && NR == 2);   // exponents kept over the vote
     static constexpr int PITCH = D == 64 ? 64 : 128;    // bytes of a box's row
     static constexpr int CHUNK = KB * PITCH;            // a box of a slice's rows
     static constexpr int SLICE = KB * D;                // bytes of a slice of keys, or of values
