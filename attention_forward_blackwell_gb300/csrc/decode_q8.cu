@@ -81,7 +81,7 @@ struct Q8Traits {
     static constexpr int SUB = D == 256 ? 1 : 2;        // 16-key parts of a slice
     static constexpr int KB = 16 * SUB;                 // keys of a slice
     static constexpr int BLOCK = WARPS * KB;            // keys of a block
-    static constexpr int SW = NR <= 2 ? SUB : 1;        // parts worked on together
+    static constexpr int SW = SUB;                       // parts worked on together
     static constexpr bool KEEP = NR == 1 || (D != 256 && NR == 2);   // exponents kept over the vote
     static constexpr int PITCH = D == 64 ? 64 : 128;    // bytes of a box's row
     static constexpr int CHUNK = KB * PITCH;            // a box of a slice's rows
