@@ -47,8 +47,15 @@ struct AppendArgs {
 };
 
 // Tasks that a thread keeps between the two passes over a block (a unit's in a warp, in
-// a CTA).
-constexpr int kKeptWarp = 4, kKeptCta = 4;
+// a CTA).  More cost a CTA's registers more than they spare (head_dim 128, 64 keys to a
+// block, 8 heads: 64 entries x 64 tokens 12.0 us with four, 10.6 with two, 10.9 with one;
+// 16 x 2,048 51.8, 50.6, 53.1).
+constexpr int kKeptWarp = 4, kKeptCta = 2;
+// A unit has 128 threads where it keeps them busy with at most kPasses tasks each and
+// there are more than kFewUnits units of keys (four an SM), else 256: 8 x 600 tokens x 8
+// heads 11.8 us with 128, 12.4 with 256; 1 x 2,048 7.3 and 6.6; at head_dim 256, 8 x 600 x 4
+// heads 13.7 and 12.0.
+constexpr int kPasses = 4, kFewUnits = 608;
 
 // Codes of a granule, its elements times inv.
 __device__ __forceinline__ uint2 codes_of(const Granule& x, float inv) {
@@ -107,11 +114,14 @@ __device__ void append_queries(const AppendArgs& a, int b, int len, int n) {
 // A unit is a block of an entry's keys or of its values, of a head; WARP: a warp has
 // one, four a CTA (few rows), else a CTA.  CTA (block, heads and keys or values -- past
 // kv_ctas: queries --, batch entry).  Two passes over the new rows of a block: their
-// reach, then their codes; what a thread has of them stays in registers in between,
-// which covers blocks of 64 keys of 128 elements, and is read again past that (from L1
-// or L2).  A block has one writer, so nothing is atomic.  Bound by the
-// bytes, 3 for an element, and for single tokens by a chain of loads: length, page,
-// scale; the rows, and the angles that need only the length, come beside it.
+// reach, then their codes; the first tasks that a thread has of them stay in registers in
+// between, the others are read again (from L1 or L2).  A block has one writer, so nothing
+// is atomic.  Single tokens are bound by a chain of loads (length, page, scale; the rows,
+// and the angles that need only the length, come beside it): 128 tokens x 8 heads, with
+// 32 heads of queries, 4.4 us.  Chunks move 3 bytes an element and are bound
+// by the instructions, half of them for the angles: 16 x 2,048 tokens x 8 heads of 128
+// 50.6 us, 4.0 TB/s.  (Four heads of keys to a CTA by the same angles, read again for
+// the codes, took 52.3 there and 14.8 for 11.7 at 8 x 600: fewer CTAs, more registers.)
 template <bool INTERLEAVED, bool WARP>
 __global__ void append_q8_kernel(const AppendArgs a) {
     constexpr int kKept = WARP ? kKeptWarp : kKeptCta;
@@ -463,7 +473,8 @@ fa_status fa_cache_append_q8(void* k_cache, void* v_cache, float* k_scale, float
     // a warp for a unit where it keeps all of its rows
     const int unit_rows = n < block ? n : block;
     const bool warp = unit_rows <= 32 / a.tasks * kKeptWarp;
-    const int threads = warp || unit_rows <= 128 / a.tasks * kKeptCta ? 128 : 256;
+    const bool many = (long long)batch * a.units * hkv > kFewUnits;
+    const int threads = warp || (many && unit_rows <= 128 / a.tasks * kPasses) ? 128 : 256;
     a.kv_ctas = warp ? (2 * hkv + 3) / 4 : 2 * hkv;
     long long q_ctas = 0;
     if (a.hq > 0 && n > 0) {
