@@ -3,12 +3,15 @@
 // (fa_cache_append_rope).
 //
 // Each element is read once and written once, 4 bytes moved for 3 operations:
-// bound by the memory.  What could hold it up is the angles, 25 instructions a
-// pair; they are the same for all heads of a token, so a thread takes one task
-// (16 elements, 8 pairs) of up to kHeads heads of a token, computes their angles
-// once while the rows are on their way, and turns them one after the other.
-// Where there are few rows, threads take one head each: a call is then bound by
-// the chain of its loads, and every row is in flight at once.
+// bound by the memory (8,192 tokens x 40 heads of 128: 27.0 us, 6.2 TB/s, 93% of a
+// copy's).  What could hold it up is the angles, 15 instructions a pair; they are the
+// same for all heads of a token, so a thread takes one task (16 elements, 8 pairs) of
+// up to kHeads heads of a token, computes their angles once while the rows are on their
+// way, and turns them one after the other.  Where there are few rows, threads take one
+// head each: a call is then bound by the chain of its loads, and every row is in flight
+// at once (one token x 40 heads: 2.1 us on the device).  Rows that pass through once are
+// loaded and stored as such: 28.5 us there without.  (64 threads a CTA: 28.1 where 256
+// took 29.5.)
 #include "../../include/fa.h"
 #include "rope.cuh"
 
@@ -142,13 +145,17 @@ fa_status strides_of(const long long* strides, long long (&to)[3]) {
     return FA_OK;
 }
 
-// Heads of a thread: four where that leaves every SM a full set of threads.
+// Heads of a thread: four past 1,280 tasks (of 16 elements) an SM, else one.  us for
+// 1, 2, 4, 5 and 8 heads: 8,192 tokens x 40 heads of 128 40.7, 30.9, 28.5, 29.3, 31.7;
+// 4 x 2,047 x 32 heads of 96, interleaved, 20.5, 17.9, 17.6, 18.4, 20.5.  One head
+// / four, by tokens x 40 heads of 128: 256 4.6 / 5.1, 512 5.3 / 5.9, 600 6.0 / 6.0,
+// 700 6.8 / 6.2, 1,000 8.0 / 6.5, 4,000 22.9 / 15.4.
 constexpr int kHeads = 4;
-constexpr long long kManyTasks = 152ll * 2048;
+constexpr long long kManyTasks = 152ll * 1280;
 
 fa_status launch_rope(RopeArgs& a, int batch, cudaStream_t s) {
     const long long rows = (long long)a.n * a.tasks;
-    const bool many = rows * a.heads * batch >= kManyTasks * kHeads;
+    const bool many = rows * a.heads * batch >= kManyTasks;
     const int per = many ? kHeads : 1;
     const long long ctas = (rows * ((a.heads + per - 1) / per) + kThreads - 1) / kThreads;
     long long copy_ctas = 0;

@@ -11,7 +11,8 @@
 // 6.7e-9 and 2.3e-10, 1.6e-7 with the roundings of fp32, and w itself by 2^-24).  Two
 // angles an instruction for all but the whole numbers: about 15 an angle, with no
 // range reduction, no branch and no selects, which the appends have too many of
-// (with quarter turns, whose sines and cosines change places, 8-bit chunks took 15 us).
+// (with quarter turns, whose sines and cosines change places, one at a time, chunks of
+// 8 x 1,024 tokens appended to an 8-bit cache and read back took 37.4 us for 35.7).
 #pragma once
 
 #include <atomic>

@@ -429,13 +429,14 @@ fa_status fa_cache_compact(void *k_cache, void *v_cache, int num_pages, int hkv,
  *   stands at positions[b * position_stride + i].  An output may be its input
  *   (in place); else it must not overlap an input.  inverse nonzero: by the angle
  *   -t, the transpose: the gradient of the inputs from that of the outputs.
- *   batch <= 65535, hq + hk <= 65535.
+ *   batch <= 65535, hq + hk <= 65535, n (hq + hk) head_dim / 16 < 2^31.
  * fa_turn: how an append turns keys, and the queries that it turns beside them.
  *   positions NULL: row i of entry b stands at seqlens[b] + i, its key; else
  *   at positions[b * position_stride + i].  q: hq heads (0: none) [batch, hq, n,
  *   head_dim] with q_strides as above; q_out [batch, hq, n, head_dim] contiguous, its
  *   rows i >= n_new[b] are not written.
  * fa_cache_append_rope: fa_cache_append with keys turned (values are not).
+ *   batch <= 65535, hkv <= 20000, hq <= 20000, n (hq + 2 hkv) head_dim / 16 < 2^31.
  */
 typedef struct fa_turn {
     const long long *freqs;
@@ -489,14 +490,16 @@ fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int 
  *   aligned), rounded once; the layout of fa_fwd_prefill_varlen.  max_seqlen is at
  *   least every length (rows beyond it are not written); keys without a page read as
  *   zeros.  Offsets are clamped to [0, total].
- * head_dim of both is a multiple of 16.
+ * Both: head_dim is a multiple of 16 and at most 2048, batch <= 65535, hkv <= 16000,
+ *   max_pages * page_size < 2^31, block * head_dim / 16 < 2^30; the append's n < 2^30
+ *   and n hq head_dim / 16 < 2^31.
  *
  * fa_fwd_decode_paged_q8: fa_fwd_decode_paged_first over such a cache: causal or
  *   not, window <= 0 or a window with `first` visible first keys (0: none), sinks or
  *   NULL.  Queries, probabilities and values are multiplied in fp16 with fp32 sums:
  *   codes exactly, queries to 2^-11 (elements below 2^-14 of their row's largest to
  *   2^-25 of that), a probability times its value's scale to 2^-11.  Scales must
- *   be finite and not negative; keys that no query row of the sequence sees may hold
+ *   be finite and not negative (a value's below 2^-126 counts as zero); keys that no query row of the sequence sees may hold
  *   anything, their scales too.  Keys whose entry is no page read as zeros.
  *   head_dim 64, 128 or 256; num_pages * hkv < 2^31.
  */
