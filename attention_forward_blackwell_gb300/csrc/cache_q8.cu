@@ -298,6 +298,7 @@ __global__ void append_q8_kernel(const AppendArgs a) {
 struct ReadArgs {
     Q8Cache c;
     int tasks;
+    int tokens;                // of a CTA
     FastDiv by_hkv;
     const int* cu;             // [batch + 1]
     int total;
@@ -305,62 +306,76 @@ struct ReadArgs {
 };
 
 constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 16;   // of a CTA, all heads
-constexpr int kReadFlight = 4;    // granules (8 codes) a thread has in flight
+constexpr int kReadTokens = 64;   // of a CTA, all heads, at most
+// Tasks (16 codes) a thread has in flight: 8 x 2,500 tokens x 8 heads of 128 21.3 us with
+// one, 18.7 with two, 19.2 with three, 18.8 with four; 1 x 4,000 7.1, 6.7, 5.3, 6.0.
+constexpr int kReadFlight = 4;
+// Below as many CTAs (two an SM) they take fewer tokens: 1,000 tokens x 8 heads 3.4 us so,
+// 3.9 with half as many, 4.5 with four times; 8 x 2,500 tokens x 2 heads 6.5, 6.5, 6.0.
+constexpr int kReadCtas = 304;
 
-// CTA (tokens of a sequence, keys or values, batch entry).  The tokens' pages are looked
-// up once, by a thread each; then granules of 8 codes in, 16 bytes out, a warp 256 and
-// 512 bytes in a row, four granules a thread in flight.
+// CTA (tokens of a sequence, keys or values, batch entry).  Where the tokens lie is
+// looked up once, by a thread each; then tasks of two granules of 8 codes, half a row
+// apart as in rope.cuh: 8 bytes in and 16 out each.  3 bytes move for an element, and
+// what can hold them up is the instructions: 16 x 5,000 tokens x 8 heads of 128 take
+// 74.3 us, 6.6 TB/s, 99% of a copy's rate (one granule a thread with its page and
+// address worked out for each: 82.2).
 __global__ void __launch_bounds__(kReadThreads) read_q8_kernel(const ReadArgs a) {
-    __shared__ int page_of[kReadTokens], row_of[kReadTokens], block_of[kReadTokens];
+    __shared__ long long code_at[kReadTokens], scale_at[kReadTokens];   // of head 0; -1: no page
     dependents_may_start();
     wait_for_previous();
     const Q8Cache& c = a.c;
-    const int b = blockIdx.z, kind = blockIdx.y, t0 = blockIdx.x * kReadTokens;
+    const int b = blockIdx.z, kind = blockIdx.y, t0 = blockIdx.x * a.tokens;
     const int q0 = min(max(a.cu[b], 0), a.total);
     const int len = min(max(a.cu[b + 1], q0), a.total) - q0;
-    const int count = min(kReadTokens, len - t0);
+    const int count = min(a.tokens, len - t0);
     if (count <= 0) return;
-    if (threadIdx.x < kReadTokens) {
-        int page = -1, row = 0;
-        if (!key_page(c.pages, b, (long long)t0 + threadIdx.x, page, row)) page = -1;
-        page_of[threadIdx.x] = page;
-        row_of[threadIdx.x] = row;
-        block_of[threadIdx.x] = (int)c.by_block((unsigned)row);
+    const int G = 2 * a.tasks;   // granules of a row
+    const size_t head_step = (size_t)c.pages.page_size * G;
+    if ((int)threadIdx.x < count) {
+        int page, row;
+        const bool there = key_page(c.pages, b, (long long)t0 + threadIdx.x, page, row);
+        code_at[threadIdx.x] = there ? (long long)(page * (size_t)c.hkv * head_step + (size_t)row * G) : -1;
+        if (there) scale_at[threadIdx.x] = (long long)page * c.hkv * c.blocks + c.by_block((unsigned)row);
     }
     __syncthreads();
-    const int G = 2 * a.tasks, slots = kReadThreads / G;   // granules of a row, rows at a time
-    const int slot = threadIdx.x / G, j = threadIdx.x - slot * G;
+    const int slots = kReadThreads / a.tasks, slot = threadIdx.x / a.tasks, j = threadIdx.x - slot * a.tasks;
     if (slot >= slots) return;
     const uint2* const codes = reinterpret_cast<const uint2*>(kind == 0 ? c.codes[0] : c.codes[1]) + j;
     const float* const scales = kind == 0 ? c.scales[0] : c.scales[1];
     uint4* const out = (kind == 0 ? a.out[0] : a.out[1]) + (size_t)(q0 + t0) * c.hkv * G + j;
     const int rows = count * c.hkv;   // (token, head), the head fastest
     for (int r0 = slot; r0 < rows; r0 += kReadFlight * slots) {
-        uint2 u[kReadFlight];
+        uint2 u[kReadFlight], w[kReadFlight];
         float s[kReadFlight];
 #pragma unroll
         for (int k = 0; k < kReadFlight; ++k) {
             const int r = r0 + k * slots;
-            u[k] = make_uint2(0, 0);
+            u[k] = w[k] = make_uint2(0, 0);
             s[k] = 0.f;
             if (r >= rows) continue;
-            const int t = (int)a.by_hkv((unsigned)r), page = page_of[t];
-            if (page < 0) continue;
-            const size_t head = (size_t)page * c.hkv + (r - t * c.hkv);
-            u[k] = codes[(head * c.pages.page_size + row_of[t]) * G];
-            s[k] = scales[head * c.blocks + block_of[t]];
+            const int t = (int)a.by_hkv((unsigned)r), h = r - t * c.hkv;
+            const long long at = code_at[t];
+            if (at < 0) continue;
+            const uint2* const p = codes + (at + h * head_step);
+            u[k] = p[0];
+            w[k] = p[a.tasks];
+            s[k] = scales[scale_at[t] + h * c.blocks];
         }
 #pragma unroll
         for (int k = 0; k < kReadFlight; ++k) {
             const int r = r0 + k * slots;
             if (r >= rows) continue;
-            float x[4], y[4];
-            q8_floats(u[k].x, x);
-            q8_floats(u[k].y, y);
-            __stcs(out + (size_t)r * G,
-                   make_uint4(pack_bf16x2(x[0] * s[k], x[1] * s[k]), pack_bf16x2(x[2] * s[k], x[3] * s[k]),
-                              pack_bf16x2(y[0] * s[k], y[1] * s[k]), pack_bf16x2(y[2] * s[k], y[3] * s[k])));
+            uint4* const to = out + (size_t)r * G;
+            const float2 by = both(s[k]);
+            auto four = [&](uint32_t four_codes) {
+                const float2 x = fmul2(halves_to_floats(q8_halves(four_codes)), by);
+                const float2 y = fmul2(halves_to_floats(q8_halves_up(four_codes)), by);
+                return make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(y.x, y.y));
+            };
+            const uint2 u0 = four(u[k].x), u1 = four(u[k].y), w0 = four(w[k].x), w1 = four(w[k].y);
+            __stcs(to, make_uint4(u0.x, u0.y, u1.x, u1.y));
+            __stcs(to + a.tasks, make_uint4(w0.x, w0.y, w1.x, w1.y));
         }
     }
 }
@@ -517,7 +532,12 @@ fa_status fa_cache_read_q8(const void* k_cache, const void* v_cache, const float
     a.out[1] = static_cast<uint4*>(v_out);
     if ((st = sm103_or_status()) != FA_OK) return st;
     const int longest = max_seqlen < total ? max_seqlen : total;
-    const dim3 grid((unsigned)((longest + kReadTokens - 1) / kReadTokens), 2, (unsigned)batch);
+    // tokens that give each thread what it has in flight, fewer where the CTAs are few
+    a.tokens = kReadFlight * (kReadThreads / a.tasks) / hkv;
+    if (a.tokens > kReadTokens) a.tokens = kReadTokens;
+    while (a.tokens > 1 && 2ll * total / a.tokens < kReadCtas) a.tokens /= 2;
+    if (a.tokens < 1) a.tokens = 1;
+    const dim3 grid((unsigned)((longest + a.tokens - 1) / a.tokens), 2, (unsigned)batch);
     const cudaError_t e = launch_dependent(read_q8_kernel, grid, dim3(kReadThreads), 0,
                                            reinterpret_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
