@@ -1,5 +1,9 @@
 """The rotation, the appends and the 8-bit cache's calls together, as a serving loop uses them: steps over
-forked sequences, prompts in chunks, captured and replayed, on streams of their own (GPU)."""
+forked sequences, prompts in chunks, captured and replayed, on streams of their own, and as the README writes
+them (GPU)."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -325,3 +329,47 @@ def test_long_lines(fa):
         assert torch.all((o[b].double() - want).abs() <= bound), f"sequence {b}"
         assert torch.all((lse[b].double() - l).abs() <= e + r * (1 + l.abs())), f"sequence {b}"
     check_device_error()
+
+
+def test_readme(fa):
+    """The README's steps over an 8-bit cache, run as they are written."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        code = [c for c in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "cache_append_q8" in c]
+    assert len(code) == 1
+    g = torch.Generator().manual_seed(9)
+    B, hq, hkv, d, P, lens, chunks = 3, 4, 2, 128, 16, [40, 0, 17], [5, 30, 1]
+    kc, ks = ref.codes8(g, 20, hkv, P, P, d)
+    vc, vs = ref.codes8(g, 20, hkv, P, P, d)
+    table = i32([[4, 9, 2, 7], [1, 3, -1, -1], [12, 11, 10, -1]])
+    old = gathered(((kc, ks), (vc, vs)), table.cpu(), [max(n, 1) for n in lens])
+    n, now = max(chunks), [a + c for a, c in zip(lens, chunks)]
+    x = {w: randn(g, B, h, m, d) for w, h, m in (("q", hq, n), ("k_new", hkv, n), ("v_new", hkv, n),
+                                                 ("q1", hq, 1), ("k1", hkv, 1), ("v1", hkv, 1))}
+    cu = lambda v: i32([sum(v[:i]) for i in range(len(v) + 1)])
+    names = dict(torch=torch, binding=fa, k8=kc, v8=vc, ks=ks, vs=vs, table=table, lens=i32(lens), chunks=chunks,
+                 n_new=i32(chunks), cu_k=cu(now), cu_q=cu(chunks), total_k=sum(now), longest=max(now),
+                 **{w: t.cuda() for w, t in x.items()})
+    exec(code[0], names)
+    check_device_error()
+    m = [a + 1 for a in now]
+    assert names["lens"].tolist() == m
+    (k, sk), (v, sv) = gathered(((kc, ks), (vc, vs)), table.cpu(), m)
+    inv, factor = names["inv_freq"], names["factor"]
+    assert factor > 1
+    for b in range(B):
+        rows = torch.cat([x["k_new"][b, :, :chunks[b]], x["k1"][b]], 1)
+        want = ref.turn64(rows, torch.arange(lens[b], m[b]), inv, factor)
+        near_rows(k[b, :, lens[b]:m[b]], sk[b, :, lens[b]:m[b]], want, f"keys of {b}")
+        near_rows(k[b, :, :lens[b]], sk[b, :, :lens[b]], old[0][0][b, :, :lens[b]], f"earlier keys of {b}")
+        qr = names["qr"][b, :, :chunks[b]]
+        want = ref.turn64(x["q"][b, :, :chunks[b]], torch.arange(lens[b], now[b]), inv, factor)
+        assert torch.all((qr.cpu().double() - want).abs() <=
+                         ref.turn_bound(x["q"][b, :, :chunks[b]], want, torch.arange(lens[b], now[b]), d, factor, False))
+        at = slice(sum(now[:b]), sum(now[:b + 1]))
+        kk, vv = (names[w][at].transpose(0, 1)[None] for w in ("k", "v"))
+        seen = serving_ref.window_seen(chunks[b], [now[b]], now[b], 0, 0, True)
+        at = slice(sum(chunks[:b]), sum(chunks[:b + 1]))
+        serving_ref.check(names["o"][at].transpose(0, 1)[None], names["lse"][:, at][None],
+                          serving_ref.attention64(qr[None], kk, vv, seen, d ** -0.5), f"chunk {b}")
+    want = ref.attention8(names["q1r"], k, v, sv, serving_ref.window_seen(1, m, max(m), 0, 0, True), d ** -0.5)
+    serving_ref.check(names["o1"], names["lse1"], want, "next token")
