@@ -57,7 +57,11 @@ APPENDS = [  # lens, n, counts, hkv, d, page, block, rot, interleaved, hq
     ([3, 500], 300, [300, 299], 1, 128, 256, 256, 0, False, 2),
     ([2, 9], 9, None, 2, 80, 16, 4, 80, False, 2),
     ([129, 77], 600, [600, 513], 2, 256, 256, 128, 256, False, 0),
-    ([4, 4], 5, [-3, 9], 1, 64, 1, 1, 16, False, 1)]
+    ([4, 4], 5, [-3, 9], 1, 64, 1, 1, 16, False, 1),
+    # many units: of 128 threads with two tasks kept or more, of a warp
+    ([7 * i % 50 for i in range(30)], 40, [41 - i for i in range(30)], 8, 128, 64, 32, 128, False, 0),
+    (list(range(26)), 50, None, 8, 64, 64, 64, 32, True, 1), ([13 * i for i in range(40)], 2, None, 16, 96, 32, 4, 48, False, 3),
+    ([3, 0], 30, None, 1, 1024, 16, 16, 512, False, 2)]
 
 
 @pytest.mark.parametrize("lens,n,counts,hkv,d,page,block,rot,interleaved,hq", APPENDS)
@@ -259,7 +263,10 @@ def test_scales_of_other_kinds(fa):
 
 
 @pytest.mark.parametrize("lens,hkv,d,page,block", [([1], 1, 64, 16, 16), ([0, 5, 300, 0, 64], 3, 128, 64, 16),
-                                                   ([33, 1000], 2, 256, 100, 50), ([700, 17], 8, 80, 48, 12)])
+                                                   ([33, 1000], 2, 256, 100, 50), ([700, 17], 8, 80, 48, 12),
+                                                   # many tokens to a CTA, one, heads past a CTA's threads
+                                                   ([2500, 0, 37], 8, 128, 64, 64), ([6000, 3999], 1, 64, 64, 64),
+                                                   ([40, 3], 1, 2048, 16, 16), ([9, 70], 40, 256, 32, 8)])
 def test_read(fa, lens, hkv, d, page, block):
     g = torch.Generator().manual_seed(d)
     table, pages = tables(g, lens, 0, page)
