@@ -692,9 +692,9 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
         a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
         return from_cuda(launch_decode_q8(p, head_dim, s));
     }
-    // (the kernel counts the blocks of all units in 32 bits)
-    const double blocks = (double)pairs * (double)((span + keys - 1) / keys);
-    if (blocks >= 2147483647.0 - 65536) return FA_ERR_INVALID_ARG;
+    // (the kernel counts the blocks of all units, and their leads, in 32 bits)
+    const double blocks = (double)pairs * (double)fine;
+    if (blocks + kQ8Lead * (double)pairs >= 2147483647.0 - 65536) return FA_ERR_INVALID_ARG;
     a.slots = (int)std::min<double>((double)wave, blocks);
     // pieces for every SM to take when it is done with its own, where there may be much
     a.levels = blocks >= 48.0 * a.slots ? 2 : 0;

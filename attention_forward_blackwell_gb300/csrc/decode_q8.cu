@@ -70,7 +70,6 @@ constexpr float kFar = 3.0e38f;  // minus a base of a row that has seen nothing
 constexpr unsigned kSiteQ8 = 72; // wait site of the ring
 
 constexpr int kLeastKeys = 256;  // of a piece
-constexpr int kSegmentBlocks = 2; // what a segment's set-up and merge are worth
 constexpr int kManyBlocks = 48;  // a CTA's share from which part of it goes in small pieces
 
 template <int D, int NR>
@@ -155,13 +154,15 @@ __device__ __forceinline__ int keys_of(const DecodeQ8Args& a, int b) {
     return max(0, min(a.seqlens_k[b], a.Sk));
 }
 
-// How the units' blocks, one unit after the other on a line of `all`, are cut: into
-// `slots` pieces of `big` blocks, then `small` ones up to the line's end; or, with
-// `aligned` blocks to a piece, unit by unit (the line then counts pieces).
+// How the units, one after the other on a line of `all`, are cut: a unit takes a lead
+// of kQ8Lead, what its set-up and merge are worth, and its blocks; the line is cut
+// into `slots` pieces of `big`, then `small` ones up to its end.  Or, with `aligned`
+// blocks to a piece, unit by unit (the line then counts pieces).
 struct Line {
     int all, slots, big, small, aligned;
+    __device__ __forceinline__ int lead() const { return aligned > 0 ? 0 : kQ8Lead; }
     __device__ __forceinline__ int of_unit(int nb) const {   // what a unit of nb blocks takes of the line
-        return aligned > 0 ? (nb + aligned - 1) / aligned : nb;
+        return aligned > 0 ? (nb + aligned - 1) / aligned : nb + kQ8Lead;
     }
     __device__ __forceinline__ int from(int x) const {   // where piece x starts
         if (aligned > 0) return min(x, all);
@@ -185,6 +186,10 @@ __device__ __forceinline__ int sum_blocks(const DecodeQ8Args& a, int b0, int b1,
     return sum;
 }
 
+// (Leads, us without / with: 300 x 10 to 4,000 keys x 2 heads at head_dim 128 86.5 / 57.9;
+// 128 x 100 to 800 x 8 42.4 / 36.4, at 256 78.3 / 58.9; a lead of one block 35.4 and 62.9
+// there, of three 35.7 and 58.3; 16 x 1K to 16K x 8 at 128 53.9 / 54.2.)
+//
 // The line's cut, by a warp together, each lane with its share of the batch.  Pieces
 // that end with their units save the set-up and merge of a second segment, worth
 // about two blocks: taken where such pieces, one for every CTA at most, are no more
@@ -198,14 +203,16 @@ __device__ __forceinline__ Line cut_line(const DecodeQ8Args& a, int& mine) {
     Line line;
     line.slots = a.slots;
     line.aligned = 0;
-    mine = units * sum_blocks<BLOCK>(a, b0, b1, [](int nb) { return nb; });
+    const int blocks = units * sum_blocks<BLOCK>(a, b0, b1, [](int nb) { return nb; });
+    mine = blocks + kQ8Lead * units * max(0, b1 - b0);
     line.all = __reduce_add_sync(0xffffffffu, mine);
     const int share = (int)(((unsigned)line.all + (unsigned)a.slots - 1) / (unsigned)a.slots);
-    const int least = max(1, kLeastKeys / BLOCK), cut = max(share, least);
+    const int least = max(1, kLeastKeys / BLOCK);
     line.small = a.levels > 0 && share >= kManyBlocks ? share / (4 * a.levels) : 0;
     line.big = max(share - a.levels * line.small, least);
     if (line.small == 0 && a.B * units <= a.slots) {
-        for (int s = cut; s <= cut + kSegmentBlocks && line.aligned == 0; ++s) {
+        const int total = __reduce_add_sync(0xffffffffu, blocks), cut = max((total + a.slots - 1) / a.slots, least);
+        for (int s = cut; s <= cut + kQ8Lead && line.aligned == 0; ++s) {
             const int count = units * sum_blocks<BLOCK>(a, b0, b1, [&](int nb) { return (nb + s - 1) / s; });
             const int all = __reduce_add_sync(0xffffffffu, count);
             if (all <= a.slots) {
@@ -219,10 +226,10 @@ __device__ __forceinline__ Line cut_line(const DecodeQ8Args& a, int& mine) {
     return line;
 }
 
-// Where position pos < line.all lies: batch entry, its units' start on the line, unit,
-// place in it, and the unit's blocks.  (A warp together; mine: of cut_line.)
+// Where position pos < line.all lies: batch entry, unit, the unit's start on the line,
+// place in it, and its blocks.  (A warp together; mine: of cut_line.)
 struct Spot {
-    int b, start, u, at, nb;
+    int b, u, start, at, nb;
 };
 template <int BLOCK>
 __device__ __forceinline__ Spot find_on_line(const DecodeQ8Args& a, const Line& line, int mine, int pos) {
@@ -249,20 +256,22 @@ __device__ __forceinline__ Spot find_on_line(const DecodeQ8Args& a, const Line& 
     p.start = __shfl_sync(0xffffffffu, at, from_lane);
     const int len = line.of_unit(p.nb);
     p.u = (pos - p.start) / len;
-    p.at = pos - p.start - p.u * len;
+    p.start += p.u * len;
+    p.at = pos - p.start;
     return p;
 }
 
-// The pieces of a unit that takes [from, from + len) of the line: the first one,
-// their number, and whether the first is its CTA's second slot.
+// The pieces that hold blocks of a unit of nb blocks that starts at `from` on the line:
+// the first one, their number, and whether the first is its CTA's second slot (it holds
+// what comes before the unit, which ends with a block).
 struct Pieces {
     int first, count, second;
     __device__ __forceinline__ int slot(int k) const { return k == 0 ? 2 * first + second : 2 * (first + k); }
 };
-__device__ __forceinline__ Pieces pieces_of(const Line& line, int from, int len) {
+__device__ __forceinline__ Pieces pieces_of(const Line& line, int from, int nb) {
     Pieces p;
-    p.first = line.piece_of(from);
-    p.count = line.piece_of(from + len - 1) - p.first + 1;
+    p.first = line.piece_of(from + line.lead());
+    p.count = line.piece_of(from + line.of_unit(nb) - 1) - p.first + 1;
     p.second = from > line.from(p.first) ? 1 : 0;
     return p;
 }
@@ -303,13 +312,23 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         const Line line = cut_line<T::BLOCK>(a, mine);
         const int begin = line.from(blockIdx.x);
         if (begin >= line.all) return;
-        spot = find_on_line<T::BLOCK>(a, line, mine, begin);
+        const int end = line.from(blockIdx.x + 1);
+        blocks = line.all - kQ8Lead * a.B * units;   // before the end, where the line ends there
+#pragma unroll 1
+        for (int side = end < line.all && line.aligned == 0 ? 1 : 0; side >= 0; --side) {
+            spot = find_on_line<T::BLOCK>(a, line, mine, side ? end : begin);
+            // blocks before the position: those of the units before, and of its own
+            const int before = spot.start - kQ8Lead * (spot.b * units + spot.u) +
+                               max(0, spot.at - kQ8Lead);
+            blocks = side ? before : blocks - before;
+        }
         if (line.aligned > 0) {
             spot.at *= line.aligned;
             blocks = min(line.aligned, spot.nb - spot.at);
         } else {
-            blocks = line.from(blockIdx.x + 1) - begin;
+            spot.at = max(0, spot.at - kQ8Lead);
         }
+        if (blocks == 0) return;   // (a piece within a lead)
         if (threadIdx.x == 0) *kept = line;
     }
 
@@ -832,8 +851,8 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         // (the unit starts here and goes on: what the merge by pieces has to know)
         if (kb == 0 && !whole_unit && a.head != nullptr && threadIdx.x == 0) {
             const Line cut = *kept;
-            const Pieces pc = cut.aligned > 0 ? Pieces{(int)blockIdx.x, cut.of_unit(nb), 0}
-                                              : pieces_of(cut, cut.from(blockIdx.x) + (blocks - left), nb);
+            const int from = cut.aligned > 0 ? (int)blockIdx.x : cut.from(blockIdx.x + 1) - n - kQ8Lead;
+            const Pieces pc = pieces_of(cut, from, nb);
             a.head[blockIdx.x] = make_int4(b, at_unit, pc.count, pc.second);
         }
         left -= n;
@@ -919,7 +938,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_q8_kernel(const De
     for (int i = lane; i < b; i += 32)
         before += units * line.of_unit(unit_blocks<BLOCK>(key_axis(a, keys_of(a, i)).span));
     before = __reduce_add_sync(0xffffffffu, before);
-    const Pieces pc = pieces_of(line, before + u * len, len);
+    const Pieces pc = pieces_of(line, before + u * len, nb);
     if (pc.count < 2) return;
     const int h = hkv * a.group + pr / a.Sq;
     auto at = [&](int k) { return (size_t)pc.slot(k) * tile + r; };
