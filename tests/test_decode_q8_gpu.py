@@ -105,6 +105,18 @@ def test_wide_tables(fa, lens, hq, hkv, n, d, page, block):
     run(fa, d + hq + 1, lens, hq, hkv, n, d, page, block, causal=True, width=-(-6000 // page))
 
 
+MANY = [  # lens, hq, hkv, n, d, page, block: several units to a piece, empty and long ones among them
+    ([7 * i % 45 for i in range(300)], 4, 2, 1, 64, 16, 16), ([1500 if i % 23 == 5 else i % 40 for i in range(70)], 15, 3, 2, 128, 16, 8),
+    ([0] * 40 + [700, 1, 64, 0, 65], 16, 8, 1, 256, 32, 32), ([200 + 13 * i for i in range(50)], 20, 4, 5, 64, 48, 12),
+    ([130] * 257, 2, 2, 1, 128, 26, 13)]
+
+
+@pytest.mark.parametrize("width", [None, 300])
+@pytest.mark.parametrize("lens,hq,hkv,n,d,page,block", MANY)
+def test_many_sequences(fa, lens, hq, hkv, n, d, page, block, width):
+    run(fa, d + hq + 2, lens, hq, hkv, n, d, page, block, causal=True, width=width, sinks=width is None)
+
+
 WINDOWS = [  # lens, hq, hkv, n, d, page, block, window, first, width
     ([300, 40, 0], 4, 1, 1, 128, 16, 16, 64, 0, None), ([300, 40, 5], 4, 2, 3, 64, 48, 12, 50, 4, None),
     ([3000, 900], 8, 1, 1, 128, 64, 64, 256, 130, 200), ([3000, 64], 16, 2, 4, 256, 128, 64, 1, 1, None),
