@@ -80,6 +80,7 @@ struct Q8Traits {
     static constexpr int SUB = D == 256 ? 1 : 2;        // 16-key parts of a slice
     static constexpr int KB = 16 * SUB;                 // keys of a slice
     static constexpr int BLOCK = WARPS * KB;            // keys of a block
+    static constexpr int SUMS = NR == 1 ? 2 : 1;         // of a score, side by side
     static constexpr int SW = SUB;                       // parts worked on together
     static constexpr bool KEEP = NR == 1 || (D != 256 && NR == 2);   // exponents kept over the vote
     static constexpr int PITCH = D == 64 ? 64 : 128;    // bytes of a box's row
@@ -548,9 +549,12 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
 #pragma unroll
                 for (int w = 0; w < T::SW; ++w) {
                     const int u16 = 16 * (part + w);
-                    float sum[NR][4];
+                    float sums[T::SUMS][NR][4];
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) sum[nr][0] = sum[nr][1] = sum[nr][2] = sum[nr][3] = 0.f;
+                    for (int i = 0; i < T::SUMS; ++i)
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr)
+                            sums[i][nr][0] = sums[i][nr][1] = sums[i][nr][2] = sums[i][nr][3] = 0.f;
 #pragma unroll
                     for (int c = 0; c < D / 64; ++c) {
                         const uint32_t at = (sk0 ^ ((c & 1) * 64)) + (c >> 1) * T::CHUNK + u16 * T::PITCH;
@@ -562,9 +566,17 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                             const uint32_t a2 = q8_halves_up(xx[e]), a3 = q8_halves_up(yy[e]);
 #pragma unroll
                             for (int nr = 0; nr < NR; ++nr)
-                                mma_f16_16816(sum[nr], a0, a1, a2, a3, qb[nr][c][2 * e], qb[nr][c][2 * e + 1]);
+                                mma_f16_16816(sums[(4 * c + e) % T::SUMS][nr], a0, a1, a2, a3, qb[nr][c][2 * e],
+                                              qb[nr][c][2 * e + 1]);
                         }
                     }
+                    auto sum_of = [&](int nr, int f) {
+                        float2 x = make_float2(sums[0][nr][2 * f], sums[0][nr][2 * f + 1]);
+#pragma unroll
+                        for (int i = 1; i < T::SUMS; ++i)
+                            x = fadd2(x, make_float2(sums[i][nr][2 * f], sums[i][nr][2 * f + 1]));
+                        return x;
+                    };
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
                         const uint32_t at = sc0 + (2 * (part + w) + f) * scale_step;
@@ -572,8 +584,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
                         lv[w][f] = lg2_approx(lds32(at + T::KB * 4));
 #pragma unroll
                         for (int nr = 0; nr < NR; ++nr)
-                            s[w][nr][f] = fmul2(make_float2(sum[nr][2 * f], sum[nr][2 * f + 1]),
-                                                fmul2(unit[nr], make_float2(ks, ks)));
+                            s[w][nr][f] = fmul2(sum_of(nr, f), fmul2(unit[nr], make_float2(ks, ks)));
                     }
                     if (!whole) {
 #pragma unroll
