@@ -696,8 +696,12 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     const double blocks = (double)pairs * (double)fine;
     if (blocks + kQ8Lead * (double)pairs >= 2147483647.0 - 65536) return FA_ERR_INVALID_ARG;
     a.slots = (int)std::min<double>((double)wave, blocks);
-    // pieces for every SM to take when it is done with its own, where there may be much
-    a.levels = blocks >= 48.0 * a.slots ? 2 : 0;
+    // small pieces for the SMs that are done with their own first, where there may be much
+    // and bytes bound it: with more rows, or fewer and larger CTAs, SMs end together and
+    // pieces only cost.  us without / with them, 8 heads: 64 x 1K to 16K keys at head_dim 128
+    // 183 / 178, 300 x 1 to 12K 568 / 537, at 64 303 / 289; 16 rows, 64 x 1K to 16K at 128 191 / 200,
+    // at 64 124 / 139; 8 rows at 256 338 / 344, 16 x 1K to 16K 96 / 113
+    a.levels = tile == 8 && head_dim < 256 && blocks >= 48.0 * a.slots ? 2 : 0;
     a.n_splits = a.slots * (1 + a.levels);
     const size_t parts = 2ull * a.n_splits * tile;
     const size_t bytes_o = parts * head_dim * sizeof(float), bytes_l = (parts * sizeof(float) + 15) / 16 * 16;

@@ -194,9 +194,8 @@ __device__ __forceinline__ int sum_blocks(const DecodeQ8Args& a, int b0, int b1,
 // The line's cut, by a warp together, each lane with its share of the batch.  Pieces
 // that end with their units save the set-up and merge of a second segment, worth
 // about two blocks: taken where such pieces, one for every CTA at most, are no more
-// than that much longer.  A long line leaves a quarter of itself to small pieces, for
-// the SMs that are done with their own first (equal shares alone ended 12% apart: 64 x
-// 1K to 16K keys x 8 heads 188 us, so 181).
+// than that much longer.  A long line may leave a quarter of itself to small pieces, for
+// the SMs that are done with their own first (a.levels; api.cu says when).
 template <int BLOCK>
 __device__ __forceinline__ Line cut_line(const DecodeQ8Args& a, int& mine) {
     const int lane = threadIdx.x & 31, units = a.Hkv * a.tiles;
