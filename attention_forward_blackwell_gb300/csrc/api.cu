@@ -662,9 +662,6 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.Sk = sk;
     a.group = hq / hkv;
     a.rows = a.group * sq;
-    const int tile = decode_q8_tile(head_dim, a.rows);
-    a.tiles = (a.rows + tile - 1) / tile;
-    if ((long long)hkv * a.tiles > 65535) return FA_ERR_INVALID_ARG;
     a.causal = causal ? 1 : 0;
     a.window = window_of(window, sk);
     a.first = window > 0 ? std::min(first, sk) : 0;
@@ -681,11 +678,20 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.scale_log2 = scale * 1.4426950408889634f;
     const long long heads_first = (a.first + 63ll) / 64 * 64;
     const long long span = window > 0 ? std::min<long long>(sk, (long long)window + sq + 62 + heads_first) : sk;
-    const long long pairs = (long long)batch * hkv * a.tiles;
     const int keys = decode_q8_block(head_dim);
-    const long long wave = (long long)di->num_sms * decode_q8_ctas(head_dim, tile);   // CTAs at once
-    const long long fine = (span + keys - 1) / keys;
-    const long long join = std::min(std::min<long long>(fine, kJoinSplits), wave / pairs);
+    const long long fine = (span + keys - 1) / keys, most = std::min<long long>(fine, kJoinSplits);
+    int tile = decode_q8_tile(head_dim, a.rows);
+    auto units = [&](int t) { return (long long)batch * hkv * ((a.rows + t - 1) / t); };
+    auto wave_of = [&](int t) { return (long long)di->num_sms * decode_q8_ctas(head_dim, t); };   // CTAs at once
+    // short caches: narrower tiles, read more than once, while all splits of all fit the SMs
+    // (us, wide / narrow, 1 x 4,000 keys x 8 heads: 32 rows at head_dim 64 13.0 / 8.9, 16 rows at
+    // 128 11.5 / 9.8, at 256 19.4 / 15.2; 1 x 500 9.0 / 5.9, 7.6 / 6.2, 10.3 / 7.8)
+    if (span <= kJoinSplits * join_keys_q8(head_dim))
+        while (tile > 8 && units(tile / 2) * most <= wave_of(tile / 2)) tile /= 2;
+    a.tiles = (a.rows + tile - 1) / tile;
+    p.tile = tile;
+    if ((long long)hkv * a.tiles > 65535) return FA_ERR_INVALID_ARG;
+    const long long pairs = units(tile), wave = wave_of(tile), join = std::min(most, wave / pairs);
     if (join >= std::min(2ll, fine) && span <= join * join_keys_q8(head_dim)) {
         a.joined = 1;
         a.chunk = (int)((fine + join - 1) / join * keys);

@@ -361,12 +361,14 @@ struct DecodeQ8Maps {
 struct DecodeQ8Launch {
     DecodeQ8Maps maps;
     DecodeQ8Args args;
+    int tile;                   // rows of a tile
 };
-// Rows of a tile: 8, 16 or, at head_dim 64, 32.  Wider tiles read and convert the keys
-// less often but hold more registers a warp (us, tiles of 16 / 32 for 16 x 1K to 16K
-// keys x 8 heads, 64 rows: head_dim 64 152 / 134; 32 rows: head_dim 128 109 / 124).
+// Rows of a tile: 8, 16 or, at head_dim 64, 32 where that leaves no half empty.  Wider
+// tiles read and convert the keys less often but hold more registers a warp (us, tiles of
+// 16 / 32 for 16 x 1K to 16K keys x 8 heads: head_dim 64 and 32 rows 68.8 / 65.5, 40 rows
+// 95.2 / 108.9, 64 rows 122 / 114; head_dim 128 and 32 rows 109 / 124).
 inline int decode_q8_tile(int head_dim, int rows) {
-    return rows <= 8 ? 8 : rows <= 16 || head_dim > 64 ? 16 : 32;
+    return rows <= 8 ? 8 : head_dim > 64 || (rows + 15) / 16 % 2 == 1 ? 16 : 32;
 }
 int decode_q8_block(int head_dim);   // keys of a block, four slices
 constexpr int kQ8Lead = 2;           // blocks that a unit's set-up and merge are worth

@@ -1049,7 +1049,7 @@ cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_dim(const DecodeQ8Launch& p, cudaStream_t s) {
-    switch (decode_q8_tile(D, p.args.rows)) {
+    switch (p.tile) {
         case 8: return launch_tile<D, 1>(p, s);
         case 16: return launch_tile<D, 2>(p, s);
         default:
