@@ -38,12 +38,12 @@
 // writes what it has, normalised, with its LSE, and a second kernel merges them in
 // their order.  (The split kernel's grid, one CTA of 256 keys and more for every
 // piece of the longest possible sequence, took 195 us for 64 x 1K to 16K keys x 8
-// heads at head_dim 128, now 177, 6.5 TB/s, and 213 for one of 130,000 keys x 2 heads
+// heads at head_dim 128, now 178, 6.4 TB/s, and 213 for one of 130,000 keys x 2 heads
 // at 256, now 35.  Merged by the CTA that writes a unit's last piece, without a second
 // kernel: 189, for the fences and counts stop its ring.)  Neither kernel lets the
 // next start early: its CTAs would take the places of this one's later pieces (195).
 // Short caches are split over the CTAs of a cluster instead, which merge without a
-// second kernel, as decode.cu's joined splits (2,000 keys x 8 heads 6.9 us).
+// second kernel, as decode.cu's joined splits (2,000 keys x 8 heads 6.7 us).
 //
 // A warp takes a slice of every block through a ring of its own.  Tensor copies
 // fill it, one lane for every box of rows that lie together (a page's, up to 32),
@@ -72,6 +72,15 @@ constexpr unsigned kSiteQ8 = 72; // wait site of the ring
 constexpr int kLeastKeys = 256;  // of a piece
 constexpr int kManyBlocks = 48;  // a CTA's share from which part of it goes in small pieces
 
+// Rows that a CTA of n joined splits holds for its part of a tile's R, n pieces of each.
+// (Not a row more than the most of any n: at head_dim 64 and 128 the CTAs of an SM fill its
+// shared memory to the last kilobyte.)
+constexpr int join_rows(int R) {
+    int most = 0;
+    for (int n = 1; n <= kJoinSplits; ++n) most = (R + n - 1) / n * n > most ? (R + n - 1) / n * n : most;
+    return most;
+}
+
 template <int D, int NR>
 struct Q8Traits {
     static constexpr int WARPS = 4;
@@ -95,12 +104,12 @@ struct Q8Traits {
     static constexpr int BARS = SCALES + WARPS * WARP_SCALES;   // a barrier a slot, the abort flag
     static constexpr int LINE = BARS + (WARPS * STAGES + 1) * 8;
     static constexpr int RING = (LINE + 32 + 15) / 16 * 16;
-    static constexpr int JOIN_ROWS = R + kJoinSplits;   // n splits, ceil(R / n) rows each
+    static constexpr int JOIN_ROWS = join_rows(R);
     static constexpr int JOIN_LSE = (JOIN_ROWS * 4 + 15) / 16 * 16;
     static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
     static constexpr int MT = D / 16;                   // tiles of O^T
     // CTAs of an SM: what the registers of a warp leave.  16 rows with two parts in
-    // hand and two CTAs at head_dim 128 take 66 us where one part and three take 76
+    // hand and two CTAs at head_dim 128 took 66 us where one part and three took 76
     // (16 x 1K to 16K keys x 8 heads; at 64, three for four, 43 for 65).
     static constexpr int MIN_CTAS = D == 256 ? 2 : (D == 64 ? 5 : 4) - (NR == 4 ? 3 : NR);
     // the merge of 8 rows goes through the slot that was read last
