@@ -691,11 +691,15 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.tiles = (a.rows + tile - 1) / tile;
     p.tile = tile;
     if ((long long)hkv * a.tiles > 65535) return FA_ERR_INVALID_ARG;
-    const long long pairs = units(tile), wave = wave_of(tile), join = std::min(most, wave / pairs);
-    if (join >= std::min(2ll, fine) && span <= join * join_keys_q8(head_dim)) {
-        a.joined = 1;
+    const long long pairs = units(tile), wave = wave_of(tile);
+    for (long long join = std::min(most, wave / pairs);
+         join >= std::min(2ll, fine) && span <= join * join_keys_q8(head_dim); --join) {
         a.chunk = (int)((fine + join - 1) / join * keys);
         a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
+        // (a cluster lies within a part of the device: fewer may fit than CTAs do.  A second
+        // wave of them costs more than a split less: 7 x 1,333 to 4,000 keys x 8 heads 18.2 us, so 12.9)
+        if (a.n_splits > 1 && pairs > decode_q8_clusters(head_dim, tile, a.n_splits)) continue;
+        a.joined = 1;
         return from_cuda(launch_decode_q8(p, head_dim, s));
     }
     // (the kernel counts the blocks of all units, and their leads, in 32 bits)

@@ -1022,15 +1022,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_q8_kernel(const De
     if (c == 0) a.lse[row] = sum > 0.f ? (M + lg2_approx(sum)) * kLn2f : -INFINITY;
 }
 
+// (What is asked of the runtime once per device: a small call takes seven microseconds.)
+constexpr int kAlign = 1024, kDevices = 64;
+
+// Lets the kernel have the shared memory that it takes on the current device.
 template <int D, int NR>
-cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
+cudaError_t allow_shared(int& dev) {
     using T = Q8Traits<D, NR>;
-    const DecodeQ8Args& a = p.args;
-    constexpr int kAlign = 1024;
-    // (once per device: a small call takes seven microseconds)
-    constexpr int kDevices = 64;
     static std::atomic<bool> allowed[kDevices];
-    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const bool keep = dev >= 0 && dev < kDevices;
@@ -1040,6 +1039,44 @@ cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         if (keep) allowed[dev].store(true, std::memory_order_relaxed);
     }
+    return cudaSuccess;
+}
+
+// Clusters of n CTAs that the current device holds at once (0: not known).
+template <int D, int NR>
+int clusters_at_once(int n) {
+    using T = Q8Traits<D, NR>;
+    static std::atomic<int> known[kDevices][kJoinSplits + 1];
+    int dev = 0, count = 0;
+    if (n < 1 || n > kJoinSplits || allow_shared<D, NR>(dev) != cudaSuccess) return 0;
+    const bool keep = dev >= 0 && dev < kDevices;
+    if (keep) count = known[dev][n].load(std::memory_order_relaxed);
+    if (count > 0) return count;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)n;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3((unsigned)n);
+    config.blockDim = dim3(T::THREADS);
+    config.dynamicSmemBytes = kAlign + T::RING + T::JOIN;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&count, decode_q8_kernel<D, NR>, &config) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (keep) known[dev][n].store(count, std::memory_order_relaxed);
+    return count;
+}
+
+template <int D, int NR>
+cudaError_t launch_tile(const DecodeQ8Launch& p, cudaStream_t s) {
+    using T = Q8Traits<D, NR>;
+    const DecodeQ8Args& a = p.args;
+    int dev = 0;
+    cudaError_t e = allow_shared<D, NR>(dev);
+    if (e != cudaSuccess) return e;
     if (a.joined)
         return launch_dependent_clusters(
             decode_q8_kernel<D, NR>, (unsigned)a.n_splits,
@@ -1078,6 +1115,17 @@ int decode_q8_ctas(int head_dim, int tile) {
                                 : Q8Traits<64, 4>::MIN_CTAS;
         case 128: return tile == 8 ? Q8Traits<128, 1>::MIN_CTAS : Q8Traits<128, 2>::MIN_CTAS;
         default: return Q8Traits<256, 1>::MIN_CTAS;
+    }
+}
+
+int decode_q8_clusters(int head_dim, int tile, int n) {
+    switch (head_dim) {
+        case 64:
+            return tile == 8    ? clusters_at_once<64, 1>(n)
+                   : tile == 16 ? clusters_at_once<64, 2>(n)
+                                : clusters_at_once<64, 4>(n);
+        case 128: return tile == 8 ? clusters_at_once<128, 1>(n) : clusters_at_once<128, 2>(n);
+        default: return tile == 8 ? clusters_at_once<256, 1>(n) : clusters_at_once<256, 2>(n);
     }
 }
 
