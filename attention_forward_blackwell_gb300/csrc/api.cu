@@ -602,13 +602,20 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
     return FA_OK;
 }
 
-// Most keys of a joined split of an 8-bit cache: past it the line's even pieces gain
-// more than their second kernel costs.  us, line / joined, 8 heads:
-//              4,000 keys     6,000 keys     8,000 keys
-//   d 64       11.1 /  8.1    12.0 /  9.7    11.8 / 11.5
-//   d 128      11.7 /  9.2    11.9 / 11.0    12.9 / 13.0
-//   d 256      14.8 / 13.6    15.6 / 17.6    15.7 / 21.6
-long long join_keys_q8(int head_dim) { return head_dim == 256 ? 512 : 768; }
+// Most keys of a joined split of an 8-bit cache, when the splits fill `fill` of the places
+// that the SMs have for CTAs: past it the line's even pieces gain more than their second
+// kernel costs, which they do the sooner the more places the splits leave empty.  us,
+// line / joined, 8 heads, keys of 1 (fill 0.1 to 0.2), 3 (0.3 to 0.6) and 5 sequences (0.5 to 0.9):
+//            1 x 8,000    1 x 12,000   3 x 8,000    3 x 12,000   5 x 8,000    5 x 12,000
+//   d 64     12.5 / 11.3  12.8 / 14.6  15.8 / 12.8  17.1 / 16.6  19.3 / 13.9  22.0 / 18.8
+//   d 128    13.6 / 12.4  14.3 / 16.0  17.5 / 14.3  19.3 / 19.1  21.2 / 17.6  31.5 / 25.1
+//   d 256    16.2 / 20.7  17.7 / 27.9  25.7 / 24.5  36.3 / 33.7  39.8 / 32.0
+// (and 1 x 5,000 at 256 15.8 / 15.3, 3 x 5,000 20.2 / 17.7); tiles of more than 8 rows take
+// longer for a key (2 x 6,000, 16 rows at 256, fill 0.4, 24.1 / 28.8).
+long long join_keys_q8(int head_dim, int tile, double fill) {
+    const double keys = (head_dim == 256 ? 550 : 900) * (tile > 8 ? 0.75 : 1.0);
+    return (long long)(keys / (1.0 - std::min(fill, 0.55)));
+}
 
 // Decode over a paged cache of 8 bits (decode_q8.cu): the splits of each unit a
 // cluster where they are short, else pieces of a line.
@@ -686,14 +693,17 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     // short caches: narrower tiles, read more than once, while all splits of all fit the SMs
     // (us, wide / narrow, 1 x 4,000 keys x 8 heads: 32 rows at head_dim 64 13.0 / 8.9, 16 rows at
     // 128 11.5 / 9.8, at 256 19.4 / 15.2; 1 x 500 9.0 / 5.9, 7.6 / 6.2, 10.3 / 7.8)
-    if (span <= kJoinSplits * join_keys_q8(head_dim))
-        while (tile > 8 && units(tile / 2) * most <= wave_of(tile / 2)) tile /= 2;
+    auto joins = [&](int t, long long n) {   // whether n splits of every unit go together
+        return units(t) * n <= wave_of(t) &&
+               span <= n * join_keys_q8(head_dim, t, (double)(units(t) * n) / (double)wave_of(t));
+    };
+    while (tile > 8 && joins(tile / 2, most)) tile /= 2;
     a.tiles = (a.rows + tile - 1) / tile;
     p.tile = tile;
     if ((long long)hkv * a.tiles > 65535) return FA_ERR_INVALID_ARG;
     const long long pairs = units(tile), wave = wave_of(tile);
     for (long long join = std::min(most, wave / pairs);
-         join >= std::min(2ll, fine) && span <= join * join_keys_q8(head_dim); --join) {
+         join >= std::min(2ll, fine) && joins(tile, join); --join) {
         a.chunk = (int)((fine + join - 1) / join * keys);
         a.n_splits = (int)((span + a.chunk - 1) / a.chunk);
         // (a cluster lies within a part of the device: fewer may fit than CTAs do.  A second
