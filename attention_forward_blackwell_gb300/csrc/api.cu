@@ -11,6 +11,7 @@
 
 #include "../../include/fa.h"
 #include "common.cuh"
+#include "q8_line.cuh"
 
 namespace fa {
 namespace {
@@ -650,7 +651,7 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.q = static_cast<const uint16_t*>(q);
     a.k = static_cast<const uint8_t*>(k);
     a.v = static_cast<const uint8_t*>(v);
-    const int slice = decode_q8_block(head_dim) / 4;
+    const int slice = q8_block(head_dim) / 4;
     a.box = std::min(page_size & -page_size, slice);
     a.flat = block % slice == 0 ? 1 : 0;
     a.planes = num_pages * hkv;
@@ -685,11 +686,11 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     a.scale_log2 = scale * 1.4426950408889634f;
     const long long heads_first = (a.first + 63ll) / 64 * 64;
     const long long span = window > 0 ? std::min<long long>(sk, (long long)window + sq + 62 + heads_first) : sk;
-    const int keys = decode_q8_block(head_dim);
+    const int keys = q8_block(head_dim);
     const long long fine = (span + keys - 1) / keys, most = std::min<long long>(fine, kJoinSplits);
     int tile = decode_q8_tile(head_dim, a.rows);
     auto units = [&](int t) { return (long long)batch * hkv * ((a.rows + t - 1) / t); };
-    auto wave_of = [&](int t) { return (long long)di->num_sms * decode_q8_ctas(head_dim, t); };   // CTAs at once
+    auto wave_of = [&](int t) { return (long long)di->num_sms * q8_ctas(head_dim, t); };   // CTAs at once
     // short caches: narrower tiles, read more than once, while all splits of all fit the SMs
     // (us, wide / narrow, 1 x 4,000 keys x 8 heads: 32 rows at head_dim 64 13.0 / 8.9, 16 rows at
     // 128 11.5 / 9.8, at 256 19.4 / 15.2; 1 x 500 9.0 / 5.9, 7.6 / 6.2, 10.3 / 7.8)
@@ -716,12 +717,7 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     const double blocks = (double)pairs * (double)fine;
     if (blocks + kQ8Lead * (double)pairs >= 2147483647.0 - 65536) return FA_ERR_INVALID_ARG;
     a.slots = (int)std::min<double>((double)wave, blocks);
-    // small pieces for the SMs that are done with their own first, where there may be much
-    // and bytes bound it: with more rows, or fewer and larger CTAs, SMs end together and
-    // pieces only cost.  us without / with them, 8 heads: 64 x 1K to 16K keys at head_dim 128
-    // 183 / 178, 300 x 1 to 12K 568 / 537, at 64 303 / 289; 16 rows, 64 x 1K to 16K at 128 191 / 200,
-    // at 64 124 / 139; 8 rows at 256 338 / 344, 16 x 1K to 16K 96 / 113
-    a.levels = tile == 8 && head_dim < 256 && blocks >= 48.0 * a.slots ? 2 : 0;
+    a.levels = q8_levels(head_dim, tile, blocks, a.slots);
     a.n_splits = a.slots * (1 + a.levels);
     const size_t parts = 2ull * a.n_splits * tile;
     const size_t bytes_o = parts * head_dim * sizeof(float), bytes_l = (parts * sizeof(float) + 15) / 16 * 16;

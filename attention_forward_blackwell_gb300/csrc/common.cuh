@@ -370,10 +370,7 @@ struct DecodeQ8Launch {
 inline int decode_q8_tile(int head_dim, int rows) {
     return rows <= 8 ? 8 : head_dim > 64 || (rows + 15) / 16 % 2 == 1 ? 16 : 32;
 }
-int decode_q8_block(int head_dim);   // keys of a block, four slices
-constexpr int kQ8Lead = 2;           // blocks that a unit's set-up and merge are worth
 int decode_q8_clusters(int head_dim, int tile, int n);   // clusters of n of them that the device holds at once
-int decode_q8_ctas(int head_dim, int tile);   // CTAs that an SM holds at once
 cudaError_t launch_decode_q8(const DecodeQ8Launch& p, int head_dim, cudaStream_t s);
 
 // -------------------------------------------------------------- span ----

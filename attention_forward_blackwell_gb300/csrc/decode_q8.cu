@@ -57,6 +57,7 @@
 #include "common.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
+#include "q8_line.cuh"
 
 namespace fa {
 namespace {
@@ -68,9 +69,6 @@ constexpr float kLift = 6.0f;
 constexpr float kFar = 3.0e38f;  // minus a base of a row that has seen nothing
 
 constexpr unsigned kSiteQ8 = 72; // wait site of the ring
-
-constexpr int kLeastKeys = 256;  // of a piece
-constexpr int kManyBlocks = 48;  // a CTA's share from which part of it goes in small pieces
 
 // Rows that a CTA of n joined splits holds for its part of a tile's R, n pieces of each.
 // (Not a row more than the most of any n: at head_dim 64 and 128 the CTAs of an SM fill its
@@ -108,10 +106,8 @@ struct Q8Traits {
     static constexpr int JOIN_LSE = (JOIN_ROWS * 4 + 15) / 16 * 16;
     static constexpr int JOIN = JOIN_LSE + JOIN_ROWS * D * 4;
     static constexpr int MT = D / 16;                   // tiles of O^T
-    // CTAs of an SM: what the registers of a warp leave.  16 rows with two parts in
-    // hand and two CTAs at head_dim 128 took 66 us where one part and three took 76
-    // (16 x 1K to 16K keys x 8 heads; at 64, three for four, 43 for 65).
-    static constexpr int MIN_CTAS = D == 256 ? 2 : (D == 64 ? 5 : 4) - (NR == 4 ? 3 : NR);
+    static constexpr int MIN_CTAS = q8_ctas(D, R);      // of an SM
+    static_assert(BLOCK == q8_block(D), "keys of a block");
     // the merge of 8 rows goes through the slot that was read last
     static_assert(8 * D * 4 <= STAGE && 16 * 4 <= SCALE_BYTES, "merge buffer");
 };
@@ -156,43 +152,21 @@ __device__ __forceinline__ uint32_t pack_halves(float lo, float hi) {
     return r;
 }
 
-template <int BLOCK>
-__device__ __forceinline__ int unit_blocks(int span) {
-    return max(1, (span + BLOCK - 1) / BLOCK);
-}
 __device__ __forceinline__ int keys_of(const DecodeQ8Args& a, int b) {
     return max(0, min(a.seqlens_k[b], a.Sk));
 }
 
-// How the units, one after the other on a line of `all`, are cut: a unit takes a lead
-// of kQ8Lead, what its set-up and merge are worth, and its blocks; the line is cut
-// into `slots` pieces of `big`, then `small` ones up to its end.  Or, with `aligned`
-// blocks to a piece, unit by unit (the line then counts pieces).
-struct Line {
-    int all, slots, big, small, aligned;
-    __device__ __forceinline__ int lead() const { return aligned > 0 ? 0 : kQ8Lead; }
-    __device__ __forceinline__ int of_unit(int nb) const {   // what a unit of nb blocks takes of the line
-        return aligned > 0 ? (nb + aligned - 1) / aligned : nb + kQ8Lead;
-    }
-    __device__ __forceinline__ int from(int x) const {   // where piece x starts
-        if (aligned > 0) return min(x, all);
-        const long long at = x < slots ? (long long)x * big
-                                       : (long long)slots * big + (long long)(x - slots) * small;
-        return (int)min(at, (long long)all);
-    }
-    __device__ __forceinline__ int piece_of(int pos) const {
-        if (aligned > 0) return pos;
-        // (slots * big < all + slots + big: within 32 bits as unsigned)
-        const unsigned bigs = (unsigned)slots * (unsigned)big;
-        return (unsigned)pos < bigs ? pos / big : slots + (int)(((unsigned)pos - bigs) / (unsigned)small);
-    }
-};
+// Blocks of a unit of batch entry b.
+template <int BLOCK>
+__device__ __forceinline__ int blocks_of(const DecodeQ8Args& a, int b) {
+    return q8_unit_blocks(key_axis(a, keys_of(a, b)).span, BLOCK);
+}
 
 // Sum of f(blocks of a unit of entry b) over the entries [b0, b1).
 template <int BLOCK, class F>
 __device__ __forceinline__ int sum_blocks(const DecodeQ8Args& a, int b0, int b1, F&& f) {
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += f(unit_blocks<BLOCK>(key_axis(a, keys_of(a, b)).span));
+    for (int b = b0; b < b1; ++b) sum += f(blocks_of<BLOCK>(a, b));
     return sum;
 }
 
@@ -200,38 +174,20 @@ __device__ __forceinline__ int sum_blocks(const DecodeQ8Args& a, int b0, int b1,
 // 128 x 100 to 800 x 8 42.4 / 36.4, at 256 78.3 / 58.9; a lead of one block 35.4 and 62.9
 // there, of three 35.7 and 58.3; 16 x 1K to 16K x 8 at 128 53.9 / 54.2.)
 //
-// The line's cut, by a warp together, each lane with its share of the batch.  Pieces
-// that end with their units save the set-up and merge of a second segment, worth
-// about two blocks: taken where such pieces, one for every CTA at most, are no more
-// than that much longer.  A long line may leave a quarter of itself to small pieces, for
-// the SMs that are done with their own first (a.levels; api.cu says when).
+// The line's cut, by a warp together, each lane with its share of the batch.  mine: what
+// this lane's entries take of the line.
 template <int BLOCK>
 __device__ __forceinline__ Line cut_line(const DecodeQ8Args& a, int& mine) {
     const int lane = threadIdx.x & 31, units = a.Hkv * a.tiles;
     const int per = (a.B + 31) >> 5, b0 = min(lane * per, a.B), b1 = min(b0 + per, a.B);
-    Line line;
-    line.slots = a.slots;
-    line.aligned = 0;
     const int blocks = units * sum_blocks<BLOCK>(a, b0, b1, [](int nb) { return nb; });
-    mine = blocks + kQ8Lead * units * max(0, b1 - b0);
-    line.all = __reduce_add_sync(0xffffffffu, mine);
-    const int share = (int)(((unsigned)line.all + (unsigned)a.slots - 1) / (unsigned)a.slots);
-    const int least = max(1, kLeastKeys / BLOCK);
-    line.small = a.levels > 0 && share >= kManyBlocks ? share / (4 * a.levels) : 0;
-    line.big = max(share - a.levels * line.small, least);
-    if (line.small == 0 && a.B * units <= a.slots) {
-        const int total = __reduce_add_sync(0xffffffffu, blocks), cut = max((total + a.slots - 1) / a.slots, least);
-        for (int s = cut; s <= cut + kQ8Lead && line.aligned == 0; ++s) {
-            const int count = units * sum_blocks<BLOCK>(a, b0, b1, [&](int nb) { return (nb + s - 1) / s; });
-            const int all = __reduce_add_sync(0xffffffffu, count);
-            if (all <= a.slots) {
-                line.aligned = s;
-                line.all = all;
-                mine = count;
-            }
-        }
-    }
-    line.small = max(line.small, 1);
+    int pieces = 0;   // of this lane's entries, of the cut tried last
+    const Line line = q8_cut(__reduce_add_sync(0xffffffffu, blocks), a.B * units, a.slots, a.levels, BLOCK,
+                             [&](int s) {
+                                 pieces = units * sum_blocks<BLOCK>(a, b0, b1, [&](int nb) { return (nb + s - 1) / s; });
+                                 return __reduce_add_sync(0xffffffffu, pieces);
+                             });
+    mine = line.aligned > 0 ? pieces : blocks + kQ8Lead * units * max(0, b1 - b0);
     return line;
 }
 
@@ -254,7 +210,7 @@ __device__ __forceinline__ Spot find_on_line(const DecodeQ8Args& a, const Line& 
     int at = end - mine, b = lane * ((a.B + 31) >> 5), nb = 1;
     if (here) {
         for (;; ++b) {
-            nb = unit_blocks<BLOCK>(key_axis(a, keys_of(a, b)).span);
+            nb = blocks_of<BLOCK>(a, b);
             if (pos < at + units * line.of_unit(nb)) break;
             at += units * line.of_unit(nb);
         }
@@ -267,21 +223,6 @@ __device__ __forceinline__ Spot find_on_line(const DecodeQ8Args& a, const Line& 
     p.u = (pos - p.start) / len;
     p.start += p.u * len;
     p.at = pos - p.start;
-    return p;
-}
-
-// The pieces that hold blocks of a unit of nb blocks that starts at `from` on the line:
-// the first one, their number, and whether the first is its CTA's second slot (it holds
-// what comes before the unit, which ends with a block).
-struct Pieces {
-    int first, count, second;
-    __device__ __forceinline__ int slot(int k) const { return k == 0 ? 2 * first + second : 2 * (first + k); }
-};
-__device__ __forceinline__ Pieces pieces_of(const Line& line, int from, int nb) {
-    Pieces p;
-    p.first = line.piece_of(from + line.lead());
-    p.count = line.piece_of(from + line.of_unit(nb) - 1) - p.first + 1;
-    p.second = from > line.from(p.first) ? 1 : 0;
     return p;
 }
 
@@ -310,11 +251,11 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     auto* const kept = reinterpret_cast<Line*>(smem + T::LINE);   // (for the end of segments)
     if (joined) {   // grid (splits of a unit, units, batch entries), the splits a cluster
         cluster_arrive();   // (waited for before the first write to another)
-        const int nb = unit_blocks<T::BLOCK>(key_axis(a, keys_of(a, blockIdx.z)).span), n = a.chunk / T::BLOCK;
+        const int nb = blocks_of<T::BLOCK>(a, blockIdx.z), n = a.chunk / T::BLOCK;
         spot.b = blockIdx.z;
         spot.u = blockIdx.y;
         spot.at = (int)blockIdx.x * n;
-        blocks = max(0, min(n, nb - spot.at));
+        blocks = q8_joined_blocks(nb, spot.at, n);
     } else {
         int mine;
         if (a.head != nullptr && threadIdx.x == 0) a.head[blockIdx.x] = make_int4(0, 0, 0, 0);
@@ -327,8 +268,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         for (int side = end < line.all && line.aligned == 0 ? 1 : 0; side >= 0; --side) {
             spot = find_on_line<T::BLOCK>(a, line, mine, side ? end : begin);
             // blocks before the position: those of the units before, and of its own
-            const int before = spot.start - kQ8Lead * (spot.b * units + spot.u) +
-                               max(0, spot.at - kQ8Lead);
+            const int before = q8_blocks_before(spot.start, spot.b * units + spot.u, spot.at);
             blocks = side ? before : blocks - before;
         }
         if (line.aligned > 0) {
@@ -462,7 +402,9 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
     do {
         const int L = keys_of(a, b);
         const Axis axis = key_axis(a, L);
-        const int nb = unit_blocks<T::BLOCK>(axis.span), n = min(nb - kb, left);
+        const int nb = q8_unit_blocks(axis.span, T::BLOCK);
+        const Segment here = q8_segment(nb, kb, left);
+        const int n = here.n;
         const int hkv = at_unit / a.tiles, rbase = (at_unit - hkv * a.tiles) * T::R;
         // ------------------------------------------------ queries
         // B fragments: lane (g, t) has row nr 8 + g, of each 64 dims the 16 from 16 t on
@@ -734,7 +676,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         // the next segment
         const bool last_unit = at_unit + 1 == units;
         const int next_b = last_unit ? b + 1 : b, next_unit = last_unit ? 0 : at_unit + 1;
-        if (NR == 1 && left > n)
+        if (NR == 1 && here.more)
             load_query(next_b, next_unit / a.tiles, next_unit % a.tiles * T::R, 0, qw);
 
         // ------------------------------------------------ merge of the warps
@@ -871,7 +813,7 @@ __global__ void __launch_bounds__(Q8Traits<D, NR>::THREADS, Q8Traits<D, NR>::MIN
         if (kb == 0 && !whole_unit && a.head != nullptr && threadIdx.x == 0) {
             const Line cut = *kept;
             const int from = cut.aligned > 0 ? (int)blockIdx.x : cut.from(blockIdx.x + 1) - n - kQ8Lead;
-            const Pieces pc = pieces_of(cut, from, nb);
+            const Pieces pc = q8_pieces(cut, from, nb);
             a.head[blockIdx.x] = make_int4(b, at_unit, pc.count, pc.second);
         }
         left -= n;
@@ -952,12 +894,12 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_q8_kernel(const De
     if (pr >= a.rows) return;
     int mine;
     const Line line = cut_line<BLOCK>(a, mine);
-    const int nb = unit_blocks<BLOCK>(key_axis(a, keys_of(a, b)).span), len = line.of_unit(nb);
+    const int nb = blocks_of<BLOCK>(a, b), len = line.of_unit(nb);
     int before = 0;   // its batch entry's place on the line
     for (int i = lane; i < b; i += 32)
-        before += units * line.of_unit(unit_blocks<BLOCK>(key_axis(a, keys_of(a, i)).span));
+        before += units * line.of_unit(blocks_of<BLOCK>(a, i));
     before = __reduce_add_sync(0xffffffffu, before);
-    const Pieces pc = pieces_of(line, before + u * len, nb);
+    const Pieces pc = q8_pieces(line, before + u * len, nb);
     if (pc.count < 2) return;
     const int h = hkv * a.group + pr / a.Sq;
     auto at = [&](int k) { return (size_t)pc.slot(k) * tile + r; };
@@ -1105,18 +1047,6 @@ cudaError_t launch_dim(const DecodeQ8Launch& p, cudaStream_t s) {
 }
 
 }  // namespace
-
-int decode_q8_block(int head_dim) { return head_dim == 256 ? Q8Traits<256, 1>::BLOCK : Q8Traits<128, 1>::BLOCK; }
-int decode_q8_ctas(int head_dim, int tile) {
-    switch (head_dim) {
-        case 64:
-            return tile == 8    ? Q8Traits<64, 1>::MIN_CTAS
-                   : tile == 16 ? Q8Traits<64, 2>::MIN_CTAS
-                                : Q8Traits<64, 4>::MIN_CTAS;
-        case 128: return tile == 8 ? Q8Traits<128, 1>::MIN_CTAS : Q8Traits<128, 2>::MIN_CTAS;
-        default: return Q8Traits<256, 1>::MIN_CTAS;
-    }
-}
 
 int decode_q8_clusters(int head_dim, int tile, int n) {
     switch (head_dim) {
