@@ -637,6 +637,7 @@ fa_status decode_q8_impl(const void* q, const void* k, const void* v, const floa
     for (const void* p : {static_cast<const void*>(k_scale), static_cast<const void*>(v_scale),
                           static_cast<const void*>(sinks)})
         if ((reinterpret_cast<uintptr_t>(p) & 3u) != 0) return FA_ERR_MISALIGNED;
+    if (sk > kQ8MostKeys) return FA_ERR_INVALID_ARG;
     // (planes of the cache, its scales and rows of the outputs are counted in 32 bits)
     if ((long long)num_pages * hkv >= (1ll << 31) ||
         (double)num_pages * hkv * (page_size / block) >= 4294967296.0)

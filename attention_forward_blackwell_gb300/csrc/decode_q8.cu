@@ -142,7 +142,7 @@ __device__ __forceinline__ Axis key_axis(const DecodeQ8Args& a, int L) {
         if (a.first > 0) s.base = 0;
         s.head = 0;
     }
-    s.span = s.head + L - s.base;
+    s.span = s.head + (L - s.base);
     return s;
 }
 

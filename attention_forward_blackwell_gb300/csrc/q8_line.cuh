@@ -33,6 +33,10 @@ constexpr int q8_ctas(int head_dim, int tile) {
     return head_dim == 256 ? 2 : (head_dim == 64 ? 5 : 4) - (tile == 32 ? 3 : tile / 8);
 }
 
+// Most keys of a table: positions go up to the end of the block behind the last one, and a
+// block's, a window's or the queries' length away from a key; all of them stay in 32 bits.
+constexpr int kQ8MostKeys = 0x7fffffff - 4095;   // 2^31 - 4096
+
 // Levels of small pieces, for the SMs that are done with their own first, where there may be
 // much and bytes bound it: with more rows, or fewer and larger CTAs, SMs end together and
 // pieces only cost.  us without / with them, 8 heads: 64 x 1K to 16K keys at head_dim 128

@@ -501,7 +501,7 @@ fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int 
  *   2^-25 of that), a probability times its value's scale to 2^-11.  Scales must
  *   be finite and not negative (a value's below 2^-126 counts as zero); keys that no query row of the sequence sees may hold
  *   anything, their scales too.  Keys whose entry is no page read as zeros.
- *   head_dim 64, 128 or 256; num_pages * hkv < 2^31.
+ *   head_dim 64, 128 or 256; num_pages * hkv < 2^31; max_pages * page_size <= 2^31 - 4096.
  */
 fa_status fa_cache_append_q8(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
                              int num_pages, int hkv, int page_size, int block, int head_dim,

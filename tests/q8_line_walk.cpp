@@ -143,6 +143,7 @@ int walk_line(const int* spans, int B, int units, int block, int slots, int leve
 int line_ctas(int head_dim, int tile) { return q8_ctas(head_dim, tile); }
 int line_block(int head_dim) { return q8_block(head_dim); }
 int line_levels(int head_dim, int tile, double blocks, int slots) { return q8_levels(head_dim, tile, blocks, slots); }
+int line_unit_blocks(int span, int block) { return q8_unit_blocks(span, block); }
 int line_many() { return kManyBlocks; }
 
 }  // extern "C"

@@ -1,11 +1,32 @@
 """How the CTAs of the 8-bit decode share the keys, walked on the host by the kernels' own arithmetic (CPU
 only): every block of keys once, no queries of a unit that is not there, and each unit's pieces where its
 merge looks for them."""
-import random
+import ctypes
 
 import pytest
 
 import q8_line
+from attention_forward_blackwell_gb300 import binding, build
+
+
+@pytest.mark.parametrize("page", [1, 7, 16, 64, 4096 - 64])
+def test_longest_tables(page):
+    """Tables whose positions would leave 32 bits on the way are refused (the host's check, before any
+    launch): a slice past the last key would wrap round to the first."""
+    build.build()
+    at = lambda x: ctypes.c_void_p(x)
+    for keys in {2 ** 31 - 1, 2 ** 31 - 32, 2 ** 31 - 128, 2 ** 31 - 4095}:
+        pages = keys // page
+        if pages * page <= 2 ** 31 - 4096:
+            pages += 1
+        if pages * page >= 2 ** 31:
+            continue
+        st = binding.lib().fa_fwd_decode_paged_q8(
+            at(1 << 12), at(1 << 12), at(1 << 12), at(1 << 12), at(1 << 12), at(1 << 12), at(1 << 12), 1, 4, 2, 1,
+            at(1 << 12), at(1 << 12), pages, page, 9, page, 64, 0.1, 1, 0, 0, None, None)
+        assert st == binding.FA_ERR_INVALID_ARG, (page, pages)
+    for block in (64, 128):   # the last block of the longest table ends within 32 bits
+        assert q8_line.lib().line_unit_blocks(2 ** 31 - 4096, block) * block + 2 * block < 2 ** 31
 
 
 @pytest.mark.parametrize("block", [64, 128])
