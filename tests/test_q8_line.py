@@ -2,6 +2,7 @@
 only): every block of keys once, no queries of a unit that is not there, and each unit's pieces where its
 merge looks for them."""
 import ctypes
+import random
 
 import pytest
 
@@ -39,3 +40,27 @@ def test_joined_splits(block):
                 if chunk * splits * block < max(spans):
                     continue
                 assert q8_line.joined(spans, 8, block, chunk, splits) == 0, (spans, splits, chunk)
+
+
+def kind_of(cut):
+    if cut["aligned"] > 0:
+        return "aligned"
+    return "two sizes" if cut["small"] > 1 else "uneven"
+
+
+@pytest.mark.parametrize("kind", ["aligned", "uneven", "two sizes"])
+def test_lines(kind):
+    """Pieces that end with their units, even pieces, and large ones with small ones behind them."""
+    rng = random.Random(kind)
+    seen = 0
+    for _ in range(4000):
+        block, units, slots = rng.choice((64, 128)), rng.choice((1, 2, 3, 8)), rng.randint(1, 40)
+        B, most = rng.randint(1, 60), 10 ** rng.uniform(0, 5)
+        spans = [int(rng.choice((0, 1, most * rng.random(), most))) for _ in range(B)]
+        levels = rng.choice((0, 2))
+        bad, cut = q8_line.line(spans, units, block, slots, levels)
+        assert bad == 0, (bad, spans, units, block, slots, levels, cut)
+        seen += kind_of(cut) == kind
+        if seen == 50:
+            return
+    assert False, f"{seen} lines"

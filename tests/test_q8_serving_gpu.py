@@ -7,6 +7,7 @@ import re
 import pytest
 import torch
 
+import q8_line
 import q8_ref as ref
 import serving_ref
 from gpu_parity import check_device_error, free_cuda
@@ -328,6 +329,58 @@ def test_long_lines(fa):
         bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * e[..., None] + r) * (1 + 2.0 ** -8) * a + low
         assert torch.all((o[b].double() - want).abs() <= bound), f"sequence {b}"
         assert torch.all((lse[b].double() - l).abs() <= e + r * (1 + l.abs())), f"sequence {b}"
+    check_device_error()
+
+
+LINES = [  # head_dim, query heads a key head, key heads, lengths (as long as they are: the cut goes by them), cut
+    (64, 8, 8, [200000, 300, 170000, 1, 140001, 50000], "two sizes"), (128, 5, 8, [160000, 0, 120033, 129, 130000], "two sizes"),
+    (128, 8, 4, [3, 350000, 500, 330001, 70000], "two sizes"), (64, 16, 8, [500 + 3777 * i % 8500 for i in range(61)], "uneven"),
+    (256, 7, 8, [977 * i % 5900 for i in range(43)], "uneven"), (64, 3, 2, [90001, 70000, 0, 1], "aligned")]
+
+
+@pytest.mark.parametrize("d,group,hkv,lens,kind", LINES)
+def test_cuts_of_long_lines(fa, d, group, hkv, lens, kind):
+    """Each way of cutting the line: large pieces with small ones behind them, even pieces over the ends of
+    units, pieces that end with their units.  What the cut is comes from the kernels' own arithmetic."""
+    page, B, hq = 64, len(lens), group * hkv
+    width = -(-max(lens) // page)
+    tile, block, line = 8 if group <= 8 else 16, q8_line.lib().line_block(d), q8_line.lib()
+    units, sms = hkv * -(-group // tile), torch.cuda.get_device_properties(0).multi_processor_count
+    slots = min(sms * line.line_ctas(d, tile), B * units * -(-width * page // block))
+    levels = line.line_levels(d, tile, float(B * units * -(-width * page // block)), slots)
+    bad, cut = q8_line.line(lens, units, block, slots, levels)
+    assert bad == 0
+    assert kind == ("aligned" if cut["aligned"] > 0 else "two sizes" if cut["small"] > 1 else "uneven"), cut
+    # A lane's sums of a segment have at most four terms a block and the product's instructions two, each
+    # off by at most 2^-22, and merges, exponents and rescalings add 2^-16 as in ref.attention8: so a piece
+    # left out or taken twice shows in the LSE, whatever the length.
+    r = 4 * max(cut["share"], cut["aligned"]) * 2.0 ** -22 + 2.0 ** -16
+    # (a pool of pages that the sequences share; the values of a block are of their scale's size)
+    g = torch.Generator(device="cuda").manual_seed(d + B)
+    pages = 3001
+    codes = [(60 * torch.randn(pages, hkv, page, d, device="cuda", generator=g)).clamp(-448, 448).to(F8) for _ in range(2)]
+    scales = [torch.exp2(torch.randint(-8, -4, (pages, hkv, 1), device="cuda", generator=g).float()) for _ in range(2)]
+    table = torch.randint(0, pages, (B, width), device="cuda", generator=g, dtype=torch.int32)
+    q = torch.randn(B, hq, 1, d, device="cuda", generator=g).bfloat16()
+    o, lse = fa.decode_paged_q8(q, *codes, *scales, table, i32(lens))
+    for b, n in enumerate(lens):   # (the bounds of ref.attention8, by the device in 64 bits)
+        if n == 0:
+            assert torch.all(o[b] == 0) and torch.all(lse[b] == float("-inf"))
+            continue
+        k, v = fa.cache_read_q8(*codes, *scales, table[b:b + 1], i32([0, n]), n, n)
+        x, k, v = q[b].double().reshape(hkv, group, d), k.double(), v.double()
+        e = torch.einsum("hgd,mhd->hgm", x.abs(), k.abs()).amax(-1) / d ** 0.5 * (d + 8) * 2.0 ** -24
+        e = e + x.abs().amax(-1) * k.abs().sum(-1).amax(0)[:, None] / d ** 0.5 * 2.0 ** -25
+        x = torch.einsum("hgd,mhd->hgm", x, k) / d ** 0.5
+        l = torch.logsumexp(x, -1)
+        p = torch.exp(x - l[..., None])
+        want, a = torch.einsum("hgm,mhd->hgd", p, v), torch.einsum("hgm,mhd->hgd", p, v.abs())
+        low = 448 * n * 2.0 ** -31 * scales[1].max().item() * p.amax(-1, keepdim=True)
+        bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2 * e[..., None] + r) * (1 + 2.0 ** -8) * a + low
+        off = (o[b].double().reshape(hkv, group, d) - want).abs()
+        assert torch.all(off <= bound), f"sequence {b}: {(off / bound).max().item()}"
+        assert torch.all((lse[b].double().reshape(hkv, group) - l).abs() <= e + r * (1 + l.abs())), f"sequence {b}"
+        del x, k, v, p
     check_device_error()
 
 
