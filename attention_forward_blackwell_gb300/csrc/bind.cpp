@@ -586,6 +586,24 @@ struct Positions {
 bool same_memory(const Tensor& a, const Tensor& b) {
     return a.data_ptr() == b.data_ptr() && a.sizes() == b.sizes() && a.strides() == b.strides();
 }
+// Whether the strides show that no two elements of t are the same: each one reaches past
+// all that the smaller ones do.
+bool no_element_twice(const Tensor& t) {
+    int64_t size[4], stride[4];
+    int n = 0;
+    for (int64_t i = 0; i < t.dim(); ++i) {
+        if (t.size(i) < 2) continue;
+        int at = n++;
+        for (; at > 0 && stride[at - 1] > t.stride(i); --at) size[at] = size[at - 1], stride[at] = stride[at - 1];
+        size[at] = t.size(i), stride[at] = t.stride(i);
+    }
+    int64_t past = 1;
+    for (int i = 0; i < n; ++i) {
+        if (stride[i] < past) return false;
+        past += (size[i] - 1) * stride[i];
+    }
+    return true;
+}
 // Refuses an output `a` that shares memory with another tensor `b` of rows [.., heads,
 // .., d] -- or may: the heads of one token of both lie within a common stride of the
 // tokens, as the parts of one projection do, apart from one another, or their ranges of
@@ -645,10 +663,10 @@ struct Turned {
             if (out.scalar_type() != at::kBFloat16 || out.sizes() != in.sizes() || !on(out, dev))
                 throw BadValue(std::string(out_name) + " must be a bf16 tensor " + text(in.sizes()) +
                                " on cuda:" + std::to_string(dev));
-            bool apart = rows_fit(out);   // (no element twice)
-            for (int64_t i = 0; i < out.dim(); ++i) apart &= out.size(i) < 2 || out.stride(i) != 0;
-            if (!apart)
+            if (!rows_fit(out))
                 throw BadValue(std::string(out_name) + " must have contiguous, 16-byte aligned rows");
+            if (out.numel() > 0 && !no_element_twice(out))
+                throw BadValue(std::string(out_name) + " may have rows that overlap");
             if (!same_memory(in, out)) apart_from(out_name, out, name, in);
         }
         if (!rows_fit(in)) {
@@ -820,6 +838,7 @@ PyObject* cache_read_q8(PyObject* const* a, Py_ssize_t n) {
                                      : tensor(names[i], a[8 + i]);
         dense(names[i], out[i], at::kBFloat16, {total, c.hkv, c.d}, c.dev);
     }
+    apart_from("k_out", out[0], "v_out", out[1]);
     return status_or(fa_cache_read_q8(c.k, c.v, s.k, s.v, c.num_pages, c.hkv, c.page_size, s.block, c.d,
                                       ints("block_table", table, {B, table.size(1)}, c.dev),
                                       small(table.size(1)), ints("cu_seqlens", cu, {B + 1}, c.dev),

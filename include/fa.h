@@ -427,7 +427,8 @@ fa_status fa_cache_compact(void *k_cache, void *v_cache, int num_pages, int hkv,
  *   n, head_dim] bf16 with strides of batch, head and token in elements (multiples
  *   of 8; the last dimension is contiguous), 16-byte aligned; row i of batch entry b
  *   stands at positions[b * position_stride + i].  An output may be its input
- *   (in place); else it must not overlap an input.  inverse nonzero: by the angle
+ *   (in place); else it must not overlap an input, nor one output the other, nor two
+ *   rows of an output each other.  inverse nonzero: by the angle
  *   -t, the transpose: the gradient of the inputs from that of the outputs.
  *   batch <= 65535, hq + hk <= 65535, n (hq + hk) head_dim / 16 < 2^31.
  * fa_turn: how an append turns keys, and the queries that it turns beside them.
@@ -487,7 +488,7 @@ fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int 
  *   appended to.  cache_copy and cache_compact do not take these caches.
  * fa_cache_read_q8: keys j < cu_seqlens[b + 1] - cu_seqlens[b] of each sequence as
  *   bf16 rows cu_seqlens[b] + j of k_out, v_out [total, hkv, head_dim] (16-byte
- *   aligned), rounded once; the layout of fa_fwd_prefill_varlen.  max_seqlen is at
+ *   aligned, apart from each other), rounded once; the layout of fa_fwd_prefill_varlen.  max_seqlen is at
  *   least every length (rows beyond it are not written); keys without a page read as
  *   zeros.  Offsets are clamped to [0, total].
  * Both: head_dim is a multiple of 16 and at most 2048, batch <= 65535, hkv <= 16000,

@@ -164,6 +164,34 @@ def test_empty_and_refused(fa):
             bad()
 
 
+def test_outputs_that_overlap_themselves(fa):
+    """Outputs whose own rows share memory are refused (two threads would write there), rows that only
+    pass one another by are not; of two outputs neither may lie in the other."""
+    x, at = rows(1, 2, 4, 6, 64), torch.arange(6, dtype=torch.int32, device="cuda")
+    freqs = fa.rope_freqs(fa.rope_inv_freq(32)[0])
+    want, _ = fa.rope(x, None, at, freqs)
+    mem = torch.zeros(20000, dtype=torch.bfloat16, device="cuda")
+    for strides in ((2000, 400, 32, 1), (2000, 56, 250, 1), (1000, 400, 64, 1), (0, 400, 64, 1)):
+        with pytest.raises(ValueError, match="overlap|16-byte"):
+            fa.rope(x, None, at, freqs, q_out=mem.as_strided(x.shape, strides))
+        with pytest.raises(ValueError, match="overlap|16-byte"):   # in place too
+            y = mem.as_strided(x.shape, strides)
+            fa.rope(y, None, at, freqs, q_out=y)
+    for strides in ((1600, 400, 64, 1), (2000, 64, 304, 1), (64, 1000, 128, 1)):
+        assert torch.equal(fa.rope(x, None, at, freqs, q_out=mem.as_strided(x.shape, strides))[0], want)
+    one = rows(2, 1, 1, 6, 64)   # (strides of dimensions of one element say nothing)
+    assert torch.equal(fa.rope(one, None, at, freqs, q_out=mem.as_strided(one.shape, (0, 8, 64, 1)))[0],
+                       fa.rope(one, None, at, freqs)[0])
+    cache = torch.zeros(3, 2, 16, 64, dtype=torch.uint8, device="cuda").view(ref.F8)
+    scale, table = torch.ones(3, 2, 1, device="cuda"), torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    k = mem[:40 * 128].view(40, 2, 64)
+    for v in (k, mem[64:64 + 40 * 128].view(40, 2, 64)):
+        with pytest.raises(ValueError, match="share memory"):
+            fa.cache_read_q8(cache, cache, scale, scale, table, cu, 40, 40, k_out=k, v_out=v)
+    fa.cache_read_q8(cache, cache, scale, scale, table, cu, 40, 40, k_out=k, v_out=mem[40 * 128:80 * 128].view(40, 2, 64))
+
+
 def test_angles_against_cuda(fa):
     """The call's sines and cosines, through pairs (1, 0) whose products are exact, in bf16."""
     g = torch.Generator().manual_seed(9)
