@@ -604,34 +604,31 @@ bool no_element_twice(const Tensor& t) {
     }
     return true;
 }
-// Refuses an output `a` that shares memory with another tensor `b` of rows [.., heads,
-// .., d] -- or may: the heads of one token of both lie within a common stride of the
-// tokens, as the parts of one projection do, apart from one another, or their ranges of
-// addresses do.
+// Refuses an output `a` that shares memory with another tensor `b` of rows -- or may: their
+// ranges of addresses are apart, or else some stride is a period in which they are.  The
+// dimensions whose strides are multiples of the period leave the place in it as it is, the
+// others reach from a tensor's first element over its extent: so lie the parts of one
+// projection, whatever the order of its dimensions.
 void apart_from(const char* a_name, const Tensor& a, const char* b_name, const Tensor& b) {
     if (a.numel() == 0 || b.numel() == 0) return;
-    auto extent = [](const Tensor& t) {   // elements from the first to past the last
+    // elements from the first to past the last, in a period (0: none)
+    auto extent = [](const Tensor& t, int64_t period) {
         int64_t n = 1;
-        for (int64_t i = 0; i < t.dim(); ++i) n += (t.size(i) - 1) * t.stride(i);
+        for (int64_t i = 0; i < t.dim(); ++i)
+            if (t.size(i) > 1 && (period == 0 || t.stride(i) % period != 0)) n += (t.size(i) - 1) * t.stride(i);
         return n;
     };
-    const auto pa = reinterpret_cast<uintptr_t>(a.data_ptr()), pb = reinterpret_cast<uintptr_t>(b.data_ptr());
-    if (pa + 2 * extent(a) <= pb || pb + 2 * extent(b) <= pa) return;
-    if (a.dim() == b.dim()) {
-        // the tokens' dimension; with one token to a batch entry, the entries'
-        const int64_t token = a.dim() == 3 || a.size(2) == 1 ? 0 : 2, period = a.stride(token);
-        bool grid = period > 0 && b.stride(token) == period && a.size(token) == b.size(token);
-        if (a.dim() == 4) {
-            grid &= a.size(2) == b.size(2) && a.size(0) == b.size(0);
-            if (a.size(0) > 1) grid &= a.stride(0) == b.stride(0) && a.stride(0) % period == 0;
-        }
-        // a token's heads of each, as offsets within the period
-        auto row = [](const Tensor& t) { return (t.size(1) - 1) * t.stride(1) + t.size(t.dim() - 1); };
-        if (grid && (pa - pb) % 2 == 0 && row(a) <= period && row(b) <= period) {
-            const int64_t off = ((static_cast<int64_t>(pb) - static_cast<int64_t>(pa)) / 2 % period + period) % period;
-            if (off >= row(a) && off + row(b) <= period) return;
-        }
-    }
+    const auto pa = reinterpret_cast<intptr_t>(a.data_ptr()), pb = reinterpret_cast<intptr_t>(b.data_ptr());
+    if (pa + 2 * extent(a, 0) <= pb || pb + 2 * extent(b, 0) <= pa) return;
+    if ((pb - pa) % 2 == 0)
+        for (const Tensor* t : {&a, &b})
+            for (int64_t i = 0; i + 1 < t->dim(); ++i) {
+                const int64_t period = t->stride(i);
+                if (t->size(i) < 2 || period <= 0) continue;
+                const int64_t of_a = extent(a, period), of_b = extent(b, period);
+                const int64_t off = ((pb - pa) / 2 % period + period) % period;
+                if (of_a <= period && off >= of_a && off + of_b <= period) return;
+            }
     throw BadValue(std::string(a_name) + " may share memory with " + b_name);
 }
 

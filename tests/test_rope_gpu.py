@@ -164,6 +164,29 @@ def test_empty_and_refused(fa):
             bad()
 
 
+@pytest.mark.parametrize("order", ["BPHN", "PBHN", "BHPN", "BHNP", "HBNP", "NBPH"])
+@pytest.mark.parametrize("B,H,n", [(2, 4, 6), (1, 3, 5), (3, 1, 7), (2, 5, 1), (1, 1, 4)])
+def test_in_place_in_any_order_of_the_dimensions(fa, order, B, H, n):
+    """Queries and keys of one projection (P), turned where they lie or into another one's parts."""
+    size = dict(B=B, P=3, H=H, N=n)
+    x = rows(4, *(size[c] for c in order), 64)
+    part = lambda t, p: t.permute(*(order.index(c) for c in "PBHN"), 4)[p]
+    at, freqs = torch.arange(n, dtype=torch.int32, device="cuda") + 3, fa.rope_freqs(fa.rope_inv_freq(64)[0])
+    before, wide = x.clone(), torch.zeros_like(x)
+    q, k = fa.rope(part(x, 0), part(x, 1), at, freqs)
+    fa.rope(part(x, 0), part(x, 1), at, freqs, q_out=part(wide, 2), k_out=part(wide, 0))
+    assert torch.equal(part(wide, 2), q) and torch.equal(part(wide, 0), k) and not part(wide, 1).any()
+    assert torch.equal(x, before)
+    for bad in (dict(q_out=part(x, 1), k_out=part(x, 0)), dict(q_out=part(x, 2), k_out=part(x, 0)),
+                dict(q_out=part(x, 2), k_out=part(x, 2))):   # swapped, or both in one place
+        with pytest.raises(ValueError, match="share memory"):
+            fa.rope(part(x, 0), part(x, 1), at, freqs, **bad)
+    fa.rope(part(x, 0), part(x, 1), at, freqs, q_out=part(x, 2), k_out=part(x, 1))
+    assert torch.equal(part(x, 2), q) and torch.equal(part(x, 1), k) and torch.equal(part(x, 0), part(before, 0))
+    fa.rope(part(x, 0), None, at, freqs, q_out=part(x, 0))
+    assert torch.equal(part(x, 0), q)
+
+
 def test_outputs_that_overlap_themselves(fa):
     """Outputs whose own rows share memory are refused (two threads would write there), rows that only
     pass one another by are not; of two outputs neither may lie in the other."""
