@@ -52,10 +52,10 @@ struct AppendArgs {
 // 16 x 2,048 51.8, 50.6, 53.1).
 constexpr int kKeptWarp = 4, kKeptCta = 2;
 // A unit has 128 threads where it keeps them busy with at most kPasses tasks each and
-// there are more than kFewUnits units of keys (four an SM), else 256: 8 x 600 tokens x 8
+// there are more than kFewUnits units of keys an SM, else 256: 8 x 600 tokens x 8
 // heads 11.8 us with 128, 12.4 with 256; 1 x 2,048 7.3 and 6.6; at head_dim 256, 8 x 600 x 4
 // heads 13.7 and 12.0.
-constexpr int kPasses = 4, kFewUnits = 608;
+constexpr int kPasses = 4, kFewUnits = 4;
 
 // Codes of a granule, its elements times inv.
 __device__ __forceinline__ uint2 codes_of(const Granule& x, float inv) {
@@ -310,9 +310,9 @@ constexpr int kReadTokens = 64;   // of a CTA, all heads, at most
 // Tasks (16 codes) a thread has in flight: 8 x 2,500 tokens x 8 heads of 128 21.3 us with
 // one, 18.7 with two, 19.2 with three, 18.8 with four; 1 x 4,000 7.1, 6.7, 5.3, 6.0.
 constexpr int kReadFlight = 4;
-// Below as many CTAs (two an SM) they take fewer tokens: 1,000 tokens x 8 heads 3.4 us so,
+// Below as many CTAs an SM they take fewer tokens: 1,000 tokens x 8 heads 3.4 us so,
 // 3.9 with half as many, 4.5 with four times; 8 x 2,500 tokens x 2 heads 6.5, 6.5, 6.0.
-constexpr int kReadCtas = 304;
+constexpr int kReadCtas = 2;
 
 // CTA (tokens of a sequence, keys or values, batch entry).  Where the tokens lie is
 // looked up once, by a thread each; then tasks of two granules of 8 codes, half a row
@@ -484,11 +484,12 @@ fa_status fa_cache_append_q8(void* k_cache, void* v_cache, float* k_scale, float
     a.units = n > 0 ? (n + block - 2) / block + 1 : 1;
     const long long x = (long long)a.units + (copies ? a.c.blocks : 0);
     if (x >= (1ll << 31)) return FA_ERR_INVALID_ARG;
-    if ((st = sm103_or_status()) != FA_OK) return st;
+    int sms = 0;
+    if ((st = sm103_or_status(sms)) != FA_OK) return st;
     // a warp for a unit where it keeps all of its rows
     const int unit_rows = n < block ? n : block;
     const bool warp = unit_rows <= 32 / a.tasks * kKeptWarp;
-    const bool many = (long long)batch * a.units * hkv > kFewUnits;
+    const bool many = (long long)batch * a.units * hkv > (long long)kFewUnits * sms;
     const int threads = warp || (many && unit_rows <= 128 / a.tasks * kPasses) ? 128 : 256;
     a.kv_ctas = warp ? (2 * hkv + 3) / 4 : 2 * hkv;
     long long q_ctas = 0;
@@ -530,12 +531,13 @@ fa_status fa_cache_read_q8(const void* k_cache, const void* v_cache, const float
     a.total = total;
     a.out[0] = static_cast<uint4*>(k_out);
     a.out[1] = static_cast<uint4*>(v_out);
-    if ((st = sm103_or_status()) != FA_OK) return st;
+    int sms = 0;
+    if ((st = sm103_or_status(sms)) != FA_OK) return st;
     const int longest = max_seqlen < total ? max_seqlen : total;
     // tokens that give each thread what it has in flight, fewer where the CTAs are few
     a.tokens = kReadFlight * (kReadThreads / a.tasks) / hkv;
     if (a.tokens > kReadTokens) a.tokens = kReadTokens;
-    while (a.tokens > 1 && 2ll * total / a.tokens < kReadCtas) a.tokens /= 2;
+    while (a.tokens > 1 && 2ll * total / a.tokens < kReadCtas * sms) a.tokens /= 2;
     if (a.tokens < 1) a.tokens = 1;
     const dim3 grid((unsigned)((longest + a.tokens - 1) / a.tokens), 2, (unsigned)batch);
     const cudaError_t e = launch_dependent(read_q8_kernel, grid, dim3(kReadThreads), 0,

@@ -151,11 +151,14 @@ fa_status strides_of(const long long* strides, long long (&to)[3]) {
 // / four, by tokens x 40 heads of 128: 256 4.6 / 5.1, 512 5.3 / 5.9, 600 6.0 / 6.0,
 // 700 6.8 / 6.2, 1,000 8.0 / 6.5, 4,000 22.9 / 15.4.
 constexpr int kHeads = 4;
-constexpr long long kManyTasks = 152ll * 1280;
+constexpr long long kManyTasks = 1280;
 
 fa_status launch_rope(RopeArgs& a, int batch, cudaStream_t s) {
+    int sms = 0;
+    const fa_status st = sm103_or_status(sms);
+    if (st != FA_OK) return st;
     const long long rows = (long long)a.n * a.tasks;
-    const bool many = rows * a.heads * batch >= kManyTasks;
+    const bool many = rows * a.heads * batch >= kManyTasks * sms;
     const int per = many ? kHeads : 1;
     const long long ctas = (rows * ((a.heads + per - 1) / per) + kThreads - 1) / kThreads;
     long long copy_ctas = 0;
@@ -220,7 +223,6 @@ fa_status fa_rope(const void* q, const long long* q_strides, void* q_out,
     a.n = n;
     a.positions = positions;
     a.position_stride = position_stride;
-    if ((st = sm103_or_status()) != FA_OK) return st;
     return launch_rope(a, batch, reinterpret_cast<cudaStream_t>(stream));
 }
 
@@ -288,7 +290,6 @@ fa_status fa_cache_append_rope(void* k_cache, void* v_cache, int num_pages, int 
     a.pages = PageTable{block_table, num_pages > 0 ? max_pages : 0, page_size, num_pages,
                         fast_div(page_size > 0 ? page_size : 1)};
     a.copies = num_pages > 0 ? copies : nullptr;
-    if ((st = sm103_or_status()) != FA_OK) return st;
     return launch_rope(a, batch, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -180,23 +180,24 @@ __device__ __forceinline__ bool key_page(const PageTable& t, int b, long long po
 inline bool is_aligned(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
-// The kernels of this library are compiled for sm_103 only.  (Asked of the runtime once
-// per device: the calls here take two microseconds.)
-inline fa_status sm103_or_status() {
+// The kernels of this library are compiled for sm_103 only; its SMs.  (Asked of the runtime
+// once per device: the calls here take two microseconds.)
+inline fa_status sm103_or_status(int& sms) {
     constexpr int kDevices = 64;
-    static std::atomic<signed char> known[kDevices];   // 0: not asked yet, 1: it is, -1: it is not
+    static std::atomic<int> known[kDevices];   // 0: not asked yet, -1: it is another, else its SMs
     int dev = 0, major = 0, minor = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
     const bool keep = dev >= 0 && dev < kDevices;
-    signed char is = keep ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (is == 0) {
+    sms = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (sms == 0) {
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return FA_ERR_CUDA;
-        is = major == 10 && minor == 3 ? 1 : -1;
-        if (keep) known[dev].store(is, std::memory_order_relaxed);
+        if (major != 10 || minor != 3 || sms <= 0) sms = -1;
+        if (keep) known[dev].store(sms, std::memory_order_relaxed);
     }
-    return is > 0 ? FA_OK : FA_ERR_UNSUPPORTED;
+    return sms > 0 ? FA_OK : FA_ERR_UNSUPPORTED;
 }
 // Frequencies and factor of a call that turns rows (freqs NULL: none).
 inline fa_status check_turn(const long long* freqs, int rot, int head_dim, float factor) {
