@@ -521,10 +521,7 @@ fa_status fa_cache_read_q8(const void* k_cache, const void* v_cache, const float
     if (max_seqlen == 0 || !cu_seqlens || !k_out || !v_out) return FA_ERR_INVALID_ARG;
     if (!is_aligned(cu_seqlens, 4) || !is_aligned(k_out, 16) || !is_aligned(v_out, 16))
         return FA_ERR_MISALIGNED;
-    if (num_pages == 0 || page_size == 0) {   // (no page: every key reads as zeros)
-        a.c.pages.max_pages = 0;
-        a.c.block = 1;
-    }
+    if (num_pages == 0 || page_size == 0) a.c.pages.max_pages = 0;   // (no page: every key reads as zeros)
     a.tasks = head_dim / 16;
     a.by_hkv = fast_div(hkv);
     a.cu = cu_seqlens;
@@ -539,7 +536,7 @@ fa_status fa_cache_read_q8(const void* k_cache, const void* v_cache, const float
     if (a.tokens > kReadTokens) a.tokens = kReadTokens;
     while (a.tokens > 1 && 2ll * total / a.tokens < kReadCtas * sms) a.tokens /= 2;
     if (a.tokens < 1) a.tokens = 1;
-    const dim3 grid((unsigned)((longest + a.tokens - 1) / a.tokens), 2, (unsigned)batch);
+    const dim3 grid((unsigned)((longest - 1) / a.tokens + 1), 2, (unsigned)batch);
     const cudaError_t e = launch_dependent(read_q8_kernel, grid, dim3(kReadThreads), 0,
                                            reinterpret_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -302,6 +302,20 @@ def test_read_bounds(fa):
     assert k.shape == (0, 2, 64)
 
 
+def test_caches_without_pages(fa):
+    """Every key reads as zeros, appended rows go nowhere; a table of no entries likewise."""
+    g = torch.Generator().manual_seed(3)
+    x = rows(g, 2, 2, 5, 64).cuda()
+    for pages, width in ((0, 3), (3, 0), (0, 0)):
+        kc, vc = (torch.zeros(pages, 2, 16, 64, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2))
+        ks, vs = (torch.ones(pages, 2, 2, device="cuda") for _ in range(2))
+        table, out = i32([[0] * width] * 2).reshape(2, width), [torch.full((70, 2, 64), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        assert fa.cache_append_q8(kc, vc, ks, vs, table, i32([0, 3]), x, x) is None
+        k, v = fa.cache_read_q8(kc, vc, ks, vs, table, i32([0, 33, 60]), 70, 33, k_out=out[0], v_out=out[1])
+        assert not k[:60].any() and not v[:60].any() and torch.all(k[60:] == 5.0) and torch.all(v[60:] == 5.0)
+        assert not kc.view(torch.uint8).any() and torch.all(ks == 1.0)
+
+
 def test_refusals(fa):
     g = torch.Generator().manual_seed(1)
     kc, ks = ref.codes8(g, 3, 2, 16, 8, 64)
