@@ -41,6 +41,15 @@ EncodeTiledFn g_encode = nullptr;
 unsigned long long* g_trace_buf = nullptr;
 int g_trace_block = 0;
 
+// Lets this thread ask the runtime for what does not go onto a stream while some stream
+// is being captured (the address of a device variable, among others).
+struct OutsideCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    OutsideCapture(const OutsideCapture&) = delete;
+};
+
 // Looks up (once) the properties of the current device.  Returns nullptr if
 // the CUDA runtime fails.
 const DeviceInfo* device_info() {
@@ -49,6 +58,7 @@ const DeviceInfo* device_info() {
     std::lock_guard<std::mutex> lock(g_mu);
     DeviceInfo& di = g_dev[dev];
     if (!di.ready) {
+        const OutsideCapture outside;   // (a process's first call may be a captured one)
         int major = 0, minor = 0, sms = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
