@@ -683,6 +683,7 @@ PyObject* rope(PyObject* const* a, Py_ssize_t n) {
     const Turned q("q", a[0], "q_out", a[7], dev, stream);
     std::optional<Turned> k;
     if (a[1] != Py_None) k.emplace("k", a[1], "k_out", a[8], dev, stream);
+    else if (a[8] != Py_None) throw BadValue("k_out without k");
     const Tensor& x = q.in;
     const bool packed = x.dim() == 3;
     if (k) {   // (rows of one are read while the other's are written)

@@ -215,6 +215,13 @@ def test_outputs_that_overlap_themselves(fa):
     fa.cache_read_q8(cache, cache, scale, scale, table, cu, 40, 40, k_out=k, v_out=mem[40 * 128:80 * 128].view(40, 2, 64))
 
 
+def test_k_out_without_k(fa):
+    """Refused: it would stay as it is."""
+    x, at = rows(1, 6, 4, 64), torch.arange(6, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="k_out without k"):
+        fa.rope(x, None, at, fa.rope_freqs(fa.rope_inv_freq(32)[0]), k_out=torch.zeros_like(x))
+
+
 def test_angles_against_cuda(fa):
     """The call's sines and cosines, through pairs (1, 0) whose products are exact, in bf16."""
     g = torch.Generator().manual_seed(9)
