@@ -576,7 +576,9 @@ def rope_inv_freq(rot, base=10000.0, method=None, stretch=1.0, original=None, fa
                 fastest kept
       "yarn"    pairs that turn ``fast`` times or more in ``original`` positions keep w_i, those that
                 turn ``slow`` times or less take w_i / stretch, linearly in the number of turns in
-                between; factor 0.1 ln(stretch) + 1
+                between; factor 0.1 ln(stretch) + 1.  (Some models go from one to the other linearly
+                in the index of the pair instead, which gives other frequencies for the same numbers:
+                for those make inv_freq by their own rule.)
     """
     if rot <= 0 or rot % 2:
         raise ValueError("rot must be positive and even")
@@ -616,8 +618,9 @@ def rope(q, k, positions, freqs, interleaved=False, inverse=False, factor=1.0, q
          stream=None):
     """Queries and keys turned by their positions through ``fa_rope``: q and k (or None) bf16
     [T, heads, d] with int32 positions [T], or [B, heads, n, d] with positions [B, n] or [n]; the first
-    2 freqs.numel() elements of a row are turned (``rope_freqs``), as pairs (i, i + rot / 2) or, with
-    ``interleaved``, (2 i, 2 i + 1), times ``factor``.  Any strides; an output may be its input.
+    rot = 2 freqs.numel() elements of a row, a multiple of 16, are turned (``rope_freqs``), as pairs
+    (i, i + rot / 2) or, with ``interleaved``, (2 i, 2 i + 1), times ``factor``.  Any strides; an output
+    may be its input and must else be apart from inputs and the other output.
     ``inverse`` turns back: the gradient of the inputs from that of the outputs.  Returns (q_out,
     k_out)."""
     r = _serving().rope(q, k, positions, freqs, interleaved, inverse, factor, q_out, k_out, _handle(stream))

@@ -620,8 +620,11 @@ fa_status decode_impl(const void* q, const void* k, const void* v, void* o, floa
 //            1 x 8,000    1 x 12,000   3 x 8,000    3 x 12,000   5 x 8,000    5 x 12,000
 //   d 64     12.5 / 11.3  12.8 / 14.6  15.8 / 12.8  17.1 / 16.6  19.3 / 13.9  22.0 / 18.8
 //   d 128    13.6 / 12.4  14.3 / 16.0  17.5 / 14.3  19.3 / 19.1  21.2 / 17.6  31.5 / 25.1
-//   d 256    16.2 / 20.7  17.7 / 27.9  25.7 / 24.5  36.3 / 33.7  39.8 / 32.0
-// (and 1 x 5,000 at 256 15.8 / 15.3, 3 x 5,000 20.2 / 17.7); tiles of more than 8 rows take
+//   d 256    16.1 / 20.4  17.6 / 27.6  25.7 / 24.3  35.7 / 33.4  39.5 / 31.8  51.8 / 43.9
+// (and 1 x 5,000 at 256 15.7 / 15.0, 2 x 12,000 23.8 / 32.3, 3 x 5,000 20.0 / 17.4, 4 x 12,000 43.0 /
+// 36.1).  At 256 the ceiling, 1,222 keys, leaves the line to the last three columns, though it is the
+// slower there (five sequences fit six splits a unit): it is set between 1 x 8,000 and 3 x 8,000 and
+// grows with the fill alone.  Tiles of more than 8 rows take
 // longer for a key (2 x 6,000, 16 rows at 256, fill 0.4, 24.1 / 28.8).
 long long join_keys_q8(int head_dim, int tile, double fill) {
     const double keys = (head_dim == 256 ? 550 : 900) * (tile > 8 ? 0.75 : 1.0);

@@ -307,8 +307,10 @@ struct ReadArgs {
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTokens = 64;   // of a CTA, all heads, at most
-// Tasks (16 codes) a thread has in flight: 8 x 2,500 tokens x 8 heads of 128 21.3 us with
-// one, 18.7 with two, 19.2 with three, 18.8 with four; 1 x 4,000 7.1, 6.7, 5.3, 6.0.
+// Tasks (16 codes) a thread has in flight, for long reads.  us with one, two, three and four:
+// 16 x 5,000 tokens x 8 heads of 128 86.2, 74.3, 74.5, 74.4; 8 x 2,500 x 8 23.4, 19.3, 19.4, 18.9;
+// x 4 heads of 256 23.1, 19.0, 19.0, 18.4.  Short ones lose what long ones gain, in CTAs:
+// 8 x 2,500 x 2 heads of 128 6.4, 5.6, 5.5, 6.5; 1 x 4,000 x 8 5.3, 5.0, 5.3, 6.1.
 constexpr int kReadFlight = 4;
 // Below as many CTAs an SM they take fewer tokens: 1,000 tokens x 8 heads 3.4 us so,
 // 3.9 with half as many, 4.5 with four times; 8 x 2,500 tokens x 2 heads 6.5, 6.5, 6.0.

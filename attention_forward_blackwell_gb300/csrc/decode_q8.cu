@@ -33,8 +33,8 @@
 // Work.  The sequences' lengths are known to the device only, and differ.  A unit
 // (batch entry, key/value head, tile of query rows) counts its blocks of keys; the
 // units' blocks, one after the other, form a line that is cut into equal pieces, one
-// per CTA, as many CTAs as fit the SMs at once (as in span.cu; cut_line has the
-// choices).  A unit that lies in one piece is finished there; of the others each CTA
+// per CTA, as many CTAs as fit the SMs at once (as in span.cu; q8_line.cuh has the
+// arithmetic and its choices).  A unit that lies in one piece is finished there; of the others each CTA
 // writes what it has, normalised, with its LSE, and a second kernel merges them in
 // their order.  (The split kernel's grid, one CTA of 256 keys and more for every
 // piece of the longest possible sequence, took 195 us for 64 x 1K to 16K keys x 8

@@ -55,7 +55,7 @@ constexpr int kScaleLow = -54, kScaleHigh = 54;   // exponents of scales
 // The smallest 2^e, kScaleLow <= e <= kScaleHigh, with 448 2^e no less than the
 // root of `square`.  (448 2^e)^2 = 49/64 2^(18 + 2 e): compared with the square
 // itself, part 2^power with part in [1/2, 1), nothing is rounded.  The limits keep
-// the squares within fp32; a reach below 2^-64 counts as none.
+// the squares within fp32; a reach below 2^-63 counts as none.
 __device__ __forceinline__ float q8_scale(float square) {
     const uint32_t bits = __float_as_uint(square);
     if (!(square >= 0x1p-126f)) return __uint_as_float((uint32_t)(127 + kScaleLow) << 23);

@@ -481,11 +481,13 @@ fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int 
  *   the sequence (keys below seqlens[b]); earlier rows are then rounded anew to codes
  *   of s, which between powers of two changes only what falls below 2^-6 s.  The
  *   reach is the largest length factor * sqrt(x^2 + y^2) of a turned pair and
- *   magnitude of the other elements, so it does not depend on positions.  A code is
+ *   magnitude of the other elements, so it does not depend on positions (lengths
+ *   below 2^-63, before the factor too, count as none, those past 2^63 as without end).  A code is
  *   its element over s, rounded to the nearest code, ties to even; beyond 448 it is
  *   448.  New rows must be finite.  With copies, blocks and scales of replaced
  *   pages come along; n may be 0.  A page that another row holds must not be
- *   appended to.  cache_copy and cache_compact do not take these caches.
+ *   appended to.  cache_copy, cache_compact and the tree's attention do not take these
+ *   caches: drafts over them are chains.
  * fa_cache_read_q8: keys j < cu_seqlens[b + 1] - cu_seqlens[b] of each sequence as
  *   bf16 rows cu_seqlens[b] + j of k_out, v_out [total, hkv, head_dim] (16-byte
  *   aligned, apart from each other), rounded once; the layout of fa_fwd_prefill_varlen.  max_seqlen is at
@@ -502,7 +504,8 @@ fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int 
  *   2^-25 of that), a probability times its value's scale to 2^-11.  Scales must
  *   be finite and not negative (a value's below 2^-126 counts as zero); keys that no query row of the sequence sees may hold
  *   anything, their scales too.  Keys whose entry is no page read as zeros.
- *   head_dim 64, 128 or 256; num_pages * hkv < 2^31; max_pages * page_size <= 2^31 - 4096.
+ *   head_dim 64, 128 or 256; num_pages * hkv < 2^31; max_pages * page_size <= 2^31 - 4096;
+ *   num_pages * hkv * page_size / block < 2^32.
  */
 fa_status fa_cache_append_q8(void *k_cache, void *v_cache, float *k_scale, float *v_scale,
                              int num_pages, int hkv, int page_size, int block, int head_dim,
