@@ -501,7 +501,8 @@ fa_status fa_cache_append_rope(void *k_cache, void *v_cache, int num_pages, int 
  *   not, window <= 0 or a window with `first` visible first keys (0: none), sinks or
  *   NULL.  Queries, probabilities and values are multiplied in fp16 with fp32 sums:
  *   codes exactly, queries to 2^-11 (elements below 2^-14 of their row's largest to
- *   2^-25 of that), a probability times its value's scale to 2^-11.  Scales must
+ *   2^-25 of that), a probability times its value's scale to 2^-11; probabilities below
+ *   2^-126, beside a far larger sink, count as zero.  Scales must
  *   be finite and not negative (a value's below 2^-126 counts as zero); keys that no query row of the sequence sees may hold
  *   anything, their scales too.  Keys whose entry is no page read as zeros.
  *   head_dim 64, 128 or 256; num_pages * hkv < 2^31; max_pages * page_size <= 2^31 - 4096;

@@ -384,6 +384,38 @@ def test_cuts_of_long_lines(fa, d, group, hkv, lens, kind):
     check_device_error()
 
 
+def test_largest_batch(fa):
+    """As many sequences as a call takes: a step of all of them, most still empty before it."""
+    B, d, page = 65535, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(7)
+    kc, vc = (torch.zeros(B, 1, page, d, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2))
+    ks, vs = (torch.zeros(B, 1, 1, device="cuda") for _ in range(2))
+    table = torch.randperm(B, device="cuda", generator=g).to(torch.int32)[:, None].contiguous()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    x = {w: torch.randn(B, h, 1, d, device="cuda", generator=g).bfloat16() for w, h in (("k", 1), ("v", 1), ("q", 2))}
+    inv = fa.rope_inv_freq(d)[0]
+    freqs = fa.rope_freqs(inv)
+    qr = fa.cache_append_q8(kc, vc, ks, vs, table, lens, x["k"], x["v"], freqs, q=x["q"])
+    at = torch.zeros(B, 1, dtype=torch.int32, device="cuda")   # (position 0: as it was)
+    assert torch.equal(qr, x["q"]) and torch.equal(fa.rope(x["q"], None, at, freqs)[0], x["q"])
+    lens[::3] += 1
+    cu = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    cu[1:] = lens.cumsum(0)
+    total = int(cu[-1])
+    k, v = fa.cache_read_q8(kc, vc, ks, vs, table, cu, total, 1)
+    assert torch.all((v.double() - x["v"][::3, :, 0].double()).abs() <= 2.0 ** -4 * x["v"][::3, :, 0].double().abs() + vs.max() * 2.0 ** -10)
+    o, lse = fa.decode_paged_q8(qr, kc, vc, ks, vs, table, lens, causal=True)
+    # one key: its value, and its score to fp32's d + 8 roundings and the LSE's 2^-16
+    assert torch.equal(o[::3], v[:, :, None].expand(-1, 2, 1, d))
+    want = torch.einsum("bhnd,bkd->bhn", qr[::3].double(), k.double()) / d ** 0.5
+    size = torch.einsum("bhnd,bkd->bhn", qr[::3].double().abs(), k.double().abs()) / d ** 0.5
+    low = qr[::3].double().abs().amax(-1) * k.double().abs().sum((1, 2))[:, None, None] / d ** 0.5 * 2.0 ** -25
+    assert torch.all((lse[::3].double() - want).abs() <= size * (d + 8) * 2.0 ** -24 + low + (1 + want.abs()) * 2.0 ** -16)
+    empty = lens == 0
+    assert torch.all(o[empty] == 0) and torch.all(lse[empty] == float("-inf"))
+    check_device_error()
+
+
 def test_readme(fa):
     """The README's steps over an 8-bit cache, run as they are written."""
     with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
